@@ -32,7 +32,10 @@ EXPORTS = ("gs_preprocess", "gs_sort_workspace_bytes", "gs_bin_and_sort", "gs_re
            "gs_densify_stats", "gs_loss_workspace_bytes", "gs_loss_l1_dssim", "gs_preprocess2d",
            "gs_render2d_fwd", "gs_render2d_bwd", "gs_preprocess2d_bwd", "gs_bin_and_sort_async",
            "gs_preprocess_bwd_stats", "gs_selftest_sort_timeout", "gs_render_bwd_sqerr",
-           "gs_step_context_create", "gs_step_context_destroy", "gs_train_step_host")
+           "gs_step_context_create", "gs_step_context_destroy", "gs_train_step_host", "gs_layer_norm_fwd",
+           "gs_layer_norm_workspace_bytes", "gs_layer_norm_bwd", "gs_cross_attention_workspace_bytes",
+           "gs_cross_attention_fwd", "gs_cross_attention_bwd")
+GS_DTYPE_F32, GS_DTYPE_F16, GS_DTYPE_BF16 = 0, 1, 2
 GS_STATIC_SORT_WORKSPACE_BYTES = 32 << 20
 GS_SELFTEST_SORT_WORKSPACE_BYTES = 128 << 10
 
@@ -74,6 +77,18 @@ class gs_adam_options(C.Structure):
                 ("lr_opacity", C.c_float), ("lr_sh_dc", C.c_float), ("lr_sh_rest", C.c_float),
                 ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float), ("step", C.c_int32),
                 ("sh_degree", C.c_int32)]
+
+
+class gs_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("len_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
+class gs_attention(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("len_q", C.c_int32), ("len_k", C.c_int32), ("scale", C.c_float),
+                ("k_len", C.c_void_p), ("key_mask", C.c_void_p), ("key_mask_stride", C.c_int64),
+                ("spin_limit", C.c_uint32)]
 
 
 class GsError(RuntimeError):
@@ -147,6 +162,18 @@ def load():
         lib.gs_step_context_destroy.restype = C.c_int
         lib.gs_train_step_host.argtypes = [P, ppar, P, pcam, popt, C.POINTER(gs_tensors), P, P, P]
         lib.gs_train_step_host.restype = C.c_int
+        F = C.c_float
+        lib.gs_layer_norm_fwd.argtypes = [P, I64, I64, I64, I32, P, P, I32, F, P, I64, P, P, P]
+        lib.gs_layer_norm_workspace_bytes.argtypes = [I64, I64]
+        lib.gs_layer_norm_workspace_bytes.restype = C.c_size_t
+        lib.gs_layer_norm_bwd.argtypes = [P, I64, P, I64, I64, I64, I32, P, P, P, I32, P, I64, P, P, P, C.c_size_t, P]
+        patt, ph = C.POINTER(gs_attention), C.POINTER(gs_heads)
+        lib.gs_cross_attention_workspace_bytes.argtypes = [patt, I32]
+        lib.gs_cross_attention_workspace_bytes.restype = C.c_size_t
+        lib.gs_cross_attention_fwd.argtypes = [patt, ph, ph, ph, ph, P, P, C.c_size_t, P]
+        lib.gs_cross_attention_bwd.argtypes = [patt, ph, ph, ph, ph, ph, P, ph, ph, ph, P, C.c_size_t, P]
+        for name in ("gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_cross_attention_fwd", "gs_cross_attention_bwd"):
+            getattr(lib, name).restype = C.c_int
         for name in ("gs_preprocess", "gs_bin_and_sort", "gs_render_fwd", "gs_render_bwd",
                      "gs_preprocess_bwd", "gs_device_error", "gs_version", "gs_selftest_timeout"):
             getattr(lib, name).restype = C.c_int

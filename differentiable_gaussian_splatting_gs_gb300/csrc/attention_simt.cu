@@ -1,0 +1,304 @@
+// Cross attention on the float32 pipes, for what the tensor-core kernels do not take: head dimensions
+// above 128. Every element type, stride, mask and length; products and sums in float32.
+//
+// Forward: a block of 256 threads per 64 queries of a head. It walks the keys in tiles of 64 with the
+// running maximum and sum of the softmax, so scores stay on chip. Backward: one kernel per 32 keys
+// (dk, dv; walks the queries of all heads that share the key head) and one per 32 queries (dq; walks
+// the keys). Each output is summed by one block in a fixed order: no atomics, the same bits every time,
+// at the price of forming S and dP twice.
+#include "attention.cuh"
+
+namespace gs {
+
+namespace {
+
+constexpr int kFM = 64, kFN = 64, kBM = 32;  // tiles of the forward and the backward kernels
+constexpr int kThreads = 256;
+
+// rows x DP floats of shared memory (row stride DP + 4) from rows first .. of a head's tensor; rows that
+// do not take part and columns from d on become 0.
+template <class T, int DP, int ROWS, bool KEYS>
+__device__ __forceinline__ void stage(float* dst, const AttnTensor& t, const AttnArgs& a, int b, int h, int first, int len) {
+    const T* src = head_base<T>(t, b, h);
+    for (int e = threadIdx.x; e < ROWS * DP; e += kThreads) {
+        const int r = e / DP, c = e % DP, row = first + r;
+        const bool in = c < a.d && (KEYS ? key_valid(a, b, row, len) : row < len);
+        dst[r * (DP + 4) + c] = in ? to_float(src[row * t.len_stride + c]) : 0.f;
+    }
+}
+
+// acc[i][j] = row (ty * R + i) of x . row (tx + 16 j) of y
+template <int DP, int R, int C>
+__device__ __forceinline__ void dots(const float* x, const float* y, int ty, int tx, float (&acc)[R][C]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        float4 u[R], v[C];
+#pragma unroll
+        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4*>(x + (ty * R + i) * (DP + 4) + d);
+#pragma unroll
+        for (int j = 0; j < C; ++j) v[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * (DP + 4) + d);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                acc[i][j] = fmaf(u[i].x, v[j].x, fmaf(u[i].y, v[j].y, fmaf(u[i].z, v[j].z, fmaf(u[i].w, v[j].w, acc[i][j]))));
+    }
+}
+
+// acc[i][m] += sum over n of p[ty * R + i][n] y[n][tx + 16 m] (p: row stride N + 4; y: DP + 4)
+template <int DP, int N, int R>
+__device__ __forceinline__ void accumulate(const float* p, const float* y, int ty, int tx, float (&acc)[R][DP / 16]) {
+    for (int n = 0; n < N; ++n) {
+        float u[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) u[i] = p[(ty * R + i) * (N + 4) + n];
+#pragma unroll
+        for (int m = 0; m < DP / 16; ++m) {
+            const float v = y[n * (DP + 4) + tx + 16 * m];
+#pragma unroll
+            for (int i = 0; i < R; ++i) acc[i][m] = fmaf(u[i], v, acc[i][m]);
+        }
+    }
+}
+
+template <class T, int DP, int R>
+__device__ __forceinline__ void store_rows(const AttnTensor& t, int d, int b, int h, int first, int len, int ty, int tx,
+                                           const float (&acc)[R][DP / 16], const float (&f)[R]) {
+    T* dst = static_cast<T*>(t.data) + b * t.batch_stride + h * t.head_stride;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int row = first + ty * R + i;
+        if (row >= len) continue;
+#pragma unroll
+        for (int m = 0; m < DP / 16; ++m)
+            if (tx + 16 * m < d) dst[row * t.len_stride + tx + 16 * m] = from_float<T>(acc[i][m] * f[i]);
+    }
+}
+
+struct Where {
+    int b, h, tile;
+};
+__device__ __forceinline__ Where where(int tiles, int heads) {
+    const int bh = blockIdx.x / tiles;
+    return {bh / heads, bh % heads, (int)blockIdx.x % tiles};
+}
+
+}  // namespace
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, int tiles) {
+    pdl_entry();
+    extern __shared__ float sm[];
+    float *sq = sm, *sk = sq + kFM * (DP + 4), *sv = sk + kFN * (DP + 4), *sp = sv + kFN * (DP + 4);
+    const Where w = where(tiles, a.heads);
+    const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int len = key_count(a, w.b);
+    stage<T, DP, kFM, false>(sq, a.q, a, w.b, w.h, w.tile * kFM, a.len_q);
+    float o[4][DP / 16] = {}, top[4], sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = -INFINITY, sum[i] = 0.f;
+    for (int n0 = 0; n0 < len; n0 += kFN) {
+        __syncthreads();
+        stage<T, DP, kFN, true>(sk, a.k, a, w.b, hk, n0, len);
+        stage<T, DP, kFN, true>(sv, a.v, a, w.b, hk, n0, len);
+        __syncthreads();
+        float s[4][4];
+        dots<DP>(sq, sk, ty, tx, s);
+        bool in[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) in[j] = key_valid(a, w.b, n0 + tx + 16 * j, len);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float m = top[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = in[j] ? s[i][j] * a.scale : -INFINITY;
+                m = fmaxf(m, s[i][j]);
+            }
+#pragma unroll
+            for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+            const float base = m == -INFINITY ? 0.f : m;  // no key so far: every term is exp(-inf) = 0
+            const float keep = expf(top[i] - base);
+            float t = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = expf(s[i][j] - base);
+                t += p;
+                sp[(ty * 4 + i) * (kFN + 4) + tx + 16 * j] = p;
+            }
+#pragma unroll
+            for (int k = 8; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
+            sum[i] = sum[i] * keep + t;
+            top[i] = m;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) o[i][c] *= keep;
+        }
+        __syncwarp();  // a row's probabilities are written and read by the same half warp
+        accumulate<DP, kFN>(sp, sv, ty, tx, o);
+    }
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+        const int row = w.tile * kFM + ty * 4 + i;
+        if (tx == 0 && row < a.len_q)
+            a.lse[((long long)w.b * a.heads + w.h) * a.len_q + row] = sum[i] == 0.f ? -INFINITY : top[i] + logf(sum[i]);
+    }
+    store_rows<T, DP>(a.out, a.d, w.b, w.h, w.tile * kFM, a.len_q, ty, tx, o, f);
+}
+
+// P and dS of a 32 x 32 tile (queries x keys, or transposed for the dk/dv kernel) into shared memory.
+template <int DP, bool T_>
+__device__ __forceinline__ void tile_gradient(const AttnArgs& a, const float* sq, const float* sdo, const float* sk, const float* sv,
+                                              float* sp, float* sds, const float* lse, const float* delta, int b, int q0,
+                                              int n0, int len, int ty, int tx) {
+    float s[2][2], dp[2][2];
+    dots<DP>(T_ ? sk : sq, T_ ? sq : sk, ty, tx, s);
+    dots<DP>(T_ ? sv : sdo, T_ ? sdo : sv, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = ty * 2 + i, c = tx + 16 * j, qi = q0 + (T_ ? c : r), n = n0 + (T_ ? r : c);
+            const bool in = qi < a.len_q && key_valid(a, b, n, len);
+            const float p = in ? expf(s[i][j] * a.scale - lse[qi]) : 0.f;
+            if (T_) sp[r * (kBM + 4) + c] = p;
+            sds[r * (kBM + 4) + c] = in ? p * (dp[i][j] - delta[qi]) * a.scale : 0.f;
+        }
+}
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, int tiles) {
+    pdl_entry();
+    extern __shared__ float sm[];
+    constexpr int kRow = kBM * (DP + 4);
+    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + kBM * (kBM + 4);
+    const Where w = where(tiles, a.kv_heads);
+    const int share = a.heads / a.kv_heads, ty = threadIdx.x / 16, tx = threadIdx.x % 16, n0 = w.tile * kBM;
+    const int len = key_count(a, w.b);
+    float dk[2][DP / 16] = {}, dv[2][DP / 16] = {};
+    if (n0 < len) {
+        stage<T, DP, kBM, true>(sk, a.k, a, w.b, w.h, n0, len);
+        stage<T, DP, kBM, true>(sv, a.v, a, w.b, w.h, n0, len);
+        for (int h = w.h * share; h < (w.h + 1) * share; ++h) {
+            const long long row = ((long long)w.b * a.heads + h) * a.len_q;
+            for (int q0 = 0; q0 < a.len_q; q0 += kBM) {
+                __syncthreads();
+                stage<T, DP, kBM, false>(sq, a.q, a, w.b, h, q0, a.len_q);
+                stage<T, DP, kBM, false>(sdo, a.dout, a, w.b, h, q0, a.len_q);
+                __syncthreads();
+                tile_gradient<DP, true>(a, sq, sdo, sk, sv, sp, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
+                __syncwarp();
+                accumulate<DP, kBM>(sp, sdo, ty, tx, dv);
+                accumulate<DP, kBM>(sds, sq, ty, tx, dk);
+            }
+        }
+    }
+    const float one[2] = {1.f, 1.f};
+    store_rows<T, DP>(a.dk, a.d, w.b, w.h, n0, a.len_k, ty, tx, dk, one);
+    store_rows<T, DP>(a.dv, a.d, w.b, w.h, n0, a.len_k, ty, tx, dv, one);
+}
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int tiles) {
+    pdl_entry();
+    extern __shared__ float sm[];
+    constexpr int kRow = kBM * (DP + 4);
+    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sds = sdo + kRow;
+    const Where w = where(tiles, a.heads);
+    const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16, q0 = w.tile * kBM;
+    const int len = key_count(a, w.b);
+    const long long row = ((long long)w.b * a.heads + w.h) * a.len_q;
+    stage<T, DP, kBM, false>(sq, a.q, a, w.b, w.h, q0, a.len_q);
+    stage<T, DP, kBM, false>(sdo, a.dout, a, w.b, w.h, q0, a.len_q);
+    float dq[2][DP / 16] = {};
+    for (int n0 = 0; n0 < len; n0 += kBM) {
+        __syncthreads();
+        stage<T, DP, kBM, true>(sk, a.k, a, w.b, hk, n0, len);
+        stage<T, DP, kBM, true>(sv, a.v, a, w.b, hk, n0, len);
+        __syncthreads();
+        tile_gradient<DP, false>(a, sq, sdo, sk, sv, nullptr, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
+        __syncwarp();
+        accumulate<DP, kBM>(sds, sk, ty, tx, dq);
+    }
+    const float one[2] = {1.f, 1.f};
+    store_rows<T, DP>(a.dq, a.d, w.b, w.h, q0, a.len_q, ty, tx, dq, one);
+}
+
+// delta = sum over the head's elements of dout out, a warp per query and head.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_attn_delta(const AttnArgs a) {
+    pdl_entry();
+    const long long rows = (long long)a.batch * a.heads * a.len_q;
+    const long long warp = ((long long)blockIdx.x * kThreads + threadIdx.x) / 32;
+    if (warp >= rows) return;
+    const int lane = threadIdx.x & 31, i = (int)(warp % a.len_q);
+    const long long bh = warp / a.len_q;
+    const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+    const T* o = head_base<T>(a.out, b, h) + i * a.out.len_stride;
+    const T* d = head_base<T>(a.dout, b, h) + i * a.dout.len_stride;
+    float s = 0.f;
+    for (int c = lane; c < a.d; c += 32) s = fmaf(to_float(o[c]), to_float(d[c]), s);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0) a.delta[warp] = s;
+}
+
+namespace {
+
+template <class K>
+cudaError_t launch_tiles(K kernel, const AttnArgs& a, int rows, int tile, int heads, size_t smem, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e) return e;
+    const int tiles = (rows + tile - 1) / tile;
+    const long long blocks = (long long)tiles * heads * a.batch;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, st, a, tiles);
+}
+
+template <class T, int DP>
+cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
+    const size_t smem = sizeof(float) * ((kFM + 2 * kFN) * (DP + 4) + kFM * (kFN + 4));
+    return launch_tiles(k_attn_fwd_simt<T, DP>, a, a.len_q, kFM, a.heads, smem, st);
+}
+
+template <class T, int DP>
+cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (4 * kBM * (DP + 4) + 2 * kBM * (kBM + 4));
+    cudaError_t e = launch_tiles(k_attn_dq_simt<T, DP>, a, a.len_q, kBM, a.heads, smem, st);
+    return e ? e : launch_tiles(k_attn_dkv_simt<T, DP>, a, a.len_k, kBM, a.kv_heads, smem, st);
+}
+
+template <class T>
+cudaError_t typed(const AttnArgs& a, bool backward, cudaStream_t st) {
+    if (a.d <= 32) return backward ? bwd<T, 32>(a, st) : fwd<T, 32>(a, st);
+    if (a.d <= 64) return backward ? bwd<T, 64>(a, st) : fwd<T, 64>(a, st);
+    if (a.d <= 128) return backward ? bwd<T, 128>(a, st) : fwd<T, 128>(a, st);
+    return backward ? bwd<T, 256>(a, st) : fwd<T, 256>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_delta(const AttnArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.batch * a.heads * a.len_q;
+    if (rows == 0) return cudaSuccess;
+    const long long blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    count_launches(1);
+    auto* kernel = a.dtype == GS_DTYPE_F32 ? k_attn_delta<float> : a.dtype == GS_DTYPE_F16 ? k_attn_delta<__half> : k_attn_delta<__nv_bfloat16>;
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+}
+
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t st) {
+    if (a.dtype == GS_DTYPE_F32) return typed<float>(a, backward, st);
+    if (a.dtype == GS_DTYPE_F16) return typed<__half>(a, backward, st);
+    return typed<__nv_bfloat16>(a, backward, st);
+}
+
+}  // namespace gs

@@ -808,5 +808,167 @@ int gs_train_step_host(gs_step_context* ctx, const gs_params* hp, const float* h
     return GS_OK;
 }
 
+// ---- layer norm and cross attention -------------------------------------------------------------
+
 }  // extern "C"
 
+namespace gs {
+namespace {
+
+size_t elem_bytes(int dtype) { return dtype == GS_DTYPE_F32 ? 4 : 2; }
+
+int check_norm(const char* where, int64_t rows, int64_t cols, int dtype, const void* weight, int wdtype) {
+    if (dtype < GS_DTYPE_F32 || dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "%s: bad dtype %d", where, dtype);
+    if (wdtype != dtype && wdtype != GS_DTYPE_F32) return fail(GS_ERR_ARG, "%s: weight_dtype %d with dtype %d", where, wdtype, dtype);
+    if (rows < 0 || rows > (1ll << 40)) return fail(GS_ERR_ARG, "%s: rows = %lld", where, (long long)rows);
+    if (cols < 1 || cols >= (1ll << 30)) return fail(GS_ERR_ARG, "%s: cols = %lld outside 1..2^30-1", where, (long long)cols);
+    if (!aligned(weight, elem_bytes(wdtype))) return fail(GS_ERR_ARG, "%s: weight misaligned", where);
+    return GS_OK;
+}
+
+int check_rows(const char* where, const char* name, const void* p, int64_t stride, int64_t rows, int64_t cols, int dtype) {
+    if (rows == 0) return GS_OK;
+    if (!p || !aligned(p, elem_bytes(dtype))) return fail(GS_ERR_ARG, "%s: %s is NULL or misaligned", where, name);
+    if (rows > 1 && (stride < cols || stride > (1ll << 40)))
+        return fail(GS_ERR_ARG, "%s: row stride %lld of %s, cols %lld", where, (long long)stride, name, (long long)cols);
+    return GS_OK;
+}
+
+int check_attention(const gs_attention* a, AttnArgs& r) {
+    if (!a) return fail(GS_ERR_ARG, "attention is NULL");
+    if (a->dtype < GS_DTYPE_F32 || a->dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "attention: bad dtype %d", a->dtype);
+    if (a->batch < 0 || a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
+        return fail(GS_ERR_ARG, "attention: batch %d, heads %d, kv_heads %d (heads must be a positive multiple of kv_heads)",
+                    a->batch, a->heads, a->kv_heads);
+    if (a->head_dim < 1 || a->head_dim > 256) return fail(GS_ERR_ARG, "attention: head_dim %d outside 1..256", a->head_dim);
+    constexpr int kMaxLen = 1 << 30;
+    if (a->len_q < 0 || a->len_k < 0 || a->len_q > kMaxLen || a->len_k > kMaxLen)
+        return fail(GS_ERR_ARG, "attention: len_q %d, len_k %d outside 0..2^30", a->len_q, a->len_k);
+    // every kernel's grid is a one-dimensional count of tiles of at least one row of one head
+    if ((double)a->batch * a->heads * (a->len_q > a->len_k ? a->len_q : a->len_k) > 2147483647.0)
+        return fail(GS_ERR_ARG, "attention: batch x heads x length is 2^31 or more");
+    if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return fail(GS_ERR_ARG, "attention: scale must be finite and not negative");
+    if (!aligned(a->k_len, 4)) return fail(GS_ERR_ARG, "attention: k_len misaligned");
+    if (a->key_mask && a->batch > 1 && a->key_mask_stride < 0) return fail(GS_ERR_ARG, "attention: negative key_mask_stride");
+    r = AttnArgs{};
+    r.k_len = a->k_len;
+    r.key_mask = a->key_mask;
+    r.mask_stride = a->key_mask_stride;
+    r.dtype = a->dtype;
+    r.batch = a->batch;
+    r.heads = a->heads;
+    r.kv_heads = a->kv_heads;
+    r.len_q = a->len_q;
+    r.len_k = a->len_k;
+    r.d = a->head_dim;
+    r.scale = a->scale == 0.f ? (float)(1.0 / std::sqrt((double)a->head_dim)) : a->scale;
+    r.spin_limit = a->spin_limit == 0u ? (1u << 18) : a->spin_limit;
+    return GS_OK;
+}
+
+int check_heads(const gs_heads* t, const char* name, const AttnArgs& a, int len, AttnTensor& r) {
+    if (!t) return fail(GS_ERR_ARG, "attention: %s is NULL", name);
+    if (a.batch > 0 && len > 0 && (!t->data || !aligned(t->data, elem_bytes(a.dtype))))
+        return fail(GS_ERR_ARG, "attention: %s data is NULL or misaligned", name);
+    r = AttnTensor{t->data, t->batch_stride, t->len_stride, t->head_stride};
+    return GS_OK;
+}
+
+int check_workspace(const AttnArgs& a, bool backward, void* workspace, size_t bytes) {
+    const size_t need = attn_workspace_bytes(a, backward);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || bytes < need))
+        return fail(GS_ERR_ARG, "attention: workspace NULL, not 256-byte aligned or smaller than %zu bytes", need);
+    return GS_OK;
+}
+
+}  // namespace
+}  // namespace gs
+
+extern "C" {
+
+int gs_layer_norm_fwd(const void* x, int64_t x_stride, int64_t rows, int64_t cols, int32_t dtype, const void* weight,
+                      const void* bias, int32_t weight_dtype, float eps, void* y, int64_t y_stride, float* mean,
+                      float* rstd, void* stream) {
+    const char* me = "gs_layer_norm_fwd";
+    int s;
+    if ((s = check_norm(me, rows, cols, dtype, weight, weight_dtype)) || (s = check_rows(me, "x", x, x_stride, rows, cols, dtype)) ||
+        (s = check_rows(me, "y", y, y_stride, rows, cols, dtype)))
+        return s;
+    if (!aligned(bias, elem_bytes(weight_dtype))) return fail(GS_ERR_ARG, "%s: bias misaligned", me);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GS_ERR_ARG, "%s: eps must be finite and not negative", me);
+    if (rows > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
+        return fail(GS_ERR_ARG, "%s: mean or rstd is NULL or misaligned", me);
+    cudaError_t e = launch_norm_fwd(dtype, x, x_stride, rows, (int)cols, weight, bias, weight_dtype, eps, y, y_stride, mean, rstd,
+                                    as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+size_t gs_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 1 || cols >= (1ll << 30)) return 0;
+    return norm_bwd_workspace_bytes(rows, (int)cols);
+}
+
+int gs_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int64_t rows, int64_t cols,
+                      int32_t dtype, const float* mean, const float* rstd, const void* weight, int32_t weight_dtype,
+                      void* dx, int64_t dx_stride, void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    const char* me = "gs_layer_norm_bwd";
+    int s;
+    if ((s = check_norm(me, rows, cols, dtype, weight, weight_dtype)) || (s = check_rows(me, "dy", dy, dy_stride, rows, cols, dtype)) ||
+        (s = check_rows(me, "x", x, x_stride, rows, cols, dtype)) || (s = check_rows(me, "dx", dx, dx_stride, rows, cols, dtype)))
+        return s;
+    if (rows > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
+        return fail(GS_ERR_ARG, "%s: mean or rstd is NULL or misaligned", me);
+    if (!aligned(dweight, elem_bytes(weight_dtype)) || !aligned(dbias, elem_bytes(weight_dtype)))
+        return fail(GS_ERR_ARG, "%s: dweight or dbias misaligned", me);
+    const size_t need = dweight || dbias ? norm_bwd_workspace_bytes(rows, (int)cols) : 0;
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+        return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
+    cudaError_t e = launch_norm_bwd(dtype, dy, dy_stride, x, x_stride, rows, (int)cols, mean, rstd, weight, weight_dtype, dx,
+                                    dx_stride, dweight, dbias, static_cast<float*>(workspace), as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+size_t gs_cross_attention_workspace_bytes(const gs_attention* a, int32_t backward) {
+    AttnArgs r;
+    return check_attention(a, r) ? 0 : attn_workspace_bytes(r, backward != 0);
+}
+
+int gs_cross_attention_fwd(const gs_attention* a, const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                           const gs_heads* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    AttnArgs r;
+    int s;
+    if ((s = check_attention(a, r)) || (s = check_heads(q, "q", r, r.len_q, r.q)) || (s = check_heads(k, "k", r, r.len_k, r.k)) ||
+        (s = check_heads(v, "v", r, r.len_k, r.v)) || (s = check_heads(out, "out", r, r.len_q, r.out)))
+        return s;
+    if (r.batch == 0 || r.len_q == 0) return GS_OK;
+    if (!lse || !aligned(lse, 4)) return fail(GS_ERR_ARG, "attention: lse is NULL or misaligned");
+    if ((s = check_workspace(r, false, workspace, workspace_bytes))) return s;
+    r.lse = lse;
+    if (!(r.err = error_word(&s))) return s;
+    cudaError_t e = launch_attn_fwd(r, workspace, as_stream(stream));
+    return e ? cuda_fail(e, "gs_cross_attention_fwd") : GS_OK;
+}
+
+int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const gs_heads* out, const float* lse, const gs_heads* dq,
+                           const gs_heads* dk, const gs_heads* dv, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    AttnArgs r;
+    int s;
+    if ((s = check_attention(a, r)) || (s = check_heads(dout, "dout", r, r.len_q, r.dout)) ||
+        (s = check_heads(q, "q", r, r.len_q, r.q)) || (s = check_heads(k, "k", r, r.len_k, r.k)) ||
+        (s = check_heads(v, "v", r, r.len_k, r.v)) || (s = check_heads(out, "out", r, r.len_q, r.out)) ||
+        (s = check_heads(dq, "dq", r, r.len_q, r.dq)) || (s = check_heads(dk, "dk", r, r.len_k, r.dk)) ||
+        (s = check_heads(dv, "dv", r, r.len_k, r.dv)))
+        return s;
+    if (r.batch == 0 || (r.len_q == 0 && r.len_k == 0)) return GS_OK;
+    if (r.len_q > 0 && (!lse || !aligned(lse, 4))) return fail(GS_ERR_ARG, "attention: lse is NULL or misaligned");
+    if ((s = check_workspace(r, true, workspace, workspace_bytes))) return s;
+    r.lse = const_cast<float*>(lse);
+    if (!(r.err = error_word(&s))) return s;
+    cudaError_t e = launch_attn_bwd(r, workspace, as_stream(stream));
+    return e ? cuda_fail(e, "gs_cross_attention_bwd") : GS_OK;
+}
+
+}  // extern "C"

@@ -151,4 +151,36 @@ cudaError_t launch_preprocess2d_bwd(int deg, int n, const gs_params& p, const Ke
                                     const float* grad, float* dm, float* dls, float* dq, float* dlg, float* dsh,
                                     int accumulate, cudaStream_t st);
 
+// ---- the Gaussian decoder's operators ----------------------------------------------------------
+cudaError_t launch_norm_fwd(int dtype, const void* x, long long x_stride, long long rows, int cols, const void* weight,
+                            const void* bias, int wdtype, float eps, void* y, long long y_stride, float* mean,
+                            float* rstd, cudaStream_t st);
+size_t norm_bwd_workspace_bytes(long long rows, int cols);
+cudaError_t launch_norm_bwd(int dtype, const void* dy, long long dy_stride, const void* x, long long x_stride,
+                            long long rows, int cols, const float* mean, const float* rstd, const void* weight,
+                            int wdtype, void* dx, long long dx_stride, void* dweight, void* dbias, float* workspace,
+                            cudaStream_t st);
+
+// A [batch][length][heads][head_dim] tensor of a cross attention (strides in elements).
+struct AttnTensor {
+    void* data;
+    long long batch_stride, len_stride, head_stride;
+};
+struct AttnArgs {
+    AttnTensor q, k, v, out, dout, dq, dk, dv;
+    float *lse, *delta;  // [batch][heads][len_q]
+    const int* k_len;
+    const unsigned char* key_mask;
+    long long mask_stride;
+    int dtype, batch, heads, kv_heads, len_q, len_k, d;
+    float scale;
+    unsigned spin_limit;
+    unsigned* err;
+};
+size_t attn_workspace_bytes(const AttnArgs& a, bool backward);
+cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st);
+cudaError_t launch_attn_bwd(const AttnArgs& a, void* workspace, cudaStream_t st);
+cudaError_t launch_attn_delta(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t st);
+
 }  // namespace gs

@@ -472,6 +472,85 @@ int gs_train_step_host(gs_step_context* ctx, const gs_params* host_params, const
                        const gs_camera* cam, const gs_options* opt, const gs_tensors* host_grads, float* host_loss,
                        int64_t* host_n_dup, void* stream);
 
+/* ---- operators of a learned Gaussian decoder ------------------------------------------------
+ * A model that predicts a scene's Gaussians from images keeps a vector per Gaussian (or group of
+ * Gaussians), normalises these vectors and lets them read the image encoder's tokens; its training
+ * gradient comes back from the rasterizer (gs_preprocess_bwd) through both operators. Values are
+ * float32, float16 or bfloat16 in memory; sums, statistics and the softmax are float32.
+ * The calls enqueue on `stream`, allocate nothing and may be captured into a CUDA graph. The same
+ * call on the same inputs gives the same bits (no floating-point atomics).                       */
+#define GS_DTYPE_F32  0
+#define GS_DTYPE_F16  1
+#define GS_DTYPE_BF16 2
+
+/* Layer norm of `rows` rows of `cols` elements: y = (x - mean) rstd w + b with the row's mean and
+ * rstd = 1 / sqrt(mean of (x - mean)^2 + eps).
+ *   x, y: rows x cols of `dtype`, consecutive rows x_stride / y_stride elements apart (>= cols);
+ *   y may be x.
+ *   weight, bias: [cols] of weight_dtype (`dtype` or GS_DTYPE_F32), each may be NULL (1 and 0).
+ *   mean, rstd: [rows] float32, read again by the backward.
+ * rows >= 0, 1 <= cols < 2^30, eps >= 0. Rows that start on 16-byte boundaries with cols a multiple
+ * of 16 bytes are moved with 16-byte accesses, others element by element.
+ * Errors: GS_ERR_ARG, GS_ERR_CUDA.                                                               */
+int gs_layer_norm_fwd(const void* x, int64_t x_stride, int64_t rows, int64_t cols, int32_t dtype, const void* weight,
+                      const void* bias, int32_t weight_dtype, float eps, void* y, int64_t y_stride, float* mean,
+                      float* rstd, void* stream);
+
+/* Backward of gs_layer_norm_fwd: with xhat = (x - mean) rstd and g = w dy,
+ *   dx = rstd (g - mean(g) - xhat mean(g xhat)),  dweight = sum over rows of dy xhat,  dbias = sum of dy.
+ * dweight, dbias: [cols] of weight_dtype, overwritten; each may be NULL. dx may be dy or x. workspace:
+ * gs_layer_norm_workspace_bytes(rows, cols) bytes, 16-byte aligned (unused when both are NULL).
+ * Errors: GS_ERR_ARG, GS_ERR_CUDA.                                                               */
+size_t gs_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+int gs_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int64_t rows, int64_t cols,
+                      int32_t dtype, const float* mean, const float* rstd, const void* weight, int32_t weight_dtype,
+                      void* dx, int64_t dx_stride, void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* A [batch][length][heads][head_dim] tensor of the attention's dtype: strides in elements, any sign;
+ * the elements of a head are contiguous. */
+typedef struct gs_heads {
+    void*   data;
+    int64_t batch_stride, len_stride, head_stride;
+} gs_heads;
+
+/* Sizes and masks of a cross attention of len_q queries over len_k keys. A key j of batch entry b
+ * takes part when j < k_len[b] and key_mask[b key_mask_stride + j] != 0; what K and V hold at other
+ * keys (NaN included) changes nothing. Zero-initialised fields select the defaults beside them. */
+typedef struct gs_attention {
+    int32_t dtype;            /* GS_DTYPE_* of Q, K, V, the output and their gradients */
+    int32_t batch;
+    int32_t heads;            /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
+    int32_t kv_heads;
+    int32_t head_dim;         /* 1..256 */
+    int32_t len_q, len_k;     /* >= 0 */
+    float   scale;            /* of the scores; 0 = 1 / sqrt(head_dim); must not be negative */
+    const int32_t* k_len;     /* device [batch] or NULL = len_k; values are clamped to 0..len_k */
+    const uint8_t* key_mask;  /* device [batch][len_k] bytes or NULL = all take part */
+    int64_t key_mask_stride;
+    uint32_t spin_limit;      /* iterations before a device-side wait gives up; 0 = 1<<18 */
+} gs_attention;
+
+/* Cross attention: S = scale q k^T, P = softmax of S over the keys that take part, out = P v,
+ * lse = log sum exp S (float32 [batch][heads][len_q], natural logarithm). A query without any key has
+ * out = 0 and lse = -inf. out must not overlap an input. workspace: device buffer of
+ * gs_cross_attention_workspace_bytes(a, 0) bytes (may be 0), 256-byte aligned.
+ * Pointers must be aligned to their element. Errors: GS_ERR_ARG, GS_ERR_CUDA; a wait that gave up is
+ * reported by gs_device_error.                                                                   */
+size_t gs_cross_attention_workspace_bytes(const gs_attention* a, int32_t backward);
+int gs_cross_attention_fwd(const gs_attention* a, const gs_heads* q, const gs_heads* k, const gs_heads* v,
+                           const gs_heads* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of gs_cross_attention_fwd, from its out and lse: with delta = sum(dout out) per query and
+ * dS = scale P (dout v^T - delta): dq = dS k, dk = dS^T q, dv = P^T dout, overwritten; dk and dv are
+ * summed over the query heads that share a key head and 0 at keys that take no part; dq is 0 for a
+ * query without any key. workspace: gs_cross_attention_workspace_bytes(a, 1) bytes, 256-byte aligned.
+ * Errors as gs_cross_attention_fwd.                                                              */
+int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const gs_heads* out, const float* lse, const gs_heads* dq,
+                           const gs_heads* dk, const gs_heads* dv, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 /* Number of kernels this library has launched in this process (all devices, all threads). */
 int64_t gs_kernel_launches(void);
 

@@ -1,0 +1,264 @@
+"""GPU cross attention against the float64 one.
+
+Tolerances. u is the element type's unit roundoff. A score is off by at most 2^-20 of scale sum |q||k| (float32
+accumulation of up to 256 products) and so is lse; a probability by that, by 2^-20 for the exponential and the
+sum, and by u where it is rounded to feed a matrix product (twice at most: once more through the running
+maximum). out is then off by its probabilities' errors against sum P |v|, and rounded once. The gradients' bounds are the
+same terms carried through dS = scale P (dP - delta), with dP accumulated to 2^-20 of sum |dout||v| and delta
+formed from the rounded out (oracle.decoder.attention_bwd).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decoder
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from differentiable_gaussian_splatting_gs_gb300 import _abi, api  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+U = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 0.0, torch.float16: 2.0 ** -25, torch.bfloat16: 0.0}
+ACC = 2.0 ** -20
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rand(shape, dtype, seed, factor=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, device=DEV, generator=g) * factor).to(dtype)
+
+
+def _valid(b, lk, k_len, key_mask):
+    v = np.ones((b, lk), bool)
+    if k_len is not None:
+        v &= np.arange(lk)[None] < k_len.cpu().numpy()[:, None]
+    if key_mask is not None:
+        v &= key_mask.bool().cpu().numpy()
+    return v
+
+
+def _check(q, k, v, k_len=None, key_mask=None, scale=None, dout=None, backward=True, seed=0):
+    u, tiny = U[q.dtype], TINY[q.dtype]
+    b, lq, h, d = q.shape
+    sc = d ** -0.5 if scale is None else scale
+    valid = _valid(b, k.shape[1], k_len, key_mask)
+    out, lse = api.gs_cross_attention_fwd(q, k, v, k_len=k_len, key_mask=key_mask, scale=scale)
+    r = decoder.attention_fwd(_np(q), _np(k), _np(v), valid, sc)
+    size = r["size"].transpose(0, 2, 1)[..., None]
+    tol = (2 * u + ACC + 2 * ACC * size) * r["mag"] + u * np.abs(r["out"]) + tiny
+    got = _np(out)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - r["out"]) <= tol).all(), np.max(np.abs(got - r["out"]) / (tol + 1e-300))
+    empty = ~np.isfinite(r["lse"])
+    assert (_np(lse)[empty] == -np.inf).all()
+    fin = ~empty
+    assert (np.abs(_np(lse)[fin] - r["lse"][fin]) <= ACC * (1 + r["size"][fin] + np.abs(r["lse"][fin]))).all()
+    if backward:
+        dout = _rand(q.shape, q.dtype, seed + 77) if dout is None else dout
+        grads = api.gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=k_len, key_mask=key_mask, scale=scale)
+        w = decoder.attention_bwd(_np(dout), _np(q), _np(k), _np(v), valid, sc, rounding=u, accumulate=ACC)
+        for name, g in zip(("dq", "dk", "dv"), grads):
+            tol = w[name + "_tol"] + tiny
+            assert torch.isfinite(g).all(), name
+            bad = np.abs(_np(g) - w[name]) / (tol + 1e-300)
+            assert (bad <= 1).all(), (name, bad.max())
+        keys = np.broadcast_to(valid[:, :, None, None], grads[1].shape)
+        assert (_np(grads[1])[~keys] == 0).all() and (_np(grads[2])[~keys] == 0).all()
+    assert api.gs_device_error() == _abi.GS_OK
+    return out, lse
+
+
+def _qkv(b, lq, lk, h, hk, d, dtype, seed=0):
+    return _rand((b, lq, h, d), dtype, seed, 1.5), _rand((b, lk, hk, d), dtype, seed + 1), _rand((b, lk, hk, d), dtype, seed + 2)
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("b,lq,lk,h,hk,d", [
+    (1, 1, 1, 1, 1, 1), (1, 1, 300, 2, 2, 64), (2, 3, 5, 2, 1, 8), (1, 128, 128, 1, 1, 64), (1, 129, 127, 2, 2, 64),
+    (2, 200, 333, 4, 2, 64), (1, 300, 65, 3, 3, 40), (1, 257, 400, 6, 1, 128), (1, 64, 64, 2, 2, 32), (1, 70, 90, 2, 2, 80),
+    (1, 45, 70, 2, 1, 33), (1, 50, 130, 2, 2, 136), (1, 33, 65, 1, 1, 256), (1, 17, 100, 2, 2, 255), (1, 2, 2000, 4, 2, 64),
+    (1, 500, 1, 2, 2, 64), (1, 9, 5000, 2, 1, 128), (3, 1, 700, 8, 2, 96), (1, 1000, 33, 2, 2, 16), (1, 700, 700, 2, 2, 128)])
+def test_sizes(dtype, b, lq, lk, h, hk, d):
+    _check(*_qkv(b, lq, lk, h, hk, d, dtype), seed=lq)
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("lq", [1, 6, 150])
+@pytest.mark.parametrize("d", [64, 128, 48, 200])
+@pytest.mark.parametrize("kind", ["len", "keys", "both"])
+def test_masks_with_empty_rows_and_non_finite_masked_keys(dtype, lq, d, kind):
+    b, lk = 5, 270
+    q, k, v = _qkv(b, lq, lk, 4, 2, d, dtype, 3)
+    k_len = torch.tensor([270, 0, 1, 128, 129], dtype=torch.int32, device=DEV) if kind != "keys" else None
+    key_mask = None
+    if kind != "len":
+        g = torch.Generator(device="cuda").manual_seed(5)
+        key_mask = torch.rand(b, lk, device=DEV, generator=g) < 0.5
+        key_mask[3] = False
+        key_mask[4, :200] = False
+    bad = torch.from_numpy(~_valid(b, lk, k_len, key_mask)).to(DEV)
+    k[bad] = float("nan")
+    v[bad] = float("inf")
+    v[:, ::2][bad[:, ::2]] = float("nan")
+    _check(q, k, v, k_len=k_len, key_mask=key_mask, seed=d)
+
+
+def test_lengths_outside_the_range_are_clamped():
+    q, k, v = _qkv(3, 20, 50, 2, 2, 64, torch.bfloat16)
+    far = torch.tensor([-7, 51, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    near = torch.tensor([0, 50, 50], dtype=torch.int32, device=DEV)
+    a, b = (api.gs_cross_attention_fwd(q, k, v, k_len=n) for n in (far, near))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", list(U))
+def test_large_scores_and_values_of_the_types_range(dtype):
+    # scores of several hundred: one key takes all the weight; later keys raise the maximum again and again
+    q, k, v = _qkv(1, 140, 500, 2, 2, 64, dtype)
+    k = (k * torch.linspace(0.1, 12, 500, device=DEV)[None, :, None, None]).to(dtype)
+    _check(q, k, v, seed=1)
+    low = torch.full_like(k, -30.0)  # all scores equal and far below zero
+    _check(torch.ones_like(q), low, v, seed=2)
+    _check(q, k, v, scale=1e-3, seed=3)
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("lq,lk,d", [(150, 260, 64), (1, 260, 64), (150, 260, 40)])
+def test_strides_orders_and_misalignment(dtype, lq, lk, d):
+    b, h = 2, 4
+    q, k, v = _qkv(b, lq, lk, h, h, d, dtype, 9)
+    want, wl = api.gs_cross_attention_fwd(q, k, v)
+    dout = _rand(q.shape, dtype, 10)
+    grads = api.gs_cross_attention_bwd(dout, q, k, v, want, wl)
+
+    def head_first(t):  # [b, h, l, d] in memory
+        return t.transpose(1, 2).contiguous().transpose(1, 2)
+
+    def packed(t, pad, at):  # rows inside a wider buffer, off by `at` elements
+        big = torch.full((t.shape[0], t.shape[1], t.shape[2] * d + pad), 7.0, dtype=dtype, device=DEV)
+        view = big[:, :, at:at + t.shape[2] * d].unflatten(2, (t.shape[2], d))
+        view.copy_(t)
+        return view
+
+    def flipped(t):  # batch entries in reverse, one buffer
+        return t.flip(0).contiguous().as_strided(t.shape, t.stride(), 0) if t.shape[0] == 1 else t
+
+    for change in (head_first, lambda t: packed(t, 8, 0), lambda t: packed(t, 5, 3), lambda t: packed(t, 8, 1), flipped):
+        got, gl = api.gs_cross_attention_fwd(change(q), change(k), change(v),
+                                             out=(change(torch.zeros_like(q)), torch.empty_like(wl)))
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        into = tuple(change(torch.zeros_like(t)) for t in (q, k, v))
+        gg = api.gs_cross_attention_bwd(change(dout), change(q), change(k), change(v), change(want), wl, grads=into)
+        assert all(torch.equal(x, y) for x, y in zip(gg, grads))
+    # one batch entry, head or token broadcast to all (stride 0)
+    kb = k[:1].expand(b, -1, -1, -1)
+    _check(q, kb, v[:, :, :1].expand(-1, -1, h, -1), backward=False)
+
+
+def test_one_buffer_for_q_k_and_v_of_a_projection():
+    qkv = _rand((2, 200, 3 * 4, 64), torch.bfloat16, 1)
+    q, k, v = qkv[:, :, :4], qkv[:, :, 4:8], qkv[:, :, 8:]
+    _check(q, k, v)
+
+
+def test_writes_stay_inside_the_outputs():
+    b, lq, lk, h, d = 1, 130, 140, 2, 72
+    q, k, v = _qkv(b, lq, lk, h, h, d, torch.float16)
+    ob = torch.full((b, lq + 20, h, d + 16), 5.0, dtype=torch.float16, device=DEV)
+    out, lse = api.gs_cross_attention_fwd(q, k, v, out=(ob[:, 10:10 + lq, :, 8:8 + d], torch.empty(b, h, lq, device=DEV)))
+    assert torch.equal(out, api.gs_cross_attention_fwd(q, k, v)[0])
+    kb = torch.full((b, lk + 20, h, d + 16), 5.0, dtype=torch.float16, device=DEV)
+    vb, qb = kb.clone(), ob.clone()
+    inner = lambda t, n: t[:, 10:10 + n, :, 8:8 + d]  # noqa: E731
+    api.gs_cross_attention_bwd(_rand(q.shape, q.dtype, 3), q, k, v, out, lse, grads=(inner(qb, lq), inner(kb, lk), inner(vb, lk)))
+    for big, n in ((ob, lq), (kb, lk), (vb, lk)):
+        inner(big, n).fill_(5.0)
+        assert (big == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", list(U))
+def test_empty_lengths(dtype):
+    q, k, v = _qkv(2, 5, 0, 2, 2, 64, dtype)
+    out, lse = api.gs_cross_attention_fwd(q, k, v)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    dq, dk, dv = api.gs_cross_attention_bwd(q, q, k, v, out, lse)
+    assert (dq == 0).all() and dk.shape == k.shape
+    q, k, v = _qkv(2, 0, 5, 2, 2, 64, dtype)
+    out, lse = api.gs_cross_attention_fwd(q, k, v)
+    dq, dk, dv = api.gs_cross_attention_bwd(q, q, k, v, out, lse, grads=(q, torch.ones_like(k), torch.ones_like(v)))
+    assert out.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+    e = torch.empty(0, 4, 2, 64, dtype=dtype, device=DEV)
+    assert api.gs_cross_attention_fwd(e, e, e)[0].shape == e.shape
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("lq,mask", [(3, False), (260, False), (260, True)])
+def test_same_bits_twice_another_stream_and_graph(dtype, lq, mask):
+    q, k, v = _qkv(2, lq, 1500, 4, 2, 64, dtype)
+    m = torch.rand(2, 1500, device=DEV, generator=torch.Generator(device="cuda").manual_seed(1)) < 0.7 if mask else None
+    dout = _rand(q.shape, dtype, 4)
+
+    def both(stream=None):
+        o = api.gs_cross_attention_fwd(q, k, v, key_mask=m, stream=stream)
+        return o + api.gs_cross_attention_bwd(dout, q, k, v, *o, key_mask=m, stream=stream)
+
+    a = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = both(side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c = both()
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("h,hk", [(4, 4), (6, 2)])
+def test_gradients_against_differences(h, hk):
+    q, k, v = _qkv(1, 9, 14, h, hk, 32, torch.float32)
+    dout = _rand(q.shape, torch.float32, 5)
+    valid = np.ones((1, 14), bool)
+    valid[0, 10:] = False
+    n = torch.tensor([10], dtype=torch.int32, device=DEV)
+    out, lse = api.gs_cross_attention_fwd(q, k, v, k_len=n)
+    grads = api.gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=n)
+    g = np.random.default_rng(1)
+    args = [_np(t) for t in (q, k, v)]
+    for at, got in enumerate(grads):
+        u = g.standard_normal(args[at].shape)
+
+        def loss(t):
+            a = list(args)
+            a[at] = a[at] + t * u
+            return (decoder.attention_fwd(*a, valid, 32 ** -0.5)["out"] * _np(dout)).sum()
+
+        want, terms = (loss(1e-5) - loss(-1e-5)) / 2e-5, np.abs(_np(got) * u).sum()
+        assert abs((_np(got) * u).sum() - want) <= 1e-5 * terms
+
+
+def test_refusals():
+    q, k, v = _qkv(2, 5, 7, 4, 2, 64, torch.float16)
+    fwd = api.gs_cross_attention_fwd
+    i = torch.ones(2, dtype=torch.int32, device=DEV)
+    for bad in (lambda: fwd(q.double(), k, v), lambda: fwd(q, k.float(), v), lambda: fwd(q, k, v[:, :6]),
+                lambda: fwd(q[0], k, v), lambda: fwd(q[:, :, :3], k, v), lambda: fwd(q, k, v, k_len=i.long()),
+                lambda: fwd(q, k, v, k_len=i[:1]), lambda: fwd(q, k, v, key_mask=i), lambda: fwd(q, k, v, scale=0.0),
+                lambda: fwd(q, k, v, scale=-1.0), lambda: fwd(q, k.transpose(2, 3), v),
+                lambda: fwd(q.transpose(1, 3), k, v), lambda: fwd(q, k, v, key_mask=torch.ones(2, 7, device=DEV)),
+                lambda: fwd(q, k, v, out=(q[:, :4], torch.empty(2, 4, 5, device=DEV))),
+                lambda: fwd(q, k, v, out=(q.clone(), torch.empty(2, 5, 4, device=DEV)))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(_abi.GsError, match="head_dim"):
+        t = torch.zeros(1, 2, 2, 300, device=DEV)
+        fwd(t, t, t)
