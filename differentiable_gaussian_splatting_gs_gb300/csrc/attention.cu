@@ -1,19 +1,147 @@
-// Cross attention: which kernels a call runs, and its workspace.
-#include "attention.cuh"
+// Cross attention: which kernels a call runs, its workspace, and the tensor maps of its copies.
+#include <cudaTypedefs.h>
+
+#include "attention_tc.cuh"
 
 namespace gs {
 
 namespace {
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr int kMaxTcDim = 128;  // head dimensions above it go to the float32 kernels
 
-size_t delta_bytes(const AttnArgs& a) { return round256((size_t)a.batch * a.heads * a.len_q * sizeof(float)); }
+// What a call packs, how it splits its walks, and where the pieces lie in the workspace (byte offsets).
+struct Plan {
+    bool tc, pack_q, pack_kv, pack_do;
+    int planes, dp, nq, splits;
+    long long rows_k;  // rows of a packed head of K or V
+    size_t count, index, q, k, v, part, part_lse, delta, bytes;
+};
+
+bool copyable(const AttnTensor& t, const AttnArgs& a, int len) {
+    // a tiled copy wants 16-byte aligned rows and positive strides; the caller's sizes of 1 have no stride
+    auto fine = [](long long stride, long long n) { return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 38)); };
+    return a.d % 8 == 0 && reinterpret_cast<uintptr_t>(t.data) % 16 == 0 && fine(t.batch_stride, a.batch) &&
+           fine(t.len_stride, len) && fine(t.head_stride, 2);
+}
+
+// `tensors`: whether a's tensors are known; the size of the workspace counts on every one being packed.
+Plan plan(const AttnArgs& a, bool backward, bool tensors) {
+    Plan p{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const size_t bq = (size_t)a.batch * a.heads * a.len_q, bk = (size_t)a.batch * a.kv_heads;
+    if (backward) p.delta = take(bq * sizeof(float));
+    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && !backward;
+    if (p.tc) {
+        const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
+        p.planes = wide ? 3 : 1;
+        p.dp = a.d <= 64 ? 64 : 128;
+        p.rows_k = ((long long)a.len_k + kTileRows - 1) / kTileRows * kTileRows;
+        p.pack_q = wide || !tensors || !copyable(a.q, a, a.len_q);
+        p.pack_kv = wide || masked || !tensors || !copyable(a.k, a, a.len_k) || !copyable(a.v, a, a.len_k);
+        const int sms = device_sm_count();
+        const bool two = !(wide && p.dp == 128) && (long long)((a.len_q + 255) / 256) * a.heads * a.batch >= sms;
+        p.nq = two ? 2 : 1;
+        const long long blocks = (long long)((a.len_q + 128 * p.nq - 1) / (128 * p.nq)) * a.heads * a.batch;
+        const long long key_tiles = p.rows_k / kTileRows;
+        long long splits = blocks > 0 ? sms / blocks : 1;
+        if (splits > (key_tiles + 1) / 2) splits = (key_tiles + 1) / 2;
+        p.splits = splits < 1 ? 1 : (int)splits;
+        const size_t row = (size_t)p.planes * p.dp * 2;
+        if (a.key_mask) {
+            p.count = take(a.batch * sizeof(int));
+            p.index = take((size_t)a.batch * a.len_k * sizeof(int));
+        }
+        if (p.pack_q) p.q = take(bq * row);
+        if (p.pack_kv) {
+            p.k = take(bk * p.rows_k * row);
+            p.v = take(bk * p.rows_k * row);
+        }
+        if (p.splits > 1) {
+            p.part = take((size_t)p.splits * bq * p.dp * sizeof(float));
+            p.part_lse = take((size_t)p.splits * bq * sizeof(float));
+        }
+    }
+    p.bytes = at;
+    return p;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::atomic<void*> cache{nullptr};
+    void* f = cache.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cache.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+cudaError_t encode(TcTensor& t, bool half, void* base, const long long (&dim)[4], const long long (&stride)[3], int box_rows) {
+    auto f = encoder();
+    if (!f) return cudaErrorNotSupported;
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)dim[i];
+    for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)(dim[i + 1] > 1 ? stride[i] * 2 : 16);
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
+    const CUresult r = f(&t.map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+                         strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The tensor as the kernels read it: packed at `at`, or the caller's.
+cudaError_t operand(TcTensor& t, const Plan& p, const AttnArgs& a, const AttnTensor& src, int heads, int len, bool packed,
+                    void* at, long long rows, int box_rows) {
+    t.packed = packed;
+    const bool half = a.dtype == GS_DTYPE_F16;
+    if (packed)
+        return encode(t, half, at, {p.dp, rows, p.planes, (long long)a.batch * heads},
+                      {p.dp, rows * p.dp, p.planes * rows * p.dp}, box_rows);
+    return encode(t, half, src.data, {a.d, len, heads, a.batch}, {src.len_stride, src.head_stride, src.batch_stride}, box_rows);
+}
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnArgs& a, bool backward) { return backward ? delta_bytes(a) : 0; }
+size_t attn_workspace_bytes(const AttnArgs& a, bool backward) { return plan(a, backward, false).bytes; }
 
-cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st) { return launch_attn_simt(a, false, st); }
+cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st) {
+    const Plan p = plan(a, false, true);
+    if (!p.tc) return launch_attn_simt(a, false, st);
+    char* ws = static_cast<char*>(workspace);
+    cudaError_t e = cudaSuccess;
+    TcArgs t{a, nullptr, nullptr, nullptr, 0, p.splits};
+    int* index = nullptr;
+    if (a.key_mask) {
+        int* count = reinterpret_cast<int*>(ws + p.count);
+        index = reinterpret_cast<int*>(ws + p.index);
+        if ((e = launch_attn_index(a, count, index, st))) return e;
+        t.count = count;
+    }
+    if (p.pack_q && (e = launch_attn_pack(a, a.q, a.heads, a.len_q, false, nullptr, nullptr, p.planes, p.dp, a.len_q, ws + p.q, st)))
+        return e;
+    if (p.pack_kv && ((e = launch_attn_pack(a, a.k, a.kv_heads, a.len_k, true, t.count, index, p.planes, p.dp, p.rows_k, ws + p.k, st)) ||
+                      (e = launch_attn_pack(a, a.v, a.kv_heads, a.len_k, true, t.count, index, p.planes, p.dp, p.rows_k, ws + p.v, st))))
+        return e;
+    const int bn = p.planes == 3 && p.dp == 128 ? 64 : 128;
+    TcTensor q, k, v;
+    if ((e = operand(q, p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, kTileRows)) ||
+        (e = operand(k, p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, bn)) ||
+        (e = operand(v, p, a, a.v, a.kv_heads, a.len_k, p.pack_kv, ws + p.v, p.rows_k, bn)))
+        return e;
+    if (p.splits > 1) {
+        t.part = reinterpret_cast<float*>(ws + p.part);
+        t.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
+    }
+    if ((e = launch_attn_fwd_tc(t, q, k, v, p.planes, p.dp, p.nq, st))) return e;
+    return p.splits > 1 ? launch_attn_combine(a, t.part, t.part_lse, p.splits, p.dp, st) : cudaSuccess;
+}
 
 cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t st) {
     AttnArgs a = args;

@@ -1,0 +1,330 @@
+// Cross attention, forward, on the tensor cores.
+//
+// A block takes NQ tiles of 128 queries of one head and walks the keys in tiles of BN. One warp copies K and
+// V tiles ahead, one thread issues the products S = Q K^T and O += P V, and a warpgroup per query tile turns S
+// into P: thread = query, so the row's maximum and sum need no exchange. S and P share columns of tensor
+// memory, O stays there too. With two query tiles the products of one run beside the softmax of the other:
+//   products: ... O0 += P0 V_j, S0 = Q0 K_j+1, O1 += P1 V_j, S1 = Q1 K_j+1, ...
+// The running maximum is only raised, and O rescaled, when a row's scores pass the one in use by 2^8: P may
+// then reach 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
+#include "attention_tc.cuh"
+
+namespace gs {
+
+template <int DP, int PL, int NQ, int BN>
+struct FwdShape {
+    static constexpr int kQ = PL * DP * kTileRows * 2;  // bytes of a query tile
+    static constexpr int kKV = PL * DP * BN * 2;        // bytes of a tile of K or V
+    static constexpr int kRoom = 226 * 1024 - 1024 - NQ * kQ;
+    static constexpr int kStages = kRoom / (2 * kKV) > 4 ? 4 : kRoom / (2 * kKV);
+    static constexpr int kSmem = NQ * kQ + kStages * 2 * kKV + 1024;
+    static constexpr int kP = PL * BN / 2 > BN ? PL * BN / 2 : BN;  // columns that S and then P take
+    static constexpr int kO = NQ * kP;                              // first column of O
+    // two query tiles: a third warpgroup of which two warps work, so that registers can be moved between whole
+    // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 224 + 128 x 56
+    static constexpr int kThreads = NQ == 2 ? 384 : 192;
+    static constexpr int kCols = kO + NQ * DP <= 256 ? 256 : 512;
+    static_assert(kO + NQ * DP <= 512 && kStages >= 1);
+};
+
+template <class T, int DP, int PL, int NQ, int BN>
+__global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
+    k_attn_fwd(const __grid_constant__ TcArgs t, const __grid_constant__ TcTensor tq, const __grid_constant__ TcTensor tk,
+               const __grid_constant__ TcTensor tv) {
+    using S = FwdShape<DP, PL, NQ, BN>;
+    using C = Pairs<PL>;
+    constexpr int kSt = S::kStages;
+    pdl_entry();
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t q_full, k_full[kSt], v_full[kSt], k_free[kSt], v_free[kSt], s_full[NQ], p_full[NQ], o_full[NQ], drain;
+    __shared__ uint32_t tmem_base;
+    const AttnArgs& a = t.a;
+    const uint32_t sq = (smem_u32(raw) + 1023u) & ~1023u, sk = sq + NQ * S::kQ, sv = sk + kSt * S::kKV;
+    int at = blockIdx.x;
+    const int tile = at % t.tiles;
+    at /= t.tiles;
+    const int split = at % t.splits;
+    at /= t.splits;
+    const int h = at % a.heads, b = at / a.heads, hk = h / (a.heads / a.kv_heads);
+    const int keys = keys_of(t, b), q0 = tile * NQ * kTileRows;
+    // this split's key tiles
+    const int all = (keys + BN - 1) / BN, per = (all + t.splits - 1) / t.splits;
+    const int first = min(split * per, all), n = min(per, all - first);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned limit = a.spin_limit;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&q_full, 1);
+        for (int i = 0; i < kSt; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_free[i], 1);
+        }
+        for (int i = 0; i < NQ; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        mbar_init(&drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == NQ * 4) tmem_alloc<S::kCols>(&tmem_base);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_base;
+
+    if (warp >= NQ * 4) {
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == NQ * 4) {  // copies
+            if (lane == 0 && n > 0) {
+                bool ok = true;
+                int sent = 0;
+                mbar_arrive_expect_tx(&q_full, NQ * S::kQ);
+                for (int i = 0; i < NQ; ++i) load_rows<DP, PL, kTileRows>(sq + i * S::kQ, tq, q0 + i * kTileRows, b, h, a.heads, &q_full);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = j % kSt;
+                    const unsigned ph = (j / kSt + 1) & 1;
+                    if (j >= kSt && !(ok = mbar_wait_bounded(&k_free[s], ph, limit, a.err))) break;
+                    mbar_arrive_expect_tx(&k_full[s], S::kKV);
+                    load_rows<DP, PL, BN>(sk + s * S::kKV, tk, (first + j) * BN, b, hk, a.kv_heads, &k_full[s]);
+                    sent = 2 * j + 1;
+                    if (j >= kSt && !(ok = mbar_wait_bounded(&v_free[s], ph, limit, a.err))) break;
+                    mbar_arrive_expect_tx(&v_full[s], S::kKV);
+                    load_rows<DP, PL, BN>(sv + s * S::kKV, tv, (first + j) * BN, b, hk, a.kv_heads, &v_full[s]);
+                    sent = 2 * j + 2;
+                }
+                // every copy lands before the block ends, whatever became of its reader
+                mbar_wait_bounded(&q_full, 0, kDrainLimit, a.err);
+                const int nk = (sent + 1) / 2, nv = sent / 2;
+                for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
+                for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
+            }
+        } else if (warp == NQ * 4 + 1 && lane == 0 && n > 0) {  // products
+            const uint32_t qk_desc = mma_desc<T>(BN, false), pv_desc = mma_desc<T>((a.d + 15) / 16 * 16, true);
+            const int steps = (a.d + 15) / 16;  // of the inner dimension of Q K^T
+            auto scores = [&](int i, int s) {
+                bool add = false;
+#pragma unroll
+                for (int c = 0; c < C::n; ++c) {
+                    const uint32_t qa = sq + i * S::kQ + C::a(c) * DP * kTileRows * 2, kb = sk + s * S::kKV + C::b(c) * DP * BN * 2;
+                    for (int x = 0; x < steps; ++x, add = true)
+                        mma_ss(tm + i * S::kP, tile_desc(qa + (x / 4) * kTileRows * 128 + (x % 4) * 32),
+                               tile_desc(kb + (x / 4) * BN * 128 + (x % 4) * 32), qk_desc, add);
+                }
+                mma_commit(&s_full[i]);
+            };
+            auto values = [&](int i, int s, bool add) {
+#pragma unroll
+                for (int c = 0; c < C::n; ++c) {
+                    const uint32_t vb = sv + s * S::kKV + C::b(c) * DP * BN * 2;
+#pragma unroll
+                    for (int x = 0; x < BN / 16; ++x, add = true)
+                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + C::a(c) * (BN / 2) + x * 8, tile_desc(vb + x * 2048, BN * 128),
+                               pv_desc, add);
+                }
+            };
+            bool ok = mbar_wait_bounded(&q_full, 0, limit, a.err) && mbar_wait_bounded(&k_full[0], 0, limit, a.err);
+            tc_fence_after();
+            if (ok) {
+                for (int i = 0; i < NQ; ++i) scores(i, 0);
+                mma_commit(&k_free[0]);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int s = j % kSt, s1 = (j + 1) % kSt;
+                for (int i = 0; i < NQ && ok; ++i) {
+                    if (i == 0) ok = mbar_wait_bounded(&v_full[s], (j / kSt) & 1, limit, a.err);
+                    ok = ok && mbar_wait_bounded(&p_full[i], j & 1, limit, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(i, s, j > 0);
+                    if (i == NQ - 1) mma_commit(&v_free[s]);
+                    if (j + 1 < n) {
+                        if (i == 0) ok = mbar_wait_bounded(&k_full[s1], ((j + 1) / kSt) & 1, limit, a.err);
+                        if (!ok) break;
+                        scores(i, s1);
+                        if (i == NQ - 1) mma_commit(&k_free[s1]);
+                    } else {
+                        mma_commit(&o_full[i]);
+                    }
+                }
+            }
+            // no product is in flight when the tensor memory is freed
+            mma_commit(&drain);
+            mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
+        }
+    } else {  // softmax: thread = query
+        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + i * S::kP + lanes, to = tm + S::kO + i * DP + lanes;
+        const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
+        float top = -INFINITY, sum = 0.f;               // top: raw score in use as the maximum
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            if (!(ok = warp_wait(&s_full[i], j & 1, limit, a.err))) break;
+            tc_fence_after();
+            uint32_t x[BN / 32][32];
+#pragma unroll
+            for (int g = 0; g < BN / 32; ++g) tmem_ld32(ts + g * 32, x[g]);
+            tmem_wait_ld();
+            const int left = keys - (first + j) * BN;
+            if (left < BN) {
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (g * 32 + e >= left) x[g][e] = 0xff800000u;  // -inf
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int g = 0; g < BN / 32; ++g)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[g][e]));
+            const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            const bool raise = (m - top) * c > 8.f || top == -INFINITY;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
+                if (raise) top = m;
+                sum *= keep;
+                if (j > 0) {
+#pragma unroll
+                    for (int g = 0; g < DP / 32; ++g) {
+                        uint32_t o[32];
+                        tmem_ld32(to + g * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                        tmem_st32(to + g * 32, o);
+                    }
+                }
+            }
+            const float base = top == -INFINITY ? 0.f : top * c;  // a score of -inf is no error: exp(-inf) = 0
+            const f32x2 c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
+            f32x2 s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+            const f32x2 one = f2_pack(1.f, 1.f);
+#pragma unroll
+            for (int g = 0; g < BN / 32; ++g) {
+                uint32_t p[PL][16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[g][2 * e]), __uint_as_float(x[g][2 * e + 1])), c2, b2));
+                    float u = ex2_approx(y.x), w = ex2_approx(y.y);
+                    s2[e & 1] = f2_fma(f2_pack(u, w), one, s2[e & 1]);
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        p[q][e] = pack2<T>(u, w);
+                        if (q + 1 < PL) {  // what the plane leaves (bfloat16 is the upper half of a float)
+                            u -= __uint_as_float(p[q][e] << 16);
+                            w -= __uint_as_float(p[q][e] & 0xffff0000u);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < PL; ++q) tmem_st16(ts + q * (BN / 2) + g * 16, p[q]);
+            }
+            const float2 sa = f2_unpack(s2[0]), sb = f2_unpack(s2[1]);
+            sum += (sa.x + sa.y) + (sb.x + sb.y);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[i]);
+        }
+        if (n > 0 && ok) ok = warp_wait(&o_full[i], 0, limit, a.err);
+        tc_fence_after();
+        const bool live = row < a.len_q && ok;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        const float lse = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
+        const long long qrow = ((long long)b * a.heads + h) * a.len_q + row;
+        if (t.part) {
+            const long long prow = (long long)split * a.batch * a.heads * a.len_q + qrow;
+            if (live) t.part_lse[prow] = lse;
+            if (n > 0) {
+#pragma unroll
+                for (int g = 0; g < DP / 32; ++g) {
+                    uint32_t o[32];
+                    tmem_ld32(to + g * 32, o);
+                    tmem_wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(t.part + prow * DP + g * 32 + e) =
+                                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                            __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else {
+            if (live) a.lse[qrow] = lse;
+            using E = typename std::conditional<PL == 3, float, T>::type;
+            E* dst = static_cast<E*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride + row * a.out.len_stride;
+            constexpr int V = 16 / (int)sizeof(E);
+            const bool vec = a.d % V == 0 && a.out.batch_stride % V == 0 && a.out.head_stride % V == 0 &&
+                             a.out.len_stride % V == 0 && reinterpret_cast<uintptr_t>(a.out.data) % 16 == 0;
+#pragma unroll
+            for (int g = 0; g < DP / 32; ++g) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(to + g * 32, o);
+                    tmem_wait_ld();
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += V) {
+                        Pack<E, V> w;
+#pragma unroll
+                        for (int y = 0; y < V; ++y) w.v[y] = from_float<E>(n > 0 ? __uint_as_float(o[e + y]) * f : 0.f);
+                        const int col = g * 32 + e;
+                        if (vec) {
+                            if (col < a.d) *reinterpret_cast<Pack<E, V>*>(dst + col) = w;
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < V; ++y)
+                                if (col + y < a.d) dst[col + y] = w.v[y];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == NQ * 4) tmem_free<S::kCols>(tm);
+}
+
+namespace {
+
+template <class T, int DP, int PL, int NQ, int BN>
+cudaError_t run(TcArgs t, const TcTensor& q, const TcTensor& k, const TcTensor& v, cudaStream_t st) {
+    using S = FwdShape<DP, PL, NQ, BN>;
+    auto* kernel = k_attn_fwd<T, DP, PL, NQ, BN>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e) return e;
+    t.tiles = (t.a.len_q + NQ * kTileRows - 1) / (NQ * kTileRows);
+    const long long blocks = (long long)t.tiles * t.splits * t.a.heads * t.a.batch;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, st, t, q, k, v);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTensor& k, const TcTensor& v, int planes, int dp,
+                               int nq, cudaStream_t st) {
+    if (planes == 3) {
+        if (dp == 128) return run<__nv_bfloat16, 128, 3, 1, 64>(t, q, k, v, st);
+        return nq == 1 ? run<__nv_bfloat16, 64, 3, 1, 128>(t, q, k, v, st) : run<__nv_bfloat16, 64, 3, 2, 128>(t, q, k, v, st);
+    }
+    const bool half = t.a.dtype == GS_DTYPE_F16;
+    if (dp == 128) {
+        if (nq == 1) return half ? run<__half, 128, 1, 1, 128>(t, q, k, v, st) : run<__nv_bfloat16, 128, 1, 1, 128>(t, q, k, v, st);
+        return half ? run<__half, 128, 1, 2, 128>(t, q, k, v, st) : run<__nv_bfloat16, 128, 1, 2, 128>(t, q, k, v, st);
+    }
+    if (nq == 1) return half ? run<__half, 64, 1, 1, 128>(t, q, k, v, st) : run<__nv_bfloat16, 64, 1, 1, 128>(t, q, k, v, st);
+    return half ? run<__half, 64, 1, 2, 128>(t, q, k, v, st) : run<__nv_bfloat16, 64, 1, 2, 128>(t, q, k, v, st);
+}
+
+}  // namespace gs

@@ -1,0 +1,140 @@
+// Cross attention: laying tensors out in the workspace for the tensor-core kernels, and joining the shares of
+// a walk that was split. All of it moves memory once with 16-byte accesses where the rows allow them.
+#include "attention_tc.cuh"
+
+namespace gs {
+
+// A block per batch entry, a thread per key of each chunk: ballots within a warp, the warps' counts summed.
+__global__ void __launch_bounds__(1024) k_attn_index(const AttnArgs a, int* count, int* index) {
+    pdl_entry();
+    __shared__ int warps[2][32];
+    const int b = blockIdx.x, len = key_count(a, b), warp = threadIdx.x >> 5;
+    int* out = index + (long long)b * a.len_k;
+    int done = 0, phase = 0;
+    for (int n0 = 0; n0 < len; n0 += 1024, phase ^= 1) {
+        const int key = n0 + threadIdx.x;
+        const bool in = key < len && a.key_mask[b * a.mask_stride + key] != 0;
+        const unsigned votes = __ballot_sync(0xffffffffu, in);
+        if ((threadIdx.x & 31) == 0) warps[phase][warp] = __popc(votes);
+        __syncthreads();
+        int before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) {
+            const int c = warps[phase][w];
+            before += w < warp ? c : 0;
+            total += c;
+        }
+        if (in) out[done + before + __popc(votes & lanemask_lt())] = key;
+        done += total;
+    }
+    if (threadIdx.x == 0) count[b] = done;
+}
+
+// A thread per eight elements of a packed row.
+template <class T, int PL>
+__global__ void __launch_bounds__(256) k_attn_pack(const AttnArgs a, const AttnTensor t, int heads, int len, int keys,
+                                                   const int* count, const int* index, int dp, long long rows,
+                                                   __nv_bfloat16* dst) {
+    pdl_entry();
+    const int per = dp / 8;
+    const long long bh = blockIdx.y + (long long)blockIdx.z * gridDim.y;
+    if (bh >= (long long)a.batch * heads) return;
+    const int b = (int)(bh / heads), h = (int)(bh % heads);
+    const int live = !keys ? len : count ? count[b] : key_count(a, b);
+    const int last = keys ? (live + kTileRows - 1) / kTileRows * kTileRows : live;  // rows that are read
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)last * per; i += (long long)gridDim.x * 256) {
+        const int row = (int)(i / per), c = (int)(i % per) * 8;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (row < live) {
+            const int src = index && keys ? index[(long long)b * a.len_k + row] : row;
+            const T* p = head_base<T>(t, b, h) + src * t.len_stride + c;
+            if (c + 8 <= a.d && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+                constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+                for (int e = 0; e < 8; e += V) {
+                    const Pack<T, V> w = *reinterpret_cast<const Pack<T, V>*>(p + e);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) x[e + k] = to_float(w.v[k]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < a.d) x[e] = to_float(p[e]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (PL == 1) {
+                    w[e] = pack2<typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type>(x[2 * e], x[2 * e + 1]);
+                } else {
+                    w[e] = pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
+                    x[2 * e] -= __uint_as_float(w[e] << 16);
+                    x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + ((bh * PL + q) * rows + row) * dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// A warp per query and head: the shares weighted by exp(lse - max lse), in order.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_combine(const AttnArgs a, const float* part, const float* part_lse, int splits,
+                                                      int dp) {
+    pdl_entry();
+    const long long rows = (long long)a.batch * a.heads * a.len_q;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / 32;
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31, i = (int)(row % a.len_q);
+    const long long bh = row / a.len_q;
+    const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+    T* dst = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride + i * a.out.len_stride;
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    for (int s = 0; s < splits; ++s) total += expf(part_lse[s * rows + row] - base);
+    for (int c = lane; c < a.d; c += 32) {
+        float o = 0.f;
+        for (int s = 0; s < splits; ++s) {
+            const float l = part_lse[s * rows + row];
+            // a share without keys was not written
+            if (l != -INFINITY) o = fmaf(expf(l - base), part[(s * rows + row) * dp + c], o);
+        }
+        dst[c] = from_float<T>(total == 0.f ? 0.f : o / total);
+    }
+    if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
+}
+
+cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st) {
+    count_launches(1);
+    return launch_pdl(k_attn_index, dim3(a.batch), dim3(1024), 0, st, a, count, index);
+}
+
+cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, int len, bool keys, const int* count,
+                             const int* index, int planes, int dp, long long rows, void* dst, cudaStream_t st) {
+    const long long bh = (long long)a.batch * heads, items = rows * (dp / 8);
+    const unsigned y = (unsigned)(bh < 32768 ? bh : 32768), z = (unsigned)((bh + y - 1) / y);
+    long long x = (items + 255) / 256;
+    if (x > 4096) x = 4096;
+    const dim3 grid((unsigned)x, y, z);
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dst);
+    count_launches(1);
+    if (planes == 3) return launch_pdl(k_attn_pack<float, 3>, grid, dim3(256), 0, st, a, t, heads, len, (int)keys, count, index, dp, rows, d);
+    auto* kernel = a.dtype == GS_DTYPE_F16 ? k_attn_pack<__half, 1> : k_attn_pack<__nv_bfloat16, 1>;
+    return launch_pdl(kernel, grid, dim3(256), 0, st, a, t, heads, len, (int)keys, count, index, dp, rows, d);
+}
+
+cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st) {
+    const long long blocks = ((long long)a.batch * a.heads * a.len_q + 7) / 8;
+    auto* kernel = a.dtype == GS_DTYPE_F32 ? k_attn_combine<float> : a.dtype == GS_DTYPE_F16 ? k_attn_combine<__half> : k_attn_combine<__nv_bfloat16>;
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, part, part_lse, splits, dp);
+}
+
+}  // namespace gs

@@ -1,0 +1,68 @@
+// Cross attention on the tensor cores: what the forward and the backward kernels share.
+//
+// Operands are 16-bit. float32 tensors are split into three bfloat16 planes, x = x0 + x1 + x2 with 8 bits of
+// the significand each; a product keeps the six pairs whose size is at least 2^-16 of the leading one (the
+// dropped ones are 2^-24 of it), accumulated in float32 like the rest.
+//
+// The kernels read Q, K, V and dout with tiled bulk copies, straight from the caller's tensors when these are
+// 16-bit with 16-byte aligned rows and every key takes part. Otherwise a copy kernel first lays a tensor out
+// in the workspace ("packed"): split into planes, padded to a row of 64 or 128 elements and, for K and V, with
+// only the keys that take part, in their order, and zeros up to the next multiple of 128 keys. A masked
+// key then costs nothing, and what it holds (NaN) never meets a product.
+#pragma once
+
+#include "attention.cuh"
+#include "tcgen05.cuh"
+
+namespace gs {
+
+constexpr int kTileRows = 128;  // rows of an operand tile's copy, and of an accumulator
+
+// The pairs of planes whose products are summed, small ones first: (1, 1), (0, 2), (2, 0), (0, 1), (1, 0), (0, 0).
+template <int PL>
+struct Pairs {
+    static constexpr int n = PL == 1 ? 1 : 6;
+    __host__ __device__ static constexpr int a(int c) { return PL == 1 ? 0 : c == 2 ? 2 : (c == 0 || c == 4); }
+    __host__ __device__ static constexpr int b(int c) { return PL == 1 ? 0 : c == 1 ? 2 : (c == 0 || c == 3); }
+};
+
+// A tensor that the tiled copies read: as the caller's (coordinates: element, row, head, batch entry) or packed
+// (element, row, plane, batch entry x head).
+struct TcTensor {
+    CUtensorMap map;
+    int packed;
+};
+
+struct TcArgs {
+    AttnArgs a;
+    const int* count;  // keys per batch entry that the key mask leaves, or NULL without one
+    float* part;       // a split's share of the output or of a gradient, float32, or NULL
+    float* part_lse;
+    int tiles, splits;
+};
+
+__device__ __forceinline__ int keys_of(const TcArgs& t, int b) { return t.count ? t.count[b] : key_count(t.a, b); }
+
+// Loads rows row0 .. row0 + ROWS - 1 of a head, all planes: PL x DP/64 tiles of ROWS x 64 elements.
+template <int DP, int PL, int ROWS>
+__device__ __forceinline__ void load_rows(uint32_t dst, const TcTensor& t, int row0, int b, int h, int heads, uint64_t* bar) {
+#pragma unroll
+    for (int p = 0; p < PL; ++p)
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c)
+            tile_load(dst + (p * (DP / 64) + c) * ROWS * 128, &t.map, c * 64, row0, t.packed ? p : h,
+                      t.packed ? b * heads + h : b, bar);
+}
+
+// count[b] and index[b][0 .. count[b]): the keys that take part, in order.
+cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st);
+// Lays `t` (heads heads; K or V when keys) out at dst as [batch x heads][planes][rows][dp] 16-bit values.
+cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, int len, bool keys, const int* count,
+                             const int* index, int planes, int dp, long long rows, void* dst, cudaStream_t st);
+// out and lse from the splits' shares [splits][batch][heads][len_q][dp].
+cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st);
+// nq: query tiles per block, 1 or 2.
+cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTensor& k, const TcTensor& v, int planes, int dp,
+                               int nq, cudaStream_t st);
+
+}  // namespace gs
