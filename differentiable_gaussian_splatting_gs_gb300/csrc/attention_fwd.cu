@@ -11,6 +11,14 @@
 
 namespace gs {
 
+// Tensor-memory column, from the start of S, of the 16 probabilities from key 16 x on, plane q. With three
+// planes a group of 32 keys' first two planes take the columns of its scores, so that P can replace S group by
+// group; the third lies behind S.
+template <int PL, int BN>
+__device__ __forceinline__ int p_column(int q, int x) {
+    return PL == 1 ? x * 8 : q < 2 ? (x / 2) * 32 + q * 16 + (x % 2) * 8 : BN + x * 8;
+}
+
 template <int DP, int PL, int NQ, int BN>
 struct FwdShape {
     static constexpr int kQ = PL * DP * kTileRows * 2;  // bytes of a query tile
@@ -18,10 +26,14 @@ struct FwdShape {
     static constexpr int kRoom = 226 * 1024 - 1024 - NQ * kQ;
     static constexpr int kStages = kRoom / (2 * kKV) > 4 ? 4 : kRoom / (2 * kKV);
     static constexpr int kSmem = NQ * kQ + kStages * 2 * kKV + 1024;
-    static constexpr int kP = PL * BN / 2 > BN ? PL * BN / 2 : BN;  // columns that S and then P take
+    static constexpr int kP = PL == 1 ? BN : BN + BN / 2;  // columns that S and then P take
+    // The tensor cores add to the accumulator by truncation: over hundreds of products that is a drift of
+    // 2^-25 each, lost in 16-bit results but not in float32 ones (-1.4e-5 at 2,500 keys). With three planes
+    // each key tile's product therefore starts from zero and is added to O in registers, rounded (2e-7).
+    static constexpr bool kRegO = PL == 3;
     static constexpr int kO = NQ * kP;                              // first column of O
     // two query tiles: a third warpgroup of which two warps work, so that registers can be moved between whole
-    // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 224 + 128 x 56
+    // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 216 + 128 x 72
     static constexpr int kThreads = NQ == 2 ? 384 : 192;
     static constexpr int kCols = kO + NQ * DP <= 256 ? 256 : 512;
     static_assert(kO + NQ * DP <= 512 && kStages >= 1);
@@ -76,7 +88,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     const uint32_t tm = tmem_base;
 
     if (warp >= NQ * 4) {
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == NQ * 4) {  // copies
             if (lane == 0 && n > 0) {
                 bool ok = true;
@@ -121,7 +133,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     const uint32_t vb = sv + s * S::kKV + C::b(c) * DP * BN * 2;
 #pragma unroll
                     for (int x = 0; x < BN / 16; ++x, add = true)
-                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + C::a(c) * (BN / 2) + x * 8, tile_desc(vb + x * 2048, BN * 128),
+                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + p_column<PL, BN>(C::a(c), x), tile_desc(vb + x * 2048, BN * 128),
                                pv_desc, add);
                 }
             };
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     ok = ok && mbar_wait_bounded(&p_full[i], j & 1, limit, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    values(i, s, j > 0);
+                    values(i, s, !S::kRegO && j > 0);
                     if (i == NQ - 1) mma_commit(&v_free[s]);
                     if (j + 1 < n) {
                         if (i == 0) ok = mbar_wait_bounded(&k_full[s1], ((j + 1) / kSt) & 1, limit, a.err);
@@ -155,39 +167,78 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
         }
     } else {  // softmax: thread = query
-        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + i * S::kP + lanes, to = tm + S::kO + i * DP + lanes;
         const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
         float top = -INFINITY, sum = 0.f;               // top: raw score in use as the maximum
+        constexpr int kOut = S::kRegO ? DP : 1;
+        float out[kOut];
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) out[e] = 0.f;
+        auto add_tile = [&]() {
+#pragma unroll
+            for (int g = 0; g < kOut / 32; ++g) {
+                uint32_t o[32];
+                tmem_ld32(to + g * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) out[(g * 32 + e) % kOut] += __uint_as_float(o[e]);
+            }
+        };
+        // 32 columns of O
+        auto get = [&](int g, uint32_t (&o)[32]) {
+            if (S::kRegO) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(out[(g * 32 + e) % kOut]);
+            } else {
+                tmem_ld32(to + g * 32, o);
+                tmem_wait_ld();
+            }
+        };
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (!(ok = warp_wait(&s_full[i], j & 1, limit, a.err))) break;
             tc_fence_after();
-            uint32_t x[BN / 32][32];
-#pragma unroll
-            for (int g = 0; g < BN / 32; ++g) tmem_ld32(ts + g * 32, x[g]);
-            tmem_wait_ld();
+            if (S::kRegO && j > 0) add_tile();
+            // 16-bit: the row's scores stay in registers. Three planes: these hold O, and the scores are read twice
+            constexpr int kHeld = S::kRegO ? 1 : BN / 32;
+            uint32_t x[kHeld][32];
             const int left = keys - (first + j) * BN;
-            if (left < BN) {
-#pragma unroll
-                for (int g = 0; g < BN / 32; ++g)
+            auto load = [&](int g) {
+                tmem_ld32(ts + g * 32, x[g % kHeld]);
+                if (S::kRegO) tmem_wait_ld();
+            };
+            auto mask = [&](int g) {
+                if (left < BN) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (g * 32 + e >= left) x[g][e] = 0xff800000u;  // -inf
-            }
+                        if (g * 32 + e >= left) x[g % kHeld][e] = 0xff800000u;  // -inf
+                }
+            };
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (!S::kRegO) {
 #pragma unroll
-            for (int g = 0; g < BN / 32; ++g)
+                for (int g = 0; g < BN / 32; ++g) load(g);
+                tmem_wait_ld();
+            }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[g][e]));
+            for (int g = 0; g < BN / 32; ++g) {
+                if (S::kRegO) load(g);
+                mask(g);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[g % kHeld][e]));
+            }
             const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const bool raise = (m - top) * c > 8.f || top == -INFINITY;
             if (__any_sync(0xffffffffu, raise)) {
                 const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
                 if (raise) top = m;
                 sum *= keep;
-                if (j > 0) {
+                if (S::kRegO) {
+#pragma unroll
+                    for (int e = 0; e < kOut; ++e) out[e] *= keep;
+                } else if (j > 0) {
 #pragma unroll
                     for (int g = 0; g < DP / 32; ++g) {
                         uint32_t o[32];
@@ -205,10 +256,14 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             const f32x2 one = f2_pack(1.f, 1.f);
 #pragma unroll
             for (int g = 0; g < BN / 32; ++g) {
+                if (S::kRegO) {
+                    load(g);
+                    mask(g);
+                }
                 uint32_t p[PL][16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[g][2 * e]), __uint_as_float(x[g][2 * e + 1])), c2, b2));
+                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[g % kHeld][2 * e]), __uint_as_float(x[g % kHeld][2 * e + 1])), c2, b2));
                     float u = ex2_approx(y.x), w = ex2_approx(y.y);
                     s2[e & 1] = f2_fma(f2_pack(u, w), one, s2[e & 1]);
 #pragma unroll
@@ -221,7 +276,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < PL; ++q) tmem_st16(ts + q * (BN / 2) + g * 16, p[q]);
+                for (int q = 0; q < PL; ++q) tmem_st16(ts + p_column<PL, BN>(q, 2 * g), p[q]);
             }
             const float2 sa = f2_unpack(s2[0]), sb = f2_unpack(s2[1]);
             sum += (sa.x + sa.y) + (sb.x + sb.y);
@@ -231,6 +286,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         }
         if (n > 0 && ok) ok = warp_wait(&o_full[i], 0, limit, a.err);
         tc_fence_after();
+        if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && ok;
         const float f = sum == 0.f ? 0.f : 1.f / sum;
         const float lse = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
@@ -242,8 +298,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
 #pragma unroll
                 for (int g = 0; g < DP / 32; ++g) {
                     uint32_t o[32];
-                    tmem_ld32(to + g * 32, o);
-                    tmem_wait_ld();
+                    get(g, o);
                     if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -264,10 +319,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
 #pragma unroll
             for (int g = 0; g < DP / 32; ++g) {
                 uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(to + g * 32, o);
-                    tmem_wait_ld();
-                }
+                if (n > 0) get(g, o);
                 if (live) {
 #pragma unroll
                     for (int e = 0; e < 32; e += V) {
