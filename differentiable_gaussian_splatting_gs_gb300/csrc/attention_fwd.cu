@@ -113,57 +113,58 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
                 for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
             }
-        } else if (warp == NQ * 4 + 1 && lane == 0 && n > 0) {  // products
+        } else if (warp == NQ * 4 + 1 && n > 0) {  // products: the warp waits, one thread issues
             const uint32_t qk_desc = mma_desc<T>(BN, false), pv_desc = mma_desc<T>((a.d + 15) / 16 * 16, true);
             const int steps = (a.d + 15) / 16;  // of the inner dimension of Q K^T
-            auto scores = [&](int i, int s) {
-                bool add = false;
+            auto scores = [&](int i, int s, bool release) {
+                if (!elect_one()) return;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
-                    const uint32_t qa = sq + i * S::kQ + C::a(c) * DP * kTileRows * 2, kb = sk + s * S::kKV + C::b(c) * DP * BN * 2;
-                    for (int x = 0; x < steps; ++x, add = true)
-                        mma_ss(tm + i * S::kP, tile_desc(qa + (x / 4) * kTileRows * 128 + (x % 4) * 32),
-                               tile_desc(kb + (x / 4) * BN * 128 + (x % 4) * 32), qk_desc, add);
+                    const uint32_t qa = tile_desc(sq + i * S::kQ + C::a(c) * DP * kTileRows * 2);
+                    const uint32_t kb = tile_desc(sk + s * S::kKV + C::b(c) * DP * BN * 2);
+#pragma unroll
+                    for (int x = 0; x < DP / 16; ++x)
+                        if (x < steps)
+                            mma_ss(tm + i * S::kP, qa + (x / 4) * kTileRows * 8 + (x % 4) * 2, kb + (x / 4) * BN * 8 + (x % 4) * 2,
+                                   qk_desc, c > 0 || x > 0);
                 }
                 mma_commit(&s_full[i]);
+                if (release) mma_commit(&k_free[s]);
             };
-            auto values = [&](int i, int s, bool add) {
+            auto values = [&](int i, int s, bool add, bool last, bool release) {
+                if (!elect_one()) return;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
-                    const uint32_t vb = sv + s * S::kKV + C::b(c) * DP * BN * 2;
+                    const uint32_t vb = tile_desc(sv + s * S::kKV + C::b(c) * DP * BN * 2, BN * 128);
 #pragma unroll
-                    for (int x = 0; x < BN / 16; ++x, add = true)
-                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + p_column<PL, BN>(C::a(c), x), tile_desc(vb + x * 2048, BN * 128),
-                               pv_desc, add);
+                    for (int x = 0; x < BN / 16; ++x)
+                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
+                               add || c > 0 || x > 0);
                 }
+                if (release) mma_commit(&v_free[s]);
+                if (last) mma_commit(&o_full[i]);
             };
-            bool ok = mbar_wait_bounded(&q_full, 0, limit, a.err) && mbar_wait_bounded(&k_full[0], 0, limit, a.err);
+            bool ok = warp_wait(&q_full, 0, limit, a.err) && warp_wait(&k_full[0], 0, limit, a.err);
             tc_fence_after();
-            if (ok) {
-                for (int i = 0; i < NQ; ++i) scores(i, 0);
-                mma_commit(&k_free[0]);
-            }
+            if (ok)
+                for (int i = 0; i < NQ; ++i) scores(i, 0, i == NQ - 1);
             for (int j = 0; j < n && ok; ++j) {
                 const int s = j % kSt, s1 = (j + 1) % kSt;
-                for (int i = 0; i < NQ && ok; ++i) {
-                    if (i == 0) ok = mbar_wait_bounded(&v_full[s], (j / kSt) & 1, limit, a.err);
-                    ok = ok && mbar_wait_bounded(&p_full[i], j & 1, limit, a.err);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    if (i == 0) ok = warp_wait(&v_full[s], (j / kSt) & 1, limit, a.err);
+                    ok = ok && warp_wait(&p_full[i], j & 1, limit, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    values(i, s, !S::kRegO && j > 0);
-                    if (i == NQ - 1) mma_commit(&v_free[s]);
+                    values(i, s, !S::kRegO && j > 0, j + 1 == n, i == NQ - 1);
                     if (j + 1 < n) {
-                        if (i == 0) ok = mbar_wait_bounded(&k_full[s1], ((j + 1) / kSt) & 1, limit, a.err);
-                        if (!ok) break;
-                        scores(i, s1);
-                        if (i == NQ - 1) mma_commit(&k_free[s1]);
-                    } else {
-                        mma_commit(&o_full[i]);
+                        if (i == 0 && !(ok = warp_wait(&k_full[s1], ((j + 1) / kSt) & 1, limit, a.err))) break;
+                        scores(i, s1, i == NQ - 1);
                     }
                 }
             }
             // no product is in flight when the tensor memory is freed
-            mma_commit(&drain);
+            if (elect_one()) mma_commit(&drain);
             mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
         }
     } else {  // softmax: thread = query

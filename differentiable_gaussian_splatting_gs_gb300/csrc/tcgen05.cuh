@@ -72,9 +72,17 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 //   K-major (the products' inner dimension along a row): 16 elements of it are 32 bytes further on;
 //   MN-major (the inner dimension down the rows): 16 of them are 2048 bytes further on, and `lead` is the
 //   distance of the tiles that hold the next 64 of the outer dimension.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead = 16) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// The lower word, to which a byte offset / 16 within the tile is added; the upper word is the same for all.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr, uint32_t lead = 16) { return (addr >> 4) | ((lead >> 4) << 16); }
+constexpr uint32_t kTileDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// True in one thread of a converged warp, always the same one. Products are issued under it rather than under
+// a comparison of the lane: the compiler then knows that their operands are uniform, and an issue takes a
+// few instead of about 60 to 100 cycles.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <class T>
@@ -95,20 +103,21 @@ __device__ __forceinline__ uint32_t mma_desc(int n, bool b_mn) {
            ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// One product over 16 of the inner dimension, issued by one thread; asynchronous, in issue order.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One product over 16 of the inner dimension, issued by one thread; asynchronous, in issue order. A and B by
+// the lower words of their descriptors.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTileDescHi)
         : "memory");
 }
 // ... with A in tensor memory: lane = row, two elements of the inner dimension per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTileDescHi)
         : "memory");
 }
 // Arrives on `bar` once every product that this thread issued so far is complete.
