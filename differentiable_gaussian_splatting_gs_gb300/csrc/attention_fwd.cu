@@ -2,11 +2,15 @@
 //
 // A block takes NQ tiles of 128 queries of one head and walks the keys in tiles of BN. One warp copies K and
 // V tiles ahead, one thread issues the products S = Q K^T and O += P V, and a warpgroup per query tile turns S
-// into P: thread = query, so the row's maximum and sum need no exchange. S and P share columns of tensor
-// memory, O stays there too. With two query tiles the products of one run beside the softmax of the other:
-//   products: ... O0 += P0 V_j, S0 = Q0 K_j+1, O1 += P1 V_j, S1 = Q1 K_j+1, ...
-// The running maximum is only raised, and O rescaled, when a row's scores pass the one in use by 2^8: P may
-// then reach 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
+// into P: thread = query, so the row's maximum and sum need no exchange. S, P and O stay in tensor memory.
+// With two query tiles the products of one run beside the softmax of the other. Where the columns suffice
+// (16-bit, heads of up to 64) P has columns of its own: the next S is then formed while this one's softmax
+// runs. Otherwise P takes the columns of S, and the next S waits for P V.
+//
+// The softmax is bound by its exponentials (4 cycles a warp instruction and scheduler), so nothing may come
+// before them: P is formed with the maximum of the tiles before while this tile's is found. Only when a row's
+// scores pass the maximum in use by 2^8 is it raised, O rescaled and the tile's P formed again; below that P
+// reaches 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -26,15 +30,17 @@ struct FwdShape {
     static constexpr int kRoom = 226 * 1024 - 1024 - NQ * kQ;
     static constexpr int kStages = kRoom / (2 * kKV) > 4 ? 4 : kRoom / (2 * kKV);
     static constexpr int kSmem = NQ * kQ + kStages * 2 * kKV + 1024;
-    static constexpr int kP = PL == 1 ? BN : BN + BN / 2;  // columns that S and then P take
+    static constexpr bool kApart = PL == 1 && DP == 64;  // P beside S
+    // columns of a query tile's S and P, and where in them P starts
+    static constexpr int kP = kApart || PL == 3 ? BN + BN / 2 : BN, kPAt = kApart ? BN : 0;
     // The tensor cores add to the accumulator by truncation: over hundreds of products that is a drift of
     // 2^-25 each, lost in 16-bit results but not in float32 ones (-1.4e-5 at 2,500 keys). With three planes
     // each key tile's product therefore starts from zero and is added to O in registers, rounded (2e-7).
     static constexpr bool kRegO = PL == 3;
     static constexpr int kO = NQ * kP;                              // first column of O
-    // two query tiles: a third warpgroup of which two warps work, so that registers can be moved between whole
+    // two query tiles: a third warpgroup of which two or three warps work, so that registers can be moved between whole
     // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 216 + 128 x 72
-    static constexpr int kThreads = NQ == 2 ? 384 : 192;
+    static constexpr int kThreads = NQ == 2 ? 384 : 224;
     static constexpr int kCols = kO + NQ * DP <= 256 ? 256 : 512;
     static_assert(kO + NQ * DP <= 512 && kStages >= 1);
 };
@@ -48,7 +54,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     constexpr int kSt = S::kStages;
     pdl_entry();
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t q_full, k_full[kSt], v_full[kSt], k_free[kSt], v_free[kSt], s_full[NQ], p_full[NQ], o_full[NQ], drain;
+    __shared__ uint64_t q_full, k_full[kSt], v_full[kSt], k_free[kSt], v_free[kSt], s_full[NQ], s_free[NQ],
+        p_full[NQ], o_done[NQ], drain[2];
     __shared__ uint32_t tmem_base;
     const AttnArgs& a = t.a;
     const uint32_t sq = (smem_u32(raw) + 1023u) & ~1023u, sk = sq + NQ * S::kQ, sv = sk + kSt * S::kKV;
@@ -75,10 +82,12 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 128);
             mbar_init(&p_full[i], 128);
-            mbar_init(&o_full[i], 1);
+            mbar_init(&o_done[i], 1);
         }
-        mbar_init(&drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         fence_mbar_init();
     }
     if (warp == NQ * 4) tmem_alloc<S::kCols>(&tmem_base);
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     if (warp >= NQ * 4) {
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == NQ * 4) {  // copies
-            if (lane == 0 && n > 0) {
+            if (n > 0 && elect_one()) {
                 bool ok = true;
                 int sent = 0;
                 mbar_arrive_expect_tx(&q_full, NQ * S::kQ);
@@ -113,11 +122,12 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
                 for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
             }
-        } else if (warp == NQ * 4 + 1 && n > 0) {  // products: the warp waits, one thread issues
+        } else if ((warp == NQ * 4 + 1 || (S::kApart && warp == NQ * 4 + 2)) && n > 0 && elect_one()) {
+            // Products, issued by one thread; where P is apart, by one thread for S and another for P V, since a
+            // wait costs a thread that issues about 70 cycles even when it is over, and a commit as many.
             const uint32_t qk_desc = mma_desc<T>(BN, false), pv_desc = mma_desc<T>((a.d + 15) / 16 * 16, true);
             const int steps = (a.d + 15) / 16;  // of the inner dimension of Q K^T
-            auto scores = [&](int i, int s, bool release) {
-                if (!elect_one()) return;
+            auto scores = [&](int i, int s) {
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t qa = tile_desc(sq + i * S::kQ + C::a(c) * DP * kTileRows * 2);
@@ -129,48 +139,62 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                                    qk_desc, c > 0 || x > 0);
                 }
                 mma_commit(&s_full[i]);
-                if (release) mma_commit(&k_free[s]);
+                if (i == NQ - 1) mma_commit(&k_free[s]);
             };
-            auto values = [&](int i, int s, bool add, bool last, bool release) {
-                if (!elect_one()) return;
+            auto values = [&](int i, int s, bool add) {
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t vb = tile_desc(sv + s * S::kKV + C::b(c) * DP * BN * 2, BN * 128);
 #pragma unroll
                     for (int x = 0; x < BN / 16; ++x)
-                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
+                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + S::kPAt + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
                                add || c > 0 || x > 0);
                 }
-                if (release) mma_commit(&v_free[s]);
-                if (last) mma_commit(&o_full[i]);
+                mma_commit(&o_done[i]);
+                if (i == NQ - 1) mma_commit(&v_free[s]);
             };
-            bool ok = warp_wait(&q_full, 0, limit, a.err) && warp_wait(&k_full[0], 0, limit, a.err);
-            tc_fence_after();
-            if (ok)
-                for (int i = 0; i < NQ; ++i) scores(i, 0, i == NQ - 1);
+            auto wait = [&](uint64_t* bar, int j) { return mbar_wait_bounded(bar, j & 1, limit, a.err); };
+            const bool does_s = warp == NQ * 4 + 1, does_pv = !S::kApart || !does_s;
+            bool ok = true;
+            if (does_s) {
+                ok = wait(&q_full, 0) && wait(&k_full[0], 0);
+                tc_fence_after();
+                if (ok)
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) scores(i, 0);
+            }
             for (int j = 0; j < n && ok; ++j) {
                 const int s = j % kSt, s1 = (j + 1) % kSt;
+                const bool more = j + 1 < n;
+                if (S::kApart && does_s && more) {
+                    ok = wait(&k_full[s1], (j + 1) / kSt);
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    if (i == 0) ok = warp_wait(&v_full[s], (j / kSt) & 1, limit, a.err);
-                    ok = ok && warp_wait(&p_full[i], j & 1, limit, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(i, s, !S::kRegO && j > 0, j + 1 == n, i == NQ - 1);
-                    if (j + 1 < n) {
-                        if (i == 0 && !(ok = warp_wait(&k_full[s1], ((j + 1) / kSt) & 1, limit, a.err))) break;
-                        scores(i, s1, i == NQ - 1);
-                    }
+                    for (int i = 0; i < NQ; ++i)
+                        if ((ok = ok && wait(&s_free[i], j))) {
+                            tc_fence_after();
+                            scores(i, s1);
+                        }
+                }
+                if (does_pv) {
+                    ok = wait(&v_full[s], j / kSt);
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i)
+                        if ((ok = ok && wait(&p_full[i], j))) {
+                            tc_fence_after();
+                            values(i, s, !S::kRegO && j > 0);
+                            if (!S::kApart && more && (i > 0 || (ok = wait(&k_full[s1], (j + 1) / kSt)))) scores(i, s1);
+                        }
                 }
             }
             // no product is in flight when the tensor memory is freed
-            if (elect_one()) mma_commit(&drain);
-            mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
+            mma_commit(&drain[warp - NQ * 4 - 1]);
+            mbar_wait_bounded(&drain[warp - NQ * 4 - 1], 0, kDrainLimit, a.err);
         }
     } else {  // softmax: thread = query
         if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + i * S::kP + lanes, to = tm + S::kO + i * DP + lanes;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + i * S::kP + lanes, tp = ts + S::kPAt,
+                       to = tm + S::kO + i * DP + lanes;
         const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
         float top = -INFINITY, sum = 0.f;               // top: raw score in use as the maximum
         constexpr int kOut = S::kRegO ? DP : 1;
@@ -182,7 +206,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             for (int g = 0; g < kOut / 32; ++g) {
                 uint32_t o[32];
                 tmem_ld32(to + g * 32, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) out[(g * 32 + e) % kOut] += __uint_as_float(o[e]);
             }
@@ -194,79 +218,36 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(out[(g * 32 + e) % kOut]);
             } else {
                 tmem_ld32(to + g * 32, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
             }
         };
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (!(ok = warp_wait(&s_full[i], j & 1, limit, a.err))) break;
             tc_fence_after();
-            if (S::kRegO && j > 0) add_tile();
-            // 16-bit: the row's scores stay in registers. Three planes: these hold O, and the scores are read twice
-            constexpr int kHeld = S::kRegO ? 1 : BN / 32;
-            uint32_t x[kHeld][32];
             const int left = keys - (first + j) * BN;
-            auto load = [&](int g) {
-                tmem_ld32(ts + g * 32, x[g % kHeld]);
-                if (S::kRegO) tmem_wait_ld();
-            };
-            auto mask = [&](int g) {
+            auto mask = [&](uint32_t (&x)[32], int g) {
                 if (left < BN) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (g * 32 + e >= left) x[g % kHeld][e] = 0xff800000u;  // -inf
+                        if (g * 32 + e >= left) x[e] = 0xff800000u;  // -inf
                 }
             };
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (!S::kRegO) {
+            auto largest = [&](const uint32_t (&x)[32], float (&m)[2]) {
 #pragma unroll
-                for (int g = 0; g < BN / 32; ++g) load(g);
-                tmem_wait_ld();
-            }
-#pragma unroll
-            for (int g = 0; g < BN / 32; ++g) {
-                if (S::kRegO) load(g);
-                mask(g);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[g % kHeld][e]));
-            }
-            const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            const bool raise = (m - top) * c > 8.f || top == -INFINITY;
-            if (__any_sync(0xffffffffu, raise)) {
-                const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
-                if (raise) top = m;
-                sum *= keep;
-                if (S::kRegO) {
-#pragma unroll
-                    for (int e = 0; e < kOut; ++e) out[e] *= keep;
-                } else if (j > 0) {
-#pragma unroll
-                    for (int g = 0; g < DP / 32; ++g) {
-                        uint32_t o[32];
-                        tmem_ld32(to + g * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                        tmem_st32(to + g * 32, o);
-                    }
+                for (int e = 0; e < 32; e += 4) {
+                    m[0] = max3(m[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    m[1] = max3(m[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                 }
-            }
-            const float base = top == -INFINITY ? 0.f : top * c;  // a score of -inf is no error: exp(-inf) = 0
-            const f32x2 c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
-            f32x2 s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-            const f32x2 one = f2_pack(1.f, 1.f);
-#pragma unroll
-            for (int g = 0; g < BN / 32; ++g) {
-                if (S::kRegO) {
-                    load(g);
-                    mask(g);
-                }
+            };
+            // P of 32 keys into its columns; s: the thread's sum
+            auto probabilities = [&](const uint32_t (&x)[32], int g, f32x2 b2, f32x2 (&s)[2]) {
                 uint32_t p[PL][16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[g % kHeld][2 * e]), __uint_as_float(x[g % kHeld][2 * e + 1])), c2, b2));
+                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2_pack(c, c), b2));
                     float u = ex2_approx(y.x), w = ex2_approx(y.y);
-                    s2[e & 1] = f2_fma(f2_pack(u, w), one, s2[e & 1]);
+                    s[e & 1] = f2_fma(f2_pack(u, w), f2_pack(1.f, 1.f), s[e & 1]);
 #pragma unroll
                     for (int q = 0; q < PL; ++q) {
                         p[q][e] = pack2<T>(u, w);
@@ -277,7 +258,90 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < PL; ++q) tmem_st16(ts + p_column<PL, BN>(q, 2 * g), p[q]);
+                for (int q = 0; q < PL; ++q) tmem_st16(tp + p_column<PL, BN>(q, 2 * g), p[q]);
+            };
+            // whether the row's maximum in use is too far below m; a score of -inf is no error: exp(-inf) = 0
+            auto passed = [&](float m) { return (m - top) * c > 8.f || (top == -INFINITY && m > -INFINITY); };
+            auto base = [&]() { const float t0 = top == -INFINITY ? 0.f : -top * c; return f2_pack(t0, t0); };
+            f32x2 s2[2];
+            float m2[2] = {-INFINITY, -INFINITY};
+            if constexpr (S::kRegO) {
+                // the registers hold O: the scores are read twice, and each group of P takes the columns of its scores
+                if (j > 0) add_tile();
+                uint32_t x[32];
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) {
+                    tmem_ld32(ts + g * 32, x);
+                    tmem_wait_ld(x);
+                    mask(x, g);
+                    largest(x, m2);
+                }
+                const float m = fmaxf(m2[0], m2[1]);
+                if (passed(m)) {
+                    const float keep = top == -INFINITY ? 0.f : ex2_approx((top - m) * c);
+                    top = m;
+                    sum *= keep;
+#pragma unroll
+                    for (int e = 0; e < kOut; ++e) out[e] *= keep;
+                }
+                __syncwarp();
+                s2[0] = s2[1] = f2_pack(0.f, 0.f);
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) {
+                    tmem_ld32(ts + g * 32, x);
+                    tmem_wait_ld(x);
+                    mask(x, g);
+                    probabilities(x, g, base(), s2);
+                }
+            } else {
+                uint32_t x[BN / 32][32];
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) tmem_ld32(ts + g * 32, x[g]);
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) tmem_wait_ld(x[g]);
+                if (S::kApart) {
+                    tc_fence_before();
+                    mbar_arrive(&s_free[i]);
+                    if (j > 0) {  // the last P V has read P and left O
+                        if (!(ok = warp_wait(&o_done[i], (j - 1) & 1, limit, a.err))) break;
+                        tc_fence_after();
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) mask(x[g], g);
+                if (j == 0) {
+#pragma unroll
+                    for (int g = 0; g < BN / 32; ++g) largest(x[g], m2);
+                    top = fmaxf(m2[0], m2[1]);
+                }
+                bool again;
+                do {
+                    s2[0] = s2[1] = f2_pack(0.f, 0.f);
+                    m2[0] = m2[1] = -INFINITY;
+                    const f32x2 b2 = base();
+#pragma unroll
+                    for (int g = 0; g < BN / 32; ++g) {
+                        largest(x[g], m2);
+                        probabilities(x[g], g, b2, s2);
+                    }
+                    const float m = fmaxf(m2[0], m2[1]);
+                    const bool raise = passed(m);
+                    again = __any_sync(0xffffffffu, raise);
+                    if (again) {  // j > 0, and only once: no row's scores pass their own maximum
+                        const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
+                        if (raise) top = m;
+                        sum *= keep;
+#pragma unroll
+                        for (int g = 0; g < DP / 32; ++g) {
+                            uint32_t o[32];
+                            tmem_ld32(to + g * 32, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tmem_st32(to + g * 32, o);
+                        }
+                    }
+                } while (again);
             }
             const float2 sa = f2_unpack(s2[0]), sb = f2_unpack(s2[1]);
             sum += (sa.x + sa.y) + (sb.x + sb.y);
@@ -285,7 +349,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             tc_fence_before();
             mbar_arrive(&p_full[i]);
         }
-        if (n > 0 && ok) ok = warp_wait(&o_full[i], 0, limit, a.err);
+        if (n > 0 && ok) ok = warp_wait(&o_done[i], (n - 1) & 1, limit, a.err);
         tc_fence_after();
         if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && ok;
