@@ -1,11 +1,12 @@
 // Cross attention, forward, on the tensor cores.
 //
 // A block takes NQ tiles of 128 queries of one head and walks the keys in tiles of BN. One warp copies K and
-// V tiles ahead, one thread issues the products S = Q K^T and O += P V, and a warpgroup per query tile turns S
-// into P: thread = query, so the row's maximum and sum need no exchange. S, P and O stay in tensor memory.
-// With two query tiles the products of one run beside the softmax of the other. Where the columns suffice
-// (16-bit, heads of up to 64) P has columns of its own: the next S is then formed while this one's softmax
-// runs. Otherwise P takes the columns of S, and the next S waits for P V.
+// V tiles ahead, a thread issues the products S = Q K^T and O += P V, and a warpgroup per query tile turns S
+// into P: thread = query, so the row's maximum and sum need no exchange. S, P and O stay in tensor memory; P
+// takes half the columns of its S. With two query tiles the products of one run beside the softmax of the
+// other. Where the columns suffice (16-bit, heads of up to 64) a tile has 192 for S, and S takes the first and the
+// last 128 of them in turn: the next S is then formed while this one's softmax runs, and the softmax
+// never waits for P V. Otherwise the next S waits for P V.
 //
 // The softmax is bound by its exponentials (4 cycles a warp instruction and scheduler), so nothing may come
 // before them: P is formed with the maximum of the tiles before while this tile's is found. Only when a row's
@@ -30,9 +31,12 @@ struct FwdShape {
     static constexpr int kRoom = 226 * 1024 - 1024 - NQ * kQ;
     static constexpr int kStages = kRoom / (2 * kKV) > 4 ? 4 : kRoom / (2 * kKV);
     static constexpr int kSmem = NQ * kQ + kStages * 2 * kKV + 1024;
-    static constexpr bool kApart = PL == 1 && DP == 64;  // P beside S
-    // columns of a query tile's S and P, and where in them P starts
-    static constexpr int kP = kApart || PL == 3 ? BN + BN / 2 : BN, kPAt = kApart ? BN : 0;
+    static constexpr bool kTurns = PL == 1 && DP == 64;  // S in two places
+    static constexpr int kP = kTurns || PL == 3 ? BN + BN / 2 : BN;  // columns of a query tile's S and P
+    // first column of S and of P of key tile j
+    __device__ static int s_at(int j) { return kTurns && (j & 1) ? BN / 2 : 0; }
+    __device__ static int p_at(int j) { return kTurns && (j & 1) ? BN : 0; }
+    static constexpr int kIssuers = kTurns ? NQ : 1;  // threads that issue products
     // The tensor cores add to the accumulator by truncation: over hundreds of products that is a drift of
     // 2^-25 each, lost in 16-bit results but not in float32 ones (-1.4e-5 at 2,500 keys). With three planes
     // each key tile's product therefore starts from zero and is added to O in registers, rounded (2e-7).
@@ -69,7 +73,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     // this split's key tiles
     const int all = (keys + BN - 1) / BN, per = (all + t.splits - 1) / t.splits;
     const int first = min(split * per, all), n = min(per, all - first);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const unsigned limit = a.spin_limit;
 
     if (threadIdx.x == 0) {
@@ -77,13 +81,13 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         for (int i = 0; i < kSt; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&v_full[i], 1);
-            mbar_init(&k_free[i], 1);
-            mbar_init(&v_free[i], 1);
+            mbar_init(&k_free[i], S::kIssuers);
+            mbar_init(&v_free[i], S::kIssuers);
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], 128);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&s_free[i], 4);
+            mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(&drain[0], 1);
@@ -122,12 +126,15 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
                 for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
             }
-        } else if ((warp == NQ * 4 + 1 || (S::kApart && warp == NQ * 4 + 2)) && n > 0 && elect_one()) {
-            // Products, issued by one thread; where P is apart, by one thread for S and another for P V, since a
-            // wait costs a thread that issues about 70 cycles even when it is over, and a commit as many.
+        } else if (warp - NQ * 4 - 1 < S::kIssuers && n > 0 && elect_one()) {
+            // Products. Where S takes turns, each query tile has a thread that issues them: a wait costs it about
+            // 70 cycles even when it is over, and a commit as many. Otherwise one thread serves both tiles, and its
+            // order (P V and S of one, then of the other) keeps their softmaxes half a turn apart.
+            const int i0 = warp - NQ * 4 - 1, i1 = S::kTurns ? i0 + 1 : NQ;
             const uint32_t qk_desc = mma_desc<T>(BN, false), pv_desc = mma_desc<T>((a.d + 15) / 16 * 16, true);
             const int steps = (a.d + 15) / 16;  // of the inner dimension of Q K^T
-            auto scores = [&](int i, int s) {
+            auto scores = [&](int i, int j) {
+                const int s = j % kSt;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t qa = tile_desc(sq + i * S::kQ + C::a(c) * DP * kTileRows * 2);
@@ -135,65 +142,53 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < DP / 16; ++x)
                         if (x < steps)
-                            mma_ss(tm + i * S::kP, qa + (x / 4) * kTileRows * 8 + (x % 4) * 2, kb + (x / 4) * BN * 8 + (x % 4) * 2,
-                                   qk_desc, c > 0 || x > 0);
+                            mma_ss(tm + i * S::kP + S::s_at(j), qa + (x / 4) * kTileRows * 8 + (x % 4) * 2,
+                                   kb + (x / 4) * BN * 8 + (x % 4) * 2, qk_desc, c > 0 || x > 0);
                 }
                 mma_commit(&s_full[i]);
-                if (i == NQ - 1) mma_commit(&k_free[s]);
+                if (i == i1 - 1) mma_commit(&k_free[s]);
             };
-            auto values = [&](int i, int s, bool add) {
+            auto values = [&](int i, int j) {
+                const int s = j % kSt;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t vb = tile_desc(sv + s * S::kKV + C::b(c) * DP * BN * 2, BN * 128);
 #pragma unroll
                     for (int x = 0; x < BN / 16; ++x)
-                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + S::kPAt + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
-                               add || c > 0 || x > 0);
+                        mma_ts(tm + S::kO + i * DP, tm + i * S::kP + S::p_at(j) + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
+                               (!S::kRegO && j > 0) || c > 0 || x > 0);
                 }
-                mma_commit(&o_done[i]);
-                if (i == NQ - 1) mma_commit(&v_free[s]);
+                if (j >= n - 2) mma_commit(&o_done[i]);
+                if (i == i1 - 1) mma_commit(&v_free[s]);
             };
             auto wait = [&](uint64_t* bar, int j) { return mbar_wait_bounded(bar, j & 1, limit, a.err); };
-            const bool does_s = warp == NQ * 4 + 1, does_pv = !S::kApart || !does_s;
-            bool ok = true;
-            if (does_s) {
-                ok = wait(&q_full, 0) && wait(&k_full[0], 0);
-                tc_fence_after();
-                if (ok)
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) scores(i, 0);
-            }
+            bool ok = wait(&q_full, 0) && wait(&k_full[0], 0);
+            tc_fence_after();
+            if (ok)
+                for (int i = i0; i < i1; ++i) scores(i, 0);
             for (int j = 0; j < n && ok; ++j) {
-                const int s = j % kSt, s1 = (j + 1) % kSt;
                 const bool more = j + 1 < n;
-                if (S::kApart && does_s && more) {
-                    ok = wait(&k_full[s1], (j + 1) / kSt);
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i)
-                        if ((ok = ok && wait(&s_free[i], j))) {
-                            tc_fence_after();
-                            scores(i, s1);
-                        }
+                if (S::kTurns && more && (ok = wait(&k_full[(j + 1) % kSt], (j + 1) / kSt) && wait(&s_free[i0], j))) {
+                    // over the P of tile j - 1, whose P V this thread issued before
+                    tc_fence_after();
+                    scores(i0, j + 1);
                 }
-                if (does_pv) {
-                    ok = wait(&v_full[s], j / kSt);
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i)
-                        if ((ok = ok && wait(&p_full[i], j))) {
-                            tc_fence_after();
-                            values(i, s, !S::kRegO && j > 0);
-                            if (!S::kApart && more && (i > 0 || (ok = wait(&k_full[s1], (j + 1) / kSt)))) scores(i, s1);
-                        }
-                }
+                ok = ok && wait(&v_full[j % kSt], j / kSt);
+                for (int i = i0; i < i1; ++i)
+                    if ((ok = ok && wait(&p_full[i], j))) {
+                        tc_fence_after();
+                        values(i, j);
+                        if (!S::kTurns && more && (i > i0 || (ok = wait(&k_full[(j + 1) % kSt], (j + 1) / kSt)))) scores(i, j + 1);
+                    }
             }
             // no product is in flight when the tensor memory is freed
-            mma_commit(&drain[warp - NQ * 4 - 1]);
-            mbar_wait_bounded(&drain[warp - NQ * 4 - 1], 0, kDrainLimit, a.err);
+            mma_commit(&drain[i0]);
+            mbar_wait_bounded(&drain[i0], 0, kDrainLimit, a.err);
         }
     } else {  // softmax: thread = query
         if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + i * S::kP + lanes, tp = ts + S::kPAt,
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ti = tm + i * S::kP + lanes,
                        to = tm + S::kO + i * DP + lanes;
         const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
         float top = -INFINITY, sum = 0.f;               // top: raw score in use as the maximum
@@ -225,9 +220,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         for (int j = 0; j < n; ++j) {
             if (!(ok = warp_wait(&s_full[i], j & 1, limit, a.err))) break;
             tc_fence_after();
+            const uint32_t ts = ti + S::s_at(j), tp = ti + S::p_at(j);
             const int left = keys - (first + j) * BN;
             auto mask = [&](uint32_t (&x)[32], int g) {
                 if (left < BN) {
+                    asm volatile("");  // a branch, not 32 selects in every tile
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (g * 32 + e >= left) x[e] = 0xff800000u;  // -inf
@@ -299,13 +296,9 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int g = 0; g < BN / 32; ++g) tmem_ld32(ts + g * 32, x[g]);
 #pragma unroll
                 for (int g = 0; g < BN / 32; ++g) tmem_wait_ld(x[g]);
-                if (S::kApart) {
+                if (S::kTurns) {
                     tc_fence_before();
-                    mbar_arrive(&s_free[i]);
-                    if (j > 0) {  // the last P V has read P and left O
-                        if (!(ok = warp_wait(&o_done[i], (j - 1) & 1, limit, a.err))) break;
-                        tc_fence_after();
-                    }
+                    warp_arrive(&s_free[i]);
                 }
 #pragma unroll
                 for (int g = 0; g < BN / 32; ++g) mask(x[g], g);
@@ -328,6 +321,13 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     const bool raise = passed(m);
                     again = __any_sync(0xffffffffu, raise);
                     if (again) {  // j > 0, and only once: no row's scores pass their own maximum
+                        // P V of tile j - 1 has left O: before this S where that takes no turns, else before the next
+                        if (S::kTurns) {
+                            if (!(ok = j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
+                                                 : warp_wait(&o_done[i], 0, limit, a.err)))
+                                break;
+                            tc_fence_after();
+                        }
                         const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
                         if (raise) top = m;
                         sum *= keep;
@@ -342,14 +342,15 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         }
                     }
                 } while (again);
+                if (!ok) break;
             }
             const float2 sa = f2_unpack(s2[0]), sb = f2_unpack(s2[1]);
             sum += (sa.x + sa.y) + (sb.x + sb.y);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&p_full[i]);
+            warp_arrive(&p_full[i]);
         }
-        if (n > 0 && ok) ok = warp_wait(&o_done[i], (n - 1) & 1, limit, a.err);
+        if (n > 0 && ok) ok = warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
         tc_fence_after();
         if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && ok;

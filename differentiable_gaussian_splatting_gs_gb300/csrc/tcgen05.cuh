@@ -136,6 +136,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One arrival for the whole warp, after all its lanes got here (128 arrivals on one word would take turns).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if (elect_one()) mbar_arrive(bar);
+}
+
 // mbar_wait_bounded by a whole warp: one answer, so that a warp whose wait gave up stays together for the
 // warp-wide tensor-memory instructions that follow.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit, unsigned* err) {
