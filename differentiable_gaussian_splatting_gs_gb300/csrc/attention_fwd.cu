@@ -8,10 +8,11 @@
 // last 128 of them in turn: the next S is then formed while this one's softmax runs, and the softmax
 // never waits for P V. Otherwise the next S waits for P V.
 //
-// The softmax is bound by its exponentials (4 cycles a warp instruction and scheduler), so nothing may come
-// before them: P is formed with the maximum of the tiles before while this tile's is found. Only when a row's
-// scores pass the maximum in use by 2^8 is it raised, O rescaled and the tile's P formed again; below that P
-// reaches 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
+// The softmax is bound by its exponentials (4 cycles a warp instruction and scheduler: 1024 for two 128 x 128
+// tiles, as many as their products take with heads of 64). Two query tiles take turns at them: while one forms P,
+// the other waits for S, loads it and finds its maximum. Left to themselves they fall into step, and the exponentials
+// stand still while both load. The maximum in use is only raised, and O rescaled, when a row's scores pass it by
+// 2^8: P may then reach 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -111,11 +112,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = 0; j < n && ok; ++j) {
                     const int s = j % kSt;
                     const unsigned ph = (j / kSt + 1) & 1;
-                    if (j >= kSt && !(ok = mbar_wait_bounded(&k_free[s], ph, limit, a.err))) break;
+                    if (j >= kSt && !(ok = mbar_sleep_bounded(&k_free[s], ph, limit, a.err))) break;
                     mbar_arrive_expect_tx(&k_full[s], S::kKV);
                     load_rows<DP, PL, BN>(sk + s * S::kKV, tk, (first + j) * BN, b, hk, a.kv_heads, &k_full[s]);
                     sent = 2 * j + 1;
-                    if (j >= kSt && !(ok = mbar_wait_bounded(&v_free[s], ph, limit, a.err))) break;
+                    if (j >= kSt && !(ok = mbar_sleep_bounded(&v_free[s], ph, limit, a.err))) break;
                     mbar_arrive_expect_tx(&v_full[s], S::kKV);
                     load_rows<DP, PL, BN>(sv + s * S::kKV, tv, (first + j) * BN, b, hk, a.kv_heads, &v_full[s]);
                     sent = 2 * j + 2;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 if (j >= n - 2) mma_commit(&o_done[i]);
                 if (i == i1 - 1) mma_commit(&v_free[s]);
             };
-            auto wait = [&](uint64_t* bar, int j) { return mbar_wait_bounded(bar, j & 1, limit, a.err); };
+            auto wait = [&](uint64_t* bar, int j) { return mbar_sleep_bounded(bar, j & 1, limit, a.err); };
             bool ok = wait(&q_full, 0) && wait(&k_full[0], 0);
             tc_fence_after();
             if (ok)
@@ -216,9 +217,15 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 tmem_wait_ld(o);
             }
         };
+        // Turns at the exponentials: a barrier per query tile, where its warps meet the other's that are done. Every
+        // warp comes through every turn, one whose wait gave up too.
+        auto my_turn = [&]() {
+            if (NQ == 2) asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory");
+        };
+        if (NQ == 2 && i == 1 && n > 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            if (!(ok = warp_wait(&s_full[i], j & 1, limit, a.err))) break;
+            ok = ok && warp_wait(&s_full[i], j & 1, limit, a.err);
             tc_fence_after();
             const uint32_t ts = ti + S::s_at(j), tp = ti + S::p_at(j);
             const int left = keys - (first + j) * BN;
@@ -230,27 +237,41 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         if (g * 32 + e >= left) x[e] = 0xff800000u;  // -inf
                 }
             };
-            auto largest = [&](const uint32_t (&x)[32], float (&m)[2]) {
+            float m8[8];  // eight chains: a maximum takes about ten cycles
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    m[0] = max3(m[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                    m[1] = max3(m[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                }
+            for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
+            auto largest = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) m8[e / 2 % 8] = max3(m8[e / 2 % 8], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             };
+            auto row_max = [&]() { return max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])); };
             // P of 32 keys into its columns; s: the thread's sum
-            auto probabilities = [&](const uint32_t (&x)[32], int g, f32x2 b2, f32x2 (&s)[2]) {
+            auto probabilities = [&](const uint32_t (&x)[32], int g, f32x2 b2, f32x2 (&s)[4]) {
                 uint32_t p[PL][16];
+                const f32x2 c2 = f2_pack(c, c), one = f2_pack(1.f, 1.f);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2_pack(c, c), b2));
-                    float u = ex2_approx(y.x), w = ex2_approx(y.y);
-                    s[e & 1] = f2_fma(f2_pack(u, w), f2_pack(1.f, 1.f), s[e & 1]);
+                for (int h = 0; h < 2; ++h) {
+                    float u[16];
 #pragma unroll
-                    for (int q = 0; q < PL; ++q) {
-                        p[q][e] = pack2<T>(u, w);
-                        if (q + 1 < PL) {  // what the plane leaves (bfloat16 is the upper half of a float)
-                            u -= __uint_as_float(p[q][e] << 16);
-                            w -= __uint_as_float(p[q][e] & 0xffff0000u);
+                    for (int e = 0; e < 8; ++e) {
+                        const int k = h * 16 + 2 * e;
+                        const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, b2));
+                        u[2 * e] = y.x;
+                        u[2 * e + 1] = y.y;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = ex2_approx(u[e]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        s[e & 3] = f2_fma(f2_pack(u[2 * e], u[2 * e + 1]), one, s[e & 3]);
+#pragma unroll
+                        for (int q = 0; q < PL; ++q) {
+                            uint32_t& w = p[q][h * 8 + e];
+                            w = pack2<T>(u[2 * e], u[2 * e + 1]);
+                            if (q + 1 < PL) {  // what the plane leaves (bfloat16 is the upper half of a float)
+                                u[2 * e] -= __uint_as_float(w << 16);
+                                u[2 * e + 1] -= __uint_as_float(w & 0xffff0000u);
+                            }
                         }
                     }
                 }
@@ -260,8 +281,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             // whether the row's maximum in use is too far below m; a score of -inf is no error: exp(-inf) = 0
             auto passed = [&](float m) { return (m - top) * c > 8.f || (top == -INFINITY && m > -INFINITY); };
             auto base = [&]() { const float t0 = top == -INFINITY ? 0.f : -top * c; return f2_pack(t0, t0); };
-            f32x2 s2[2];
-            float m2[2] = {-INFINITY, -INFINITY};
+            f32x2 s2[4];
             if constexpr (S::kRegO) {
                 // the registers hold O: the scores are read twice, and each group of P takes the columns of its scores
                 if (j > 0) add_tile();
@@ -271,9 +291,9 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     tmem_ld32(ts + g * 32, x);
                     tmem_wait_ld(x);
                     mask(x, g);
-                    largest(x, m2);
+                    largest(x);
                 }
-                const float m = fmaxf(m2[0], m2[1]);
+                const float m = row_max();
                 if (passed(m)) {
                     const float keep = top == -INFINITY ? 0.f : ex2_approx((top - m) * c);
                     top = m;
@@ -282,7 +302,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     for (int e = 0; e < kOut; ++e) out[e] *= keep;
                 }
                 __syncwarp();
-                s2[0] = s2[1] = f2_pack(0.f, 0.f);
+                my_turn();
+                s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int g = 0; g < BN / 32; ++g) {
                     tmem_ld32(ts + g * 32, x);
@@ -302,35 +323,21 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 }
 #pragma unroll
                 for (int g = 0; g < BN / 32; ++g) mask(x[g], g);
-                if (j == 0) {
 #pragma unroll
-                    for (int g = 0; g < BN / 32; ++g) largest(x[g], m2);
-                    top = fmaxf(m2[0], m2[1]);
-                }
-                bool again;
-                do {
-                    s2[0] = s2[1] = f2_pack(0.f, 0.f);
-                    m2[0] = m2[1] = -INFINITY;
-                    const f32x2 b2 = base();
-#pragma unroll
-                    for (int g = 0; g < BN / 32; ++g) {
-                        largest(x[g], m2);
-                        probabilities(x[g], g, b2, s2);
-                    }
-                    const float m = fmaxf(m2[0], m2[1]);
-                    const bool raise = passed(m);
-                    again = __any_sync(0xffffffffu, raise);
-                    if (again) {  // j > 0, and only once: no row's scores pass their own maximum
+                for (int g = 0; g < BN / 32; ++g) largest(x[g]);
+                const float m = row_max();
+                const bool raise = passed(m);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
+                    if (raise) top = m;
+                    sum *= keep;
+                    if (j > 0) {
                         // P V of tile j - 1 has left O: before this S where that takes no turns, else before the next
                         if (S::kTurns) {
-                            if (!(ok = j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
-                                                 : warp_wait(&o_done[i], 0, limit, a.err)))
-                                break;
+                            ok = ok && (j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
+                                                  : warp_wait(&o_done[i], 0, limit, a.err));
                             tc_fence_after();
                         }
-                        const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
-                        if (raise) top = m;
-                        sum *= keep;
 #pragma unroll
                         for (int g = 0; g < DP / 32; ++g) {
                             uint32_t o[32];
@@ -341,16 +348,22 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                             tmem_st32(to + g * 32, o);
                         }
                     }
-                } while (again);
-                if (!ok) break;
+                }
+                my_turn();
+                s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
+                const f32x2 b2 = base();
+#pragma unroll
+                for (int g = 0; g < BN / 32; ++g) probabilities(x[g], g, b2, s2);
             }
-            const float2 sa = f2_unpack(s2[0]), sb = f2_unpack(s2[1]);
+            const f32x2 one = f2_pack(1.f, 1.f);
+            const float2 sa = f2_unpack(f2_fma(s2[0], one, s2[2])), sb = f2_unpack(f2_fma(s2[1], one, s2[3]));
             sum += (sa.x + sa.y) + (sb.x + sb.y);
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&p_full[i]);
+            if (NQ == 2 && (i == 0 || j + 1 < n)) asm volatile("bar.arrive %0, 256;" ::"r"(2 - i) : "memory");
         }
-        if (n > 0 && ok) ok = warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
+        if (n > 0) ok = ok && warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
         tc_fence_after();
         if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && ok;
