@@ -13,8 +13,10 @@ constexpr int kMaxTcDim = 128;  // head dimensions above it go to the float32 ke
 struct Plan {
     bool tc, pack_q, pack_kv, pack_do;
     int planes, dp, nq, splits;
-    long long rows_k;  // rows of a packed head of K or V
-    size_t count, index, q, k, v, part, part_lse, delta, bytes;
+    int splits_q, splits_k;  // backward: of the walks for dq, and for dk and dv
+    long long rows_k;        // rows of a packed head of K or V
+    long long qpad;          // queries of a head, rounded up to the tiles that the backward walks
+    size_t count, index, q, k, v, dout, part, part_lse, delta, nlse, norms, factor, bytes;
 };
 
 bool copyable(const AttnTensor& t, const AttnArgs& a, int len) {
@@ -34,34 +36,56 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         return here;
     };
     const size_t bq = (size_t)a.batch * a.heads * a.len_q, bk = (size_t)a.batch * a.kv_heads;
-    if (backward) p.delta = take(bq * sizeof(float));
-    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && !backward;
+    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && a.len_q > 0 && !(backward && a.dtype == GS_DTYPE_F32);
+    if (backward && !p.tc) p.delta = take(bq * sizeof(float));
     if (p.tc) {
         const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
         p.planes = wide ? 3 : 1;
         p.dp = a.d <= 64 ? 64 : 128;
         p.rows_k = ((long long)a.len_k + kTileRows - 1) / kTileRows * kTileRows;
         p.pack_q = wide || !tensors || !copyable(a.q, a, a.len_q);
+        p.pack_do = backward && (!tensors || !copyable(a.dout, a, a.len_q));
         p.pack_kv = wide || masked || !tensors || !copyable(a.k, a, a.len_k) || !copyable(a.v, a, a.len_k);
+        // Few blocks: the walk is split, at least `least` tiles each, so that every SM has one.
         const int sms = device_sm_count();
-        const bool two = !(wide && p.dp == 128) && (long long)((a.len_q + 255) / 256) * a.heads * a.batch >= sms;
-        p.nq = two ? 2 : 1;
-        const long long blocks = (long long)((a.len_q + 128 * p.nq - 1) / (128 * p.nq)) * a.heads * a.batch;
-        const long long key_tiles = p.rows_k / kTileRows;
-        long long splits = blocks > 0 ? sms / blocks : 1;
-        if (splits > (key_tiles + 1) / 2) splits = (key_tiles + 1) / 2;
-        p.splits = splits < 1 ? 1 : (int)splits;
+        auto split = [&](long long blocks, long long tiles, long long least) {
+            long long s = blocks > 0 ? sms / blocks : 1;
+            if (s > (tiles + least - 1) / least) s = (tiles + least - 1) / least;
+            return s < 1 ? 1 : (int)s;
+        };
+        auto over = [](long long n, long long m) { return (n + m - 1) / m; };
+        if (!backward) {
+            const bool two = !(wide && p.dp == 128) && over(a.len_q, 256) * a.heads * a.batch >= sms;
+            p.nq = two ? 2 : 1;
+            p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
+        } else {
+            p.qpad = over(a.len_q, attn_bwd_walk()) * attn_bwd_walk();
+            p.splits_q = split(over(a.len_q, attn_bwd_rows(false, p.dp)) * a.heads * a.batch, over(a.len_k, attn_bwd_walk()), 4);
+            p.splits_k = split(over(a.len_k, attn_bwd_rows(true, p.dp)) * a.kv_heads * a.batch,
+                               p.qpad / attn_bwd_walk() * (a.heads / a.kv_heads), 4);
+            p.nlse = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
+            p.delta = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
+            if (a.dtype == GS_DTYPE_F16) {
+                p.norms = take(bk * 2 * sizeof(unsigned));
+                p.factor = take(bk * sizeof(float2));
+            }
+        }
         const size_t row = (size_t)p.planes * p.dp * 2;
         if (a.key_mask) {
             p.count = take(a.batch * sizeof(int));
             p.index = take((size_t)a.batch * a.len_k * sizeof(int));
         }
         if (p.pack_q) p.q = take(bq * row);
+        if (p.pack_do) p.dout = take(bq * row);
         if (p.pack_kv) {
             p.k = take(bk * p.rows_k * row);
             p.v = take(bk * p.rows_k * row);
         }
-        if (p.splits > 1) {
+        if (backward) {
+            const size_t q = p.splits_q > 1 ? (size_t)p.splits_q * bq * p.dp * sizeof(float) : 0;
+            const size_t k = p.splits_k > 1 ? (size_t)p.splits_k * 2 * bk * p.rows_k * p.dp * sizeof(float) : 0;
+            p.part = take(q > k ? q : k);
+        } else if (p.splits > 1) {
             p.part = take((size_t)p.splits * bq * p.dp * sizeof(float));
             p.part_lse = take((size_t)p.splits * bq * sizeof(float));
         }
@@ -107,6 +131,27 @@ cudaError_t operand(TcTensor& t, const Plan& p, const AttnArgs& a, const AttnTen
     return encode(t, half, src.data, {a.d, len, heads, a.batch}, {src.len_stride, src.head_stride, src.batch_stride}, box_rows);
 }
 
+// The key mask's index, and K, V, Q and dout laid out where the kernels cannot read them as they are.
+cudaError_t lay_out(const Plan& p, const AttnArgs& a, char* ws, int*& count, int*& index, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    count = index = nullptr;
+    if (a.key_mask) {
+        count = reinterpret_cast<int*>(ws + p.count);
+        index = reinterpret_cast<int*>(ws + p.index);
+        if ((e = launch_attn_index(a, count, index, st))) return e;
+    }
+    auto queries = [&](const AttnTensor& t, size_t at) {
+        return launch_attn_pack(a, t, a.heads, a.len_q, false, nullptr, nullptr, p.planes, p.dp, a.len_q, ws + at, st);
+    };
+    auto keys = [&](const AttnTensor& t, size_t at) {
+        return launch_attn_pack(a, t, a.kv_heads, a.len_k, true, count, index, p.planes, p.dp, p.rows_k, ws + at, st);
+    };
+    if (p.pack_q && (e = queries(a.q, p.q))) return e;
+    if (p.pack_do && (e = queries(a.dout, p.dout))) return e;
+    if (p.pack_kv && ((e = keys(a.k, p.k)) || (e = keys(a.v, p.v)))) return e;
+    return e;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a, bool backward) { return plan(a, backward, false).bytes; }
@@ -115,20 +160,10 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
     const Plan p = plan(a, false, true);
     if (!p.tc) return launch_attn_simt(a, false, st);
     char* ws = static_cast<char*>(workspace);
-    cudaError_t e = cudaSuccess;
-    TcArgs t{a, nullptr, nullptr, nullptr, 0, p.splits};
-    int* index = nullptr;
-    if (a.key_mask) {
-        int* count = reinterpret_cast<int*>(ws + p.count);
-        index = reinterpret_cast<int*>(ws + p.index);
-        if ((e = launch_attn_index(a, count, index, st))) return e;
-        t.count = count;
-    }
-    if (p.pack_q && (e = launch_attn_pack(a, a.q, a.heads, a.len_q, false, nullptr, nullptr, p.planes, p.dp, a.len_q, ws + p.q, st)))
-        return e;
-    if (p.pack_kv && ((e = launch_attn_pack(a, a.k, a.kv_heads, a.len_k, true, t.count, index, p.planes, p.dp, p.rows_k, ws + p.k, st)) ||
-                      (e = launch_attn_pack(a, a.v, a.kv_heads, a.len_k, true, t.count, index, p.planes, p.dp, p.rows_k, ws + p.v, st))))
-        return e;
+    int *count, *index;
+    cudaError_t e = lay_out(p, a, ws, count, index, st);
+    if (e) return e;
+    TcArgs t{a, count, nullptr, nullptr, 0, p.splits};
     const int bn = p.planes == 3 && p.dp == 128 ? 64 : 128;
     TcTensor q, k, v;
     if ((e = operand(q, p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, kTileRows)) ||
@@ -144,10 +179,29 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
 }
 
 cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t st) {
+    const Plan p = plan(args, true, true);
     AttnArgs a = args;
-    a.delta = static_cast<float*>(workspace);
-    cudaError_t e = launch_attn_delta(a, st);
-    return e ? e : launch_attn_simt(a, true, st);
+    char* ws = static_cast<char*>(workspace);
+    cudaError_t e;
+    if (!p.tc) {
+        a.delta = reinterpret_cast<float*>(ws + p.delta);
+        return (e = launch_attn_delta(a, st)) ? e : launch_attn_simt(a, true, st);
+    }
+    int *count, *index;
+    if ((e = lay_out(p, a, ws, count, index, st))) return e;
+    const TcBwd w{a, count, index, reinterpret_cast<float*>(ws + p.nlse), reinterpret_cast<float*>(ws + p.delta),
+                  reinterpret_cast<unsigned*>(ws + p.norms), reinterpret_cast<float2*>(ws + p.factor), reinterpret_cast<float*>(ws + p.part), p.qpad, p.rows_k, p.dp, p.splits_q, p.splits_k};
+    TcTensor x[2][4];  // as row tiles, as walked tiles: Q, dout, K, V
+    for (int i = 0; i < 2; ++i) {
+        const int box = i == 0 ? kTileRows : attn_bwd_walk();
+        if ((e = operand(x[i][0], p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, box)) ||
+            (e = operand(x[i][1], p, a, a.dout, a.heads, a.len_q, p.pack_do, ws + p.dout, a.len_q, box)) ||
+            (e = operand(x[i][2], p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, box)) ||
+            (e = operand(x[i][3], p, a, a.v, a.kv_heads, a.len_k, p.pack_kv, ws + p.v, p.rows_k, box)))
+            return e;
+    }
+    if ((a.key_mask || a.k_len) && (e = launch_attn_zero(a, st))) return e;
+    return launch_attn_bwd_tc(w, x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3], st);
 }
 
 }  // namespace gs

@@ -1,0 +1,513 @@
+// Cross attention, backward, on the tensor cores (16-bit types).
+//
+// One kernel in two roles. In both a block holds 128 or 256 rows and walks the other side in tiles of 64, forming
+//   S = A1 B1^T,  dP = A2 B2^T,  P = exp(scale S - lse),  dS = P (dP - delta):
+//   queries: rows are queries, A1 = Q, A2 = dout, B1 = K, B2 = V:   dq = scale sum dS B1;
+//   keys:    rows are keys,    A1 = K, A2 = V, B1 = Q, B2 = dout:   dk = scale sum dS B1,  dv = sum P B2,
+//            over the queries of every head that shares the key head.
+// So each result is summed by one block in a fixed order, without atomics or a float32 copy in memory, at the
+// price of forming S and dP twice (7 products instead of 5); what bounds the kernel is the elementwise part
+// between the products, and atomics would add 32 KB of it per tile. lse and delta are known, so nothing is
+// rescaled and a tile's elements are independent of the others'.
+//
+// float16: P is formed 2^15 times as large, and dS as many times (a power of two for each key head) as its bound
+// |dS| <= 2 scale max|dout| max|v| allows below the type's largest value; the sums are scaled back. Unscaled, the
+// small probabilities of long or peaked rows fell into the type's subnormal range (or, with large dout, out of it).
+//
+// Thread = row: a warpgroup turns a 128 x 64 tile of S and dP from tensor memory into dS and P, 16-bit in the
+// same columns, which feed the next products as their A operand there. Two warpgroups, each with columns of its own:
+// of two row tiles (kRows = 2), or of one with the walked tiles in turn. Products are issued by one thread, in an
+// order that does not depend on the timing.
+#include "attention_tc.cuh"
+
+namespace gs {
+
+constexpr int kBN = 64;  // walked rows per tile
+
+template <int DP, bool KEYS>
+struct BwdShape {
+    // Row tiles: two where their accumulators fit beside 2 x 128 columns of S and dP.
+    static constexpr int kRows = KEYS && DP == 128 ? 1 : 2;
+    static constexpr int kA = DP * kTileRows * 2;       // bytes of one operand's row tile
+    static constexpr int kB = DP * kBN * 2;             // bytes of one operand's walked tile
+    static constexpr int kStage = 2 * kB + 1024;        // with the tile's lse and delta (KEYS)
+    static constexpr int kRoom = (225 * 1024 - 1024 - 2 * kRows * kA) / kStage;
+    static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
+    static constexpr int kSmem = 2 * kRows * kA + kStages * kStage + 1024;
+    static constexpr int kAcc = 256;                    // first accumulator column
+    static constexpr int kAccs = KEYS ? 2 : 1;
+    static_assert(kAcc + kRows * kAccs * DP <= 512 && kStages >= (kRows == 1 ? 3 : 2));
+};
+
+struct BwdArgs {
+    TcArgs t;              // t.part: float32 shares of dq, or of dk and then dv, or NULL; t.tiles: row blocks of a head
+    const float* nlse;     // [batch x heads][len_q padded]: the exponent's offset of each query (k_attn_stats)
+    const float* ndelta;   // likewise: -delta times `ds_in`
+    long long qpad;
+    // dS = P (dP ds_in + ndelta); the sums of dS B1 and of P B2 times ds_out and p_out. factor: ds_in and ds_out of
+    // each batch entry and key head instead, or NULL
+    float ds_in, ds_out, p_out;
+    const float2* factor;
+    const int* index;      // packed key -> key, or NULL
+    long long rows_k;
+};
+
+template <class T, int DP, bool KEYS>
+__global__ void __launch_bounds__(384, 1)
+    k_attn_bwd(const __grid_constant__ BwdArgs g, const __grid_constant__ TcTensor ta1, const __grid_constant__ TcTensor ta2,
+               const __grid_constant__ TcTensor tb1, const __grid_constant__ TcTensor tb2) {
+    using S = BwdShape<DP, KEYS>;
+    constexpr int kSt = S::kStages, kR = S::kRows;
+    pdl_entry();
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t a_full, full[kSt], empty[kSt], s_full[2], p_full[2], done, drain;
+    __shared__ uint32_t tmem_base;
+    const TcArgs& t = g.t;
+    const AttnArgs& a = t.a;
+    unsigned char* base = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
+    const uint32_t sa1 = smem_u32(base), sa2 = sa1 + kR * S::kA, sb = sa2 + kR * S::kA;
+    auto stats = [&](int s) { return reinterpret_cast<float*>(base + 2 * kR * S::kA + s * S::kStage + 2 * S::kB); };
+
+    int at = blockIdx.x;
+    const int block = at % t.tiles;
+    at /= t.tiles;
+    const int split = at % t.splits;
+    at /= t.splits;
+    const int share = a.heads / a.kv_heads, row_heads = KEYS ? a.kv_heads : a.heads;
+    const int h = at % row_heads, b = at / row_heads;
+    const int keys = keys_of(t, b), row0 = block * kR * kTileRows;
+    const int rows = KEYS ? keys : a.len_q;
+    // walked tiles: of the keys, or of the queries of `share` heads one after the other
+    const int per_head = KEYS ? (a.len_q + kBN - 1) / kBN : (keys + kBN - 1) / kBN;
+    const int all = KEYS ? per_head * share : per_head, per = (all + t.splits - 1) / t.splits;
+    const int first = min(split * per, all), n = row0 < rows ? min(per, all - first) : 0;
+    const int warp = threadIdx.x >> 5;
+    const unsigned limit = a.spin_limit;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&a_full, 1);
+        for (int i = 0; i < kSt; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(&done, 1);
+        mbar_init(&drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc<512>(&tmem_base);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_base;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8 && n > 0 && elect_one()) {  // copies
+            mbar_arrive_expect_tx(&a_full, 2 * kR * S::kA);
+            for (int i = 0; i < kR; ++i) {
+                load_rows<DP, 1, kTileRows>(sa1 + i * S::kA, ta1, row0 + i * kTileRows, b, h, row_heads, &a_full);
+                load_rows<DP, 1, kTileRows>(sa2 + i * S::kA, ta2, row0 + i * kTileRows, b, h, row_heads, &a_full);
+            }
+            int sent = 0;
+            for (int j = 0; j < n; ++j) {
+                const int s = j % kSt, x = first + j;
+                if (j >= kSt && !mbar_sleep_bounded(&empty[s], (j / kSt + 1) & 1, limit, a.err)) break;
+                const int wh = KEYS ? h * share + x / per_head : h / share, w0 = (KEYS ? x % per_head : x) * kBN;
+                mbar_arrive_expect_tx(&full[s], 2 * S::kB + (KEYS ? 2 * kBN * 4 : 0));
+                load_rows<DP, 1, kBN>(sb + s * S::kStage, tb1, w0, b, wh, KEYS ? a.heads : a.kv_heads, &full[s]);
+                load_rows<DP, 1, kBN>(sb + s * S::kStage + S::kB, tb2, w0, b, wh, KEYS ? a.heads : a.kv_heads, &full[s]);
+                if (KEYS) {
+                    const long long q = ((long long)b * a.heads + wh) * g.qpad + w0;
+                    bulk_copy_g2s(stats(s), g.nlse + q, kBN * 4, &full[s]);
+                    bulk_copy_g2s(stats(s) + kBN, g.ndelta + q, kBN * 4, &full[s]);
+                }
+                sent = j + 1;
+            }
+            // every copy lands before the block ends, whatever became of its reader
+            mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
+            for (int j = max(0, sent - kSt); j < sent; ++j) mbar_wait_bounded(&full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
+        } else if (warp == 9 && n > 0 && elect_one()) {  // products
+            const int steps = (a.d + 15) / 16;
+            const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
+            auto wait = [&](uint64_t* bar, int k) { return mbar_sleep_bounded(bar, k & 1, limit, a.err); };
+            // S and dP of walked tile j in warpgroup w's columns
+            auto scores = [&](int w, int j) {
+                const uint32_t row = (kR == 2 ? w : 0) * S::kA, tile = sb + (j % kSt) * S::kStage;
+                const uint32_t x1 = tile_desc(sa1 + row), x2 = tile_desc(sa2 + row), y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB);
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x)
+                    if (x < steps)
+                        mma_ss(tm + w * 128, x1 + (x / 4) * kTileRows * 8 + (x % 4) * 2, y1 + (x / 4) * kBN * 8 + (x % 4) * 2, s_desc, x > 0);
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x)
+                    if (x < steps)
+                        mma_ss(tm + w * 128 + 64, x2 + (x / 4) * kTileRows * 8 + (x % 4) * 2, y2 + (x / 4) * kBN * 8 + (x % 4) * 2, s_desc, x > 0);
+                mma_commit(&s_full[w]);
+            };
+            auto gradients = [&](int w, int j) {
+                const uint32_t acc = tm + S::kAcc + (kR == 2 ? w : 0) * S::kAccs * DP, tile = sb + (j % kSt) * S::kStage;
+                const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
+#pragma unroll
+                for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, tm + w * 128 + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
+                if (KEYS)
+#pragma unroll
+                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, tm + w * 128 + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
+                if (kR == 1 || w == 1) mma_commit(&empty[j % kSt]);
+            };
+            bool ok = wait(&a_full, 0);
+            for (int w = 0; w < 2 && ok; ++w) {
+                const int j = kR == 2 ? 0 : w;
+                if (j < n && (ok = wait(&full[j % kSt], j / kSt))) {
+                    tc_fence_after();
+                    scores(w, j);
+                }
+            }
+            for (int j = 0; j < n && ok; ++j)
+                for (int w = kR == 2 ? 0 : j & 1; w < (kR == 2 ? 2 : (j & 1) + 1) && ok; ++w) {
+                    if (!(ok = wait(&p_full[w], kR == 2 ? j : j / 2))) break;
+                    tc_fence_after();
+                    gradients(w, j);
+                    const int next = kR == 2 ? j + 1 : j + 2;
+                    if (next < n && (ok = wait(&full[next % kSt], next / kSt))) scores(w, next);
+                }
+            mma_commit(&done);
+            // no product is in flight when the tensor memory is freed
+            mma_commit(&drain);
+            mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
+        }
+    } else {  // elementwise: thread = row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int w = warp / 4;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + w * 128 + lanes;
+        const int row = row0 + (kR == 2 ? w * kTileRows : 0) + (threadIdx.x & 127);
+        const float c = a.scale * 1.4426950408889634f;
+        const float2 factor = g.factor ? g.factor[b * a.kv_heads + (KEYS ? h : h / share)] : make_float2(g.ds_in, g.ds_out);
+        const f32x2 c2 = f2_pack(c, c), i2 = f2_pack(factor.x, factor.x);
+        f32x2 l2 = 0, d2 = 0;  // the row's own, where rows are queries
+        if (!KEYS) {
+            const long long q = ((long long)b * a.heads + h) * g.qpad + row;
+            const float l = row < a.len_q ? g.nlse[q] : -INFINITY, d = row < a.len_q ? g.ndelta[q] : 0.f;
+            l2 = f2_pack(l, l);
+            d2 = f2_pack(d, d);
+        }
+        bool ok = true;
+        for (int j = kR == 2 ? 0 : w, k = 0; j < n; j += kR == 2 ? 1 : 2, ++k) {
+            ok = ok && warp_wait(&s_full[w], k & 1, limit, a.err);
+            if (!ok) break;  // the same in all lanes; nothing below waits for this warp without a limit
+            tc_fence_after();
+            uint32_t s[2][32], dp[2][32];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                tmem_ld32(ts + y * 32, s[y]);
+                tmem_ld32(ts + 64 + y * 32, dp[y]);
+            }
+            const float* st = stats(j % kSt);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                tmem_wait_ld(s[y]);
+                tmem_wait_ld(dp[y]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t p[16], ds[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (KEYS) {  // columns are queries
+                        const float2 l = *reinterpret_cast<const float2*>(st + y * 32 + 2 * e);
+                        const float2 d = *reinterpret_cast<const float2*>(st + kBN + y * 32 + 2 * e);
+                        l2 = f2_pack(l.x, l.y);
+                        d2 = f2_pack(d.x, d.y);
+                    }
+                    const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y][2 * e]), __uint_as_float(s[y][2 * e + 1])), c2, l2));
+                    const float u0 = ex2_approx(z.x), u1 = ex2_approx(z.y);
+                    const f32x2 x = f2_fma(f2_pack(__uint_as_float(dp[y][2 * e]), __uint_as_float(dp[y][2 * e + 1])), i2, d2);
+                    const float2 v = f2_unpack(f2_mul(f2_pack(u0, u1), x));
+                    if (KEYS) p[e] = pack2<T>(u0, u1);
+                    ds[e] = pack2<T>(v.x, v.y);
+                }
+                if (!KEYS) {
+                    const int left = keys - (first + j) * kBN - y * 32;
+                    if (left < 32) {
+                        asm volatile("");  // a branch
+                        // a key beyond the last one: exp of an unbounded number came of its score of 0
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            if (2 * e >= left) ds[e] = 0u;
+                            else if (2 * e + 1 >= left) ds[e] &= 0xffffu;
+                        }
+                    }
+                }
+                tmem_st16(ts + 64 + y * 16, ds);
+                if (KEYS) tmem_st16(ts + y * 16, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&p_full[w]);
+        }
+        if (n > 0) ok = warp_wait(&done, 0, limit, a.err) && ok;
+        tc_fence_after();
+        // a row tile per warpgroup, or one with an accumulator each
+#pragma unroll
+        for (int x = 0; x < (kR == 2 ? S::kAccs : 1); ++x) {
+            const int which = kR == 2 ? x : w;  // 0: of dS B1, 1: of P B2
+            const uint32_t acc = tm + S::kAcc + lanes + (kR == 2 ? w * S::kAccs * DP : 0) + which * DP;
+            const float f = which == 0 ? factor.y : g.p_out;
+            const bool live = row < rows && ok;
+            const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
+            const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
+            T* dst = static_cast<T*>(out.data) + b * out.batch_stride + h * out.head_stride + to * out.len_stride;
+            const long long part_rows = KEYS ? g.rows_k : a.len_q;
+            const long long heads_all = (long long)a.batch * row_heads;
+            float* part = t.part ? t.part + ((((long long)split * S::kAccs + which) * heads_all + (long long)b * row_heads + h) * part_rows + row) * DP
+                                 : nullptr;
+            const bool vec = a.d % 8 == 0 && out.batch_stride % 8 == 0 && out.head_stride % 8 == 0 && out.len_stride % 8 == 0 &&
+                             reinterpret_cast<uintptr_t>(out.data) % 16 == 0;
+#pragma unroll
+            for (int y = 0; y < DP / 32; ++y) {
+                uint32_t o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+                if (n > 0) {
+                    tmem_ld32(acc + y * 32, o);
+                    tmem_wait_ld(o);
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const int col = y * 32 + e;
+                        if (part) {
+                            *reinterpret_cast<float4*>(part + col) = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                                                                 __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                            *reinterpret_cast<float4*>(part + col + 4) = make_float4(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f,
+                                                                                     __uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
+                            continue;
+                        }
+                        Pack<T, 8> v;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v.v[k] = from_float<T>(__uint_as_float(o[e + k]) * f);
+                        if (vec) {
+                            if (col < a.d) *reinterpret_cast<Pack<T, 8>*>(dst + col) = v;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (col + k < a.d) dst[col + k] = v.v[k];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_free<512>(tm);
+}
+
+// The largest squared norms of dout's and of v's rows of each batch entry and key head, as bits of floats (zero
+// before): where = 0: queries, 1: keys. Eight lanes per row; maxima do not depend on their order.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_norms(const AttnArgs a, long long pad, int where, unsigned* norms) {
+    pdl_entry();
+    __shared__ unsigned most;
+    if (threadIdx.x == 0) most = 0u;
+    __syncthreads();
+    const int heads = where ? a.kv_heads : a.heads, lane = threadIdx.x & 7;
+    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8, bh = at / pad, i = at % pad;  // a block is within a head
+    const int b = (int)(bh / heads), h = (int)(bh % heads);
+    float s = 0.f;
+    if (b < a.batch && (where ? i < a.len_k && key_valid(a, b, (int)i, key_count(a, b)) : i < a.len_q)) {
+        const AttnTensor& t = where ? a.v : a.dout;
+        const T* x = head_base<T>(t, b, h) + i * t.len_stride;
+        for (int c = lane * 8; c < a.d; c += 64)
+            for (int k = 0; k < 8 && c + k < a.d; ++k) s = fmaf(to_float(x[c + k]), to_float(x[c + k]), s);
+    }
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    atomicMax(&most, __float_as_uint(fabsf(s)));  // NaN compares above every number
+    __syncthreads();
+    if (threadIdx.x == 0 && b < a.batch) atomicMax(norms + (b * a.kv_heads + (where ? h : h / (a.heads / a.kv_heads))) * 2 + where, most);
+}
+
+// Of every query, padded: boost - lse log2(e), so that P times 2^boost = exp2(scale log2(e) S + that); and -delta
+// times ds_in. -inf and 0 where there is no query, -inf where it has no key. Eight lanes per query. With norms,
+// ds_in comes from them, and the first query of a key head's first head leaves its factors.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long qpad, float boost, float ds_in, const unsigned* norms,
+                                                    float2* factor, float* nlse, float* ndelta) {
+    pdl_entry();
+    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8;
+    const int lane = threadIdx.x & 7;
+    const long long bh = at / qpad, i = at % qpad;
+    const bool in = bh < (long long)a.batch * a.heads && i < a.len_q;
+    float s = 0.f;
+    if (in) {
+        const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+        const T* o = head_base<T>(a.out, b, h) + i * a.out.len_stride;
+        const T* d = head_base<T>(a.dout, b, h) + i * a.dout.len_stride;
+        constexpr int V = 16 / (int)sizeof(T);
+        if (a.d % V == 0 && (reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(d)) % 16 == 0) {
+            for (int c = lane * V; c < a.d; c += 8 * V) {
+                const Pack<T, V> x = *reinterpret_cast<const Pack<T, V>*>(o + c), y = *reinterpret_cast<const Pack<T, V>*>(d + c);
+#pragma unroll
+                for (int k = 0; k < V; ++k) s = fmaf(to_float(x.v[k]), to_float(y.v[k]), s);
+            }
+        } else {
+            // the same elements per lane as above, so that a layout changes no sum
+            for (int c = lane * V; c < a.d; c += 8 * V)
+                for (int k = 0; k < V && c + k < a.d; ++k) s = fmaf(to_float(o[c + k]), to_float(d[c + k]), s);
+        }
+    }
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0 && bh < (long long)a.batch * a.heads) {
+        if (norms) {
+            const int share = a.heads / a.kv_heads, b = (int)(bh / a.heads), h = (int)(bh % a.heads), at2 = b * a.kv_heads + h / share;
+            const float bound = 2.f * a.scale * sqrtf(__uint_as_float(norms[2 * at2])) * sqrtf(__uint_as_float(norms[2 * at2 + 1]));
+            // the power of two that leaves the bound below 2^15; 1 where there is none
+            int e = 0;
+            if (bound < 3e38f) {
+                frexpf(bound, &e);  // bound < 2^e
+                e = bound > 0.f ? min(max(15 - e, -24), 24) : 0;
+            }
+            ds_in = a.scale * exp2f((float)e - boost);
+            if (i == 0 && h % share == 0) factor[at2] = make_float2(ds_in, exp2f((float)-e));
+        }
+        const float l = in ? a.lse[bh * a.len_q + i] : -INFINITY;
+        nlse[at] = l == -INFINITY ? -INFINITY : boost - l * 1.4426950408889634f;
+        ndelta[at] = -s * ds_in;
+    }
+}
+
+// What a walk that was split left: the shares added up in order, a thread per eight elements of a row. index: as
+// BwdArgs; rows: of a head in the shares, of which the first `live` of a batch entry were written.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_sum(const BwdArgs g, const AttnTensor t, int heads, int keys, const float* part,
+                                                  long long split_stride, int splits, int dp, long long rows) {
+    pdl_entry();
+    const AttnArgs& a = g.t.a;
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int per = dp / 8, c = (int)(at % per) * 8;
+    const long long r = at / per, bh = r / rows;
+    const int row = (int)(r % rows), b = (int)(bh / heads), h = (int)(bh % heads);
+    if (b >= a.batch || c >= a.d || row >= (keys ? keys_of(g.t, b) : a.len_q)) return;
+    float x[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4* p = reinterpret_cast<const float4*>(part + s * split_stride + r * dp + c);
+        const float4 u = p[0], v = p[1];
+        x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w, x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
+    }
+    const long long to = keys && g.index ? g.index[(long long)b * a.len_k + row] : row;
+    T* dst = static_cast<T*>(t.data) + b * t.batch_stride + h * t.head_stride + to * t.len_stride + c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (c + k < a.d) dst[k] = from_float<T>(x[k]);
+}
+
+// 0 into the gradients of keys that take no part, a warp per key and head.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_zero(const AttnArgs a) {
+    pdl_entry();
+    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 32;
+    const int key = (int)(at % a.len_k);
+    const long long bh = at / a.len_k;
+    const int b = (int)(bh / a.kv_heads), h = (int)(bh % a.kv_heads);
+    if (b >= a.batch || key_valid(a, b, key, key_count(a, b))) return;
+    T* dk = static_cast<T*>(a.dk.data) + b * a.dk.batch_stride + h * a.dk.head_stride + key * a.dk.len_stride;
+    T* dv = static_cast<T*>(a.dv.data) + b * a.dv.batch_stride + h * a.dv.head_stride + key * a.dv.len_stride;
+    for (int c = threadIdx.x & 31; c < a.d; c += 32) dk[c] = dv[c] = from_float<T>(0.f);
+}
+
+namespace {
+
+template <class T, int DP, bool KEYS>
+cudaError_t run(BwdArgs g, const TcTensor (&x)[4], cudaStream_t st) {
+    using S = BwdShape<DP, KEYS>;
+    auto* kernel = k_attn_bwd<T, DP, KEYS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e) return e;
+    const int len = KEYS ? g.t.a.len_k : g.t.a.len_q;
+    g.t.tiles = (len + S::kRows * kTileRows - 1) / (S::kRows * kTileRows);
+    const long long blocks = (long long)g.t.tiles * g.t.splits * (KEYS ? g.t.a.kv_heads : g.t.a.heads) * g.t.a.batch;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(384), S::kSmem, st, g, x[0], x[1], x[2], x[3]);
+}
+
+template <class T>
+cudaError_t typed(const BwdArgs& g, bool keys, int dp, const TcTensor (&x)[4], cudaStream_t st) {
+    if (keys) return dp == 64 ? run<T, 64, true>(g, x, st) : run<T, 128, true>(g, x, st);
+    return dp == 64 ? run<T, 64, false>(g, x, st) : run<T, 128, false>(g, x, st);
+}
+
+template <class F>
+cudaError_t by_type(int dtype, F&& f) {
+    return dtype == GS_DTYPE_F32 ? f(float()) : dtype == GS_DTYPE_F16 ? f(__half()) : f(__nv_bfloat16());
+}
+
+unsigned blocks_of(long long threads) { return (unsigned)((threads + 255) / 256); }
+
+}  // namespace
+
+int attn_bwd_rows(bool keys, int dp) { return (keys && dp == 128 ? 1 : 2) * kTileRows; }
+int attn_bwd_walk() { return kBN; }
+
+cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st) {
+    count_launches(1);
+    return by_type(a.dtype, [&](auto e) {
+        return launch_pdl(k_attn_zero<decltype(e)>, dim3(blocks_of((long long)a.batch * a.kv_heads * a.len_k * 32)), dim3(256), 0, st, a);
+    });
+}
+
+cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor& dout, const TcTensor& k, const TcTensor& v,
+                               const TcTensor& q64, const TcTensor& dout64, const TcTensor& k64, const TcTensor& v64,
+                               cudaStream_t st) {
+    const AttnArgs& a = w.a;
+    const bool half = a.dtype == GS_DTYPE_F16;
+    const float boost = half ? 15.f : 0.f;
+    cudaError_t e;
+    if (half) {
+        if ((e = cudaMemsetAsync(w.norms, 0, (size_t)a.batch * a.kv_heads * 2 * sizeof(unsigned), st))) return e;
+        for (int where = 0; where < 2; ++where) {
+            const long long pad = where ? w.rows_k : w.qpad;
+            count_launches(1);
+            if ((e = launch_pdl(k_attn_norms<__half>, dim3(blocks_of((long long)a.batch * (where ? a.kv_heads : a.heads) * pad * 8)), dim3(256),
+                                0, st, a, pad, where, w.norms)))
+                return e;
+        }
+    }
+    count_launches(1);
+    e = by_type(a.dtype, [&](auto t) {
+        return launch_pdl(k_attn_stats<decltype(t)>, dim3(blocks_of((long long)a.batch * a.heads * w.qpad * 8)), dim3(256), 0, st, a,
+                          w.qpad, boost, a.scale, (const unsigned*)(half ? w.norms : nullptr), w.factor, w.nlse, w.ndelta);
+    });
+    if (e) return e;
+    for (int keys = 0; keys < 2; ++keys) {
+        const int splits = keys ? w.splits_k : w.splits_q, heads = keys ? a.kv_heads : a.heads;
+        const long long rows = keys ? w.rows_k : a.len_q, share = (long long)a.batch * heads * rows * w.dp;
+        const BwdArgs g{{a, w.count, splits > 1 ? w.part : nullptr, nullptr, 0, splits}, w.nlse, w.ndelta, w.qpad, a.scale,
+                        1.f, half ? 1.f / 32768.f : 1.f, half ? w.factor : nullptr, w.index, w.rows_k};
+        const TcTensor* x[2][4] = {{&q, &dout, &k64, &v64}, {&k, &v, &q64, &dout64}};
+        const TcTensor in[4] = {*x[keys][0], *x[keys][1], *x[keys][2], *x[keys][3]};
+        if ((e = half ? typed<__half>(g, keys, w.dp, in, st) : typed<__nv_bfloat16>(g, keys, w.dp, in, st))) return e;
+        if (splits == 1) continue;
+        for (int i = 0; i < 1 + keys; ++i) {
+            count_launches(1);
+            e = by_type(a.dtype, [&](auto t) {
+                return launch_pdl(k_attn_sum<decltype(t)>, dim3(blocks_of((long long)a.batch * heads * rows * (w.dp / 8))), dim3(256), 0, st,
+                                  g, !keys ? a.dq : i == 0 ? a.dk : a.dv, heads, keys, (const float*)w.part + i * share,
+                                  share * (1 + keys), splits, w.dp, rows);
+            });
+            if (e) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace gs

@@ -65,4 +65,25 @@ cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const floa
 cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTensor& k, const TcTensor& v, int planes, int dp,
                                int nq, cudaStream_t st);
 
+
+// Rows per block of the backward kernel that sums dk and dv (keys) or dq, and per tile that it walks.
+int attn_bwd_rows(bool keys, int dp);
+int attn_bwd_walk();
+struct TcBwd {
+    AttnArgs a;
+    const int *count, *index;    // of the key mask, or NULL
+    float *nlse, *ndelta;        // [batch x heads][qpad], written first
+    unsigned* norms;             // float16: [batch x kv_heads][2], as is factor
+    float2* factor;
+    float* part;                 // shares of dq and then of dk and dv, where splits > 1
+    long long qpad, rows_k;
+    int dp, splits_q, splits_k;  // of the walk for dq, and for dk and dv
+};
+// dq, then dk and dv of the keys that take part. The tensors as row tiles, then as walked tiles.
+cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor& dout, const TcTensor& k, const TcTensor& v,
+                               const TcTensor& q64, const TcTensor& dout64, const TcTensor& k64, const TcTensor& v64,
+                               cudaStream_t st);
+// dk = dv = 0 at keys that take no part.
+cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st);
+
 }  // namespace gs
