@@ -104,6 +104,8 @@ _lib = None
 def load():
     """Loads libgs_gb300.so (built by `build()`); raises if it is missing."""
     global _lib
+    if _lib is not None:  # set once, after everything below
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

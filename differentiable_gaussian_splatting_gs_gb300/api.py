@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import functools
 
 import torch
 
@@ -420,52 +421,67 @@ def gs_preprocess2d_bwd(params: dict, cam, opt: gs_options, proj: Proj, grad2d, 
 
 DTYPES = {torch.float32: _abi.GS_DTYPE_F32, torch.float16: _abi.GS_DTYPE_F16, torch.bfloat16: _abi.GS_DTYPE_BF16}
 
+# The decoder's operators are called many times a step on small tensors, where the host's work counts: their bindings
+# ask torch for as little as they can (a torch.cuda.device block or a Stream object costs as much as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _dtype(t, where: str) -> int:
-    if not t.is_cuda or t.dtype not in DTYPES:
+    code = DTYPES.get(t.dtype)
+    if code is None or not t.is_cuda:
         raise ValueError(f"{where}: tensors must be float32, float16 or bfloat16 CUDA tensors")
-    return DTYPES[t.dtype]
+    return code
 
 
-def _on(t, stream) -> int:
-    """The stream to enqueue on: `stream`, or the current stream of t's device."""
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else _stream(stream)
+def _call(like, stream, function, *args) -> int:
+    """function(*args, stream) on like's device: `stream`, or that device's current stream."""
+    index = like.get_device()
+    if torch.cuda.current_device() == index:
+        return function(*args, _raw_stream(index) if stream is None else _stream(stream))
+    with torch.cuda.device(index):
+        return function(*args, _raw_stream(index) if stream is None else _stream(stream))
 
 
 def _alloc(shape, like, stream, dtype=None):
     """A new tensor beside `like` that belongs to the stream it will be used on."""
-    new = dict(dtype=dtype or like.dtype, device=like.device)
     if stream is None:
-        return torch.empty(shape, **new)
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, **new)
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _rows(t, like, where: str):
     """(rows, row stride) of a tensor of like's shape, dtype and device whose last dimension is contiguous and whose
     other dimensions have one common stride."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{where}: a tensor of shape {tuple(like.shape)}, {like.dtype}, {like.device} is needed")
-    if t.dim() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape = t.shape
+    if shape and t.is_contiguous():
+        cols = shape[-1]
+        return t.numel() // cols if cols else 0, cols
+    if not shape or (shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{where}: the last dimension must be contiguous")
-    if t.numel() == 0:
-        return t.numel() // max(t.shape[-1], 1), t.shape[-1]
-    dims = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    dims = [(n, st) for n, st in zip(shape[:-1], t.stride()[:-1]) if n > 1]
     if not dims:
-        return 1, t.shape[-1]
+        return 1, shape[-1]
     for (_, outer), (n, inner) in zip(dims, dims[1:]):
         if outer != n * inner:
             raise ValueError(f"{where}: the rows must have one common stride")
-    return t.numel() // t.shape[-1], dims[-1][1]
+    return t.numel() // shape[-1], dims[-1][1]
 
 
 def _vector(t, like, where: str):
-    if t is not None and (t.shape != like.shape[-1:] or not t.is_contiguous() or t.device != like.device or
-                          t.dtype not in (like.dtype, torch.float32)):
+    if t is not None and (t.dim() != 1 or t.shape[0] != like.shape[-1] or not t.is_contiguous() or t.device != like.device or
+                          (t.dtype is not like.dtype and t.dtype is not torch.float32)):
         raise ValueError(f"{where}: weight and bias must be contiguous [{like.shape[-1]}] tensors of x's dtype or float32")
-    return t
+
+
+def _floats(t, shape, like, where: str):
+    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{where}: a contiguous float32 tensor of shape {tuple(shape)} on {like.device} is needed")
 
 
 def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
@@ -474,26 +490,27 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, st
     where = "gs_layer_norm_fwd"
     dtype = _dtype(x, where)
     rows, xs = _rows(x, x, where)
-    _vector(weight, x, where), _vector(bias, x, where)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    _vector(weight, x, where)
+    _vector(bias, x, where)
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise ValueError(f"{where}: weight and bias must have one dtype")
     given = weight if weight is not None else bias
     if out is None:
-        out = (_alloc(x.shape, x, stream), _alloc((rows,), x, stream, torch.float32),
-               _alloc((rows,), x, stream, torch.float32))
-    y, mean, rstd = out
-    for t in (mean, rstd):
-        _floats(t, (rows,), x, where)
-    with torch.cuda.device(x.device):
-        check(_abi.load().gs_layer_norm_fwd(_ptr(x), xs, rows, x.shape[-1], dtype, _ptr(weight), _ptr(bias),
-                                            dtype if given is None else DTYPES[given.dtype], float(eps), _ptr(y),
-                                            _rows(y, x, where)[1], _ptr(mean), _ptr(rstd), _on(x, stream)), where)
+        y, ys = _alloc(x.shape, x, stream), x.shape[-1]
+        mean, rstd = _alloc((rows,), x, stream, torch.float32), _alloc((rows,), x, stream, torch.float32)
+    else:
+        y, mean, rstd = out
+        ys = _rows(y, x, where)[1]
+        _floats(mean, (rows,), x, where)
+        _floats(rstd, (rows,), x, where)
+    check(_call(x, stream, _abi.load().gs_layer_norm_fwd, _ptr(x), xs, rows, x.shape[-1], dtype, _ptr(weight), _ptr(bias),
+                dtype if given is None else DTYPES[given.dtype], eps, _ptr(y), ys, _ptr(mean), _ptr(rstd)), where)
     return y, mean, rstd
 
 
-def _floats(t, shape, like, where: str):
-    if tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{where}: a contiguous float32 tensor of shape {tuple(shape)} on {like.device} is needed")
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_abi.load().gs_layer_norm_workspace_bytes(rows, cols))
 
 
 def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, stream=None):
@@ -502,35 +519,40 @@ def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, 
     where = "gs_layer_norm_bwd"
     dtype = _dtype(x, where)
     rows, xs = _rows(x, x, where)
+    cols = x.shape[-1]
     _vector(weight, x, where)
-    _floats(mean, (rows,), x, where), _floats(rstd, (rows,), x, where)
+    _floats(mean, (rows,), x, where)
+    _floats(rstd, (rows,), x, where)
     if out is None:
-        out = (_alloc(x.shape, x, stream),) + ((None, None) if weight is None else
-                                              (_alloc(weight.shape, weight, stream), _alloc(weight.shape, weight, stream)))
-    dx, dweight, dbias = out
-    _vector(dweight, x, where), _vector(dbias, x, where)
-    kinds = {t.dtype for t in (weight, dweight, dbias) if t is not None}
-    if len(kinds) > 1:
-        raise ValueError(f"{where}: weight, dweight and dbias must have one dtype")
-    lib = _abi.load()
-    need = int(lib.gs_layer_norm_workspace_bytes(rows, x.shape[-1])) if dweight is not None or dbias is not None else 0
+        dx, dxs = _alloc(x.shape, x, stream), cols
+        dweight, dbias = (None, None) if weight is None else (_alloc((cols,), weight, stream), _alloc((cols,), weight, stream))
+        kind = weight
+    else:
+        dx, dweight, dbias = out
+        dxs = _rows(dx, x, where)[1]
+        _vector(dweight, x, where)
+        _vector(dbias, x, where)
+        kinds = [t for t in (weight, dweight, dbias) if t is not None]
+        kind = kinds[0] if kinds else None
+        if any(t.dtype is not kind.dtype for t in kinds):
+            raise ValueError(f"{where}: weight, dweight and dbias must have one dtype")
+    need = _norm_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = _alloc((need,), x, stream, torch.uint8)
-    with torch.cuda.device(x.device):
-        check(lib.gs_layer_norm_bwd(_ptr(dy), _rows(dy, x, where)[1], _ptr(x), xs, rows, x.shape[-1], dtype, _ptr(mean),
-                                    _ptr(rstd), _ptr(weight), DTYPES[kinds.pop()] if kinds else dtype, _ptr(dx),
-                                    _rows(dx, x, where)[1], _ptr(dweight), _ptr(dbias), _ptr(workspace) if need else None,
-                                    need, _on(x, stream)), where)
+    check(_call(x, stream, _abi.load().gs_layer_norm_bwd, _ptr(dy), _rows(dy, x, where)[1], _ptr(x), xs, rows, cols, dtype,
+                _ptr(mean), _ptr(rstd), _ptr(weight), dtype if kind is None else DTYPES[kind.dtype], _ptr(dx), dxs,
+                _ptr(dweight), _ptr(dbias), _ptr(workspace) if need else None, need), where)
     return dx, dweight, dbias
 
 
 def _heads(t, shape, like, where: str) -> _abi.gs_heads:
-    if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.shape != shape or t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {like.dtype}, {like.device} is needed, "
                          f"got {tuple(t.shape)}, {t.dtype}, {t.device}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    b, n, h, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise ValueError(f"{where}: the elements of a head must be contiguous")
-    return _abi.gs_heads(data=_ptr(t), batch_stride=t.stride(0), len_stride=t.stride(1), head_stride=t.stride(2))
+    return _abi.gs_heads(_ptr(t), b, n, h)
 
 
 def _attention(q, k, v, k_len, key_mask, scale, where: str):
@@ -541,7 +563,6 @@ def _attention(q, k, v, k_len, key_mask, scale, where: str):
     lk, hk = k.shape[1:3]
     if h < 1 or hk < 1 or h % hk:
         raise ValueError(f"{where}: {h} query heads must be a multiple of {hk} key heads")
-    kv = (b, lk, hk, d)
     if k_len is not None and (k_len.shape != (b,) or k_len.dtype != torch.int32 or not k_len.is_contiguous() or
                               k_len.device != q.device):
         raise ValueError(f"{where}: k_len must be a contiguous int32 [{b}] tensor on {q.device}")
@@ -550,23 +571,32 @@ def _attention(q, k, v, k_len, key_mask, scale, where: str):
         raise ValueError(f"{where}: key_mask must be a bool or uint8 [{b}, {lk}] tensor on {q.device} with contiguous rows")
     if scale is not None and not scale > 0:
         raise ValueError(f"{where}: scale must be positive")
-    a = _abi.gs_attention(dtype=dtype, batch=b, heads=h, kv_heads=hk, head_dim=d, len_q=lq, len_k=lk,
-                          scale=0.0 if scale is None else float(scale), k_len=_ptr(k_len), key_mask=_ptr(key_mask),
-                          key_mask_stride=key_mask.stride(0) if key_mask is not None else 0)
-    return a, (b, lq, h, d), kv
+    a = _abi.gs_attention(dtype, b, h, hk, d, lq, lk, scale or 0.0, _ptr(k_len), _ptr(key_mask),
+                          0 if key_mask is None else key_mask.stride(0))
+    return a, q.shape, (b, lk, hk, d)
 
 
-def _attention_workspace(a, backward: bool, workspace, like, stream):
-    need = int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), int(backward)))
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace_bytes(device, backward, dtype, b, h, hk, d, lq, lk, k_len, key_mask) -> int:
+    # only whether there is a length or a mask counts, and the current device's number of SMs
+    a = _abi.gs_attention(dtype, b, h, hk, d, lq, lk, 0.0, 16 if k_len else None, 16 if key_mask else None)
+    with torch.cuda.device(device):
+        return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), backward))
+
+
+def _attention_workspace(a, backward: int, workspace, like, stream):
+    need = _attention_workspace_bytes(like.get_device(), backward, a.dtype, a.batch, a.heads, a.kv_heads, a.head_dim, a.len_q,
+                                      a.len_k, a.k_len is not None, a.key_mask is not None)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = _alloc((need,), like, stream, torch.uint8)
-    return (_ptr(workspace), need) if need else (None, 0), workspace
+    return workspace, need
 
 
 def gs_cross_attention_workspace_bytes(q, k, v, k_len=None, key_mask=None, backward: bool = False) -> int:
     """Bytes of workspace that gs_cross_attention_fwd / _bwd of these tensors use."""
     a, _, _ = _attention(q, k, v, k_len, key_mask, None, "gs_cross_attention_workspace_bytes")
-    return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), int(backward)))
+    with torch.cuda.device(q.device):
+        return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), int(backward)))
 
 
 def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | None = None, out=None, workspace=None,
@@ -578,15 +608,17 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     tensor kept by the caller (allocated when None or too small)."""
     where = "gs_cross_attention_fwd"
     a, qs, kvs = _attention(q, k, v, k_len, key_mask, scale, where)
+    hq, hk, hv = _heads(q, qs, q, where), _heads(k, kvs, q, where), _heads(v, kvs, q, where)
+    stats = (qs[0], qs[2], qs[1])
     if out is None:
-        out = (_alloc(qs, q, stream), _alloc((qs[0], qs[2], qs[1]), q, stream, torch.float32))
-    o, lse = out
-    _floats(lse, (qs[0], qs[2], qs[1]), q, where)
-    hq, hk, hv, ho = _heads(q, qs, q, where), _heads(k, kvs, q, where), _heads(v, kvs, q, where), _heads(o, qs, q, where)
-    (ws, need), keep = _attention_workspace(a, False, workspace, q, stream)
-    with torch.cuda.device(q.device):
-        check(_abi.load().gs_cross_attention_fwd(C.byref(a), C.byref(hq), C.byref(hk), C.byref(hv), C.byref(ho),
-                                                 _ptr(lse), ws, need, _on(q, stream)), where)
+        o, lse = _alloc(qs, q, stream), _alloc(stats, q, stream, torch.float32)
+    else:
+        o, lse = out
+        _floats(lse, stats, q, where)
+    ho = _heads(o, qs, q, where)
+    workspace, need = _attention_workspace(a, 0, workspace, q, stream)
+    check(_call(q, stream, _abi.load().gs_cross_attention_fwd, C.byref(a), C.byref(hq), C.byref(hk), C.byref(hv), C.byref(ho),
+                _ptr(lse), _ptr(workspace) if need else None, need), where)
     return o, lse
 
 
@@ -595,16 +627,15 @@ def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, s
     """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given."""
     where = "gs_cross_attention_bwd"
     a, qs, kvs = _attention(q, k, v, k_len, key_mask, scale, where)
+    ins = [_heads(dout, qs, q, where), _heads(q, qs, q, where), _heads(k, kvs, q, where), _heads(v, kvs, q, where),
+           _heads(out, qs, q, where)]
+    _floats(lse, (qs[0], qs[2], qs[1]), q, where)
     if grads is None:
         grads = (_alloc(qs, q, stream), _alloc(kvs, q, stream), _alloc(kvs, q, stream))
-    _floats(lse, (qs[0], qs[2], qs[1]), q, where)
-    hs = [_heads(t, qs, q, where) for t in (dout, q)] + [_heads(t, kvs, q, where) for t in (k, v)]
-    hs.append(_heads(out, qs, q, where))
-    gs = [_heads(t, sh, q, where) for t, sh in zip(grads, (qs, kvs, kvs))]
-    (ws, need), keep = _attention_workspace(a, True, workspace, q, stream)
-    with torch.cuda.device(q.device):
-        check(_abi.load().gs_cross_attention_bwd(C.byref(a), *(C.byref(h) for h in hs), _ptr(lse),
-                                                 *(C.byref(g) for g in gs), ws, need, _on(q, stream)), where)
+    outs = [_heads(t, sh, q, where) for t, sh in zip(grads, (qs, kvs, kvs))]
+    workspace, need = _attention_workspace(a, 1, workspace, q, stream)
+    check(_call(q, stream, _abi.load().gs_cross_attention_bwd, C.byref(a), *map(C.byref, ins), _ptr(lse), *map(C.byref, outs),
+                _ptr(workspace) if need else None, need), where)
     return tuple(grads)
 
 

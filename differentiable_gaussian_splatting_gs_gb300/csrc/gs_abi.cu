@@ -898,8 +898,11 @@ int gs_layer_norm_fwd(const void* x, int64_t x_stride, int64_t rows, int64_t col
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GS_ERR_ARG, "%s: eps must be finite and not negative", me);
     if (rows > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
         return fail(GS_ERR_ARG, "%s: mean or rstd is NULL or misaligned", me);
+    if (rows == 0) return GS_OK;
+    unsigned* err = error_word(&s);
+    if (!err) return s;
     cudaError_t e = launch_norm_fwd(dtype, x, x_stride, rows, (int)cols, weight, bias, weight_dtype, eps, y, y_stride, mean, rstd,
-                                    as_stream(stream));
+                                    err, as_stream(stream));
     return e ? cuda_fail(e, me) : GS_OK;
 }
 
@@ -924,8 +927,10 @@ int gs_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t 
     const size_t need = dweight || dbias ? norm_bwd_workspace_bytes(rows, (int)cols) : 0;
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
         return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
+    unsigned* err = error_word(&s);
+    if (!err) return s;
     cudaError_t e = launch_norm_bwd(dtype, dy, dy_stride, x, x_stride, rows, (int)cols, mean, rstd, weight, weight_dtype, dx,
-                                    dx_stride, dweight, dbias, static_cast<float*>(workspace), as_stream(stream));
+                                    dx_stride, dweight, dbias, static_cast<float*>(workspace), err, as_stream(stream));
     return e ? cuda_fail(e, me) : GS_OK;
 }
 

@@ -154,12 +154,12 @@ cudaError_t launch_preprocess2d_bwd(int deg, int n, const gs_params& p, const Ke
 // ---- the Gaussian decoder's operators ----------------------------------------------------------
 cudaError_t launch_norm_fwd(int dtype, const void* x, long long x_stride, long long rows, int cols, const void* weight,
                             const void* bias, int wdtype, float eps, void* y, long long y_stride, float* mean,
-                            float* rstd, cudaStream_t st);
+                            float* rstd, unsigned* err, cudaStream_t st);
 size_t norm_bwd_workspace_bytes(long long rows, int cols);
 cudaError_t launch_norm_bwd(int dtype, const void* dy, long long dy_stride, const void* x, long long x_stride,
                             long long rows, int cols, const float* mean, const float* rstd, const void* weight,
                             int wdtype, void* dx, long long dx_stride, void* dweight, void* dbias, float* workspace,
-                            cudaStream_t st);
+                            unsigned* err, cudaStream_t st);
 
 // A [batch][length][heads][head_dim] tensor of a cross attention (strides in elements).
 struct AttnTensor {

@@ -1,10 +1,10 @@
 // Layer norm, forward: y = (x - mean) rstd w + b over each row, with rstd = 1 / sqrt(var + eps).
 //
 // The work is bound by memory: x is read once and y written once. A row stays in the registers of
-// the threads it is laid over (layer_norm.cuh), where the mean is formed first and the variance then
-// from the centred values: sum(x^2) - sum(x)^2 / C in one pass would lose the variance of channels
-// whose mean is large. The grid is persistent, so the weights are read into registers once, and each
-// thread loads its next row before it reduces the present one.
+// the threads it is laid over (layer_norm.cuh), in its own type, where the mean is formed first and the variance
+// then from the centred values: sum(x^2) - sum(x)^2 / C in one pass would lose the variance of channels
+// whose mean is large. The grid is persistent, with the weights in shared memory, and each thread loads its next
+// row before it reduces the present one; rows of more than a vector per thread come through shared memory (NormRing).
 #include "layer_norm.cuh"
 
 namespace gs {
@@ -16,72 +16,107 @@ struct NormFwdArgs {
     long long rows, x_stride, y_stride;
     int cols, wdtype;
     float eps;
+    unsigned* err;
 };
 
 template <class T, int VEC, int NV, int LPR>
 __global__ void __launch_bounds__(kNormBlock) k_norm_fwd(const NormFwdArgs a) {
     pdl_entry();
+    extern __shared__ __align__(16) float weights[];  // w, then b
     __shared__ float buf[2 * kNormBlock / 32];
     int phase = 0;
     constexpr int kRows = kNormBlock / LPR;  // rows of a block at a time
     const int l = threadIdx.x % LPR, nvec = a.cols / VEC;
     const float inv = 1.f / (float)a.cols;
-    float w[NV * VEC], b[NV * VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (l + i * LPR) * VEC + j;
-            w[i * VEC + j] = a.weight && c < a.cols ? load_elem(a.weight, c, a.wdtype) : 1.f;
-            b[i * VEC + j] = a.bias && c < a.cols ? load_elem(a.bias, c, a.wdtype) : 0.f;
-        }
+    const bool affine = a.weight || a.bias;
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.y);
     const long long step = (long long)gridDim.x * kRows;
     long long base = (long long)blockIdx.x * kRows;  // uniform over the block: all lanes take part in the sums
-    Pack<T, VEC> raw[NV];
-    load_row<T, VEC, NV, LPR>(raw, x + (base + threadIdx.x / LPR) * a.x_stride, l, nvec, base + threadIdx.x / LPR < a.rows);
+    constexpr bool kRing = norm_ring<VEC, NV, LPR>;
+    Pack<T, VEC> raw[NV], next[NV];
+    constexpr int kStages = norm_stages<NV, LPR>;
+    __shared__ uint64_t bars[kRing ? kRows * kStages : 1];
+    NormRing<1, kRing ? LPR : 32, kStages> ring;
+    if constexpr (kRing) {
+        init_ring_bars<kRows * kStages>(bars);
+        ring.src[0] = reinterpret_cast<const char*>(x);
+        ring.stride[0] = a.x_stride * (long long)sizeof(T);
+        ring.start(reinterpret_cast<unsigned char*>(weights + (affine ? 2 * a.cols : 0)), bars, a.cols, sizeof(T),
+                   base + threadIdx.x / LPR, a.rows, step, kNormSpin, a.err);
+    } else {
+        load_row<T, VEC, NV, LPR>(next, x + (base + threadIdx.x / LPR) * a.x_stride, l, nvec, base + threadIdx.x / LPR < a.rows);
+    }
+    if (affine) {
+        stage_weights<VEC>(weights, a.weight, a.wdtype, a.cols, 1.f);
+        stage_weights<VEC>(weights + a.cols, a.bias, a.wdtype, a.cols, 0.f);
+        __syncthreads();
+    }
     for (; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / LPR;
         const bool live = row < a.rows;
-        float v[NV * VEC];
+        if constexpr (kRing) {
+            if (live) {
+                ring.wait();
+                load_row<T, VEC, NV, LPR>(raw, reinterpret_cast<const T*>(ring.at(0)), l, nvec, true);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) raw[i] = next[i];
+            load_row<T, VEC, NV, LPR>(next, x + (row + step) * a.x_stride, l, nvec, row + step < a.rows);
+        }
+        float f[VEC], t[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
+            if (live && l + i * LPR < nvec) {
+                unpack<T, VEC>(raw[i], f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                v[i * VEC + j] = live && l + i * LPR < nvec ? to_float(raw[i].v[j]) : 0.f;
-        load_row<T, VEC, NV, LPR>(raw, x + (row + step) * a.x_stride, l, nvec, row + step < a.rows);
-        float s[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < NV * VEC; ++i) s[0] += v[i];
+                for (int k = 0; k < VEC; ++k) t[k & 1] += f[k];
+            }
+        float s[1] = {t[0] + t[1]};
         row_sum<LPR>(s, buf, phase);
+        if (kRing && live) {
+            __syncwarp();
+            ring.next();
+        }
         const float mean = s[0] * inv;
-        s[0] = 0.f;
+        t[0] = t[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (l + i * LPR < nvec)
+            if (live && l + i * LPR < nvec) {
+                unpack<T, VEC>(raw[i], f);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    v[i * VEC + j] -= mean;
-                    s[0] = fmaf(v[i * VEC + j], v[i * VEC + j], s[0]);
+                for (int k = 0; k < VEC; ++k) {
+                    const float d = f[k] - mean;
+                    t[k & 1] = fmaf(d, d, t[k & 1]);
                 }
+            }
+        s[0] = t[0] + t[1];
         row_sum<LPR>(s, buf, phase);
         const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
         if (!live) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (l + i * LPR < nvec) {
-                Pack<T, VEC> o;
+                float w[VEC], b[VEC];
+                if (affine) {
+                    load_floats<VEC>(w, weights, l + i * LPR, nvec);
+                    load_floats<VEC>(b, weights + a.cols, l + i * LPR, nvec);
+                }
+                unpack<T, VEC>(raw[i], f);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    o.v[j] = from_float<T>(fmaf(v[i * VEC + j] * rstd, w[i * VEC + j], b[i * VEC + j]));
-                *reinterpret_cast<Pack<T, VEC>*>(y + row * a.y_stride + (size_t)(l + i * LPR) * VEC) = o;
+                for (int k = 0; k < VEC; ++k) {
+                    f[k] = (f[k] - mean) * rstd;
+                    if (affine) f[k] = fmaf(f[k], w[k], b[k]);
+                }
+                *reinterpret_cast<Pack<T, VEC>*>(y + row * a.y_stride + (size_t)(l + i * LPR) * VEC) = repack<T, VEC>(f);
             }
         if (l == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
         }
     }
+    if constexpr (kRing) ring.finish();
 }
 
 // Rows of more than kNormMaxCols elements: a block per row, which reads it again for each pass (the
@@ -121,14 +156,26 @@ namespace {
 
 template <class T, int VEC>
 cudaError_t run(const NormFwdArgs& a, cudaStream_t st) {
-    return norm_dispatch<VEC>(a.cols / VEC, [&](auto shape) {
+    // 32 elements a thread: each sum is a shuffle reduction and, over several warps, a barrier
+    return norm_dispatch<VEC, VEC == 8 ? 4 : 8>(a.cols / VEC, [&](auto shape) {
         using S = decltype(shape);
         static std::atomic<int> cache[256] = {};
         auto* kernel = k_norm_fwd<T, VEC, S::NV, S::LPR>;
-        const int most = resident_blocks(kernel, kNormBlock, 0, cache);
+        constexpr bool kRing = norm_ring<VEC, S::NV, S::LPR>;
+        constexpr int kCols = S::NV * S::LPR * VEC;
+        auto smem_of = [&](int cols, bool affine) {
+            return (affine ? 2 * cols * sizeof(float) : 0) + (kRing ? NormRing<1, kRing ? S::LPR : 32, norm_stages<S::NV, S::LPR>>::smem(cols, sizeof(T)) : 0);
+        };
+        const int kMost = (int)smem_of(kCols, true);
+        if (kMost > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+            if (e) return e;
+        }
+        const int most = resident_blocks(kernel, kNormBlock, kMost, cache);
+        const size_t smem = smem_of(a.cols, a.weight || a.bias);
         const long long want = (a.rows + kNormBlock / S::LPR - 1) / (kNormBlock / S::LPR);
         count_launches(1);
-        return launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kNormBlock), 0, st, a);
+        return launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kNormBlock), smem, st, a);
     });
 }
 
@@ -151,9 +198,9 @@ cudaError_t run_typed(const NormFwdArgs& a, cudaStream_t st) {
 
 cudaError_t launch_norm_fwd(int dtype, const void* x, long long x_stride, long long rows, int cols, const void* weight,
                             const void* bias, int wdtype, float eps, void* y, long long y_stride, float* mean,
-                            float* rstd, cudaStream_t st) {
+                            float* rstd, unsigned* err, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    const NormFwdArgs a{x, weight, bias, y, mean, rstd, rows, x_stride, y_stride, cols, wdtype, eps};
+    const NormFwdArgs a{x, weight, bias, y, mean, rstd, rows, x_stride, y_stride, cols, wdtype, eps, err};
     if (dtype == GS_DTYPE_F32) return run_typed<float>(a, st);
     if (dtype == GS_DTYPE_F16) return run_typed<__half>(a, st);
     return run_typed<__nv_bfloat16>(a, st);

@@ -8,7 +8,7 @@
 
 namespace gs {
 
-// A row belongs to LPR threads: a part of a warp (8 or 16 lanes), a warp, or a block of kNormBlock
+// A row belongs to LPR threads: a part of a warp (8 or 16 lanes), or 1, 2, 4 or 8 warps of a block of kNormBlock
 // threads. Thread l holds the vectors l, l + LPR, ..., l + (NV - 1) LPR of the row, VEC elements each,
 // in registers, so that every pass over the row after the first reads no memory.
 constexpr int kNormBlock = 256;   // threads per block of the row kernels
@@ -26,12 +26,13 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* buf, int& phase) {
         for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
     if (LPR > 32) {
         constexpr int kWarps = LPR / 32;
-        float* b = buf + phase * (N * kWarps);
+        const int group = threadIdx.x / LPR;
+        float* b = buf + (group * 2 + phase) * (N * kWarps);
         phase ^= 1;
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) b[i * kWarps + (threadIdx.x >> 5)] = s[i];
-        __syncthreads();
+            for (int i = 0; i < N; ++i) b[i * kWarps + (threadIdx.x % LPR >> 5)] = s[i];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(LPR) : "memory");
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float t = 0.f;
@@ -49,32 +50,157 @@ __device__ __forceinline__ void load_row(Pack<T, VEC> (&raw)[NV], const T* row, 
         if (live && l + i * LPR < nvec) raw[i] = *reinterpret_cast<const Pack<T, VEC>*>(row + (size_t)(l + i * LPR) * VEC);
 }
 
-// Calls f with the layout's constants for rows of `nvec` vectors of VEC elements of type T, at most
-// kNormMaxElems elements per thread. Parts of a warp for rows of up to 8 or 16 vectors, a warp as long
-// as its 32 elements per lane reach (a shuffle reduction needs no barrier), then a block.
+// The weights as floats in shared memory, `missing` where there are none. (In registers they would take as many
+// as the row itself does in the forward, and keep the warps from being many enough to cover the memory's latency.)
+// Element j of vector v lies where consecutive threads, which hold consecutive vectors, meet no bank twice: fours of
+// a vector's elements as planes.
+template <int VEC>
+__device__ __forceinline__ int plane_at(int c, int nvec) {
+    constexpr int P = VEC % 4 == 0 ? 4 : 1;
+    return ((c % VEC) / P * nvec + c / VEC) * P + c % P;
+}
+
+template <int VEC>
+__device__ __forceinline__ void stage_weights(float* dst, const void* w, int dtype, int cols, float missing) {
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) dst[plane_at<VEC>(c, cols / VEC)] = w ? load_elem(w, c, dtype) : missing;
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void unpack(const Pack<T, VEC>& p, float (&f)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] = to_float(p.v[k]);
+}
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> repack(const float (&f)[VEC]) {
+    Pack<T, VEC> p;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) p.v[k] = from_float<T>(f[k]);
+    return p;
+}
+
+// Vector v of an array of floats in shared memory.
+template <int VEC>
+__device__ __forceinline__ void load_floats(float (&f)[VEC], const float* p, int v, int nvec) {
+    if constexpr (VEC == 1) {
+        f[0] = p[v];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+            const float4 q = reinterpret_cast<const float4*>(p)[j / 4 * nvec + v];
+            f[j] = q.x, f[j + 1] = q.y, f[j + 2] = q.z, f[j + 3] = q.w;
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_floats(const float (&f)[VEC], float* p, int v, int nvec) {
+    if constexpr (VEC == 1) {
+        p[v] = f[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) reinterpret_cast<float4*>(p)[j / 4 * nvec + v] = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    }
+}
+
+// Rows on their way: of each of ARRAYS arrays the row of the next STAGES turns, copied into shared memory with bulk
+// copies by the first thread of the row's threads (a warp or the block). So many bytes are in flight
+// whatever registers the row takes, which decides how many warps there are.
+template <int NV, int LPR>
+constexpr int norm_stages = LPR > 128 && NV >= 8 ? 2 : 3;  // two of the longest rows' 64 KB beside their weights
+template <int ARRAYS, int LPR, int kNormStages>
+struct NormRing {
+    static_assert(LPR >= 32);
+    unsigned char* data;  // [STAGES][ARRAYS][bytes]
+    uint64_t* full;
+    const char* src[ARRAYS];
+    long long stride[ARRAYS], row, rows, step;  // row: the next to ask for
+    unsigned bytes, limit, *err;
+    int turn = 0, asked = 0;
+    bool ok = true;
+
+    static __host__ __device__ size_t smem(int cols, size_t elem) { return (size_t)(kNormBlock / LPR) * kNormStages * ARRAYS * cols * elem; }
+
+    __device__ __forceinline__ void ask() {
+        if (row < rows) {
+            if (threadIdx.x % LPR == 0) {
+                const int s = asked % kNormStages;
+                mbar_arrive_expect_tx(full + s, ARRAYS * bytes);
+#pragma unroll
+                for (int a = 0; a < ARRAYS; ++a)
+                    bulk_copy_g2s(data + (size_t)(s * ARRAYS + a) * bytes, src[a] + row * stride[a], bytes, full + s);
+            }
+            ++asked;
+        }
+        row += step;
+    }
+    // After the block's barriers were initialised (bars: kNormStages of them for each row of the block).
+    __device__ __forceinline__ void start(unsigned char* smem, uint64_t* bars, int cols, int elem, long long first, long long rows_, long long step_,
+                                          unsigned limit_, unsigned* err_) {
+        const int g = threadIdx.x / LPR;
+        bytes = (unsigned)(cols * elem);
+        data = smem + (size_t)g * kNormStages * ARRAYS * bytes;
+        full = bars + g * kNormStages;
+        row = first, rows = rows_, step = step_, limit = limit_, err = err_;
+        for (int s = 0; s < kNormStages; ++s) ask();
+    }
+    // The present turn's row of array a; a wait that gave up leaves garbage and goes on, since others wait at barriers.
+    __device__ __forceinline__ void wait() {
+        if (ok) ok = mbar_wait_bounded(full + turn % kNormStages, (turn / kNormStages) & 1, limit, err);
+    }
+    __device__ __forceinline__ const unsigned char* at(int a) const { return data + (size_t)((turn % kNormStages) * ARRAYS + a) * bytes; }
+    // Once all threads of the row have read it.
+    __device__ __forceinline__ void next() {
+        ++turn;
+        ask();
+    }
+    // Every copy has landed before the block ends.
+    __device__ __forceinline__ void finish() {
+        if (!ok && threadIdx.x % LPR == 0)
+            for (int t = asked > kNormStages ? asked - kNormStages : 0; t < asked; ++t)
+                mbar_wait_bounded(full + t % kNormStages, (t / kNormStages) & 1, kDrainLimit, err);
+    }
+};
+
+constexpr unsigned kNormSpin = 1u << 18;  // polls before a wait gives up
+// Rows that come through the ring: 16-byte vectors, several per thread of a warp, or a block's.
+template <int VEC, int NV, int LPR>
+constexpr bool norm_ring = VEC > 1 && (LPR > 32 || (LPR == 32 && NV > 1));
+
+template <int BARS>
+__device__ __forceinline__ void init_ring_bars(uint64_t* bars) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < BARS; ++i) mbar_init(bars + i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+}
+
+// Calls f with the layout's constants for rows of `nvec` vectors of VEC elements of type T: as few threads as hold
+// the row with MOST vectors each (a sum over a warp needs no barrier), or up to kNormMaxElems elements in the
+// longest rows.
 template <int NV_, int LPR_>
 struct NormShape {
     static constexpr int NV = NV_, LPR = LPR_;
 };
 
-template <int VEC, class F>
+template <int VEC, int MOST, class F>
 cudaError_t norm_dispatch(int nvec, F&& f) {
     if constexpr (VEC > 1) {
         if (nvec <= 8) return f(NormShape<1, 8>());
         if (nvec <= 16) return f(NormShape<1, 16>());
         if (nvec <= 32) return f(NormShape<1, 32>());
         if (nvec <= 64) return f(NormShape<2, 32>());
-        if (nvec <= 96) return f(NormShape<3, 32>());
-        if (nvec <= 128) return f(NormShape<4, 32>());
-        if constexpr (VEC == 4) {
+        if constexpr (MOST >= 4) {
+            if (nvec <= 96) return f(NormShape<3, 32>());
+            if (nvec <= 128) return f(NormShape<4, 32>());
+        }
+        if constexpr (MOST >= 8) {
             if (nvec <= 192) return f(NormShape<6, 32>());
             if (nvec <= 256) return f(NormShape<8, 32>());
         }
-        if (nvec <= 256) return f(NormShape<1, 256>());
-        if (nvec <= 512) return f(NormShape<2, 256>());
-        if constexpr (VEC == 8) return f(NormShape<4, 256>());
-        if (nvec <= 1024) return f(NormShape<4, 256>());
-        return f(NormShape<8, 256>());
+        if (nvec <= 64 * MOST) return f(NormShape<MOST, 64>());
+        if (nvec <= 128 * MOST) return f(NormShape<MOST, 128>());
+        if (nvec <= 256 * MOST) return f(NormShape<MOST, 256>());
+        return f(NormShape<kNormMaxElems / VEC, 256>());
     } else {
         if (nvec <= 32) return f(NormShape<1, 32>());
         if (nvec <= 64) return f(NormShape<2, 32>());
@@ -82,9 +208,8 @@ cudaError_t norm_dispatch(int nvec, F&& f) {
         if (nvec <= 256) return f(NormShape<8, 32>());
         if (nvec <= 384) return f(NormShape<12, 32>());
         if (nvec <= 512) return f(NormShape<16, 32>());
-        if (nvec <= 768) return f(NormShape<24, 32>());
-        if (nvec <= 1024) return f(NormShape<32, 32>());
-        if (nvec <= 2048) return f(NormShape<8, 256>());
+        if (nvec <= 1024) return f(NormShape<16, 64>());
+        if (nvec <= 2048) return f(NormShape<16, 128>());
         if (nvec <= 4096) return f(NormShape<16, 256>());
         return f(NormShape<32, 256>());
     }

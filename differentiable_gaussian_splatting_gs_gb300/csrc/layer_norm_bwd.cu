@@ -5,7 +5,8 @@
 // Bound by memory: x and dy are read once, dx is written once. A row's elements stay in registers, and
 // so do the thread's columns of dw and db: the grid is persistent, each thread adds up the rows it
 // meets, the block adds its threads' sums in shared memory and leaves them in the workspace, and a
-// second kernel adds the blocks'. All in a fixed order, so the same call gives the same bits.
+// second kernel adds the blocks'. All in a fixed order, so the same call gives the same bits. The sums leave
+// no registers for loads ahead: rows of more than a vector per thread come through shared memory (NormRing).
 #include "layer_norm.cuh"
 
 namespace gs {
@@ -17,95 +18,132 @@ struct NormBwdArgs {
     float* part;  // [blocks][2][cols]: each block's share of dw and db
     long long rows, dy_stride, x_stride, dx_stride;
     int cols, wdtype;
+    unsigned* err;
 };
 
 template <class T, int VEC, int NV, int LPR>
 __global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
     pdl_entry();
-    extern __shared__ float share[];  // rows per block x 2 x cols: the block's sums (LPR < 256)
+    extern __shared__ __align__(16) float share[];  // w; at the end the block's sums, 2 x cols
     __shared__ float buf[2 * 2 * kNormBlock / 32];
     int phase = 0;
-    constexpr int kRows = kNormBlock / LPR, E = NV * VEC;
+    constexpr int kRows = kNormBlock / LPR;
     const int l = threadIdx.x % LPR, nvec = a.cols / VEC;
     const float inv = 1.f / (float)a.cols;
-    float w[E], dw[E], db[E];
+    float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (l + i * LPR) * VEC + j;
-            w[i * VEC + j] = a.weight && c < a.cols ? load_elem(a.weight, c, a.wdtype) : 1.f;
-            dw[i * VEC + j] = db[i * VEC + j] = 0.f;
-        }
+        for (int k = 0; k < VEC; ++k) dw[i][k] = db[i][k] = 0.f;
+    if (a.weight) {
+        stage_weights<VEC>(share, a.weight, a.wdtype, a.cols, 1.f);
+        __syncthreads();
+    }
     const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.dx);
     const long long step = (long long)gridDim.x * kRows;
+    constexpr bool kRing = norm_ring<VEC, NV, LPR>;
+    constexpr int kStages = norm_stages<NV, LPR>;
+    __shared__ uint64_t bars[kRing ? kRows * kStages : 1];
+    NormRing<2, kRing ? LPR : 32, kStages> ring;
+    if constexpr (kRing) {
+        init_ring_bars<kRows * kStages>(bars);
+        ring.src[0] = reinterpret_cast<const char*>(x);
+        ring.src[1] = reinterpret_cast<const char*>(dy);
+        ring.stride[0] = a.x_stride * (long long)sizeof(T);
+        ring.stride[1] = a.dy_stride * (long long)sizeof(T);
+        ring.start(reinterpret_cast<unsigned char*>(share + 2 * a.cols), bars, a.cols, sizeof(T),
+                   (long long)blockIdx.x * kRows + threadIdx.x / LPR, a.rows, step, kNormSpin, a.err);
+    }
+    const long long first = (long long)blockIdx.x * kRows + threadIdx.x / LPR;
+    float next_m = first < a.rows ? a.mean[first] : 0.f, next_r = first < a.rows ? a.rstd[first] : 0.f;
     for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / LPR;
         const bool live = row < a.rows;
+        const float m = next_m, r = next_r;
+        if (row + step < a.rows) {
+            next_m = a.mean[row + step];
+            next_r = a.rstd[row + step];
+        }
         Pack<T, VEC> rx[NV], rd[NV];
-        load_row<T, VEC, NV, LPR>(rx, x + row * a.x_stride, l, nvec, live);
-        load_row<T, VEC, NV, LPR>(rd, dy + row * a.dy_stride, l, nvec, live);
-        const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
-        float s[2] = {0.f, 0.f};
+        if constexpr (kRing) {
+            if (live) {
+                ring.wait();
+                load_row<T, VEC, NV, LPR>(rx, reinterpret_cast<const T*>(ring.at(0)), l, nvec, true);
+                load_row<T, VEC, NV, LPR>(rd, reinterpret_cast<const T*>(ring.at(1)), l, nvec, true);
+            }
+        } else {
+            load_row<T, VEC, NV, LPR>(rx, x + row * a.x_stride, l, nvec, live);
+            load_row<T, VEC, NV, LPR>(rd, dy + row * a.dy_stride, l, nvec, live);
+        }
+        float x1[VEC], d1[VEC], w[VEC], s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (live && l + i * LPR < nvec)
+            if (live && l + i * LPR < nvec) {
+                if (a.weight) load_floats<VEC>(w, share, l + i * LPR, nvec);
+                unpack<T, VEC>(rx[i], x1);
+                unpack<T, VEC>(rd[i], d1);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const int e = i * VEC + j;
-                    const float d = to_float(rd[i].v[j]), h = (to_float(rx[i].v[j]) - mean) * rstd, g = d * w[e];
-                    dw[e] = fmaf(d, h, dw[e]);
-                    db[e] += d;
-                    s[0] += g;
-                    s[1] = fmaf(g, h, s[1]);
+                for (int k = 0; k < VEC; ++k) {
+                    const float h = (x1[k] - m) * r, g = a.weight ? d1[k] * w[k] : d1[k];
+                    dw[i][k] = fmaf(d1[k], h, dw[i][k]);
+                    db[i][k] += d1[k];
+                    s0 += g;
+                    s1 = fmaf(g, h, s1);
                 }
+            }
+        float s[2] = {s0, s1};
         row_sum<LPR>(s, buf, phase);
         if (!live) continue;
-        const float m0 = s[0] * inv, m1 = s[1] * inv;
+        if constexpr (kRing) {
+            __syncwarp();
+            ring.next();
+        }
+        // rstd (g - mean(g) - h mean(g h))
+        const float c0 = -s[0] * inv * r, c1 = -s[1] * inv * r;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (l + i * LPR < nvec) {
-                Pack<T, VEC> o;
+                if (a.weight) load_floats<VEC>(w, share, l + i * LPR, nvec);
+                unpack<T, VEC>(rx[i], x1);
+                unpack<T, VEC>(rd[i], d1);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float h = (to_float(rx[i].v[j]) - mean) * rstd, g = to_float(rd[i].v[j]) * w[i * VEC + j];
-                    o.v[j] = from_float<T>(rstd * (g - m0 - h * m1));
+                for (int k = 0; k < VEC; ++k) {
+                    const float h = (x1[k] - m) * r, g = a.weight ? d1[k] * w[k] : d1[k];
+                    x1[k] = fmaf(g, r, fmaf(h, c1, c0));
                 }
-                *reinterpret_cast<Pack<T, VEC>*>(dx + row * a.dx_stride + (size_t)(l + i * LPR) * VEC) = o;
+                *reinterpret_cast<Pack<T, VEC>*>(dx + row * a.dx_stride + (size_t)(l + i * LPR) * VEC) = repack<T, VEC>(x1);
             }
     }
+    if constexpr (kRing) ring.finish();
     if (!a.part) return;
     float* part = a.part + (size_t)blockIdx.x * 2 * a.cols;
-    if (LPR == kNormBlock) {
+    // the rows' threads one after the other
+#pragma unroll 1
+    for (int r = 0; r < kRows; ++r) {
+        __syncthreads();
+        if ((int)threadIdx.x / LPR != r) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
+            if (l + i * LPR < nvec) {
+                if (r > 0) {
+                    float u[VEC], v[VEC];
+                    load_floats<VEC>(u, share, l + i * LPR, nvec);
+                    load_floats<VEC>(v, share + a.cols, l + i * LPR, nvec);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int c = (l + i * LPR) * VEC + j;
-                if (c < a.cols) {
-                    part[c] = dw[i * VEC + j];
-                    part[a.cols + c] = db[i * VEC + j];
+                    for (int k = 0; k < VEC; ++k) {
+                        dw[i][k] = u[k] + dw[i][k];
+                        db[i][k] = v[k] + db[i][k];
+                    }
                 }
+                store_floats<VEC>(dw[i], share, l + i * LPR, nvec);
+                store_floats<VEC>(db[i], share + a.cols, l + i * LPR, nvec);
             }
-        return;
     }
-    float* mine = share + (size_t)(threadIdx.x / LPR) * 2 * a.cols;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (l + i * LPR) * VEC + j;
-            if (c < a.cols) {
-                mine[c] = dw[i * VEC + j];
-                mine[a.cols + c] = db[i * VEC + j];
-            }
-        }
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.cols; c += kNormBlock) {
-        float t = 0.f;
-        for (int r = 0; r < kRows; ++r) t += share[(size_t)r * 2 * a.cols + c];
-        part[c] = t;
+    for (int c = threadIdx.x; c < a.cols; c += kNormBlock) {
+        part[c] = share[plane_at<VEC>(c, nvec)];
+        part[a.cols + c] = share[a.cols + plane_at<VEC>(c, nvec)];
     }
 }
 
@@ -155,27 +193,28 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd_long_cols(const NormBwd
     part[a.cols + c] = db;
 }
 
-// dw, db = the sums of the blocks' shares: a warp per 32 columns and slice of the shares, eight slices
-// to a block, in order.
-__global__ void __launch_bounds__(256) k_norm_bwd_sum(const float* part, int blocks, int cols, void* dweight, void* dbias,
-                                                      int wdtype) {
+// dw, db = the sums of the blocks' shares: 32 columns to a block, whose 32 warps take the shares in turn, in order.
+__global__ void __launch_bounds__(1024) k_norm_bwd_sum(const float* part, int blocks, int cols, void* dweight, void* dbias,
+                                                       int wdtype) {
     pdl_entry();
-    __shared__ float share[8][33];
+    __shared__ float share[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;  // c counts dw's columns, then db's
     float t = 0.f;
     if (c < 2 * cols) {
 #pragma unroll 8
-        for (int b = s; b < blocks; b += 8) t += part[(size_t)b * 2 * cols + c];
+        for (int b = s; b < blocks; b += 32) t += part[(size_t)b * 2 * cols + c];
     }
     share[s][threadIdx.x & 31] = t;
     __syncthreads();
-    if (s != 0 || c >= 2 * cols) return;
+    t = share[threadIdx.x & 31][s];  // a warp per column
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += share[i][threadIdx.x & 31];
-    if (c < cols) {
-        if (dweight) store_elem(dweight, c, wdtype, t);
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const int col = blockIdx.x * 32 + s;
+    if ((threadIdx.x & 31) != 0 || col >= 2 * cols) return;
+    if (col < cols) {
+        if (dweight) store_elem(dweight, col, wdtype, t);
     } else if (dbias) {
-        store_elem(dbias, c - cols, wdtype, t);
+        store_elem(dbias, col - cols, wdtype, t);
     }
 }
 
@@ -187,14 +226,19 @@ long long shares(long long rows) { return rows < kMaxShares ? rows : kMaxShares;
 
 template <class T, int VEC>
 cudaError_t run(const NormBwdArgs& a, int* blocks, cudaStream_t st) {
-    return norm_dispatch<VEC>(a.cols / VEC, [&](auto shape) {
+    // 16 elements a thread: with 32, their two sums leave registers for 8 warps an SM, too few to keep the memory
+    // busy (139,072 x 1024 bfloat16: 286 us)
+    return norm_dispatch<VEC, VEC == 8 ? 2 : 4>(a.cols / VEC, [&](auto shape) {
         using S = decltype(shape);
         constexpr int kRows = kNormBlock / S::LPR;
         static std::atomic<int> cache[256] = {};
         auto* kernel = k_norm_bwd<T, VEC, S::NV, S::LPR>;
-        // at most 2 x 8 x 1024 floats (a warp's row) or 2 x 32 x 8 VEC (8 lanes' row)
-        const size_t smem = kRows > 1 ? (size_t)kRows * 2 * a.cols * sizeof(float) : 0;
-        constexpr int kMost = kRows > 1 ? kRows * 2 * S::NV * S::LPR * VEC * (int)sizeof(float) : 0;
+        constexpr bool kRing = norm_ring<VEC, S::NV, S::LPR>;
+        auto smem_of = [&](int cols) {
+            return 2 * cols * sizeof(float) + (kRing ? NormRing<2, kRing ? S::LPR : 32, norm_stages<S::NV, S::LPR>>::smem(cols, sizeof(T)) : 0);
+        };
+        const int kMost = (int)smem_of(S::NV * S::LPR * VEC);
+        const size_t smem = smem_of(a.cols);
         if (kMost > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             if (e) return e;
@@ -234,9 +278,9 @@ size_t norm_bwd_workspace_bytes(long long rows, int cols) { return (size_t)share
 cudaError_t launch_norm_bwd(int dtype, const void* dy, long long dy_stride, const void* x, long long x_stride,
                             long long rows, int cols, const float* mean, const float* rstd, const void* weight,
                             int wdtype, void* dx, long long dx_stride, void* dweight, void* dbias, float* workspace,
-                            cudaStream_t st) {
+                            unsigned* err, cudaStream_t st) {
     const bool sums = dweight || dbias;
-    const NormBwdArgs a{dy, x, weight, mean, rstd, dx, sums ? workspace : nullptr, rows, dy_stride, x_stride, dx_stride, cols, wdtype};
+    const NormBwdArgs a{dy, x, weight, mean, rstd, dx, sums ? workspace : nullptr, rows, dy_stride, x_stride, dx_stride, cols, wdtype, err};
     int blocks = 0;
     cudaError_t e = cudaSuccess;
     if (rows > 0) {
@@ -246,7 +290,7 @@ cudaError_t launch_norm_bwd(int dtype, const void* dy, long long dy_stride, cons
     }
     if (e || !sums) return e;
     count_launches(1);
-    return launch_pdl(k_norm_bwd_sum, dim3((unsigned)((2ll * cols + 31) / 32)), dim3(256), 0, st, (const float*)workspace, blocks,
+    return launch_pdl(k_norm_bwd_sum, dim3((unsigned)((2ll * cols + 31) / 32)), dim3(1024), 0, st, (const float*)workspace, blocks,
                       cols, dweight, dbias, wdtype);
 }
 
