@@ -7,7 +7,9 @@ namespace gs {
 
 namespace {
 
-constexpr int kMaxTcDim = 128;  // head dimensions above it go to the float32 kernels
+// Head dimensions above it go to the float32 kernels, as does the backward of float32 heads above 64: three planes of
+// its rows and of two walked tiles do not fit shared memory.
+constexpr int kMaxTcDim = 128;
 
 // What a call packs, how it splits its walks, and where the pieces lie in the workspace (byte offsets).
 struct Plan {
@@ -36,7 +38,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         return here;
     };
     const size_t bq = (size_t)a.batch * a.heads * a.len_q, bk = (size_t)a.batch * a.kv_heads;
-    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && a.len_q > 0 && !(backward && a.dtype == GS_DTYPE_F32);
+    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && a.len_q > 0 && !(backward && a.dtype == GS_DTYPE_F32 && a.d > 64);
     if (backward && !p.tc) p.delta = take(bq * sizeof(float));
     if (p.tc) {
         const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
@@ -44,7 +46,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         p.dp = a.d <= 64 ? 64 : 128;
         p.rows_k = ((long long)a.len_k + kTileRows - 1) / kTileRows * kTileRows;
         p.pack_q = wide || !tensors || !copyable(a.q, a, a.len_q);
-        p.pack_do = backward && (!tensors || !copyable(a.dout, a, a.len_q));
+        p.pack_do = backward && (wide || !tensors || !copyable(a.dout, a, a.len_q));
         p.pack_kv = wide || masked || !tensors || !copyable(a.k, a, a.len_k) || !copyable(a.v, a, a.len_k);
         // Few blocks: the walk is split, at least `least` tiles each, so that every SM has one.
         const int sms = device_sm_count();
@@ -60,8 +62,8 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
         } else {
             p.qpad = over(a.len_q, attn_bwd_walk()) * attn_bwd_walk();
-            p.splits_q = split(over(a.len_q, attn_bwd_rows(false, p.dp)) * a.heads * a.batch, over(a.len_k, attn_bwd_walk()), 4);
-            p.splits_k = split(over(a.len_k, attn_bwd_rows(true, p.dp)) * a.kv_heads * a.batch,
+            p.splits_q = split(over(a.len_q, attn_bwd_rows(false, p.dp, p.planes)) * a.heads * a.batch, over(a.len_k, attn_bwd_walk()), 4);
+            p.splits_k = split(over(a.len_k, attn_bwd_rows(true, p.dp, p.planes)) * a.kv_heads * a.batch,
                                p.qpad / attn_bwd_walk() * (a.heads / a.kv_heads), 4);
             p.nlse = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
             p.delta = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));

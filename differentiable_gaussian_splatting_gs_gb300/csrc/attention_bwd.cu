@@ -22,7 +22,6 @@
 
 namespace gs {
 
-constexpr int kBN = 64;  // walked rows per tile
 
 template <int DP, bool KEYS>
 struct BwdShape {
@@ -37,19 +36,6 @@ struct BwdShape {
     static constexpr int kAcc = 256;                    // first accumulator column
     static constexpr int kAccs = KEYS ? 2 : 1;
     static_assert(kAcc + kRows * kAccs * DP <= 512 && kStages >= (kRows == 1 ? 3 : 2));
-};
-
-struct BwdArgs {
-    TcArgs t;              // t.part: float32 shares of dq, or of dk and then dv, or NULL; t.tiles: row blocks of a head
-    const float* nlse;     // [batch x heads][len_q padded]: the exponent's offset of each query (k_attn_stats)
-    const float* ndelta;   // likewise: -delta times `ds_in`
-    long long qpad;
-    // dS = P (dP ds_in + ndelta); the sums of dS B1 and of P B2 times ds_out and p_out. factor: ds_in and ds_out of
-    // each batch entry and key head instead, or NULL
-    float ds_in, ds_out, p_out;
-    const float2* factor;
-    const int* index;      // packed key -> key, or NULL
-    long long rows_k;
 };
 
 template <class T, int DP, bool KEYS>
@@ -455,7 +441,7 @@ unsigned blocks_of(long long threads) { return (unsigned)((threads + 255) / 256)
 
 }  // namespace
 
-int attn_bwd_rows(bool keys, int dp) { return (keys && dp == 128 ? 1 : 2) * kTileRows; }
+int attn_bwd_rows(bool keys, int dp, int planes) { return (planes == 3 || (keys && dp == 128) ? 1 : 2) * kTileRows; }
 int attn_bwd_walk() { return kBN; }
 
 cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st) {
@@ -495,7 +481,9 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor
                         1.f, half ? 1.f / 32768.f : 1.f, half ? w.factor : nullptr, w.index, w.rows_k};
         const TcTensor* x[2][4] = {{&q, &dout, &k64, &v64}, {&k, &v, &q64, &dout64}};
         const TcTensor in[4] = {*x[keys][0], *x[keys][1], *x[keys][2], *x[keys][3]};
-        if ((e = half ? typed<__half>(g, keys, w.dp, in, st) : typed<__nv_bfloat16>(g, keys, w.dp, in, st))) return e;
+        if (a.dtype == GS_DTYPE_F32) e = launch_attn_bwd_wide(g, keys, in, st);
+        else e = half ? typed<__half>(g, keys, w.dp, in, st) : typed<__nv_bfloat16>(g, keys, w.dp, in, st);
+        if (e) return e;
         if (splits == 1) continue;
         for (int i = 0; i < 1 + keys; ++i) {
             count_launches(1);

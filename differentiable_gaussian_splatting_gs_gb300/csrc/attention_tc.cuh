@@ -66,8 +66,24 @@ cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTenso
                                int nq, cudaStream_t st);
 
 
+constexpr int kBN = 64;  // rows per tile that the backward walks
+struct BwdArgs {
+    TcArgs t;              // t.part: float32 shares of dq, or of dk and then dv, or NULL; t.tiles: row blocks of a head
+    const float* nlse;     // [batch x heads][len_q padded]: the exponent's offset of each query (k_attn_stats)
+    const float* ndelta;   // likewise: -delta times `ds_in`
+    long long qpad;
+    // dS = P (dP ds_in + ndelta); the sums of dS B1 and of P B2 times ds_out and p_out. factor: ds_in and ds_out of
+    // each batch entry and key head instead, or NULL
+    float ds_in, ds_out, p_out;
+    const float2* factor;
+    const int* index;      // packed key -> key, or NULL
+    long long rows_k;
+};
+// The backward of three planes, heads of up to 64; x: the row operands, then the walked ones.
+cudaError_t launch_attn_bwd_wide(const BwdArgs& g, bool keys, const TcTensor (&x)[4], cudaStream_t st);
+
 // Rows per block of the backward kernel that sums dk and dv (keys) or dq, and per tile that it walks.
-int attn_bwd_rows(bool keys, int dp);
+int attn_bwd_rows(bool keys, int dp, int planes);
 int attn_bwd_walk();
 struct TcBwd {
     AttnArgs a;
