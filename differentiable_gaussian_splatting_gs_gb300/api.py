@@ -545,48 +545,48 @@ def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, 
     return dx, dweight, dbias
 
 
-def _heads(t, shape, like, where: str) -> _abi.gs_heads:
-    if t is not like and (t.shape != shape or t.dtype is not like.dtype or t.device != like.device):
-        raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {like.dtype}, {like.device} is needed, "
+def _heads(t, shape, dtype, device, where: str) -> _abi.gs_heads:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {dtype}, {device} is needed, "
                          f"got {tuple(t.shape)}, {t.dtype}, {t.device}")
     b, n, h, d = t.stride()
     if d != 1 and shape[3] > 1:
         raise ValueError(f"{where}: the elements of a head must be contiguous")
-    return _abi.gs_heads(_ptr(t), b, n, h)
+    return _abi.gs_heads(t.data_ptr() or _ptr(t), b, n, h)
 
 
-def _attention(q, k, v, k_len, key_mask, scale, where: str):
-    dtype = _dtype(q, where)
+def _attention(q, k, k_len, key_mask, scale, where: str):
+    """(gs_attention, q's shape, k's and v's shape, what the workspace's size depends on)"""
+    code, device = _dtype(q, where), q.device
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"{where}: q, k and v must be [batch, length, heads, head_dim]")
     b, lq, h, d = q.shape
-    lk, hk = k.shape[1:3]
+    _, lk, hk, _ = k.shape
     if h < 1 or hk < 1 or h % hk:
         raise ValueError(f"{where}: {h} query heads must be a multiple of {hk} key heads")
     if k_len is not None and (k_len.shape != (b,) or k_len.dtype != torch.int32 or not k_len.is_contiguous() or
-                              k_len.device != q.device):
-        raise ValueError(f"{where}: k_len must be a contiguous int32 [{b}] tensor on {q.device}")
+                              k_len.device != device):
+        raise ValueError(f"{where}: k_len must be a contiguous int32 [{b}] tensor on {device}")
     if key_mask is not None and (key_mask.shape != (b, lk) or key_mask.dtype not in (torch.bool, torch.uint8) or
-                                 (lk > 1 and key_mask.stride(1) != 1) or key_mask.device != q.device):
-        raise ValueError(f"{where}: key_mask must be a bool or uint8 [{b}, {lk}] tensor on {q.device} with contiguous rows")
+                                 (lk > 1 and key_mask.stride(1) != 1) or key_mask.device != device):
+        raise ValueError(f"{where}: key_mask must be a bool or uint8 [{b}, {lk}] tensor on {device} with contiguous rows")
     if scale is not None and not scale > 0:
         raise ValueError(f"{where}: scale must be positive")
-    a = _abi.gs_attention(dtype, b, h, hk, d, lq, lk, scale or 0.0, _ptr(k_len), _ptr(key_mask),
+    a = _abi.gs_attention(code, b, h, hk, d, lq, lk, scale or 0.0, _ptr(k_len), _ptr(key_mask),
                           0 if key_mask is None else key_mask.stride(0))
-    return a, q.shape, (b, lk, hk, d)
+    return a, (b, lq, h, d), (b, lk, hk, d), (device.index, code, b, h, hk, d, lq, lk, k_len is not None, key_mask is not None)
 
 
 @functools.lru_cache(maxsize=4096)
-def _attention_workspace_bytes(device, backward, dtype, b, h, hk, d, lq, lk, k_len, key_mask) -> int:
+def _attention_workspace_bytes(backward, device, dtype, b, h, hk, d, lq, lk, k_len, key_mask) -> int:
     # only whether there is a length or a mask counts, and the current device's number of SMs
     a = _abi.gs_attention(dtype, b, h, hk, d, lq, lk, 0.0, 16 if k_len else None, 16 if key_mask else None)
     with torch.cuda.device(device):
         return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), backward))
 
 
-def _attention_workspace(a, backward: int, workspace, like, stream):
-    need = _attention_workspace_bytes(like.get_device(), backward, a.dtype, a.batch, a.heads, a.kv_heads, a.head_dim, a.len_q,
-                                      a.len_k, a.k_len is not None, a.key_mask is not None)
+def _attention_workspace(key, backward: int, workspace, like, stream):
+    need = _attention_workspace_bytes(backward, *key)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = _alloc((need,), like, stream, torch.uint8)
     return workspace, need
@@ -594,9 +594,7 @@ def _attention_workspace(a, backward: int, workspace, like, stream):
 
 def gs_cross_attention_workspace_bytes(q, k, v, k_len=None, key_mask=None, backward: bool = False) -> int:
     """Bytes of workspace that gs_cross_attention_fwd / _bwd of these tensors use."""
-    a, _, _ = _attention(q, k, v, k_len, key_mask, None, "gs_cross_attention_workspace_bytes")
-    with torch.cuda.device(q.device):
-        return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), int(backward)))
+    return _attention_workspace_bytes(int(backward), *_attention(q, k, k_len, key_mask, None, "gs_cross_attention_workspace_bytes")[3])
 
 
 def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | None = None, out=None, workspace=None,
@@ -606,36 +604,35 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     k_len: int32 [batch], keys that count per batch entry; key_mask: bool [batch, len_k], True where a key
     counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a byte
     tensor kept by the caller (allocated when None or too small)."""
-    where = "gs_cross_attention_fwd"
-    a, qs, kvs = _attention(q, k, v, k_len, key_mask, scale, where)
-    hq, hk, hv = _heads(q, qs, q, where), _heads(k, kvs, q, where), _heads(v, kvs, q, where)
+    where, dtype, device = "gs_cross_attention_fwd", q.dtype, q.device
+    a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
+    hq, hk, hv = _heads(q, qs, dtype, device, where), _heads(k, kvs, dtype, device, where), _heads(v, kvs, dtype, device, where)
     stats = (qs[0], qs[2], qs[1])
     if out is None:
         o, lse = _alloc(qs, q, stream), _alloc(stats, q, stream, torch.float32)
     else:
         o, lse = out
         _floats(lse, stats, q, where)
-    ho = _heads(o, qs, q, where)
-    workspace, need = _attention_workspace(a, 0, workspace, q, stream)
+    ho = _heads(o, qs, dtype, device, where)
+    workspace, need = _attention_workspace(key, 0, workspace, q, stream)
     check(_call(q, stream, _abi.load().gs_cross_attention_fwd, C.byref(a), C.byref(hq), C.byref(hk), C.byref(hv), C.byref(ho),
-                _ptr(lse), _ptr(workspace) if need else None, need), where)
+                _ptr(lse), workspace.data_ptr() if need else None, need), where)
     return o, lse
 
 
 def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, scale: float | None = None, grads=None,
                            workspace=None, stream=None):
     """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given."""
-    where = "gs_cross_attention_bwd"
-    a, qs, kvs = _attention(q, k, v, k_len, key_mask, scale, where)
-    ins = [_heads(dout, qs, q, where), _heads(q, qs, q, where), _heads(k, kvs, q, where), _heads(v, kvs, q, where),
-           _heads(out, qs, q, where)]
+    where, dtype, device = "gs_cross_attention_bwd", q.dtype, q.device
+    a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
+    ins = [_heads(t, s, dtype, device, where) for t, s in ((dout, qs), (q, qs), (k, kvs), (v, kvs), (out, qs))]
     _floats(lse, (qs[0], qs[2], qs[1]), q, where)
     if grads is None:
         grads = (_alloc(qs, q, stream), _alloc(kvs, q, stream), _alloc(kvs, q, stream))
-    outs = [_heads(t, sh, q, where) for t, sh in zip(grads, (qs, kvs, kvs))]
-    workspace, need = _attention_workspace(a, 1, workspace, q, stream)
+    outs = [_heads(t, s, dtype, device, where) for t, s in zip(grads, (qs, kvs, kvs))]
+    workspace, need = _attention_workspace(key, 1, workspace, q, stream)
     check(_call(q, stream, _abi.load().gs_cross_attention_bwd, C.byref(a), *map(C.byref, ins), _ptr(lse), *map(C.byref, outs),
-                _ptr(workspace) if need else None, need), where)
+                workspace.data_ptr() if need else None, need), where)
     return tuple(grads)
 
 

@@ -13,7 +13,7 @@ constexpr int kMaxTcDim = 128;
 
 // What a call packs, how it splits its walks, and where the pieces lie in the workspace (byte offsets).
 struct Plan {
-    bool tc, pack_q, pack_kv, pack_do;
+    bool tc, decode, pack_q, pack_kv, pack_do;
     int planes, dp, nq, splits;
     int splits_q, splits_k;  // backward: of the walks for dq, and for dk and dv
     long long rows_k;        // rows of a packed head of K or V
@@ -39,6 +39,20 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
     };
     const size_t bq = (size_t)a.batch * a.heads * a.len_q, bk = (size_t)a.batch * a.kv_heads;
     p.tc = a.d <= kMaxTcDim && a.len_k > 0 && a.len_q > 0 && !(backward && a.dtype == GS_DTYPE_F32 && a.d > 64);
+    if (!backward && a.len_q == 1 && a.len_k > 0 && a.heads == a.kv_heads) {
+        // two blocks an SM, with at least 64 keys each
+        p.tc = false;
+        p.decode = true;
+        p.dp = a.d;
+        const long long blocks = (long long)bk, most = (a.len_k + 63) / 64;
+        long long splits = 2 * device_sm_count() / (blocks > 0 ? blocks : 1);
+        if (splits > most) splits = most;
+        p.splits = splits < 1 ? 1 : (int)splits;
+        if (p.splits > 1) {
+            p.part = take((size_t)p.splits * bq * p.dp * sizeof(float));
+            p.part_lse = take((size_t)p.splits * bq * sizeof(float));
+        }
+    }
     if (backward && !p.tc) p.delta = take(bq * sizeof(float));
     if (p.tc) {
         const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
@@ -160,10 +174,17 @@ size_t attn_workspace_bytes(const AttnArgs& a, bool backward) { return plan(a, b
 
 cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st) {
     const Plan p = plan(a, false, true);
-    if (!p.tc) return launch_attn_simt(a, false, st);
     char* ws = static_cast<char*>(workspace);
+    cudaError_t e;
+    if (p.decode) {
+        float* part = p.splits > 1 ? reinterpret_cast<float*>(ws + p.part) : nullptr;
+        float* part_lse = p.splits > 1 ? reinterpret_cast<float*>(ws + p.part_lse) : nullptr;
+        e = launch_attn_decode(a, p.splits, p.dp, part, part_lse, st);
+        return e || !part ? e : launch_attn_combine(a, part, part_lse, p.splits, p.dp, st);
+    }
+    if (!p.tc) return launch_attn_simt(a, false, st);
     int *count, *index;
-    cudaError_t e = lay_out(p, a, ws, count, index, st);
+    e = lay_out(p, a, ws, count, index, st);
     if (e) return e;
     TcArgs t{a, count, nullptr, nullptr, 0, p.splits};
     const int bn = p.planes == 3 && p.dp == 128 ? 64 : 128;

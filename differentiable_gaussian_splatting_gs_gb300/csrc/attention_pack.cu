@@ -82,33 +82,73 @@ __global__ void __launch_bounds__(256) k_attn_pack(const AttnArgs a, const AttnT
     }
 }
 
-// A warp per query and head: the shares weighted by exp(lse - max lse), in order.
-template <class T>
+// The shares weighted by exp(lse - max lse), WARPS warps to a query and head, each with its part of the shares; they are
+// joined in order.
+template <class T, int WARPS>
 __global__ void __launch_bounds__(256) k_attn_combine(const AttnArgs a, const float* part, const float* part_lse, int splits,
                                                       int dp) {
     pdl_entry();
+    __shared__ float meet[WARPS > 1 ? WARPS : 1][256 + 2];
     const long long rows = (long long)a.batch * a.heads * a.len_q;
-    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / 32;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / (32 * WARPS);
     if (row >= rows) return;
-    const int lane = threadIdx.x & 31, i = (int)(row % a.len_q);
+    const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0, i = (int)(row % a.len_q);
     const long long bh = row / a.len_q;
     const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
-    float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, part_lse[s * rows + row]);
-    T* dst = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride + i * a.out.len_stride;
-    const float base = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
-    for (int s = 0; s < splits; ++s) total += expf(part_lse[s * rows + row] - base);
-    for (int c = lane; c < a.d; c += 32) {
-        float o = 0.f;
-        for (int s = 0; s < splits; ++s) {
-            const float l = part_lse[s * rows + row];
-            // a share without keys was not written
-            if (l != -INFINITY) o = fmaf(expf(l - base), part[(s * rows + row) * dp + c], o);
+    constexpr int kMost = 8, kAhead = 4;  // columns of a lane (heads of up to 256), shares under way
+    float o[kMost] = {}, total = 0.f, top = -INFINITY;
+    for (int s0 = warp; s0 < splits; s0 += WARPS * kAhead) {
+        float l[kAhead], x[kAhead][kMost], m = top;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = s0 + u * WARPS;
+            l[u] = s < splits ? part_lse[s * rows + row] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kMost; ++k)
+                if (s < splits && lane + 32 * k < a.d) x[u][k] = part[(s * rows + row) * dp + lane + 32 * k];
         }
-        dst[c] = from_float<T>(total == 0.f ? 0.f : o / total);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) m = fmaxf(m, l[u]);
+        const float zero = m == -INFINITY ? 0.f : m, keep = expf(top - zero);
+        top = m;
+        total *= keep;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) o[k] *= keep;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float w = expf(l[u] - zero);
+            total += w;
+#pragma unroll
+            for (int k = 0; k < kMost; ++k)
+                if (lane + 32 * k < a.d) o[k] += l[u] == -INFINITY ? 0.f : w * x[u][k];  // a share without keys was not written
+        }
     }
-    if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
+    if (WARPS > 1) {
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) meet[warp][lane + 32 * k] = o[k];
+        if (lane == 0) meet[warp][256] = top, meet[warp][257] = total;
+        __syncthreads();
+        if (warp != 0) return;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, meet[w][256]);
+        total = 0.f;
+        top = m;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) o[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float keep = expf(meet[w][256] - (m == -INFINITY ? 0.f : m));
+            total = fmaf(keep, meet[w][257], total);
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) o[k] = fmaf(keep, meet[w][lane + 32 * k], o[k]);
+        }
+    }
+    T* dst = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride + i * a.out.len_stride;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+        if (lane + 32 * k < a.d) dst[lane + 32 * k] = from_float<T>(total == 0.f ? 0.f : o[k] / total);
+    if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : top + logf(total);
 }
 
 cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st) {
@@ -131,8 +171,11 @@ cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, 
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st) {
-    const long long blocks = ((long long)a.batch * a.heads * a.len_q + 7) / 8;
-    auto* kernel = a.dtype == GS_DTYPE_F32 ? k_attn_combine<float> : a.dtype == GS_DTYPE_F16 ? k_attn_combine<__half> : k_attn_combine<__nv_bfloat16>;
+    const bool many = splits > 4;  // a block per row: eight times four shares under way together
+    const long long rows = (long long)a.batch * a.heads * a.len_q, blocks = many ? rows : (rows + 7) / 8;
+    auto* kernel = a.dtype == GS_DTYPE_F32   ? (many ? k_attn_combine<float, 8> : k_attn_combine<float, 1>)
+                   : a.dtype == GS_DTYPE_F16 ? (many ? k_attn_combine<__half, 8> : k_attn_combine<__half, 1>)
+                                             : (many ? k_attn_combine<__nv_bfloat16, 8> : k_attn_combine<__nv_bfloat16, 1>);
     count_launches(1);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, part, part_lse, splits, dp);
 }

@@ -61,6 +61,8 @@ cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, 
                              const int* index, int planes, int dp, long long rows, void* dst, cudaStream_t st);
 // out and lse from the splits' shares [splits][batch][heads][len_q][dp].
 cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st);
+// One query, no shared heads; part, part_lse: the splits' shares, or NULL.
+cudaError_t launch_attn_decode(const AttnArgs& a, int splits, int dp, float* part, float* part_lse, cudaStream_t st);
 // nq: query tiles per block, 1 or 2.
 cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTensor& k, const TcTensor& v, int planes, int dp,
                                int nq, cudaStream_t st);
