@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(384, 1)
             int sent = 0;
             for (int j = 0; j < n; ++j) {
                 const int s = j % kSt, x = first + j;
-                if (j >= kSt && !mbar_sleep_bounded(&empty[s], (j / kSt + 1) & 1, limit, a.err)) break;
+                if (j >= kSt && !mbar_wait_bounded(&empty[s], (j / kSt + 1) & 1, limit, a.err)) break;
                 const int wh = KEYS ? h * share + x / per_head : h / share, w0 = (KEYS ? x % per_head : x) * kBN;
                 mbar_arrive_expect_tx(&full[s], 2 * S::kB + (KEYS ? 2 * kBN * 4 : 0));
                 load_rows<DP, 1, kBN>(sb + s * S::kStage, tb1, w0, b, wh, KEYS ? a.heads : a.kv_heads, &full[s]);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(384, 1)
         } else if (warp == 9 && n > 0 && elect_one()) {  // products
             const int steps = (a.d + 15) / 16;
             const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
-            auto wait = [&](uint64_t* bar, int k) { return mbar_sleep_bounded(bar, k & 1, limit, a.err); };
+            auto wait = [&](uint64_t* bar, int k) { return mbar_wait_bounded(bar, k & 1, limit, a.err); };
             // S and dP of walked tile j in warpgroup w's columns
             auto scores = [&](int w, int j) {
                 const uint32_t row = (kR == 2 ? w : 0) * S::kA, tile = sb + (j % kSt) * S::kStage;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(512, 1)
             int sent = 0;
             for (int j = 0; j < n; ++j) {
                 const int s = j & 1, x = first + j;
-                if (j >= 2 && !mbar_sleep_bounded(&empty[s], (j / 2 + 1) & 1, limit, a.err)) break;
+                if (j >= 2 && !mbar_wait_bounded(&empty[s], (j / 2 + 1) & 1, limit, a.err)) break;
                 const int wh = KEYS ? h * share + x / per_head : h / share, w0 = (KEYS ? x % per_head : x) * kBN;
                 mbar_arrive_expect_tx(&full[s], 2 * kWalkBytes + (KEYS ? 2 * kBN * 4 : 0));
                 load_rows<kDP, kPL, kBN>(sb + s * kStage, tb1, w0, b, wh, KEYS ? a.heads : a.kv_heads, &full[s]);
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(512, 1)
         } else if (warp == 13 && n > 0 && elect_one()) {  // products
             const int steps = (a.d + 15) / 16;
             const uint32_t s_desc = mma_desc<__nv_bfloat16>(kBN, false), g_desc = mma_desc<__nv_bfloat16>(steps * 16, true);
-            auto wait = [&](uint64_t* bar, int k) { return mbar_sleep_bounded(bar, k & 1, limit, a.err); };
+            auto wait = [&](uint64_t* bar, int k) { return mbar_wait_bounded(bar, k & 1, limit, a.err); };
             bool ok = wait(&a_full, 0);
             auto scores = [&](int j) {
                 const int w = j & 1;

@@ -8,11 +8,11 @@
 // last 128 of them in turn: the next S is then formed while this one's softmax runs, and the softmax
 // never waits for P V. Otherwise the next S waits for P V.
 //
-// The softmax is bound by its exponentials (4 cycles a warp instruction and scheduler: 1024 for two 128 x 128
-// tiles, as many as their products take with heads of 64). Two query tiles take turns at them: while one forms P,
-// the other waits for S, loads it and finds its maximum. Left to themselves they fall into step, and the exponentials
-// stand still while both load. The maximum in use is only raised, and O rescaled, when a row's scores pass it by
-// 2^8: P may then reach 2^8, which float32 sums and 16-bit P (relative rounding) carry as well as 1.
+// The softmax is bound by what a warp issues one after the other, its exponentials first (4 cycles a warp instruction
+// and scheduler: 1024 for two 128 x 128 tiles, as many as their products take with heads of 64). So 16-bit tiles do not
+// look for the row's maximum: P is formed with the one in use, and only when the tile's sum shows that a score passed
+// it far (a sum above 2^12) is the maximum found and raised, O rescaled and P formed again. Below that P, its sums and its
+// products are as exact as with the maximum itself (relative rounding, float16 reaches 2^16).
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -112,11 +112,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = 0; j < n && ok; ++j) {
                     const int s = j % kSt;
                     const unsigned ph = (j / kSt + 1) & 1;
-                    if (j >= kSt && !(ok = mbar_sleep_bounded(&k_free[s], ph, limit, a.err))) break;
+                    if (j >= kSt && !(ok = mbar_wait_bounded(&k_free[s], ph, limit, a.err))) break;
                     mbar_arrive_expect_tx(&k_full[s], S::kKV);
                     load_rows<DP, PL, BN>(sk + s * S::kKV, tk, (first + j) * BN, b, hk, a.kv_heads, &k_full[s]);
                     sent = 2 * j + 1;
-                    if (j >= kSt && !(ok = mbar_sleep_bounded(&v_free[s], ph, limit, a.err))) break;
+                    if (j >= kSt && !(ok = mbar_wait_bounded(&v_free[s], ph, limit, a.err))) break;
                     mbar_arrive_expect_tx(&v_full[s], S::kKV);
                     load_rows<DP, PL, BN>(sv + s * S::kKV, tv, (first + j) * BN, b, hk, a.kv_heads, &v_full[s]);
                     sent = 2 * j + 2;
@@ -127,15 +127,16 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
                 for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
             }
-        } else if (warp - NQ * 4 - 1 < S::kIssuers && n > 0 && elect_one()) {
-            // Products. Where S takes turns, each query tile has a thread that issues them: a wait costs it about
-            // 70 cycles even when it is over, and a commit as many. Otherwise one thread serves both tiles, and its
-            // order (P V and S of one, then of the other) keeps their softmaxes half a turn apart.
+        } else if (warp - NQ * 4 - 1 < S::kIssuers && n > 0) {
+            // Products: the warp waits, one thread issues. Where S takes turns, each query tile has a warp that
+            // issues them. Otherwise one serves both tiles, and its order (P V and S of one, then of the other) keeps
+            // their softmaxes half a turn apart.
             const int i0 = warp - NQ * 4 - 1, i1 = S::kTurns ? i0 + 1 : NQ;
             const uint32_t qk_desc = mma_desc<T>(BN, false), pv_desc = mma_desc<T>((a.d + 15) / 16 * 16, true);
             const int steps = (a.d + 15) / 16;  // of the inner dimension of Q K^T
             auto scores = [&](int i, int j) {
                 const int s = j % kSt;
+                if (!elect_one()) return;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t qa = tile_desc(sq + i * S::kQ + C::a(c) * DP * kTileRows * 2);
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             };
             auto values = [&](int i, int j) {
                 const int s = j % kSt;
+                if (!elect_one()) return;
 #pragma unroll
                 for (int c = 0; c < C::n; ++c) {
                     const uint32_t vb = tile_desc(sv + s * S::kKV + C::b(c) * DP * BN * 2, BN * 128);
@@ -162,29 +164,40 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 if (j >= n - 2) mma_commit(&o_done[i]);
                 if (i == i1 - 1) mma_commit(&v_free[s]);
             };
-            auto wait = [&](uint64_t* bar, int j) { return mbar_sleep_bounded(bar, j & 1, limit, a.err); };
-            bool ok = wait(&q_full, 0) && wait(&k_full[0], 0);
+            bool ok = warp_wait_all(&q_full, 0, &k_full[0], 0, limit, a.err);
             tc_fence_after();
             if (ok)
                 for (int i = i0; i < i1; ++i) scores(i, 0);
             for (int j = 0; j < n && ok; ++j) {
                 const bool more = j + 1 < n;
-                if (S::kTurns && more && (ok = wait(&k_full[(j + 1) % kSt], (j + 1) / kSt) && wait(&s_free[i0], j))) {
-                    // over the P of tile j - 1, whose P V this thread issued before
+                uint64_t *vf = &v_full[j % kSt], *kf = &k_full[(j + 1) % kSt];
+                const unsigned vp = j / kSt, kp = (j + 1) / kSt;
+                if (S::kTurns) {
+                    if (more) {
+                        // over the P of tile j - 1, whose P V this thread issued before
+                        if (!(ok = warp_wait_all(kf, kp, &s_free[i0], j, limit, a.err))) break;
+                        tc_fence_after();
+                        scores(i0, j + 1);
+                    }
+                    if (!(ok = warp_wait_all(vf, vp, &p_full[i0], j, limit, a.err))) break;
                     tc_fence_after();
-                    scores(i0, j + 1);
-                }
-                ok = ok && wait(&v_full[j % kSt], j / kSt);
-                for (int i = i0; i < i1; ++i)
-                    if ((ok = ok && wait(&p_full[i], j))) {
+                    values(i0, j);
+                } else {
+                    for (int i = 0; i < NQ; ++i) {
+                        if (!(ok = more ? warp_wait_all(vf, vp, &p_full[i], j, kf, kp, limit, a.err)
+                                        : warp_wait_all(vf, vp, &p_full[i], j, limit, a.err)))
+                            break;
                         tc_fence_after();
                         values(i, j);
-                        if (!S::kTurns && more && (i > i0 || (ok = wait(&k_full[(j + 1) % kSt], (j + 1) / kSt)))) scores(i, j + 1);
+                        if (more) scores(i, j + 1);
                     }
+                }
             }
             // no product is in flight when the tensor memory is freed
-            mma_commit(&drain[i0]);
-            mbar_wait_bounded(&drain[i0], 0, kDrainLimit, a.err);
+            if (elect_one()) {
+                mma_commit(&drain[i0]);
+                mbar_wait_bounded(&drain[i0], 0, kDrainLimit, a.err);
+            }
         }
     } else {  // softmax: thread = query
         if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -217,12 +230,6 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 tmem_wait_ld(o);
             }
         };
-        // Turns at the exponentials: a barrier per query tile, where its warps meet the other's that are done. Every
-        // warp comes through every turn, one whose wait gave up too.
-        auto my_turn = [&]() {
-            if (NQ == 2) asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory");
-        };
-        if (NQ == 2 && i == 1 && n > 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             ok = ok && warp_wait(&s_full[i], j & 1, limit, a.err);
@@ -278,6 +285,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < PL; ++q) tmem_st16(tp + p_column<PL, BN>(q, 2 * g), p[q]);
             };
+            auto total = [&](const f32x2 (&s)[4]) {
+                const f32x2 one = f2_pack(1.f, 1.f);
+                const float2 p = f2_unpack(f2_fma(s[0], one, s[2])), q = f2_unpack(f2_fma(s[1], one, s[3]));
+                return (p.x + p.y) + (q.x + q.y);
+            };
             // whether the row's maximum in use is too far below m; a score of -inf is no error: exp(-inf) = 0
             auto passed = [&](float m) { return (m - top) * c > 8.f || (top == -INFINITY && m > -INFINITY); };
             auto base = [&]() { const float t0 = top == -INFINITY ? 0.f : -top * c; return f2_pack(t0, t0); };
@@ -302,7 +314,6 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     for (int e = 0; e < kOut; ++e) out[e] *= keep;
                 }
                 __syncwarp();
-                my_turn();
                 s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int g = 0; g < BN / 32; ++g) {
@@ -312,24 +323,50 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     probabilities(x, g, base(), s2);
                 }
             } else {
-                uint32_t x[BN / 32][32];
+                constexpr int G = BN / 32;
+                uint32_t x[G][32];
+                // the second half of the scores is on its way while the first becomes P
 #pragma unroll
-                for (int g = 0; g < BN / 32; ++g) tmem_ld32(ts + g * 32, x[g]);
+                for (int g = 0; g < G / 2; ++g) tmem_ld32(ts + g * 32, x[g]);
 #pragma unroll
-                for (int g = 0; g < BN / 32; ++g) tmem_wait_ld(x[g]);
+                for (int g = 0; g < G / 2; ++g) {
+                    tmem_wait_ld(x[g]);
+                    mask(x[g], g);
+                }
+#pragma unroll
+                for (int g = G / 2; g < G; ++g) tmem_ld32(ts + g * 32, x[g]);
+                auto second_half = [&]() {
+#pragma unroll
+                    for (int g = G / 2; g < G; ++g) {
+                        tmem_wait_ld(x[g]);
+                        mask(x[g], g);
+                    }
+                };
+                auto find_max = [&]() {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) largest(x[g]);
+                    return row_max();
+                };
+                if (j == 0) {
+                    second_half();
+                    top = find_max();
+                }
+                s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
+                f32x2 b2 = base();
+#pragma unroll
+                for (int g = 0; g < G / 2; ++g) probabilities(x[g], g, b2, s2);
+                second_half();
                 if (S::kTurns) {
                     tc_fence_before();
                     warp_arrive(&s_free[i]);
                 }
 #pragma unroll
-                for (int g = 0; g < BN / 32; ++g) mask(x[g], g);
-#pragma unroll
-                for (int g = 0; g < BN / 32; ++g) largest(x[g]);
-                const float m = row_max();
-                const bool raise = passed(m);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float keep = raise ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
-                    if (raise) top = m;
+                for (int g = G / 2; g < G; ++g) probabilities(x[g], g, b2, s2);
+                const bool far = total(s2) > 4096.f;
+                if (__any_sync(0xffffffffu, far)) {
+                    const float m = find_max();
+                    const float keep = far ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
+                    if (far) top = m;
                     sum *= keep;
                     if (j > 0) {
                         // P V of tile j - 1 has left O: before this S where that takes no turns, else before the next
@@ -348,20 +385,16 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                             tmem_st32(to + g * 32, o);
                         }
                     }
-                }
-                my_turn();
-                s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
-                const f32x2 b2 = base();
+                    s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
+                    b2 = base();
 #pragma unroll
-                for (int g = 0; g < BN / 32; ++g) probabilities(x[g], g, b2, s2);
+                    for (int g = 0; g < G; ++g) probabilities(x[g], g, b2, s2);
+                }
             }
-            const f32x2 one = f2_pack(1.f, 1.f);
-            const float2 sa = f2_unpack(f2_fma(s2[0], one, s2[2])), sb = f2_unpack(f2_fma(s2[1], one, s2[3]));
-            sum += (sa.x + sa.y) + (sb.x + sb.y);
+            sum += total(s2);
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&p_full[i]);
-            if (NQ == 2 && (i == 0 || j + 1 < n)) asm volatile("bar.arrive %0, 256;" ::"r"(2 - i) : "memory");
         }
         if (n > 0) ok = ok && warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
         tc_fence_after();

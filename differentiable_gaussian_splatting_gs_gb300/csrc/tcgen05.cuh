@@ -142,30 +142,21 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     if (elect_one()) mbar_arrive(bar);
 }
 
-// As mbar_wait_bounded, but each poll may suspend the thread for up to two microseconds: a thread that waits beside
-// warps that compute then leaves them its issue slots. `limit` polls are at least as long as its.
-__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, unsigned parity, unsigned limit, unsigned* err) {
-    for (unsigned i = 0; i < limit; ++i) {
-        unsigned ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-            : "memory");
-        if (ok) return true;
-        if ((i & 1023u) == 1023u && (*(volatile unsigned*)err & kErrTimeout)) return false;
-    }
-    atomicOr(err, kErrTimeout);
-    return false;
-}
-
-// The same by a whole warp: one answer, so that a warp whose wait gave up stays together for the warp-wide
-// tensor-memory instructions that follow.
+// mbar_wait_bounded by a whole warp: one answer, so that a warp whose wait gave up stays together for the warp-wide
+// tensor-memory instructions that follow. Lanes may name different barriers: all of them are waited for, at the price
+// of one (about 100 cycles where they are over, which a thread that issues products cannot spend on each).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit, unsigned* err) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_sleep_bounded(bar, parity, limit, err));
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit, err));
+}
+__device__ __forceinline__ bool warp_wait_all(uint64_t* a, unsigned pa, uint64_t* b, unsigned pb, unsigned limit, unsigned* err) {
+    const bool odd = threadIdx.x & 1;
+    return warp_wait(odd ? b : a, (odd ? pb : pa) & 1, limit, err);
+}
+__device__ __forceinline__ bool warp_wait_all(uint64_t* a, unsigned pa, uint64_t* b, unsigned pb, uint64_t* c, unsigned pc, unsigned limit,
+                                              unsigned* err) {
+    const bool odd = threadIdx.x & 1, two = threadIdx.x & 2;
+    return warp_wait(two ? c : odd ? b : a, (two ? pc : odd ? pb : pa) & 1, limit, err);
 }
 
 // ---- tiled bulk copies -------------------------------------------------------------------------------
