@@ -184,12 +184,15 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     values(i0, j);
                 } else {
                     for (int i = 0; i < NQ; ++i) {
-                        if (!(ok = more ? warp_wait_all(vf, vp, &p_full[i], j, kf, kp, limit, a.err)
-                                        : warp_wait_all(vf, vp, &p_full[i], j, limit, a.err)))
+                        // with one stage the next K comes while P V runs
+                        if (!(ok = more && kSt > 1 ? warp_wait_all(vf, vp, &p_full[i], j, kf, kp, limit, a.err)
+                                                   : warp_wait_all(vf, vp, &p_full[i], j, limit, a.err)))
                             break;
                         tc_fence_after();
                         values(i, j);
-                        if (more) scores(i, j + 1);
+                        if (!more) continue;
+                        if (kSt == 1 && i == 0 && !(ok = warp_wait(kf, kp & 1, limit, a.err))) break;
+                        scores(i, j + 1);
                     }
                 }
             }
@@ -230,6 +233,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 tmem_wait_ld(o);
             }
         };
+        // Two tiles whose softmaxes nothing else keeps apart fall into step, and the exponentials stand still while both
+        // load: one may begin its tile when the other is half through. Every warp comes through every turn, one
+        // whose wait gave up too.
+        constexpr bool kStagger = S::kTurns && NQ == 2;
+        if (kStagger && i == 1 && n > 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             ok = ok && warp_wait(&s_full[i], j & 1, limit, a.err);
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             } else {
                 constexpr int G = BN / 32;
                 uint32_t x[G][32];
-                // the second half of the scores is on its way while the first becomes P
+                // where S takes no turns, the second half of the scores is on its way while the first becomes P
 #pragma unroll
                 for (int g = 0; g < G / 2; ++g) tmem_ld32(ts + g * 32, x[g]);
 #pragma unroll
@@ -347,19 +355,22 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     for (int g = 0; g < G; ++g) largest(x[g]);
                     return row_max();
                 };
-                if (j == 0) {
+                if (S::kTurns) {  // the next S can start
                     second_half();
+                    tc_fence_before();
+                    warp_arrive(&s_free[i]);
+                }
+                if (j == 0) {
+                    if (!S::kTurns) second_half();
                     top = find_max();
                 }
                 s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
                 f32x2 b2 = base();
+                if (kStagger) asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory");
 #pragma unroll
                 for (int g = 0; g < G / 2; ++g) probabilities(x[g], g, b2, s2);
-                second_half();
-                if (S::kTurns) {
-                    tc_fence_before();
-                    warp_arrive(&s_free[i]);
-                }
+                if (kStagger && (i == 0 || j + 1 < n)) asm volatile("bar.arrive %0, 256;" ::"r"(2 - i) : "memory");
+                if (!S::kTurns) second_half();
 #pragma unroll
                 for (int g = G / 2; g < G; ++g) probabilities(x[g], g, b2, s2);
                 const bool far = total(s2) > 4096.f;
