@@ -75,10 +75,10 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             p.nq = two ? 2 : 1;
             p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
         } else {
-            p.qpad = over(a.len_q, attn_bwd_walk()) * attn_bwd_walk();
-            p.splits_q = split(over(a.len_q, attn_bwd_rows(false, p.dp, p.planes)) * a.heads * a.batch, over(a.len_k, attn_bwd_walk()), 4);
-            p.splits_k = split(over(a.len_k, attn_bwd_rows(true, p.dp, p.planes)) * a.kv_heads * a.batch,
-                               p.qpad / attn_bwd_walk() * (a.heads / a.kv_heads), 4);
+            p.qpad = over(a.len_q, kBN) * kBN;
+            p.splits_q = split(over(a.len_q, kTileRows) * a.heads * a.batch, over(a.len_k, kBN), 4);
+            p.splits_k = split(over(a.len_k, kTileRows) * a.kv_heads * a.batch,
+                               p.qpad / kBN * (a.heads / a.kv_heads), 4);
             p.nlse = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
             p.delta = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
             if (a.dtype == GS_DTYPE_F16) {
@@ -216,7 +216,7 @@ cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t 
                   reinterpret_cast<unsigned*>(ws + p.norms), reinterpret_cast<float2*>(ws + p.factor), reinterpret_cast<float*>(ws + p.part), p.qpad, p.rows_k, p.dp, p.splits_q, p.splits_k};
     TcTensor x[2][4];  // as row tiles, as walked tiles: Q, dout, K, V
     for (int i = 0; i < 2; ++i) {
-        const int box = i == 0 ? kTileRows : attn_bwd_walk();
+        const int box = i == 0 ? kTileRows : kBN;
         if ((e = operand(x[i][0], p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, box)) ||
             (e = operand(x[i][1], p, a, a.dout, a.heads, a.len_q, p.pack_do, ws + p.dout, a.len_q, box)) ||
             (e = operand(x[i][2], p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, box)) ||

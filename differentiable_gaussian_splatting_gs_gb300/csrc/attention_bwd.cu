@@ -1,23 +1,27 @@
 // Cross attention, backward, on the tensor cores (16-bit types).
 //
-// One kernel in two roles. In both a block holds 128 or 256 rows and walks the other side in tiles of 64, forming
+// One kernel in two roles. In both a block holds 128 rows and walks the other side in tiles of 64, forming
 //   S = A1 B1^T,  dP = A2 B2^T,  P = exp(scale S - lse),  dS = P (dP - delta):
 //   queries: rows are queries, A1 = Q, A2 = dout, B1 = K, B2 = V:   dq = scale sum dS B1;
 //   keys:    rows are keys,    A1 = K, A2 = V, B1 = Q, B2 = dout:   dk = scale sum dS B1,  dv = sum P B2,
 //            over the queries of every head that shares the key head.
 // So each result is summed by one block in a fixed order, without atomics or a float32 copy in memory, at the
-// price of forming S and dP twice (7 products instead of 5); what bounds the kernel is the elementwise part
-// between the products, and atomics would add 32 KB of it per tile. lse and delta are known, so nothing is
-// rescaled and a tile's elements are independent of the others'.
+// price of forming S and dP twice (7 products instead of 5); atomics would add 32 KB to every tile's work. lse and delta
+// are known, so nothing is rescaled and a tile's elements are independent of the others'.
 //
 // float16: P is formed 2^15 times as large, and dS as many times (a power of two for each key head) as its bound
 // |dS| <= 2 scale max|dout| max|v| allows below the type's largest value; the sums are scaled back. Unscaled, the
 // small probabilities of long or peaked rows fell into the type's subnormal range (or, with large dout, out of it).
 //
 // Thread = row: a warpgroup turns a 128 x 64 tile of S and dP from tensor memory into dS and P, 16-bit in the
-// same columns, which feed the next products as their A operand there. Two warpgroups, each with columns of its own:
-// of two row tiles (kRows = 2), or of one with the walked tiles in turn. Products are issued by one thread, in an
-// order that does not depend on the timing.
+// same columns, which feed the next products as their A operand there; two warpgroups take the tiles in turn. A tile's way
+// (products, load, elementwise part, store, products) takes about 2200 cycles and its products 400 to 1300, so tensor
+// memory holds as many tiles as fit beside the sums: three (two for dk and dv of heads above 64). One thread
+// issues S and dP, another the sums, in the tiles' order.
+//
+// A product of 64 columns with both operands in shared memory takes 49 cycles, with A in tensor memory 33 (the
+// products' reads of shared memory bound it). Where columns are left (queries, heads of up to 64) Q and dout are moved there
+// first.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -25,17 +29,18 @@ namespace gs {
 
 template <int DP, bool KEYS>
 struct BwdShape {
-    // Row tiles: two where their accumulators fit beside 2 x 128 columns of S and dP.
-    static constexpr int kRows = KEYS && DP == 128 ? 1 : 2;
-    static constexpr int kA = DP * kTileRows * 2;       // bytes of one operand's row tile
+    static constexpr int kA = DP * kTileRows * 2;       // bytes of one operand's rows
     static constexpr int kB = DP * kBN * 2;             // bytes of one operand's walked tile
-    static constexpr int kStage = 2 * kB + 1024;        // with the tile's lse and delta (KEYS)
-    static constexpr int kRoom = (225 * 1024 - 1024 - 2 * kRows * kA) / kStage;
+    static constexpr int kStage = 2 * kB + 1024;        // with the tile's exponent offsets and deltas (KEYS)
+    static constexpr int kRoom = (225 * 1024 - 1024 - 2 * kA) / kStage;
     static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
-    static constexpr int kSmem = 2 * kRows * kA + kStages * kStage + 1024;
-    static constexpr int kAcc = 256;                    // first accumulator column
+    static constexpr int kSmem = 2 * kA + kStages * kStage + 1024;
     static constexpr int kAccs = KEYS ? 2 : 1;
-    static_assert(kAcc + kRows * kAccs * DP <= 512 && kStages >= (kRows == 1 ? 3 : 2));
+    static constexpr int kBuffers = KEYS && DP == 128 ? 2 : 3;  // walked tiles in tensor memory, 128 columns each
+    static constexpr int kAcc = kBuffers * 128;                 // first accumulator column
+    static constexpr bool kInTmem = !KEYS && DP == 64;          // the row operands, 32 columns each
+    static constexpr int kRowCol = kAcc + kAccs * DP;
+    static_assert(kRowCol + (kInTmem ? 64 : 0) <= 512 && kStages > kBuffers);
 };
 
 template <class T, int DP, bool KEYS>
@@ -43,16 +48,16 @@ __global__ void __launch_bounds__(384, 1)
     k_attn_bwd(const __grid_constant__ BwdArgs g, const __grid_constant__ TcTensor ta1, const __grid_constant__ TcTensor ta2,
                const __grid_constant__ TcTensor tb1, const __grid_constant__ TcTensor tb2) {
     using S = BwdShape<DP, KEYS>;
-    constexpr int kSt = S::kStages, kR = S::kRows;
+    constexpr int kSt = S::kStages, kNB = S::kBuffers;
     pdl_entry();
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t a_full, full[kSt], empty[kSt], s_full[2], p_full[2], done, drain;
+    __shared__ uint64_t a_full, a_moved, full[kSt], empty[kSt], s_full[kNB], p_full[kNB], b_free[kNB], done, drain[2];
     __shared__ uint32_t tmem_base;
     const TcArgs& t = g.t;
     const AttnArgs& a = t.a;
     unsigned char* base = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
-    const uint32_t sa1 = smem_u32(base), sa2 = sa1 + kR * S::kA, sb = sa2 + kR * S::kA;
-    auto stats = [&](int s) { return reinterpret_cast<float*>(base + 2 * kR * S::kA + s * S::kStage + 2 * S::kB); };
+    const uint32_t sa1 = smem_u32(base), sa2 = sa1 + S::kA, sb = sa2 + S::kA;
+    auto stats = [&](int s) { return reinterpret_cast<float*>(base + 2 * S::kA + s * S::kStage + 2 * S::kB); };
 
     int at = blockIdx.x;
     const int block = at % t.tiles;
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(384, 1)
     at /= t.splits;
     const int share = a.heads / a.kv_heads, row_heads = KEYS ? a.kv_heads : a.heads;
     const int h = at % row_heads, b = at / row_heads;
-    const int keys = keys_of(t, b), row0 = block * kR * kTileRows;
+    const int keys = keys_of(t, b), row0 = block * kTileRows;
     const int rows = KEYS ? keys : a.len_q;
     // walked tiles: of the keys, or of the queries of `share` heads one after the other
     const int per_head = KEYS ? (a.len_q + kBN - 1) / kBN : (keys + kBN - 1) / kBN;
@@ -72,16 +77,19 @@ __global__ void __launch_bounds__(384, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(&a_full, 1);
+        mbar_init(&a_moved, 8);
         for (int i = 0; i < kSt; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kNB; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+            mbar_init(&b_free[i], 1);
         }
         mbar_init(&done, 1);
-        mbar_init(&drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc<512>(&tmem_base);
@@ -92,12 +100,11 @@ __global__ void __launch_bounds__(384, 1)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int steps = (a.d + 15) / 16;
         if (warp == 8 && n > 0 && elect_one()) {  // copies
-            mbar_arrive_expect_tx(&a_full, 2 * kR * S::kA);
-            for (int i = 0; i < kR; ++i) {
-                load_rows<DP, 1, kTileRows>(sa1 + i * S::kA, ta1, row0 + i * kTileRows, b, h, row_heads, &a_full);
-                load_rows<DP, 1, kTileRows>(sa2 + i * S::kA, ta2, row0 + i * kTileRows, b, h, row_heads, &a_full);
-            }
+            mbar_arrive_expect_tx(&a_full, 2 * S::kA);
+            load_rows<DP, 1, kTileRows>(sa1, ta1, row0, b, h, row_heads, &a_full);
+            load_rows<DP, 1, kTileRows>(sa2, ta2, row0, b, h, row_heads, &a_full);
             int sent = 0;
             for (int j = 0; j < n; ++j) {
                 const int s = j % kSt, x = first + j;
@@ -116,60 +123,60 @@ __global__ void __launch_bounds__(384, 1)
             // every copy lands before the block ends, whatever became of its reader
             mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
             for (int j = max(0, sent - kSt); j < sent; ++j) mbar_wait_bounded(&full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
-        } else if (warp == 9 && n > 0 && elect_one()) {  // products
-            const int steps = (a.d + 15) / 16;
-            const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
-            auto wait = [&](uint64_t* bar, int k) { return mbar_wait_bounded(bar, k & 1, limit, a.err); };
-            // S and dP of walked tile j in warpgroup w's columns
-            auto scores = [&](int w, int j) {
-                const uint32_t row = (kR == 2 ? w : 0) * S::kA, tile = sb + (j % kSt) * S::kStage;
-                const uint32_t x1 = tile_desc(sa1 + row), x2 = tile_desc(sa2 + row), y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB);
+        } else if (warp == 9 && n > 0) {  // S and dP: the warp waits, one thread issues
+            const uint32_t s_desc = mma_desc<T>(kBN, false);
+            const uint32_t x1 = tile_desc(sa1), x2 = tile_desc(sa2);
+            bool ok = warp_wait(S::kInTmem ? &a_moved : &a_full, 0, limit, a.err);
+            for (int j = 0; j < n && ok; ++j) {
+                const int w = j % kNB, s = j % kSt;
+                if (!(ok = j < kNB ? warp_wait(&full[s], (j / kSt) & 1, limit, a.err)
+                                   : warp_wait_all(&full[s], j / kSt, &b_free[w], j / kNB - 1, limit, a.err)))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t tile = sb + s * S::kStage, y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB), d = tm + w * 128;
 #pragma unroll
-                for (int x = 0; x < DP / 16; ++x)
-                    if (x < steps)
-                        mma_ss(tm + w * 128, x1 + (x / 4) * kTileRows * 8 + (x % 4) * 2, y1 + (x / 4) * kBN * 8 + (x % 4) * 2, s_desc, x > 0);
+                    for (int which = 0; which < 2; ++which)
 #pragma unroll
-                for (int x = 0; x < DP / 16; ++x)
-                    if (x < steps)
-                        mma_ss(tm + w * 128 + 64, x2 + (x / 4) * kTileRows * 8 + (x % 4) * 2, y2 + (x / 4) * kBN * 8 + (x % 4) * 2, s_desc, x > 0);
-                mma_commit(&s_full[w]);
-            };
-            auto gradients = [&](int w, int j) {
-                const uint32_t acc = tm + S::kAcc + (kR == 2 ? w : 0) * S::kAccs * DP, tile = sb + (j % kSt) * S::kStage;
-                const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
-#pragma unroll
-                for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, tm + w * 128 + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
-                if (KEYS)
-#pragma unroll
-                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, tm + w * 128 + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
-                if (kR == 1 || w == 1) mma_commit(&empty[j % kSt]);
-            };
-            bool ok = wait(&a_full, 0);
-            for (int w = 0; w < 2 && ok; ++w) {
-                const int j = kR == 2 ? 0 : w;
-                if (j < n && (ok = wait(&full[j % kSt], j / kSt))) {
-                    tc_fence_after();
-                    scores(w, j);
+                        for (int x = 0; x < DP / 16; ++x) {
+                            if (x >= steps) continue;
+                            const uint32_t y = (which ? y2 : y1) + (x / 4) * kBN * 8 + (x % 4) * 2;
+                            if (S::kInTmem) mma_ts(d + which * 64, tm + S::kRowCol + which * 32 + x * 8, y, s_desc, x > 0);
+                            else mma_ss(d + which * 64, (which ? x2 : x1) + (x / 4) * kTileRows * 8 + (x % 4) * 2, y, s_desc, x > 0);
+                        }
+                    mma_commit(&s_full[w]);
                 }
             }
-            for (int j = 0; j < n && ok; ++j)
-                for (int w = kR == 2 ? 0 : j & 1; w < (kR == 2 ? 2 : (j & 1) + 1) && ok; ++w) {
-                    if (!(ok = wait(&p_full[w], kR == 2 ? j : j / 2))) break;
-                    tc_fence_after();
-                    gradients(w, j);
-                    const int next = kR == 2 ? j + 1 : j + 2;
-                    if (next < n && (ok = wait(&full[next % kSt], next / kSt))) scores(w, next);
+        } else if (warp == 10 && n > 0) {  // the sums
+            const uint32_t g_desc = mma_desc<T>(steps * 16, true);
+            for (int j = 0; j < n; ++j) {
+                const int w = j % kNB, s = j % kSt;
+                if (!warp_wait(&p_full[w], (j / kNB) & 1, limit, a.err)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t acc = tm + S::kAcc, tile = sb + s * S::kStage, buffer = tm + w * 128;
+                    const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
+#pragma unroll
+                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
+                    if (KEYS)
+#pragma unroll
+                        for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
+                    mma_commit(&b_free[w]);
+                    mma_commit(&empty[s]);
                 }
-            mma_commit(&done);
-            // no product is in flight when the tensor memory is freed
-            mma_commit(&drain);
-            mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
+            }
+            if (elect_one()) mma_commit(&done);
+        }
+        // no product is in flight when the tensor memory is freed
+        if ((warp == 9 || warp == 10) && n > 0 && elect_one()) {
+            mma_commit(&drain[warp - 9]);
+            mbar_wait_bounded(&drain[warp - 9], 0, kDrainLimit, a.err);
         }
     } else {  // elementwise: thread = row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int w = warp / 4;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tm + w * 128 + lanes;
-        const int row = row0 + (kR == 2 ? w * kTileRows : 0) + (threadIdx.x & 127);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const int row = row0 + (threadIdx.x & 127);
         const float c = a.scale * 1.4426950408889634f;
         const float2 factor = g.factor ? g.factor[b * a.kv_heads + (KEYS ? h : h / share)] : make_float2(g.ds_in, g.ds_out);
         const f32x2 c2 = f2_pack(c, c), i2 = f2_pack(factor.x, factor.x);
@@ -181,8 +188,25 @@ __global__ void __launch_bounds__(384, 1)
             d2 = f2_pack(d, d);
         }
         bool ok = true;
-        for (int j = kR == 2 ? 0 : w, k = 0; j < n; j += kR == 2 ? 1 : 2, ++k) {
-            ok = ok && warp_wait(&s_full[w], k & 1, limit, a.err);
+        if (S::kInTmem && n > 0) {
+            // a warpgroup per operand, the thread's row of it: 128 bytes, whose 16-byte pieces the copy's swizzle has exchanged
+            ok = warp_wait(&a_full, 0, limit, a.err);
+            const int r = threadIdx.x & 127;
+            const unsigned char* from = base + w * S::kA + r * 128;
+            uint32_t v[32];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint4 q = *reinterpret_cast<const uint4*>(from + ((x ^ (r & 7)) * 16));
+                v[4 * x] = q.x, v[4 * x + 1] = q.y, v[4 * x + 2] = q.z, v[4 * x + 3] = q.w;
+            }
+            tmem_st32(tm + S::kRowCol + w * 32 + lanes, v);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&a_moved);
+        }
+        for (int j = w; j < n; j += 2) {
+            const uint32_t ts = tm + j % kNB * 128 + lanes;
+            ok = ok && warp_wait(&s_full[j % kNB], (j / kNB) & 1, limit, a.err);
             if (!ok) break;  // the same in all lanes; nothing below waits for this warp without a limit
             tc_fence_after();
             uint32_t s[2][32], dp[2][32];
@@ -200,13 +224,16 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 uint32_t p[16], ds[16];
+                float4 l4, d4;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (KEYS) {  // columns are queries
-                        const float2 l = *reinterpret_cast<const float2*>(st + y * 32 + 2 * e);
-                        const float2 d = *reinterpret_cast<const float2*>(st + kBN + y * 32 + 2 * e);
-                        l2 = f2_pack(l.x, l.y);
-                        d2 = f2_pack(d.x, d.y);
+                        if (e % 2 == 0) {
+                            l4 = *reinterpret_cast<const float4*>(st + y * 32 + 2 * e);
+                            d4 = *reinterpret_cast<const float4*>(st + kBN + y * 32 + 2 * e);
+                        }
+                        l2 = e % 2 ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
+                        d2 = e % 2 ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
                     }
                     const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y][2 * e]), __uint_as_float(s[y][2 * e + 1])), c2, l2));
                     const float u0 = ex2_approx(z.x), u1 = ex2_approx(z.y);
@@ -232,60 +259,58 @@ __global__ void __launch_bounds__(384, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&p_full[w]);
+            warp_arrive(&p_full[j % kNB]);
         }
         if (n > 0) ok = warp_wait(&done, 0, limit, a.err) && ok;
         tc_fence_after();
-        // a row tile per warpgroup, or one with an accumulator each
+        // keys: a sum per warpgroup; queries: half of its columns
+        const int which = KEYS ? w : 0;  // 0: of dS B1, 1: of P B2
+        constexpr int kOut = KEYS ? DP : DP / 2;
+        const int col0 = KEYS ? 0 : w * kOut;
+        const uint32_t acc = tm + S::kAcc + lanes + which * DP + col0;
+        const float f = which == 0 ? factor.y : g.p_out;
+        const bool live = row < rows && ok;
+        const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
+        const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
+        T* dst = static_cast<T*>(out.data) + b * out.batch_stride + h * out.head_stride + to * out.len_stride;
+        const long long part_rows = KEYS ? g.rows_k : a.len_q, heads_all = (long long)a.batch * row_heads;
+        float* part = t.part ? t.part + ((((long long)split * S::kAccs + which) * heads_all + (long long)b * row_heads + h) * part_rows + row) * DP
+                             : nullptr;
+        const bool vec = a.d % 8 == 0 && out.batch_stride % 8 == 0 && out.head_stride % 8 == 0 && out.len_stride % 8 == 0 &&
+                         reinterpret_cast<uintptr_t>(out.data) % 16 == 0;
 #pragma unroll
-        for (int x = 0; x < (kR == 2 ? S::kAccs : 1); ++x) {
-            const int which = kR == 2 ? x : w;  // 0: of dS B1, 1: of P B2
-            const uint32_t acc = tm + S::kAcc + lanes + (kR == 2 ? w * S::kAccs * DP : 0) + which * DP;
-            const float f = which == 0 ? factor.y : g.p_out;
-            const bool live = row < rows && ok;
-            const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
-            const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
-            T* dst = static_cast<T*>(out.data) + b * out.batch_stride + h * out.head_stride + to * out.len_stride;
-            const long long part_rows = KEYS ? g.rows_k : a.len_q;
-            const long long heads_all = (long long)a.batch * row_heads;
-            float* part = t.part ? t.part + ((((long long)split * S::kAccs + which) * heads_all + (long long)b * row_heads + h) * part_rows + row) * DP
-                                 : nullptr;
-            const bool vec = a.d % 8 == 0 && out.batch_stride % 8 == 0 && out.head_stride % 8 == 0 && out.len_stride % 8 == 0 &&
-                             reinterpret_cast<uintptr_t>(out.data) % 16 == 0;
+        for (int y = 0; y < kOut / 32; ++y) {
+            uint32_t o[32];
 #pragma unroll
-            for (int y = 0; y < DP / 32; ++y) {
-                uint32_t o[32];
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+            if (n > 0) {
+                tmem_ld32(acc + y * 32, o);
+                tmem_wait_ld(o);
+            }
+            if (live) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0u;
-                if (n > 0) {
-                    tmem_ld32(acc + y * 32, o);
-                    tmem_wait_ld(o);
-                }
-                if (live) {
+                for (int e = 0; e < 32; e += 8) {
+                    const int col = col0 + y * 32 + e;
+                    if (part) {
+                        *reinterpret_cast<float4*>(part + col) = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                                                             __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                        *reinterpret_cast<float4*>(part + col + 4) = make_float4(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f,
+                                                                                 __uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
+                        continue;
+                    }
+                    Pack<T, 8> v;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        const int col = y * 32 + e;
-                        if (part) {
-                            *reinterpret_cast<float4*>(part + col) = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
-                                                                                 __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-                            *reinterpret_cast<float4*>(part + col + 4) = make_float4(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f,
-                                                                                     __uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
-                            continue;
-                        }
-                        Pack<T, 8> v;
+                    for (int k = 0; k < 8; ++k) v.v[k] = from_float<T>(__uint_as_float(o[e + k]) * f);
+                    if (vec) {
+                        if (col < a.d) *reinterpret_cast<Pack<T, 8>*>(dst + col) = v;
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v.v[k] = from_float<T>(__uint_as_float(o[e + k]) * f);
-                        if (vec) {
-                            if (col < a.d) *reinterpret_cast<Pack<T, 8>*>(dst + col) = v;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (col + k < a.d) dst[col + k] = v.v[k];
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            if (col + k < a.d) dst[col + k] = v.v[k];
                     }
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
         tc_fence_before();
     }
@@ -418,7 +443,7 @@ cudaError_t run(BwdArgs g, const TcTensor (&x)[4], cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e) return e;
     const int len = KEYS ? g.t.a.len_k : g.t.a.len_q;
-    g.t.tiles = (len + S::kRows * kTileRows - 1) / (S::kRows * kTileRows);
+    g.t.tiles = (len + kTileRows - 1) / kTileRows;
     const long long blocks = (long long)g.t.tiles * g.t.splits * (KEYS ? g.t.a.kv_heads : g.t.a.heads) * g.t.a.batch;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -440,9 +465,6 @@ cudaError_t by_type(int dtype, F&& f) {
 unsigned blocks_of(long long threads) { return (unsigned)((threads + 255) / 256); }
 
 }  // namespace
-
-int attn_bwd_rows(bool keys, int dp, int planes) { return (planes == 3 || (keys && dp == 128) ? 1 : 2) * kTileRows; }
-int attn_bwd_walk() { return kBN; }
 
 cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st) {
     count_launches(1);

@@ -84,9 +84,6 @@ struct BwdArgs {
 // The backward of three planes, heads of up to 64; x: the row operands, then the walked ones.
 cudaError_t launch_attn_bwd_wide(const BwdArgs& g, bool keys, const TcTensor (&x)[4], cudaStream_t st);
 
-// Rows per block of the backward kernel that sums dk and dv (keys) or dq, and per tile that it walks.
-int attn_bwd_rows(bool keys, int dp, int planes);
-int attn_bwd_walk();
 struct TcBwd {
     AttnArgs a;
     const int *count, *index;    // of the key mask, or NULL
