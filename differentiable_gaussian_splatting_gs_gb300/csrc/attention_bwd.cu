@@ -14,10 +14,10 @@
 // small probabilities of long or peaked rows fell into the type's subnormal range (or, with large dout, out of it).
 //
 // Thread = row: a warpgroup turns a 128 x 64 tile of S and dP from tensor memory into dS and P, 16-bit in the
-// same columns, which feed the next products as their A operand there; two warpgroups take the tiles in turn. A tile's way
-// (products, load, elementwise part, store, products) takes about 2200 cycles and its products 400 to 1300, so tensor
-// memory holds as many tiles as fit beside the sums: three (two for dk and dv of heads above 64). One thread
-// issues S and dP, another the sums, in the tiles' order.
+// same columns, which feed the next products as their A operand there. A tile's way (products, load, elementwise part,
+// store, products) takes about 2200 cycles and its products 400 to 1300, so tensor memory holds as many tiles as fit
+// beside the sums, three (two for dk and dv of heads above 64), each with a warpgroup of its own. One thread issues S and
+// dP, another the sums, in the tiles' order; with two tiles one thread issues both, since the next S follows the sums at once.
 //
 // A product of 64 columns with both operands in shared memory takes 49 cycles, with A in tensor memory 33 (the
 // products' reads of shared memory bound it). Where columns are left (queries, heads of up to 64) Q and dout are moved there
@@ -37,6 +37,11 @@ struct BwdShape {
     static constexpr int kSmem = 2 * kA + kStages * kStage + 1024;
     static constexpr int kAccs = KEYS ? 2 : 1;
     static constexpr int kBuffers = KEYS && DP == 128 ? 2 : 3;  // walked tiles in tensor memory, 128 columns each
+    static constexpr bool kOneIssuer = kBuffers == 2;
+    // a warpgroup per buffer and one that copies and issues. Registers are moved between them (setmaxnreg):
+    // 512 threads x 128 at launch = 384 x 144 + 128 x 80, or 384 x 168 = 256 x 216 + 128 x 72
+    static constexpr int kElem = kBuffers * 4;  // elementwise warps
+    static constexpr int kThreads = kElem * 32 + 128;
     static constexpr int kAcc = kBuffers * 128;                 // first accumulator column
     static constexpr bool kInTmem = !KEYS && DP == 64;          // the row operands, 32 columns each
     static constexpr int kRowCol = kAcc + kAccs * DP;
@@ -44,7 +49,7 @@ struct BwdShape {
 };
 
 template <class T, int DP, bool KEYS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
     k_attn_bwd(const __grid_constant__ BwdArgs g, const __grid_constant__ TcTensor ta1, const __grid_constant__ TcTensor ta2,
                const __grid_constant__ TcTensor tb1, const __grid_constant__ TcTensor tb2) {
     using S = BwdShape<DP, KEYS>;
@@ -92,16 +97,17 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(&drain[1], 1);
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc<512>(&tmem_base);
+    if (warp == S::kElem) tmem_alloc<512>(&tmem_base);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp >= S::kElem) {
+        if (kNB == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int steps = (a.d + 15) / 16;
-        if (warp == 8 && n > 0 && elect_one()) {  // copies
+        if (warp == S::kElem && n > 0 && elect_one()) {  // copies
             mbar_arrive_expect_tx(&a_full, 2 * S::kA);
             load_rows<DP, 1, kTileRows>(sa1, ta1, row0, b, h, row_heads, &a_full);
             load_rows<DP, 1, kTileRows>(sa2, ta2, row0, b, h, row_heads, &a_full);
@@ -123,57 +129,67 @@ __global__ void __launch_bounds__(384, 1)
             // every copy lands before the block ends, whatever became of its reader
             mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
             for (int j = max(0, sent - kSt); j < sent; ++j) mbar_wait_bounded(&full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
-        } else if (warp == 9 && n > 0) {  // S and dP: the warp waits, one thread issues
-            const uint32_t s_desc = mma_desc<T>(kBN, false);
+        } else if ((warp == S::kElem + 1 || warp == S::kElem + 2) && n > 0) {  // products: the warp waits, one thread issues
+            const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
             const uint32_t x1 = tile_desc(sa1), x2 = tile_desc(sa2);
-            bool ok = warp_wait(S::kInTmem ? &a_moved : &a_full, 0, limit, a.err);
-            for (int j = 0; j < n && ok; ++j) {
-                const int w = j % kNB, s = j % kSt;
-                if (!(ok = j < kNB ? warp_wait(&full[s], (j / kSt) & 1, limit, a.err)
-                                   : warp_wait_all(&full[s], j / kSt, &b_free[w], j / kNB - 1, limit, a.err)))
-                    break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t tile = sb + s * S::kStage, y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB), d = tm + w * 128;
+            auto scores = [&](int j) {
+                if (!elect_one()) return;
+                const uint32_t tile = sb + j % kSt * S::kStage, y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB), d = tm + j % kNB * 128;
 #pragma unroll
-                    for (int which = 0; which < 2; ++which)
+                for (int which = 0; which < 2; ++which)
 #pragma unroll
-                        for (int x = 0; x < DP / 16; ++x) {
-                            if (x >= steps) continue;
-                            const uint32_t y = (which ? y2 : y1) + (x / 4) * kBN * 8 + (x % 4) * 2;
-                            if (S::kInTmem) mma_ts(d + which * 64, tm + S::kRowCol + which * 32 + x * 8, y, s_desc, x > 0);
-                            else mma_ss(d + which * 64, (which ? x2 : x1) + (x / 4) * kTileRows * 8 + (x % 4) * 2, y, s_desc, x > 0);
-                        }
-                    mma_commit(&s_full[w]);
+                    for (int x = 0; x < DP / 16; ++x) {
+                        if (x >= steps) continue;
+                        const uint32_t y = (which ? y2 : y1) + (x / 4) * kBN * 8 + (x % 4) * 2;
+                        if (S::kInTmem) mma_ts(d + which * 64, tm + S::kRowCol + which * 32 + x * 8, y, s_desc, x > 0);
+                        else mma_ss(d + which * 64, (which ? x2 : x1) + (x / 4) * kTileRows * 8 + (x % 4) * 2, y, s_desc, x > 0);
+                    }
+                mma_commit(&s_full[j % kNB]);
+            };
+            auto sums = [&](int j) {
+                if (!elect_one()) return;
+                const uint32_t acc = tm + S::kAcc, tile = sb + j % kSt * S::kStage, buffer = tm + j % kNB * 128;
+                const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
+#pragma unroll
+                for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
+                if (KEYS)
+#pragma unroll
+                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
+                if (!S::kOneIssuer) mma_commit(&b_free[j % kNB]);
+                mma_commit(&empty[j % kSt]);
+            };
+            const bool does_s = warp == S::kElem + 1, does_g = S::kOneIssuer ? does_s : !does_s;
+            bool ok = !does_s || warp_wait(S::kInTmem ? &a_moved : &a_full, 0, limit, a.err);
+            if (does_s)
+                for (int j = 0; j < (S::kOneIssuer ? min(kNB, n) : n) && ok; ++j) {
+                    if (!(ok = j < kNB ? warp_wait(&full[j % kSt], (j / kSt) & 1, limit, a.err)
+                                       : warp_wait_all(&full[j % kSt], j / kSt, &b_free[j % kNB], j / kNB - 1, limit, a.err)))
+                        break;
+                    tc_fence_after();
+                    scores(j);
                 }
-            }
-        } else if (warp == 10 && n > 0) {  // the sums
-            const uint32_t g_desc = mma_desc<T>(steps * 16, true);
-            for (int j = 0; j < n; ++j) {
-                const int w = j % kNB, s = j % kSt;
-                if (!warp_wait(&p_full[w], (j / kNB) & 1, limit, a.err)) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t acc = tm + S::kAcc, tile = sb + s * S::kStage, buffer = tm + w * 128;
-                    const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
-#pragma unroll
-                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
-                    if (KEYS)
-#pragma unroll
-                        for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
-                    mma_commit(&b_free[w]);
-                    mma_commit(&empty[s]);
+            if (does_g) {
+                for (int j = 0; j < n && ok; ++j) {
+                    const int next = j + kNB;
+                    const bool more = S::kOneIssuer && next < n;
+                    if (!(ok = more ? warp_wait_all(&p_full[j % kNB], j / kNB, &full[next % kSt], next / kSt, limit, a.err)
+                                    : warp_wait(&p_full[j % kNB], (j / kNB) & 1, limit, a.err)))
+                        break;
+                    tc_fence_after();
+                    sums(j);
+                    if (more) scores(next);
                 }
+                if (elect_one()) mma_commit(&done);
             }
-            if (elect_one()) mma_commit(&done);
-        }
-        // no product is in flight when the tensor memory is freed
-        if ((warp == 9 || warp == 10) && n > 0 && elect_one()) {
-            mma_commit(&drain[warp - 9]);
-            mbar_wait_bounded(&drain[warp - 9], 0, kDrainLimit, a.err);
+            // no product is in flight when the tensor memory is freed
+            if (elect_one()) {
+                mma_commit(&drain[does_s]);
+                mbar_wait_bounded(&drain[does_s], 0, kDrainLimit, a.err);
+            }
         }
     } else {  // elementwise: thread = row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (kNB == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int w = warp / 4;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const int row = row0 + (threadIdx.x & 127);
@@ -188,7 +204,7 @@ __global__ void __launch_bounds__(384, 1)
             d2 = f2_pack(d, d);
         }
         bool ok = true;
-        if (S::kInTmem && n > 0) {
+        if (S::kInTmem && n > 0 && w < 2) {
             // a warpgroup per operand, the thread's row of it: 128 bytes, whose 16-byte pieces the copy's swizzle has exchanged
             ok = warp_wait(&a_full, 0, limit, a.err);
             const int r = threadIdx.x & 127;
@@ -204,26 +220,19 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_before();
             warp_arrive(&a_moved);
         }
-        for (int j = w; j < n; j += 2) {
-            const uint32_t ts = tm + j % kNB * 128 + lanes;
-            ok = ok && warp_wait(&s_full[j % kNB], (j / kNB) & 1, limit, a.err);
+        for (int j = w; j < n; j += kNB) {
+            const uint32_t ts = tm + w * 128 + lanes;
+            ok = ok && warp_wait(&s_full[w], (j / kNB) & 1, limit, a.err);
             if (!ok) break;  // the same in all lanes; nothing below waits for this warp without a limit
             tc_fence_after();
-            uint32_t s[2][32], dp[2][32];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                tmem_ld32(ts + y * 32, s[y]);
-                tmem_ld32(ts + 64 + y * 32, dp[y]);
-            }
             const float* st = stats(j % kSt);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                tmem_wait_ld(s[y]);
-                tmem_wait_ld(dp[y]);
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t p[16], ds[16];
+                uint32_t s[32], dp[32], p[16], ds[16];
+                tmem_ld32(ts + y * 32, s);
+                tmem_ld32(ts + 64 + y * 32, dp);
+                tmem_wait_ld(s);
+                tmem_wait_ld(dp);
                 float4 l4, d4;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -235,9 +244,9 @@ __global__ void __launch_bounds__(384, 1)
                         l2 = e % 2 ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
                         d2 = e % 2 ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
                     }
-                    const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y][2 * e]), __uint_as_float(s[y][2 * e + 1])), c2, l2));
+                    const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, l2));
                     const float u0 = ex2_approx(z.x), u1 = ex2_approx(z.y);
-                    const f32x2 x = f2_fma(f2_pack(__uint_as_float(dp[y][2 * e]), __uint_as_float(dp[y][2 * e + 1])), i2, d2);
+                    const f32x2 x = f2_fma(f2_pack(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), i2, d2);
                     const float2 v = f2_unpack(f2_mul(f2_pack(u0, u1), x));
                     if (KEYS) p[e] = pack2<T>(u0, u1);
                     ds[e] = pack2<T>(v.x, v.y);
@@ -259,17 +268,17 @@ __global__ void __launch_bounds__(384, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&p_full[j % kNB]);
+            warp_arrive(&p_full[w]);
         }
         if (n > 0) ok = warp_wait(&done, 0, limit, a.err) && ok;
         tc_fence_after();
-        // keys: a sum per warpgroup; queries: half of its columns
-        const int which = KEYS ? w : 0;  // 0: of dS B1, 1: of P B2
+        // of the first two warpgroups: a sum each for keys, half of its columns for queries
+        const int which = KEYS ? w & 1 : 0;  // 0: of dS B1, 1: of P B2
         constexpr int kOut = KEYS ? DP : DP / 2;
-        const int col0 = KEYS ? 0 : w * kOut;
+        const int col0 = KEYS ? 0 : (w & 1) * kOut;
         const uint32_t acc = tm + S::kAcc + lanes + which * DP + col0;
         const float f = which == 0 ? factor.y : g.p_out;
-        const bool live = row < rows && ok;
+        const bool live = row < rows && ok && w < 2;
         const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
         const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
         T* dst = static_cast<T*>(out.data) + b * out.batch_stride + h * out.head_stride + to * out.len_stride;
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_free<512>(tm);
+    if (warp == S::kElem) tmem_free<512>(tm);
 }
 
 // The largest squared norms of dout's and of v's rows of each batch entry and key head, as bits of floats (zero
@@ -448,7 +457,7 @@ cudaError_t run(BwdArgs g, const TcTensor (&x)[4], cudaStream_t st) {
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     count_launches(1);
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(384), S::kSmem, st, g, x[0], x[1], x[2], x[3]);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, st, g, x[0], x[1], x[2], x[3]);
 }
 
 template <class T>
