@@ -16,8 +16,9 @@
 // Thread = row: a warpgroup turns a 128 x 64 tile of S and dP from tensor memory into dS and P, 16-bit in the
 // same columns, which feed the next products as their A operand there. A tile's way (products, load, elementwise part,
 // store, products) takes about 2200 cycles and its products 400 to 1300, so tensor memory holds as many tiles as fit
-// beside the sums, three (two for dk and dv of heads above 64), each with a warpgroup of its own. One thread issues S and
-// dP, another the sums, in the tiles' order; with two tiles one thread issues both, since the next S follows the sums at once.
+// beside the sums, three (two for dk and dv of heads above 64), each with a warpgroup of its own. A thread each
+// issues S, dP and the sums, in the tiles' order (an issue takes 20 to 45 cycles, a commit 75); with two tiles one thread
+// issues all, since the next S follows the sums at once.
 //
 // A product of 64 columns with both operands in shared memory takes 49 cycles, with A in tensor memory 33 (the
 // products' reads of shared memory bound it). Where columns are left (queries, heads of up to 64) Q and dout are moved there
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
     constexpr int kSt = S::kStages, kNB = S::kBuffers;
     pdl_entry();
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t a_full, a_moved, full[kSt], empty[kSt], s_full[kNB], p_full[kNB], b_free[kNB], done, drain[2];
+    __shared__ uint64_t a_full, a_moved, full[kSt], empty[kSt], s_full[kNB], p_full[kNB], b_free[kNB], done, drain[3];
     __shared__ uint32_t tmem_base;
     const TcArgs& t = g.t;
     const AttnArgs& a = t.a;
@@ -88,13 +89,14 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kNB; ++i) {
-            mbar_init(&s_full[i], 1);
+            mbar_init(&s_full[i], S::kOneIssuer ? 1 : 2);
             mbar_init(&p_full[i], 4);
             mbar_init(&b_free[i], 1);
         }
         mbar_init(&done, 1);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
+        mbar_init(&drain[2], 1);
         fence_mbar_init();
     }
     if (warp == S::kElem) tmem_alloc<512>(&tmem_base);
@@ -129,21 +131,29 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
             // every copy lands before the block ends, whatever became of its reader
             mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
             for (int j = max(0, sent - kSt); j < sent; ++j) mbar_wait_bounded(&full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
-        } else if ((warp == S::kElem + 1 || warp == S::kElem + 2) && n > 0) {  // products: the warp waits, one thread issues
+        } else if (warp > S::kElem && (!S::kOneIssuer || warp == S::kElem + 1) && n > 0) {  // products: the warp waits, one thread issues
             const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
-            const uint32_t x1 = tile_desc(sa1), x2 = tile_desc(sa2);
+            const int me = warp - S::kElem - 1;  // 0: S (and all with one issuer), 1: dP, 2: the sums
+            // S or dP of walked tile j
+            auto product = [&](int j, int which) {
+                const uint32_t tile = sb + j % kSt * S::kStage, d = tm + j % kNB * 128 + which * 64;
+                const uint32_t r = tile_desc(which ? sa2 : sa1), y = tile_desc(tile + which * S::kB);
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x) {
+                    if (x >= steps) continue;
+                    const uint32_t yx = y + (x / 4) * kBN * 8 + (x % 4) * 2;
+                    if (S::kInTmem) mma_ts(d, tm + S::kRowCol + which * 32 + x * 8, yx, s_desc, x > 0);
+                    else mma_ss(d, r + (x / 4) * kTileRows * 8 + (x % 4) * 2, yx, s_desc, x > 0);
+                }
+            };
             auto scores = [&](int j) {
                 if (!elect_one()) return;
-                const uint32_t tile = sb + j % kSt * S::kStage, y1 = tile_desc(tile), y2 = tile_desc(tile + S::kB), d = tm + j % kNB * 128;
-#pragma unroll
-                for (int which = 0; which < 2; ++which)
-#pragma unroll
-                    for (int x = 0; x < DP / 16; ++x) {
-                        if (x >= steps) continue;
-                        const uint32_t y = (which ? y2 : y1) + (x / 4) * kBN * 8 + (x % 4) * 2;
-                        if (S::kInTmem) mma_ts(d + which * 64, tm + S::kRowCol + which * 32 + x * 8, y, s_desc, x > 0);
-                        else mma_ss(d + which * 64, (which ? x2 : x1) + (x / 4) * kTileRows * 8 + (x % 4) * 2, y, s_desc, x > 0);
-                    }
+                if (S::kOneIssuer) {
+                    product(j, 0);
+                    product(j, 1);
+                } else {
+                    product(j, me);
+                }
                 mma_commit(&s_full[j % kNB]);
             };
             auto sums = [&](int j) {
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
                 if (!S::kOneIssuer) mma_commit(&b_free[j % kNB]);
                 mma_commit(&empty[j % kSt]);
             };
-            const bool does_s = warp == S::kElem + 1, does_g = S::kOneIssuer ? does_s : !does_s;
+            const bool does_s = me < 2, does_g = S::kOneIssuer || me == 2;
             bool ok = !does_s || warp_wait(S::kInTmem ? &a_moved : &a_full, 0, limit, a.err);
             if (does_s)
                 for (int j = 0; j < (S::kOneIssuer ? min(kNB, n) : n) && ok; ++j) {
@@ -183,8 +193,8 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
             }
             // no product is in flight when the tensor memory is freed
             if (elect_one()) {
-                mma_commit(&drain[does_s]);
-                mbar_wait_bounded(&drain[does_s], 0, kDrainLimit, a.err);
+                mma_commit(&drain[me]);
+                mbar_wait_bounded(&drain[me], 0, kDrainLimit, a.err);
             }
         }
     } else {  // elementwise: thread = row

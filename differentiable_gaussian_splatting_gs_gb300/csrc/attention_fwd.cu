@@ -44,7 +44,8 @@ struct FwdShape {
     static constexpr bool kRegO = PL == 3;
     static constexpr int kO = NQ * kP;                              // first column of O
     // two query tiles: a third warpgroup of which two or three warps work, so that registers can be moved between whole
-    // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 216 + 128 x 72
+    // warpgroups (setmaxnreg): 384 threads x 168 at launch = 256 x 216 + 128 x 72,
+    // or 256 x 200 + 128 x 104 with six products to issue for one
     static constexpr int kThreads = NQ == 2 ? 384 : 224;
     static constexpr int kCols = kO + NQ * DP <= 256 ? 256 : 512;
     static_assert(kO + NQ * DP <= 512 && kStages >= 1);
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     const uint32_t tm = tmem_base;
 
     if (warp >= NQ * 4) {
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (NQ == 2 && PL == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (NQ == 2 && PL == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == NQ * 4) {  // copies
             if (n > 0 && elect_one()) {
                 bool ok = true;
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             }
         }
     } else {  // softmax: thread = query
-        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (NQ == 2 && PL == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (NQ == 2 && PL == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ti = tm + i * S::kP + lanes,
                        to = tm + S::kO + i * DP + lanes;
