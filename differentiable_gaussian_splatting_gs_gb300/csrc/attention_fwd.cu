@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 if (!S::kTurns) second_half();
 #pragma unroll
                 for (int g = G / 2; g < G; ++g) probabilities(x[g], g, b2, s2);
-                const bool far = total(s2) > 4096.f;
+                // (a row whose scores were all -inf has no maximum in use: it is looked for too)
+                const bool far = total(s2) > 4096.f || top == -INFINITY;
                 if (__any_sync(0xffffffffu, far)) {
                     const float m = find_max();
                     const float keep = far ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;

@@ -1,9 +1,9 @@
 // Cross attention on the float32 pipes, for what the tensor-core kernels do not take: head dimensions
-// above 128. Every element type, stride, mask and length; products and sums in float32.
+// above 128, and the backward of float32 heads above 64. Every stride, mask and length; products and sums in float32.
 //
 // Forward: a block of 256 threads per 64 queries of a head. It walks the keys in tiles of 64 with the
-// running maximum and sum of the softmax, so scores stay on chip. Backward: one kernel per 32 keys
-// (dk, dv; walks the queries of all heads that share the key head) and one per 32 queries (dq; walks
+// running maximum and sum of the softmax, so scores stay on chip. Backward: one kernel per 64 (heads above 128: 32) keys
+// (dk, dv; walks the queries of all heads that share the key head) and one per as many queries (dq; walks
 // the keys). Each output is summed by one block in a fixed order: no atomics, the same bits every time,
 // at the price of forming S and dP twice.
 #include "attention.cuh"
@@ -12,7 +12,10 @@ namespace gs {
 
 namespace {
 
-constexpr int kFM = 64, kFN = 64, kBM = 32;  // tiles of the forward and the backward kernels
+constexpr int kFM = 64, kFN = 64;  // tile of the forward kernel
+// side of the backward kernels' tile: four operands' rows and two tiles of gradients share shared memory
+template <int DP>
+constexpr int kSide = DP <= 128 ? 64 : 32;
 constexpr int kThreads = 256;
 
 // rows x DP floats of shared memory (row stride DP + 4) from rows first .. of a head's tensor; rows that
@@ -20,10 +23,23 @@ constexpr int kThreads = 256;
 template <class T, int DP, int ROWS, bool KEYS>
 __device__ __forceinline__ void stage(float* dst, const AttnTensor& t, const AttnArgs& a, int b, int h, int first, int len) {
     const T* src = head_base<T>(t, b, h);
-    for (int e = threadIdx.x; e < ROWS * DP; e += kThreads) {
-        const int r = e / DP, c = e % DP, row = first + r;
-        const bool in = c < a.d && (KEYS ? key_valid(a, b, row, len) : row < len);
-        dst[r * (DP + 4) + c] = in ? to_float(src[row * t.len_stride + c]) : 0.f;
+    constexpr int kBatch = 16;  // loads under way together
+    static_assert(ROWS * DP % (kBatch * kThreads) == 0);
+#pragma unroll 1
+    for (int e0 = threadIdx.x; e0 < ROWS * DP; e0 += kBatch * kThreads) {
+        float v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int e = e0 + u * kThreads, c = e % DP, row = first + e / DP;
+            const bool in = c < a.d && (KEYS ? key_valid(a, b, row, len) : row < len);
+            v[u] = 0.f;
+            if (in) v[u] = to_float(src[row * t.len_stride + c]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int e = e0 + u * kThreads;
+            dst[e / DP * (DP + 4) + e % DP] = v[u];
+        }
     }
 }
 
@@ -52,16 +68,20 @@ __device__ __forceinline__ void dots(const float* x, const float* y, int ty, int
 // acc[i][m] += sum over n of p[ty * R + i][n] y[n][tx + 16 m] (p: row stride N + 4; y: DP + 4)
 template <int DP, int N, int R>
 __device__ __forceinline__ void accumulate(const float* p, const float* y, int ty, int tx, float (&acc)[R][DP / 16]) {
-    for (int n = 0; n < N; ++n) {
-        float u[R];
+#pragma unroll 1
+    for (int n0 = 0; n0 < N; n0 += 4) {
+        float4 u[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) u[i] = p[(ty * R + i) * (N + 4) + n];
+        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4*>(p + (ty * R + i) * (N + 4) + n0);
 #pragma unroll
-        for (int m = 0; m < DP / 16; ++m) {
-            const float v = y[n * (DP + 4) + tx + 16 * m];
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int i = 0; i < R; ++i) acc[i][m] = fmaf(u[i], v, acc[i][m]);
-        }
+            for (int m = 0; m < DP / 16; ++m) {
+                const float v = y[(n0 + k) * (DP + 4) + tx + 16 * m];
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    acc[i][m] = fmaf(k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w, v, acc[i][m]);
+            }
     }
 }
 
@@ -151,23 +171,24 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, in
     store_rows<T, DP>(a.out, a.d, w.b, w.h, w.tile * kFM, a.len_q, ty, tx, o, f);
 }
 
-// P and dS of a 32 x 32 tile (queries x keys, or transposed for the dk/dv kernel) into shared memory.
+// P and dS of a square tile (queries x keys, or transposed for the dk/dv kernel) into shared memory.
 template <int DP, bool T_>
 __device__ __forceinline__ void tile_gradient(const AttnArgs& a, const float* sq, const float* sdo, const float* sk, const float* sv,
                                               float* sp, float* sds, const float* lse, const float* delta, int b, int q0,
                                               int n0, int len, int ty, int tx) {
-    float s[2][2], dp[2][2];
+    constexpr int M = kSide<DP>, R = M / 16;
+    float s[R][R], dp[R][R];
     dots<DP>(T_ ? sk : sq, T_ ? sq : sk, ty, tx, s);
     dots<DP>(T_ ? sv : sdo, T_ ? sdo : sv, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = ty * 2 + i, c = tx + 16 * j, qi = q0 + (T_ ? c : r), n = n0 + (T_ ? r : c);
+        for (int j = 0; j < R; ++j) {
+            const int r = ty * R + i, c = tx + 16 * j, qi = q0 + (T_ ? c : r), n = n0 + (T_ ? r : c);
             const bool in = qi < a.len_q && key_valid(a, b, n, len);
             const float p = in ? expf(s[i][j] * a.scale - lse[qi]) : 0.f;
-            if (T_) sp[r * (kBM + 4) + c] = p;
-            sds[r * (kBM + 4) + c] = in ? p * (dp[i][j] - delta[qi]) * a.scale : 0.f;
+            if (T_) sp[r * (M + 4) + c] = p;
+            sds[r * (M + 4) + c] = in ? p * (dp[i][j] - delta[qi]) * a.scale : 0.f;
         }
 }
 
@@ -175,30 +196,32 @@ template <class T, int DP>
 __global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, int tiles) {
     pdl_entry();
     extern __shared__ float sm[];
-    constexpr int kRow = kBM * (DP + 4);
-    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + kBM * (kBM + 4);
+    constexpr int M = kSide<DP>, R = M / 16, kRow = M * (DP + 4);
+    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + M * (M + 4);
     const Where w = where(tiles, a.kv_heads);
-    const int share = a.heads / a.kv_heads, ty = threadIdx.x / 16, tx = threadIdx.x % 16, n0 = w.tile * kBM;
+    const int share = a.heads / a.kv_heads, ty = threadIdx.x / 16, tx = threadIdx.x % 16, n0 = w.tile * M;
     const int len = key_count(a, w.b);
-    float dk[2][DP / 16] = {}, dv[2][DP / 16] = {};
+    float dk[R][DP / 16] = {}, dv[R][DP / 16] = {};
     if (n0 < len) {
-        stage<T, DP, kBM, true>(sk, a.k, a, w.b, w.h, n0, len);
-        stage<T, DP, kBM, true>(sv, a.v, a, w.b, w.h, n0, len);
+        stage<T, DP, M, true>(sk, a.k, a, w.b, w.h, n0, len);
+        stage<T, DP, M, true>(sv, a.v, a, w.b, w.h, n0, len);
         for (int h = w.h * share; h < (w.h + 1) * share; ++h) {
             const long long row = ((long long)w.b * a.heads + h) * a.len_q;
-            for (int q0 = 0; q0 < a.len_q; q0 += kBM) {
+            for (int q0 = 0; q0 < a.len_q; q0 += M) {
                 __syncthreads();
-                stage<T, DP, kBM, false>(sq, a.q, a, w.b, h, q0, a.len_q);
-                stage<T, DP, kBM, false>(sdo, a.dout, a, w.b, h, q0, a.len_q);
+                stage<T, DP, M, false>(sq, a.q, a, w.b, h, q0, a.len_q);
+                stage<T, DP, M, false>(sdo, a.dout, a, w.b, h, q0, a.len_q);
                 __syncthreads();
                 tile_gradient<DP, true>(a, sq, sdo, sk, sv, sp, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
                 __syncwarp();
-                accumulate<DP, kBM>(sp, sdo, ty, tx, dv);
-                accumulate<DP, kBM>(sds, sq, ty, tx, dk);
+                accumulate<DP, M>(sp, sdo, ty, tx, dv);
+                accumulate<DP, M>(sds, sq, ty, tx, dk);
             }
         }
     }
-    const float one[2] = {1.f, 1.f};
+    float one[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) one[i] = 1.f;
     store_rows<T, DP>(a.dk, a.d, w.b, w.h, n0, a.len_k, ty, tx, dk, one);
     store_rows<T, DP>(a.dv, a.d, w.b, w.h, n0, a.len_k, ty, tx, dv, one);
 }
@@ -207,25 +230,27 @@ template <class T, int DP>
 __global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int tiles) {
     pdl_entry();
     extern __shared__ float sm[];
-    constexpr int kRow = kBM * (DP + 4);
+    constexpr int M = kSide<DP>, R = M / 16, kRow = M * (DP + 4);
     float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sds = sdo + kRow;
     const Where w = where(tiles, a.heads);
-    const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16, q0 = w.tile * kBM;
+    const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16, q0 = w.tile * M;
     const int len = key_count(a, w.b);
     const long long row = ((long long)w.b * a.heads + w.h) * a.len_q;
-    stage<T, DP, kBM, false>(sq, a.q, a, w.b, w.h, q0, a.len_q);
-    stage<T, DP, kBM, false>(sdo, a.dout, a, w.b, w.h, q0, a.len_q);
-    float dq[2][DP / 16] = {};
-    for (int n0 = 0; n0 < len; n0 += kBM) {
+    stage<T, DP, M, false>(sq, a.q, a, w.b, w.h, q0, a.len_q);
+    stage<T, DP, M, false>(sdo, a.dout, a, w.b, w.h, q0, a.len_q);
+    float dq[R][DP / 16] = {};
+    for (int n0 = 0; n0 < len; n0 += M) {
         __syncthreads();
-        stage<T, DP, kBM, true>(sk, a.k, a, w.b, hk, n0, len);
-        stage<T, DP, kBM, true>(sv, a.v, a, w.b, hk, n0, len);
+        stage<T, DP, M, true>(sk, a.k, a, w.b, hk, n0, len);
+        stage<T, DP, M, true>(sv, a.v, a, w.b, hk, n0, len);
         __syncthreads();
         tile_gradient<DP, false>(a, sq, sdo, sk, sv, nullptr, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
         __syncwarp();
-        accumulate<DP, kBM>(sds, sk, ty, tx, dq);
+        accumulate<DP, M>(sds, sk, ty, tx, dq);
     }
-    const float one[2] = {1.f, 1.f};
+    float one[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) one[i] = 1.f;
     store_rows<T, DP>(a.dq, a.d, w.b, w.h, q0, a.len_q, ty, tx, dq, one);
 }
 
@@ -270,14 +295,15 @@ cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
 
 template <class T, int DP>
 cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (4 * kBM * (DP + 4) + 2 * kBM * (kBM + 4));
-    cudaError_t e = launch_tiles(k_attn_dq_simt<T, DP>, a, a.len_q, kBM, a.heads, smem, st);
-    return e ? e : launch_tiles(k_attn_dkv_simt<T, DP>, a, a.len_k, kBM, a.kv_heads, smem, st);
+    constexpr int M = kSide<DP>;
+    const size_t smem = sizeof(float) * (4 * M * (DP + 4) + 2 * M * (M + 4));
+    cudaError_t e = launch_tiles(k_attn_dq_simt<T, DP>, a, a.len_q, M, a.heads, smem, st);
+    return e ? e : launch_tiles(k_attn_dkv_simt<T, DP>, a, a.len_k, M, a.kv_heads, smem, st);
 }
 
+// What comes here: 16-bit heads above 128, any head without a key, and in the backward float32 heads above 64.
 template <class T>
 cudaError_t typed(const AttnArgs& a, bool backward, cudaStream_t st) {
-    if (a.d <= 32) return backward ? bwd<T, 32>(a, st) : fwd<T, 32>(a, st);
     if (a.d <= 64) return backward ? bwd<T, 64>(a, st) : fwd<T, 64>(a, st);
     if (a.d <= 128) return backward ? bwd<T, 128>(a, st) : fwd<T, 128>(a, st);
     return backward ? bwd<T, 256>(a, st) : fwd<T, 256>(a, st);
