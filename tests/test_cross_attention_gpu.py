@@ -262,3 +262,53 @@ def test_refusals():
     with pytest.raises(_abi.GsError, match="head_dim"):
         t = torch.zeros(1, 2, 2, 300, device=DEV)
         fwd(t, t, t)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lq", [1, 200])
+def test_scores_of_minus_infinity_before_very_low_ones(dtype, lq):
+    # the first keys' scores are -inf, the others' around -500: these alone make the result
+    q, k, v = _qkv(1, lq, 400, 2, 2, 64, dtype, 7)
+    q, k = q.abs() + 0.25, torch.zeros_like(k)
+    k[:, :150, :, 3] = -float("inf")
+    k[:, 150:, :, 5] = torch.linspace(-4000, -4100, 250, device=DEV).to(dtype)[None, :, None]
+    out, lse = api.gs_cross_attention_fwd(q, k, v)
+    r = decoder.attention_fwd(_np(q), _np(k[:, 150:]), _np(v[:, 150:]), np.ones((1, 250), bool), 0.125)
+    size = r["size"].transpose(0, 2, 1)[..., None]
+    tol = (2 * U[dtype] + ACC + 2 * ACC * size) * r["mag"] + U[dtype] * np.abs(r["out"]) + TINY[dtype]
+    assert (np.abs(_np(out) - r["out"]) <= tol).all()
+    assert (np.abs(_np(lse) - r["lse"]) <= ACC * (1 + r["size"] + np.abs(r["lse"]))).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.float16, 128), (torch.float32, 64)])
+def test_waits_that_give_up_are_reported_and_leave_the_context_usable(dtype, d):
+    import ctypes as C
+
+    q, k, v = _qkv(1, 400, 2000, 2, 2, d, dtype)
+    dout = _rand(q.shape, dtype, 5)
+    want = api.gs_cross_attention_fwd(q, k, v)
+    grads = api.gs_cross_attention_bwd(dout, q, k, v, *want)
+    a, qs, kvs, key = api._attention(q, k, None, None, None, "test")
+    a.spin_limit = 1  # every wait gives up at its first poll
+    lib, stream = _abi.load(), torch.cuda.current_stream().cuda_stream
+    out, lse = torch.empty_like(q), torch.empty_like(want[1])
+    spare = [torch.empty_like(t) for t in (q, k, v)]
+
+    def heads(*ts):
+        return [C.byref(api._heads(t, t.shape, dtype, q.device, "test")) for t in ts]
+
+    for backward in (0, 1):
+        need = api._attention_workspace_bytes(backward, *key)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
+        if backward:
+            st = lib.gs_cross_attention_bwd(C.byref(a), *heads(dout, q, k, v, want[0]), want[1].data_ptr(), *heads(*spare),
+                                            ws.data_ptr(), need, stream)
+        else:
+            st = lib.gs_cross_attention_fwd(C.byref(a), *heads(q, k, v, out), lse.data_ptr(), ws.data_ptr(), need, stream)
+        assert st == _abi.GS_OK  # enqueued
+        assert api.gs_device_error() == _abi.GS_ERR_TIMEOUT
+        assert api.gs_device_error() == _abi.GS_OK
+    again = api.gs_cross_attention_fwd(q, k, v)
+    assert all(torch.equal(x, y) for x, y in zip(again, want))
+    assert all(torch.equal(x, y) for x, y in zip(api.gs_cross_attention_bwd(dout, q, k, v, *again), grads))
+    assert api.gs_device_error() == _abi.GS_OK
