@@ -456,7 +456,7 @@ def _alloc(shape, like, stream, dtype=None):
 def _rows(t, like, where: str):
     """(rows, row stride) of a tensor of like's shape, dtype and device whose last dimension is contiguous and whose
     other dimensions have one common stride."""
-    if t is not like and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if t is not like and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{where}: a tensor of shape {tuple(like.shape)}, {like.dtype}, {like.device} is needed")
     shape = t.shape
     if shape and t.is_contiguous():
@@ -473,14 +473,18 @@ def _rows(t, like, where: str):
     return t.numel() // shape[-1], dims[-1][1]
 
 
+def _address(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
 def _vector(t, like, where: str):
-    if t is not None and (t.dim() != 1 or t.shape[0] != like.shape[-1] or not t.is_contiguous() or t.device != like.device or
+    if t is not None and (t.shape != like.shape[-1:] or not t.is_contiguous() or t.get_device() != like.get_device() or
                           (t.dtype is not like.dtype and t.dtype is not torch.float32)):
         raise ValueError(f"{where}: weight and bias must be contiguous [{like.shape[-1]}] tensors of x's dtype or float32")
 
 
 def _floats(t, shape, like, where: str):
-    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or t.device != like.device:
+    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{where}: a contiguous float32 tensor of shape {tuple(shape)} on {like.device} is needed")
 
 
@@ -503,8 +507,9 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, st
         ys = _rows(y, x, where)[1]
         _floats(mean, (rows,), x, where)
         _floats(rstd, (rows,), x, where)
-    check(_call(x, stream, _abi.load().gs_layer_norm_fwd, _ptr(x), xs, rows, x.shape[-1], dtype, _ptr(weight), _ptr(bias),
-                dtype if given is None else DTYPES[given.dtype], eps, _ptr(y), ys, _ptr(mean), _ptr(rstd)), where)
+    check(_call(x, stream, _abi.load().gs_layer_norm_fwd, x.data_ptr(), xs, rows, x.shape[-1], dtype, _address(weight),
+                _address(bias), dtype if given is None else DTYPES[given.dtype], eps, y.data_ptr(), ys, mean.data_ptr(),
+                rstd.data_ptr()), where)
     return y, mean, rstd
 
 
@@ -539,20 +544,20 @@ def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, 
     need = _norm_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = _alloc((need,), x, stream, torch.uint8)
-    check(_call(x, stream, _abi.load().gs_layer_norm_bwd, _ptr(dy), _rows(dy, x, where)[1], _ptr(x), xs, rows, cols, dtype,
-                _ptr(mean), _ptr(rstd), _ptr(weight), dtype if kind is None else DTYPES[kind.dtype], _ptr(dx), dxs,
-                _ptr(dweight), _ptr(dbias), _ptr(workspace) if need else None, need), where)
+    check(_call(x, stream, _abi.load().gs_layer_norm_bwd, dy.data_ptr(), _rows(dy, x, where)[1], x.data_ptr(), xs, rows, cols,
+                dtype, mean.data_ptr(), rstd.data_ptr(), _address(weight), dtype if kind is None else DTYPES[kind.dtype],
+                dx.data_ptr(), dxs, _address(dweight), _address(dbias), _address(workspace) if need else None, need), where)
     return dx, dweight, dbias
 
 
-def _heads(t, shape, dtype, device, where: str) -> _abi.gs_heads:
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {dtype}, {device} is needed, "
+def _heads(t, shape, dtype, device: int, where: str) -> _abi.gs_heads:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {dtype}, on cuda:{device} is needed, "
                          f"got {tuple(t.shape)}, {t.dtype}, {t.device}")
     b, n, h, d = t.stride()
     if d != 1 and shape[3] > 1:
         raise ValueError(f"{where}: the elements of a head must be contiguous")
-    return _abi.gs_heads(t.data_ptr() or _ptr(t), b, n, h)
+    return _abi.gs_heads(t.data_ptr(), b, n, h)
 
 
 def _attention(q, k, k_len, key_mask, scale, where: str):
@@ -572,9 +577,9 @@ def _attention(q, k, k_len, key_mask, scale, where: str):
         raise ValueError(f"{where}: key_mask must be a bool or uint8 [{b}, {lk}] tensor on {device} with contiguous rows")
     if scale is not None and not scale > 0:
         raise ValueError(f"{where}: scale must be positive")
-    a = _abi.gs_attention(code, b, h, hk, d, lq, lk, scale or 0.0, _ptr(k_len), _ptr(key_mask),
+    a = _abi.gs_attention(code, b, h, hk, d, lq, lk, scale or 0.0, _address(k_len), _address(key_mask),
                           0 if key_mask is None else key_mask.stride(0))
-    return a, (b, lq, h, d), (b, lk, hk, d), (device.index, code, b, h, hk, d, lq, lk, k_len is not None, key_mask is not None)
+    return a, (b, lq, h, d), (b, lk, hk, d), (q.get_device(), code, b, h, hk, d, lq, lk, k_len is not None, key_mask is not None)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -604,7 +609,7 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     k_len: int32 [batch], keys that count per batch entry; key_mask: bool [batch, len_k], True where a key
     counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a byte
     tensor kept by the caller (allocated when None or too small)."""
-    where, dtype, device = "gs_cross_attention_fwd", q.dtype, q.device
+    where, dtype, device = "gs_cross_attention_fwd", q.dtype, q.get_device()
     a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
     hq, hk, hv = _heads(q, qs, dtype, device, where), _heads(k, kvs, dtype, device, where), _heads(v, kvs, dtype, device, where)
     stats = (qs[0], qs[2], qs[1])
@@ -616,14 +621,14 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     ho = _heads(o, qs, dtype, device, where)
     workspace, need = _attention_workspace(key, 0, workspace, q, stream)
     check(_call(q, stream, _abi.load().gs_cross_attention_fwd, C.byref(a), C.byref(hq), C.byref(hk), C.byref(hv), C.byref(ho),
-                _ptr(lse), workspace.data_ptr() if need else None, need), where)
+                lse.data_ptr(), workspace.data_ptr() if need else None, need), where)
     return o, lse
 
 
 def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, scale: float | None = None, grads=None,
                            workspace=None, stream=None):
     """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given."""
-    where, dtype, device = "gs_cross_attention_bwd", q.dtype, q.device
+    where, dtype, device = "gs_cross_attention_bwd", q.dtype, q.get_device()
     a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
     ins = [_heads(t, s, dtype, device, where) for t, s in ((dout, qs), (q, qs), (k, kvs), (v, kvs), (out, qs))]
     _floats(lse, (qs[0], qs[2], qs[1]), q, where)
@@ -631,7 +636,7 @@ def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, s
         grads = (_alloc(qs, q, stream), _alloc(kvs, q, stream), _alloc(kvs, q, stream))
     outs = [_heads(t, s, dtype, device, where) for t, s in zip(grads, (qs, kvs, kvs))]
     workspace, need = _attention_workspace(key, 1, workspace, q, stream)
-    check(_call(q, stream, _abi.load().gs_cross_attention_bwd, C.byref(a), *map(C.byref, ins), _ptr(lse), *map(C.byref, outs),
+    check(_call(q, stream, _abi.load().gs_cross_attention_bwd, C.byref(a), *map(C.byref, ins), lse.data_ptr(), *map(C.byref, outs),
                 workspace.data_ptr() if need else None, need), where)
     return tuple(grads)
 

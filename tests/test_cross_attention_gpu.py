@@ -295,7 +295,7 @@ def test_waits_that_give_up_are_reported_and_leave_the_context_usable(dtype, d):
     spare = [torch.empty_like(t) for t in (q, k, v)]
 
     def heads(*ts):
-        return [C.byref(api._heads(t, t.shape, dtype, q.device, "test")) for t in ts]
+        return [C.byref(api._heads(t, t.shape, dtype, q.get_device(), "test")) for t in ts]
 
     for backward in (0, 1):
         need = api._attention_workspace_bytes(backward, *key)
