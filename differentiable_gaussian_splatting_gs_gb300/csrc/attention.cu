@@ -156,16 +156,15 @@ cudaError_t lay_out(const Plan& p, const AttnArgs& a, char* ws, int*& count, int
         index = reinterpret_cast<int*>(ws + p.index);
         if ((e = launch_attn_index(a, count, index, st))) return e;
     }
-    auto queries = [&](const AttnTensor& t, size_t at) {
-        return launch_attn_pack(a, t, a.heads, a.len_q, false, nullptr, nullptr, p.planes, p.dp, a.len_q, ws + at, st);
-    };
-    auto keys = [&](const AttnTensor& t, size_t at) {
-        return launch_attn_pack(a, t, a.kv_heads, a.len_k, true, count, index, p.planes, p.dp, p.rows_k, ws + at, st);
-    };
-    if (p.pack_q && (e = queries(a.q, p.q))) return e;
-    if (p.pack_do && (e = queries(a.dout, p.dout))) return e;
-    if (p.pack_kv && ((e = keys(a.k, p.k)) || (e = keys(a.v, p.v)))) return e;
-    return e;
+    PackJob jobs[4];
+    int n = 0;
+    if (p.pack_q) jobs[n++] = {a.q, a.heads, a.len_q, 0, a.len_q, ws + p.q};
+    if (p.pack_do) jobs[n++] = {a.dout, a.heads, a.len_q, 0, a.len_q, ws + p.dout};
+    if (p.pack_kv) {
+        jobs[n++] = {a.k, a.kv_heads, a.len_k, 1, p.rows_k, ws + p.k};
+        jobs[n++] = {a.v, a.kv_heads, a.len_k, 1, p.rows_k, ws + p.v};
+    }
+    return launch_attn_pack(a, jobs, n, count, index, p.planes, p.dp, st);
 }
 
 }  // namespace

@@ -340,10 +340,12 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
 }
 
 // The largest squared norms of dout's and of v's rows of each batch entry and key head, as bits of floats (zero
-// before): where = 0: queries, 1: keys. Eight lanes per row; maxima do not depend on their order.
+// before): blockIdx.y = 0: queries, 1: keys. Eight lanes per row; maxima do not depend on their order.
 template <class T>
-__global__ void __launch_bounds__(256) k_attn_norms(const AttnArgs a, long long pad, int where, unsigned* norms) {
+__global__ void __launch_bounds__(256) k_attn_norms(const AttnArgs a, long long qpad, long long rows_k, unsigned* norms) {
     pdl_entry();
+    const int where = blockIdx.y;
+    const long long pad = where ? rows_k : qpad;
     __shared__ unsigned most;
     if (threadIdx.x == 0) most = 0u;
     __syncthreads();
@@ -414,13 +416,15 @@ __global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long 
     }
 }
 
-// What a walk that was split left: the shares added up in order, a thread per eight elements of a row. index: as
-// BwdArgs; rows: of a head in the shares, of which the first `live` of a batch entry were written.
+// What a walk that was split left: the shares added up in order, a thread per eight elements of a row; dq, or dk and dv
+// (blockIdx.y). rows: of a head in the shares, of which the first `live` of a batch entry were written.
 template <class T>
-__global__ void __launch_bounds__(256) k_attn_sum(const BwdArgs g, const AttnTensor t, int heads, int keys, const float* part,
-                                                  long long split_stride, int splits, int dp, long long rows) {
+__global__ void __launch_bounds__(256) k_attn_sum(const BwdArgs g, int heads, int keys, const float* part, int splits, int dp, long long rows) {
     pdl_entry();
     const AttnArgs& a = g.t.a;
+    const AttnTensor& t = !keys ? a.dq : blockIdx.y == 0 ? a.dk : a.dv;
+    const long long share = (long long)a.batch * heads * rows * dp, split_stride = share * gridDim.y;
+    part += blockIdx.y * share;
     const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
     const int per = dp / 8, c = (int)(at % per) * 8;
     const long long r = at / per, bh = r / rows;
@@ -501,13 +505,10 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor
     cudaError_t e;
     if (half) {
         if ((e = cudaMemsetAsync(w.norms, 0, (size_t)a.batch * a.kv_heads * 2 * sizeof(unsigned), st))) return e;
-        for (int where = 0; where < 2; ++where) {
-            const long long pad = where ? w.rows_k : w.qpad;
-            count_launches(1);
-            if ((e = launch_pdl(k_attn_norms<__half>, dim3(blocks_of((long long)a.batch * (where ? a.kv_heads : a.heads) * pad * 8)), dim3(256),
-                                0, st, a, pad, where, w.norms)))
-                return e;
-        }
+        const long long q = (long long)a.batch * a.heads * w.qpad * 8, k = (long long)a.batch * a.kv_heads * w.rows_k * 8;
+        count_launches(1);
+        if ((e = launch_pdl(k_attn_norms<__half>, dim3(blocks_of(q > k ? q : k), 2), dim3(256), 0, st, a, w.qpad, w.rows_k, w.norms)))
+            return e;
     }
     count_launches(1);
     e = by_type(a.dtype, [&](auto t) {
@@ -517,7 +518,7 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor
     if (e) return e;
     for (int keys = 0; keys < 2; ++keys) {
         const int splits = keys ? w.splits_k : w.splits_q, heads = keys ? a.kv_heads : a.heads;
-        const long long rows = keys ? w.rows_k : a.len_q, share = (long long)a.batch * heads * rows * w.dp;
+        const long long rows = keys ? w.rows_k : a.len_q;
         const BwdArgs g{{a, w.count, splits > 1 ? w.part : nullptr, nullptr, 0, splits}, w.nlse, w.ndelta, w.qpad, a.scale,
                         1.f, half ? 1.f / 32768.f : 1.f, half ? w.factor : nullptr, w.index, w.rows_k};
         const TcTensor* x[2][4] = {{&q, &dout, &k64, &v64}, {&k, &v, &q64, &dout64}};
@@ -526,15 +527,12 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor
         else e = half ? typed<__half>(g, keys, w.dp, in, st) : typed<__nv_bfloat16>(g, keys, w.dp, in, st);
         if (e) return e;
         if (splits == 1) continue;
-        for (int i = 0; i < 1 + keys; ++i) {
-            count_launches(1);
-            e = by_type(a.dtype, [&](auto t) {
-                return launch_pdl(k_attn_sum<decltype(t)>, dim3(blocks_of((long long)a.batch * heads * rows * (w.dp / 8))), dim3(256), 0, st,
-                                  g, !keys ? a.dq : i == 0 ? a.dk : a.dv, heads, keys, (const float*)w.part + i * share,
-                                  share * (1 + keys), splits, w.dp, rows);
-            });
-            if (e) return e;
-        }
+        count_launches(1);
+        e = by_type(a.dtype, [&](auto t) {
+            return launch_pdl(k_attn_sum<decltype(t)>, dim3(blocks_of((long long)a.batch * heads * rows * (w.dp / 8)), 1 + keys), dim3(256), 0,
+                              st, g, heads, keys, (const float*)w.part, splits, w.dp, rows);
+        });
+        if (e) return e;
     }
     return cudaSuccess;
 }

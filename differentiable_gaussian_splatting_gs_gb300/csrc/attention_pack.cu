@@ -30,54 +30,59 @@ __global__ void __launch_bounds__(1024) k_attn_index(const AttnArgs a, int* coun
     if (threadIdx.x == 0) count[b] = done;
 }
 
-// A thread per eight elements of a packed row.
+// A thread per eight elements of a packed row, all tensors of a call in one launch (blockIdx.z).
+struct PackJobs {
+    PackJob job[4];
+};
 template <class T, int PL>
-__global__ void __launch_bounds__(256) k_attn_pack(const AttnArgs a, const AttnTensor t, int heads, int len, int keys,
-                                                   const int* count, const int* index, int dp, long long rows,
-                                                   __nv_bfloat16* dst) {
+__global__ void __launch_bounds__(256) k_attn_pack(const AttnArgs a, const PackJobs jobs, const int* count, const int* index, int dp) {
     pdl_entry();
-    const int per = dp / 8;
-    const long long bh = blockIdx.y + (long long)blockIdx.z * gridDim.y;
-    if (bh >= (long long)a.batch * heads) return;
-    const int b = (int)(bh / heads), h = (int)(bh % heads);
-    const int live = !keys ? len : count ? count[b] : key_count(a, b);
-    const int last = keys ? (live + kTileRows - 1) / kTileRows * kTileRows : live;  // rows that are read
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)last * per; i += (long long)gridDim.x * 256) {
-        const int row = (int)(i / per), c = (int)(i % per) * 8;
-        float x[8];
+    const PackJob& j = jobs.job[blockIdx.z];
+    const AttnTensor& t = j.t;
+    const int heads = j.heads, keys = j.keys, per = dp / 8;
+    const long long rows = j.rows;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(j.dst);
+    for (long long bh = blockIdx.y; bh < (long long)a.batch * heads; bh += gridDim.y) {
+        const int b = (int)(bh / heads), h = (int)(bh % heads);
+        const int live = !keys ? j.len : count ? count[b] : key_count(a, b);
+        const int last = keys ? (live + kTileRows - 1) / kTileRows * kTileRows : live;  // rows that are read
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)last * per; i += (long long)gridDim.x * 256) {
+            const int row = (int)(i / per), c = (int)(i % per) * 8;
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (row < live) {
-            const int src = index && keys ? index[(long long)b * a.len_k + row] : row;
-            const T* p = head_base<T>(t, b, h) + src * t.len_stride + c;
-            if (c + 8 <= a.d && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-                constexpr int V = 16 / (int)sizeof(T);
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            if (row < live) {
+                const int src = index && keys ? index[(long long)b * a.len_k + row] : row;
+                const T* p = head_base<T>(t, b, h) + src * t.len_stride + c;
+                if (c + 8 <= a.d && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+                    constexpr int V = 16 / (int)sizeof(T);
 #pragma unroll
-                for (int e = 0; e < 8; e += V) {
-                    const Pack<T, V> w = *reinterpret_cast<const Pack<T, V>*>(p + e);
+                    for (int e = 0; e < 8; e += V) {
+                        const Pack<T, V> w = *reinterpret_cast<const Pack<T, V>*>(p + e);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) x[e + k] = to_float(w.v[k]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < a.d) x[e] = to_float(p[e]);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < PL; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (PL == 1) {
-                    w[e] = pack2<typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type>(x[2 * e], x[2 * e + 1]);
+                        for (int k = 0; k < V; ++k) x[e + k] = to_float(w.v[k]);
+                    }
                 } else {
-                    w[e] = pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
-                    x[2 * e] -= __uint_as_float(w[e] << 16);
-                    x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < a.d) x[e] = to_float(p[e]);
                 }
             }
-            *reinterpret_cast<uint4*>(dst + ((bh * PL + q) * rows + row) * dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int q = 0; q < PL; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (PL == 1) {
+                        w[e] = pack2<typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type>(x[2 * e], x[2 * e + 1]);
+                    } else {
+                        w[e] = pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
+                        x[2 * e] -= __uint_as_float(w[e] << 16);
+                        x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+                    }
+                }
+                *reinterpret_cast<uint4*>(dst + ((bh * PL + q) * rows + row) * dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
     }
 }
@@ -156,18 +161,21 @@ cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStr
     return launch_pdl(k_attn_index, dim3(a.batch), dim3(1024), 0, st, a, count, index);
 }
 
-cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, int len, bool keys, const int* count,
-                             const int* index, int planes, int dp, long long rows, void* dst, cudaStream_t st) {
-    const long long bh = (long long)a.batch * heads, items = rows * (dp / 8);
-    const unsigned y = (unsigned)(bh < 32768 ? bh : 32768), z = (unsigned)((bh + y - 1) / y);
-    long long x = (items + 255) / 256;
-    if (x > 4096) x = 4096;
-    const dim3 grid((unsigned)x, y, z);
-    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dst);
+cudaError_t launch_attn_pack(const AttnArgs& a, const PackJob* jobs, int n, const int* count, const int* index, int planes, int dp,
+                             cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    PackJobs all{};
+    long long x = 1, y = 1;
+    for (int i = 0; i < n; ++i) {
+        all.job[i] = jobs[i];
+        const long long blocks = (jobs[i].rows * (dp / 8) + 255) / 256, bh = (long long)a.batch * jobs[i].heads;
+        x = blocks > x ? blocks : x;
+        y = bh > y ? bh : y;
+    }
+    const dim3 grid((unsigned)(x < 4096 ? x : 4096), (unsigned)(y < 32768 ? y : 32768), (unsigned)n);
+    auto* kernel = planes == 3 ? k_attn_pack<float, 3> : a.dtype == GS_DTYPE_F16 ? k_attn_pack<__half, 1> : k_attn_pack<__nv_bfloat16, 1>;
     count_launches(1);
-    if (planes == 3) return launch_pdl(k_attn_pack<float, 3>, grid, dim3(256), 0, st, a, t, heads, len, (int)keys, count, index, dp, rows, d);
-    auto* kernel = a.dtype == GS_DTYPE_F16 ? k_attn_pack<__half, 1> : k_attn_pack<__nv_bfloat16, 1>;
-    return launch_pdl(kernel, grid, dim3(256), 0, st, a, t, heads, len, (int)keys, count, index, dp, rows, d);
+    return launch_pdl(kernel, grid, dim3(256), 0, st, a, all, count, index, dp);
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st) {

@@ -56,9 +56,15 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const TcTensor& t, int r
 
 // count[b] and index[b][0 .. count[b]): the keys that take part, in order.
 cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st);
-// Lays `t` (heads heads; K or V when keys) out at dst as [batch x heads][planes][rows][dp] 16-bit values.
-cudaError_t launch_attn_pack(const AttnArgs& a, const AttnTensor& t, int heads, int len, bool keys, const int* count,
-                             const int* index, int planes, int dp, long long rows, void* dst, cudaStream_t st);
+// A tensor (heads heads; K or V when keys) to be laid out at dst as [batch x heads][planes][rows][dp] 16-bit values.
+struct PackJob {
+    AttnTensor t;
+    int heads, len, keys;
+    long long rows;
+    void* dst;
+};
+cudaError_t launch_attn_pack(const AttnArgs& a, const PackJob* jobs, int n, const int* count, const int* index, int planes, int dp,
+                             cudaStream_t st);
 // out and lse from the splits' shares [splits][batch][heads][len_q][dp].
 cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st);
 // One query, no shared heads; part, part_lse: the splits' shares, or NULL.
