@@ -71,7 +71,11 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         };
         auto over = [](long long n, long long m) { return (n + m - 1) / m; };
         if (!backward) {
-            const bool two = !(wide && p.dp == 128) && over(a.len_q, 256) * a.heads * a.batch >= sms;
+            // Two query tiles per block work beside each other; a block of one takes 0.81 (16-bit heads of 64) to 0.89
+            // (128) of their time. So two, unless blocks of one fill the last round of the SMs better: 2432 queries of
+            // 16 heads of 64 over 2500 keys are 160 blocks of two, 45.7 us, or 304 of one, 38.5 us; 4864 are 47 and 76 us.
+            auto rounds = [&](int tiles) { return over(over(a.len_q, 128 * tiles) * a.heads * a.batch, sms); };
+            const bool two = !(wide && p.dp == 128) && 100 * rounds(2) <= 85 * rounds(1);
             p.nq = two ? 2 : 1;
             p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
         } else {
