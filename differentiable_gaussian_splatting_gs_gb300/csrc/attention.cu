@@ -13,12 +13,12 @@ constexpr int kMaxTcDim = 128;
 
 // What a call packs, how it splits its walks, and where the pieces lie in the workspace (byte offsets).
 struct Plan {
-    bool tc, decode, pack_q, pack_kv, pack_do;
+    bool tc, decode, pack_q, pack_kv, pack_do, keys_first;
     int planes, dp, nq, splits;
     int splits_q, splits_k;  // backward: of the walks for dq, and for dk and dv
     long long rows_k;        // rows of a packed head of K or V
     long long qpad;          // queries of a head, rounded up to the tiles that the backward walks
-    size_t count, index, q, k, v, dout, part, part_lse, delta, nlse, norms, factor, bytes;
+    size_t count, index, q, k, v, dout, part, part_k, part_lse, delta, nlse, norms, bytes;
 };
 
 bool copyable(const AttnTensor& t, const AttnArgs& a, int len) {
@@ -80,15 +80,17 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
         } else {
             p.qpad = over(a.len_q, kBN) * kBN;
-            p.splits_q = split(over(a.len_q, kTileRows) * a.heads * a.batch, over(a.len_k, kBN), 4);
-            p.splits_k = split(over(a.len_k, kTileRows) * a.kv_heads * a.batch,
-                               p.qpad / kBN * (a.heads / a.kv_heads), 4);
+            // A block walks no more than an SM's share of all walks, or than four tiles.
+            const long long walk_q = over(a.len_k, kBN), walk_k = p.qpad / kBN * (a.heads / a.kv_heads),
+                            all = over(a.len_q, kTileRows) * a.heads * a.batch * walk_q +
+                                  over(a.len_k, kTileRows) * a.kv_heads * a.batch * walk_k,
+                            share = all > 4ll * sms ? over(all, sms) : 4;
+            p.splits_q = (int)over(walk_q, share);
+            p.splits_k = (int)over(walk_k, share);
+            p.keys_first = over(walk_k, p.splits_k) > over(walk_q, p.splits_q);
             p.nlse = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
             p.delta = take((size_t)a.batch * a.heads * p.qpad * sizeof(float));
-            if (a.dtype == GS_DTYPE_F16) {
-                p.norms = take(bk * 2 * sizeof(unsigned));
-                p.factor = take(bk * sizeof(float2));
-            }
+            if (a.dtype == GS_DTYPE_F16) p.norms = take(bk * 2 * sizeof(unsigned));
         }
         const size_t row = (size_t)p.planes * p.dp * 2;
         if (a.key_mask) {
@@ -102,9 +104,8 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             p.v = take(bk * p.rows_k * row);
         }
         if (backward) {
-            const size_t q = p.splits_q > 1 ? (size_t)p.splits_q * bq * p.dp * sizeof(float) : 0;
-            const size_t k = p.splits_k > 1 ? (size_t)p.splits_k * 2 * bk * p.rows_k * p.dp * sizeof(float) : 0;
-            p.part = take(q > k ? q : k);
+            if (p.splits_q > 1) p.part = take((size_t)p.splits_q * bq * p.dp * sizeof(float));
+            if (p.splits_k > 1) p.part_k = take((size_t)p.splits_k * 2 * bk * p.rows_k * p.dp * sizeof(float));
         } else if (p.splits > 1) {
             p.part = take((size_t)p.splits * bq * p.dp * sizeof(float));
             p.part_lse = take((size_t)p.splits * bq * sizeof(float));
@@ -214,20 +215,25 @@ cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t 
         return (e = launch_attn_delta(a, st)) ? e : launch_attn_simt(a, true, st);
     }
     int *count, *index;
+    unsigned* norms = reinterpret_cast<unsigned*>(ws + p.norms);
+    const size_t norm_bytes = (size_t)a.batch * a.kv_heads * 2 * sizeof(unsigned);
+    if (a.dtype == GS_DTYPE_F16 && (e = cudaMemsetAsync(norms, 0, norm_bytes, st))) return e;
     if ((e = lay_out(p, a, ws, count, index, st))) return e;
-    const TcBwd w{a, count, index, reinterpret_cast<float*>(ws + p.nlse), reinterpret_cast<float*>(ws + p.delta),
-                  reinterpret_cast<unsigned*>(ws + p.norms), reinterpret_cast<float2*>(ws + p.factor), reinterpret_cast<float*>(ws + p.part), p.qpad, p.rows_k, p.dp, p.splits_q, p.splits_k};
-    TcTensor x[2][4];  // as row tiles, as walked tiles: Q, dout, K, V
+    auto shares = [&](int splits, size_t at) { return splits > 1 ? reinterpret_cast<float*>(ws + at) : nullptr; };
+    const TcBwd w{a, count, index, reinterpret_cast<float*>(ws + p.nlse), reinterpret_cast<float*>(ws + p.delta), norms,
+                  shares(p.splits_q, p.part), shares(p.splits_k, p.part_k), p.qpad, p.rows_k, p.dp, p.splits_q, p.splits_k,
+                  p.keys_first};
+    BwdTensors x;
+    TcTensor* to[2][4] = {{&x.q, &x.dout, &x.k, &x.v}, {&x.q_walk, &x.dout_walk, &x.k_walk, &x.v_walk}};
     for (int i = 0; i < 2; ++i) {
         const int box = i == 0 ? kTileRows : kBN;
-        if ((e = operand(x[i][0], p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, box)) ||
-            (e = operand(x[i][1], p, a, a.dout, a.heads, a.len_q, p.pack_do, ws + p.dout, a.len_q, box)) ||
-            (e = operand(x[i][2], p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, box)) ||
-            (e = operand(x[i][3], p, a, a.v, a.kv_heads, a.len_k, p.pack_kv, ws + p.v, p.rows_k, box)))
+        if ((e = operand(*to[i][0], p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, box)) ||
+            (e = operand(*to[i][1], p, a, a.dout, a.heads, a.len_q, p.pack_do, ws + p.dout, a.len_q, box)) ||
+            (e = operand(*to[i][2], p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, box)) ||
+            (e = operand(*to[i][3], p, a, a.v, a.kv_heads, a.len_k, p.pack_kv, ws + p.v, p.rows_k, box)))
             return e;
     }
-    if ((a.key_mask || a.k_len) && (e = launch_attn_zero(a, st))) return e;
-    return launch_attn_bwd_tc(w, x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3], st);
+    return launch_attn_bwd_tc(w, x, st);
 }
 
 }  // namespace gs

@@ -27,6 +27,17 @@
 
 namespace gs {
 
+constexpr int kBoost = 15;  // float16: P times 2^kBoost
+
+// float16: the power of two that leaves the bound of dS / scale, 2 max|dout| max|v|, below 2^15; 0 where there is none.
+// norms: their squares, as bits.
+__device__ __forceinline__ int ds_exponent(const unsigned* norms) {
+    const float bound = 2.f * sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
+    if (!(bound < 3e38f) || bound <= 0.f) return 0;
+    int e;
+    frexpf(bound, &e);  // bound < 2^e
+    return min(max(15 - e, -24), 24);
+}
 
 template <int DP, bool KEYS>
 struct BwdShape {
@@ -39,23 +50,22 @@ struct BwdShape {
     static constexpr int kAccs = KEYS ? 2 : 1;
     static constexpr int kBuffers = KEYS && DP == 128 ? 2 : 3;  // walked tiles in tensor memory, 128 columns each
     static constexpr bool kOneIssuer = kBuffers == 2;
-    // a warpgroup per buffer and one that copies and issues. Registers are moved between them (setmaxnreg):
-    // 512 threads x 128 at launch = 384 x 144 + 128 x 80, or 384 x 168 = 256 x 216 + 128 x 72
+    // a warpgroup per buffer, one that copies and issues, and with two buffers one that rests. Registers are moved
+    // between them (setmaxnreg): 512 threads x 128 at launch = 384 x 144 + 128 x 80 = 256 x 208 + 128 x 72 + 128 x 24
     static constexpr int kElem = kBuffers * 4;  // elementwise warps
-    static constexpr int kThreads = kElem * 32 + 128;
     static constexpr int kAcc = kBuffers * 128;                 // first accumulator column
     static constexpr bool kInTmem = !KEYS && DP == 64;          // the row operands, 32 columns each
     static constexpr int kRowCol = kAcc + kAccs * DP;
     static_assert(kRowCol + (kInTmem ? 64 : 0) <= 512 && kStages > kBuffers);
 };
 
+// One block in its role; at: its number among the role's blocks. ta1, ta2: A1 and A2; tb1, tb2: B1 and B2.
 template <class T, int DP, bool KEYS>
-__global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
-    k_attn_bwd(const __grid_constant__ BwdArgs g, const __grid_constant__ TcTensor ta1, const __grid_constant__ TcTensor ta2,
-               const __grid_constant__ TcTensor tb1, const __grid_constant__ TcTensor tb2) {
+__device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTensor& ta1, const TcTensor& ta2, const TcTensor& tb1,
+                                          const TcTensor& tb2) {
     using S = BwdShape<DP, KEYS>;
     constexpr int kSt = S::kStages, kNB = S::kBuffers;
-    pdl_entry();
+    constexpr bool kHalf = std::is_same<T, __half>::value;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t a_full, a_moved, full[kSt], empty[kSt], s_full[kNB], p_full[kNB], b_free[kNB], done, drain[3];
     __shared__ uint32_t tmem_base;
@@ -65,7 +75,6 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
     const uint32_t sa1 = smem_u32(base), sa2 = sa1 + S::kA, sb = sa2 + S::kA;
     auto stats = [&](int s) { return reinterpret_cast<float*>(base + 2 * S::kA + s * S::kStage + 2 * S::kB); };
 
-    int at = blockIdx.x;
     const int block = at % t.tiles;
     at /= t.tiles;
     const int split = at % t.splits;
@@ -105,7 +114,9 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
     tc_fence_after();
     const uint32_t tm = tmem_base;
 
-    if (warp >= S::kElem) {
+    if (warp >= S::kElem + 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+    } else if (warp >= S::kElem) {
         if (kNB == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int steps = (a.d + 15) / 16;
@@ -199,19 +210,25 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
         }
     } else {  // elementwise: thread = row
         if (kNB == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int w = warp / 4;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const int row = row0 + (threadIdx.x & 127);
         const float c = a.scale * 1.4426950408889634f;
-        const float2 factor = g.factor ? g.factor[b * a.kv_heads + (KEYS ? h : h / share)] : make_float2(g.ds_in, g.ds_out);
-        const f32x2 c2 = f2_pack(c, c), i2 = f2_pack(factor.x, factor.x);
+        // of dS / scale as it is stored, over P's times dP - delta; and of the sum of dS B1
+        float ds_in = 1.f, ds_out = a.scale;
+        if (kHalf) {
+            const int e = ds_exponent(g.norms + (b * a.kv_heads + (KEYS ? h : h / share)) * 2);
+            ds_in = exp2f((float)(e - kBoost));
+            ds_out *= exp2f((float)-e);
+        }
+        const f32x2 c2 = f2_pack(c, c), i2 = f2_pack(ds_in, ds_in);
         f32x2 l2 = 0, d2 = 0;  // the row's own, where rows are queries
         if (!KEYS) {
             const long long q = ((long long)b * a.heads + h) * g.qpad + row;
             const float l = row < a.len_q ? g.nlse[q] : -INFINITY, d = row < a.len_q ? g.ndelta[q] : 0.f;
             l2 = f2_pack(l, l);
-            d2 = f2_pack(d, d);
+            d2 = f2_pack(d * ds_in, d * ds_in);
         }
         bool ok = true;
         if (S::kInTmem && n > 0 && w < 2) {
@@ -256,7 +273,9 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
                     }
                     const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, l2));
                     const float u0 = ex2_approx(z.x), u1 = ex2_approx(z.y);
-                    const f32x2 x = f2_fma(f2_pack(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), i2, d2);
+                    f32x2 x = f2_pack(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1]));
+                    x = KEYS || !kHalf ? f2_add(x, d2) : f2_fma(x, i2, d2);
+                    if (KEYS && kHalf) x = f2_mul(x, i2);
                     const float2 v = f2_unpack(f2_mul(f2_pack(u0, u1), x));
                     if (KEYS) p[e] = pack2<T>(u0, u1);
                     ds[e] = pack2<T>(v.x, v.y);
@@ -287,7 +306,7 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
         constexpr int kOut = KEYS ? DP : DP / 2;
         const int col0 = KEYS ? 0 : (w & 1) * kOut;
         const uint32_t acc = tm + S::kAcc + lanes + which * DP + col0;
-        const float f = which == 0 ? factor.y : g.p_out;
+        const float f = which == 0 ? ds_out : kHalf ? 1.f / (1 << kBoost) : 1.f;
         const bool live = row < rows && ok && w < 2;
         const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
         const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
@@ -339,80 +358,79 @@ __global__ void __launch_bounds__(BwdShape<DP, KEYS>::kThreads, 1)
     if (warp == S::kElem) tmem_free<512>(tm);
 }
 
-// The largest squared norms of dout's and of v's rows of each batch entry and key head, as bits of floats (zero
-// before): blockIdx.y = 0: queries, 1: keys. Eight lanes per row; maxima do not depend on their order.
-template <class T>
-__global__ void __launch_bounds__(256) k_attn_norms(const AttnArgs a, long long qpad, long long rows_k, unsigned* norms) {
+// Both roles in one launch, so that the blocks of the second fill the SMs that the first's last round leaves: keys
+// first where their walks are longer.
+template <class T, int DP>
+__global__ void __launch_bounds__(512, 1)
+    k_attn_bwd(const __grid_constant__ BwdArgs gq, const __grid_constant__ BwdArgs gk, const __grid_constant__ BwdTensors x,
+               int keys_first) {
     pdl_entry();
-    const int where = blockIdx.y;
-    const long long pad = where ? rows_k : qpad;
-    __shared__ unsigned most;
-    if (threadIdx.x == 0) most = 0u;
-    __syncthreads();
-    const int heads = where ? a.kv_heads : a.heads, lane = threadIdx.x & 7;
-    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8, bh = at / pad, i = at % pad;  // a block is within a head
-    const int b = (int)(bh / heads), h = (int)(bh % heads);
-    float s = 0.f;
-    if (b < a.batch && (where ? i < a.len_k && key_valid(a, b, (int)i, key_count(a, b)) : i < a.len_q)) {
-        const AttnTensor& t = where ? a.v : a.dout;
-        const T* x = head_base<T>(t, b, h) + i * t.len_stride;
-        for (int c = lane * 8; c < a.d; c += 64)
-            for (int k = 0; k < 8 && c + k < a.d; ++k) s = fmaf(to_float(x[c + k]), to_float(x[c + k]), s);
-    }
-#pragma unroll
-    for (int k = 4; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    atomicMax(&most, __float_as_uint(fabsf(s)));  // NaN compares above every number
-    __syncthreads();
-    if (threadIdx.x == 0 && b < a.batch) atomicMax(norms + (b * a.kv_heads + (where ? h : h / (a.heads / a.kv_heads))) * 2 + where, most);
+    const int at = blockIdx.x, n = keys_first ? gk.blocks : gq.blocks;
+    if ((at < n) == (keys_first != 0))
+        bwd_block<T, DP, true>(gk, keys_first ? at : at - n, x.k, x.v, x.q_walk, x.dout_walk);
+    else
+        bwd_block<T, DP, false>(gq, keys_first ? at - n : at, x.q, x.dout, x.k_walk, x.v_walk);
 }
 
-// Of every query, padded: boost - lse log2(e), so that P times 2^boost = exp2(scale log2(e) S + that); and -delta
-// times ds_in. -inf and 0 where there is no query, -inf where it has no key. Eight lanes per query. With norms,
-// ds_in comes from them, and the first query of a key head's first head leaves its factors.
+// What the walks need of every row, eight lanes each. blockIdx.y = 0: of every query, padded: boost - lse log2(e), so
+// that P times 2^boost = exp2(scale log2(e) S + that), and -delta; -inf and 0 where there is no query, -inf where it
+// has no key. 1: zero gradients of the keys that take no part. With norms, the largest squared norms of dout's (0) and
+// of v's rows (1) of each batch entry and key head too, as bits of floats (zero before; maxima do not depend on
+// their order).
 template <class T>
-__global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long qpad, float boost, float ds_in, const unsigned* norms,
-                                                    float2* factor, float* nlse, float* ndelta) {
+__global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long qpad, long long rows_k, int boost, unsigned* norms,
+                                                    float* nlse, float* ndelta) {
     pdl_entry();
-    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8;
-    const int lane = threadIdx.x & 7;
-    const long long bh = at / qpad, i = at % qpad;
-    const bool in = bh < (long long)a.batch * a.heads && i < a.len_q;
-    float s = 0.f;
-    if (in) {
-        const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
-        const T* o = head_base<T>(a.out, b, h) + i * a.out.len_stride;
-        const T* d = head_base<T>(a.dout, b, h) + i * a.dout.len_stride;
-        constexpr int V = 16 / (int)sizeof(T);
-        if (a.d % V == 0 && (reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(d)) % 16 == 0) {
-            for (int c = lane * V; c < a.d; c += 8 * V) {
-                const Pack<T, V> x = *reinterpret_cast<const Pack<T, V>*>(o + c), y = *reinterpret_cast<const Pack<T, V>*>(d + c);
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool keys = blockIdx.y;
+    const long long pad = keys ? rows_k : qpad, at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8, bh = at / pad, i = at % pad;
+    const int heads = keys ? a.kv_heads : a.heads, b = (int)(bh / heads), h = (int)(bh % heads), lane = threadIdx.x & 7;
+    if (b >= a.batch) return;  // the whole block: its rows are of one head (pad is a multiple of 32)
+    __shared__ unsigned most;
+    if (norms && threadIdx.x == 0) most = 0u;
+    const bool in = i < (keys ? a.len_k : a.len_q), valid = in && (!keys || key_valid(a, b, (int)i, key_count(a, b)));
+    float s = 0.f, n2 = 0.f;  // of out and dout; of dout or v with itself
+    if (valid && (!keys || norms)) {
+        const AttnTensor& t = keys ? a.v : a.dout;
+        const T* d = head_base<T>(t, b, h) + i * t.len_stride;
+        const T* o = keys ? d : head_base<T>(a.out, b, h) + i * a.out.len_stride;
+        const bool vec = a.d % V == 0 && (reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(d)) % 16 == 0;
+        for (int c = lane * V; c < a.d; c += 8 * V) {
+            Pack<T, V> x, y;
+            if (vec) {
+                x = *reinterpret_cast<const Pack<T, V>*>(o + c), y = *reinterpret_cast<const Pack<T, V>*>(d + c);
+            } else {  // the same elements per lane, so that a layout changes no sum
+                const T zero = from_float<T>(0.f);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s = fmaf(to_float(x.v[k]), to_float(y.v[k]), s);
+                for (int k = 0; k < V; ++k) x.v[k] = c + k < a.d ? o[c + k] : zero, y.v[k] = c + k < a.d ? d[c + k] : zero;
             }
-        } else {
-            // the same elements per lane as above, so that a layout changes no sum
-            for (int c = lane * V; c < a.d; c += 8 * V)
-                for (int k = 0; k < V && c + k < a.d; ++k) s = fmaf(to_float(o[c + k]), to_float(d[c + k]), s);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                s = fmaf(to_float(x.v[k]), to_float(y.v[k]), s);
+                if (norms) n2 = fmaf(to_float(y.v[k]), to_float(y.v[k]), n2);
+            }
         }
     }
 #pragma unroll
     for (int k = 4; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (lane == 0 && bh < (long long)a.batch * a.heads) {
-        if (norms) {
-            const int share = a.heads / a.kv_heads, b = (int)(bh / a.heads), h = (int)(bh % a.heads), at2 = b * a.kv_heads + h / share;
-            const float bound = 2.f * a.scale * sqrtf(__uint_as_float(norms[2 * at2])) * sqrtf(__uint_as_float(norms[2 * at2 + 1]));
-            // the power of two that leaves the bound below 2^15; 1 where there is none
-            int e = 0;
-            if (bound < 3e38f) {
-                frexpf(bound, &e);  // bound < 2^e
-                e = bound > 0.f ? min(max(15 - e, -24), 24) : 0;
-            }
-            ds_in = a.scale * exp2f((float)e - boost);
-            if (i == 0 && h % share == 0) factor[at2] = make_float2(ds_in, exp2f((float)-e));
-        }
+    if (!keys && lane == 0) {
         const float l = in ? a.lse[bh * a.len_q + i] : -INFINITY;
-        nlse[at] = l == -INFINITY ? -INFINITY : boost - l * 1.4426950408889634f;
-        ndelta[at] = -s * ds_in;
+        nlse[at] = l == -INFINITY ? -INFINITY : (float)boost - l * 1.4426950408889634f;
+        ndelta[at] = -s;
+    }
+    if (keys && in && !valid) {
+        T* dk = static_cast<T*>(a.dk.data) + b * a.dk.batch_stride + h * a.dk.head_stride + i * a.dk.len_stride;
+        T* dv = static_cast<T*>(a.dv.data) + b * a.dv.batch_stride + h * a.dv.head_stride + i * a.dv.len_stride;
+        for (int c = lane; c < a.d; c += 8) dk[c] = dv[c] = from_float<T>(0.f);
+    }
+    if (norms) {
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, k);
+        const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(n2)));  // NaN compares above every number
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) atomicMax(&most, w);
+        __syncthreads();
+        if (threadIdx.x == 0) atomicMax(norms + (b * a.kv_heads + (keys ? h : h / (a.heads / a.kv_heads))) * 2 + keys, most);
     }
 }
 
@@ -443,41 +461,15 @@ __global__ void __launch_bounds__(256) k_attn_sum(const BwdArgs g, int heads, in
         if (c + k < a.d) dst[k] = from_float<T>(x[k]);
 }
 
-// 0 into the gradients of keys that take no part, a warp per key and head.
-template <class T>
-__global__ void __launch_bounds__(256) k_attn_zero(const AttnArgs a) {
-    pdl_entry();
-    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / 32;
-    const int key = (int)(at % a.len_k);
-    const long long bh = at / a.len_k;
-    const int b = (int)(bh / a.kv_heads), h = (int)(bh % a.kv_heads);
-    if (b >= a.batch || key_valid(a, b, key, key_count(a, b))) return;
-    T* dk = static_cast<T*>(a.dk.data) + b * a.dk.batch_stride + h * a.dk.head_stride + key * a.dk.len_stride;
-    T* dv = static_cast<T*>(a.dv.data) + b * a.dv.batch_stride + h * a.dv.head_stride + key * a.dv.len_stride;
-    for (int c = threadIdx.x & 31; c < a.d; c += 32) dk[c] = dv[c] = from_float<T>(0.f);
-}
-
 namespace {
 
-template <class T, int DP, bool KEYS>
-cudaError_t run(BwdArgs g, const TcTensor (&x)[4], cudaStream_t st) {
-    using S = BwdShape<DP, KEYS>;
-    auto* kernel = k_attn_bwd<T, DP, KEYS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+template <class T, int DP>
+cudaError_t run(const BwdArgs& gq, const BwdArgs& gk, const BwdTensors& x, bool keys_first, cudaStream_t st) {
+    constexpr int smem = BwdShape<DP, false>::kSmem > BwdShape<DP, true>::kSmem ? BwdShape<DP, false>::kSmem : BwdShape<DP, true>::kSmem;
+    auto* kernel = k_attn_bwd<T, DP>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    const int len = KEYS ? g.t.a.len_k : g.t.a.len_q;
-    g.t.tiles = (len + kTileRows - 1) / kTileRows;
-    const long long blocks = (long long)g.t.tiles * g.t.splits * (KEYS ? g.t.a.kv_heads : g.t.a.heads) * g.t.a.batch;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    count_launches(1);
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, st, g, x[0], x[1], x[2], x[3]);
-}
-
-template <class T>
-cudaError_t typed(const BwdArgs& g, bool keys, int dp, const TcTensor (&x)[4], cudaStream_t st) {
-    if (keys) return dp == 64 ? run<T, 64, true>(g, x, st) : run<T, 128, true>(g, x, st);
-    return dp == 64 ? run<T, 64, false>(g, x, st) : run<T, 128, false>(g, x, st);
+    return launch_pdl(kernel, dim3((unsigned)(gq.blocks + gk.blocks)), dim3(512), smem, st, gq, gk, x, (int)keys_first);
 }
 
 template <class F>
@@ -489,48 +481,41 @@ unsigned blocks_of(long long threads) { return (unsigned)((threads + 255) / 256)
 
 }  // namespace
 
-cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st) {
-    count_launches(1);
-    return by_type(a.dtype, [&](auto e) {
-        return launch_pdl(k_attn_zero<decltype(e)>, dim3(blocks_of((long long)a.batch * a.kv_heads * a.len_k * 32)), dim3(256), 0, st, a);
-    });
-}
-
-cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor& dout, const TcTensor& k, const TcTensor& v,
-                               const TcTensor& q64, const TcTensor& dout64, const TcTensor& k64, const TcTensor& v64,
-                               cudaStream_t st) {
+cudaError_t launch_attn_bwd_tc(const TcBwd& w, const BwdTensors& x, cudaStream_t st) {
     const AttnArgs& a = w.a;
-    const bool half = a.dtype == GS_DTYPE_F16;
-    const float boost = half ? 15.f : 0.f;
-    cudaError_t e;
-    if (half) {
-        if ((e = cudaMemsetAsync(w.norms, 0, (size_t)a.batch * a.kv_heads * 2 * sizeof(unsigned), st))) return e;
-        const long long q = (long long)a.batch * a.heads * w.qpad * 8, k = (long long)a.batch * a.kv_heads * w.rows_k * 8;
-        count_launches(1);
-        if ((e = launch_pdl(k_attn_norms<__half>, dim3(blocks_of(q > k ? q : k), 2), dim3(256), 0, st, a, w.qpad, w.rows_k, w.norms)))
-            return e;
-    }
+    const bool half = a.dtype == GS_DTYPE_F16, by_key = half || a.key_mask || a.k_len;
+    const long long q = (long long)a.batch * a.heads * w.qpad * 8, k = by_key ? (long long)a.batch * a.kv_heads * w.rows_k * 8 : 0;
     count_launches(1);
-    e = by_type(a.dtype, [&](auto t) {
-        return launch_pdl(k_attn_stats<decltype(t)>, dim3(blocks_of((long long)a.batch * a.heads * w.qpad * 8)), dim3(256), 0, st, a,
-                          w.qpad, boost, a.scale, (const unsigned*)(half ? w.norms : nullptr), w.factor, w.nlse, w.ndelta);
+    cudaError_t e = by_type(a.dtype, [&](auto t) {
+        return launch_pdl(k_attn_stats<decltype(t)>, dim3(blocks_of(q > k ? q : k), by_key ? 2 : 1), dim3(256), 0, st, a, w.qpad,
+                          w.rows_k, half ? kBoost : 0, half ? w.norms : nullptr, w.nlse, w.ndelta);
     });
     if (e) return e;
+    const int tiles_q = (a.len_q + kTileRows - 1) / kTileRows, tiles_k = (a.len_k + kTileRows - 1) / kTileRows;
+    const long long blocks_q = (long long)tiles_q * w.splits_q * a.heads * a.batch,
+                    blocks_k = (long long)tiles_k * w.splits_k * a.kv_heads * a.batch;
+    if (blocks_q + blocks_k > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const BwdArgs gq{{a, w.count, w.part_q, nullptr, tiles_q, w.splits_q}, w.nlse, w.ndelta, w.qpad, half ? w.norms : nullptr,
+                     w.index, w.rows_k, (int)blocks_q};
+    BwdArgs gk = gq;
+    gk.t.part = w.part_k;
+    gk.t.tiles = tiles_k;
+    gk.t.splits = w.splits_k;
+    gk.blocks = (int)blocks_k;
+    count_launches(1);
+    if (a.dtype == GS_DTYPE_F32) e = launch_attn_bwd_wide(gq, gk, x, w.keys_first, st);
+    else if (half) e = w.dp == 64 ? run<__half, 64>(gq, gk, x, w.keys_first, st) : run<__half, 128>(gq, gk, x, w.keys_first, st);
+    else e = w.dp == 64 ? run<__nv_bfloat16, 64>(gq, gk, x, w.keys_first, st) : run<__nv_bfloat16, 128>(gq, gk, x, w.keys_first, st);
+    if (e) return e;
     for (int keys = 0; keys < 2; ++keys) {
-        const int splits = keys ? w.splits_k : w.splits_q, heads = keys ? a.kv_heads : a.heads;
+        const BwdArgs& g = keys ? gk : gq;
+        if (g.t.splits == 1) continue;
+        const int heads = keys ? a.kv_heads : a.heads;
         const long long rows = keys ? w.rows_k : a.len_q;
-        const BwdArgs g{{a, w.count, splits > 1 ? w.part : nullptr, nullptr, 0, splits}, w.nlse, w.ndelta, w.qpad, a.scale,
-                        1.f, half ? 1.f / 32768.f : 1.f, half ? w.factor : nullptr, w.index, w.rows_k};
-        const TcTensor* x[2][4] = {{&q, &dout, &k64, &v64}, {&k, &v, &q64, &dout64}};
-        const TcTensor in[4] = {*x[keys][0], *x[keys][1], *x[keys][2], *x[keys][3]};
-        if (a.dtype == GS_DTYPE_F32) e = launch_attn_bwd_wide(g, keys, in, st);
-        else e = half ? typed<__half>(g, keys, w.dp, in, st) : typed<__nv_bfloat16>(g, keys, w.dp, in, st);
-        if (e) return e;
-        if (splits == 1) continue;
         count_launches(1);
         e = by_type(a.dtype, [&](auto t) {
             return launch_pdl(k_attn_sum<decltype(t)>, dim3(blocks_of((long long)a.batch * heads * rows * (w.dp / 8)), 1 + keys), dim3(256), 0,
-                              st, g, heads, keys, (const float*)w.part, splits, w.dp, rows);
+                              st, g, heads, keys, (const float*)g.t.part, g.t.splits, w.dp, rows);
         });
         if (e) return e;
     }

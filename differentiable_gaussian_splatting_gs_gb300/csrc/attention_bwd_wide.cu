@@ -46,13 +46,11 @@ __device__ __forceinline__ void store_planes(uint32_t buffer, int which, int y, 
 }  // namespace
 
 template <bool KEYS>
-__global__ void __launch_bounds__(512, 1)
-    k_attn_bwd_wide(const __grid_constant__ BwdArgs g, const __grid_constant__ TcTensor ta1, const __grid_constant__ TcTensor ta2,
-                    const __grid_constant__ TcTensor tb1, const __grid_constant__ TcTensor tb2) {
+__device__ __forceinline__ void wide_block(const BwdArgs& g, int at, const TcTensor& ta1, const TcTensor& ta2, const TcTensor& tb1,
+                                           const TcTensor& tb2) {
     using C = Pairs<kPL>;
     constexpr int kProducts = KEYS ? 1 : 2;              // places of a tile's product: dk and dv, or dq in turn
     constexpr int kCols = KEYS ? 2 * kDP : kDP;          // columns of one
-    pdl_entry();
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t a_full, full[2], empty[2], s_full[2], p_full[2], x_full[2], x_free[2], drain;
     __shared__ uint32_t tmem_base;
@@ -62,7 +60,6 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t sa1 = smem_u32(base), sa2 = sa1 + kRowBytes, sb = sa2 + kRowBytes;
     auto stats = [&](int s) { return reinterpret_cast<float*>(base + 2 * kRowBytes + s * kStage + 2 * kWalkBytes); };
 
-    int at = blockIdx.x;
     const int block = at % t.tiles;
     at /= t.tiles;
     const int split = at % t.splits;
@@ -198,6 +195,8 @@ __global__ void __launch_bounds__(512, 1)
         }
         const bool live = row < rows && ok;
 #pragma unroll
+        for (int e = 0; e < kDP; ++e) sum[e] *= a.scale;  // dS was formed without it
+#pragma unroll
         for (int which = 0; which < (KEYS ? 2 : 1); ++which) {  // 0: of dS B1, 1: of P B2
             const AttnTensor& out = KEYS ? (which == 0 ? a.dk : a.dv) : a.dq;
             const long long to = KEYS && g.index && live ? g.index[(long long)b * a.len_k + row] : row;
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(512, 1)
                         d = st[kBN + y * 32 + e];
                     }
                     p[e] = ex2_approx(fmaf(__uint_as_float(s[e]), c, l));
-                    ds[e] = p[e] * fmaf(__uint_as_float(dp[e]), g.ds_in, d);
+                    ds[e] = p[e] * (__uint_as_float(dp[e]) + d);
                 }
                 if (!KEYS && left < 32) {
                     asm volatile("");  // a branch
@@ -275,25 +274,22 @@ __global__ void __launch_bounds__(512, 1)
     if (warp == 12) tmem_free<512>(tm);
 }
 
-namespace {
-
-template <bool KEYS>
-cudaError_t run(BwdArgs g, const TcTensor (&x)[4], cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_bwd_wide<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e) return e;
-    const int len = KEYS ? g.t.a.len_k : g.t.a.len_q;
-    g.t.tiles = (len + kTileRows - 1) / kTileRows;
-    const long long blocks = (long long)g.t.tiles * g.t.splits * (KEYS ? g.t.a.kv_heads : g.t.a.heads) * g.t.a.batch;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    count_launches(1);
-    return launch_pdl(k_attn_bwd_wide<KEYS>, dim3((unsigned)blocks), dim3(512), kSmem, st, g, x[0], x[1], x[2], x[3]);
+// Both roles in one launch (attention_bwd.cu).
+__global__ void __launch_bounds__(512, 1)
+    k_attn_bwd_wide(const __grid_constant__ BwdArgs gq, const __grid_constant__ BwdArgs gk, const __grid_constant__ BwdTensors x,
+                    int keys_first) {
+    pdl_entry();
+    const int at = blockIdx.x, n = keys_first ? gk.blocks : gq.blocks;
+    if ((at < n) == (keys_first != 0))
+        wide_block<true>(gk, keys_first ? at : at - n, x.k, x.v, x.q_walk, x.dout_walk);
+    else
+        wide_block<false>(gq, keys_first ? at - n : at, x.q, x.dout, x.k_walk, x.v_walk);
 }
 
-}  // namespace
-
-cudaError_t launch_attn_bwd_wide(const BwdArgs& g, bool keys, const TcTensor (&x)[4], cudaStream_t st) {
-    return keys ? run<true>(g, x, st) : run<false>(g, x, st);
+cudaError_t launch_attn_bwd_wide(const BwdArgs& gq, const BwdArgs& gk, const BwdTensors& x, bool keys_first, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(k_attn_bwd_wide, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e) return e;
+    return launch_pdl(k_attn_bwd_wide, dim3((unsigned)(gq.blocks + gk.blocks)), dim3(512), kSmem, st, gq, gk, x, (int)keys_first);
 }
 
 }  // namespace gs

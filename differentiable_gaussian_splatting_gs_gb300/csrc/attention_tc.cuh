@@ -78,33 +78,30 @@ constexpr int kBN = 64;  // rows per tile that the backward walks
 struct BwdArgs {
     TcArgs t;              // t.part: float32 shares of dq, or of dk and then dv, or NULL; t.tiles: row blocks of a head
     const float* nlse;     // [batch x heads][len_q padded]: the exponent's offset of each query (k_attn_stats)
-    const float* ndelta;   // likewise: -delta times `ds_in`
+    const float* ndelta;   // likewise: -delta
     long long qpad;
-    // dS = P (dP ds_in + ndelta); the sums of dS B1 and of P B2 times ds_out and p_out. factor: ds_in and ds_out of
-    // each batch entry and key head instead, or NULL
-    float ds_in, ds_out, p_out;
-    const float2* factor;
+    const unsigned* norms; // float16: the largest squared norms of each batch entry's and key head's dout and v, or NULL
     const int* index;      // packed key -> key, or NULL
     long long rows_k;
+    int blocks;            // of the role
 };
-// The backward of three planes, heads of up to 64; x: the row operands, then the walked ones.
-cudaError_t launch_attn_bwd_wide(const BwdArgs& g, bool keys, const TcTensor (&x)[4], cudaStream_t st);
+struct BwdTensors {
+    TcTensor q, dout, k, v, q_walk, dout_walk, k_walk, v_walk;  // as row tiles; as walked tiles
+};
+// The backward of three planes, heads of up to 64: the roles of queries and of keys.
+cudaError_t launch_attn_bwd_wide(const BwdArgs& gq, const BwdArgs& gk, const BwdTensors& x, bool keys_first, cudaStream_t st);
 
 struct TcBwd {
     AttnArgs a;
     const int *count, *index;    // of the key mask, or NULL
     float *nlse, *ndelta;        // [batch x heads][qpad], written first
-    unsigned* norms;             // float16: [batch x kv_heads][2], as is factor
-    float2* factor;
-    float* part;                 // shares of dq and then of dk and dv, where splits > 1
+    unsigned* norms;             // float16: [batch x kv_heads][2], zero
+    float *part_q, *part_k;      // shares of dq and of dk and dv, or NULL
     long long qpad, rows_k;
     int dp, splits_q, splits_k;  // of the walk for dq, and for dk and dv
+    bool keys_first;
 };
-// dq, then dk and dv of the keys that take part. The tensors as row tiles, then as walked tiles.
-cudaError_t launch_attn_bwd_tc(const TcBwd& w, const TcTensor& q, const TcTensor& dout, const TcTensor& k, const TcTensor& v,
-                               const TcTensor& q64, const TcTensor& dout64, const TcTensor& k64, const TcTensor& v64,
-                               cudaStream_t st);
-// dk = dv = 0 at keys that take no part.
-cudaError_t launch_attn_zero(const AttnArgs& a, cudaStream_t st);
+// dq, dk and dv.
+cudaError_t launch_attn_bwd_tc(const TcBwd& w, const BwdTensors& x, cudaStream_t st);
 
 }  // namespace gs
