@@ -15,6 +15,8 @@ constexpr int kMaxTcDim = 128;
 struct Plan {
     bool tc, decode, pack_q, pack_kv, pack_do, keys_first;
     int planes, dp, nq, splits;
+    int tiles, tail;         // forward: of a head's queries; blocks whose walk is split
+    long long whole;         // blocks that walk all keys
     int splits_q, splits_k;  // backward: of the walks for dq, and for dk and dv
     long long rows_k;        // rows of a packed head of K or V
     long long qpad;          // queries of a head, rounded up to the tiles that the backward walks
@@ -43,7 +45,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         // two blocks an SM, with at least 64 keys each
         p.tc = false;
         p.decode = true;
-        p.dp = a.d;
+        p.dp = (a.d + 3) / 4 * 4;
         const long long blocks = (long long)bk, most = (a.len_k + 63) / 64;
         long long splits = 2 * device_sm_count() / (blocks > 0 ? blocks : 1);
         if (splits > most) splits = most;
@@ -62,29 +64,38 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         p.pack_q = wide || !tensors || !copyable(a.q, a, a.len_q);
         p.pack_do = backward && (wide || !tensors || !copyable(a.dout, a, a.len_q));
         p.pack_kv = wide || masked || !tensors || !copyable(a.k, a, a.len_k) || !copyable(a.v, a, a.len_k);
-        // Few blocks: the walk is split, at least `least` tiles each, so that every SM has one.
         const int sms = device_sm_count();
-        auto split = [&](long long blocks, long long tiles, long long least) {
-            long long s = blocks > 0 ? sms / blocks : 1;
-            if (s > (tiles + least - 1) / least) s = (tiles + least - 1) / least;
-            return s < 1 ? 1 : (int)s;
-        };
         auto over = [](long long n, long long m) { return (n + m - 1) / m; };
         if (!backward) {
-            // Two query tiles per block work beside each other; a block of one takes 0.81 (16-bit heads of 64) to 0.89
-            // (128) of their time. So two, unless blocks of one fill the last round of the SMs better: 2432 queries of
-            // 16 heads of 64 over 2500 keys are 160 blocks of two, 45.7 us, or 304 of one, 38.5 us; 4864 are 47 and 76 us.
-            auto rounds = [&](int tiles) { return over(over(a.len_q, 128 * tiles) * a.heads * a.batch, sms); };
-            const bool two = !(wide && p.dp == 128) && 100 * rounds(2) <= 85 * rounds(1);
-            p.nq = two ? 2 : 1;
-            p.splits = split(over(a.len_q, 128 * p.nq) * a.heads * a.batch, p.rows_k / kTileRows, 2);
+            // Whole rounds of the SMs walk all keys; the blocks of the last round split their walks where that fills it.
+            // A split block costs about `extra` tiles' time at its start and end, the shares' joining as much again. 5000 x
+            // 2500 float32, 16 heads of 64 (2 rounds and 16 blocks): 293 us whole, 229 us with nine shares; 16384 x 4346
+            // bf16, 32 heads (13 rounds and 72 blocks): 501 and 491 us. Two query tiles per block work beside each
+            // other; a block of one takes 0.81 (16-bit heads of 64) to 0.89 (128) of their time.
+            const long long extra = wide ? 2 : 3, walk = p.rows_k / kTileRows;
+            long long best = 0;
+            for (int nq = wide && p.dp == 128 ? 1 : 2; nq >= 1; --nq) {
+                const long long tiles = over(a.len_q, 128 * nq), blocks = tiles * a.heads * a.batch, tail = blocks % sms;
+                for (long long s = 1; s == 1 || (tail > 0 && 2 * s <= walk && tail * s <= 4 * sms); ++s) {
+                    const long long time = (blocks / sms * (walk + extra) + over(tail * s, sms) * (over(walk, s) + extra) +
+                                            (s > 1 ? extra : 0)) * (nq == 1 ? 85 : 100);
+                    if (p.nq && time >= best) continue;
+                    best = time;
+                    p.nq = nq;
+                    p.splits = (int)s;
+                    p.tiles = (int)tiles;
+                    p.tail = s > 1 ? (int)tail : 0;
+                    p.whole = blocks - p.tail;
+                }
+            }
         } else {
             p.qpad = over(a.len_q, kBN) * kBN;
-            // A block walks no more than an SM's share of all walks, or than four tiles.
+            // A block walks at most one and a half times an SM's share of all walks, at least four tiles: 500 x 2500 bf16, 8
+            // heads of 64, splits of 3: 25.4 us, 2: 25.4; 4000 x 500: 1: 43.2, 2: 32.9, 3: 34.4, 8: 44.2 us.
             const long long walk_q = over(a.len_k, kBN), walk_k = p.qpad / kBN * (a.heads / a.kv_heads),
                             all = over(a.len_q, kTileRows) * a.heads * a.batch * walk_q +
                                   over(a.len_k, kTileRows) * a.kv_heads * a.batch * walk_k,
-                            share = all > 4ll * sms ? over(all, sms) : 4;
+                            share = 3 * all > 8ll * sms ? over(3 * all, 2 * sms) : 4;
             p.splits_q = (int)over(walk_q, share);
             p.splits_k = (int)over(walk_k, share);
             p.keys_first = over(walk_k, p.splits_k) > over(walk_q, p.splits_q);
@@ -107,8 +118,9 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             if (p.splits_q > 1) p.part = take((size_t)p.splits_q * bq * p.dp * sizeof(float));
             if (p.splits_k > 1) p.part_k = take((size_t)p.splits_k * 2 * bk * p.rows_k * p.dp * sizeof(float));
         } else if (p.splits > 1) {
-            p.part = take((size_t)p.splits * bq * p.dp * sizeof(float));
-            p.part_lse = take((size_t)p.splits * bq * sizeof(float));
+            const size_t rows = (size_t)p.splits * p.tail * p.nq * kTileRows;
+            p.part = take(rows * p.dp * sizeof(float));
+            p.part_lse = take(rows * sizeof(float));
         }
     }
     p.bytes = at;
@@ -184,13 +196,15 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
         float* part = p.splits > 1 ? reinterpret_cast<float*>(ws + p.part) : nullptr;
         float* part_lse = p.splits > 1 ? reinterpret_cast<float*>(ws + p.part_lse) : nullptr;
         e = launch_attn_decode(a, p.splits, p.dp, part, part_lse, st);
-        return e || !part ? e : launch_attn_combine(a, part, part_lse, p.splits, p.dp, st);
+        const TcArgs t{a, nullptr, part, part_lse, 1, p.splits, 0, a.batch * a.heads};
+        return e || !part ? e : launch_attn_combine(t, 1, p.dp, st);
     }
     if (!p.tc) return launch_attn_simt(a, false, st);
+    if (p.whole > 0x7fffff00ll) return cudaErrorInvalidConfiguration;
     int *count, *index;
     e = lay_out(p, a, ws, count, index, st);
     if (e) return e;
-    TcArgs t{a, count, nullptr, nullptr, 0, p.splits};
+    TcArgs t{a, count, nullptr, nullptr, p.tiles, p.splits, (int)p.whole, p.tail};
     const int bn = p.planes == 3 && p.dp == 128 ? 64 : 128;
     TcTensor q, k, v;
     if ((e = operand(q, p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, kTileRows)) ||
@@ -202,7 +216,7 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
         t.part_lse = reinterpret_cast<float*>(ws + p.part_lse);
     }
     if ((e = launch_attn_fwd_tc(t, q, k, v, p.planes, p.dp, p.nq, st))) return e;
-    return p.splits > 1 ? launch_attn_combine(a, t.part, t.part_lse, p.splits, p.dp, st) : cudaSuccess;
+    return p.splits > 1 ? launch_attn_combine(t, p.nq * kTileRows, p.dp, st) : cudaSuccess;
 }
 
 cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t st) {

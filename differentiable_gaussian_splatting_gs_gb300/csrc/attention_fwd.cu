@@ -65,15 +65,13 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     __shared__ uint32_t tmem_base;
     const AttnArgs& a = t.a;
     const uint32_t sq = (smem_u32(raw) + 1023u) & ~1023u, sk = sq + NQ * S::kQ, sv = sk + kSt * S::kKV;
-    int at = blockIdx.x;
-    const int tile = at % t.tiles;
-    at /= t.tiles;
-    const int split = at % t.splits;
-    at /= t.splits;
-    const int h = at % a.heads, b = at / a.heads, hk = h / (a.heads / a.kv_heads);
+    const bool whole = (int)blockIdx.x < t.whole;
+    const int shared = (int)blockIdx.x - t.whole, split = whole ? 0 : shared % t.splits;
+    const int block = whole ? (int)blockIdx.x : t.whole + shared / t.splits, tile = block % t.tiles, bh = block / t.tiles;
+    const int h = bh % a.heads, b = bh / a.heads, hk = h / (a.heads / a.kv_heads);
     const int keys = keys_of(t, b), q0 = tile * NQ * kTileRows;
-    // this split's key tiles
-    const int all = (keys + BN - 1) / BN, per = (all + t.splits - 1) / t.splits;
+    // this block's key tiles
+    const int all = (keys + BN - 1) / BN, per = whole ? all : (all + t.splits - 1) / t.splits;
     const int first = min(split * per, all), n = min(per, all - first);
     const int warp = threadIdx.x >> 5;
     const unsigned limit = a.spin_limit;
@@ -418,8 +416,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         const float f = sum == 0.f ? 0.f : 1.f / sum;
         const float lse = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
         const long long qrow = ((long long)b * a.heads + h) * a.len_q + row;
-        if (t.part) {
-            const long long prow = (long long)split * a.batch * a.heads * a.len_q + qrow;
+        if (!whole) {
+            const long long prow = ((long long)split * t.tail + block - t.whole) * (NQ * kTileRows) + row - q0;
             if (live) t.part_lse[prow] = lse;
             if (n > 0) {
 #pragma unroll
@@ -482,8 +480,7 @@ cudaError_t run(TcArgs t, const TcTensor& q, const TcTensor& k, const TcTensor& 
     auto* kernel = k_attn_fwd<T, DP, PL, NQ, BN>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e) return e;
-    t.tiles = (t.a.len_q + NQ * kTileRows - 1) / (NQ * kTileRows);
-    const long long blocks = (long long)t.tiles * t.splits * t.a.heads * t.a.batch;
+    const long long blocks = t.whole + (long long)t.tail * t.splits;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     count_launches(1);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, st, t, q, k, v);

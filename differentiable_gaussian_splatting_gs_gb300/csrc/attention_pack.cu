@@ -87,73 +87,74 @@ __global__ void __launch_bounds__(256) k_attn_pack(const AttnArgs a, const PackJ
     }
 }
 
-// The shares weighted by exp(lse - max lse), WARPS warps to a query and head, each with its part of the shares; they are
-// joined in order.
-template <class T, int WARPS>
-__global__ void __launch_bounds__(256) k_attn_combine(const AttnArgs a, const float* part, const float* part_lse, int splits,
-                                                      int dp) {
+// The shares weighted by exp(lse - max lse): 2^log_lanes threads to a query and head, four columns each, GROUPS times,
+// each group with every GROUPS-th share; the groups are joined in order. Eight shares are under way together: the loads'
+// latency bounds it (18,432 rows of two shares, or 4,096 of nine, of 64 columns: 5 us).
+template <class T, int GROUPS>
+__global__ void __launch_bounds__(256) k_attn_combine(const TcArgs t, int per, int dp, int log_lanes) {
     pdl_entry();
-    __shared__ float meet[WARPS > 1 ? WARPS : 1][256 + 2];
-    const long long rows = (long long)a.batch * a.heads * a.len_q;
-    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / (32 * WARPS);
-    if (row >= rows) return;
-    const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0, i = (int)(row % a.len_q);
-    const long long bh = row / a.len_q;
-    const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
-    constexpr int kMost = 8, kAhead = 4;  // columns of a lane (heads of up to 256), shares under way
-    float o[kMost] = {}, total = 0.f, top = -INFINITY;
-    for (int s0 = warp; s0 < splits; s0 += WARPS * kAhead) {
-        float l[kAhead], x[kAhead][kMost], m = top;
+    constexpr int kAhead = 8;
+    __shared__ float meet[GROUPS > 1 ? 6 : 1][256];
+    const AttnArgs& a = t.a;
+    const long long rows = (long long)t.tail * per, unit = ((long long)blockIdx.x * 256 + threadIdx.x) >> log_lanes;
+    const long long row = unit / GROUPS;
+    const int group = GROUPS > 1 ? (int)(unit % GROUPS) : 0, col = (threadIdx.x & ((1 << log_lanes) - 1)) * 4;
+    const int block = t.whole + (int)(row / per), bh = block / t.tiles, i = block % t.tiles * per + (int)(row % per);
+    const int b = bh / a.heads, h = bh % a.heads;
+    const bool in = row < rows && i < a.len_q && col < a.d;
+    float o[4] = {}, total = 0.f, top = -INFINITY;
+    for (int s0 = group; s0 < t.splits && in; s0 += GROUPS * kAhead) {
+        float l[kAhead], m = top;
+        float4 x[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int s = s0 + u * WARPS;
-            l[u] = s < splits ? part_lse[s * rows + row] : -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kMost; ++k)
-                if (s < splits && lane + 32 * k < a.d) x[u][k] = part[(s * rows + row) * dp + lane + 32 * k];
+            const int s = min(s0 + u * GROUPS, t.splits - 1);
+            l[u] = t.part_lse[s * rows + row];
+            x[u] = *reinterpret_cast<const float4*>(t.part + (s * rows + row) * dp + col);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) m = fmaxf(m, l[u]);
+        for (int u = 0; u < kAhead; ++u) {
+            if (s0 + u * GROUPS >= t.splits) l[u] = -INFINITY;
+            m = fmaxf(m, l[u]);
+        }
         const float zero = m == -INFINITY ? 0.f : m, keep = expf(top - zero);
         top = m;
         total *= keep;
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) o[k] *= keep;
+        for (int k = 0; k < 4; ++k) o[k] *= keep;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
+            if (l[u] == -INFINITY) continue;  // a share without keys was not written
             const float w = expf(l[u] - zero);
             total += w;
-#pragma unroll
-            for (int k = 0; k < kMost; ++k)
-                if (lane + 32 * k < a.d) o[k] += l[u] == -INFINITY ? 0.f : w * x[u][k];  // a share without keys was not written
+            o[0] += w * x[u].x, o[1] += w * x[u].y, o[2] += w * x[u].z, o[3] += w * x[u].w;
         }
     }
-    if (WARPS > 1) {
+    if (GROUPS > 1) {
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) meet[warp][lane + 32 * k] = o[k];
-        if (lane == 0) meet[warp][256] = top, meet[warp][257] = total;
+        for (int k = 0; k < 4; ++k) meet[k][threadIdx.x] = o[k];
+        meet[4][threadIdx.x] = top;
+        meet[5][threadIdx.x] = total;
         __syncthreads();
-        if (warp != 0) return;
-        float m = -INFINITY;
+        if (group != 0) return;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, meet[w][256]);
-        total = 0.f;
-        top = m;
+        for (int g = 1; g < GROUPS; ++g) top = fmaxf(top, meet[4][threadIdx.x + (g << log_lanes)]);
+        total = o[0] = o[1] = o[2] = o[3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) o[k] = 0.f;
+        for (int g = 0; g < GROUPS; ++g) {
+            const int at = threadIdx.x + (g << log_lanes);
+            const float keep = expf(meet[4][at] - (top == -INFINITY ? 0.f : top));
+            total = fmaf(keep, meet[5][at], total);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const float keep = expf(meet[w][256] - (m == -INFINITY ? 0.f : m));
-            total = fmaf(keep, meet[w][257], total);
-#pragma unroll
-            for (int k = 0; k < kMost; ++k) o[k] = fmaf(keep, meet[w][lane + 32 * k], o[k]);
+            for (int k = 0; k < 4; ++k) o[k] = fmaf(keep, meet[k][at], o[k]);
         }
     }
+    if (!in) return;
     T* dst = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride + i * a.out.len_stride;
 #pragma unroll
-    for (int k = 0; k < kMost; ++k)
-        if (lane + 32 * k < a.d) dst[lane + 32 * k] = from_float<T>(total == 0.f ? 0.f : o[k] / total);
-    if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : top + logf(total);
+    for (int k = 0; k < 4; ++k)
+        if (col + k < a.d) dst[col + k] = from_float<T>(total == 0.f ? 0.f : o[k] / total);
+    if (col == 0) a.lse[(long long)bh * a.len_q + i] = total == 0.f ? -INFINITY : top + logf(total);
 }
 
 cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st) {
@@ -178,14 +179,17 @@ cudaError_t launch_attn_pack(const AttnArgs& a, const PackJob* jobs, int n, cons
     return launch_pdl(kernel, grid, dim3(256), 0, st, a, all, count, index, dp);
 }
 
-cudaError_t launch_attn_combine(const AttnArgs& a, const float* part, const float* part_lse, int splits, int dp, cudaStream_t st) {
-    const bool many = splits > 4;  // a block per row: eight times four shares under way together
-    const long long rows = (long long)a.batch * a.heads * a.len_q, blocks = many ? rows : (rows + 7) / 8;
-    auto* kernel = a.dtype == GS_DTYPE_F32   ? (many ? k_attn_combine<float, 8> : k_attn_combine<float, 1>)
-                   : a.dtype == GS_DTYPE_F16 ? (many ? k_attn_combine<__half, 8> : k_attn_combine<__half, 1>)
-                                             : (many ? k_attn_combine<__nv_bfloat16, 8> : k_attn_combine<__nv_bfloat16, 1>);
+cudaError_t launch_attn_combine(const TcArgs& t, int rows, int dp, cudaStream_t st) {
+    const bool many = t.splits > 8;  // more than are under way together
+    int log_lanes = 0;
+    while (4 << log_lanes < dp) ++log_lanes;
+    const long long threads = ((long long)t.tail * rows * (many ? 4 : 1)) << log_lanes;
+    const int type = t.a.dtype;
+    auto* kernel = type == GS_DTYPE_F32   ? (many ? k_attn_combine<float, 4> : k_attn_combine<float, 1>)
+                   : type == GS_DTYPE_F16 ? (many ? k_attn_combine<__half, 4> : k_attn_combine<__half, 1>)
+                                          : (many ? k_attn_combine<__nv_bfloat16, 4> : k_attn_combine<__nv_bfloat16, 1>);
     count_launches(1);
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, part, part_lse, splits, dp);
+    return launch_pdl(kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, t, rows, dp, log_lanes);
 }
 
 }  // namespace gs
