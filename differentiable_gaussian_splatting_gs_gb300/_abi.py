@@ -7,11 +7,14 @@ library has not been built: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libgs_gb300.so")
+BIND_PATH = os.path.join(_PKG, "_build", "gs_bind.so")
 
 GS_OK = 0
 GS_ERR_ARG = -1
@@ -99,6 +102,7 @@ class GsError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 def load():
@@ -181,6 +185,28 @@ def load():
             getattr(lib, name).restype = C.c_int
         _lib = lib
         return lib
+
+
+def binding():
+    """The compiled module of the decoder operators' calls on torch tensors (csrc/bind.cpp); raises if it is missing."""
+    return _binding or _load_binding()
+
+
+def _load_binding():
+    global _binding
+    load()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BIND_PATH):
+                raise RuntimeError(f"{BIND_PATH} is not built; call __graft_entry__.build() or "
+                                   "differentiable_gaussian_splatting_gs_gb300.build.build_library()")
+            import torch  # its libraries are loaded before the module
+            loader = importlib.machinery.ExtensionFileLoader("gs_bind", BIND_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gs_bind", BIND_PATH, loader=loader))
+            loader.exec_module(module)
+            module.init(check, torch.OutOfMemoryError)
+            _binding = module
+    return _binding
 
 
 def check(status: int, where: str) -> int:

@@ -3,7 +3,8 @@
 The functions carry the C entry points' names (gs_preprocess, gs_bin_and_sort, gs_render_fwd,
 gs_render_bwd, gs_preprocess_bwd). They allocate outputs with torch when the caller passes none,
 marshal pointers and the current CUDA stream, and raise GsError on a non-zero status. All
-arithmetic runs in libgs_gb300.so.
+arithmetic runs in libgs_gb300.so. The calls of the decoder's operators (layer norm, cross attention) go
+through a compiled module (csrc/bind.cpp) instead of ctypes, with the same checks and errors.
 
 Dtypes: arrays the C ABI declares as uint32 (vals, tile ranges, contributor counts,
 tiles_touched) are torch.int32 tensors holding the same bits; 64-bit keys are torch.int64.
@@ -12,7 +13,6 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
-import functools
 
 import torch
 
@@ -23,7 +23,7 @@ from ._abi import (GS_BWD_ADAPTIVE, GS_BWD_DIRECT, GS_BWD_SM, GS_BWD_WARP, GS_ER
 __all__ = ["Proj", "BinResult", "StepContext", "gs_train_step_host", "make_camera", "make_options", "alloc_proj", "gs_preprocess",
            "gs_sort_workspace_bytes", "gs_bin_and_sort", "gs_bin_and_sort_async", "gs_render_fwd", "gs_render_bwd",
            "gs_preprocess_bwd", "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_cross_attention_fwd",
-           "gs_cross_attention_bwd",
+           "gs_cross_attention_bwd", "gs_cross_attention_workspace_bytes",
            "gs_device_error", "GsError", "GS_BWD_DIRECT", "GS_BWD_WARP", "GS_BWD_ADAPTIVE", "GS_BWD_SM"]
 
 
@@ -419,187 +419,35 @@ def gs_preprocess2d_bwd(params: dict, cam, opt: gs_options, proj: Proj, grad2d, 
     return out
 
 
-DTYPES = {torch.float32: _abi.GS_DTYPE_F32, torch.float16: _abi.GS_DTYPE_F16, torch.bfloat16: _abi.GS_DTYPE_BF16}
-
-# The decoder's operators are called many times a step on small tensors, where the host's work counts: their bindings
-# ask torch for as little as they can (a torch.cuda.device block or a Stream object costs as much as a launch).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _dtype(t, where: str) -> int:
-    code = DTYPES.get(t.dtype)
-    if code is None or not t.is_cuda:
-        raise ValueError(f"{where}: tensors must be float32, float16 or bfloat16 CUDA tensors")
-    return code
-
-
-def _call(like, stream, function, *args) -> int:
-    """function(*args, stream) on like's device: `stream`, or that device's current stream."""
-    index = like.get_device()
-    if torch.cuda.current_device() == index:
-        return function(*args, _raw_stream(index) if stream is None else _stream(stream))
-    with torch.cuda.device(index):
-        return function(*args, _raw_stream(index) if stream is None else _stream(stream))
-
-
-def _alloc(shape, like, stream, dtype=None):
-    """A new tensor beside `like` that belongs to the stream it will be used on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+def _on(stream, like):
+    """A block on `stream` (a torch stream or a raw handle): its tensors belong to it, and the calls go to it."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
-
-
-def _rows(t, like, where: str):
-    """(rows, row stride) of a tensor of like's shape, dtype and device whose last dimension is contiguous and whose
-    other dimensions have one common stride."""
-    if t is not like and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
-        raise ValueError(f"{where}: a tensor of shape {tuple(like.shape)}, {like.dtype}, {like.device} is needed")
-    shape = t.shape
-    if shape and t.is_contiguous():
-        cols = shape[-1]
-        return t.numel() // cols if cols else 0, cols
-    if not shape or (shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{where}: the last dimension must be contiguous")
-    dims = [(n, st) for n, st in zip(shape[:-1], t.stride()[:-1]) if n > 1]
-    if not dims:
-        return 1, shape[-1]
-    for (_, outer), (n, inner) in zip(dims, dims[1:]):
-        if outer != n * inner:
-            raise ValueError(f"{where}: the rows must have one common stride")
-    return t.numel() // shape[-1], dims[-1][1]
-
-
-def _address(t) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _vector(t, like, where: str):
-    if t is not None and (t.shape != like.shape[-1:] or not t.is_contiguous() or t.get_device() != like.get_device() or
-                          (t.dtype is not like.dtype and t.dtype is not torch.float32)):
-        raise ValueError(f"{where}: weight and bias must be contiguous [{like.shape[-1]}] tensors of x's dtype or float32")
-
-
-def _floats(t, shape, like, where: str):
-    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != like.get_device():
-        raise ValueError(f"{where}: a contiguous float32 tensor of shape {tuple(shape)} on {like.device} is needed")
+    return torch.cuda.stream(stream)
 
 
 def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
     """Layer norm over the last dimension: (y, mean, rstd); mean and rstd float32 [rows]. weight, bias:
     [cols] of x's dtype or float32 (both the same), or None. out: (y, mean, rstd) to write into."""
-    where = "gs_layer_norm_fwd"
-    dtype = _dtype(x, where)
-    rows, xs = _rows(x, x, where)
-    _vector(weight, x, where)
-    _vector(bias, x, where)
-    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
-        raise ValueError(f"{where}: weight and bias must have one dtype")
-    given = weight if weight is not None else bias
-    if out is None:
-        y, ys = _alloc(x.shape, x, stream), x.shape[-1]
-        mean, rstd = _alloc((rows,), x, stream, torch.float32), _alloc((rows,), x, stream, torch.float32)
-    else:
-        y, mean, rstd = out
-        ys = _rows(y, x, where)[1]
-        _floats(mean, (rows,), x, where)
-        _floats(rstd, (rows,), x, where)
-    check(_call(x, stream, _abi.load().gs_layer_norm_fwd, x.data_ptr(), xs, rows, x.shape[-1], dtype, _address(weight),
-                _address(bias), dtype if given is None else DTYPES[given.dtype], eps, y.data_ptr(), ys, mean.data_ptr(),
-                rstd.data_ptr()), where)
-    return y, mean, rstd
-
-
-@functools.lru_cache(maxsize=4096)
-def _norm_workspace_bytes(rows: int, cols: int) -> int:
-    return int(_abi.load().gs_layer_norm_workspace_bytes(rows, cols))
+    if stream is not None:
+        with _on(stream, x):
+            return gs_layer_norm_fwd(x, weight, bias, eps, out)
+    return _abi.binding().layer_norm_fwd(x, weight, bias, eps, out)
 
 
 def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, stream=None):
     """Backward of gs_layer_norm_fwd: (dx, dweight, dbias); the last two are None without a weight (a layer
-    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into."""
-    where = "gs_layer_norm_bwd"
-    dtype = _dtype(x, where)
-    rows, xs = _rows(x, x, where)
-    cols = x.shape[-1]
-    _vector(weight, x, where)
-    _floats(mean, (rows,), x, where)
-    _floats(rstd, (rows,), x, where)
-    if out is None:
-        dx, dxs = _alloc(x.shape, x, stream), cols
-        dweight, dbias = (None, None) if weight is None else (_alloc((cols,), weight, stream), _alloc((cols,), weight, stream))
-        kind = weight
-    else:
-        dx, dweight, dbias = out
-        dxs = _rows(dx, x, where)[1]
-        _vector(dweight, x, where)
-        _vector(dbias, x, where)
-        kinds = [t for t in (weight, dweight, dbias) if t is not None]
-        kind = kinds[0] if kinds else None
-        if any(t.dtype is not kind.dtype for t in kinds):
-            raise ValueError(f"{where}: weight, dweight and dbias must have one dtype")
-    need = _norm_workspace_bytes(rows, cols) if dweight is not None or dbias is not None else 0
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = _alloc((need,), x, stream, torch.uint8)
-    check(_call(x, stream, _abi.load().gs_layer_norm_bwd, dy.data_ptr(), _rows(dy, x, where)[1], x.data_ptr(), xs, rows, cols,
-                dtype, mean.data_ptr(), rstd.data_ptr(), _address(weight), dtype if kind is None else DTYPES[kind.dtype],
-                dx.data_ptr(), dxs, _address(dweight), _address(dbias), _address(workspace) if need else None, need), where)
-    return dx, dweight, dbias
-
-
-def _heads(t, shape, dtype, device: int, where: str) -> _abi.gs_heads:
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
-        raise ValueError(f"{where}: a tensor of shape {tuple(shape)}, {dtype}, on cuda:{device} is needed, "
-                         f"got {tuple(t.shape)}, {t.dtype}, {t.device}")
-    b, n, h, d = t.stride()
-    if d != 1 and shape[3] > 1:
-        raise ValueError(f"{where}: the elements of a head must be contiguous")
-    return _abi.gs_heads(t.data_ptr(), b, n, h)
-
-
-def _attention(q, k, k_len, key_mask, scale, where: str):
-    """(gs_attention, q's shape, k's and v's shape, what the workspace's size depends on)"""
-    code, device = _dtype(q, where), q.device
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"{where}: q, k and v must be [batch, length, heads, head_dim]")
-    b, lq, h, d = q.shape
-    _, lk, hk, _ = k.shape
-    if h < 1 or hk < 1 or h % hk:
-        raise ValueError(f"{where}: {h} query heads must be a multiple of {hk} key heads")
-    if k_len is not None and (k_len.shape != (b,) or k_len.dtype != torch.int32 or not k_len.is_contiguous() or
-                              k_len.device != device):
-        raise ValueError(f"{where}: k_len must be a contiguous int32 [{b}] tensor on {device}")
-    if key_mask is not None and (key_mask.shape != (b, lk) or key_mask.dtype not in (torch.bool, torch.uint8) or
-                                 (lk > 1 and key_mask.stride(1) != 1) or key_mask.device != device):
-        raise ValueError(f"{where}: key_mask must be a bool or uint8 [{b}, {lk}] tensor on {device} with contiguous rows")
-    if scale is not None and not scale > 0:
-        raise ValueError(f"{where}: scale must be positive")
-    a = _abi.gs_attention(code, b, h, hk, d, lq, lk, scale or 0.0, _address(k_len), _address(key_mask),
-                          0 if key_mask is None else key_mask.stride(0))
-    return a, (b, lq, h, d), (b, lk, hk, d), (q.get_device(), code, b, h, hk, d, lq, lk, k_len is not None, key_mask is not None)
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_workspace_bytes(backward, device, dtype, b, h, hk, d, lq, lk, k_len, key_mask) -> int:
-    # only whether there is a length or a mask counts, and the current device's number of SMs
-    a = _abi.gs_attention(dtype, b, h, hk, d, lq, lk, 0.0, 16 if k_len else None, 16 if key_mask else None)
-    with torch.cuda.device(device):
-        return int(_abi.load().gs_cross_attention_workspace_bytes(C.byref(a), backward))
-
-
-def _attention_workspace(key, backward: int, workspace, like, stream):
-    need = _attention_workspace_bytes(backward, *key)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = _alloc((need,), like, stream, torch.uint8)
-    return workspace, need
+    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into. workspace: a byte tensor
+    kept by the caller (allocated when None or too small)."""
+    if stream is not None:
+        with _on(stream, x):
+            return gs_layer_norm_bwd(dy, x, mean, rstd, weight, out, workspace)
+    return _abi.binding().layer_norm_bwd(dy, x, mean, rstd, weight, out, workspace)
 
 
 def gs_cross_attention_workspace_bytes(q, k, v, k_len=None, key_mask=None, backward: bool = False) -> int:
     """Bytes of workspace that gs_cross_attention_fwd / _bwd of these tensors use."""
-    return _attention_workspace_bytes(int(backward), *_attention(q, k, k_len, key_mask, None, "gs_cross_attention_workspace_bytes")[3])
+    return _abi.binding().cross_attention_workspace_bytes(q, k, k_len, key_mask, backward)
 
 
 def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | None = None, out=None, workspace=None,
@@ -609,36 +457,19 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     k_len: int32 [batch], keys that count per batch entry; key_mask: bool [batch, len_k], True where a key
     counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a byte
     tensor kept by the caller (allocated when None or too small)."""
-    where, dtype, device = "gs_cross_attention_fwd", q.dtype, q.get_device()
-    a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
-    hq, hk, hv = _heads(q, qs, dtype, device, where), _heads(k, kvs, dtype, device, where), _heads(v, kvs, dtype, device, where)
-    stats = (qs[0], qs[2], qs[1])
-    if out is None:
-        o, lse = _alloc(qs, q, stream), _alloc(stats, q, stream, torch.float32)
-    else:
-        o, lse = out
-        _floats(lse, stats, q, where)
-    ho = _heads(o, qs, dtype, device, where)
-    workspace, need = _attention_workspace(key, 0, workspace, q, stream)
-    check(_call(q, stream, _abi.load().gs_cross_attention_fwd, C.byref(a), C.byref(hq), C.byref(hk), C.byref(hv), C.byref(ho),
-                lse.data_ptr(), workspace.data_ptr() if need else None, need), where)
-    return o, lse
+    if stream is not None:
+        with _on(stream, q):
+            return gs_cross_attention_fwd(q, k, v, k_len, key_mask, scale, out, workspace)
+    return _abi.binding().cross_attention_fwd(q, k, v, k_len, key_mask, scale, out, workspace)
 
 
 def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, scale: float | None = None, grads=None,
                            workspace=None, stream=None):
     """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given."""
-    where, dtype, device = "gs_cross_attention_bwd", q.dtype, q.get_device()
-    a, qs, kvs, key = _attention(q, k, k_len, key_mask, scale, where)
-    ins = [_heads(t, s, dtype, device, where) for t, s in ((dout, qs), (q, qs), (k, kvs), (v, kvs), (out, qs))]
-    _floats(lse, (qs[0], qs[2], qs[1]), q, where)
-    if grads is None:
-        grads = (_alloc(qs, q, stream), _alloc(kvs, q, stream), _alloc(kvs, q, stream))
-    outs = [_heads(t, s, dtype, device, where) for t, s in zip(grads, (qs, kvs, kvs))]
-    workspace, need = _attention_workspace(key, 1, workspace, q, stream)
-    check(_call(q, stream, _abi.load().gs_cross_attention_bwd, C.byref(a), *map(C.byref, ins), lse.data_ptr(), *map(C.byref, outs),
-                workspace.data_ptr() if need else None, need), where)
-    return tuple(grads)
+    if stream is not None:
+        with _on(stream, q):
+            return gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len, key_mask, scale, grads, workspace)
+    return _abi.binding().cross_attention_bwd(dout, q, k, v, out, lse, k_len, key_mask, scale, grads, workspace)
 
 
 def gs_kernel_launches() -> int:

@@ -1,15 +1,18 @@
 """Builds the CUDA library libgs_gb300.so in-tree with nvcc for sm_103a.
 
 The translation units under csrc/ are compiled in parallel and linked into one shared object
-with the C ABI of include/gs.h. The output goes to `_build/` beside this file.
+with the C ABI of include/gs.h; csrc/bind.cpp becomes the Python module gs_bind.so, which calls it on
+torch tensors. The output goes to `_build/` beside this file.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgs_gb300.so")
+BIND = os.path.join(BUILD, "gs_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,6 +46,21 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_commands(src: str, obj: str, out: str, nvcc: str) -> tuple[list[str], list[str]]:
+    """The host compiler's commands for the Python module of the decoder operators' calls: compile, link."""
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    torch_lib = os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cxx = os.environ.get("CXX") or "g++"
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE] + [f for d in include for f in ("-isystem", d)] +
+            ["-c", src, "-o", obj],
+            [cxx, "-shared", obj, "-o", out, "-L" + torch_lib, "-L" + BUILD] +
+            ["-l" + x for x in ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch_python")] +
+            ["-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN:" + torch_lib])
+
+
 def build_library(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -56,16 +75,20 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc] + flags + ["-c", src, "-o", obj])
 
+    bind, bind_obj, bind_tmp = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o"), BIND + f".tmp{os.getpid()}"
+    bind_compile, bind_link = _bind_commands(bind, bind_obj, bind_tmp, nvcc)
+    bind_jobs = [bind_compile] if force or _stale(bind_obj, [bind, os.path.join(INCLUDE, "gs.h")]) else []
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed ({r.returncode}):\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed ({r.returncode}):\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        for msg in ex.map(run, jobs):
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs + bind_jobs), os.cpu_count() or 1))) as ex:
+        for msg in ex.map(run, bind_jobs + jobs):
             if verbose and msg:
                 print(msg)
     if force or jobs or _stale(LIB, objs):
@@ -73,6 +96,9 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
         run([nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs +
             ["-Xlinker", "-rpath," + _cuda_lib_dir(nvcc)])
         os.replace(tmp, LIB)
+    if bind_jobs or _stale(BIND, [bind_obj]):
+        run(bind_link)
+        os.replace(bind_tmp, BIND)
     return LIB
 
 

@@ -3,6 +3,8 @@
 
 #include "attention_tc.cuh"
 
+#include <algorithm>
+
 namespace gs {
 
 namespace {
@@ -76,7 +78,10 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             long long best = 0;
             for (int nq = wide && p.dp == 128 ? 1 : 2; nq >= 1; --nq) {
                 const long long tiles = over(a.len_q, 128 * nq), blocks = tiles * a.heads * a.batch, tail = blocks % sms;
-                for (long long s = 1; s == 1 || (tail > 0 && 2 * s <= walk && tail * s <= 4 * sms); ++s) {
+                for (int rounds = 0; rounds <= (tail > 0 ? 4 : 0); ++rounds) {  // that the shares take; 0: no split
+                    long long s = rounds == 0 ? 1 : std::min((long long)sms * rounds / tail, walk / 2);
+                    if (rounds > 0 && s < 2) continue;
+                    s = over(walk, over(walk, s));  // no share without tiles
                     const long long time = (blocks / sms * (walk + extra) + over(tail * s, sms) * (over(walk, s) + extra) +
                                             (s > 1 ? extra : 0)) * (nq == 1 ? 85 : 100);
                     if (p.nq && time >= best) continue;

@@ -288,17 +288,19 @@ def test_waits_that_give_up_are_reported_and_leave_the_context_usable(dtype, d):
     dout = _rand(q.shape, dtype, 5)
     want = api.gs_cross_attention_fwd(q, k, v)
     grads = api.gs_cross_attention_bwd(dout, q, k, v, *want)
-    a, qs, kvs, key = api._attention(q, k, None, None, None, "test")
+    (b, lq, h, _), (_, lk, hk, _) = q.shape, k.shape
+    code = {torch.float32: _abi.GS_DTYPE_F32, torch.float16: _abi.GS_DTYPE_F16, torch.bfloat16: _abi.GS_DTYPE_BF16}[dtype]
+    a = _abi.gs_attention(code, b, h, hk, d, lq, lk)
     a.spin_limit = 1  # every wait gives up at its first poll
     lib, stream = _abi.load(), torch.cuda.current_stream().cuda_stream
     out, lse = torch.empty_like(q), torch.empty_like(want[1])
     spare = [torch.empty_like(t) for t in (q, k, v)]
 
     def heads(*ts):
-        return [C.byref(api._heads(t, t.shape, dtype, q.get_device(), "test")) for t in ts]
+        return [C.byref(_abi.gs_heads(t.data_ptr(), *t.stride()[:3])) for t in ts]
 
     for backward in (0, 1):
-        need = api._attention_workspace_bytes(backward, *key)
+        need = lib.gs_cross_attention_workspace_bytes(C.byref(a), backward)
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
         if backward:
             st = lib.gs_cross_attention_bwd(C.byref(a), *heads(dout, q, k, v, want[0]), want[1].data_ptr(), *heads(*spare),
