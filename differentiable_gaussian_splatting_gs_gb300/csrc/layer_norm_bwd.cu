@@ -21,8 +21,8 @@ struct NormBwdArgs {
     unsigned* err;
 };
 
-template <class T, int VEC, int NV, int LPR>
-__global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
+template <class T, int VEC, int NV, int LPR, int FULL>
+__global__ void __launch_bounds__(kNormBlock, NV * VEC >= 12 && NV * VEC <= 16 ? 2 : 1) k_norm_bwd(const NormBwdArgs a) {
     pdl_entry();
     extern __shared__ __align__(16) float share[];  // w; at the end the block's sums, 2 x cols
     __shared__ float buf[2 * 2 * kNormBlock / 32];
@@ -35,10 +35,9 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) dw[i][k] = db[i][k] = 0.f;
-    if (a.weight) {
-        stage_weights<VEC>(share, a.weight, a.wdtype, a.cols, 1.f);
-        __syncthreads();
-    }
+    auto in = [&](int i) { return i < FULL || l + i * LPR < nvec; };
+    stage_weights<VEC>(share, a.weight, a.wdtype, a.cols, 1.f);
+    __syncthreads();
     const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.dx);
     const long long step = (long long)gridDim.x * kRows;
@@ -60,6 +59,7 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
     for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / LPR;
         const bool live = row < a.rows;
+        if (LPR >= 32 && !live) break;  // the same in all threads of the row
         const float m = next_m, r = next_r;
         if (row + step < a.rows) {
             next_m = a.mean[row + step];
@@ -69,50 +69,59 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
         if constexpr (kRing) {
             if (live) {
                 ring.wait();
-                load_row<T, VEC, NV, LPR>(rx, reinterpret_cast<const T*>(ring.at(0)), l, nvec, true);
-                load_row<T, VEC, NV, LPR>(rd, reinterpret_cast<const T*>(ring.at(1)), l, nvec, true);
+                load_row<T, VEC, NV, LPR, FULL>(rx, reinterpret_cast<const T*>(ring.at(0)), l, nvec, true);
+                load_row<T, VEC, NV, LPR, FULL>(rd, reinterpret_cast<const T*>(ring.at(1)), l, nvec, true);
             }
         } else {
-            load_row<T, VEC, NV, LPR>(rx, x + row * a.x_stride, l, nvec, live);
-            load_row<T, VEC, NV, LPR>(rd, dy + row * a.dy_stride, l, nvec, live);
+            load_row<T, VEC, NV, LPR, FULL>(rx, x + row * a.x_stride, l, nvec, live);
+            load_row<T, VEC, NV, LPR, FULL>(rd, dy + row * a.dy_stride, l, nvec, live);
         }
-        float x1[VEC], d1[VEC], w[VEC], s0 = 0.f, s1 = 0.f;
+        // xhat and w dy of a 16-bit row, or of one read an element at a time, stay as floats: 139,072 x 1024 bfloat16
+        // takes 170 us when both are formed again for dx, 137 us so. Float32 vectors would take more registers than x and dy.
+        constexpr bool kKeep = VEC == 1 || sizeof(T) == 2;
+        float h[kKeep ? NV : 1][VEC], g[kKeep ? NV : 1][VEC], s[2] = {0.f, 0.f};
+        auto form = [&](int i, float (&hi)[VEC], float (&gi)[VEC], float (&d)[VEC]) {
+            load_floats<VEC>(gi, share, l + i * LPR, nvec);
+            unpack<T, VEC>(rx[i], hi);
+            unpack<T, VEC>(rd[i], d);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                hi[k] = (hi[k] - m) * r;
+                gi[k] *= d[k];
+            }
+        };
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (live && l + i * LPR < nvec) {
-                if (a.weight) load_floats<VEC>(w, share, l + i * LPR, nvec);
-                unpack<T, VEC>(rx[i], x1);
-                unpack<T, VEC>(rd[i], d1);
+            if (live && in(i)) {
+                float d[VEC];
+                auto &hi = h[kKeep ? i : 0], &gi = g[kKeep ? i : 0];
+                form(i, hi, gi, d);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    const float h = (x1[k] - m) * r, g = a.weight ? d1[k] * w[k] : d1[k];
-                    dw[i][k] = fmaf(d1[k], h, dw[i][k]);
-                    db[i][k] += d1[k];
-                    s0 += g;
-                    s1 = fmaf(g, h, s1);
+                    dw[i][k] = fmaf(d[k], hi[k], dw[i][k]);
+                    db[i][k] += d[k];
+                    s[0] += gi[k];
+                    s[1] = fmaf(gi[k], hi[k], s[1]);
                 }
             }
-        float s[2] = {s0, s1};
         row_sum<LPR>(s, buf, phase);
         if (!live) continue;
         if constexpr (kRing) {
             __syncwarp();
             ring.next();
         }
-        // rstd (g - mean(g) - h mean(g h))
+        // rstd (g - mean(g) - xhat mean(g xhat))
         const float c0 = -s[0] * inv * r, c1 = -s[1] * inv * r;
+        T* to = dx + row * a.dx_stride + l * VEC;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (l + i * LPR < nvec) {
-                if (a.weight) load_floats<VEC>(w, share, l + i * LPR, nvec);
-                unpack<T, VEC>(rx[i], x1);
-                unpack<T, VEC>(rd[i], d1);
+            if (in(i)) {
+                float o[VEC];
+                auto &hi = h[kKeep ? i : 0], &gi = g[kKeep ? i : 0];
+                if (!kKeep) form(i, hi, gi, o);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float h = (x1[k] - m) * r, g = a.weight ? d1[k] * w[k] : d1[k];
-                    x1[k] = fmaf(g, r, fmaf(h, c1, c0));
-                }
-                *reinterpret_cast<Pack<T, VEC>*>(dx + row * a.dx_stride + (size_t)(l + i * LPR) * VEC) = repack<T, VEC>(x1);
+                for (int k = 0; k < VEC; ++k) o[k] = fmaf(gi[k], r, fmaf(hi[k], c1, c0));
+                *reinterpret_cast<Pack<T, VEC>*>(to + i * LPR * VEC) = repack<T, VEC>(o);
             }
     }
     if constexpr (kRing) ring.finish();
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd(const NormBwdArgs a) {
         if ((int)threadIdx.x / LPR != r) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (l + i * LPR < nvec) {
+            if (in(i)) {
                 if (r > 0) {
                     float u[VEC], v[VEC];
                     load_floats<VEC>(u, share, l + i * LPR, nvec);
@@ -226,13 +235,13 @@ long long shares(long long rows) { return rows < kMaxShares ? rows : kMaxShares;
 
 template <class T, int VEC>
 cudaError_t run(const NormBwdArgs& a, int* blocks, cudaStream_t st) {
-    // 16 elements a thread. 139,072 x 1024 bfloat16: 170 us; with 32 (two sums each leave registers for 8 warps an
-    // SM) 243 us, with 8 (a barrier of four warps for each row) 253 us
+    // 16 elements a thread. 139,072 x 1024 bfloat16: 137 us; with 32 (two sums each leave registers for 8 warps an
+    // SM) and with 8 (a barrier of four warps for each row) 1.4 and 1.5 times as long
     return norm_dispatch<VEC, VEC == 8 ? 2 : 4>(a.cols / VEC, [&](auto shape) {
         using S = decltype(shape);
         constexpr int kRows = kNormBlock / S::LPR;
         static std::atomic<int> cache[256] = {};
-        auto* kernel = k_norm_bwd<T, VEC, S::NV, S::LPR>;
+        auto* kernel = k_norm_bwd<T, VEC, S::NV, S::LPR, S::FULL>;
         constexpr bool kRing = norm_ring<VEC, S::NV, S::LPR>;
         auto smem_of = [&](int cols) {
             return 2 * cols * sizeof(float) + (kRing ? NormRing<2, kRing ? S::LPR : 32, norm_stages<S::NV, S::LPR>>::smem(cols, sizeof(T)) : 0);

@@ -175,3 +175,11 @@ def test_refusals():
             bad()
     with pytest.raises(_abi.GsError, match="eps"):
         api.gs_layer_norm_fwd(x, eps=-1.0)
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("rows,cols", [(1000, 8), (999, 16), (517, 32), (301, 24), (130, 48), (61, 34), (41, 70), (33, 126), (29, 250),
+                                       (23, 382), (19, 510), (17, 1022), (9, 2046), (7, 4094), (3, 6002)])
+def test_narrow_rows_and_rows_of_odd_pairs(dtype, rows, cols):
+    x = _rand((rows, cols), dtype, rows + cols, 2.0, 0.5)
+    _check(x, _rand((cols,), dtype, 1, 0.3, 1.0), _rand((cols,), dtype, 2), _rand((rows, cols), dtype, 3))
