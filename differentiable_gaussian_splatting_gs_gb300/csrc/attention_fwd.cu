@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     const bool whole = (int)blockIdx.x < t.whole;
     const int shared = (int)blockIdx.x - t.whole, split = whole ? 0 : shared % t.splits;
     const int block = whole ? (int)blockIdx.x : t.whole + shared / t.splits, tile = block % t.tiles, bh = block / t.tiles;
-    const int h = bh % a.heads, b = bh / a.heads, hk = h / (a.heads / a.kv_heads);
-    const int keys = keys_of(t, b), q0 = tile * NQ * kTileRows;
+    const int groups = a.heads / t.fold, h0 = bh % groups * t.fold, b = bh / groups, hk = h0 / (a.heads / a.kv_heads);
+    const int keys = keys_of(t, b), q0 = tile * NQ * t.fold_rows;
     // this block's key tiles
     const int all = (keys + BN - 1) / BN, per = whole ? all : (all + t.splits - 1) / t.splits;
     const int first = min(split * per, all), n = min(per, all - first);
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             if (n > 0 && elect_one()) {
                 bool ok = true;
                 int sent = 0;
-                mbar_arrive_expect_tx(&q_full, NQ * S::kQ);
-                for (int i = 0; i < NQ; ++i) load_rows<DP, PL, kTileRows>(sq + i * S::kQ, tq, q0 + i * kTileRows, b, h, a.heads, &q_full);
+                mbar_arrive_expect_tx(&q_full, NQ * S::kQ / kTileRows * t.fold * t.fold_rows);
+                for (int i = 0; i < NQ; ++i) load_rows<DP, PL, kTileRows>(sq + i * S::kQ, tq, q0 + i * t.fold_rows, b, h0, a.heads, &q_full);
                 for (int j = 0; j < n && ok; ++j) {
                     const int s = j % kSt;
                     const unsigned ph = (j / kSt + 1) & 1;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     } else {  // softmax: thread = query
         if (NQ == 2 && PL == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         if (NQ == 2 && PL == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        const int i = warp / 4, row = q0 + i * kTileRows + (threadIdx.x & 127);
+        const int i = warp / 4, r = threadIdx.x & 127, h = h0 + r / t.fold_rows, row = q0 + i * t.fold_rows + r % t.fold_rows;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ti = tm + i * S::kP + lanes,
                        to = tm + S::kO + i * DP + lanes;
         const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
@@ -412,12 +412,12 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         if (n > 0) ok = ok && warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
         tc_fence_after();
         if (S::kRegO && n > 0) add_tile();
-        const bool live = row < a.len_q && ok;
+        const bool live = row < a.len_q && h < h0 + t.fold && ok;
         const float f = sum == 0.f ? 0.f : 1.f / sum;
         const float lse = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
         const long long qrow = ((long long)b * a.heads + h) * a.len_q + row;
         if (!whole) {
-            const long long prow = ((long long)split * t.tail + block - t.whole) * (NQ * kTileRows) + row - q0;
+            const long long prow = ((long long)split * t.tail + block - t.whole) * (NQ * kTileRows) + i * kTileRows + r;
             if (live) t.part_lse[prow] = lse;
             if (n > 0) {
 #pragma unroll

@@ -99,9 +99,10 @@ __global__ void __launch_bounds__(256) k_attn_combine(const TcArgs t, int per, i
     const long long rows = (long long)t.tail * per, unit = ((long long)blockIdx.x * 256 + threadIdx.x) >> log_lanes;
     const long long row = unit / GROUPS;
     const int group = GROUPS > 1 ? (int)(unit % GROUPS) : 0, col = (threadIdx.x & ((1 << log_lanes) - 1)) * 4;
-    const int block = t.whole + (int)(row / per), bh = block / t.tiles, i = block % t.tiles * per + (int)(row % per);
-    const int b = bh / a.heads, h = bh % a.heads;
-    const bool in = row < rows && i < a.len_q && col < a.d;
+    const int block = t.whole + (int)(row / per), x = (int)(row % per), r = x % kTileRows, groups = a.heads / t.fold;
+    const int b = block / t.tiles / groups, h0 = block / t.tiles % groups * t.fold, h = h0 + r / t.fold_rows;
+    const int i = (block % t.tiles * (per / kTileRows) + x / kTileRows) * t.fold_rows + r % t.fold_rows;
+    const bool in = row < rows && i < a.len_q && h < h0 + t.fold && col < a.d;
     float o[4] = {}, total = 0.f, top = -INFINITY;
     for (int s0 = group; s0 < t.splits && in; s0 += GROUPS * kAhead) {
         float l[kAhead], m = top;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(256) k_attn_combine(const TcArgs t, int per, i
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (col + k < a.d) dst[col + k] = from_float<T>(total == 0.f ? 0.f : o[k] / total);
-    if (col == 0) a.lse[(long long)bh * a.len_q + i] = total == 0.f ? -INFINITY : top + logf(total);
+    if (col == 0) a.lse[((long long)b * a.heads + h) * a.len_q + i] = total == 0.f ? -INFINITY : top + logf(total);
 }
 
 cudaError_t launch_attn_index(const AttnArgs& a, int* count, int* index, cudaStream_t st) {

@@ -40,6 +40,7 @@ struct TcArgs {
     float* part_lse;
     int tiles, splits;
     int whole, tail;   // forward: the first `whole` blocks of (head, tile) walk all keys, `tail` more share their walk
+    int fold, fold_rows;  // forward: a tile's 128 rows are `fold` heads that share a key head, of fold_rows queries each
 };
 
 __device__ __forceinline__ int keys_of(const TcArgs& t, int b) { return t.count ? t.count[b] : key_count(t.a, b); }
@@ -66,7 +67,7 @@ struct PackJob {
 };
 cudaError_t launch_attn_pack(const AttnArgs& a, const PackJob* jobs, int n, const int* count, const int* index, int planes, int dp,
                              cudaStream_t st);
-// out and lse of t.tail blocks of `rows` queries from the splits' shares [t.splits][t.tail][rows][dp].
+// out and lse of t.tail blocks of `rows` rows (tiles of 128, or one row) from the splits' shares [t.splits][t.tail][rows][dp].
 cudaError_t launch_attn_combine(const TcArgs& t, int rows, int dp, cudaStream_t st);
 // One query, no shared heads; part, part_lse: the splits' shares, or NULL.
 cudaError_t launch_attn_decode(const AttnArgs& a, int splits, int dp, float* part, float* part_lse, cudaStream_t st);

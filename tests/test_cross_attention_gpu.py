@@ -314,3 +314,15 @@ def test_waits_that_give_up_are_reported_and_leave_the_context_usable(dtype, d):
     assert all(torch.equal(x, y) for x, y in zip(again, want))
     assert all(torch.equal(x, y) for x, y in zip(api.gs_cross_attention_bwd(dout, q, k, v, *again), grads))
     assert api.gs_device_error() == _abi.GS_OK
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("b,lq,lk,h,hk,d,masked", [
+    (1, 1, 3000, 8, 2, 64, False), (2, 1, 1500, 12, 4, 128, True), (1, 7, 900, 10, 2, 64, False), (1, 33, 700, 16, 1, 40, True),
+    (2, 5, 600, 32, 2, 128, False), (1, 26, 400, 5, 1, 64, False), (1, 1, 500, 136, 1, 64, False), (1, 2, 640, 100, 1, 64, True),
+    (1, 90, 300, 6, 2, 128, False), (3, 1, 9000, 4, 1, 80, True)])
+def test_shared_heads_of_few_queries(dtype, b, lq, lk, h, hk, d, masked):
+    q, k, v = _qkv(b, lq, lk, h, hk, d, dtype, lq)
+    q = torch.randn(b, h, lq, d, device=DEV, generator=torch.Generator(device="cuda").manual_seed(lk)).to(dtype).transpose(1, 2)
+    k_len = torch.tensor([lk, 0, lk // 2][:b], dtype=torch.int32, device=DEV) if masked else None
+    _check(q, k, v, k_len=k_len, seed=lk)
