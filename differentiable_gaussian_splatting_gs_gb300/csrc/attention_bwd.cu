@@ -383,38 +383,45 @@ __global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long 
     pdl_entry();
     constexpr int V = 16 / (int)sizeof(T);
     const bool keys = blockIdx.y;
-    const long long pad = keys ? rows_k : qpad, at = ((long long)blockIdx.x * 256 + threadIdx.x) / 8, bh = at / pad, i = at % pad;
-    const int heads = keys ? a.kv_heads : a.heads, b = (int)(bh / heads), h = (int)(bh % heads), lane = threadIdx.x & 7;
-    if (b >= a.batch) return;  // the whole block: its rows are of one head (pad is a multiple of 32)
+    const unsigned blocks = (unsigned)((keys ? rows_k : qpad) / 32);  // of a head: a block's 32 rows are of one head
+    const int bh = (int)(blockIdx.x / blocks), i = (int)(blockIdx.x % blocks) * 32 + threadIdx.x / 8, lane = threadIdx.x & 7;
+    const int heads = keys ? a.kv_heads : a.heads, b = bh / heads, h = bh % heads;
+    const long long at = (long long)bh * qpad + i;
+    if (b >= a.batch) return;  // the whole block
     __shared__ unsigned most;
     if (norms && threadIdx.x == 0) most = 0u;
-    const bool in = i < (keys ? a.len_k : a.len_q), valid = in && (!keys || key_valid(a, b, (int)i, key_count(a, b)));
+    const bool in = i < (keys ? a.len_k : a.len_q), valid = in && (!keys || key_valid(a, b, i, key_count(a, b)));
+    const float l = !keys && in ? a.lse[(long long)bh * a.len_q + i] : -INFINITY;
     float s = 0.f, n2 = 0.f;  // of out and dout; of dout or v with itself
     if (valid && (!keys || norms)) {
         const AttnTensor& t = keys ? a.v : a.dout;
-        const T* d = head_base<T>(t, b, h) + i * t.len_stride;
-        const T* o = keys ? d : head_base<T>(a.out, b, h) + i * a.out.len_stride;
+        const T* d = head_base<T>(t, b, h) + (long long)i * t.len_stride;
+        const T* o = keys ? d : head_base<T>(a.out, b, h) + (long long)i * a.out.len_stride;
         const bool vec = a.d % V == 0 && (reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(d)) % 16 == 0;
-        for (int c = lane * V; c < a.d; c += 8 * V) {
-            Pack<T, V> x, y;
-            if (vec) {
-                x = *reinterpret_cast<const Pack<T, V>*>(o + c), y = *reinterpret_cast<const Pack<T, V>*>(d + c);
+        constexpr int kTurns = (sizeof(T) == 2 ? 128 : 64) / (8 * V);  // heads of up to 128, float32 of up to 64
+        Pack<T, V> x[kTurns], y[kTurns];
+        const T zero = from_float<T>(0.f);
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int c = (u * 8 + lane) * V;
+            if (vec && c < a.d) {
+                x[u] = *reinterpret_cast<const Pack<T, V>*>(o + c), y[u] = *reinterpret_cast<const Pack<T, V>*>(d + c);
             } else {  // the same elements per lane, so that a layout changes no sum
-                const T zero = from_float<T>(0.f);
 #pragma unroll
-                for (int k = 0; k < V; ++k) x.v[k] = c + k < a.d ? o[c + k] : zero, y.v[k] = c + k < a.d ? d[c + k] : zero;
-            }
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                s = fmaf(to_float(x.v[k]), to_float(y.v[k]), s);
-                if (norms) n2 = fmaf(to_float(y.v[k]), to_float(y.v[k]), n2);
+                for (int k = 0; k < V; ++k) x[u].v[k] = c + k < a.d ? o[c + k] : zero, y[u].v[k] = c + k < a.d ? d[c + k] : zero;
             }
         }
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                s = fmaf(to_float(x[u].v[k]), to_float(y[u].v[k]), s);
+                if (norms) n2 = fmaf(to_float(y[u].v[k]), to_float(y[u].v[k]), n2);
+            }
     }
 #pragma unroll
     for (int k = 4; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
     if (!keys && lane == 0) {
-        const float l = in ? a.lse[bh * a.len_q + i] : -INFINITY;
         nlse[at] = l == -INFINITY ? -INFINITY : (float)boost - l * 1.4426950408889634f;
         ndelta[at] = -s;
     }
@@ -430,7 +437,11 @@ __global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a, long long 
         __syncthreads();
         if ((threadIdx.x & 31) == 0) atomicMax(&most, w);
         __syncthreads();
-        if (threadIdx.x == 0) atomicMax(norms + (b * a.kv_heads + (keys ? h : h / (a.heads / a.kv_heads))) * 2 + keys, most);
+        if (threadIdx.x == 0) {
+            // (thousands of blocks' atomics on a few words follow one another: only those that raise the maximum)
+            unsigned* to = norms + (b * a.kv_heads + (keys ? h : h / (a.heads / a.kv_heads))) * 2 + keys;
+            if (most > *static_cast<volatile unsigned*>(to)) atomicMax(to, most);
+        }
     }
 }
 

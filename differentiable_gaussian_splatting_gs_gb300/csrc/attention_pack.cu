@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(256) k_attn_combine(const TcArgs t, int per, i
     constexpr int kAhead = 8;
     __shared__ float meet[GROUPS > 1 ? 6 : 1][256];
     const AttnArgs& a = t.a;
-    const long long rows = (long long)t.tail * per, unit = ((long long)blockIdx.x * 256 + threadIdx.x) >> log_lanes;
-    const long long row = unit / GROUPS;
-    const int group = GROUPS > 1 ? (int)(unit % GROUPS) : 0, col = (threadIdx.x & ((1 << log_lanes) - 1)) * 4;
+    const long long rows = (long long)t.tail * per;
+    const unsigned unit = blockIdx.x * (256u >> log_lanes) + (threadIdx.x >> log_lanes), row = unit / GROUPS;
+    const int group = unit % GROUPS, col = (threadIdx.x & ((1 << log_lanes) - 1)) * 4;
     const int block = t.whole + (int)(row / per), x = (int)(row % per), r = x % kTileRows, groups = a.heads / t.fold;
     const int b = block / t.tiles / groups, h0 = block / t.tiles % groups * t.fold, h = h0 + r / t.fold_rows;
     const int i = (block % t.tiles * (per / kTileRows) + x / kTileRows) * t.fold_rows + r % t.fold_rows;
