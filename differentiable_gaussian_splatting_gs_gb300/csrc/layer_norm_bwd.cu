@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_bwd_long(const NormBwdArgs 
     }
 }
 
-// ... and dw, db of such rows: a thread per column over the block's share of the rows.
+// ... and, before it, dw and db of such rows: a thread per column over the block's share of the rows.
 template <class T>
 __global__ void __launch_bounds__(kNormBlock) k_norm_bwd_long_cols(const NormBwdArgs a) {
     pdl_entry();
@@ -265,14 +265,16 @@ template <class T>
 cudaError_t run_typed(const NormBwdArgs& a, int* blocks, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
     if (a.cols > kNormMaxCols) {
+        if (a.part) {  // first: dx may overwrite dy or x
+            *blocks = (int)(shares(a.rows) < 64 ? shares(a.rows) : 64);
+            count_launches(1);
+            const cudaError_t e = launch_pdl(k_norm_bwd_long_cols<T>, dim3((a.cols + kNormBlock - 1) / kNormBlock, *blocks), dim3(kNormBlock), 0, st, a);
+            if (e) return e;
+        }
         static std::atomic<int> cache[256] = {};
         const int most = resident_blocks(k_norm_bwd_long<T>, kNormBlock, 0, cache);
         count_launches(1);
-        cudaError_t e = launch_pdl(k_norm_bwd_long<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
-        if (e || !a.part) return e;
-        *blocks = (int)(shares(a.rows) < 64 ? shares(a.rows) : 64);
-        count_launches(1);
-        return launch_pdl(k_norm_bwd_long_cols<T>, dim3((a.cols + kNormBlock - 1) / kNormBlock, *blocks), dim3(kNormBlock), 0, st, a);
+        return launch_pdl(k_norm_bwd_long<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
     }
     const bool vec = a.cols % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && a.dx_stride % V == 0 &&
                      (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.dy) |

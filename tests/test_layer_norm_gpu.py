@@ -183,3 +183,20 @@ def test_refusals():
 def test_narrow_rows_and_rows_of_odd_pairs(dtype, rows, cols):
     x = _rand((rows, cols), dtype, rows + cols, 2.0, 0.5)
     _check(x, _rand((cols,), dtype, 1, 0.3, 1.0), _rand((cols,), dtype, 2), _rand((rows, cols), dtype, 3))
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("rows,cols", [(300, 64), (2000, 256), (900, 333), (400, 1024), (70, 4096), (40, 8193), (200, 9000)])
+def test_gradient_written_over_an_input(dtype, rows, cols):
+    x, dy = _rand((rows, cols), dtype, 1), _rand((rows, cols), dtype, 2)
+    w = _rand((cols,), dtype, 3, 0.3, 1.0)
+    _, mean, rstd = api.gs_layer_norm_fwd(x, w, None)
+    want = api.gs_layer_norm_bwd(dy, x, mean, rstd, w)
+    for over in (0, 1):
+        a, b = x.clone(), dy.clone()
+        got = api.gs_layer_norm_bwd(b, a, mean, rstd, w, out=((a, b)[over], torch.empty_like(w), torch.empty_like(w)))
+        for g, t in zip(got, want):
+            assert torch.equal(g, t)
+    y = x.clone()
+    api.gs_layer_norm_fwd(y, w, w, out=(y, torch.empty_like(mean), torch.empty_like(rstd)))
+    assert torch.equal(y, api.gs_layer_norm_fwd(x, w, w)[0])
