@@ -1,6 +1,7 @@
 // Cross attention, forward, on the tensor cores.
 //
-// A block takes NQ tiles of 128 queries of one head and walks the keys in tiles of BN. One warp copies K and
+// A block takes NQ tiles of 128 queries of one head (or of the heads that share a key head, where queries are few) and
+// walks the keys, or its share of them, in tiles of BN. One warp copies K and
 // V tiles ahead, a thread issues the products S = Q K^T and O += P V, and a warpgroup per query tile turns S
 // into P: thread = query, so the row's maximum and sum need no exchange. S, P and O stay in tensor memory; P
 // takes half the columns of its S. With two query tiles the products of one run beside the softmax of the
