@@ -9,9 +9,9 @@ namespace gs {
 
 namespace {
 
-// Head dimensions above it go to the float32 kernels, as does the backward of float32 heads above 64: three planes of
-// its rows and of two walked tiles do not fit shared memory.
-constexpr int kMaxTcDim = 128;
+// The largest head dimension on the tensor cores; the float32 kernels take the others. Three planes of wider float32 rows and of
+// two tiles do not fit shared memory, nor do the backward's two accumulators of 256 columns with a walked tile the tensor memory.
+int max_tc_dim(int dtype, bool backward) { return dtype == GS_DTYPE_F32 ? (backward ? 64 : 128) : backward ? 128 : 256; }
 
 // What a call packs, how it splits its walks, and where the pieces lie in the workspace (byte offsets).
 struct Plan {
@@ -43,7 +43,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
         return here;
     };
     const size_t bq = (size_t)a.batch * a.heads * a.len_q, bk = (size_t)a.batch * a.kv_heads;
-    p.tc = a.d <= kMaxTcDim && a.len_k > 0 && a.len_q > 0 && !(backward && a.dtype == GS_DTYPE_F32 && a.d > 64);
+    p.tc = a.d <= max_tc_dim(a.dtype, backward) && a.len_k > 0 && a.len_q > 0;
     if (!backward && a.len_q == 1 && a.len_k > 0 && a.heads == a.kv_heads) {
         // two blocks an SM, with at least 64 keys each
         p.tc = false;
@@ -62,7 +62,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
     if (p.tc) {
         const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
         p.planes = wide ? 3 : 1;
-        p.dp = a.d <= 64 ? 64 : 128;
+        p.dp = a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256;
         p.rows_k = ((long long)a.len_k + kTileRows - 1) / kTileRows * kTileRows;
         p.pack_q = wide || !tensors || !copyable(a.q, a, a.len_q);
         p.pack_do = backward && (wide || !tensors || !copyable(a.dout, a, a.len_q));
@@ -82,7 +82,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             const int group = a.heads / a.kv_heads;
             for (int way = 0; way < 4; ++way) {
                 const int nq = way % 2 ? 1 : 2, fold = way / 2 ? group : 1, fold_rows = kTileRows / fold;
-                if ((nq == 2 && wide && p.dp == 128) || (way / 2 && group == 1) || fold > kTileRows) continue;
+                if ((nq == 2 && (wide ? p.dp == 128 : p.dp == 256)) || (way / 2 && group == 1) || fold > kTileRows) continue;
                 const long long tiles = over(a.len_q, fold_rows * nq), blocks = tiles * (a.heads / fold) * a.batch, tail = blocks % sms;
                 for (int rounds = 0; rounds <= (tail > 0 ? 4 : 0); ++rounds) {  // that the shares take; 0: no split
                     long long s = rounds == 0 ? 1 : std::min((long long)sms * rounds / tail, walk / 2);
@@ -219,7 +219,7 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
     e = lay_out(p, a, ws, count, index, st);
     if (e) return e;
     TcArgs t{a, count, nullptr, nullptr, p.tiles, p.splits, (int)p.whole, p.tail, p.fold, p.fold_rows};
-    const int bn = p.planes == 3 && p.dp == 128 ? 64 : 128;
+    const int bn = (p.planes == 3 && p.dp == 128) || p.dp == 256 ? 64 : 128;
     TcTensor q, k, v;
     if ((e = operand(q, p, a, a.q, a.heads, a.len_q, p.pack_q, ws + p.q, a.len_q, p.fold_rows, p.fold)) ||
         (e = operand(k, p, a, a.k, a.kv_heads, a.len_k, p.pack_kv, ws + p.k, p.rows_k, bn)) ||

@@ -496,6 +496,7 @@ cudaError_t launch_attn_fwd_tc(const TcArgs& t, const TcTensor& q, const TcTenso
         return nq == 1 ? run<__nv_bfloat16, 64, 3, 1, 128>(t, q, k, v, st) : run<__nv_bfloat16, 64, 3, 2, 128>(t, q, k, v, st);
     }
     const bool half = t.a.dtype == GS_DTYPE_F16;
+    if (dp == 256) return half ? run<__half, 256, 1, 1, 64>(t, q, k, v, st) : run<__nv_bfloat16, 256, 1, 1, 64>(t, q, k, v, st);
     if (dp == 128) {
         if (nq == 1) return half ? run<__half, 128, 1, 1, 128>(t, q, k, v, st) : run<__nv_bfloat16, 128, 1, 1, 128>(t, q, k, v, st);
         return half ? run<__half, 128, 1, 2, 128>(t, q, k, v, st) : run<__nv_bfloat16, 128, 1, 2, 128>(t, q, k, v, st);

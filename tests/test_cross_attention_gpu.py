@@ -326,3 +326,13 @@ def test_shared_heads_of_few_queries(dtype, b, lq, lk, h, hk, d, masked):
     q = torch.randn(b, h, lq, d, device=DEV, generator=torch.Generator(device="cuda").manual_seed(lk)).to(dtype).transpose(1, 2)
     k_len = torch.tensor([lk, 0, lk // 2][:b], dtype=torch.int32, device=DEV) if masked else None
     _check(q, k, v, k_len=k_len, seed=lk)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("b,lq,lk,h,hk,d,masked", [
+    (1, 300, 700, 2, 2, 256, False), (2, 129, 1000, 4, 2, 192, True), (1, 1, 3000, 8, 2, 256, False), (1, 3, 900, 3, 3, 160, True),
+    (1, 2000, 130, 1, 1, 144, False), (1, 260, 64, 2, 1, 250, False)])
+def test_wide_heads(dtype, b, lq, lk, h, hk, d, masked):
+    q, k, v = _qkv(b, lq, lk, h, hk, d, dtype, lq)
+    k_len = torch.tensor([lk - 70, 0][:b], dtype=torch.int32, device=DEV) if masked else None
+    _check(q, k, v, k_len=k_len, seed=lk, backward=False)
