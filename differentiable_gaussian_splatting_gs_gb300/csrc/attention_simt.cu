@@ -1,11 +1,14 @@
-// Cross attention on the float32 pipes, for what the tensor-core kernels do not take: head dimensions
-// above 128, and the backward of float32 heads above 64. Every stride, mask and length; products and sums in float32.
+// Cross attention on the float32 pipes, for what the tensor-core kernels do not take: float32 heads above 128 (backward:
+// above 64), the backward of 16-bit heads above 128, and calls without a key. Every stride, mask and length; products and
+// sums in float32.
 //
 // Forward: a block of 256 threads per 64 queries of a head. It walks the keys in tiles of 64 with the
 // running maximum and sum of the softmax, so scores stay on chip. Backward: one kernel per 64 (heads above 128: 32) keys
 // (dk, dv; walks the queries of all heads that share the key head) and one per as many queries (dq; walks
 // the keys). Each output is summed by one block in a fixed order: no atomics, the same bits every time,
-// at the price of forming S and dP twice.
+// at the price of forming S and dP twice. Bound by the reads of shared memory (69% of their rate) beside the multiply-adds
+// (54%), with eight warps an SM: 2 x 8 heads of 128, 2000 x 2500 float32, backward 4.7 ms (5.7 with single multiply-adds and
+// tiles staged an element at a time).
 #include "attention.cuh"
 
 namespace gs {
@@ -23,6 +26,32 @@ constexpr int kThreads = 256;
 template <class T, int DP, int ROWS, bool KEYS>
 __device__ __forceinline__ void stage(float* dst, const AttnTensor& t, const AttnArgs& a, int b, int h, int first, int len) {
     const T* src = head_base<T>(t, b, h);
+    constexpr int V = 16 / (int)sizeof(T), kVectors = ROWS * DP / V / kThreads;
+    if (kVectors > 0 && a.d % V == 0 && t.len_stride % V == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+        constexpr int kTurn = kVectors > 8 ? 8 : kVectors > 0 ? kVectors : 1;  // loads under way together
+        static_assert(kVectors % kTurn == 0);
+#pragma unroll 1
+        for (int v0 = 0; v0 < kVectors; v0 += kTurn) {
+            Pack<T, V> w[kTurn];
+#pragma unroll
+            for (int u = 0; u < kTurn; ++u) {
+                const int e = (threadIdx.x + (v0 + u) * kThreads) * V, c = e % DP, row = first + e / DP;
+                const bool in = c < a.d && (KEYS ? key_valid(a, b, row, len) : row < len);
+#pragma unroll
+                for (int k = 0; k < V; ++k) w[u].v[k] = from_float<T>(0.f);
+                if (in) w[u] = *reinterpret_cast<const Pack<T, V>*>(src + row * t.len_stride + c);
+            }
+#pragma unroll
+            for (int u = 0; u < kTurn; ++u) {
+                const int e = (threadIdx.x + (v0 + u) * kThreads) * V;
+#pragma unroll
+                for (int k = 0; k < V; k += 4)
+                    *reinterpret_cast<float4*>(dst + e / DP * (DP + 4) + e % DP + k) =
+                        make_float4(to_float(w[u].v[k]), to_float(w[u].v[k + 1]), to_float(w[u].v[k + 2]), to_float(w[u].v[k + 3]));
+            }
+        }
+        return;
+    }
     constexpr int kBatch = 16;  // loads under way together
     static_assert(ROWS * DP % (kBatch * kThreads) == 0);
 #pragma unroll 1
@@ -43,59 +72,95 @@ __device__ __forceinline__ void stage(float* dst, const AttnTensor& t, const Att
     }
 }
 
-// acc[i][j] = row (ty * R + i) of x . row (tx + 16 j) of y
+// acc[i][j] = row (ty * R + i) of x . row (tx + 16 j) of y; multiply-adds in pairs, of even and of odd elements.
 template <int DP, int R, int C>
 __device__ __forceinline__ void dots(const float* x, const float* y, int ty, int tx, float (&acc)[R][C]) {
+    f32x2 sum[R][C];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < C; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < C; ++j) sum[i][j] = f2_pack(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < DP; d += 4) {
-        float4 u[R], v[C];
+        ulonglong2 u[R], v[C];
 #pragma unroll
-        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4*>(x + (ty * R + i) * (DP + 4) + d);
+        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const ulonglong2*>(x + (ty * R + i) * (DP + 4) + d);
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * (DP + 4) + d);
+        for (int j = 0; j < C; ++j) v[j] = *reinterpret_cast<const ulonglong2*>(y + (tx + 16 * j) * (DP + 4) + d);
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                acc[i][j] = fmaf(u[i].x, v[j].x, fmaf(u[i].y, v[j].y, fmaf(u[i].z, v[j].z, fmaf(u[i].w, v[j].w, acc[i][j]))));
+            for (int j = 0; j < C; ++j) sum[i][j] = f2_fma(u[i].x, v[j].x, f2_fma(u[i].y, v[j].y, sum[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const float2 t = f2_unpack(sum[i][j]);
+            acc[i][j] = t.x + t.y;
+        }
 }
 
-// acc[i][m] += sum over n of p[ty * R + i][n] y[n][tx + 16 m] (p: row stride N + 4; y: DP + 4)
-template <int DP, int N, int R>
-__device__ __forceinline__ void accumulate(const float* p, const float* y, int ty, int tx, float (&acc)[R][DP / 16]) {
+// A tile of probabilities or of dS: rows of N elements, each TWICE (a pair for f2_fma) where shared memory has the room.
+template <int N, bool TWICE>
+constexpr int kTileRow = (N + 4) * (TWICE ? 2 : 1);
+template <int N, bool TWICE>
+__device__ __forceinline__ void put(float* p, int row, int n, float v) {
+    if (TWICE) *reinterpret_cast<float2*>(p + row * kTileRow<N, TWICE> + 2 * n) = make_float2(v, v);
+    else p[row * kTileRow<N, TWICE> + n] = v;
+}
+
+// acc[i][m] += sum over n of p[ty * R + i][n] times elements 2 (tx + 16 m) and the next of y's row n (y: row stride DP + 4)
+template <int DP, int N, bool TWICE, int R>
+__device__ __forceinline__ void accumulate(const float* p, const float* y, int ty, int tx, f32x2 (&acc)[R][DP / 32]) {
 #pragma unroll 1
     for (int n0 = 0; n0 < N; n0 += 4) {
-        float4 u[R];
+        f32x2 u[R][4];
 #pragma unroll
-        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4*>(p + (ty * R + i) * (N + 4) + n0);
+        for (int i = 0; i < R; ++i) {
+            const float* from = p + (ty * R + i) * kTileRow<N, TWICE> + n0 * (TWICE ? 2 : 1);
+            if (TWICE) {
+                const ulonglong2 w0 = *reinterpret_cast<const ulonglong2*>(from), w1 = *reinterpret_cast<const ulonglong2*>(from + 4);
+                u[i][0] = w0.x, u[i][1] = w0.y, u[i][2] = w1.x, u[i][3] = w1.y;
+            } else {
+                const float4 w = *reinterpret_cast<const float4*>(from);
+                u[i][0] = f2_pack(w.x, w.x), u[i][1] = f2_pack(w.y, w.y), u[i][2] = f2_pack(w.z, w.z), u[i][3] = f2_pack(w.w, w.w);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int m = 0; m < DP / 16; ++m) {
-                const float v = y[(n0 + k) * (DP + 4) + tx + 16 * m];
+            for (int m = 0; m < DP / 32; ++m) {
+                const f32x2 v = *reinterpret_cast<const f32x2*>(y + (n0 + k) * (DP + 4) + 2 * (tx + 16 * m));
 #pragma unroll
-                for (int i = 0; i < R; ++i)
-                    acc[i][m] = fmaf(k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w, v, acc[i][m]);
+                for (int i = 0; i < R; ++i) acc[i][m] = f2_fma(u[i][k], v, acc[i][m]);
             }
     }
 }
 
+template <int DP, int R>
+__device__ __forceinline__ void clear(f32x2 (&acc)[R][DP / 32]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int m = 0; m < DP / 32; ++m) acc[i][m] = f2_pack(0.f, 0.f);
+}
+
 template <class T, int DP, int R>
 __device__ __forceinline__ void store_rows(const AttnTensor& t, int d, int b, int h, int first, int len, int ty, int tx,
-                                           const float (&acc)[R][DP / 16], const float (&f)[R]) {
+                                           const f32x2 (&acc)[R][DP / 32], const float (&f)[R]) {
     T* dst = static_cast<T*>(t.data) + b * t.batch_stride + h * t.head_stride;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int row = first + ty * R + i;
         if (row >= len) continue;
 #pragma unroll
-        for (int m = 0; m < DP / 16; ++m)
-            if (tx + 16 * m < d) dst[row * t.len_stride + tx + 16 * m] = from_float<T>(acc[i][m] * f[i]);
+        for (int m = 0; m < DP / 32; ++m) {
+            const float2 v = f2_unpack(acc[i][m]);
+            const int c = 2 * (tx + 16 * m);
+            if (c < d) dst[row * t.len_stride + c] = from_float<T>(v.x * f[i]);
+            if (c + 1 < d) dst[row * t.len_stride + c + 1] = from_float<T>(v.y * f[i]);
+        }
     }
 }
 
@@ -113,12 +178,15 @@ template <class T, int DP>
 __global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, int tiles) {
     pdl_entry();
     extern __shared__ float sm[];
+    constexpr bool kTwice = DP <= 128;
     float *sq = sm, *sk = sq + kFM * (DP + 4), *sv = sk + kFN * (DP + 4), *sp = sv + kFN * (DP + 4);
     const Where w = where(tiles, a.heads);
     const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int len = key_count(a, w.b);
     stage<T, DP, kFM, false>(sq, a.q, a, w.b, w.h, w.tile * kFM, a.len_q);
-    float o[4][DP / 16] = {}, top[4], sum[4];
+    f32x2 o[4][DP / 32];
+    float top[4], sum[4];
+    clear<DP>(o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) top[i] = -INFINITY, sum[i] = 0.f;
     for (int n0 = 0; n0 < len; n0 += kFN) {
@@ -148,17 +216,17 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, in
             for (int j = 0; j < 4; ++j) {
                 const float p = expf(s[i][j] - base);
                 t += p;
-                sp[(ty * 4 + i) * (kFN + 4) + tx + 16 * j] = p;
+                put<kFN, kTwice>(sp, ty * 4 + i, tx + 16 * j, p);
             }
 #pragma unroll
             for (int k = 8; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
             sum[i] = sum[i] * keep + t;
             top[i] = m;
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) o[i][c] *= keep;
+            for (int c = 0; c < DP / 32; ++c) o[i][c] = f2_mul(o[i][c], f2_pack(keep, keep));
         }
         __syncwarp();  // a row's probabilities are written and read by the same half warp
-        accumulate<DP, kFN>(sp, sv, ty, tx, o);
+        accumulate<DP, kFN, kTwice>(sp, sv, ty, tx, o);
     }
     float f[4];
 #pragma unroll
@@ -187,8 +255,8 @@ __device__ __forceinline__ void tile_gradient(const AttnArgs& a, const float* sq
             const int r = ty * R + i, c = tx + 16 * j, qi = q0 + (T_ ? c : r), n = n0 + (T_ ? r : c);
             const bool in = qi < a.len_q && key_valid(a, b, n, len);
             const float p = in ? expf(s[i][j] * a.scale - lse[qi]) : 0.f;
-            if (T_) sp[r * (M + 4) + c] = p;
-            sds[r * (M + 4) + c] = in ? p * (dp[i][j] - delta[qi]) * a.scale : 0.f;
+            if (T_) put<M, true>(sp, r, c, p);
+            put<M, true>(sds, r, c, in ? p * (dp[i][j] - delta[qi]) * a.scale : 0.f);
         }
 }
 
@@ -197,11 +265,13 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, in
     pdl_entry();
     extern __shared__ float sm[];
     constexpr int M = kSide<DP>, R = M / 16, kRow = M * (DP + 4);
-    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + M * (M + 4);
+    float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + M * kTileRow<M, true>;
     const Where w = where(tiles, a.kv_heads);
     const int share = a.heads / a.kv_heads, ty = threadIdx.x / 16, tx = threadIdx.x % 16, n0 = w.tile * M;
     const int len = key_count(a, w.b);
-    float dk[R][DP / 16] = {}, dv[R][DP / 16] = {};
+    f32x2 dk[R][DP / 32], dv[R][DP / 32];
+    clear<DP>(dk);
+    clear<DP>(dv);
     if (n0 < len) {
         stage<T, DP, M, true>(sk, a.k, a, w.b, w.h, n0, len);
         stage<T, DP, M, true>(sv, a.v, a, w.b, w.h, n0, len);
@@ -214,8 +284,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, in
                 __syncthreads();
                 tile_gradient<DP, true>(a, sq, sdo, sk, sv, sp, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
                 __syncwarp();
-                accumulate<DP, M>(sp, sdo, ty, tx, dv);
-                accumulate<DP, M>(sds, sq, ty, tx, dk);
+                accumulate<DP, M, true>(sp, sdo, ty, tx, dv);
+                accumulate<DP, M, true>(sds, sq, ty, tx, dk);
             }
         }
     }
@@ -238,7 +308,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int
     const long long row = ((long long)w.b * a.heads + w.h) * a.len_q;
     stage<T, DP, M, false>(sq, a.q, a, w.b, w.h, q0, a.len_q);
     stage<T, DP, M, false>(sdo, a.dout, a, w.b, w.h, q0, a.len_q);
-    float dq[R][DP / 16] = {};
+    f32x2 dq[R][DP / 32];
+    clear<DP>(dq);
     for (int n0 = 0; n0 < len; n0 += M) {
         __syncthreads();
         stage<T, DP, M, true>(sk, a.k, a, w.b, hk, n0, len);
@@ -246,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int
         __syncthreads();
         tile_gradient<DP, false>(a, sq, sdo, sk, sv, nullptr, sds, a.lse + row, a.delta + row, w.b, q0, n0, len, ty, tx);
         __syncwarp();
-        accumulate<DP, M>(sds, sk, ty, tx, dq);
+        accumulate<DP, M, true>(sds, sk, ty, tx, dq);
     }
     float one[R];
 #pragma unroll
@@ -289,14 +360,14 @@ cudaError_t launch_tiles(K kernel, const AttnArgs& a, int rows, int tile, int he
 
 template <class T, int DP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
-    const size_t smem = sizeof(float) * ((kFM + 2 * kFN) * (DP + 4) + kFM * (kFN + 4));
+    const size_t smem = sizeof(float) * ((kFM + 2 * kFN) * (DP + 4) + kFM * kTileRow<kFN, DP <= 128>);
     return launch_tiles(k_attn_fwd_simt<T, DP>, a, a.len_q, kFM, a.heads, smem, st);
 }
 
 template <class T, int DP>
 cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     constexpr int M = kSide<DP>;
-    const size_t smem = sizeof(float) * (4 * M * (DP + 4) + 2 * M * (M + 4));
+    const size_t smem = sizeof(float) * (4 * M * (DP + 4) + 2 * M * kTileRow<M, true>);
     cudaError_t e = launch_tiles(k_attn_dq_simt<T, DP>, a, a.len_q, M, a.heads, smem, st);
     return e ? e : launch_tiles(k_attn_dkv_simt<T, DP>, a, a.len_k, M, a.kv_heads, smem, st);
 }
