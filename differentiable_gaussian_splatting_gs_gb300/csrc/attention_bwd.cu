@@ -23,6 +23,8 @@
 // A product of 64 columns with both operands in shared memory takes 49 cycles, with A in tensor memory 33 (the
 // products' reads of shared memory bound it). Where columns are left (queries, heads of up to 64) Q and dout are moved there
 // first.
+//
+// Small calls (FINE) keep what the rounding of P and dS to 16 bits left beside them and multiply it too.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -37,6 +39,17 @@ __device__ __forceinline__ int ds_exponent(const unsigned* norms) {
     int e;
     frexpf(bound, &e);  // bound < 2^e
     return min(max(15 - e, -24), 24);
+}
+
+// Column of P or dS of 16 walked rows from 16 x on; what their rounding left of them (FINE) lies 16 columns behind.
+__device__ __forceinline__ constexpr int part_column(int x) { return x / 2 * 32 + x % 2 * 8; }
+
+// Two floats less their rounded values, rounded.
+template <class T>
+__device__ __forceinline__ uint32_t rest2(uint32_t rounded, float x, float y) {
+    Pack<T, 2> r;
+    memcpy(&r, &rounded, 4);
+    return pack2<T>(x - to_float(r.v[0]), y - to_float(r.v[1]));
 }
 
 template <int DP, bool KEYS>
@@ -60,7 +73,7 @@ struct BwdShape {
 };
 
 // One block in its role; at: its number among the role's blocks. ta1, ta2: A1 and A2; tb1, tb2: B1 and B2.
-template <class T, int DP, bool KEYS>
+template <class T, int DP, bool KEYS, bool FINE>
 __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTensor& ta1, const TcTensor& ta2, const TcTensor& tb1,
                                           const TcTensor& tb2) {
     using S = BwdShape<DP, KEYS>;
@@ -172,10 +185,17 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
                 const uint32_t acc = tm + S::kAcc, tile = sb + j % kSt * S::kStage, buffer = tm + j % kNB * 128;
                 const uint32_t y1 = tile_desc(tile, kBN * 128), y2 = tile_desc(tile + S::kB, kBN * 128);
 #pragma unroll
-                for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + x * 8, y1 + x * 128, g_desc, j > 0 || x > 0);
+                for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + part_column(x), y1 + x * 128, g_desc, j > 0 || x > 0);
                 if (KEYS)
 #pragma unroll
-                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + x * 8, y2 + x * 128, g_desc, j > 0 || x > 0);
+                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + part_column(x), y2 + x * 128, g_desc, j > 0 || x > 0);
+                if (FINE) {
+#pragma unroll
+                    for (int x = 0; x < kBN / 16; ++x) mma_ts(acc, buffer + 64 + 16 + part_column(x), y1 + x * 128, g_desc, true);
+                    if (KEYS)
+#pragma unroll
+                        for (int x = 0; x < kBN / 16; ++x) mma_ts(acc + DP, buffer + 16 + part_column(x), y2 + x * 128, g_desc, true);
+                }
                 if (!S::kOneIssuer) mma_commit(&b_free[j % kNB]);
                 mma_commit(&empty[j % kSt]);
             };
@@ -255,7 +275,7 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
             const float* st = stats(j % kSt);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                uint32_t s[32], dp[32], p[16], ds[16];
+                uint32_t s[32], dp[32], p[16], ds[16], p_rest[FINE ? 16 : 1], ds_rest[FINE ? 16 : 1];
                 tmem_ld32(ts + y * 32, s);
                 tmem_ld32(ts + 64 + y * 32, dp);
                 tmem_wait_ld(s);
@@ -279,6 +299,10 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
                     const float2 v = f2_unpack(f2_mul(f2_pack(u0, u1), x));
                     if (KEYS) p[e] = pack2<T>(u0, u1);
                     ds[e] = pack2<T>(v.x, v.y);
+                    if (FINE) {
+                        if (KEYS) p_rest[e] = rest2<T>(p[e], u0, u1);
+                        ds_rest[e] = rest2<T>(ds[e], v.x, v.y);
+                    }
                 }
                 if (!KEYS) {
                     const int left = keys - (first + j) * kBN - y * 32;
@@ -289,11 +313,19 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
                         for (int e = 0; e < 16; ++e) {
                             if (2 * e >= left) ds[e] = 0u;
                             else if (2 * e + 1 >= left) ds[e] &= 0xffffu;
+                            if (!FINE) continue;
+                            if (2 * e >= left) ds_rest[e] = 0u;
+                            else if (2 * e + 1 >= left) ds_rest[e] &= 0xffffu;
                         }
                     }
                 }
-                tmem_st16(ts + 64 + y * 16, ds);
-                if (KEYS) tmem_st16(ts + y * 16, p);
+                // over the scores of their own half
+                tmem_st16(ts + 64 + y * 32, ds);
+                if (KEYS) tmem_st16(ts + y * 32, p);
+                if constexpr (FINE) {
+                    tmem_st16(ts + 64 + 16 + y * 32, ds_rest);
+                    if (KEYS) tmem_st16(ts + 16 + y * 32, p_rest);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -360,16 +392,16 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
 
 // Both roles in one launch, so that the blocks of the second fill the SMs that the first's last round leaves: keys
 // first where their walks are longer.
-template <class T, int DP>
+template <class T, int DP, bool FINE>
 __global__ void __launch_bounds__(512, 1)
     k_attn_bwd(const __grid_constant__ BwdArgs gq, const __grid_constant__ BwdArgs gk, const __grid_constant__ BwdTensors x,
                int keys_first) {
     pdl_entry();
     const int at = blockIdx.x, n = keys_first ? gk.blocks : gq.blocks;
     if ((at < n) == (keys_first != 0))
-        bwd_block<T, DP, true>(gk, keys_first ? at : at - n, x.k, x.v, x.q_walk, x.dout_walk);
+        bwd_block<T, DP, true, FINE>(gk, keys_first ? at : at - n, x.k, x.v, x.q_walk, x.dout_walk);
     else
-        bwd_block<T, DP, false>(gq, keys_first ? at - n : at, x.q, x.dout, x.k_walk, x.v_walk);
+        bwd_block<T, DP, false, FINE>(gq, keys_first ? at - n : at, x.q, x.dout, x.k_walk, x.v_walk);
 }
 
 // What the walks need of every row, eight lanes each. blockIdx.y = 0: of every query, padded: boost - lse log2(e), so
@@ -474,13 +506,19 @@ __global__ void __launch_bounds__(256) k_attn_sum(const BwdArgs g, int heads, in
 
 namespace {
 
-template <class T, int DP>
+template <class T, int DP, bool FINE>
 cudaError_t run(const BwdArgs& gq, const BwdArgs& gk, const BwdTensors& x, bool keys_first, cudaStream_t st) {
     constexpr int smem = BwdShape<DP, false>::kSmem > BwdShape<DP, true>::kSmem ? BwdShape<DP, false>::kSmem : BwdShape<DP, true>::kSmem;
-    auto* kernel = k_attn_bwd<T, DP>;
+    auto* kernel = k_attn_bwd<T, DP, FINE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
     return launch_pdl(kernel, dim3((unsigned)(gq.blocks + gk.blocks)), dim3(512), smem, st, gq, gk, x, (int)keys_first);
+}
+
+template <class T>
+cudaError_t typed(const BwdArgs& gq, const BwdArgs& gk, const BwdTensors& x, bool keys_first, int dp, bool fine, cudaStream_t st) {
+    if (dp == 64) return fine ? run<T, 64, true>(gq, gk, x, keys_first, st) : run<T, 64, false>(gq, gk, x, keys_first, st);
+    return fine ? run<T, 128, true>(gq, gk, x, keys_first, st) : run<T, 128, false>(gq, gk, x, keys_first, st);
 }
 
 template <class F>
@@ -513,10 +551,15 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const BwdTensors& x, cudaStream_t
     gk.t.tiles = tiles_k;
     gk.t.splits = w.splits_k;
     gk.blocks = (int)blocks_k;
+    // Rounding P and dS to 16 bits makes errors as large as the results' own rounding. Over many queries that is 1.4 times
+    // it; a few probabilities that carry a small call's gradients may all be rounded the far way. There the products
+    // take what the rounding left too (100
+    // queries of 8 heads over 400 keys of 64, bfloat16: 11.3 us without, 12.3 with it; 256 over 4346: 25.9 and 30.2).
+    const bool fine = (long long)a.batch * a.heads * a.len_q <= 512;
     count_launches(1);
     if (a.dtype == GS_DTYPE_F32) e = launch_attn_bwd_wide(gq, gk, x, w.keys_first, st);
-    else if (half) e = w.dp == 64 ? run<__half, 64>(gq, gk, x, w.keys_first, st) : run<__half, 128>(gq, gk, x, w.keys_first, st);
-    else e = w.dp == 64 ? run<__nv_bfloat16, 64>(gq, gk, x, w.keys_first, st) : run<__nv_bfloat16, 128>(gq, gk, x, w.keys_first, st);
+    else if (half) e = typed<__half>(gq, gk, x, w.keys_first, w.dp, fine, st);
+    else e = typed<__nv_bfloat16>(gq, gk, x, w.keys_first, w.dp, fine, st);
     if (e) return e;
     for (int keys = 0; keys < 2; ++keys) {
         const BwdArgs& g = keys ? gk : gq;

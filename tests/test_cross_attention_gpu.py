@@ -336,3 +336,17 @@ def test_wide_heads(dtype, b, lq, lk, h, hk, d, masked):
     q, k, v = _qkv(b, lq, lk, h, hk, d, dtype, lq)
     k_len = torch.tensor([lk - 70, 0][:b], dtype=torch.int32, device=DEV) if masked else None
     _check(q, k, v, k_len=k_len, seed=lk, backward=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lq,lk,h,hk,d", [(1, 3000, 8, 8, 40), (5, 390, 16, 16, 32), (2, 700, 8, 2, 128), (60, 100, 4, 4, 64)])
+def test_few_queries_lose_no_more_than_the_results_rounding(dtype, lq, lk, h, hk, d):
+    # dv = P^T dout: with P in two parts (relative 2 u^2) the result's own rounding is all that counts
+    q, k, v = _qkv(1, lq, lk, h, hk, d, dtype, 11)
+    q = q * 2
+    dout = _rand(q.shape, dtype, 5)
+    out, lse = api.gs_cross_attention_fwd(q, k, v)
+    _, _, dv = api.gs_cross_attention_bwd(dout, q, k, v, out, lse)
+    want = decoder.attention_bwd(_np(dout), _np(q), _np(k), _np(v), np.ones((1, lk), bool), d ** -0.5)["dv"]
+    least = np.linalg.norm(_np(torch.from_numpy(want).to(dtype)) - want)
+    assert np.linalg.norm(_np(dv) - want) <= 1.1 * least
