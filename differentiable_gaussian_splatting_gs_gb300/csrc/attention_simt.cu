@@ -3,12 +3,12 @@
 // sums in float32.
 //
 // Forward: a block of 256 threads per 64 queries of a head. It walks the keys in tiles of 64 with the
-// running maximum and sum of the softmax, so scores stay on chip. Backward: one kernel per 64 (heads above 128: 32) keys
+// running maximum and sum of the softmax, so scores stay on chip. Backward: a block per 64 (heads above 128: 32) keys
 // (dk, dv; walks the queries of all heads that share the key head) and one per as many queries (dq; walks
 // the keys). Each output is summed by one block in a fixed order: no atomics, the same bits every time,
 // at the price of forming S and dP twice. Bound by the reads of shared memory (69% of their rate) beside the multiply-adds
-// (54%), with eight warps an SM: 2 x 8 heads of 128, 2000 x 2500 float32, backward 4.7 ms (5.7 with single multiply-adds and
-// tiles staged an element at a time).
+// (54%), with eight warps an SM: 2 x 8 heads of 128, 2000 x 2500 float32, backward 4.1 ms (4.7 in two
+// launches; 5.7 with single multiply-adds and tiles staged an element at a time too).
 #include "attention.cuh"
 
 namespace gs {
@@ -167,9 +167,9 @@ __device__ __forceinline__ void store_rows(const AttnTensor& t, int d, int b, in
 struct Where {
     int b, h, tile;
 };
-__device__ __forceinline__ Where where(int tiles, int heads) {
-    const int bh = blockIdx.x / tiles;
-    return {bh / heads, bh % heads, (int)blockIdx.x % tiles};
+__device__ __forceinline__ Where where(int block, int tiles, int heads) {
+    const int bh = block / tiles;
+    return {bh / heads, bh % heads, block % tiles};
 }
 
 }  // namespace
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, in
     extern __shared__ float sm[];
     constexpr bool kTwice = DP <= 128;
     float *sq = sm, *sk = sq + kFM * (DP + 4), *sv = sk + kFN * (DP + 4), *sp = sv + kFN * (DP + 4);
-    const Where w = where(tiles, a.heads);
+    const Where w = where(blockIdx.x, tiles, a.heads);
     const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int len = key_count(a, w.b);
     stage<T, DP, kFM, false>(sq, a.q, a, w.b, w.h, w.tile * kFM, a.len_q);
@@ -261,12 +261,10 @@ __device__ __forceinline__ void tile_gradient(const AttnArgs& a, const float* sq
 }
 
 template <class T, int DP>
-__global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, int tiles) {
-    pdl_entry();
-    extern __shared__ float sm[];
+__device__ __forceinline__ void dkv_block(const AttnArgs& a, int block, int tiles, float* sm) {
     constexpr int M = kSide<DP>, R = M / 16, kRow = M * (DP + 4);
     float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sp = sdo + kRow, *sds = sp + M * kTileRow<M, true>;
-    const Where w = where(tiles, a.kv_heads);
+    const Where w = where(block, tiles, a.kv_heads);
     const int share = a.heads / a.kv_heads, ty = threadIdx.x / 16, tx = threadIdx.x % 16, n0 = w.tile * M;
     const int len = key_count(a, w.b);
     f32x2 dk[R][DP / 32], dv[R][DP / 32];
@@ -297,12 +295,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv_simt(const AttnArgs a, in
 }
 
 template <class T, int DP>
-__global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int tiles) {
-    pdl_entry();
-    extern __shared__ float sm[];
+__device__ __forceinline__ void dq_block(const AttnArgs& a, int block, int tiles, float* sm) {
     constexpr int M = kSide<DP>, R = M / 16, kRow = M * (DP + 4);
     float *sk = sm, *sv = sk + kRow, *sq = sv + kRow, *sdo = sq + kRow, *sds = sdo + kRow;
-    const Where w = where(tiles, a.heads);
+    const Where w = where(block, tiles, a.heads);
     const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16, q0 = w.tile * M;
     const int len = key_count(a, w.b);
     const long long row = ((long long)w.b * a.heads + w.h) * a.len_q;
@@ -323,6 +319,16 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq_simt(const AttnArgs a, int
 #pragma unroll
     for (int i = 0; i < R; ++i) one[i] = 1.f;
     store_rows<T, DP>(a.dq, a.d, w.b, w.h, q0, a.len_q, ty, tx, dq, one);
+}
+
+// The dk, dv blocks, then the dq blocks, which fill the SMs that the others' last round leaves.
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_bwd_simt(const AttnArgs a, int tiles_k, int tiles_q) {
+    pdl_entry();
+    extern __shared__ float sm[];
+    const int block = blockIdx.x, keys = tiles_k * a.kv_heads * a.batch;
+    if (block < keys) dkv_block<T, DP>(a, block, tiles_k, sm);
+    else dq_block<T, DP>(a, block - keys, tiles_q, sm);
 }
 
 // delta = sum over the head's elements of dout out, a warp per query and head.
@@ -346,30 +352,30 @@ __global__ void __launch_bounds__(kThreads) k_attn_delta(const AttnArgs a) {
 
 namespace {
 
-template <class K>
-cudaError_t launch_tiles(K kernel, const AttnArgs& a, int rows, int tile, int heads, size_t smem, cudaStream_t st) {
+template <class K, class... A>
+cudaError_t launch_blocks(K kernel, long long blocks, size_t smem, cudaStream_t st, const A&... args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e) return e;
-    const int tiles = (rows + tile - 1) / tile;
-    const long long blocks = (long long)tiles * heads * a.batch;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     count_launches(1);
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, st, a, tiles);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, st, args...);
 }
 
 template <class T, int DP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * ((kFM + 2 * kFN) * (DP + 4) + kFM * kTileRow<kFN, DP <= 128>);
-    return launch_tiles(k_attn_fwd_simt<T, DP>, a, a.len_q, kFM, a.heads, smem, st);
+    const int tiles = (a.len_q + kFM - 1) / kFM;
+    return launch_blocks(k_attn_fwd_simt<T, DP>, (long long)tiles * a.heads * a.batch, smem, st, a, tiles);
 }
 
 template <class T, int DP>
 cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     constexpr int M = kSide<DP>;
     const size_t smem = sizeof(float) * (4 * M * (DP + 4) + 2 * M * kTileRow<M, true>);
-    cudaError_t e = launch_tiles(k_attn_dq_simt<T, DP>, a, a.len_q, M, a.heads, smem, st);
-    return e ? e : launch_tiles(k_attn_dkv_simt<T, DP>, a, a.len_k, M, a.kv_heads, smem, st);
+    const int tiles_k = (a.len_k + M - 1) / M, tiles_q = (a.len_q + M - 1) / M;
+    const long long blocks = (long long)tiles_k * a.kv_heads * a.batch + (long long)tiles_q * a.heads * a.batch;
+    return launch_blocks(k_attn_bwd_simt<T, DP>, blocks, smem, st, a, tiles_k, tiles_q);
 }
 
 // What comes here: 16-bit heads above 128, any head without a key, and in the backward float32 heads above 64.
