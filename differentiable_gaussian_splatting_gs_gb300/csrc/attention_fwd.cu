@@ -7,7 +7,10 @@
 // takes half the columns of its S. With two query tiles the products of one run beside the softmax of the
 // other. Where the columns suffice (16-bit, heads of up to 64) a tile has 192 for S, and S takes the first and the
 // last 128 of them in turn: the next S is then formed while this one's softmax runs, and the softmax
-// never waits for P V. Otherwise the next S waits for P V.
+// never waits for P V. A warp may then be a tile ahead of the other three of its query tile (one that raises its maximum
+// takes about twice as long), so what counts the warps' P, and what says that a product is done, has a barrier for even
+// and one for odd key tiles: an arrival, or a wait by parity, cannot be taken for the tile before. Otherwise the next
+// S waits for P V.
 //
 // The softmax is bound by what a warp issues one after the other, its exponentials first (4 cycles a warp instruction
 // and scheduler: 1024 for two 128 x 128 tiles, as many as their products take with heads of 64). So 16-bit tiles do not
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
     pdl_entry();
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t q_full, k_full[kSt], v_full[kSt], k_free[kSt], v_free[kSt], s_full[NQ], s_free[NQ],
-        p_full[NQ], o_done[NQ], drain[2];
+        p_full[NQ][2], o_done[NQ][2], drain[2];  // [2]: of even and of odd key tiles
     __shared__ uint32_t tmem_base;
     const AttnArgs& a = t.a;
     const uint32_t sq = (smem_u32(raw) + 1023u) & ~1023u, sk = sq + NQ * S::kQ, sv = sk + kSt * S::kKV;
@@ -88,8 +91,10 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], 4);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_done[i], 1);
+            for (int e = 0; e < 2; ++e) {
+                mbar_init(&p_full[i][e], 4);
+                mbar_init(&o_done[i][e], 1);
+            }
         }
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         mma_ts(tm + S::kO + i * DP, tm + i * S::kP + S::p_at(j) + p_column<PL, BN>(C::a(c), x), vb + x * 128, pv_desc,
                                (!S::kRegO && j > 0) || c > 0 || x > 0);
                 }
-                if (j >= n - 2) mma_commit(&o_done[i]);
+                if (j >= n - 2) mma_commit(&o_done[i][j & 1]);
                 if (i == i1 - 1) mma_commit(&v_free[s]);
             };
             bool ok = warp_wait_all(&q_full, 0, &k_full[0], 0, limit, a.err);
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             for (int j = 0; j < n && ok; ++j) {
                 const bool more = j + 1 < n;
                 uint64_t *vf = &v_full[j % kSt], *kf = &k_full[(j + 1) % kSt];
-                const unsigned vp = j / kSt, kp = (j + 1) / kSt;
+                const unsigned vp = j / kSt, kp = (j + 1) / kSt, pp = j / 2;
                 if (S::kTurns) {
                     if (more) {
                         // over the P of tile j - 1, whose P V this thread issued before
@@ -180,14 +185,14 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         tc_fence_after();
                         scores(i0, j + 1);
                     }
-                    if (!(ok = warp_wait_all(vf, vp, &p_full[i0], j, limit, a.err))) break;
+                    if (!(ok = warp_wait_all(vf, vp, &p_full[i0][j & 1], pp, limit, a.err))) break;
                     tc_fence_after();
                     values(i0, j);
                 } else {
                     for (int i = 0; i < NQ; ++i) {
                         // with one stage the next K comes while P V runs
-                        if (!(ok = more && kSt > 1 ? warp_wait_all(vf, vp, &p_full[i], j, kf, kp, limit, a.err)
-                                                   : warp_wait_all(vf, vp, &p_full[i], j, limit, a.err)))
+                        if (!(ok = more && kSt > 1 ? warp_wait_all(vf, vp, &p_full[i][j & 1], pp, kf, kp, limit, a.err)
+                                                   : warp_wait_all(vf, vp, &p_full[i][j & 1], pp, limit, a.err)))
                             break;
                         tc_fence_after();
                         values(i, j);
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         // P V of tile j - 1 has left O: before this S where that takes no turns, else before the next
                         if (S::kTurns) {
                             ok = ok && (j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
-                                                  : warp_wait(&o_done[i], 0, limit, a.err));
+                                                  : warp_wait(&o_done[i][(j - 1) & 1], 0, limit, a.err));
                             tc_fence_after();
                         }
 #pragma unroll
@@ -408,9 +413,10 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             sum += total(s2);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&p_full[i]);
+            warp_arrive(&p_full[i][j & 1]);
         }
-        if (n > 0) ok = ok && warp_wait(&o_done[i], n > 1, limit, a.err);  // committed for the last two tiles
+        // committed for the last two tiles, on a barrier each; the last one's commit covers every product before it
+        if (n > 0) ok = ok && warp_wait(&o_done[i][(n - 1) & 1], 0, limit, a.err);
         tc_fence_after();
         if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && h < h0 + t.fold && ok;
