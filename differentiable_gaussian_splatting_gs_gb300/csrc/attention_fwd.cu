@@ -7,10 +7,7 @@
 // takes half the columns of its S. With two query tiles the products of one run beside the softmax of the
 // other. Where the columns suffice (16-bit, heads of up to 64) a tile has 192 for S, and S takes the first and the
 // last 128 of them in turn: the next S is then formed while this one's softmax runs, and the softmax
-// never waits for P V. A warp may then be a tile ahead of the other three of its query tile (one that raises its maximum
-// takes about twice as long), so what counts the warps' P, and what says that a product is done, has a barrier for even
-// and one for odd key tiles: an arrival, or a wait by parity, cannot be taken for the tile before. Otherwise the next
-// S waits for P V.
+// never waits for P V. Otherwise the next S waits for P V.
 //
 // The softmax is bound by what a warp issues one after the other, its exponentials first (4 cycles a warp instruction
 // and scheduler: 1024 for two 128 x 128 tiles, as many as their products take with heads of 64). So 16-bit tiles do not
@@ -42,6 +39,13 @@ struct FwdShape {
     __device__ static int s_at(int j) { return kTurns && (j & 1) ? BN / 2 : 0; }
     __device__ static int p_at(int j) { return kTurns && (j & 1) ? BN : 0; }
     static constexpr int kIssuers = kTurns ? NQ : 1;  // threads that issue products
+    // Tiles whose softmaxes nothing else keeps apart begin them half a tile apart.
+    static constexpr bool kStagger = kTurns && NQ == 2;
+    // Barriers that count a query tile's warps whose P is written. Where S takes turns a warp may be a key tile ahead of
+    // the other three (one that raises its maximum takes about twice as long): with a barrier for even and one for odd
+    // key tiles its arrival cannot be taken for theirs. The stagger's barriers bring a query tile's warps together before
+    // each P, so that one suffices there (16384 x 4346 bf16, 32 heads: 495 us, with two 527).
+    static constexpr int kPF = kTurns && !kStagger ? 2 : 1;
     // The tensor cores add to the accumulator by truncation: over hundreds of products that is a drift of
     // 2^-25 each, lost in 16-bit results but not in float32 ones (-1.4e-5 at 2,500 keys). With three planes
     // each key tile's product therefore starts from zero and is added to O in registers, rounded (2e-7).
@@ -61,11 +65,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                const __grid_constant__ TcTensor tv) {
     using S = FwdShape<DP, PL, NQ, BN>;
     using C = Pairs<PL>;
-    constexpr int kSt = S::kStages;
+    constexpr int kSt = S::kStages, kPF = S::kPF;
     pdl_entry();
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t q_full, k_full[kSt], v_full[kSt], k_free[kSt], v_free[kSt], s_full[NQ], s_free[NQ],
-        p_full[NQ][2], o_done[NQ][2], drain[2];  // [2]: of even and of odd key tiles
+        p_full[NQ][kPF], o_done[NQ][2], drain[2];
     __shared__ uint32_t tmem_base;
     const AttnArgs& a = t.a;
     const uint32_t sq = (smem_u32(raw) + 1023u) & ~1023u, sk = sq + NQ * S::kQ, sv = sk + kSt * S::kKV;
@@ -91,10 +95,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], 4);
-            for (int e = 0; e < 2; ++e) {
-                mbar_init(&p_full[i][e], 4);
-                mbar_init(&o_done[i][e], 1);
-            }
+            for (int e = 0; e < kPF; ++e) mbar_init(&p_full[i][e], 4);
+            for (int e = 0; e < 2; ++e) mbar_init(&o_done[i][e], 1);
         }
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             for (int j = 0; j < n && ok; ++j) {
                 const bool more = j + 1 < n;
                 uint64_t *vf = &v_full[j % kSt], *kf = &k_full[(j + 1) % kSt];
-                const unsigned vp = j / kSt, kp = (j + 1) / kSt, pp = j / 2;
+                const unsigned vp = j / kSt, kp = (j + 1) / kSt, pp = j / kPF;
                 if (S::kTurns) {
                     if (more) {
                         // over the P of tile j - 1, whose P V this thread issued before
@@ -185,14 +187,14 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                         tc_fence_after();
                         scores(i0, j + 1);
                     }
-                    if (!(ok = warp_wait_all(vf, vp, &p_full[i0][j & 1], pp, limit, a.err))) break;
+                    if (!(ok = warp_wait_all(vf, vp, &p_full[i0][j % kPF], pp, limit, a.err))) break;
                     tc_fence_after();
                     values(i0, j);
                 } else {
                     for (int i = 0; i < NQ; ++i) {
                         // with one stage the next K comes while P V runs
-                        if (!(ok = more && kSt > 1 ? warp_wait_all(vf, vp, &p_full[i][j & 1], pp, kf, kp, limit, a.err)
-                                                   : warp_wait_all(vf, vp, &p_full[i][j & 1], pp, limit, a.err)))
+                        if (!(ok = more && kSt > 1 ? warp_wait_all(vf, vp, &p_full[i][j % kPF], pp, kf, kp, limit, a.err)
+                                                   : warp_wait_all(vf, vp, &p_full[i][j % kPF], pp, limit, a.err)))
                             break;
                         tc_fence_after();
                         values(i, j);
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         // Two tiles whose softmaxes nothing else keeps apart fall into step, and the exponentials stand still while both
         // load: one may begin its tile when the other is half through. Every warp comes through every turn, one
         // whose wait gave up too.
-        constexpr bool kStagger = S::kTurns && NQ == 2;
+        constexpr bool kStagger = S::kStagger;
         if (kStagger && i == 1 && n > 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             sum += total(s2);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&p_full[i][j & 1]);
+            warp_arrive(&p_full[i][j % kPF]);
         }
         // committed for the last two tiles, on a barrier each; the last one's commit covers every product before it
         if (n > 0) ok = ok && warp_wait(&o_done[i][(n - 1) & 1], 0, limit, a.err);
