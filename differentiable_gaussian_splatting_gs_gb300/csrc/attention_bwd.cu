@@ -153,8 +153,8 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
                 sent = j + 1;
             }
             // every copy lands before the block ends, whatever became of its reader
-            mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
-            for (int j = max(0, sent - kSt); j < sent; ++j) mbar_wait_bounded(&full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
+            mbar_drain(&a_full, 0, a.err);
+            for (int j = max(0, sent - kSt); j < sent; ++j) mbar_drain(&full[j % kSt], (j / kSt) & 1, a.err);
         } else if (warp > S::kElem && (!S::kOneIssuer || warp == S::kElem + 1) && n > 0) {  // products: the warp waits, one thread issues
             const uint32_t s_desc = mma_desc<T>(kBN, false), g_desc = mma_desc<T>(steps * 16, true);
             const int me = warp - S::kElem - 1;  // 0: S (and all with one issuer), 1: dP, 2: the sums
@@ -225,7 +225,7 @@ __device__ __forceinline__ void bwd_block(const BwdArgs& g, int at, const TcTens
             // no product is in flight when the tensor memory is freed
             if (elect_one()) {
                 mma_commit(&drain[me]);
-                mbar_wait_bounded(&drain[me], 0, kDrainLimit, a.err);
+                mbar_drain(&drain[me], 0, a.err);
             }
         }
     } else {  // elementwise: thread = row

@@ -118,8 +118,8 @@ __device__ __forceinline__ void wide_block(const BwdArgs& g, int at, const TcTen
                 sent = j + 1;
             }
             // every copy lands before the block ends, whatever became of its reader
-            mbar_wait_bounded(&a_full, 0, kDrainLimit, a.err);
-            for (int j = max(0, sent - 2); j < sent; ++j) mbar_wait_bounded(&full[j & 1], (j / 2) & 1, kDrainLimit, a.err);
+            mbar_drain(&a_full, 0, a.err);
+            for (int j = max(0, sent - 2); j < sent; ++j) mbar_drain(&full[j & 1], (j / 2) & 1, a.err);
         } else if (warp == 13 && n > 0 && elect_one()) {  // products
             const int steps = (a.d + 15) / 16;
             const uint32_t s_desc = mma_desc<__nv_bfloat16>(kBN, false), g_desc = mma_desc<__nv_bfloat16>(steps * 16, true);
@@ -169,7 +169,7 @@ __device__ __forceinline__ void wide_block(const BwdArgs& g, int at, const TcTen
             }
             // no product is in flight when the tensor memory is freed
             mma_commit(&drain);
-            mbar_wait_bounded(&drain, 0, kDrainLimit, a.err);
+            mbar_drain(&drain, 0, a.err);
         }
     } else if (warp >= 8) {  // sums of the tiles' products, and the results: thread = row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");

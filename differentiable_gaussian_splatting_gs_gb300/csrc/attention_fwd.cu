@@ -130,10 +130,10 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     sent = 2 * j + 2;
                 }
                 // every copy lands before the block ends, whatever became of its reader
-                mbar_wait_bounded(&q_full, 0, kDrainLimit, a.err);
+                mbar_drain(&q_full, 0, a.err);
                 const int nk = (sent + 1) / 2, nv = sent / 2;
-                for (int j = max(0, nk - kSt); j < nk; ++j) mbar_wait_bounded(&k_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
-                for (int j = max(0, nv - kSt); j < nv; ++j) mbar_wait_bounded(&v_full[j % kSt], (j / kSt) & 1, kDrainLimit, a.err);
+                for (int j = max(0, nk - kSt); j < nk; ++j) mbar_drain(&k_full[j % kSt], (j / kSt) & 1, a.err);
+                for (int j = max(0, nv - kSt); j < nv; ++j) mbar_drain(&v_full[j % kSt], (j / kSt) & 1, a.err);
             }
         } else if (warp - NQ * 4 - 1 < S::kIssuers && n > 0) {
             // Products: the warp waits, one thread issues. Where S takes turns, each query tile has a warp that
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
             // no product is in flight when the tensor memory is freed
             if (elect_one()) {
                 mma_commit(&drain[i0]);
-                mbar_wait_bounded(&drain[i0], 0, kDrainLimit, a.err);
+                mbar_drain(&drain[i0], 0, a.err);
             }
         }
     } else {  // softmax: thread = query

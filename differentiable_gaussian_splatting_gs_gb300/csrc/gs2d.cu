@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kB2) k_render2d_fwd(const float4* __restrict__
             mbar_arrive_expect_tx(&s.bar[slot], (unsigned)min(kB2, count - (b + 2) * kB2) * 64u);
         if (__syncthreads_count(!(done0 && done1)) == 0) break;
     }
-    for (int k = consumed + 1; k <= issued; ++k) mbar_wait_bounded(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, 1u << 22, err);
+    for (int k = consumed + 1; k <= issued; ++k) mbar_drain(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, err);
     const size_t plane = (size_t)cam.width * cam.height;
     if (in0) {
         const size_t pix = (size_t)py0 * cam.width + px;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kB2) k_render2d_bwd(const float4* __restrict__
         if (threadIdx.x == 0 && b >= 2) mbar_arrive_expect_tx(&s.bar[slot], (unsigned)kB2 * 64u);
         __syncthreads();
     }
-    for (int k = consumed + 1; k <= issued; ++k) mbar_wait_bounded(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, 1u << 22, err);
+    for (int k = consumed + 1; k <= issued; ++k) mbar_drain(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, err);
 }
 
 // Gradients of the record fields from the backward sums, in place. With the natural-unit sums

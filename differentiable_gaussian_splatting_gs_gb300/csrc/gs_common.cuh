@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "gs.h"
+#include "wait.h"
 
 namespace gs {
 
@@ -186,10 +187,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, unsigned parity) {
     return ok != 0;
 }
 
-// Bound of the waits that let in-flight bulk copies land before a block exits early; independent
-// of the caller's spin limit so that a small limit cannot leave copies running into a dead block.
-constexpr unsigned kDrainLimit = 1u << 22;
-
 // Bounded wait for phase `parity` of `bar`; false (and the timeout bit set) when it gives up.
 // Every 1024 polls it also gives up if another wait has already set the timeout bit, so that a
 // systematic failure costs one wait bound in total rather than one per block.
@@ -200,6 +197,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, unsigned parity
     }
     atomicOr(err, kErrTimeout);
     return false;
+}
+
+// Waits for phase `parity` of `bar` before the block ends or its memory is freed: copies in flight land, products finish,
+// whatever became of the waits before (poll_drain). Sets the timeout bit when even that is not enough.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, unsigned parity, unsigned* err) {
+    if (!poll_drain([&] { return mbar_try_wait(bar, parity); })) atomicOr(err, kErrTimeout);
 }
 
 // ---- reductions (inline PTX) -----------------------------------------------------------------

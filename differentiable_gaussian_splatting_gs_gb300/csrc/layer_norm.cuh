@@ -156,7 +156,7 @@ struct NormRing {
     __device__ __forceinline__ void finish() {
         if (!ok && threadIdx.x % LPR == 0)
             for (int t = asked > kNormStages ? asked - kNormStages : 0; t < asked; ++t)
-                mbar_wait_bounded(full + t % kNormStages, (t / kNormStages) & 1, kDrainLimit, err);
+                mbar_drain(full + t % kNormStages, (t / kNormStages) & 1, err);
     }
 };
 

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kFwdThreads) k_preprocess_pipe(int n, const fl
         }
         if (vis) {
             if (!mbar_wait_bounded(bar, parity, spin_limit, err)) {
-                mbar_wait_bounded(bar, parity, kDrainLimit, err);  // let the copies land, then give up
+                mbar_drain(bar, parity, err);  // let the copies land, then give up
                 return;
             }
             parity ^= 1u;
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kBwdThreads, 5) k_preprocess_bwd_pipe(
         const int rad_next = nxt < groups && j < n ? radius[j] : 0;
         if (seen) {
             if (!mbar_wait_bounded(bar, parity, spin_limit, err)) {
-                mbar_wait_bounded(bar, parity, kDrainLimit, err);  // let the copies land, then give up
+                mbar_drain(bar, parity, err);  // let the copies land, then give up
                 return;
             }
             parity ^= 1u;

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kFwdBlock) k_render_fwd(const float4* __restri
     // bulk copies issued but not waited for (early termination or a wait that gave up) must land
     // before the block exits
     if (STAGING == GS_STAGE_BULK)
-        for (int k = consumed + 1; k <= issued; ++k) mbar_wait_bounded(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, kDrainLimit, err);
+        for (int k = consumed + 1; k <= issued; ++k) mbar_drain(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, err);
     const size_t plane = (size_t)cam.width * cam.height;
     if (in0) {
         const size_t pix = (size_t)py0 * cam.width + px;
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(BwdLayout<PX>::kThreads) k_render_bwd(
     }
     // after a wait that gave up, bulk copies still in flight must land before the block exits
     if (STAGING == GS_STAGE_BULK)
-        for (int k = consumed + 1; k <= issued; ++k) mbar_wait_bounded(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, kDrainLimit, err);
+        for (int k = consumed + 1; k <= issued; ++k) mbar_drain(&s.bar[k & 1], (unsigned)(k >> 1) & 1u, err);
 }
 
 // ---- host-side launchers ------------------------------------------------------------------------
