@@ -437,8 +437,8 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, st
 
 def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, stream=None):
     """Backward of gs_layer_norm_fwd: (dx, dweight, dbias); the last two are None without a weight (a layer
-    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into. workspace: a byte tensor
-    kept by the caller (allocated when None or too small)."""
+    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into. workspace: a
+    contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that starts on 16 bytes."""
     if stream is not None:
         with _on(stream, x):
             return gs_layer_norm_bwd(dy, x, mean, rstd, weight, out, workspace)
@@ -455,8 +455,8 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     """Cross attention of q [batch, len_q, heads, head_dim] over k, v [batch, len_k, kv_heads, head_dim] (heads a
     multiple of kv_heads; any strides with contiguous heads): (out like q, lse float32 [batch, heads, len_q]).
     k_len: int32 [batch], keys that count per batch entry; key_mask: bool [batch, len_k], True where a key
-    counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a byte
-    tensor kept by the caller (allocated when None or too small)."""
+    counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a
+    contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that starts on 256 bytes."""
     if stream is not None:
         with _on(stream, q):
             return gs_cross_attention_fwd(q, k, v, k_len, key_mask, scale, out, workspace)
@@ -465,7 +465,8 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
 
 def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, scale: float | None = None, grads=None,
                            workspace=None, stream=None):
-    """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given."""
+    """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given.
+    workspace: as gs_cross_attention_fwd's."""
     if stream is not None:
         with _on(stream, q):
             return gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len, key_mask, scale, grads, workspace)

@@ -138,8 +138,11 @@ void call(const at::Tensor& like, const char* where, F&& f) {
     throw Raised();
 }
 
-// A workspace of `need` bytes: the caller's when it is large enough, or `own`.
-void* workspace_of(const Given& given, size_t need, at::Tensor& own, const at::Tensor& like) {
+// A workspace of `need` bytes: the caller's when it is large enough, or `own`. The kernels write to all of these bytes, so
+// that the caller's must be one piece of the device's memory whatever its size.
+void* workspace_of(const Given& given, size_t need, at::Tensor& own, const at::Tensor& like, const char* where) {
+    if (given && (!given->is_contiguous() || given->device() != like.device()))
+        refuse(where, "workspace must be a contiguous tensor on ", like.device());
     if (need == 0) return nullptr;
     if (given && (size_t)given->numel() * given->element_size() >= need) return given->data_ptr();
     own = alloc({(int64_t)need}, at::kByte, like);
@@ -235,7 +238,7 @@ PyObject* layer_norm_bwd(PyObject* const* arg) {
     }
     at::Tensor own;
     const size_t need = out[1].defined() || out[2].defined() ? gs_layer_norm_workspace_bytes(rows.n, cols) : 0;
-    void* workspace = workspace_of(room, need, own, x);
+    void* workspace = workspace_of(room, need, own, x, me);
     auto address = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
     call(x, me, [&](void* stream) {
         return gs_layer_norm_bwd(dy.data_ptr(), dy_stride, x.data_ptr(), rows.stride, rows.n, cols, dtype, mean.data_ptr<float>(),
@@ -329,7 +332,7 @@ PyObject* attention_fwd(PyObject* const* arg) {
     const gs_heads ho = heads_of(out[0], r.q, q, me);
     at::Tensor own;
     const size_t need = attention_bytes(r, q, 0);
-    void* workspace = workspace_of(room, need, own, q);
+    void* workspace = workspace_of(room, need, own, q, me);
     call(q, me, [&](void* stream) {
         return gs_cross_attention_fwd(&r.a, &hq, &hk, &hv, &ho, out[1].data_ptr<float>(), workspace, need, stream);
     });
@@ -356,7 +359,7 @@ PyObject* attention_bwd(PyObject* const* arg) {
     const gs_heads gq = heads_of(grad[0], r.q, q, me), gk = heads_of(grad[1], r.kv, q, me), gv = heads_of(grad[2], r.kv, q, me);
     at::Tensor own;
     const size_t need = attention_bytes(r, q, 1);
-    void* workspace = workspace_of(room, need, own, q);
+    void* workspace = workspace_of(room, need, own, q, me);
     call(q, me, [&](void* stream) {
         return gs_cross_attention_bwd(&r.a, &hd, &hq, &hk, &hv, &ho, lse.data_ptr<float>(), &gq, &gk, &gv, workspace, need, stream);
     });
