@@ -10,10 +10,15 @@
 // never waits for P V. Otherwise the next S waits for P V.
 //
 // The softmax is bound by what a warp issues one after the other, its exponentials first (4 cycles a warp instruction
-// and scheduler: 1024 for two 128 x 128 tiles, as many as their products take with heads of 64). So 16-bit tiles do not
+// and scheduler: 1024 for two 128 x 128 tiles, as many as their products take with heads of 64). So bfloat16 tiles do not
 // look for the row's maximum: P is formed with the one in use, and only when the tile's sum shows that a score passed
 // it far (a sum above 2^12) is the maximum found and raised, O rescaled and P formed again. Below that P, its sums and its
-// products are as exact as with the maximum itself (relative rounding, float16 reaches 2^16).
+// products are as exact as with the maximum itself.
+//
+// float16 has no such room: P loses bits below 2^-14 and vanishes below 2^-25, and thousands of keys there may carry
+// the output, where the few others' values are zero or cancel. P is formed 2^12 times as large, so that a key keeps its
+// bits down to 2^-26 of the maximum in use (18 nats below it), and the maximum of every tile is looked for before P is formed
+// and raised as soon as P would pass 2^15.9.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -218,6 +223,11 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                        to = tm + S::kO + i * DP + lanes;
         const float c = a.scale * 1.4426950408889634f;  // scores in units of log2
         float top = -INFINITY, sum = 0.f;               // top: raw score in use as the maximum
+        constexpr bool kHalf = std::is_same<T, __half>::value;
+        // how far (log2) a score may pass the maximum in use where every tile's is looked for; the power of P for its range
+        constexpr float kRoom = kHalf ? 3.9f : 8.f, kBoost = kHalf ? 12.f : 0.f;
+        // the exponent's offset of a maximum in use; float16: rounded down, so that P of the maximum is 2^12 at most
+        auto offset = [&](float t) { return t == -INFINITY ? 0.f : kHalf ? __fmaf_rd(-t, c, kBoost) : -t * c; };
         constexpr int kOut = S::kRegO ? DP : 1;
         float out[kOut];
 #pragma unroll
@@ -308,8 +318,8 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                 return (p.x + p.y) + (q.x + q.y);
             };
             // whether the row's maximum in use is too far below m; a score of -inf is no error: exp(-inf) = 0
-            auto passed = [&](float m) { return (m - top) * c > 8.f || (top == -INFINITY && m > -INFINITY); };
-            auto base = [&]() { const float t0 = top == -INFINITY ? 0.f : -top * c; return f2_pack(t0, t0); };
+            auto passed = [&](float m) { return (m - top) * c > kRoom || (top == -INFINITY && m > -INFINITY); };
+            auto base = [&]() { const float t0 = offset(top); return f2_pack(t0, t0); };
             f32x2 s2[4];
             if constexpr (S::kRegO) {
                 // the registers hold O: the scores are read twice, and each group of P takes the columns of its scores
@@ -369,9 +379,35 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
                     tc_fence_before();
                     warp_arrive(&s_free[i]);
                 }
-                if (j == 0) {
+                // O times keep, once P V of tile j - 1 has left it: before this S where that takes no turns, else before the next
+                auto rescale = [&](float keep) {
+                    if (S::kTurns) {
+                        ok = ok && (j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
+                                              : warp_wait(&o_done[i][(j - 1) & 1], 0, limit, a.err));
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int g = 0; g < DP / 32; ++g) {
+                        uint32_t o[32];
+                        tmem_ld32(to + g * 32, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                        tmem_st32(to + g * 32, o);
+                    }
+                };
+                bool far = false;
+                float keep = 1.f;
+                if (kHalf || j == 0) {
                     if (!S::kTurns) second_half();
-                    top = find_max();
+                    const float m = find_max();
+                    if (!kHalf) {
+                        top = m;
+                    } else if ((far = passed(m))) {
+                        keep = top == -INFINITY ? 0.f : ex2_approx(offset(m) - offset(top));
+                        top = m;
+                        sum *= keep;
+                    }
                 }
                 s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
                 f32x2 b2 = base();
@@ -379,33 +415,20 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
 #pragma unroll
                 for (int g = 0; g < G / 2; ++g) probabilities(x[g], g, b2, s2);
                 if (kStagger && (i == 0 || j + 1 < n)) asm volatile("bar.arrive %0, 256;" ::"r"(2 - i) : "memory");
-                if (!S::kTurns) second_half();
+                if (!kHalf && !S::kTurns) second_half();
 #pragma unroll
                 for (int g = G / 2; g < G; ++g) probabilities(x[g], g, b2, s2);
-                // (a row whose scores were all -inf has no maximum in use: it is looked for too)
-                const bool far = total(s2) > 4096.f || top == -INFINITY;
-                if (__any_sync(0xffffffffu, far)) {
+                if (kHalf) {
+                    if (j > 0 && __any_sync(0xffffffffu, far)) rescale(keep);
+                } else if (far = total(s2) > 4096.f || top == -INFINITY; __any_sync(0xffffffffu, far)) {
+                    // (a row whose scores were all -inf has no maximum in use: it is looked for too)
                     const float m = find_max();
-                    const float keep = far ? (top == -INFINITY ? 0.f : ex2_approx((top - m) * c)) : 1.f;
-                    if (far) top = m;
-                    sum *= keep;
-                    if (j > 0) {
-                        // P V of tile j - 1 has left O: before this S where that takes no turns, else before the next
-                        if (S::kTurns) {
-                            ok = ok && (j + 1 < n ? warp_wait(&s_full[i], (j + 1) & 1, limit, a.err)
-                                                  : warp_wait(&o_done[i][(j - 1) & 1], 0, limit, a.err));
-                            tc_fence_after();
-                        }
-#pragma unroll
-                        for (int g = 0; g < DP / 32; ++g) {
-                            uint32_t o[32];
-                            tmem_ld32(to + g * 32, o);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                            tmem_st32(to + g * 32, o);
-                        }
+                    if (far) {
+                        keep = top == -INFINITY ? 0.f : ex2_approx((top - m) * c);
+                        top = m;
                     }
+                    sum *= keep;
+                    if (j > 0) rescale(keep);
                     s2[0] = s2[1] = s2[2] = s2[3] = f2_pack(0.f, 0.f);
                     b2 = base();
 #pragma unroll
@@ -423,7 +446,7 @@ __global__ void __launch_bounds__(FwdShape<DP, PL, NQ, BN>::kThreads, 1)
         if (S::kRegO && n > 0) add_tile();
         const bool live = row < a.len_q && h < h0 + t.fold && ok;
         const float f = sum == 0.f ? 0.f : 1.f / sum;
-        const float lse = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
+        const float lse = sum == 0.f ? -INFINITY : (kHalf ? log2f(sum) - offset(top) : top * c + log2f(sum)) * 0.6931471805599453f;
         const long long qrow = ((long long)b * a.heads + h) * a.len_q + row;
         if (!whole) {
             const long long prow = ((long long)split * t.tail + block - t.whole) * (NQ * kTileRows) + i * kTileRows + r;
