@@ -120,6 +120,13 @@ struct Items {
     PyObject* operator[](int i) const { return PySequence_Fast_GET_ITEM(fast, i); }
 };
 
+// The interpreter's lock is given up for as long as this lives, and taken again however the block is left (a tensor without
+// memory of its own throws where its address is asked for).
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The C entry on like's device and its current stream, without the interpreter's lock.
 template <class F>
 void call(const at::Tensor& like, const char* where, F&& f) {
@@ -127,9 +134,8 @@ void call(const at::Tensor& like, const char* where, F&& f) {
     {
         const c10::cuda::OptionalCUDAGuard guard(like.device());
         void* stream = c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
-        PyThreadState* state = PyEval_SaveThread();
+        const Unlocked unlocked;
         status = f(stream);
-        PyEval_RestoreThread(state);
     }
     if (status == GS_OK) return;
     PyObject* r = PyObject_CallFunction(g_check, "is", status, where);
