@@ -428,7 +428,7 @@ def _on(stream, like):
 
 def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
     """Layer norm over the last dimension: (y, mean, rstd); mean and rstd float32 [rows]. weight, bias:
-    [cols] of x's dtype or float32 (both the same), or None. out: (y, mean, rstd) to write into."""
+    [cols] of x's dtype or float32 (both the same), or None. out: (y, mean, rstd) to write into (y may be x)."""
     if stream is not None:
         with _on(stream, x):
             return gs_layer_norm_fwd(x, weight, bias, eps, out)
@@ -437,7 +437,7 @@ def gs_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, st
 
 def gs_layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, workspace=None, stream=None):
     """Backward of gs_layer_norm_fwd: (dx, dweight, dbias); the last two are None without a weight (a layer
-    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into. workspace: a
+    norm with a bias alone passes out=(dx, None, dbias)). out: the tensors to write into (dx may be dy or x). workspace: a
     contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that starts on 16 bytes."""
     if stream is not None:
         with _on(stream, x):
@@ -455,7 +455,7 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
     """Cross attention of q [batch, len_q, heads, head_dim] over k, v [batch, len_k, kv_heads, head_dim] (heads a
     multiple of kv_heads; any strides with contiguous heads): (out like q, lse float32 [batch, heads, len_q]).
     k_len: int32 [batch], keys that count per batch entry; key_mask: bool [batch, len_k], True where a key
-    counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into. workspace: a
+    counts. scale: of the scores, default 1 / sqrt(head_dim). out: (out, lse) to write into, apart from the inputs. workspace: a
     contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that starts on 256 bytes."""
     if stream is not None:
         with _on(stream, q):
@@ -465,7 +465,8 @@ def gs_cross_attention_fwd(q, k, v, k_len=None, key_mask=None, scale: float | No
 
 def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, scale: float | None = None, grads=None,
                            workspace=None, stream=None):
-    """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given.
+    """Backward of gs_cross_attention_fwd from its outputs and dout: (dq, dk, dv), written into `grads` when given (apart from
+    the inputs and from one another).
     workspace: as gs_cross_attention_fwd's."""
     if stream is not None:
         with _on(stream, q):

@@ -834,6 +834,13 @@ int check_rows(const char* where, const char* name, const void* p, int64_t strid
     return GS_OK;
 }
 
+// Rows may be written over the rows they are formed from, each over its own.
+int check_in_place(const char* where, const char* to, const void* y, int64_t y_stride, const char* from, const void* x, int64_t x_stride, int64_t rows) {
+    if (rows > 1 && y == x && y_stride != x_stride)
+        return fail(GS_ERR_ARG, "%s: %s lies on %s with another row stride (%lld, %lld)", where, to, from, (long long)y_stride, (long long)x_stride);
+    return GS_OK;
+}
+
 int check_attention(const gs_attention* a, AttnArgs& r) {
     if (!a) return fail(GS_ERR_ARG, "attention is NULL");
     if (a->dtype < GS_DTYPE_F32 || a->dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "attention: bad dtype %d", a->dtype);
@@ -874,6 +881,17 @@ int check_heads(const gs_heads* t, const char* name, const AttnArgs& a, int len,
     return GS_OK;
 }
 
+// A tensor that a call writes: elements of its own, and another start than what the call reads and writes besides. (A
+// tensor of another start may still overlap: that is for the caller to rule out.)
+int check_output(const AttnArgs& a, const char* name, const AttnTensor& t, int len, int heads, const AttnTensor* others, const int* lens, int n) {
+    if (len == 0) return GS_OK;
+    if ((a.batch > 1 && t.batch_stride == 0) || (len > 1 && t.len_stride == 0) || (heads > 1 && t.head_stride == 0))
+        return fail(GS_ERR_ARG, "attention: elements of %s share memory (a stride of 0)", name);
+    for (int i = 0; i < n; ++i)
+        if (lens[i] > 0 && others[i].data == t.data) return fail(GS_ERR_ARG, "attention: %s lies on another tensor of the call", name);
+    return GS_OK;
+}
+
 int check_workspace(const AttnArgs& a, bool backward, void* workspace, size_t bytes) {
     const size_t need = attn_workspace_bytes(a, backward);
     if (need > 0 && (!workspace || !aligned(workspace, 256) || bytes < need))
@@ -895,6 +913,7 @@ int gs_layer_norm_fwd(const void* x, int64_t x_stride, int64_t rows, int64_t col
         (s = check_rows(me, "y", y, y_stride, rows, cols, dtype)))
         return s;
     if (!aligned(bias, elem_bytes(weight_dtype))) return fail(GS_ERR_ARG, "%s: bias misaligned", me);
+    if ((s = check_in_place(me, "y", y, y_stride, "x", x, x_stride, rows))) return s;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GS_ERR_ARG, "%s: eps must be finite and not negative", me);
     if (rows > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
         return fail(GS_ERR_ARG, "%s: mean or rstd is NULL or misaligned", me);
@@ -919,6 +938,9 @@ int gs_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t 
     int s;
     if ((s = check_norm(me, rows, cols, dtype, weight, weight_dtype)) || (s = check_rows(me, "dy", dy, dy_stride, rows, cols, dtype)) ||
         (s = check_rows(me, "x", x, x_stride, rows, cols, dtype)) || (s = check_rows(me, "dx", dx, dx_stride, rows, cols, dtype)))
+        return s;
+    if ((s = check_in_place(me, "dx", dx, dx_stride, "dy", dy, dy_stride, rows)) ||
+        (s = check_in_place(me, "dx", dx, dx_stride, "x", x, x_stride, rows)))
         return s;
     if (rows > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
         return fail(GS_ERR_ARG, "%s: mean or rstd is NULL or misaligned", me);
@@ -949,6 +971,9 @@ int gs_cross_attention_fwd(const gs_attention* a, const gs_heads* q, const gs_he
     if (r.batch == 0 || r.len_q == 0) return GS_OK;
     if (!lse || !aligned(lse, 4)) return fail(GS_ERR_ARG, "attention: lse is NULL or misaligned");
     if ((s = check_workspace(r, false, workspace, workspace_bytes))) return s;
+    const AttnTensor read[] = {r.q, r.k, r.v};
+    const int lens[] = {r.len_q, r.len_k, r.len_k};
+    if ((s = check_output(r, "out", r.out, r.len_q, r.heads, read, lens, 3))) return s;
     r.lse = lse;
     if (!(r.err = error_word(&s))) return s;
     cudaError_t e = launch_attn_fwd(r, workspace, as_stream(stream));
@@ -970,6 +995,12 @@ int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs
     if (r.batch == 0 || (r.len_q == 0 && r.len_k == 0)) return GS_OK;
     if (r.len_q > 0 && (!lse || !aligned(lse, 4))) return fail(GS_ERR_ARG, "attention: lse is NULL or misaligned");
     if ((s = check_workspace(r, true, workspace, workspace_bytes))) return s;
+    const AttnTensor all[] = {r.dout, r.q, r.out, r.k, r.v, r.dq, r.dk};
+    const int lens[] = {r.len_q, r.len_q, r.len_q, r.len_k, r.len_k, r.len_q, r.len_k};
+    if ((s = check_output(r, "dq", r.dq, r.len_q, r.heads, all, lens, 5)) ||
+        (s = check_output(r, "dk", r.dk, r.len_k, r.kv_heads, all, lens, 6)) ||
+        (s = check_output(r, "dv", r.dv, r.len_k, r.kv_heads, all, lens, 7)))
+        return s;
     r.lse = const_cast<float*>(lse);
     if (!(r.err = error_word(&s))) return s;
     cudaError_t e = launch_attn_bwd(r, workspace, as_stream(stream));

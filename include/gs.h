@@ -486,7 +486,7 @@ int gs_train_step_host(gs_step_context* ctx, const gs_params* host_params, const
 /* Layer norm of `rows` rows of `cols` elements: y = (x - mean) rstd w + b with the row's mean and
  * rstd = 1 / sqrt(mean of (x - mean)^2 + eps).
  *   x, y: rows x cols of `dtype`, consecutive rows x_stride / y_stride elements apart (>= cols);
- *   y may be x.
+ *   y may be x (with x's row stride).
  *   weight, bias: [cols] of weight_dtype (`dtype` or GS_DTYPE_F32), each may be NULL (1 and 0).
  *   mean, rstd: [rows] float32, read again by the backward.
  * rows >= 0, 1 <= cols < 2^30, eps >= 0. Rows that start on 16-byte boundaries with cols a multiple
@@ -498,7 +498,7 @@ int gs_layer_norm_fwd(const void* x, int64_t x_stride, int64_t rows, int64_t col
 
 /* Backward of gs_layer_norm_fwd: with xhat = (x - mean) rstd and g = w dy,
  *   dx = rstd (g - mean(g) - xhat mean(g xhat)),  dweight = sum over rows of dy xhat,  dbias = sum of dy.
- * dweight, dbias: [cols] of weight_dtype, overwritten; each may be NULL. dx may be dy or x. workspace:
+ * dweight, dbias: [cols] of weight_dtype, overwritten; each may be NULL. dx may be dy or x (with its row stride). workspace:
  * gs_layer_norm_workspace_bytes(rows, cols) bytes, 16-byte aligned (unused when both are NULL).
  * Errors: GS_ERR_ARG, GS_ERR_CUDA.                                                               */
 size_t gs_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
@@ -534,7 +534,7 @@ typedef struct gs_attention {
 
 /* Cross attention: S = scale q k^T, P = softmax of S over the keys that take part, out = P v,
  * lse = log sum exp S (float32 [batch][heads][len_q], natural logarithm). A query without any key has
- * out = 0 and lse = -inf. out must not overlap an input. workspace: device buffer of
+ * out = 0 and lse = -inf. out must have elements of its own (no stride of 0) and not overlap an input. workspace: device buffer of
  * gs_cross_attention_workspace_bytes(a, 0) bytes (may be 0), 256-byte aligned.
  * Pointers must be aligned to their element. Errors: GS_ERR_ARG, GS_ERR_CUDA; a wait that gave up is
  * reported by gs_device_error.                                                                   */
@@ -545,7 +545,8 @@ int gs_cross_attention_fwd(const gs_attention* a, const gs_heads* q, const gs_he
 /* Backward of gs_cross_attention_fwd, from its out and lse: with delta = sum(dout out) per query and
  * dS = scale P (dout v^T - delta): dq = dS k, dk = dS^T q, dv = P^T dout, overwritten; dk and dv are
  * summed over the query heads that share a key head and 0 at keys that take no part; dq is 0 for a
- * query without any key. workspace: gs_cross_attention_workspace_bytes(a, 1) bytes, 256-byte aligned.
+ * query without any key. dq, dk and dv must have elements of their own and overlap neither an input nor one
+ * another. workspace: gs_cross_attention_workspace_bytes(a, 1) bytes, 256-byte aligned.
  * Errors as gs_cross_attention_fwd.                                                              */
 int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs_heads* q, const gs_heads* k,
                            const gs_heads* v, const gs_heads* out, const float* lse, const gs_heads* dq,

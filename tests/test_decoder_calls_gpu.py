@@ -8,6 +8,8 @@ import torch
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+from differentiable_gaussian_splatting_gs_gb300 import _abi, api  # noqa: E402
+
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 
@@ -38,3 +40,29 @@ def test_tensors_without_memory_raise():
     # in a process of its own: an exception that leaves the interpreter without its lock ends it
     r = subprocess.run([sys.executable, "-c", WITHOUT_MEMORY], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("usable"), (r.returncode, r.stderr[-2000:])
+
+
+def test_outputs_on_inputs_on_one_another_or_on_themselves_are_refused():
+    q, k, v = (torch.randn(2, n, h, 64, device=DEV) for n, h in ((40, 4), (90, 2), (90, 2)))
+    out, lse = api.gs_cross_attention_fwd(q, k, v)
+    dout = torch.randn_like(q)
+    fresh = lambda: [torch.empty_like(t) for t in (q, k, v)]  # noqa: E731
+    dq, dk, dv = fresh()
+    bad = [lambda: api.gs_cross_attention_fwd(q, k, v, out=(q, lse)),
+           lambda: api.gs_cross_attention_fwd(q, k, v, out=(torch.empty(2, 40, 1, 64, device=DEV).expand(-1, -1, 4, -1), lse)),
+           lambda: api.gs_cross_attention_fwd(q, k, v, out=(torch.empty(1, 40, 4, 64, device=DEV).expand(2, -1, -1, -1), lse))]
+    for grads in ((q, dk, dv), (dout, dk, dv), (out, dk, dv), (dq, k, dv), (dq, dk, v), (dq, v, dv), (dq, dk, dk),
+                  (dq, dk, torch.empty(2, 1, 2, 64, device=DEV).expand(-1, 90, -1, -1))):
+        bad.append(lambda g=grads: api.gs_cross_attention_bwd(dout, q, k, v, out, lse, grads=g))
+    x = torch.randn(50, 128, device=DEV)
+    over = x.as_strided((30, 64), (128, 1))
+    stats = [torch.empty(30, device=DEV) for _ in range(2)]
+    bad.append(lambda: api.gs_layer_norm_fwd(over, out=(x.as_strided((30, 64), (100, 1)), *stats)))
+    for call in bad:
+        with pytest.raises(_abi.GsError, match="lies on|share memory"):
+            call()
+    # interleaved in one buffer, elements of their own
+    both = torch.empty(2, 90, 4, 64, device=DEV)
+    grads = api.gs_cross_attention_bwd(dout, q, k, v, out, lse, grads=(dq, both[:, :, :2], both[:, :, 2:]))
+    want = api.gs_cross_attention_bwd(dout, q, k, v, out, lse)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
