@@ -7,6 +7,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -286,7 +287,8 @@ Attention attention_of(const at::Tensor& q, const at::Tensor& k, const Given& k_
     if (scale != Py_None) {
         s = PyFloat_AsDouble(scale);
         if (s == -1.0 && PyErr_Occurred()) throw Raised();
-        if (!(s > 0.0)) refuse(where, "scale must be positive");
+        // (below float32's range it would become 0, which stands for the default)
+        if (!((float)s > 0.f) || !std::isfinite((float)s)) refuse(where, "scale must be a positive, finite float32");
     }
     r.a.dtype = code;
     r.a.batch = (int32_t)b;

@@ -66,3 +66,10 @@ def test_outputs_on_inputs_on_one_another_or_on_themselves_are_refused():
     grads = api.gs_cross_attention_bwd(dout, q, k, v, out, lse, grads=(dq, both[:, :, :2], both[:, :, 2:]))
     want = api.gs_cross_attention_bwd(dout, q, k, v, out, lse)
     assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+@pytest.mark.parametrize("scale", [1e-50, 1e-46, 1e39, float("inf"), float("nan"), -1.0, 0.0])
+def test_scales_that_are_none_in_float32_are_refused(scale):
+    q = torch.randn(1, 5, 2, 16, device=DEV)
+    with pytest.raises(ValueError, match="scale"):
+        api.gs_cross_attention_fwd(q, q.clone(), q.clone(), scale=scale)
