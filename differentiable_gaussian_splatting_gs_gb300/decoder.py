@@ -56,7 +56,10 @@ class GaussianDecoder:
         return api.gs_layer_norm_bwd(dy, x, *stats, w, out=out)[0]
 
     def forward(self, tokens, k_len=None, key_mask=None) -> dict:
-        """The Gaussians' parameters (float32, as gs_preprocess takes them)."""
+        """The Gaussians' parameters (float32, as gs_preprocess takes them) from one scene's tokens [1, length,
+        token_channels]; k_len [1], key_mask [1, length] as gs_cross_attention_fwd's."""
+        if tokens.dim() != 3 or tokens.shape[0] != 1 or tokens.shape[2] != self.weights["wk"].shape[0]:
+            raise ValueError(f"tokens must be [1, length, {self.weights['wk'].shape[0]}] (one scene), got {tuple(tokens.shape)}")
         w = {k: v.to(self.dtype) for k, v in self.weights.items()}
         x, tokens = w["queries"], tokens[0].to(self.dtype)
         h, *stats_q = self._norm(x, "q")
