@@ -2,11 +2,12 @@
 
 The translation units under csrc/ are compiled in parallel and linked into one shared object
 with the C ABI of include/gs.h; csrc/bind.cpp becomes the Python module gs_bind.so, which calls it on
-torch tensors. The output goes to `_build/` beside this file.
+torch tensors (where torch is installed). The output goes to `_build/` beside this file.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import dataclasses
 import glob
 import importlib.util
 import os
@@ -46,9 +47,21 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _bind_commands(src: str, obj: str, out: str, nvcc: str) -> tuple[list[str], list[str]]:
+def _torch() -> tuple[str, str] | None:
+    """torch's folder and version, without importing it; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch_dir = list(spec.submodule_search_locations)[0]
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            return torch_dir, f.read()
+    except OSError:
+        return torch_dir, ""
+
+
+def _bind_commands(torch_dir: str, src: str, obj: str, out: str, nvcc: str) -> tuple[list[str], list[str]]:
     """The host compiler's commands for the Python module of the decoder operators' calls: compile, link."""
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
     torch_lib = os.path.join(torch_dir, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -59,6 +72,34 @@ def _bind_commands(src: str, obj: str, out: str, nvcc: str) -> tuple[list[str], 
             [cxx, "-shared", obj, "-o", out, "-L" + torch_lib, "-L" + BUILD] +
             ["-l" + x for x in ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch_python")] +
             ["-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN:" + torch_lib])
+
+
+@dataclasses.dataclass
+class _Bind:
+    """What the Python module's build takes; made: what it is made with, kept beside the object."""
+    obj: str
+    tmp: str
+    made: str
+    compile: list[str]
+    link: list[str]
+    stale: bool
+
+
+def _bind_jobs(nvcc: str, force: bool) -> _Bind | None:
+    """None without torch, whose headers the module needs and the library does not. Another torch, Python or compiler than the
+    module was made with makes it stale as much as its source does."""
+    found = _torch()
+    if found is None:
+        return None
+    src, obj, tmp = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o"), BIND + f".tmp{os.getpid()}"
+    compile_, link = _bind_commands(found[0], src, obj, tmp, nvcc)
+    made = " ".join(compile_) + "\n" + found[1]
+    try:
+        with open(obj + ".made") as f:
+            same = f.read() == made
+    except OSError:
+        same = False
+    return _Bind(obj, tmp, made, compile_, link, force or not same or _stale(obj, [src, os.path.join(INCLUDE, "gs.h")]))
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -75,10 +116,6 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc] + flags + ["-c", src, "-o", obj])
 
-    bind, bind_obj, bind_tmp = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o"), BIND + f".tmp{os.getpid()}"
-    bind_compile, bind_link = _bind_commands(bind, bind_obj, bind_tmp, nvcc)
-    bind_jobs = [bind_compile] if force or _stale(bind_obj, [bind, os.path.join(INCLUDE, "gs.h")]) else []
-
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -87,8 +124,9 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
             raise RuntimeError(f"{cmd[0]} failed ({r.returncode}):\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs + bind_jobs), os.cpu_count() or 1))) as ex:
-        for msg in ex.map(run, bind_jobs + jobs):
+    bind = _bind_jobs(nvcc, force)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        for msg in ex.map(run, ([bind.compile] if bind and bind.stale else []) + jobs):
             if verbose and msg:
                 print(msg)
     if force or jobs or _stale(LIB, objs):
@@ -96,9 +134,11 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
         run([nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs +
             ["-Xlinker", "-rpath," + _cuda_lib_dir(nvcc)])
         os.replace(tmp, LIB)
-    if bind_jobs or _stale(BIND, [bind_obj]):
-        run(bind_link)
-        os.replace(bind_tmp, BIND)
+    if bind and (bind.stale or _stale(BIND, [bind.obj])):
+        run(bind.link)
+        os.replace(bind.tmp, BIND)
+        with open(bind.obj + ".made", "w") as f:
+            f.write(bind.made)
     return LIB
 
 
