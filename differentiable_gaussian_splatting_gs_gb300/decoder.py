@@ -65,8 +65,8 @@ class GaussianDecoder:
         h, *stats_q = self._norm(x, "q")
         t, *stats_t = self._norm(tokens, "t")
         q = (h @ w["wq"]).view(1, self.n, self.heads, self.head_dim)
-        k = (t @ w["wk"]).view(1, -1, self.kv_heads, self.head_dim)
-        v = (t @ w["wv"]).view(1, -1, self.kv_heads, self.head_dim)
+        k = (t @ w["wk"]).view(1, t.shape[0], self.kv_heads, self.head_dim)
+        v = (t @ w["wv"]).view(1, t.shape[0], self.kv_heads, self.head_dim)
         a, lse = api.gs_cross_attention_fwd(q, k, v, k_len=k_len, key_mask=key_mask)
         x2 = x + a.view(self.n, -1) @ w["wo"]
         y, *stats_x = self._norm(x2, "x")
@@ -87,7 +87,7 @@ class GaussianDecoder:
         g["wo"].copy_(a.view(self.n, -1).t() @ dx2)
         da = (dx2 @ w["wo"].t()).view_as(a)
         dq, dk, dv = api.gs_cross_attention_bwd(da, q, k, v, a, lse, k_len=k_len, key_mask=key_mask)
-        dq, dk, dv = dq.view(self.n, -1), dk.view(t.shape[0], -1), dv.view(t.shape[0], -1)
+        dq, dk, dv = (x.flatten(2)[0] for x in (dq, dk, dv))
         g["wq"].copy_(h.t() @ dq)
         g["wk"].copy_(t.t() @ dk)
         g["wv"].copy_(t.t() @ dv)

@@ -73,3 +73,21 @@ def test_scales_that_are_none_in_float32_are_refused(scale):
     q = torch.randn(1, 5, 2, 16, device=DEV)
     with pytest.raises(ValueError, match="scale"):
         api.gs_cross_attention_fwd(q, q.clone(), q.clone(), scale=scale)
+
+
+def test_a_scene_without_tokens_has_the_gaussians_of_the_queries_alone():
+    from differentiable_gaussian_splatting_gs_gb300 import decoder
+
+    n = 20
+    base = {"mean3d": torch.zeros(n, 3, device=DEV), "log_scale": torch.zeros(n, 3, device=DEV), "quat": torch.ones(n, 4, device=DEV),
+            "opacity_logit": torch.zeros(n, device=DEV), "sh": torch.zeros(n, 1, 3, device=DEV)}
+    d = decoder.GaussianDecoder(base, 24, channels=16, heads=2, head_dim=8)
+    none = d.forward(torch.zeros(1, 0, 24, device=DEV))
+    masked = d.forward(torch.randn(1, 30, 24, device=DEV), k_len=torch.zeros(1, dtype=torch.int32, device=DEV))
+    assert all(torch.equal(none[k], masked[k]) for k in none)
+    grads = {k: torch.randn_like(v) for k, v in none.items()}
+    d.backward(grads)
+    want = {k: v.clone() for k, v in d.grads.items()}
+    d.forward(torch.zeros(1, 0, 24, device=DEV))
+    assert d.backward(grads).shape == (1, 0, 24)
+    assert all(torch.equal(d.grads[k], want[k]) for k in want)
