@@ -24,7 +24,7 @@
 // products' reads of shared memory bound it). Where columns are left (queries, heads of up to 64) Q and dout are moved there
 // first.
 //
-// Small calls (FINE) keep what the rounding of P and dS to 16 bits left beside them and multiply it too.
+// Sums over few rows (FINE) keep what the rounding of P and dS to 16 bits left beside them and multiply it too.
 #include "attention_tc.cuh"
 
 namespace gs {
@@ -551,11 +551,13 @@ cudaError_t launch_attn_bwd_tc(const TcBwd& w, const BwdTensors& x, cudaStream_t
     gk.t.tiles = tiles_k;
     gk.t.splits = w.splits_k;
     gk.blocks = (int)blocks_k;
-    // Rounding P and dS to 16 bits makes errors as large as the results' own rounding. Over many queries that is 1.4 times
-    // it; a few probabilities that carry a small call's gradients may all be rounded the far way. There the products
-    // take what the rounding left too (100
-    // queries of 8 heads over 400 keys of 64, bfloat16: 11.3 us without, 12.3 with it; 256 over 4346: 25.9 and 30.2).
-    const bool fine = (long long)a.batch * a.heads * a.len_q <= 512;
+    // Rounding P and dS to 16 bits makes errors as large as the results' own rounding: 1.4 times it over a call's gradients
+    // whatever its size, but the fewer rows a sum of dk or dv runs over, the more may be rounded the same way. The worst key
+    // head of 8 x 16 (bfloat16, dv) is off by 2.3 times that rounding with one row, 2.0 with five, 1.6 with 64 and 1.5 from
+    // 128 on. So sums of up to 64 rows (a walked tile) take what the rounding left too, which leaves 1.0 (8 x 16 heads of
+    // 64, 5 queries over 400 keys: 27.4 us without, 31.6 with it; 64 over 2000: 87 and 101), and small calls do, whose
+    // time is mostly latency (one head of 512 over 2500: 18.0 and 19.4; 2 x 16 heads of 256 over 2500, which stay without: 42 and 51).
+    const bool fine = (long long)a.len_q * (a.heads / a.kv_heads) <= kBN || (long long)a.batch * a.heads * a.len_q <= 512;
     count_launches(1);
     if (a.dtype == GS_DTYPE_F32) e = launch_attn_bwd_wide(gq, gk, x, w.keys_first, st);
     else if (half) e = typed<__half>(gq, gk, x, w.keys_first, w.dp, fine, st);
