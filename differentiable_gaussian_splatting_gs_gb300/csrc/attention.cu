@@ -58,7 +58,7 @@ Plan plan(const AttnArgs& a, bool backward, bool tensors) {
             p.part_lse = take((size_t)p.splits * bq * sizeof(float));
         }
     }
-    if (backward && !p.tc) p.delta = take(bq * sizeof(float));
+    if (backward && !p.tc && a.len_k > 0) p.delta = take(bq * sizeof(float));
     if (p.tc) {
         const bool wide = a.dtype == GS_DTYPE_F32, masked = a.key_mask || a.k_len;
         p.planes = wide ? 3 : 1;
@@ -213,7 +213,8 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st)
         const TcArgs t{a, nullptr, part, part_lse, 1, p.splits, 0, a.batch * a.heads, 1, 1};
         return e || !part ? e : launch_attn_combine(t, 1, p.dp, st);
     }
-    if (!p.tc) return launch_attn_simt(a, false, st);
+    if (a.len_k == 0) return launch_attn_zero(a, a.out, a.heads, a.len_q, a.lse, st);
+    if (!p.tc) return launch_attn_fwd_simt(a, st);
     if (p.whole > 0x7fffff00ll) return cudaErrorInvalidConfiguration;
     int *count, *index;
     e = lay_out(p, a, ws, count, index, st);
@@ -238,9 +239,13 @@ cudaError_t launch_attn_bwd(const AttnArgs& args, void* workspace, cudaStream_t 
     AttnArgs a = args;
     char* ws = static_cast<char*>(workspace);
     cudaError_t e;
+    if (a.len_q == 0 || a.len_k == 0) {
+        if ((e = launch_attn_zero(a, a.dq, a.heads, a.len_q, nullptr, st)) || (e = launch_attn_zero(a, a.dk, a.kv_heads, a.len_k, nullptr, st))) return e;
+        return launch_attn_zero(a, a.dv, a.kv_heads, a.len_k, nullptr, st);
+    }
     if (!p.tc) {
         a.delta = reinterpret_cast<float*>(ws + p.delta);
-        return (e = launch_attn_delta(a, st)) ? e : launch_attn_simt(a, true, st);
+        return (e = launch_attn_delta(a, st)) ? e : launch_attn_bwd_simt(a, st);
     }
     int *count, *index;
     unsigned* norms = reinterpret_cast<unsigned*>(ws + p.norms);

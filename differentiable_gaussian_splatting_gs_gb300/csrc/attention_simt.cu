@@ -1,6 +1,6 @@
 // Cross attention on the float32 pipes, for what the tensor-core kernels do not take: float32 heads above 128 (backward:
-// above 64), the backward of 16-bit heads above 128, and calls without a key. Every stride, mask and length; products and
-// sums in float32.
+// above 64) and the backward of 16-bit heads above 128. Every stride, mask and length; products and sums in float32.
+// Calls without a query or without a key, of any type, have only zeros (and an lse of -inf) to write.
 //
 // Forward: a block of 256 threads per 64 queries of a head. It walks the keys in tiles of 64 with the
 // running maximum and sum of the softmax, so scores stay on chip. Backward: a block per 64 (heads above 128: 32) keys
@@ -178,7 +178,7 @@ template <class T, int DP>
 __global__ void __launch_bounds__(kThreads) k_attn_fwd_simt(const AttnArgs a, int tiles) {
     pdl_entry();
     extern __shared__ float sm[];
-    constexpr bool kTwice = DP <= 128;
+    constexpr bool kTwice = false;  // heads of 256 leave no room for pairs
     float *sq = sm, *sk = sq + kFM * (DP + 4), *sv = sk + kFN * (DP + 4), *sp = sv + kFN * (DP + 4);
     const Where w = where(blockIdx.x, tiles, a.heads);
     const int hk = w.h / (a.heads / a.kv_heads), ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -350,6 +350,19 @@ __global__ void __launch_bounds__(kThreads) k_attn_delta(const AttnArgs a) {
     if (lane == 0) a.delta[warp] = s;
 }
 
+// Zeros, and an lse of -inf where there is one: a warp per row of a head.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_attn_zero(const AttnTensor t, int heads, int len, int d, long long rows, float* lse) {
+    pdl_entry();
+    const int lane = threadIdx.x & 31;
+    for (long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) / 32; row < rows; row += (long long)gridDim.x * (kThreads / 32)) {
+        const long long bh = row / len;
+        T* to = static_cast<T*>(t.data) + bh / heads * t.batch_stride + bh % heads * t.head_stride + row % len * t.len_stride;
+        for (int c = lane; c < d; c += 32) to[c] = T(0);
+        if (lse && lane == 0) lse[row] = -INFINITY;
+    }
+}
+
 namespace {
 
 template <class K, class... A>
@@ -378,14 +391,6 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     return launch_blocks(k_attn_bwd_simt<T, DP>, blocks, smem, st, a, tiles_k, tiles_q);
 }
 
-// What comes here: 16-bit heads above 128, any head without a key, and in the backward float32 heads above 64.
-template <class T>
-cudaError_t typed(const AttnArgs& a, bool backward, cudaStream_t st) {
-    if (a.d <= 64) return backward ? bwd<T, 64>(a, st) : fwd<T, 64>(a, st);
-    if (a.d <= 128) return backward ? bwd<T, 128>(a, st) : fwd<T, 128>(a, st);
-    return backward ? bwd<T, 256>(a, st) : fwd<T, 256>(a, st);
-}
-
 }  // namespace
 
 cudaError_t launch_attn_delta(const AttnArgs& a, cudaStream_t st) {
@@ -398,10 +403,20 @@ cudaError_t launch_attn_delta(const AttnArgs& a, cudaStream_t st) {
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
 }
 
-cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t st) {
-    if (a.dtype == GS_DTYPE_F32) return typed<float>(a, backward, st);
-    if (a.dtype == GS_DTYPE_F16) return typed<__half>(a, backward, st);
-    return typed<__nv_bfloat16>(a, backward, st);
+cudaError_t launch_attn_fwd_simt(const AttnArgs& a, cudaStream_t st) { return fwd<float, 256>(a, st); }
+
+cudaError_t launch_attn_bwd_simt(const AttnArgs& a, cudaStream_t st) {
+    if (a.dtype == GS_DTYPE_F32) return a.d <= 128 ? bwd<float, 128>(a, st) : bwd<float, 256>(a, st);
+    return a.dtype == GS_DTYPE_F16 ? bwd<__half, 256>(a, st) : bwd<__nv_bfloat16, 256>(a, st);
+}
+
+cudaError_t launch_attn_zero(const AttnArgs& a, const AttnTensor& t, int heads, int len, float* lse, cudaStream_t st) {
+    const long long rows = (long long)a.batch * heads * len;
+    if (rows == 0) return cudaSuccess;
+    const long long blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    count_launches(1);
+    auto* kernel = a.dtype == GS_DTYPE_F32 ? k_attn_zero<float> : k_attn_zero<unsigned short>;  // zero is all bits zero
+    return launch_pdl(kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, st, t, heads, len, a.d, rows, lse);
 }
 
 }  // namespace gs

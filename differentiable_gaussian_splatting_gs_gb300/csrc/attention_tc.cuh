@@ -6,7 +6,7 @@
 //
 // The kernels read Q, K, V and dout with tiled bulk copies, straight from the caller's tensors when these are
 // 16-bit with 16-byte aligned rows and every key takes part. Otherwise a copy kernel first lays a tensor out
-// in the workspace ("packed"): split into planes, padded to a row of 64 or 128 elements and, for K and V, with
+// in the workspace ("packed"): split into planes, padded to a row of 64, 128 or 256 elements and, for K and V, with
 // only the keys that take part, in their order, and zeros up to the next multiple of 128 keys. A masked
 // key then costs nothing, and what it holds (NaN) never meets a product.
 #pragma once

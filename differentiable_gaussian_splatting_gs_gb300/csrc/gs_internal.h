@@ -181,6 +181,9 @@ size_t attn_workspace_bytes(const AttnArgs& a, bool backward);
 cudaError_t launch_attn_fwd(const AttnArgs& a, void* workspace, cudaStream_t st);
 cudaError_t launch_attn_bwd(const AttnArgs& a, void* workspace, cudaStream_t st);
 cudaError_t launch_attn_delta(const AttnArgs& a, cudaStream_t st);
-cudaError_t launch_attn_simt(const AttnArgs& a, bool backward, cudaStream_t st);
+cudaError_t launch_attn_fwd_simt(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_bwd_simt(const AttnArgs& a, cudaStream_t st);
+// Zeros in all rows of t; lse (or NULL): -inf. Where there is no query, or no key.
+cudaError_t launch_attn_zero(const AttnArgs& a, const AttnTensor& t, int heads, int len, float* lse, cudaStream_t st);
 
 }  // namespace gs
