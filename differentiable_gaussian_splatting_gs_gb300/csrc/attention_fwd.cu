@@ -18,7 +18,11 @@
 // float16 has no such room: P loses bits below 2^-14 and vanishes below 2^-25, and thousands of keys there may carry
 // the output, where the few others' values are zero or cancel. P is formed 2^12 times as large, so that a key keeps its
 // bits down to 2^-26 of the maximum in use (18 nats below it), and the maximum of every tile is looked for before P is formed
-// and raised as soon as P would pass 2^15.9.
+// and raised as soon as P would pass 2^15.9 (16384 x 4346, 32 heads of 64: 544 us, 498 without. Scores of spread 10: 623 us,
+// where bfloat16's way takes 822. Forming P first and again where it passed took 557 to 1142).
+//
+// P is rounded to the tensors' type, the operand's of P V: the output's error against 64 bits is 1.4 times that of its own
+// rounding. Multiplying what the rounding leaves too would be half as many products again.
 #include "attention_tc.cuh"
 
 namespace gs {

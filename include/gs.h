@@ -516,8 +516,8 @@ typedef struct gs_heads {
 
 /* Sizes and masks of a cross attention of len_q queries over len_k keys. A key j of batch entry b
  * takes part when j < k_len[b] and key_mask[b key_mask_stride + j] != 0; what K and V hold at other
- * keys (NaN included) changes nothing. float32 elements that take part and are infinite give NaN (they
- * are computed with as sums of bfloat16 values). Zero-initialised fields select the defaults beside them. */
+ * keys (NaN included) changes nothing. float32 elements that take part and are infinite, or above the
+ * largest bfloat16 (3.39e38), give NaN (they are computed with as sums of bfloat16 values). Zero-initialised fields select the defaults beside them. */
 typedef struct gs_attention {
     int32_t dtype;            /* GS_DTYPE_* of Q, K, V, the output and their gradients */
     int32_t batch;
