@@ -37,7 +37,8 @@ EXPORTS = ("gs_preprocess", "gs_sort_workspace_bytes", "gs_bin_and_sort", "gs_re
            "gs_preprocess_bwd_stats", "gs_selftest_sort_timeout", "gs_render_bwd_sqerr",
            "gs_step_context_create", "gs_step_context_destroy", "gs_train_step_host", "gs_layer_norm_fwd",
            "gs_layer_norm_workspace_bytes", "gs_layer_norm_bwd", "gs_cross_attention_workspace_bytes",
-           "gs_cross_attention_fwd", "gs_cross_attention_bwd")
+           "gs_cross_attention_fwd", "gs_cross_attention_bwd", "gs_rms_norm_fwd", "gs_rms_norm_workspace_bytes",
+           "gs_rms_norm_bwd", "gs_quantize_fp8", "gs_matmul_fp8", "gs_clip_workspace_bytes", "gs_clip_grads")
 GS_DTYPE_F32, GS_DTYPE_F16, GS_DTYPE_BF16 = 0, 1, 2
 GS_STATIC_SORT_WORKSPACE_BYTES = 32 << 20
 GS_SELFTEST_SORT_WORKSPACE_BYTES = 128 << 10
@@ -92,6 +93,15 @@ class gs_attention(C.Structure):
                 ("head_dim", C.c_int32), ("len_q", C.c_int32), ("len_k", C.c_int32), ("scale", C.c_float),
                 ("k_len", C.c_void_p), ("key_mask", C.c_void_p), ("key_mask_stride", C.c_int64),
                 ("spin_limit", C.c_uint32)]
+
+
+class gs_fp8(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride", C.c_int64), ("scale", C.c_void_p), ("scale_row", C.c_int64),
+                ("scale_block", C.c_int64), ("block_rows", C.c_int32)]
+
+
+class gs_gradient(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
 
 
 class GsError(RuntimeError):
@@ -178,7 +188,18 @@ def load():
         lib.gs_cross_attention_workspace_bytes.restype = C.c_size_t
         lib.gs_cross_attention_fwd.argtypes = [patt, ph, ph, ph, ph, P, P, C.c_size_t, P]
         lib.gs_cross_attention_bwd.argtypes = [patt, ph, ph, ph, ph, ph, P, ph, ph, ph, P, C.c_size_t, P]
-        for name in ("gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_cross_attention_fwd", "gs_cross_attention_bwd"):
+        pq, pg = C.POINTER(gs_fp8), C.POINTER(gs_gradient)
+        lib.gs_rms_norm_fwd.argtypes = [P, I64, P, I64, I64, I64, I32, P, I32, F, P, I64, P, I64, pq, P, P]
+        lib.gs_rms_norm_workspace_bytes.argtypes = [I64, I64]
+        lib.gs_rms_norm_workspace_bytes.restype = C.c_size_t
+        lib.gs_rms_norm_bwd.argtypes = [P, I64, P, I64, P, I64, I64, I64, I32, P, P, I32, P, I64, P, P, C.c_size_t, P]
+        lib.gs_quantize_fp8.argtypes = [P, I64, I64, I64, I64, I32, pq, P]
+        lib.gs_matmul_fp8.argtypes = [pq, pq, I64, I64, I64, I32, P, I64, P]
+        lib.gs_clip_workspace_bytes.argtypes = [pg, I32]
+        lib.gs_clip_workspace_bytes.restype = C.c_size_t
+        lib.gs_clip_grads.argtypes = [pg, I32, I32, C.c_double, C.c_double, P, P, C.c_size_t, P]
+        for name in ("gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_cross_attention_fwd", "gs_cross_attention_bwd",
+                     "gs_rms_norm_fwd", "gs_rms_norm_bwd", "gs_quantize_fp8", "gs_matmul_fp8", "gs_clip_grads"):
             getattr(lib, name).restype = C.c_int
         for name in ("gs_preprocess", "gs_bin_and_sort", "gs_render_fwd", "gs_render_bwd",
                      "gs_preprocess_bwd", "gs_device_error", "gs_version", "gs_selftest_timeout"):

@@ -3,7 +3,7 @@
 The functions carry the C entry points' names (gs_preprocess, gs_bin_and_sort, gs_render_fwd,
 gs_render_bwd, gs_preprocess_bwd). They allocate outputs with torch when the caller passes none,
 marshal pointers and the current CUDA stream, and raise GsError on a non-zero status. All
-arithmetic runs in libgs_gb300.so. The calls of the decoder's operators (layer norm, cross attention) go
+arithmetic runs in libgs_gb300.so. The calls of the decoder's operators (norms, cross attention, 8-bit products, clipping) go
 through a compiled module (csrc/bind.cpp) instead of ctypes, with the same checks and errors.
 
 Dtypes: arrays the C ABI declares as uint32 (vals, tile ranges, contributor counts,
@@ -23,7 +23,8 @@ from ._abi import (GS_BWD_ADAPTIVE, GS_BWD_DIRECT, GS_BWD_SM, GS_BWD_WARP, GS_ER
 __all__ = ["Proj", "BinResult", "StepContext", "gs_train_step_host", "make_camera", "make_options", "alloc_proj", "gs_preprocess",
            "gs_sort_workspace_bytes", "gs_bin_and_sort", "gs_bin_and_sort_async", "gs_render_fwd", "gs_render_bwd",
            "gs_preprocess_bwd", "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_cross_attention_fwd",
-           "gs_cross_attention_bwd", "gs_cross_attention_workspace_bytes",
+           "gs_cross_attention_bwd", "gs_cross_attention_workspace_bytes", "gs_rms_norm_fwd", "gs_rms_norm_fp8", "gs_rms_norm_bwd",
+           "gs_quantize_fp8", "gs_matmul_fp8", "gs_grad_norm", "gs_clip_grads",
            "gs_device_error", "GsError", "GS_BWD_DIRECT", "GS_BWD_WARP", "GS_BWD_ADAPTIVE", "GS_BWD_SM"]
 
 
@@ -472,6 +473,85 @@ def gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len=None, key_mask=None, s
         with _on(stream, q):
             return gs_cross_attention_bwd(dout, q, k, v, out, lse, k_len, key_mask, scale, grads, workspace)
     return _abi.binding().cross_attention_bwd(dout, q, k, v, out, lse, k_len, key_mask, scale, grads, workspace)
+
+
+def gs_rms_norm_fwd(x, weight=None, residual=None, eps: float = 1e-6, out=None, stream=None):
+    """Root-mean-square norm of h = x + residual over the last dimension: (y, h, rstd), y = h rstd weight; h has x's dtype (x
+    itself without a residual), rstd is float32 [rows]. weight: [cols] of x's dtype or float32, or None. residual: like x.
+    out: (y, h, rstd) to write into; y and h may be x or the residual."""
+    if stream is not None:
+        with _on(stream, x):
+            return gs_rms_norm_fwd(x, weight, residual, eps, out)
+    return _abi.binding().rms_norm_fwd(x, weight, residual, eps, False, out)
+
+
+def gs_rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, out=None, stream=None):
+    """gs_rms_norm_fwd with y in 8 bits: (q, scale, h, rstd), q and scale as gs_quantize_fp8's, for gs_matmul_fp8."""
+    if stream is not None:
+        with _on(stream, x):
+            return gs_rms_norm_fp8(x, weight, residual, eps, out)
+    return _abi.binding().rms_norm_fwd(x, weight, residual, eps, True, out)
+
+
+def gs_rms_norm_bwd(dy, h, rstd, weight=None, dh=None, out=None, workspace=None, stream=None):
+    """Backward of gs_rms_norm_fwd: (dx, dweight); dx is the gradient of x and of the residual. dh: the gradient of h from its
+    other readers, or None. dweight is None without a weight. out: the tensors to write into (dx may be dy, h or dh).
+    workspace: a contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that
+    starts on 16 bytes."""
+    if stream is not None:
+        with _on(stream, h):
+            return gs_rms_norm_bwd(dy, h, rstd, weight, dh, out, workspace)
+    return _abi.binding().rms_norm_bwd(dy, h, rstd, weight, dh, out, workspace)
+
+
+def gs_quantize_fp8(x, block_rows: int = 1, out=None, stream=None):
+    """x [.., cols] in 8 bits: (q, scale). q: float8_e4m3fn of x's shape in rows that start on 16 bytes; scale: float32 [rows /
+    block_rows, cols / 128] (rounded up), one for each block of block_rows (1: activations and gradients; 128: weights) x 128
+    elements: max |x| of the block / 448. x may be the transpose of a matrix with contiguous rows. out: (q, scale) to
+    write into."""
+    if stream is not None:
+        with _on(stream, x):
+            return gs_quantize_fp8(x, block_rows, out)
+    return _abi.binding().quantize_fp8(x, block_rows, out)
+
+
+_DTYPE_CODES = {torch.float32: _abi.GS_DTYPE_F32, torch.float16: _abi.GS_DTYPE_F16, torch.bfloat16: _abi.GS_DTYPE_BF16}
+
+
+def gs_matmul_fp8(a, a_scale, b, b_scale, dtype=None, out=None, stream=None):
+    """a b^T of 8-bit values with scales: [.., n] of `dtype` (float32, float16 or bfloat16, the default) from a [.., k] with
+    a scale for each row and 128 columns, and b [n, k] with one for each 128 x 128, or for each row and 128 columns, as
+    gs_quantize_fp8 and gs_rms_norm_fp8 give them. Summed in float32. Rows start on 16 bytes. out: the tensor to write into.
+
+    Of y = x w^T the gradients are dx = gs_matmul_fp8 of dy and w^T (w.t() quantized by 128 x 128), and dw = of dy^T and
+    x^T (dy.t() and x.t() quantized by rows)."""
+    if stream is not None:
+        with _on(stream, a):
+            return gs_matmul_fp8(a, a_scale, b, b_scale, dtype, out)
+    if dtype is None:
+        code = -1 if out is not None else _abi.GS_DTYPE_BF16
+    elif dtype in _DTYPE_CODES:
+        code = _DTYPE_CODES[dtype]
+    else:
+        raise ValueError(f"gs_matmul_fp8: results are float32, float16 or bfloat16, not {dtype}")
+    return _abi.binding().matmul_fp8(a, a_scale, b, b_scale, code, out)
+
+
+def gs_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """2-norm of all elements of the gradients (a list of float32, float16 and bfloat16 tensors, each one piece of
+    memory): a float32 tensor without dimensions. norm: the tensor to write into. workspace: as gs_clip_grads's."""
+    return gs_clip_grads(grads, None, norm=norm, workspace=workspace, stream=stream)
+
+
+def gs_clip_grads(grads, max_norm: float | None, eps: float = 1e-6, out=None, norm=None, workspace=None, stream=None):
+    """Multiplies the gradients by min(1, max_norm / (norm + eps)), norm the 2-norm of all their elements, and returns the
+    norm as gs_grad_norm does. In place, or into `out` (tensors of the same shapes and dtypes). With a norm that is not a
+    number all elements become so. workspace: a contiguous tensor on the gradients' device, kept by the caller (one is
+    allocated when None or too small), that starts on 16 bytes."""
+    if stream is not None:
+        with _on(stream, grads[0]):
+            return gs_clip_grads(grads, max_norm, eps, out, norm, workspace)
+    return _abi.binding().clip_grads(grads, max_norm, eps, out, norm, workspace)
 
 
 def gs_kernel_launches() -> int:

@@ -1,5 +1,5 @@
 // The decoder operators' calls on torch tensors: checks, allocation of what the caller leaves out, the device's
-// current stream, and the C entry. A Python module of four functions and one size, wrapped with their documentation in
+// current stream, and the C entry. A Python module of nine functions and one size, wrapped with their documentation in
 // api.py. These calls are short (a layer norm of 2,000 x 256: 3 us on the GPU), and the same steps written in Python
 // cost 12 us (layer norm) to 26 us (attention, backward) around the C entry's 4 to 8.
 #include <ATen/cuda/EmptyTensor.h>
@@ -11,6 +11,7 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "gs.h"
 
@@ -374,6 +375,246 @@ PyObject* attention_bwd(PyObject* const* arg) {
     return tuple_of(grad, 3);
 }
 
+constexpr int64_t kFp8Block = 128;
+
+// Rows of t, also where they are empty.
+int64_t leading(const at::Tensor& t) {
+    int64_t n = 1;
+    for (int64_t i = 0; i + 1 < t.dim(); ++i) n *= t.size(i);
+    return n;
+}
+
+// 8-bit values for like's shape, in rows that start on 16 bytes.
+at::Tensor alloc_fp8(const at::Tensor& like) {
+    const int64_t dims = like.dim();
+    std::vector<int64_t> strides(dims, 1);
+    int64_t next = (like.size(-1) + 15) / 16 * 16;
+    for (int64_t i = dims - 2; i >= 0; --i) {
+        strides[i] = next;
+        next *= like.size(i) > 0 ? like.size(i) : 1;
+    }
+    return at::detail::empty_strided_cuda(like.sizes(), strides, at::kFloat8_e4m3fn, like.device());
+}
+
+// Scales of `rows` x `cols` values: those of consecutive rows lie together.
+at::Tensor alloc_scales(int64_t rows, int64_t cols, int64_t block, const at::Tensor& like) {
+    const int64_t up = (rows + block - 1) / block, across = (cols + kFp8Block - 1) / kFp8Block;
+    return at::detail::empty_strided_cuda({up, across}, {1, up > 0 ? up : 1}, at::kFloat, like.device());
+}
+
+// q, whose last dimension is contiguous and whose rows have one stride, with scales [rows / block, cols / 128]; block 0: 1 or
+// 128, by the scales' rows.
+gs_fp8 fp8_of(const at::Tensor& q, const at::Tensor& scale, int64_t block, const at::Tensor& like, const char* where) {
+    if (!q.is_cuda() || q.scalar_type() != at::kFloat8_e4m3fn || q.device() != like.device())
+        refuse(where, "8-bit values must be float8_e4m3fn CUDA tensors on ", like.device());
+    const Rows rows = rows_of(q, q, where);
+    const int64_t across = (q.size(-1) + kFp8Block - 1) / kFp8Block;
+    if (scale.scalar_type() != at::kFloat || scale.dim() != 2 || scale.device() != like.device())
+        refuse(where, "scales must be a float32 tensor of two dimensions on ", like.device());
+    const int64_t n = leading(q);
+    if (block == 0) block = scale.size(0) == n ? 1 : kFp8Block;
+    if (scale.size(0) != (n + block - 1) / block || scale.size(1) != across)
+        refuse(where, "scales of shape ", shape(scale.sizes()), " for values of shape ", shape(q.sizes()));
+    return {q.data_ptr(), rows.stride, scale.data_ptr<float>(), scale.stride(0), scale.stride(1), (int32_t)block};
+}
+
+// rms_norm_fwd(x, weight, residual, eps, fp8, out)
+PyObject* rms_norm_fwd(PyObject* const* arg) {
+    const bool fp8 = PyObject_IsTrue(arg[4]) == 1;
+    const char* me = fp8 ? "gs_rms_norm_fp8" : "gs_rms_norm_fwd";
+    const at::Tensor& x = tensor(arg[0], me);
+    const int dtype = dtype_code(x, me);
+    const Rows rows = rows_of(x, x, me);
+    const Given weight(arg[1], me), residual(arg[2], me);
+    check_vector(weight, x, me);
+    const int64_t cols = x.size(-1), r_stride = residual ? rows_of(*residual, x, me).stride : 0;
+    const double eps = PyFloat_AsDouble(arg[3]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    at::Tensor out[4];  // y or q, (scale,) h, rstd
+    const int n = fp8 ? 4 : 3;
+    at::Tensor &h = out[n - 2], &rstd = out[n - 1];
+    int64_t h_stride = cols, y_stride = cols;
+    if (arg[5] == Py_None) {
+        out[0] = fp8 ? alloc_fp8(x) : alloc(x.sizes(), x.scalar_type(), x);
+        if (fp8) out[1] = alloc_scales(rows.n, cols, 1, x);
+        if (residual) h = alloc(x.sizes(), x.scalar_type(), x);
+        rstd = alloc({rows.n}, at::kFloat, x);
+    } else {
+        const Items given(arg[5], n, me);
+        for (int i = 0; i < n; ++i)
+            if (i != n - 2 || residual) out[i] = tensor(given[i], me);
+        if (!fp8) y_stride = rows_of(out[0], x, me).stride;
+        else if (out[0].sizes() != x.sizes()) refuse(me, "8-bit values of shape ", shape(x.sizes()), " are needed, got ", shape(out[0].sizes()));
+        if (residual) h_stride = rows_of(h, x, me).stride;
+        check_floats(rstd, {rows.n}, x, me);
+    }
+    gs_fp8 q{};
+    if (fp8) q = fp8_of(out[0], out[1], 1, x, me);
+    call(x, me, [&](void* stream) {
+        return gs_rms_norm_fwd(x.data_ptr(), rows.stride, residual.address(), r_stride, rows.n, cols, dtype, weight.address(),
+                               weight ? dtype_code(*weight, me) : dtype, (float)eps, residual ? h.data_ptr() : nullptr, h_stride,
+                               fp8 ? nullptr : out[0].data_ptr(), y_stride, fp8 ? &q : nullptr, rstd.data_ptr<float>(), stream);
+    });
+    if (!residual) h = x;
+    return tuple_of(out, n);
+}
+
+// rms_norm_bwd(dy, h, rstd, weight, dh, out, workspace)
+PyObject* rms_norm_bwd(PyObject* const* arg) {
+    const char* me = "gs_rms_norm_bwd";
+    const at::Tensor &dy = tensor(arg[0], me), &h = tensor(arg[1], me), &rstd = tensor(arg[2], me);
+    const int dtype = dtype_code(h, me);
+    const Rows rows = rows_of(h, h, me);
+    const int64_t cols = h.size(-1), dy_stride = rows_of(dy, h, me).stride;
+    const Given weight(arg[3], me), dh(arg[4], me), room(arg[6], me);
+    check_vector(weight, h, me);
+    check_floats(rstd, {rows.n}, h, me);
+    const int64_t dh_stride = dh ? rows_of(*dh, h, me).stride : 0;
+    at::Tensor out[2];
+    int64_t dx_stride = cols;
+    if (arg[5] == Py_None) {
+        out[0] = alloc(h.sizes(), h.scalar_type(), h);
+        if (weight) out[1] = alloc({cols}, weight->scalar_type(), h);
+    } else {
+        const Items given(arg[5], 2, me);
+        out[0] = tensor(given[0], me);
+        dx_stride = rows_of(out[0], h, me).stride;
+        const Given g(given[1], me);
+        check_vector(g, h, me);
+        if (g && weight && g->scalar_type() != weight->scalar_type()) refuse(me, "weight and dweight must have one dtype");
+        if (g) out[1] = *g;
+    }
+    const int kind = weight ? dtype_code(*weight, me) : out[1].defined() ? dtype_code(out[1], me) : dtype;
+    at::Tensor own;
+    const size_t need = out[1].defined() ? gs_rms_norm_workspace_bytes(rows.n, cols) : 0;
+    void* workspace = workspace_of(room, need, own, h, me);
+    call(h, me, [&](void* stream) {
+        return gs_rms_norm_bwd(dy.data_ptr(), dy_stride, h.data_ptr(), rows.stride, dh.address(), dh_stride, rows.n, cols, dtype,
+                               rstd.data_ptr<float>(), weight.address(), kind, out[0].data_ptr(), dx_stride,
+                               out[1].defined() ? out[1].data_ptr() : nullptr, workspace, need, stream);
+    });
+    return tuple_of(out, 2);
+}
+
+// quantize_fp8(x, block_rows, out)
+PyObject* quantize_fp8(PyObject* const* arg) {
+    const char* me = "gs_quantize_fp8";
+    const at::Tensor& x = tensor(arg[0], me);
+    const int dtype = dtype_code(x, me);
+    const int64_t block = PyLong_AsLongLong(arg[1]);
+    if (block == -1 && PyErr_Occurred()) throw Raised();
+    if (block != 1 && block != kFp8Block) refuse(me, "block_rows must be 1 or 128, got ", block);
+    if (x.dim() == 0) refuse(me, "the last dimension must be contiguous");
+    const int64_t cols = x.size(-1);
+    int64_t rows, row_stride, col_stride = 1;
+    if (x.dim() == 2 && x.stride(1) != 1 && x.stride(0) == 1) {  // a transposed matrix
+        rows = x.size(0);
+        row_stride = 1;
+        col_stride = x.stride(1);
+    } else {
+        row_stride = rows_of(x, x, me).stride;
+        rows = leading(x);
+    }
+    at::Tensor out[2];
+    if (arg[2] == Py_None) {
+        out[0] = alloc_fp8(x);
+        out[1] = alloc_scales(rows, cols, block, x);
+    } else {
+        const Items given(arg[2], 2, me);
+        for (int i = 0; i < 2; ++i) out[i] = tensor(given[i], me);
+        if (out[0].sizes() != x.sizes()) refuse(me, "8-bit values of shape ", shape(x.sizes()), " are needed, got ", shape(out[0].sizes()));
+    }
+    const gs_fp8 q = fp8_of(out[0], out[1], block, x, me);
+    call(x, me, [&](void* stream) { return gs_quantize_fp8(x.data_ptr(), row_stride, col_stride, rows, cols, dtype, &q, stream); });
+    return tuple_of(out, 2);
+}
+
+// matmul_fp8(a, a_scale, b, b_scale, dtype, out); dtype: GS_DTYPE_*, or -1: out's
+PyObject* matmul_fp8(PyObject* const* arg) {
+    const char* me = "gs_matmul_fp8";
+    const at::Tensor &a = tensor(arg[0], me), &a_scale = tensor(arg[1], me), &b = tensor(arg[2], me), &b_scale = tensor(arg[3], me);
+    if (a.dim() == 0 || b.dim() != 2 || a.size(-1) != b.size(1))
+        refuse(me, "a [.., k] and b [n, k] are needed, got ", shape(a.sizes()), " and ", shape(b.sizes()));
+    const gs_fp8 qa = fp8_of(a, a_scale, 1, a, me), qb = fp8_of(b, b_scale, 0, a, me);
+    long code = PyLong_AsLong(arg[4]);
+    if (code == -1 && PyErr_Occurred()) throw Raised();
+    const int64_t n = b.size(0), k = b.size(1);
+    const int64_t m = leading(a);
+    int64_t stride = n;
+    std::vector<int64_t> sizes(a.sizes().begin(), a.sizes().end());
+    sizes.back() = n;
+    at::Tensor out;
+    if (arg[5] == Py_None) {
+        out = alloc(sizes, code == GS_DTYPE_F32 ? at::kFloat : code == GS_DTYPE_F16 ? at::kHalf : at::kBFloat16, a);
+    } else {
+        out = tensor(arg[5], me);
+        const int own = dtype_code(out, me);
+        if ((code >= 0 && code != own) || out.sizes() != at::IntArrayRef(sizes) || out.device() != a.device())
+            refuse(me, "a result of shape ", shape(sizes), " and the dtype asked for is needed on ", a.device());
+        code = own;
+        stride = rows_of(out, out, me).stride;
+    }
+    if (code < 0) code = GS_DTYPE_BF16;
+    call(a, me, [&](void* stream) { return gs_matmul_fp8(&qa, &qb, m, n, k, (int32_t)code, out.data_ptr(), stride, stream); });
+    return wrap(out);
+}
+
+// clip_grads(grads, max_norm, eps, out, norm, workspace); max_norm None: the norm alone
+PyObject* clip_grads(PyObject* const* arg) {
+    const char* me = "gs_clip_grads";
+    PyObject* fast = PySequence_Fast(arg[0], "a list of tensors is needed");
+    if (!fast) throw Raised();
+    struct Release {
+        PyObject* o;
+        ~Release() { Py_XDECREF(o); }
+    } grads{fast}, outs{nullptr};
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
+    if (n == 0 || n > 1000000) refuse(me, "1 to 1,000,000 gradients are needed, got ", n);
+    const bool clip = arg[1] != Py_None;
+    const double max_norm = clip ? PyFloat_AsDouble(arg[1]) : 0.0, eps = PyFloat_AsDouble(arg[2]);
+    if (PyErr_Occurred()) throw Raised();
+    if (arg[3] != Py_None) {
+        if (!clip) refuse(me, "out without max_norm");
+        if (!(outs.o = PySequence_Fast(arg[3], "a list of tensors is needed"))) throw Raised();
+        if (PySequence_Fast_GET_SIZE(outs.o) != n) refuse(me, n, " outputs are needed");
+    }
+    std::vector<gs_gradient> list(n);
+    const at::Tensor& first = tensor(PySequence_Fast_GET_ITEM(fast, 0), me);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor& g = tensor(PySequence_Fast_GET_ITEM(fast, i), me);
+        list[i].dtype = dtype_code(g, me);
+        if (g.device() != first.device()) refuse(me, "gradient ", i, " is not on ", first.device());
+        if (!g.is_non_overlapping_and_dense()) refuse(me, "gradient ", i, " is not one piece of memory");
+        list[i].grad = g.numel() ? g.data_ptr() : nullptr;
+        list[i].n = g.numel();
+        list[i].out = nullptr;
+        if (!outs.o) continue;
+        const at::Tensor& o = tensor(PySequence_Fast_GET_ITEM(outs.o, i), me);
+        if (o.scalar_type() != g.scalar_type() || o.device() != g.device() || o.sizes() != g.sizes() || (g.numel() > 1 && o.strides() != g.strides()))
+            refuse(me, "output ", i, " must have the shape, strides, dtype and device of its gradient");
+        list[i].out = o.numel() ? o.data_ptr() : nullptr;
+    }
+    const Given given(arg[4], me), room(arg[5], me);
+    at::Tensor norm;
+    if (given) {
+        norm = *given;
+        check_floats(norm, {}, first, me);
+    } else {
+        norm = alloc({}, at::kFloat, first);
+    }
+    size_t need;
+    {
+        const c10::cuda::OptionalCUDAGuard guard(first.device());  // the size depends on the device's number of SMs
+        need = gs_clip_workspace_bytes(list.data(), (int32_t)n);
+    }
+    at::Tensor own;
+    void* workspace = workspace_of(room, need, own, first, me);
+    call(first, me, [&](void* stream) {
+        return gs_clip_grads(list.data(), (int32_t)n, clip, max_norm, eps, norm.data_ptr<float>(), workspace, need, stream);
+    });
+    return wrap(norm);
+}
+
 // init(check, memory_error)
 PyObject* init(PyObject* const* arg) {
     Py_INCREF(arg[0]);
@@ -414,6 +655,11 @@ PyMethodDef methods[] = {method<init, 2>("init"),
                          method<attention_workspace_bytes, 5>("cross_attention_workspace_bytes"),
                          method<attention_fwd, 8>("cross_attention_fwd"),
                          method<attention_bwd, 11>("cross_attention_bwd"),
+                         method<rms_norm_fwd, 6>("rms_norm_fwd"),
+                         method<rms_norm_bwd, 7>("rms_norm_bwd"),
+                         method<quantize_fp8, 3>("quantize_fp8"),
+                         method<matmul_fp8, 6>("matmul_fp8"),
+                         method<clip_grads, 6>("clip_grads"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gs_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,42 @@
+// 8-bit values with a scale for each block of 128: q = e4m3(x / scale), scale = max |x| of the block / 448, which the
+// block's largest element meets exactly. A block without elements above 448 2^-126 has scale 1 (its elements become 0), so
+// that no scale is 0 or subnormal. Magnitudes are compared as integers, where NaN is the largest: a block with one has a NaN
+// scale and NaN elements, one with an infinity an infinite scale, which nothing finite can stand beside.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gs {
+
+constexpr int kQBlock = 128;  // columns (or rows and columns) that share a scale
+
+__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ float block_scale(unsigned top) {
+    const float s = __uint_as_float(top) / 448.f;
+    return s < 1.17549435e-38f ? 1.f : s;
+}
+
+// Four values times the scale's reciprocal, the first in the lowest byte. (Rounding the reciprocal moves a quotient by an
+// ulp of float32, which changes the 4-bit significand of about one element in a million.)
+__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+}
+__device__ __forceinline__ uint8_t quantize1(float a, float inv) {
+    uint16_t lo;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(0.f), "f"(a * inv));
+    return (uint8_t)lo;
+}
+
+// Where a scale is: scale[row * row_stride + block * block_stride].
+struct ScaleAt {
+    float* p;
+    long long row, block;
+    __device__ __forceinline__ float& at(long long r, long long b) const { return p[r * row + b * block]; }
+};
+
+}  // namespace gs

@@ -1,12 +1,14 @@
 // C ABI of the library (declared in include/gs.h): argument checks, option defaults, camera
 // set-up and kernel launches. No exception crosses this boundary; failures return a GS_ERR_*
 // status and leave a message for gs_last_error_message().
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <string>
+#include <vector>
 
 #include "gs_common.cuh"
 #include "gs_internal.h"
@@ -1005,6 +1007,264 @@ int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs
     if (!(r.err = error_word(&s))) return s;
     cudaError_t e = launch_attn_bwd(r, workspace, as_stream(stream));
     return e ? cuda_fail(e, "gs_cross_attention_bwd") : GS_OK;
+}
+
+}  // extern "C"
+
+// ---- the 8-bit decoder: root-mean-square norm, 8-bit values, their product, clipping ---------------
+
+namespace gs {
+namespace {
+
+// Rows of `bytes` bytes each, `stride` bytes apart.
+struct Span {
+    const char* name;
+    const void* p;
+    int64_t rows, bytes, stride;
+};
+
+Span span_of(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride, size_t size) {
+    const int64_t bytes = cols * (int64_t)size, apart = stride * (int64_t)size;
+    if (rows > 1 && apart == bytes) return {name, p, 1, rows * bytes, rows * bytes};  // one piece
+    return {name, p, rows, bytes, rows > 1 ? apart : bytes};
+}
+
+constexpr int kFp8Block = 128;
+
+// Whether rows of one meet rows of the other: exact where the strides agree (as in slices of one buffer); where they do not
+// and the ranges meet, only a common start is taken for it.
+bool meet(const Span& a, const Span& b) {
+    if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.bytes == 0 || b.bytes == 0) return false;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    const uintptr_t p_end = p + (a.rows - 1) * a.stride + a.bytes, q_end = q + (b.rows - 1) * b.stride + b.bytes;
+    if (p_end <= q || q_end <= p) return false;
+    if (a.rows == 1 || b.rows == 1) {
+        const Span &one = a.rows == 1 ? a : b, &many = a.rows == 1 ? b : a;
+        const uintptr_t s = reinterpret_cast<uintptr_t>(one.p), m = reinterpret_cast<uintptr_t>(many.p);
+        if (many.rows == 1 || s <= m) return true;
+        const int64_t in = (int64_t)((s - m) % (uintptr_t)many.stride);
+        return in < many.bytes || in + one.bytes > many.stride;
+    }
+    if (a.stride != b.stride) return a.p == b.p;
+    const int64_t in = (int64_t)(q >= p ? (q - p) % (uintptr_t)a.stride : (a.stride - (int64_t)((p - q) % (uintptr_t)a.stride)) % a.stride);
+    return in < a.bytes || in + b.bytes > a.stride;
+}
+
+// What a call writes may lie on one of the first `same` inputs, row over row, and on nothing else.
+int check_apart(const char* where, const Span& out, const Span* in, int n, int same) {
+    for (int i = 0; i < n; ++i) {
+        if (i < same && out.p == in[i].p && out.stride == in[i].stride && out.bytes == in[i].bytes) continue;
+        if (meet(out, in[i])) return fail(GS_ERR_ARG, "%s: %s lies on %s", where, out.name, in[i].name);
+    }
+    return GS_OK;
+}
+
+int check_fp8(const char* where, const char* name, const gs_fp8* t, int64_t rows, int64_t cols, bool tiles) {
+    if (!t) return fail(GS_ERR_ARG, "%s: %s is NULL", where, name);
+    if (t->block_rows != 1 && !(tiles && t->block_rows == kFp8Block))
+        return fail(GS_ERR_ARG, "%s: block_rows %d of %s", where, t->block_rows, name);
+    if (rows == 0 || cols == 0) return GS_OK;
+    if (!t->data || !aligned(t->data, 16)) return fail(GS_ERR_ARG, "%s: %s is NULL or not 16-byte aligned", where, name);
+    if (rows > 1 && (t->stride < cols || t->stride > (1ll << 39) || t->stride % 16 != 0))
+        return fail(GS_ERR_ARG, "%s: row stride %lld of %s: a multiple of 16 of at least %lld is needed", where, (long long)t->stride, name, (long long)cols);
+    if (!t->scale || !aligned(t->scale, 4)) return fail(GS_ERR_ARG, "%s: the scales of %s are NULL or misaligned", where, name);
+    return GS_OK;
+}
+
+// Scales that a call writes: a place for each block.
+int check_scales(const char* where, const gs_fp8& t, int64_t rows, int64_t cols) {
+    const int64_t up = (rows + t.block_rows - 1) / t.block_rows, across = (cols + kFp8Block - 1) / kFp8Block;
+    if ((up > 1 && t.scale_row == 0) || (across > 1 && t.scale_block == 0))
+        return fail(GS_ERR_ARG, "%s: scales share memory (a stride of 0)", where);
+    return GS_OK;
+}
+
+int check_gradients(const char* me, const gs_gradient* g, int32_t count, bool clip) {
+    if (count < 0 || (count > 0 && !g)) return fail(GS_ERR_ARG, "%s: %d gradients at %p", me, count, (const void*)g);
+    struct Range {
+        uintptr_t from, to;
+        int32_t i;
+        bool out;
+    };
+    std::vector<Range> ranges;
+    ranges.reserve(2 * (size_t)count);
+    for (int32_t i = 0; i < count; ++i) {
+        const gs_gradient& t = g[i];
+        if (t.dtype < GS_DTYPE_F32 || t.dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "%s: bad dtype %d of gradient %d", me, t.dtype, i);
+        if (t.n < 0 || t.n > (1ll << 40)) return fail(GS_ERR_ARG, "%s: gradient %d of %lld elements", me, i, (long long)t.n);
+        if (t.n == 0) continue;
+        const size_t size = elem_bytes(t.dtype);
+        if (!t.grad || !aligned(t.grad, size) || !aligned(t.out, size)) return fail(GS_ERR_ARG, "%s: gradient %d is NULL or misaligned", me, i);
+        if (!clip) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t.grad), q = t.out ? reinterpret_cast<uintptr_t>(t.out) : p;
+        if (p != q) ranges.push_back({p, p + t.n * size, i, false});
+        ranges.push_back({q, q + t.n * size, i, true});
+    }
+    // in the order of their starts, each against what reaches furthest of those before it
+    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+    uintptr_t read = 0, written = 0;
+    for (const Range& r : ranges) {
+        if (r.from < written || (r.out && r.from < read)) return fail(GS_ERR_ARG, "%s: gradient %d lies on another that is written", me, r.i);
+        (r.out ? written : read) = std::max(r.out ? written : read, r.to);
+    }
+    return GS_OK;
+}
+
+}  // namespace
+}  // namespace gs
+
+extern "C" {
+
+int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int64_t rows,
+                    int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, float eps, void* h,
+                    int64_t h_stride, void* y, int64_t y_stride, const gs_fp8* q, float* rstd, void* stream) {
+    const char* me = "gs_rms_norm_fwd";
+    int s;
+    if ((s = check_norm(me, rows, cols, dtype, weight, weight_dtype)) || (s = check_rows(me, "x", x, x_stride, rows, cols, dtype)) ||
+        (residual && ((s = check_rows(me, "residual", residual, residual_stride, rows, cols, dtype)) ||
+                      (s = check_rows(me, "h", h, h_stride, rows, cols, dtype)))))
+        return s;
+    if ((y && q) || (!y && !q && rows > 0)) return fail(GS_ERR_ARG, "%s: one of y and q is needed", me);
+    if ((s = !q ? check_rows(me, "y", y, y_stride, rows, cols, dtype) : check_fp8(me, "q", q, rows, cols, false))) return s;
+    if (q && (s = check_scales(me, *q, rows, cols))) return s;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GS_ERR_ARG, "%s: eps must be finite and not negative", me);
+    if (rows > 0 && (!rstd || !aligned(rstd, 4))) return fail(GS_ERR_ARG, "%s: rstd is NULL or misaligned", me);
+    const size_t size = elem_bytes(dtype);
+    const Span to_h = span_of("h", residual ? h : nullptr, rows, cols, h_stride, size),
+               to_y = !q ? span_of("y", y, rows, cols, y_stride, size) : span_of("q", q->data, rows, cols, q->stride, 1),
+               in[] = {span_of("x", x, rows, cols, x_stride, size), span_of("the residual", residual, rows, cols, residual_stride, size), to_h};
+    if ((s = check_apart(me, to_h, in, 2, 2)) || (s = check_apart(me, to_y, in, 3, y ? 2 : 0))) return s;
+    if (rows == 0) return GS_OK;
+    unsigned* err = error_word(&s);
+    if (!err) return s;
+    RmsTensors t{};
+    t.x = x;
+    t.r = residual;
+    t.weight = weight;
+    t.h = residual ? h : nullptr;
+    t.y = y;
+    t.rstd = rstd;
+    t.x_stride = x_stride;
+    t.r_stride = residual_stride;
+    t.h_stride = h_stride;
+    t.y_stride = y_stride;
+    if (q) {
+        t.q = q->data;
+        t.q_stride = q->stride;
+        t.scale = q->scale;
+        t.scale_row = q->scale_row;
+        t.scale_block = q->scale_block;
+    }
+    cudaError_t e = launch_rms_fwd(dtype, t, rows, (int)cols, weight_dtype, eps, err, as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+size_t gs_rms_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 1 || cols >= (1ll << 30)) return 0;
+    return rms_bwd_workspace_bytes(rows, (int)cols);
+}
+
+int gs_rms_norm_bwd(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, const void* dh,
+                    int64_t dh_stride, int64_t rows, int64_t cols, int32_t dtype, const float* rstd, const void* weight,
+                    int32_t weight_dtype, void* dx, int64_t dx_stride, void* dweight, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    const char* me = "gs_rms_norm_bwd";
+    int s;
+    if ((s = check_norm(me, rows, cols, dtype, weight, weight_dtype)) || (s = check_rows(me, "dy", dy, dy_stride, rows, cols, dtype)) ||
+        (s = check_rows(me, "h", h, h_stride, rows, cols, dtype)) || (s = check_rows(me, "dx", dx, dx_stride, rows, cols, dtype)) ||
+        (dh && (s = check_rows(me, "dh", dh, dh_stride, rows, cols, dtype))))
+        return s;
+    if (rows > 0 && (!rstd || !aligned(rstd, 4))) return fail(GS_ERR_ARG, "%s: rstd is NULL or misaligned", me);
+    if (!aligned(dweight, elem_bytes(weight_dtype))) return fail(GS_ERR_ARG, "%s: dweight misaligned", me);
+    const size_t need = dweight ? rms_bwd_workspace_bytes(rows, (int)cols) : 0, size = elem_bytes(dtype);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+        return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
+    const Span to = span_of("dx", dx, rows, cols, dx_stride, size),
+               in[] = {span_of("dy", dy, rows, cols, dy_stride, size), span_of("h", h, rows, cols, h_stride, size),
+                       span_of("dh", dh, rows, cols, dh_stride, size)};
+    if ((s = check_apart(me, to, in, 3, 3))) return s;
+    unsigned* err = error_word(&s);
+    if (!err) return s;
+    RmsTensors t{};
+    t.weight = weight;
+    t.h = const_cast<void*>(h);
+    t.h_stride = h_stride;
+    t.rstd = const_cast<float*>(rstd);
+    cudaError_t e = launch_rms_bwd(dtype, t, dy, dy_stride, dh, dh_stride, rows, (int)cols, weight_dtype, dx, dx_stride, dweight,
+                                   static_cast<float*>(workspace), err, as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+int gs_quantize_fp8(const void* x, int64_t x_row_stride, int64_t x_col_stride, int64_t rows, int64_t cols, int32_t dtype,
+                    const gs_fp8* q, void* stream) {
+    const char* me = "gs_quantize_fp8";
+    int s;
+    if (dtype < GS_DTYPE_F32 || dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "%s: bad dtype %d", me, dtype);
+    if (rows < 0 || rows > (1ll << 40) || cols < 0 || cols >= (1ll << 30))
+        return fail(GS_ERR_ARG, "%s: %lld rows, %lld columns", me, (long long)rows, (long long)cols);
+    if ((s = check_fp8(me, "q", q, rows, cols, true))) return s;
+    if (rows == 0 || cols == 0) return GS_OK;
+    if ((s = check_scales(me, *q, rows, cols))) return s;
+    const size_t size = elem_bytes(dtype);
+    if (!x || !aligned(x, size)) return fail(GS_ERR_ARG, "%s: x is NULL or misaligned", me);
+    const bool by_cols = x_col_stride != 1 && cols > 1;
+    if (by_cols && x_row_stride != 1 && rows > 1)
+        return fail(GS_ERR_ARG, "%s: strides %lld, %lld of x: one must be 1", me, (long long)x_row_stride, (long long)x_col_stride);
+    const int64_t lines = by_cols ? cols : rows, len = by_cols ? rows : cols, stride = by_cols ? x_col_stride : x_row_stride;
+    if (lines > 1 && (stride < 0 || stride > (1ll << 40))) return fail(GS_ERR_ARG, "%s: stride %lld of x", me, (long long)stride);
+    const Span in = span_of("x", x, lines, len, stride < len ? len : stride, size);
+    if ((s = check_apart(me, span_of("q", q->data, rows, cols, q->stride, 1), &in, 1, 0))) return s;
+    unsigned* err = error_word(&s);
+    if (!err) return s;
+    cudaError_t e = launch_quantize(dtype, x, lines > 1 ? stride : 0, by_cols, rows, (int)cols, q->block_rows != 1, q->data, q->stride, q->scale,
+                                    q->scale_row, q->scale_block, as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+int gs_matmul_fp8(const gs_fp8* a, const gs_fp8* b, int64_t m, int64_t n, int64_t k, int32_t dtype, void* out,
+                  int64_t out_stride, void* stream) {
+    const char* me = "gs_matmul_fp8";
+    int s;
+    if (dtype < GS_DTYPE_F32 || dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "%s: bad dtype %d", me, dtype);
+    constexpr int64_t kMost = 1ll << 30;
+    if (m < 0 || n < 0 || k < 0 || m > kMost || n > kMost || k > kMost)
+        return fail(GS_ERR_ARG, "%s: m %lld, n %lld, k %lld outside 0..2^30", me, (long long)m, (long long)n, (long long)k);
+    if ((s = check_fp8(me, "a", a, m, k, false)) || (s = check_fp8(me, "b", b, n, k, true))) return s;
+    if (m == 0 || n == 0) return GS_OK;
+    if ((s = check_rows(me, "out", out, out_stride, m, n, dtype))) return s;
+    const Span to = span_of("out", out, m, n, out_stride, elem_bytes(dtype)),
+               in[] = {span_of("a", k ? a->data : nullptr, m, k, a->stride, 1), span_of("b", k ? b->data : nullptr, n, k, b->stride, 1)};
+    if ((s = check_apart(me, to, in, 2, 0))) return s;
+    unsigned* err = error_word(&s);
+    if (!err) return s;
+    auto matrix = [](const gs_fp8& t) { return Fp8Matrix{t.data, t.stride, t.scale, t.scale_row, t.scale_block, t.block_rows}; };
+    cudaError_t e = launch_matmul_fp8(MatmulFp8{matrix(*a), matrix(*b), m, n, k, out, out_stride, dtype}, err, as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
+}
+
+size_t gs_clip_workspace_bytes(const gs_gradient* grads, int32_t count) {
+    if (count < 0 || (count > 0 && !grads)) return 0;
+    return clip_workspace_bytes(grads, count);
+}
+
+int gs_clip_grads(const gs_gradient* grads, int32_t count, int32_t clip, double max_norm, double eps, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    const char* me = "gs_clip_grads";
+    int s;
+    try {
+        if ((s = check_gradients(me, grads, count, clip != 0))) return s;
+    } catch (const std::exception&) {
+        return fail(GS_ERR_ARG, "%s: no memory to check %d gradients", me, count);
+    }
+    if (clip && (!(max_norm >= 0.0) || !(eps >= 0.0))) return fail(GS_ERR_ARG, "%s: max_norm %g, eps %g", me, max_norm, eps);
+    if (!norm || !aligned(norm, 4)) return fail(GS_ERR_ARG, "%s: norm is NULL or misaligned", me);
+    const size_t need = clip_workspace_bytes(grads, count);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+        return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
+    unsigned* err = error_word(&s);
+    if (!err) return s;
+    cudaError_t e = launch_clip(grads, count, clip != 0, max_norm, eps, workspace, norm, as_stream(stream));
+    return e ? cuda_fail(e, me) : GS_OK;
 }
 
 }  // extern "C"

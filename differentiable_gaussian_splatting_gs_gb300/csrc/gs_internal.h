@@ -186,4 +186,40 @@ cudaError_t launch_attn_bwd_simt(const AttnArgs& a, cudaStream_t st);
 // Zeros in all rows of t; lse (or NULL): -inf. Where there is no query, or no key.
 cudaError_t launch_attn_zero(const AttnArgs& a, const AttnTensor& t, int heads, int len, float* lse, cudaStream_t st);
 
+// ---- the 8-bit decoder's operators ---------------------------------------------------------------
+// Rows of a root-mean-square norm (strides in elements): y, or q with its scales; r and h NULL without a residual.
+struct RmsTensors {
+    const void *x, *r, *weight;
+    void *h, *y, *q;
+    float *scale, *rstd;
+    long long x_stride, r_stride, h_stride, y_stride, q_stride, scale_row, scale_block;
+};
+cudaError_t launch_rms_fwd(int dtype, const RmsTensors& t, long long rows, int cols, int wdtype, float eps, unsigned* err, cudaStream_t st);
+size_t rms_bwd_workspace_bytes(long long rows, int cols);
+// Of t: h, weight and rstd.
+cudaError_t launch_rms_bwd(int dtype, const RmsTensors& t, const void* dy, long long dy_stride, const void* dh, long long dh_stride,
+                           long long rows, int cols, int wdtype, void* dx, long long dx_stride, void* dweight, float* workspace,
+                           unsigned* err, cudaStream_t st);
+// by_cols: the columns are contiguous, and x_stride is from one to the next.
+cudaError_t launch_quantize(int dtype, const void* x, long long x_stride, bool by_cols, long long rows, int cols, bool block, void* q,
+                            long long q_stride, float* scale, long long scale_row, long long scale_block, cudaStream_t st);
+// Rows of 8-bit values; `block` of them share a scale.
+struct Fp8Matrix {
+    const void* data;
+    long long stride;
+    const float* scale;
+    long long scale_row, scale_block;
+    int block;
+};
+struct MatmulFp8 {
+    Fp8Matrix a, b;
+    long long m, n, k;
+    void* out;
+    long long out_stride;
+    int dtype;
+};
+cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st);
+size_t clip_workspace_bytes(const gs_gradient* g, int n);
+cudaError_t launch_clip(const gs_gradient* g, int n, bool clip, double max_norm, double eps, void* workspace, float* norm, cudaStream_t st);
+
 }  // namespace gs

@@ -553,6 +553,78 @@ int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs
                            const gs_heads* dk, const gs_heads* dv, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* ---- the same decoder in 8 bits, and its training --------------------------------------------
+ * 8-bit values are e4m3 (sign, 4 bits of exponent, 3 of significand, largest 448, no infinities) with
+ * a float32 scale for each block of 128 columns of a row, or of 128 x 128: x = q scale with
+ * scale = max |x| of the block / 448 (1 where that is below 2^-126) and q = x / scale rounded to the
+ * nearest. A block with a NaN or an infinity has no finite values. Conventions as above: the calls
+ * enqueue on `stream`, allocate nothing, may be captured and give the same bits every time; sums are
+ * float32 or float64. Row strides are in elements.                                              */
+
+/* Rows of 8-bit values, 16-byte aligned with a row stride that is a multiple of 16. The scale of row r
+ * and columns 128 j .. is scale[r / block_rows * scale_row + j * scale_block] (any strides). */
+typedef struct gs_fp8 {
+    void*   data;
+    int64_t stride;
+    float*  scale;
+    int64_t scale_row, scale_block;
+    int32_t block_rows;       /* 1 or 128 */
+} gs_fp8;
+
+/* Root-mean-square norm of x + residual: h = x + residual rounded to `dtype` (h = x without a
+ * residual), rstd = 1 / sqrt(mean of h^2 + eps) (float32 [rows]), y = h rstd w.
+ *   residual: NULL, or rows as x's; h is written only with one.
+ *   weight: [cols] of weight_dtype (`dtype` or GS_DTYPE_F32) or NULL (1).
+ *   Squares are float32: a row whose mean square passes its range has rstd = 0 and y = 0.
+ *   y: rows of `dtype`; or NULL, and q receives y in 8 bits (block_rows 1), quantized from float32.
+ * h and y may be x or the residual (with its row stride), each over its own rows; h, y and q must not
+ * overlap one another or otherwise an input. rows >= 0, 1 <= cols < 2^30, eps >= 0.
+ * Errors: GS_ERR_ARG, GS_ERR_CUDA.                                                               */
+int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int64_t rows,
+                    int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, float eps, void* h,
+                    int64_t h_stride, void* y, int64_t y_stride, const gs_fp8* q, float* rstd, void* stream);
+
+/* Backward of gs_rms_norm_fwd: with hhat = h rstd and g = w dy, dx = rstd (g - hhat mean(g hhat)) + dh,
+ * the gradient of x and of the residual alike, and dweight = sum over rows of dy hhat ([cols] of
+ * weight_dtype, overwritten, or NULL).
+ *   dh: rows, the gradient of h from its other readers, or NULL (0).
+ * dx may be dy, h or dh (with its row stride). workspace: gs_rms_norm_workspace_bytes(rows, cols) bytes,
+ * 16-byte aligned (unused without dweight). Errors: GS_ERR_ARG, GS_ERR_CUDA.                      */
+size_t gs_rms_norm_workspace_bytes(int64_t rows, int64_t cols);
+int gs_rms_norm_bwd(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, const void* dh,
+                    int64_t dh_stride, int64_t rows, int64_t cols, int32_t dtype, const float* rstd, const void* weight,
+                    int32_t weight_dtype, void* dx, int64_t dx_stride, void* dweight, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* x in 8 bits. Element (r, c) of x is at r x_row_stride + c x_col_stride; one of the two strides is 1.
+ * q->block_rows chooses the blocks. q must not overlap x. Errors: GS_ERR_ARG, GS_ERR_CUDA.        */
+int gs_quantize_fp8(const void* x, int64_t x_row_stride, int64_t x_col_stride, int64_t rows, int64_t cols, int32_t dtype,
+                    const gs_fp8* q, void* stream);
+
+/* out[m][n] (GS_DTYPE_*, row stride out_stride) = a b^T of the values that a [m][k] and b [n][k] stand
+ * for; a's block_rows is 1, b's 1 or 128. Products are summed in float32, by blocks of 128 of k. k = 0
+ * gives zeros. out must not overlap an input. Errors: GS_ERR_ARG, GS_ERR_CUDA; a wait that gave up is reported by gs_device_error. */
+int gs_matmul_fp8(const gs_fp8* a, const gs_fp8* b, int64_t m, int64_t n, int64_t k, int32_t dtype, void* out,
+                  int64_t out_stride, void* stream);
+
+/* A gradient of n contiguous elements and where it goes clipped: `out`, of the same type, or NULL: over itself. */
+typedef struct gs_gradient {
+    void*   grad;
+    void*   out;
+    int64_t n;
+    int32_t dtype;
+} gs_gradient;
+
+/* norm (one float32) = 2-norm of all elements of `count` gradients; with `clip`, each gradient times
+ * min(1, max_norm / (norm + eps)) (all NaN where the norm is). Squares that float32 does not hold are
+ * summed in float64. Gradients that stay as they are (the factor is 1, in place) are not written.
+ * What is written must not overlap a gradient but its own, nor another `out`.
+ * max_norm and eps must not be negative or NaN. workspace: gs_clip_workspace_bytes(grads, count) bytes,
+ * 16-byte aligned. Errors: GS_ERR_ARG, GS_ERR_CUDA.                                              */
+size_t gs_clip_workspace_bytes(const gs_gradient* grads, int32_t count);
+int gs_clip_grads(const gs_gradient* grads, int32_t count, int32_t clip, double max_norm, double eps, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of kernels this library has launched in this process (all devices, all threads). */
 int64_t gs_kernel_launches(void);
 
