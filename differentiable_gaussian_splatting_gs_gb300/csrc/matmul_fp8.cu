@@ -36,7 +36,7 @@ struct MmArgs {
     int p_shift, q_shift;                      // 2^shift rows share a scale
     void* out;
     long long out_p, out_q;  // strides of the result, one of them 1
-    int dtype, np, nq, blocks, tiles_p, tiles, splits;
+    int dtype, wide, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie in whole 32 bytes
     unsigned limit, *err;
 };
 
@@ -89,24 +89,77 @@ __device__ __forceinline__ float peer_float(const float* p, unsigned rank) {
 // What the sizes of a tile decide.
 template <int TN>
 struct MmShape {
-    static constexpr int kWarps = TN >= 128 ? 8 : 4;     // elementwise
-    static constexpr int kCols = TN / (kWarps / 4);      // columns of each
-    static constexpr int kThreads = 32 * (kWarps + 2);   // and one that copies, one that issues
-    static constexpr int kBytes = (kMmRows + TN) * kMmBlock;
-    // one block on an SM for the largest tiles, else two
-    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 3 : TN == 64 ? 4 : 6;
-    static constexpr int kTmem = 2 * TN;  // two accumulators
+    static constexpr int kCols = TN == 256 ? 128 : TN < 64 ? TN : 64;  // columns of an elementwise warp
+    static constexpr int kWarps = 4 * (TN / kCols);             // elementwise
+    static constexpr int kThreads = 32 * (kWarps + 4);          // and a warpgroup for the copies and the products
+    // Registers, where a warp's sums are 128 columns: of what the launch gives each thread (168), the third warpgroup
+    // leaves all but 24, and the elementwise two take 240: 128 x 24 + 256 x 240 = 384 x 168.
+    static constexpr bool kShift = kCols == 128;
+    static constexpr int kLaunch = 168, kFew = 24, kMany = 240;
+    static_assert(!kShift || 128 * kFew + (kThreads - 128) * kMany <= kThreads * kLaunch);
+    static constexpr int kBytes = (kMmRows + TN) * kMmBlock;    // a stage: both operands' tiles
+    static constexpr int kResident = TN >= 128 ? 1 : 2;         // blocks of threads on an SM
+    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 6 : TN == 64 ? 4 : 5;
+    static constexpr int kBufs = TN == 128 ? 4 : 2;             // accumulators
+    static constexpr int kTmem = kBufs * TN;
     static constexpr int kSmem = 1024 + kStages * kBytes;
-    static_assert(kTmem >= 32 && kTmem <= 512 && (kTmem & (kTmem - 1)) == 0);
-    static_assert(kStages * kBytes >= kMmRows * TN * 4 || TN == 256, "a cluster's sums take the tiles' place");
+    static_assert(kTmem >= 32 && kResident * kTmem <= 512 && (kTmem & (kTmem - 1)) == 0);
+    static_assert(kStages * kBytes >= kMmRows * TN * 4, "a cluster's sums take the tiles' place");
 };
 
+// 32 bytes of a row of the result at once: whole sectors of the L2, which 16 bytes of a thread's own row each are not.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// The thread's row of a tile, COLS columns that end at `left`: 32 bytes at a time where the result allows (`wide`).
+template <int COLS>
+__device__ __forceinline__ void store_row(const MmArgs& a, const f32x2 (&acc)[COLS / 2], long long at, int left) {
+    const int size = a.dtype == GS_DTYPE_F32 ? 4 : 2;
+    if (a.wide && left >= COLS) {
+        char* to = static_cast<char*>(a.out) + at * size;
+        if (a.dtype == GS_DTYPE_F32) {
+#pragma unroll
+            for (int c = 0; c < COLS; c += 8) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = f2_unpack(acc[c / 2 + i]);
+                    v[2 * i] = __float_as_uint(f.x);
+                    v[2 * i + 1] = __float_as_uint(f.y);
+                }
+                store32(to + c * 4, v);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < COLS; c += 16) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = f2_unpack(acc[c / 2 + i]);
+                    v[i] = a.dtype == GS_DTYPE_F16 ? pack2<__half>(f.x, f.y) : pack2<__nv_bfloat16>(f.x, f.y);
+                }
+                store32(to + c * 2, v);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) {
+        const float2 v = f2_unpack(acc[i]);
+        if (2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
+        if (2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
+    }
+}
+
 template <int TN, bool COLS>
-__global__ void __launch_bounds__(MmShape<TN>::kThreads, TN == 256 ? 1 : 2) k_matmul_fp8(const __grid_constant__ MmArgs a) {
+__global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident) k_matmul_fp8(const __grid_constant__ MmArgs a) {
     using S = MmShape<TN>;
-    constexpr int kStages = S::kStages, kCols = S::kCols, kPart = kCols < 32 ? 16 : 32;
+    constexpr int kStages = S::kStages, kBufs = S::kBufs, kCols = S::kCols, kPart = kCols < 32 || kCols == 128 ? 16 : 32;
     extern __shared__ unsigned char dynamic[];
-    __shared__ uint64_t full[kStages], empty[kStages], done[2], drained[2], last;
+    __shared__ uint64_t full[kStages], empty[kStages], done[kBufs], drained[kBufs], last;
     __shared__ uint32_t tmem_at;
     __shared__ __align__(16) float col_scales[COLS ? S::kWarps : 1][2][COLS ? kCols : 4];
     const uint32_t tiles = (smem_u32(dynamic) + 1023) & ~1023u;
@@ -116,7 +169,7 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, TN == 256 ? 1 : 2) k_ma
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(done + i, 1);
             mbar_init(drained + i, S::kWarps);
         }
@@ -135,57 +188,61 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, TN == 256 ? 1 : 2) k_ma
     // this block's tiles and its share of their inner dimension
     const int rank = blockIdx.x % a.splits, step = gridDim.x / a.splits;
     const int k0 = (int)((long long)a.blocks * rank / a.splits), k1 = (int)((long long)a.blocks * (rank + 1) / a.splits);
-    if (warp == S::kWarps) {
-        // ---- copies ----
-        int turn = 0;
-        if (elect_one()) {
-            bool ok = true;
-            for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step) {
-                const int p0 = t % a.tiles_p * kMmRows, q0 = t / a.tiles_p * TN;
-                for (int k = k0; k < k1 && ok; ++k, ++turn) {
-                    const int s = turn % kStages;
-                    if (turn >= kStages && !mbar_wait_bounded(empty + s, (turn / kStages - 1) & 1, a.limit, a.err)) {
-                        ok = false;
-                        break;
+    if (warp >= S::kWarps) {
+        if constexpr (S::kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
+        if (warp == S::kWarps) {
+            // ---- copies ----
+            int turn = 0;
+            if (elect_one()) {
+                bool ok = true;
+                for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step) {
+                    const int p0 = t % a.tiles_p * kMmRows, q0 = t / a.tiles_p * TN;
+                    for (int k = k0; k < k1 && ok; ++k, ++turn) {
+                        const int s = turn % kStages;
+                        if (turn >= kStages && !mbar_wait_bounded(empty + s, (turn / kStages - 1) & 1, a.limit, a.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t at = tiles + s * S::kBytes;
+                        mbar_arrive_expect_tx(full + s, S::kBytes);
+                        tile_load2(at, &a.p, k * kMmBlock, p0, full + s);
+                        tile_load2(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, full + s);
                     }
-                    const uint32_t at = tiles + s * S::kBytes;
-                    mbar_arrive_expect_tx(full + s, S::kBytes);
-                    tile_load2(at, &a.p, k * kMmBlock, p0, full + s);
-                    tile_load2(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, full + s);
                 }
+                // every copy has landed before the block ends
+                for (int i = turn > kStages ? turn - kStages : 0; i < turn; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
             }
-            // every copy has landed before the block ends
-            for (int i = turn > kStages ? turn - kStages : 0; i < turn; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
-        }
-        __syncwarp();
-    } else if (warp == S::kWarps + 1) {
-        // ---- products ----
-        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);  // e4m3 x e4m3, float32
-        int turn = 0;
-        bool ok = true;
-        for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step)
-            for (int k = k0; k < k1 && ok; ++k, ++turn) {
-                const int s = turn % kStages, b = turn & 1;
-                if (turn >= 2) ok = warp_wait(drained + b, (turn / 2 - 1) & 1, a.limit, a.err);
-                ok = ok && warp_wait(full + s, (turn / kStages) & 1, a.limit, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t at = tiles + s * S::kBytes, p = tile_desc(at), q = tile_desc(at + kMmRows * kMmBlock);
+            __syncwarp();
+        } else if (warp == S::kWarps + 1) {
+            // ---- products ----
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);  // e4m3 x e4m3, float32
+            int turn = 0;
+            bool ok = true;
+            for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step)
+                for (int k = k0; k < k1 && ok; ++k, ++turn) {
+                    const int s = turn % kStages, b = turn % kBufs;
+                    if (turn >= kBufs) ok = warp_wait(drained + b, (turn / kBufs - 1) & 1, a.limit, a.err);
+                    ok = ok && warp_wait(full + s, (turn / kStages) & 1, a.limit, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = tiles + s * S::kBytes, p = tile_desc(at), q = tile_desc(at + kMmRows * kMmBlock);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma8_ss(tmem + b * TN, p + 2 * j, q + 2 * j, idesc, j > 0);
-                    mma_commit(empty + s);
-                    mma_commit(done + b);
+                        for (int j = 0; j < 4; ++j) mma8_ss(tmem + b * TN, p + 2 * j, q + 2 * j, idesc, j > 0);
+                        mma_commit(empty + s);
+                        mma_commit(done + b);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            // every product is complete before the tensor memory is freed
+            if (elect_one()) {
+                mma_commit(&last);
+                mbar_drain(&last, 0, a.err);
             }
-        // every product is complete before the tensor memory is freed
-        if (elect_one()) {
-            mma_commit(&last);
-            mbar_drain(&last, 0, a.err);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        if constexpr (S::kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
         // ---- scales and sums ----
         const int row = warp % 4 * 32 + lane, c0 = warp / 4 * kCols;
         const uint32_t from = tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0;
@@ -200,61 +257,71 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, TN == 256 ? 1 : 2) k_ma
 #pragma unroll
             for (int j = 0; j < kMine; ++j)
                 qs[j] = a.q_scale + (long long)(min(q0 + (COLS ? 32 * j + lane : 0), a.nq - 1) >> a.q_shift) * a.q_row;
-            float next_p = 0.f, next_q[kMine];
-            auto ask = [&](int k) {  // a block's scales, a turn ahead of their use
+            // a block's scales are asked for two turns ahead of their use
+            float ahead_p[2], ahead_q[2][kMine];
+            auto ask = [&](int k, float& p, float (&q)[kMine]) {
                 if (k >= k1) return;
-                next_p = ps[k * a.p_block];
+                p = ps[k * a.p_block];
 #pragma unroll
-                for (int j = 0; j < kMine; ++j) next_q[j] = qs[j][k * a.q_block];
+                for (int j = 0; j < kMine; ++j) q[j] = qs[j][k * a.q_block];
             };
-            ask(k0);
             f32x2 acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-            for (int k = k0; k < k1; ++k, ++turn) {
-                const int b = turn & 1;
+            auto add = [&](int k, float& next_p, float (&next_q)[kMine]) {
+                const int b = turn % kBufs;
                 float scale = next_p;
                 if (!COLS) scale *= next_q[0];
-                float* cs = col_scales[COLS ? warp : 0][b & (COLS ? 1 : 0)];
+                float* cs = col_scales[COLS ? warp : 0][COLS ? turn & 1 : 0];
                 if (COLS) {
 #pragma unroll
                     for (int j = 0; j < kMine; ++j)
                         if (32 * j + lane < kCols) cs[32 * j + lane] = next_q[j];
                     __syncwarp();
                 }
-                ask(k + 1);
+                ask(k + 2, next_p, next_q);
                 const f32x2 scale2 = f2_pack(scale, scale);
-                if (ok) ok = warp_wait(done + b, (turn / 2) & 1, a.limit, a.err);
-                if (!ok) continue;
+                if (ok) ok = warp_wait(done + b, (turn / kBufs) & 1, a.limit, a.err);
+                ++turn;
+                if (!ok) return;
                 tc_fence_after();
+                // parts of the row: one is on its way while the one before is added
+                uint32_t v[2][kPart];
+                auto load = [&](int i) {
+                    if constexpr (kPart == 32) tmem_ld32(from + b * TN + i * kPart, v[i & 1]);
+                    else tmem_ld16(from + b * TN + i * kPart, v[i & 1]);
+                };
+                load(0);
 #pragma unroll
-                for (int c = 0; c < kCols; c += kPart) {
-                    uint32_t v[kPart];
-                    if constexpr (kPart == 32) {
-                        tmem_ld32(from + b * TN + c, v);
-                        tmem_wait_ld(v);
+                for (int i = 0; i < kCols / kPart; ++i) {
+                    if constexpr (kPart == 32) tmem_wait_ld(v[i & 1]);
+                    else tmem_wait_ld16(v[i & 1]);
+                    if ((i + 1) * kPart < kCols) {
+                        load(i + 1);
                     } else {
-                        tmem_ld16(from + b * TN + c, v);
-                        tmem_wait_ld16(v);
-                    }
-                    if (c + kPart == kCols) {
                         tc_fence_before();
                         warp_arrive(drained + b);
                     }
 #pragma unroll
-                    for (int i = 0; i < kPart; i += 4) {
-                        f32x2 part[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) part[j] = f2_pack(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+                    for (int j = 0; j < kPart; j += 4) {
+                        const uint32_t* u = v[i & 1] + j;
+                        f32x2 lo = f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), hi = f2_pack(__uint_as_float(u[2]), __uint_as_float(u[3]));
                         if (COLS) {
-                            const float4 w = *reinterpret_cast<const float4*>(cs + c + i);
-                            part[0] = f2_mul(part[0], f2_pack(w.x, w.y));
-                            part[1] = f2_mul(part[1], f2_pack(w.z, w.w));
+                            const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + j);
+                            lo = f2_mul(lo, f2_pack(w.x, w.y));
+                            hi = f2_mul(hi, f2_pack(w.z, w.w));
                         }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[(c + i) / 2 + j] = f2_fma(part[j], scale2, acc[(c + i) / 2 + j]);
+                        f32x2* to = acc + (i * kPart + j) / 2;
+                        to[0] = f2_fma(lo, scale2, to[0]);
+                        to[1] = f2_fma(hi, scale2, to[1]);
                     }
                 }
+            };
+            ask(k0, ahead_p[0], ahead_q[0]);
+            ask(k0 + 1, ahead_p[1], ahead_q[1]);
+            for (int k = k0; k < k1; k += 2) {
+                add(k, ahead_p[0], ahead_q[0]);
+                if (k + 1 < k1) add(k + 1, ahead_p[1], ahead_q[1]);
             }
             if (a.splits > 1) {
                 // the cluster's shares, column by column, in the tiles' place
@@ -267,15 +334,7 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, TN == 256 ? 1 : 2) k_ma
                 }
                 break;  // one tile for a cluster
             }
-            if (p0 + row < a.np) {
-                const long long at = (p0 + row) * a.out_p + (long long)q0 * a.out_q;
-#pragma unroll
-                for (int i = 0; i < kCols / 2; ++i) {
-                    const float2 v = f2_unpack(acc[i]);
-                    if (q0 + 2 * i < a.nq) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
-                    if (q0 + 2 * i + 1 < a.nq) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
-                }
-            }
+            if (p0 + row < a.np) store_row<kCols>(a, acc, (p0 + row) * a.out_p + (long long)q0 * a.out_q, a.nq - q0);
         }
     }
     tc_fence_before();
@@ -336,6 +395,16 @@ cudaError_t launch(const MmArgs& a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e) return e;
     const int most = resident_blocks(kernel, S::kThreads, S::kSmem, cache);
+    if constexpr (S::kShift) {  // registers that the launch does not give would be waited for without end
+        static std::atomic<int> given{0};
+        int regs = given.load(std::memory_order_relaxed);
+        if (regs == 0) {
+            cudaFuncAttributes f;
+            if ((e = cudaFuncGetAttributes(&f, kernel))) return e;
+            given.store(regs = f.numRegs, std::memory_order_relaxed);
+        }
+        if (regs < S::kLaunch) return cudaErrorLaunchOutOfResources;
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -358,6 +427,7 @@ cudaError_t launch(int tn, const MmArgs& a, cudaStream_t st) {
         if (tn == 16) return launch<16, true>(a, st);
         if (tn == 32) return launch<32, true>(a, st);
         if (tn == 64) return launch<64, true>(a, st);
+        if (tn == 256) return launch<256, true>(a, st);
         return launch<128, true>(a, st);
     } else {
         if (tn == 64) return launch<64, false>(a, st);
@@ -388,6 +458,8 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     a.out_p = swap ? 1 : x.out_stride;
     a.out_q = swap ? x.out_stride : 1;
     a.dtype = x.dtype;
+    const int size = x.dtype == GS_DTYPE_F32 ? 4 : 2;
+    a.wide = !swap && x.out_stride * size % 32 == 0 && reinterpret_cast<uintptr_t>(x.out) % 32 == 0;
     a.limit = 1u << 18;
     a.err = err;
     const int sms = device_sm_count();
@@ -395,14 +467,14 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     const long long tiles_p = over(a.np, kMmRows);
     int tn;
     if (swap) tn = a.nq <= 16 ? 16 : a.nq <= 32 ? 32 : 64;
-    else tn = cols ? 128 : tiles_p * over(a.nq, 256) >= sms ? 256 : tiles_p * over(a.nq, 128) >= sms ? 128 : 64;
+    else tn = tiles_p * over(a.nq, 256) >= sms / 2 ? 256 : cols || tiles_p * over(a.nq, 128) >= sms / 2 ? 128 : 64;
     a.tiles_p = (int)tiles_p;
     const long long tiles = tiles_p * over(a.nq, tn);
     if (tiles > 0x0fffffffll) return cudaErrorInvalidConfiguration;
     a.tiles = (int)tiles;
     a.splits = 1;
-    if (tn < 256)
-        while (a.splits < 8 && 2 * a.splits * tiles <= 2 * sms && 2 * a.splits <= a.blocks) a.splits *= 2;
+    const int slots = tn >= 128 ? sms : 2 * sms;
+    while (a.splits < 8 && 2 * a.splits * tiles <= slots && 2 * a.splits <= a.blocks) a.splits *= 2;
     if (x.k > 0) {
         cudaError_t e;
         if ((e = encode(a.p, p.data, x.k, a.np, p.stride, kMmRows)) || (e = encode(a.q, q.data, x.k, a.nq, q.stride, tn))) return e;
