@@ -10,9 +10,12 @@
 // multiplies all its columns by the lane's scale; scales that differ by column (COLS) take one more multiplication, read
 // from shared memory, where columns of the same block of 128 share one (b's 128 x 128 blocks).
 //
-// A warp copies tiles (128 bytes of inner dimension, 128-byte swizzle), one issues the products, the others multiply and
-// add; accumulators alternate between two places, so that a block's products run beside the additions of the one before.
+// A warp copies tiles (128 bytes of inner dimension, 128-byte swizzle), two copy scales, one issues the products, the
+// others multiply and add; accumulators alternate between places, so that a block's products run beside the additions of the one before.
 // Blocks of threads take tiles in turn, and go on copying and multiplying while the result of the last one is stored.
+// Large products take tiles of 256 x 256 by pairs of blocks on two SMs, whose products each read both blocks' shared memory
+// (every block copies its 128 rows of P and half of Q): one block's 128 x 256 would move 96 KB through its shared memory for
+// 512 cycles of products (750 cycles' worth), a pair's moves 64 KB.
 // Where tiles are few, a cluster of up to 8 blocks shares the inner dimension of one, joined through their shared
 // memory in a fixed order.
 #include <cudaTypedefs.h>
@@ -28,6 +31,7 @@ namespace gs {
 
 constexpr int kMmRows = 128;   // lanes: rows of P in a tile
 constexpr int kMmBlock = 128;  // inner dimension of a block, bytes
+constexpr int kMmSplits = 8;   // blocks of a cluster that share a tile's inner dimension, at most
 
 struct MmArgs {
     CUtensorMap p, q;
@@ -36,22 +40,70 @@ struct MmArgs {
     int p_shift, q_shift;                      // 2^shift rows share a scale
     void* out;
     long long out_p, out_q;  // strides of the result, one of them 1
-    int dtype, wide, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie in whole 32 bytes
+    int dtype, wide, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes
     unsigned limit, *err;
 };
 
+// One product over 32 of the inner dimension; PAIR: of both blocks' rows, issued by the first.
+template <bool PAIR>
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTileDescHi)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTileDescHi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTileDescHi)
+            : "memory");
+}
+// mma_commit; PAIR: on the barrier at this place in each of the blocks of `mask`.
+template <bool PAIR>
+__device__ __forceinline__ void mma8_commit(uint64_t* bar, uint16_t mask) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "h"(mask)
+                     : "memory");
+    else
+        mma_commit(bar);
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS));
 }
 
-__device__ __forceinline__ void tile_load2(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-                 : "memory");
+// The address of block `rank`'s shared memory at this block's p.
+__device__ __forceinline__ uint32_t peer_address(const void* p, unsigned rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// One arrival for the whole warp on a barrier of the cluster. Relaxed: it tells of tensor memory that was read, which
+// tc_fence_before orders; to release what the thread wrote besides took 1,600 cycles.
+__device__ __forceinline__ void warp_arrive_at(uint32_t bar) {
+    __syncwarp();
+    if (elect_one()) asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A box of a matrix -> this block's shared memory, counted on `bar`: this block's, or (PAIR) one of the pair's.
+template <bool PAIR>
+__device__ __forceinline__ void tile_load2(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                     "l"(map), "r"(bar), "r"(c0), "r"(c1)
+                     : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
@@ -71,97 +123,120 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// A float of block `rank`'s shared memory at this block's address p.
-__device__ __forceinline__ float peer_float(const float* p, unsigned rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(smem_u32(p)), "r"(rank)
-                 : "memory");
+// Four floats of block `rank`'s shared memory at this block's address p.
+__device__ __forceinline__ float4 peer_floats(const float* p, unsigned rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_address(p, rank)) : "memory");
     return v;
 }
 
 // What the sizes of a tile decide.
 template <int TN>
 struct MmShape {
-    static constexpr int kCols = TN == 256 ? 128 : TN < 64 ? TN : 64;  // columns of an elementwise warp
-    static constexpr int kWarps = 4 * (TN / kCols);             // elementwise
-    static constexpr int kThreads = 32 * (kWarps + 4);          // and a warpgroup for the copies and the products
-    // Registers, where a warp's sums are 128 columns: of what the launch gives each thread (168), the third warpgroup
-    // leaves all but 24, and the elementwise two take 240: 128 x 24 + 256 x 240 = 384 x 168.
-    static constexpr bool kShift = kCols == 128;
-    static constexpr int kLaunch = 168, kFew = 24, kMany = 240;
-    static_assert(!kShift || 128 * kFew + (kThreads - 128) * kMany <= kThreads * kLaunch);
-    static constexpr int kBytes = (kMmRows + TN) * kMmBlock;    // a stage: both operands' tiles
-    static constexpr int kResident = TN >= 128 ? 1 : 2;         // blocks of threads on an SM
-    static constexpr int kStages = TN == 256 ? 4 : TN == 128 ? 6 : TN == 64 ? 4 : 5;
-    static constexpr int kBufs = TN == 128 ? 4 : 2;             // accumulators
+    static constexpr bool kPair = TN == 256;                     // two blocks on two SMs, each with half of Q's tile
+    static constexpr int kCols = kPair ? 128 : TN < 64 ? TN : 64;  // columns of an elementwise warp
+    static constexpr int kWarps = 4 * (TN / kCols);              // elementwise
+    static constexpr int kThreads = 32 * (kWarps + 4);           // and a warpgroup for the copies and the products
+    // Registers of the pair's 384 threads: of the 168 that the launch gives each, the last warpgroup leaves all but 40,
+    // and the elementwise two take 232: 128 x 40 + 256 x 232 = 384 x 168.
+    static constexpr int kLaunch = 168, kFew = 40, kMany = 232;
+    static_assert(!kPair || 128 * kFew + (kThreads - 128) * kMany <= kThreads * kLaunch);
+    static constexpr int kTileQ = kPair ? TN / 2 : TN;           // rows of Q that a block copies
+    static constexpr int kBytes = (kMmRows + kTileQ) * kMmBlock; // a stage: both operands' tiles
+    template <bool COLS>
+    static constexpr bool kStaged = !COLS || TN >= 128;          // results' rows go through shared memory (never with b's along the lanes)
+    static constexpr int kResident = TN >= 128 ? 1 : 2;          // blocks of threads on an SM
+    template <bool COLS>
+    static constexpr int kStages = kPair && COLS ? 5 : TN >= 128 ? 6 : TN == 64 ? 4 : 5;
+    static constexpr int kBufs = TN == 128 ? 4 : 2;              // accumulators
     static constexpr int kTmem = kBufs * TN;
-    static constexpr int kSmem = 1024 + kStages * kBytes;
+    template <bool COLS>
+    static constexpr int kSmem = 1024 + kStages<COLS> * kBytes;
     static_assert(kTmem >= 32 && kResident * kTmem <= 512 && (kTmem & (kTmem - 1)) == 0);
-    static_assert(kStages * kBytes >= kMmRows * TN * 4, "a cluster's sums take the tiles' place");
+    static_assert(kPair || kStages<false> * kBytes >= kMmRows * (TN + 4) * 4, "a cluster's sums take the tiles' place");
 };
 
-// 32 bytes of a row of the result at once: whole sectors of the L2, which 16 bytes of a thread's own row each are not.
-__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// Scales of so many blocks of the inner dimension are copied at a time, to so many places: 8 to 12 blocks ahead of their use.
+// (Loaded into registers two blocks ahead, their latency under the tiles' traffic decided the pace of 256 x 256 tiles: 16384 x 4096
+// x 4096 bf16 took 707 us.)
+constexpr int kMmBatch = 4, kMmPlaces = 3;
+template <int TN, bool COLS>
+struct MmScales {
+    float p[kMmPlaces][kMmRows][kMmBatch];
+    float q[kMmPlaces][COLS ? kMmBatch * TN : (TN + kQBlock - 1) / kQBlock * kMmBatch];  // COLS: [batch][column], else [column / 128][batch]
+};
+
+// Counts an arrival of the thread once its asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The thread's row of a tile, COLS columns that end at `left`: 32 bytes at a time where the result allows (`wide`).
+// A warp's 32 rows of a tile, COLS columns of them in every thread's sums, `rows` and `left` of them inside the result, which
+// is at `at` (elements): 64 bytes of each row at a time through the warp's 2 KB of shared memory, so that a store writes
+// 8 rows' pieces and not 32 rows' 16 bytes each (which took 2.2 us for a tile of 256 x 256, between which the products
+// can only go two blocks ahead). Element by element where the result's rows do not lie on 16 bytes, and at its right edge.
 template <int COLS>
-__device__ __forceinline__ void store_row(const MmArgs& a, const f32x2 (&acc)[COLS / 2], long long at, int left) {
-    const int size = a.dtype == GS_DTYPE_F32 ? 4 : 2;
-    if (a.wide && left >= COLS) {
-        char* to = static_cast<char*>(a.out) + at * size;
-        if (a.dtype == GS_DTYPE_F32) {
+__device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[COLS / 2], unsigned char* stage, long long at, int rows, int left) {
+    const int lane = threadIdx.x & 31, wide = a.dtype == GS_DTYPE_F32;
+    auto piece = [&](auto word, auto per) {  // word(i): 16 bytes of the thread's row, `per` columns
+        constexpr int kPer = decltype(per)::value;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 8) {
-                uint32_t v[8];
+        for (int c = 0; c < COLS; c += 4 * kPer) {
+            if (left < c + 4 * kPer) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = word(c + i * kPer);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + lane / 4, q = lane % 4;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
+                if (r < rows) *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (at + r * a.out_p + c + q * kPer) * (16 / kPer)) = v;
+            }
+            __syncwarp();
+        }
+    };
+    int done = 0;
+    if (a.wide && a.out_q == 1) {
+        if (wide) {
+            piece([&](int c) {
+                const float2 x = f2_unpack(acc[c / 2]), y = f2_unpack(acc[c / 2 + 1]);
+                return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+            }, std::integral_constant<int, 4>());
+        } else {
+            piece([&](int c) {
+                uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = f2_unpack(acc[c / 2 + i]);
-                    v[2 * i] = __float_as_uint(f.x);
-                    v[2 * i + 1] = __float_as_uint(f.y);
+                    const float2 x = f2_unpack(acc[c / 2 + i]);
+                    w[i] = a.dtype == GS_DTYPE_F16 ? pack2<__half>(x.x, x.y) : pack2<__nv_bfloat16>(x.x, x.y);
                 }
-                store32(to + c * 4, v);
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < COLS; c += 16) {
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = f2_unpack(acc[c / 2 + i]);
-                    v[i] = a.dtype == GS_DTYPE_F16 ? pack2<__half>(f.x, f.y) : pack2<__nv_bfloat16>(f.x, f.y);
-                }
-                store32(to + c * 2, v);
-            }
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            }, std::integral_constant<int, 8>());
         }
-        return;
+        if (left >= COLS) return;
+        done = left / (wide ? 16 : 32) * (wide ? 16 : 32);
     }
+    if (lane >= rows) return;
+    at += lane * a.out_p;
 #pragma unroll
     for (int i = 0; i < COLS / 2; ++i) {
         const float2 v = f2_unpack(acc[i]);
-        if (2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
-        if (2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
+        if (2 * i >= done && 2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
+        if (2 * i >= done && 2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
     }
 }
 
 template <int TN, bool COLS>
 __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident) k_matmul_fp8(const __grid_constant__ MmArgs a) {
     using S = MmShape<TN>;
-    constexpr int kStages = S::kStages, kBufs = S::kBufs, kCols = S::kCols, kPart = kCols < 32 || kCols == 128 ? 16 : 32;
+    constexpr bool kPair = S::kPair;
+    constexpr int kStages = S::template kStages<COLS>, kBufs = S::kBufs, kCols = S::kCols, kPart = TN == 128 ? 32 : 16;
     extern __shared__ unsigned char dynamic[];
     __shared__ uint64_t full[kStages], empty[kStages], done[kBufs], drained[kBufs], last;
     __shared__ uint32_t tmem_at;
-    __shared__ __align__(16) float col_scales[COLS ? S::kWarps : 1][2][COLS ? kCols : 4];
+    __shared__ uint64_t scaled[kMmPlaces], used[kMmPlaces];
+    __shared__ __align__(16) MmScales<TN, COLS> scales;
+    __shared__ __align__(16) unsigned char staged[S::template kStaged<COLS> ? S::kWarps : 1][S::template kStaged<COLS> ? 2048 : 16];
     const uint32_t tiles = (smem_u32(dynamic) + 1023) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -171,7 +246,11 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(done + i, 1);
-            mbar_init(drained + i, S::kWarps);
+            mbar_init(drained + i, kPair ? 2 * S::kWarps : S::kWarps);
+        }
+        for (int i = 0; i < kMmPlaces; ++i) {
+            mbar_init(scaled + i, 64);
+            mbar_init(used + i, S::kWarps);
         }
         mbar_init(&last, 1);
         fence_mbar_init();
@@ -179,47 +258,52 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
     // Tensor memory is taken once the kernel before has given up its own, and before the next one's blocks may come, which
     // would otherwise hold what a block of this or of that one waits for.
     pdl_wait();
-    if (warp == S::kWarps + 1) tmem_alloc<S::kTmem>(&tmem_at);
+    if (warp == S::kWarps + 1) {
+        if constexpr (kPair) tmem_alloc_pair<S::kTmem>(&tmem_at);
+        else tmem_alloc<S::kTmem>(&tmem_at);
+    }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();  // the barriers of both are ready
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = tmem_at;
-    // this block's tiles and its share of their inner dimension
-    const int rank = blockIdx.x % a.splits, step = gridDim.x / a.splits;
-    const int k0 = (int)((long long)a.blocks * rank / a.splits), k1 = (int)((long long)a.blocks * (rank + 1) / a.splits);
+    // The blocks that share a tile: a pair with 128 of its rows each, or a cluster with shares of the inner dimension.
+    const int group = kPair ? 2 : a.splits, rank = blockIdx.x % group, first = blockIdx.x / group, step = gridDim.x / group;
+    const int k0 = kPair ? 0 : (int)((long long)a.blocks * rank / group), k1 = kPair ? a.blocks : (int)((long long)a.blocks * (rank + 1) / group);
+    constexpr int kRows = kPair ? 2 * kMmRows : kMmRows;  // of P in a tile
+    const int row_of = kPair ? rank * kMmRows : 0;
     if (warp >= S::kWarps) {
-        if constexpr (S::kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
+        if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
         if (warp == S::kWarps) {
             // ---- copies ----
             int turn = 0;
             if (elect_one()) {
                 bool ok = true;
-                for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step) {
-                    const int p0 = t % a.tiles_p * kMmRows, q0 = t / a.tiles_p * TN;
-                    for (int k = k0; k < k1 && ok; ++k, ++turn) {
+                for (int t = first; t < a.tiles && ok; t += step) {
+                    const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN + (kPair ? rank * S::kTileQ : 0);
+                    for (int k = k0; k < k1; ++k, ++turn) {
                         const int s = turn % kStages;
-                        if (turn >= kStages && !mbar_wait_bounded(empty + s, (turn / kStages - 1) & 1, a.limit, a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t at = tiles + s * S::kBytes;
-                        mbar_arrive_expect_tx(full + s, S::kBytes);
-                        tile_load2(at, &a.p, k * kMmBlock, p0, full + s);
-                        tile_load2(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, full + s);
+                        if (turn >= kStages && !(ok = mbar_wait_bounded(empty + s, (turn / kStages - 1) & 1, a.limit, a.err))) break;
+                        const uint32_t at = tiles + s * S::kBytes, bar = kPair ? peer_address(full + s, 0) : smem_u32(full + s);
+                        // (a pair's bytes are all counted by its first block, which issues the products)
+                        if (row_of == 0) mbar_arrive_expect_tx(full + s, kPair ? 2 * S::kBytes : S::kBytes);
+                        tile_load2<kPair>(at, &a.p, k * kMmBlock, p0, bar);
+                        tile_load2<kPair>(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, bar);
                     }
                 }
-                // every copy has landed before the block ends
-                for (int i = turn > kStages ? turn - kStages : 0; i < turn; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
+                // every copy has landed before the blocks end
+                if (row_of == 0)
+                    for (int i = turn > kStages ? turn - kStages : 0; i < turn; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
             }
             __syncwarp();
         } else if (warp == S::kWarps + 1) {
             // ---- products ----
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);  // e4m3 x e4m3, float32
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);  // e4m3 x e4m3, float32
             int turn = 0;
-            bool ok = true;
-            for (int t = blockIdx.x / a.splits; t < a.tiles && ok; t += step)
-                for (int k = k0; k < k1 && ok; ++k, ++turn) {
+            bool ok = row_of == 0;
+            for (int t = first; t < a.tiles && ok; t += step)
+                for (int k = k0; k < k1; ++k, ++turn) {
                     const int s = turn % kStages, b = turn % kBufs;
                     if (turn >= kBufs) ok = warp_wait(drained + b, (turn / kBufs - 1) & 1, a.limit, a.err);
                     ok = ok && warp_wait(full + s, (turn / kStages) & 1, a.limit, a.err);
@@ -228,137 +312,191 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                     if (elect_one()) {
                         const uint32_t at = tiles + s * S::kBytes, p = tile_desc(at), q = tile_desc(at + kMmRows * kMmBlock);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma8_ss(tmem + b * TN, p + 2 * j, q + 2 * j, idesc, j > 0);
-                        mma_commit(empty + s);
-                        mma_commit(done + b);
+                        for (int j = 0; j < 4; ++j) mma8_ss<kPair>(tmem + b * TN, p + 2 * j, q + 2 * j, idesc, j > 0);
+                        mma8_commit<kPair>(done + b, 3);
+                        mma8_commit<kPair>(empty + s, 3);
                     }
                     __syncwarp();
                 }
             // every product is complete before the tensor memory is freed
-            if (elect_one()) {
-                mma_commit(&last);
+            if (row_of == 0 && elect_one()) {
+                mma8_commit<kPair>(&last, 1);
                 mbar_drain(&last, 0, a.err);
             }
             __syncwarp();
+        } else {
+            // ---- scales: one warp P's, one Q's, each lane its rows (or columns) ----
+            const bool of_q = warp == S::kWarps + 3;
+            constexpr int kOfQ = COLS ? (TN + 31) / 32 : 1, kMost = kOfQ > kMmRows / 32 ? kOfQ : kMmRows / 32;
+            const long long next = of_q ? a.q_block : a.p_block;
+            int batch = 0;
+            bool ok = true;
+            for (int t = first; t < a.tiles && ok; t += step) {
+                const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN;
+                const float* from[kMost];
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) {
+                    const int p = min(p0 + 32 * i + lane, a.np - 1), q = min(q0 + (COLS ? 32 * i + lane : lane * kQBlock), a.nq - 1);
+                    from[i] = of_q ? a.q_scale + (long long)(q >> a.q_shift) * a.q_row : a.p_scale + (long long)(p >> a.p_shift) * a.p_row;
+                    from[i] += k0 * next;
+                }
+                for (int k = k0; k < k1; k += kMmBatch, ++batch) {
+                    const int at = batch % kMmPlaces;
+                    if (batch >= kMmPlaces && !(ok = warp_wait(used + at, (batch / kMmPlaces - 1) & 1, a.limit, a.err))) break;
+#pragma unroll
+                    for (int j = 0; j < kMmBatch; ++j) {
+                        if (k + j >= k1) break;
+                        if (of_q) {
+#pragma unroll
+                            for (int i = 0; i < kOfQ; ++i)
+                                if (COLS ? 32 * i + lane < TN : lane * kQBlock < TN) cp_async4(&scales.q[at][COLS ? j * TN + 32 * i + lane : lane * kMmBatch + j], from[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kMmRows / 32; ++i) cp_async4(&scales.p[at][32 * i + lane][j], from[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kMost; ++i) from[i] += next;
+                    }
+                    cp_async_arrive(scaled + at);
+                }
+            }
+            cp_async_wait_all();
+            __syncwarp();
         }
     } else {
-        if constexpr (S::kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
+        if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
         // ---- scales and sums ----
         const int row = warp % 4 * 32 + lane, c0 = warp / 4 * kCols;
         const uint32_t from = tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0;
-        int turn = 0;
+        int b = 0, at = 0;  // the next block's accumulators, its batch's place of scales
+        unsigned b_phase = 0, at_phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x / a.splits; t < a.tiles; t += step) {
-            const int p0 = t % a.tiles_p * kMmRows, q0 = t / a.tiles_p * TN + c0;
-            const float* ps = a.p_scale + (long long)(min(p0 + row, a.np - 1) >> a.p_shift) * a.p_row;
-            // columns that share a scale: one for all of the warp's; else the lane's of them
-            constexpr int kMine = COLS ? (kCols + 31) / 32 : 1;
-            const float* qs[kMine];
-#pragma unroll
-            for (int j = 0; j < kMine; ++j)
-                qs[j] = a.q_scale + (long long)(min(q0 + (COLS ? 32 * j + lane : 0), a.nq - 1) >> a.q_shift) * a.q_row;
-            // a block's scales are asked for two turns ahead of their use
-            float ahead_p[2], ahead_q[2][kMine];
-            auto ask = [&](int k, float& p, float (&q)[kMine]) {
-                if (k >= k1) return;
-                p = ps[k * a.p_block];
-#pragma unroll
-                for (int j = 0; j < kMine; ++j) q[j] = qs[j][k * a.q_block];
-            };
+        const uint32_t drained_at = kPair ? peer_address(drained, 0) : 0;
+        for (int t = first; t < a.tiles; t += step) {
+            const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN + c0;
             f32x2 acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-            auto add = [&](int k, float& next_p, float (&next_q)[kMine]) {
-                const int b = turn % kBufs;
-                float scale = next_p;
-                if (!COLS) scale *= next_q[0];
-                float* cs = col_scales[COLS ? warp : 0][COLS ? turn & 1 : 0];
-                if (COLS) {
-#pragma unroll
-                    for (int j = 0; j < kMine; ++j)
-                        if (32 * j + lane < kCols) cs[32 * j + lane] = next_q[j];
-                    __syncwarp();
-                }
-                ask(k + 2, next_p, next_q);
-                const f32x2 scale2 = f2_pack(scale, scale);
-                if (ok) ok = warp_wait(done + b, (turn / kBufs) & 1, a.limit, a.err);
-                ++turn;
-                if (!ok) return;
+            // The row in parts: one is on its way while the one before is added.
+            constexpr int kParts = kCols / kPart;
+            for (int k = k0, j = 0; k < k1; ++k) {
+                if (j == 0 && ok) ok = warp_wait(scaled + at, at_phase, a.limit, a.err);
+                if (ok) ok = warp_wait(done + b, b_phase, a.limit, a.err);
+                if (!ok) break;
                 tc_fence_after();
-                // parts of the row: one is on its way while the one before is added
                 uint32_t v[2][kPart];
                 auto load = [&](int i) {
                     if constexpr (kPart == 32) tmem_ld32(from + b * TN + i * kPart, v[i & 1]);
                     else tmem_ld16(from + b * TN + i * kPart, v[i & 1]);
                 };
                 load(0);
+                const float scale = scales.p[at][row][j] * (COLS ? 1.f : scales.q[at][c0 / kQBlock * kMmBatch + j]);
+                const f32x2 scale2 = f2_pack(scale, scale);
+                const float* cs = scales.q[at] + (COLS ? j * TN + c0 : 0);
+                const bool ends = j == kMmBatch - 1 || k + 1 == k1;
 #pragma unroll
-                for (int i = 0; i < kCols / kPart; ++i) {
+                for (int i = 0; i < kParts; ++i) {
                     if constexpr (kPart == 32) tmem_wait_ld(v[i & 1]);
                     else tmem_wait_ld16(v[i & 1]);
-                    if ((i + 1) * kPart < kCols) {
+                    if (i + 1 < kParts) {
                         load(i + 1);
                     } else {
                         tc_fence_before();
-                        warp_arrive(drained + b);
+                        if constexpr (kPair) warp_arrive_at(drained_at + 8 * b);
+                        else warp_arrive(drained + b);
+                        if (++b == kBufs) b = 0, b_phase ^= 1;
                     }
 #pragma unroll
-                    for (int j = 0; j < kPart; j += 4) {
-                        const uint32_t* u = v[i & 1] + j;
+                    for (int c = 0; c < kPart; c += 4) {
+                        const uint32_t* u = v[i & 1] + c;
                         f32x2 lo = f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), hi = f2_pack(__uint_as_float(u[2]), __uint_as_float(u[3]));
                         if (COLS) {
-                            const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + j);
+                            const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + c);
                             lo = f2_mul(lo, f2_pack(w.x, w.y));
                             hi = f2_mul(hi, f2_pack(w.z, w.w));
                         }
-                        f32x2* to = acc + (i * kPart + j) / 2;
+                        f32x2* to = acc + (i * kPart + c) / 2;
                         to[0] = f2_fma(lo, scale2, to[0]);
                         to[1] = f2_fma(hi, scale2, to[1]);
                     }
                 }
-            };
-            ask(k0, ahead_p[0], ahead_q[0]);
-            ask(k0 + 1, ahead_p[1], ahead_q[1]);
-            for (int k = k0; k < k1; k += 2) {
-                add(k, ahead_p[0], ahead_q[0]);
-                if (k + 1 < k1) add(k + 1, ahead_p[1], ahead_q[1]);
+                ++j;
+                if (ends) {
+                    warp_arrive(used + at);
+                    if (++at == kMmPlaces) at = 0, at_phase ^= 1;
+                    j = 0;
+                }
             }
-            if (a.splits > 1) {
-                // the cluster's shares, column by column, in the tiles' place
+            if (!kPair && group > 1) {
+                // the cluster's shares, in the tiles' place: rows where the result's rows are the lanes', else columns
                 float* sums = reinterpret_cast<float*>(dynamic + (tiles - smem_u32(dynamic)));
 #pragma unroll
-                for (int i = 0; i < kCols / 2; ++i) {
-                    const float2 v = f2_unpack(acc[i]);
-                    sums[(c0 + 2 * i) * kMmRows + row] = v.x;
-                    sums[(c0 + 2 * i + 1) * kMmRows + row] = v.y;
+                for (int i = 0; i < kCols / 2; i += 2) {
+                    const float2 x = f2_unpack(acc[i]), y = f2_unpack(acc[i + 1]);
+                    if (a.out_q == 1) {
+                        *reinterpret_cast<float4*>(sums + row * (TN + 4) + c0 + 2 * i) = make_float4(x.x, x.y, y.x, y.y);
+                    } else {
+                        float* to = sums + (c0 + 2 * i) * kMmRows + row;
+                        to[0] = x.x, to[kMmRows] = x.y, to[2 * kMmRows] = y.x, to[3 * kMmRows] = y.y;
+                    }
                 }
                 break;  // one tile for a cluster
             }
-            if (p0 + row < a.np) store_row<kCols>(a, acc, (p0 + row) * a.out_p + (long long)q0 * a.out_q, a.nq - q0);
+            const int r0 = p0 + warp % 4 * 32;
+            if (r0 < a.np) store_rows<kCols>(a, acc, staged[S::template kStaged<COLS> ? warp : 0], r0 * a.out_p + (long long)q0 * a.out_q, min(32, a.np - r0), a.nq - q0);
+            __syncwarp();  // the instructions on tensor memory and the cluster's barriers take whole warps
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == S::kWarps + 1) {
-        tc_fence_after();
-        tmem_free<S::kTmem>(tmem);
+    if constexpr (kPair) {
+        cluster_sync();  // the first block's products and copies are over, which use the second's memory too
+        if (warp == S::kWarps + 1) {
+            tc_fence_after();
+            tmem_free_pair<S::kTmem>(tmem);
+        }
+    } else {
+        if (warp == S::kWarps + 1) {
+            tc_fence_after();
+            tmem_free<S::kTmem>(tmem);
+        }
+        if (group == 1) return;
+        // The tensor memory is free before blocks wait for one another: a block that waits for some never holds up one that
+        // waits for it.
+        cluster_sync();
+        const float* sums = reinterpret_cast<const float*>(dynamic + (tiles - smem_u32(dynamic)));
+        const int p0 = first % a.tiles_p * kMmRows, q0 = first / a.tiles_p * TN;
+        const bool by_row = a.out_q == 1;  // four elements that lie together in the result to a thread
+        const int lines = by_row ? kMmRows : TN, fours = (by_row ? TN : kMmRows) / 4, pitch = by_row ? TN + 4 : kMmRows;
+        const int l0 = lines * rank / group, l1 = lines * (rank + 1) / group;
+        for (int i = l0 * fours + threadIdx.x; i < l1 * fours; i += S::kThreads) {
+            const int line = i / fours, at = i % fours * 4;
+            const int p = p0 + (by_row ? line : at), q = q0 + (by_row ? at : line), left = by_row ? a.nq - q : a.np - p;
+            if (p >= a.np || q >= a.nq) continue;
+            float4 v[kMmSplits];
+#pragma unroll
+            for (int r = 0; r < kMmSplits; ++r)
+                if (r < group) v[r] = peer_floats(sums + line * pitch + at, r);
+            float4 t = v[0];
+#pragma unroll
+            for (int r = 1; r < kMmSplits; ++r)
+                if (r < group) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
+            const long long to = p * a.out_p + q * a.out_q;
+            if (a.wide && left >= 4) {
+                if (a.dtype == GS_DTYPE_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = t;
+                else if (a.dtype == GS_DTYPE_F16) *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) = make_uint2(pack2<__half>(t.x, t.y), pack2<__half>(t.z, t.w));
+                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) = make_uint2(pack2<__nv_bfloat16>(t.x, t.y), pack2<__nv_bfloat16>(t.z, t.w));
+            } else {
+                const float each[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) store_elem(a.out, to + e, a.dtype, each[e]);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no block's shared memory goes before the others have read it
     }
-    if (a.splits == 1) return;
-    // The tensor memory is free before blocks wait for one another: a block that waits for some never holds up one that
-    // waits for it.
-    cluster_sync();
-    const float* sums = reinterpret_cast<const float*>(dynamic + (tiles - smem_u32(dynamic)));
-    const int t = blockIdx.x / a.splits, p0 = t % a.tiles_p * kMmRows, q0 = t / a.tiles_p * TN;
-    const unsigned me = cluster_rank();
-    const int cols = TN / a.splits;  // of the tile, that this block adds and stores
-    for (int i = threadIdx.x; i < cols * kMmRows; i += S::kThreads) {
-        const int row = i % kMmRows, c = (int)me * cols + i / kMmRows;
-        if (p0 + row >= a.np || q0 + c >= a.nq) continue;
-        float sum = 0.f;
-        for (int r = 0; r < a.splits; ++r) sum += peer_float(sums + c * kMmRows + row, r);
-        store_elem(a.out, (p0 + row) * a.out_p + (q0 + c) * a.out_q, a.dtype, sum);
-    }
-    cluster_sync();  // no block's shared memory goes before the others have read it
 }
 
 namespace {
@@ -387,16 +525,27 @@ cudaError_t encode(CUtensorMap& map, const void* data, long long k, long long ro
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Pairs of blocks that run at once on the current device (an SM may have no partner), looked up once.
+template <class Kernel>
+int resident_pairs(Kernel kernel, const cudaLaunchConfig_t& cfg, std::atomic<int> (&cache)[256]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return 0;
+    int v = cache[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess) return 0;
+        cache[dev].store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
 template <int TN, bool COLS>
 cudaError_t launch(const MmArgs& a, cudaStream_t st) {
     using S = MmShape<TN>;
     auto* kernel = k_matmul_fp8<TN, COLS>;
-    static std::atomic<int> cache[256] = {};
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<int> cache[256] = {}, given{0};
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::template kSmem<COLS>);
     if (e) return e;
-    const int most = resident_blocks(kernel, S::kThreads, S::kSmem, cache);
-    if constexpr (S::kShift) {  // registers that the launch does not give would be waited for without end
-        static std::atomic<int> given{0};
+    if constexpr (S::kPair) {  // registers that the launch does not give would be waited for without end
         int regs = given.load(std::memory_order_relaxed);
         if (regs == 0) {
             cudaFuncAttributes f;
@@ -405,18 +554,23 @@ cudaError_t launch(const MmArgs& a, cudaStream_t st) {
         }
         if (regs < S::kLaunch) return cudaErrorLaunchOutOfResources;
     }
+    const int group = S::kPair ? 2 : a.splits;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {(unsigned)a.splits, 1, 1};
+    attr[1].val.clusterDim = {(unsigned)group, 1, 1};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.splits > 1 ? a.tiles * a.splits : std::min(a.tiles, most)));
+    cfg.gridDim = dim3((unsigned)group);
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = S::template kSmem<COLS>;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = a.splits > 1 ? 2 : 1;
+    cfg.numAttrs = group > 1 ? 2 : 1;
+    int most;  // groups that run at once; clusters with shares of the inner dimension take a tile each
+    if constexpr (S::kPair) most = resident_pairs(kernel, cfg, cache);
+    else most = group > 1 ? a.tiles : resident_blocks(kernel, S::kThreads, S::template kSmem<COLS>, cache);
+    cfg.gridDim = dim3((unsigned)(group * std::min(a.tiles, most > 0 ? most : 1)));
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
@@ -459,25 +613,26 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     a.out_q = swap ? x.out_stride : 1;
     a.dtype = x.dtype;
     const int size = x.dtype == GS_DTYPE_F32 ? 4 : 2;
-    a.wide = !swap && x.out_stride * size % 32 == 0 && reinterpret_cast<uintptr_t>(x.out) % 32 == 0;
+    a.wide = x.out_stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(x.out) % 16 == 0;
     a.limit = 1u << 18;
     a.err = err;
     const int sms = device_sm_count();
     auto over = [](long long n, long long m) { return (n + m - 1) / m; };
-    const long long tiles_p = over(a.np, kMmRows);
+    long long tiles_p = over(a.np, kMmRows);
     int tn;
     if (swap) tn = a.nq <= 16 ? 16 : a.nq <= 32 ? 32 : 64;
     else tn = tiles_p * over(a.nq, 256) >= sms / 2 ? 256 : cols || tiles_p * over(a.nq, 128) >= sms / 2 ? 128 : 64;
+    if (tn == 256) tiles_p = over(a.np, 2 * kMmRows);
     a.tiles_p = (int)tiles_p;
     const long long tiles = tiles_p * over(a.nq, tn);
     if (tiles > 0x0fffffffll) return cudaErrorInvalidConfiguration;
     a.tiles = (int)tiles;
     a.splits = 1;
     const int slots = tn >= 128 ? sms : 2 * sms;
-    while (a.splits < 8 && 2 * a.splits * tiles <= slots && 2 * a.splits <= a.blocks) a.splits *= 2;
+    while (tn < 256 && a.splits < kMmSplits && 2 * a.splits * tiles <= slots && 2 * a.splits <= a.blocks) a.splits *= 2;
     if (x.k > 0) {
         cudaError_t e;
-        if ((e = encode(a.p, p.data, x.k, a.np, p.stride, kMmRows)) || (e = encode(a.q, q.data, x.k, a.nq, q.stride, tn))) return e;
+        if ((e = encode(a.p, p.data, x.k, a.np, p.stride, kMmRows)) || (e = encode(a.q, q.data, x.k, a.nq, q.stride, tn == 256 ? 128 : tn))) return e;
     }
     return cols ? launch<true>(tn, a, st) : launch<false>(tn, a, st);
 }
