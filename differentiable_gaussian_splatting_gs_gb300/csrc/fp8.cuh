@@ -7,19 +7,25 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gs_common.cuh"
+
 namespace gs {
 
 constexpr int kQBlock = 128;  // columns (or rows and columns) that share a scale
 
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// A product with 1/448, within an ulp of the quotient: a division for each 128 elements in every lane took a third of the
+// quantizing kernels' instructions.
 __device__ __forceinline__ float block_scale(unsigned top) {
-    const float s = __uint_as_float(top) / 448.f;
+    const float s = __uint_as_float(top) * (1.f / 448.f);
     return s < 1.17549435e-38f ? 1.f : s;
 }
+// The scale's reciprocal to an ulp: a quotient moves by 1.5 ulps of float32, which changes the 4-bit significand of about one
+// element in a million.
+__device__ __forceinline__ float scale_back(float scale) { return rcp_approx(scale); }
 
-// Four values times the scale's reciprocal, the first in the lowest byte. (Rounding the reciprocal moves a quotient by an
-// ulp of float32, which changes the 4-bit significand of about one element in a million.)
+// Four values times the scale's reciprocal, the first in the lowest byte.
 __device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv) {
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));

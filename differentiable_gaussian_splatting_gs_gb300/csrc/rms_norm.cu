@@ -24,10 +24,13 @@ struct RmsFwdArgs {
 // The largest of a block's magnitudes: over LANES neighbouring lanes.
 template <int LANES>
 __device__ __forceinline__ unsigned lanes_max(unsigned m) {
-    if (LANES == 32) return __reduce_max_sync(0xffffffffu, m);
+    if constexpr (LANES == 32) {
+        return __reduce_max_sync(0xffffffffu, m);
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+        for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
 }
 
 template <class T, int VEC, int NV, int LPR, int FULL, bool RES>
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd(const RmsFwdArgs a) {
                 }
                 const float scale = block_scale(lanes_max<kLanes>(top));
                 if (mine) {
-                    const float back = 1.f / scale;
+                    const float back = scale_back(scale);
                     Pack<uint32_t, VEC / 4> out;
 #pragma unroll
                     for (int k = 0; k < VEC; k += 4) out.v[k / 4] = quantize4(f[k], f[k + 1], f[k + 2], f[k + 3], back);
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd(const RmsFwdArgs a) {
                         top = max(top, magnitude(f[0]));
                     }
                 }
-                const float scale = block_scale(lanes_max<32>(top)), back = 1.f / scale;
+                const float scale = block_scale(lanes_max<32>(top)), back = scale_back(scale);
 #pragma unroll
                 for (int j = 0; j < kTurn; ++j)
                     if (live && in(i0 + j)) q[at(i0 + j)] = quantize1(y[j], back);
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd_long(const RmsFwdArgs a)
                 scale = block_scale(lanes_max<32>(top));
                 if (lane == 0) a.scale.at(row, c0 / kQBlock) = scale;
             }
-            const float back = 1.f / scale;
+            const float back = scale_back(scale);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = c0 + j * 32 + lane;
