@@ -34,13 +34,13 @@ constexpr int kMmBlock = 128;  // inner dimension of a block, bytes
 constexpr int kMmSplits = 8;   // blocks of a cluster that share a tile's inner dimension, at most
 
 struct MmArgs {
-    CUtensorMap p, q;
+    CUtensorMap p, q, to;
     const float *p_scale, *q_scale;
     long long p_row, p_block, q_row, q_block;  // strides of the scales
     int p_shift, q_shift;                      // 2^shift rows share a scale
     void* out;
     long long out_p, out_q;  // strides of the result, one of them 1
-    int dtype, wide, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes
+    int dtype, wide, boxes, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes; boxes: and `to` is it
     unsigned limit, *err;
 };
 
@@ -143,15 +143,16 @@ struct MmShape {
     static_assert(!kPair || 128 * kFew + (kThreads - 128) * kMany <= kThreads * kLaunch);
     static constexpr int kTileQ = kPair ? TN / 2 : TN;           // rows of Q that a block copies
     static constexpr int kBytes = (kMmRows + kTileQ) * kMmBlock; // a stage: both operands' tiles
+    // Results' rows leave by boxes of 32 rows x 128 bytes, so many of each warp's (none with b's rows along the lanes).
     template <bool COLS>
-    static constexpr bool kStaged = !COLS || TN >= 128;          // results' rows go through shared memory (never with b's along the lanes)
+    static constexpr int kBoxes = kPair ? 2 : !COLS || TN >= 128 ? 1 : 0;
     static constexpr int kResident = TN >= 128 ? 1 : 2;          // blocks of threads on an SM
     template <bool COLS>
-    static constexpr int kStages = kPair && COLS ? 5 : TN >= 128 ? 6 : TN == 64 ? 4 : 5;
+    static constexpr int kStages = kPair ? 4 : TN == 64 && !COLS ? 3 : TN == 64 ? 4 : 5;
     static constexpr int kBufs = TN == 128 ? 4 : 2;              // accumulators
     static constexpr int kTmem = kBufs * TN;
     template <bool COLS>
-    static constexpr int kSmem = 1024 + kStages<COLS> * kBytes;
+    static constexpr int kSmem = 1024 + kStages<COLS> * kBytes + kWarps * kBoxes<COLS> * 4096;
     static_assert(kTmem >= 32 && kResident * kTmem <= 512 && (kTmem & (kTmem - 1)) == 0);
     static_assert(kPair || kStages<false> * kBytes >= kMmRows * (TN + 4) * 4, "a cluster's sums take the tiles' place");
 };
@@ -171,39 +172,64 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// A warp's 32 rows of a tile, COLS columns of them in every thread's sums, `rows` and `left` of them inside the result, which
-// is at `at` (elements): 64 bytes of each row at a time through the warp's 2 KB of shared memory, so that a store writes
-// 8 rows' pieces and not 32 rows' 16 bytes each (which took 2.2 us for a tile of 256 x 256, between which the products
-// can only go two blocks ahead). Element by element where the result's rows do not lie on 16 bytes, and at its right edge.
-template <int COLS>
-__device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[COLS / 2], unsigned char* stage, long long at, int rows, int left) {
-    const int lane = threadIdx.x & 31, wide = a.dtype == GS_DTYPE_F32;
-    auto piece = [&](auto word, auto per) {  // word(i): 16 bytes of the thread's row, `per` columns
-        constexpr int kPer = decltype(per)::value;
+// A box of this block's shared memory -> a matrix; what lies outside is left out. Counts to the thread's bulk group.
+__device__ __forceinline__ void tile_store2(const CUtensorMap* map, int c0, int c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(map), "r"(src),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
+// A warp's 32 rows of a tile, COLS columns of them in every thread's sums, the first at (q0, p0) of the result. Where its rows lie
+// on 16 bytes: by tiled copies of 128 bytes of each row, laid out (with the copies' swizzle) in BOXES times 4 KB of the warp's, which
+// the warp leaves under way. (Until they are stored the products can only go two blocks ahead. Stored by each thread from its
+// row a tile of 256 x 256 took 2.2 us, coalesced through 2 KB of shared memory 1.9 us.) Else element by element.
+template <int COLS, int BOXES>
+__device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[COLS / 2], unsigned char* stage, int p0, int q0) {
+    const int lane = threadIdx.x & 31, rows = a.np - p0, left = a.nq - q0;
+    if (rows <= 0 || left <= 0) return;
+    if (!a.boxes) {
+        if (lane >= rows) return;
+        const long long at = (p0 + lane) * a.out_p + q0 * a.out_q;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 4 * kPer) {
-            if (left < c + 4 * kPer) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = word(c + i * kPer);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + lane / 4, q = lane % 4;
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
-                if (r < rows) *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (at + r * a.out_p + c + q * kPer) * (16 / kPer)) = v;
-            }
-            __syncwarp();
+        for (int i = 0; i < COLS / 2; ++i) {
+            const float2 v = f2_unpack(acc[i]);
+            if (2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
+            if (2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
         }
-    };
-    int done = 0;
-    if (a.wide && a.out_q == 1) {
-        if (wide) {
-            piece([&](int c) {
+        return;
+    }
+    if constexpr (BOXES > 0) {
+        auto boxes = [&](auto per, auto word) {  // word(i): the 16 bytes of the thread's row from column i on, `per` columns
+            constexpr int kPer = decltype(per)::value, kBox = 8 * kPer;
+#pragma unroll
+            for (int c0 = 0; c0 < COLS; c0 += BOXES * kBox) {
+                if (left <= c0) break;
+                if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the copies before have read the boxes
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < BOXES; ++x) {
+                    if (c0 + x * kBox >= COLS) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c0 + x * kBox + i * kPer < COLS)
+                            *reinterpret_cast<uint4*>(stage + x * 4096 + lane * 128 + ((i ^ lane) & 7) * 16) = word(c0 + x * kBox + i * kPer);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one())
+#pragma unroll
+                    for (int x = 0; x < BOXES; ++x)
+                        if (c0 + x * kBox < COLS && c0 + x * kBox < left) tile_store2(&a.to, q0 + c0 + x * kBox, p0, smem_u32(stage) + x * 4096);
+                __syncwarp();
+            }
+        };
+        if (a.dtype == GS_DTYPE_F32)
+            boxes(std::integral_constant<int, 4>(), [&](int c) {
                 const float2 x = f2_unpack(acc[c / 2]), y = f2_unpack(acc[c / 2 + 1]);
                 return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
-            }, std::integral_constant<int, 4>());
-        } else {
-            piece([&](int c) {
+            });
+        else
+            boxes(std::integral_constant<int, 8>(), [&](int c) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -211,18 +237,7 @@ __device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[C
                     w[i] = a.dtype == GS_DTYPE_F16 ? pack2<__half>(x.x, x.y) : pack2<__nv_bfloat16>(x.x, x.y);
                 }
                 return make_uint4(w[0], w[1], w[2], w[3]);
-            }, std::integral_constant<int, 8>());
-        }
-        if (left >= COLS) return;
-        done = left / (wide ? 16 : 32) * (wide ? 16 : 32);
-    }
-    if (lane >= rows) return;
-    at += lane * a.out_p;
-#pragma unroll
-    for (int i = 0; i < COLS / 2; ++i) {
-        const float2 v = f2_unpack(acc[i]);
-        if (2 * i >= done && 2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
-        if (2 * i >= done && 2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
+            });
     }
 }
 
@@ -236,7 +251,6 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
     __shared__ uint32_t tmem_at;
     __shared__ uint64_t scaled[kMmPlaces], used[kMmPlaces];
     __shared__ __align__(16) MmScales<TN, COLS> scales;
-    __shared__ __align__(16) unsigned char staged[S::template kStaged<COLS> ? S::kWarps : 1][S::template kStaged<COLS> ? 2048 : 16];
     const uint32_t tiles = (smem_u32(dynamic) + 1023) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -277,37 +291,39 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
         if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
         if (warp == S::kWarps) {
             // ---- copies ----
-            int turn = 0;
             if (elect_one()) {
+                const uint32_t bars = kPair ? peer_address(full, 0) : smem_u32(full);
+                int s = 0, turns = 0;
+                unsigned phase = 1;  // of the stage's products before: a new barrier's is over
                 bool ok = true;
                 for (int t = first; t < a.tiles && ok; t += step) {
                     const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN + (kPair ? rank * S::kTileQ : 0);
-                    for (int k = k0; k < k1; ++k, ++turn) {
-                        const int s = turn % kStages;
-                        if (turn >= kStages && !(ok = mbar_wait_bounded(empty + s, (turn / kStages - 1) & 1, a.limit, a.err))) break;
-                        const uint32_t at = tiles + s * S::kBytes, bar = kPair ? peer_address(full + s, 0) : smem_u32(full + s);
+                    for (int k = k0; k < k1; ++k) {
+                        if (!(ok = mbar_wait_bounded(empty + s, phase, a.limit, a.err))) break;
+                        const uint32_t at = tiles + s * S::kBytes;
                         // (a pair's bytes are all counted by its first block, which issues the products)
                         if (row_of == 0) mbar_arrive_expect_tx(full + s, kPair ? 2 * S::kBytes : S::kBytes);
-                        tile_load2<kPair>(at, &a.p, k * kMmBlock, p0, bar);
-                        tile_load2<kPair>(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, bar);
+                        tile_load2<kPair>(at, &a.p, k * kMmBlock, p0, bars + 8 * s);
+                        tile_load2<kPair>(at + kMmRows * kMmBlock, &a.q, k * kMmBlock, q0, bars + 8 * s);
+                        ++turns;
+                        if (++s == kStages) s = 0, phase ^= 1;
                     }
                 }
                 // every copy has landed before the blocks end
                 if (row_of == 0)
-                    for (int i = turn > kStages ? turn - kStages : 0; i < turn; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
+                    for (int i = turns > kStages ? turns - kStages : 0; i < turns; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
             }
             __syncwarp();
         } else if (warp == S::kWarps + 1) {
             // ---- products ----
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);  // e4m3 x e4m3, float32
-            int turn = 0;
+            int s = 0, b = 0;
+            unsigned s_phase = 0, b_phase = 1;  // (a new accumulator's reading is over)
             bool ok = row_of == 0;
             for (int t = first; t < a.tiles && ok; t += step)
-                for (int k = k0; k < k1; ++k, ++turn) {
-                    const int s = turn % kStages, b = turn % kBufs;
-                    if (turn >= kBufs) ok = warp_wait(drained + b, (turn / kBufs - 1) & 1, a.limit, a.err);
-                    ok = ok && warp_wait(full + s, (turn / kStages) & 1, a.limit, a.err);
-                    if (!ok) break;
+                for (int k = k0; k < k1; ++k) {
+                    // lanes wait for the tiles or for the accumulator
+                    if (!(ok = warp_wait_all(full + s, s_phase, drained + b, b_phase, a.limit, a.err))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t at = tiles + s * S::kBytes, p = tile_desc(at), q = tile_desc(at + kMmRows * kMmBlock);
@@ -317,6 +333,8 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                         mma8_commit<kPair>(empty + s, 3);
                     }
                     __syncwarp();
+                    if (++s == kStages) s = 0, s_phase ^= 1;
+                    if (++b == kBufs) b = 0, b_phase ^= 1;
                 }
             // every product is complete before the tensor memory is freed
             if (row_of == 0 && elect_one()) {
@@ -379,53 +397,58 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
             // The row in parts: one is on its way while the one before is added.
             constexpr int kParts = kCols / kPart;
-            for (int k = k0, j = 0; k < k1; ++k) {
-                if (j == 0 && ok) ok = warp_wait(scaled + at, at_phase, a.limit, a.err);
-                if (ok) ok = warp_wait(done + b, b_phase, a.limit, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t v[2][kPart];
-                auto load = [&](int i) {
-                    if constexpr (kPart == 32) tmem_ld32(from + b * TN + i * kPart, v[i & 1]);
-                    else tmem_ld16(from + b * TN + i * kPart, v[i & 1]);
-                };
-                load(0);
-                const float scale = scales.p[at][row][j] * (COLS ? 1.f : scales.q[at][c0 / kQBlock * kMmBatch + j]);
-                const f32x2 scale2 = f2_pack(scale, scale);
-                const float* cs = scales.q[at] + (COLS ? j * TN + c0 : 0);
-                const bool ends = j == kMmBatch - 1 || k + 1 == k1;
+            for (int k = k0; k < k1 && ok; k += kMmBatch) {
+                if (!(ok = warp_wait(scaled + at, at_phase, a.limit, a.err))) break;
+                // (unrolled, with the batch's scales of the rows in registers: 98 instead of 107 us for 4096 x 1024 x 17,384 with scales by column,
+                // whose turns wait for shared memory, but 236 instead of 223 for 16384 x 4096 x 4096 without, for want of registers)
+                float4 of_p = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (COLS) of_p = *reinterpret_cast<const float4*>(scales.p[at][row]);
+                const float each[kMmBatch] = {of_p.x, of_p.y, of_p.z, of_p.w};
+#pragma unroll(COLS ? kMmBatch : 1)
+                for (int j = 0; j < kMmBatch; ++j) {
+                    if (k + j >= k1) break;
+                    if (!(ok = warp_wait(done + b, b_phase, a.limit, a.err))) break;
+                    tc_fence_after();
+                    uint32_t v[2][kPart];
+                    auto load = [&](int i) {
+                        if constexpr (kPart == 32) tmem_ld32(from + b * TN + i * kPart, v[i & 1]);
+                        else tmem_ld16(from + b * TN + i * kPart, v[i & 1]);
+                    };
+                    load(0);
+                    float scale;
+                    if constexpr (COLS) scale = each[j];
+                    else scale = scales.p[at][row][j] * scales.q[at][c0 / kQBlock * kMmBatch + j];
+                    const f32x2 scale2 = f2_pack(scale, scale);
+                    const float* cs = scales.q[at] + (COLS ? j * TN + c0 : 0);
 #pragma unroll
-                for (int i = 0; i < kParts; ++i) {
-                    if constexpr (kPart == 32) tmem_wait_ld(v[i & 1]);
-                    else tmem_wait_ld16(v[i & 1]);
-                    if (i + 1 < kParts) {
-                        load(i + 1);
-                    } else {
-                        tc_fence_before();
-                        if constexpr (kPair) warp_arrive_at(drained_at + 8 * b);
-                        else warp_arrive(drained + b);
-                        if (++b == kBufs) b = 0, b_phase ^= 1;
-                    }
-#pragma unroll
-                    for (int c = 0; c < kPart; c += 4) {
-                        const uint32_t* u = v[i & 1] + c;
-                        f32x2 lo = f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), hi = f2_pack(__uint_as_float(u[2]), __uint_as_float(u[3]));
-                        if (COLS) {
-                            const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + c);
-                            lo = f2_mul(lo, f2_pack(w.x, w.y));
-                            hi = f2_mul(hi, f2_pack(w.z, w.w));
+                    for (int i = 0; i < kParts; ++i) {
+                        if constexpr (kPart == 32) tmem_wait_ld(v[i & 1]);
+                        else tmem_wait_ld16(v[i & 1]);
+                        if (i + 1 < kParts) {
+                            load(i + 1);
+                        } else {
+                            tc_fence_before();
+                            if constexpr (kPair) warp_arrive_at(drained_at + 8 * b);
+                            else warp_arrive(drained + b);
                         }
-                        f32x2* to = acc + (i * kPart + c) / 2;
-                        to[0] = f2_fma(lo, scale2, to[0]);
-                        to[1] = f2_fma(hi, scale2, to[1]);
+#pragma unroll
+                        for (int c = 0; c < kPart; c += 4) {
+                            const uint32_t* u = v[i & 1] + c;
+                            f32x2 lo = f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), hi = f2_pack(__uint_as_float(u[2]), __uint_as_float(u[3]));
+                            if (COLS) {
+                                const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + c);
+                                lo = f2_mul(lo, f2_pack(w.x, w.y));
+                                hi = f2_mul(hi, f2_pack(w.z, w.w));
+                            }
+                            f32x2* to = acc + (i * kPart + c) / 2;
+                            to[0] = f2_fma(lo, scale2, to[0]);
+                            to[1] = f2_fma(hi, scale2, to[1]);
+                        }
                     }
+                    if (++b == kBufs) b = 0, b_phase ^= 1;
                 }
-                ++j;
-                if (ends) {
-                    warp_arrive(used + at);
-                    if (++at == kMmPlaces) at = 0, at_phase ^= 1;
-                    j = 0;
-                }
+                warp_arrive(used + at);
+                if (++at == kMmPlaces) at = 0, at_phase ^= 1;
             }
             if (!kPair && group > 1) {
                 // the cluster's shares, in the tiles' place: rows where the result's rows are the lanes', else columns
@@ -442,10 +465,12 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                 }
                 break;  // one tile for a cluster
             }
-            const int r0 = p0 + warp % 4 * 32;
-            if (r0 < a.np) store_rows<kCols>(a, acc, staged[S::template kStaged<COLS> ? warp : 0], r0 * a.out_p + (long long)q0 * a.out_q, min(32, a.np - r0), a.nq - q0);
+            store_rows<kCols, S::template kBoxes<COLS>>(a, acc, dynamic + (tiles - smem_u32(dynamic)) + kStages * S::kBytes + warp * (S::template kBoxes<COLS> * 4096),
+                                                        p0 + warp % 4 * 32, q0);
             __syncwarp();  // the instructions on tensor memory and the cluster's barriers take whole warps
         }
+        if (S::template kBoxes<COLS> && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the result is written
+        __syncwarp();
     }
     __syncwarp();
     tc_fence_before();
@@ -514,14 +539,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-cudaError_t encode(CUtensorMap& map, const void* data, long long k, long long rows, long long stride, int box_rows) {
+// Boxes of 128 bytes x box_rows of `rows` rows of `cols` elements, `stride` elements apart.
+cudaError_t encode(CUtensorMap& map, CUtensorMapDataType type, int size, const void* data, long long cols, long long rows, long long stride, int box_rows) {
     auto f = encoder();
     if (!f) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(rows > 1 ? stride : (k + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {kMmBlock, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    const CUresult r = f(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, step,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(rows > 1 ? stride * size : (cols * size + 15) / 16 * 16)};
+    const cuuint32_t box[2] = {(cuuint32_t)(kMmBlock / size), (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = f(&map, type, 2, const_cast<void*>(data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -630,10 +655,14 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     a.splits = 1;
     const int slots = tn >= 128 ? sms : 2 * sms;
     while (tn < 256 && a.splits < kMmSplits && 2 * a.splits * tiles <= slots && 2 * a.splits <= a.blocks) a.splits *= 2;
-    if (x.k > 0) {
-        cudaError_t e;
-        if ((e = encode(a.p, p.data, x.k, a.np, p.stride, kMmRows)) || (e = encode(a.q, q.data, x.k, a.nq, q.stride, tn == 256 ? 128 : tn))) return e;
-    }
+    cudaError_t e;
+    constexpr auto kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (x.k > 0 && ((e = encode(a.p, kBytes, 1, p.data, x.k, a.np, p.stride, kMmRows)) ||
+                    (e = encode(a.q, kBytes, 1, q.data, x.k, a.nq, q.stride, tn == 256 ? 128 : tn))))
+        return e;
+    a.boxes = a.wide && !swap && a.splits == 1;
+    if (a.boxes && (e = encode(a.to, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size, x.out, x.n, x.m, x.out_stride, 32)))
+        return e;
     return cols ? launch<true>(tn, a, st) : launch<false>(tn, a, st);
 }
 
