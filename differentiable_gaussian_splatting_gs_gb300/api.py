@@ -497,7 +497,7 @@ def gs_rms_norm_bwd(dy, h, rstd, weight=None, dh=None, out=None, workspace=None,
     """Backward of gs_rms_norm_fwd: (dx, dweight); dx is the gradient of x and of the residual. dh: the gradient of h from its
     other readers, or None. dweight is None without a weight. out: the tensors to write into (dx may be dy, h or dh).
     workspace: a contiguous tensor on the inputs' device, kept by the caller (one is allocated when None or too small), that
-    starts on 16 bytes."""
+    starts on 16 bytes; calls that may run at once need one each."""
     if stream is not None:
         with _on(stream, h):
             return gs_rms_norm_bwd(dy, h, rstd, weight, dh, out, workspace)
@@ -547,8 +547,11 @@ def gs_clip_grads(grads, max_norm: float | None, eps: float = 1e-6, out=None, no
     """Multiplies the gradients by min(1, max_norm / (norm + eps)), norm the 2-norm of all their elements, and returns the
     norm as gs_grad_norm does. In place, or into `out` (tensors of the same shapes and dtypes). With a norm that is not a
     number all elements become so. workspace: a contiguous tensor on the gradients' device, kept by the caller (one is
-    allocated when None or too small), that starts on 16 bytes."""
+    allocated when None or too small), that starts on 16 bytes; calls that may run at once need one each."""
     if stream is not None:
+        grads = list(grads)
+        if not grads:
+            raise ValueError("gs_clip_grads: at least one gradient is needed")
         with _on(stream, grads[0]):
             return gs_clip_grads(grads, max_norm, eps, out, norm, workspace)
     return _abi.binding().clip_grads(grads, max_norm, eps, out, norm, workspace)

@@ -57,6 +57,13 @@ const at::Tensor& tensor(PyObject* o, const char* where) {
     return THPVariable_Unpack(o);
 }
 
+// t's address; NULL, which stands for an argument left out, only where it has no elements.
+void* address_of(const at::Tensor& t) {
+    void* p = t.data_ptr();
+    if (!p && t.numel() > 0) throw Refusal("a tensor without memory of its own");
+    return p;
+}
+
 // An argument that may be None.
 struct Given {
     const at::Tensor* t;
@@ -64,7 +71,7 @@ struct Given {
     explicit operator bool() const { return t != nullptr; }
     const at::Tensor& operator*() const { return *t; }
     const at::Tensor* operator->() const { return t; }
-    void* address() const { return t ? t->data_ptr() : nullptr; }
+    void* address() const { return t ? address_of(*t) : nullptr; }
 };
 
 at::Tensor alloc(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& like) {
@@ -452,7 +459,7 @@ PyObject* rms_norm_fwd(PyObject* const* arg) {
     if (fp8) q = fp8_of(out[0], out[1], 1, x, me);
     call(x, me, [&](void* stream) {
         return gs_rms_norm_fwd(x.data_ptr(), rows.stride, residual.address(), r_stride, rows.n, cols, dtype, weight.address(),
-                               weight ? dtype_code(*weight, me) : dtype, (float)eps, residual ? h.data_ptr() : nullptr, h_stride,
+                               weight ? dtype_code(*weight, me) : dtype, (float)eps, residual ? address_of(h) : nullptr, h_stride,
                                fp8 ? nullptr : out[0].data_ptr(), y_stride, fp8 ? &q : nullptr, rstd.data_ptr<float>(), stream);
     });
     if (!residual) h = x;
@@ -491,7 +498,7 @@ PyObject* rms_norm_bwd(PyObject* const* arg) {
     call(h, me, [&](void* stream) {
         return gs_rms_norm_bwd(dy.data_ptr(), dy_stride, h.data_ptr(), rows.stride, dh.address(), dh_stride, rows.n, cols, dtype,
                                rstd.data_ptr<float>(), weight.address(), kind, out[0].data_ptr(), dx_stride,
-                               out[1].defined() ? out[1].data_ptr() : nullptr, workspace, need, stream);
+                               out[1].defined() ? address_of(out[1]) : nullptr, workspace, need, stream);
     });
     return tuple_of(out, 2);
 }
@@ -585,14 +592,14 @@ PyObject* clip_grads(PyObject* const* arg) {
         list[i].dtype = dtype_code(g, me);
         if (g.device() != first.device()) refuse(me, "gradient ", i, " is not on ", first.device());
         if (!g.is_non_overlapping_and_dense()) refuse(me, "gradient ", i, " is not one piece of memory");
-        list[i].grad = g.numel() ? g.data_ptr() : nullptr;
+        list[i].grad = address_of(g);
         list[i].n = g.numel();
         list[i].out = nullptr;
         if (!outs.o) continue;
         const at::Tensor& o = tensor(PySequence_Fast_GET_ITEM(outs.o, i), me);
         if (o.scalar_type() != g.scalar_type() || o.device() != g.device() || o.sizes() != g.sizes() || (g.numel() > 1 && o.strides() != g.strides()))
             refuse(me, "output ", i, " must have the shape, strides, dtype and device of its gradient");
-        list[i].out = o.numel() ? o.data_ptr() : nullptr;
+        list[i].out = address_of(o);
     }
     const Given given(arg[4], me), room(arg[5], me);
     at::Tensor norm;

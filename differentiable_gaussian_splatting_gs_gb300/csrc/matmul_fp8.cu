@@ -40,7 +40,7 @@ struct MmArgs {
     int p_shift, q_shift;                      // 2^shift rows share a scale
     void* out;
     long long out_p, out_q;  // strides of the result, one of them 1
-    int dtype, wide, boxes, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes; boxes: and `to` is it
+    int dtype, wide, boxes, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes; boxes: columns that `to` has
     unsigned limit, *err;
 };
 
@@ -187,23 +187,24 @@ template <int COLS, int BOXES>
 __device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[COLS / 2], unsigned char* stage, int p0, int q0) {
     const int lane = threadIdx.x & 31, rows = a.np - p0, left = a.nq - q0;
     if (rows <= 0 || left <= 0) return;
-    if (!a.boxes) {
-        if (lane >= rows) return;
+    // a tiled copy writes whole 16 bytes: what the result has behind its last is stored by the threads
+    const int whole = a.boxes - q0;
+    if (whole < min(left, COLS) && lane < rows) {
         const long long at = (p0 + lane) * a.out_p + q0 * a.out_q;
 #pragma unroll
         for (int i = 0; i < COLS / 2; ++i) {
             const float2 v = f2_unpack(acc[i]);
-            if (2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
-            if (2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
+            if (2 * i >= whole && 2 * i < left) store_elem(a.out, at + 2 * i * a.out_q, a.dtype, v.x);
+            if (2 * i + 1 >= whole && 2 * i + 1 < left) store_elem(a.out, at + (2 * i + 1) * a.out_q, a.dtype, v.y);
         }
-        return;
     }
+    __syncwarp();
     if constexpr (BOXES > 0) {
         auto boxes = [&](auto per, auto word) {  // word(i): the 16 bytes of the thread's row from column i on, `per` columns
             constexpr int kPer = decltype(per)::value, kBox = 8 * kPer;
 #pragma unroll
             for (int c0 = 0; c0 < COLS; c0 += BOXES * kBox) {
-                if (left <= c0) break;
+                if (whole <= c0) break;
                 if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the copies before have read the boxes
                 __syncwarp();
 #pragma unroll
@@ -219,7 +220,7 @@ __device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[C
                 if (elect_one())
 #pragma unroll
                     for (int x = 0; x < BOXES; ++x)
-                        if (c0 + x * kBox < COLS && c0 + x * kBox < left) tile_store2(&a.to, q0 + c0 + x * kBox, p0, smem_u32(stage) + x * 4096);
+                        if (c0 + x * kBox < COLS && c0 + x * kBox < whole) tile_store2(&a.to, q0 + c0 + x * kBox, p0, smem_u32(stage) + x * 4096);
                 __syncwarp();
             }
         };
@@ -660,8 +661,8 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     if (x.k > 0 && ((e = encode(a.p, kBytes, 1, p.data, x.k, a.np, p.stride, kMmRows)) ||
                     (e = encode(a.q, kBytes, 1, q.data, x.k, a.nq, q.stride, tn == 256 ? 128 : tn))))
         return e;
-    a.boxes = a.wide && !swap && a.splits == 1;
-    if (a.boxes && (e = encode(a.to, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size, x.out, x.n, x.m, x.out_stride, 32)))
+    a.boxes = a.wide && !swap && a.splits == 1 ? (int)(x.n / (16 / size) * (16 / size)) : 0;
+    if (a.boxes && (e = encode(a.to, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size, x.out, a.boxes, x.m, x.out_stride, 32)))
         return e;
     return cols ? launch<true>(tn, a, st) : launch<false>(tn, a, st);
 }
