@@ -113,8 +113,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
+// Completes the thread's loads (`wait`, once for several); v's values pass through, as in tmem_wait_ld.
+__device__ __forceinline__ void tmem_landed(uint32_t (&v)[16], bool wait) {
+    if (wait) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile(""
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
                    "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
@@ -245,8 +247,8 @@ __device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[C
 template <int TN, bool COLS>
 __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident) k_matmul_fp8(const __grid_constant__ MmArgs a) {
     using S = MmShape<TN>;
-    constexpr bool kPair = S::kPair;
-    constexpr int kStages = S::template kStages<COLS>, kBufs = S::kBufs, kCols = S::kCols, kPart = TN == 128 ? 32 : 16;
+    constexpr bool kPair = S::kPair, kAlone = !COLS && TN >= 128;
+    constexpr int kStages = S::template kStages<COLS>, kBufs = S::kBufs, kCols = S::kCols, kGroup = kAlone ? 64 : 16;
     extern __shared__ unsigned char dynamic[];
     __shared__ uint64_t full[kStages], empty[kStages], done[kBufs], drained[kBufs], last;
     __shared__ uint32_t tmem_at;
@@ -391,15 +393,14 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
         unsigned b_phase = 0, at_phase = 0;
         bool ok = true;
         const uint32_t drained_at = kPair ? peer_address(drained, 0) : 0;
+        bool mine = true;
         for (int t = first; t < a.tiles; t += step) {
             const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN + c0;
             f32x2 acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-            // The row in parts: one is on its way while the one before is added.
-            constexpr int kParts = kCols / kPart;
             for (int k = k0; k < k1 && ok; k += kMmBatch) {
-                if (!(ok = warp_wait(scaled + at, at_phase, a.limit, a.err))) break;
+                if (!(ok = warp_wait(scaled + at, at_phase, a.limit, a.err) && (!kAlone || __all_sync(0xffffffffu, mine)))) break;
                 // (unrolled, with the batch's scales of the rows in registers: 98 instead of 107 us for 4096 x 1024 x 17,384 with scales by column,
                 // whose turns wait for shared memory, but 236 instead of 223 for 16384 x 4096 x 4096 without, for want of registers)
                 float4 of_p = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -408,40 +409,42 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
 #pragma unroll(COLS ? kMmBatch : 1)
                 for (int j = 0; j < kMmBatch; ++j) {
                     if (k + j >= k1) break;
-                    if (!(ok = warp_wait(done + b, b_phase, a.limit, a.err))) break;
-                    tc_fence_after();
-                    uint32_t v[2][kPart];
-                    auto load = [&](int i) {
-                        if constexpr (kPart == 32) tmem_ld32(from + b * TN + i * kPart, v[i & 1]);
-                        else tmem_ld16(from + b * TN + i * kPart, v[i & 1]);
-                    };
-                    load(0);
                     float scale;
                     if constexpr (COLS) scale = each[j];
                     else scale = scales.p[at][row][j] * scales.q[at][c0 / kQBlock * kMmBatch + j];
                     const f32x2 scale2 = f2_pack(scale, scale);
+                    // (kAlone: each lane waits for itself, 217 -> 205 us for 16384 x 4096 x 4096: a lane that gave up goes on with its warp to the next
+                    // batch, where all learn of it)
+                    if constexpr (kAlone) {
+                        mine &= __builtin_expect(mbar_try_wait(done + b, b_phase), 1) || mbar_wait_bounded(done + b, b_phase, a.limit, a.err);
+                        __syncwarp();
+                    } else if (!(ok = warp_wait(done + b, b_phase, a.limit, a.err))) {
+                        break;
+                    }
+                    tc_fence_after();
                     const float* cs = scales.q[at] + (COLS ? j * TN + c0 : 0);
 #pragma unroll
-                    for (int i = 0; i < kParts; ++i) {
-                        if constexpr (kPart == 32) tmem_wait_ld(v[i & 1]);
-                        else tmem_wait_ld16(v[i & 1]);
-                        if (i + 1 < kParts) {
-                            load(i + 1);
-                        } else {
+                    for (int g = 0; g < kCols; g += kGroup) {
+                        uint32_t v[kGroup / 16][16];
+#pragma unroll
+                        for (int i = 0; i < kGroup / 16; ++i) tmem_ld16(from + b * TN + g + 16 * i, v[i]);
+#pragma unroll
+                        for (int i = 0; i < kGroup / 16; ++i) tmem_landed(v[i], i == 0);
+                        if (g + kGroup == kCols) {
                             tc_fence_before();
                             if constexpr (kPair) warp_arrive_at(drained_at + 8 * b);
                             else warp_arrive(drained + b);
                         }
 #pragma unroll
-                        for (int c = 0; c < kPart; c += 4) {
-                            const uint32_t* u = v[i & 1] + c;
+                        for (int c = 0; c < kGroup; c += 4) {
+                            const uint32_t* u = v[c / 16] + c % 16;
                             f32x2 lo = f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), hi = f2_pack(__uint_as_float(u[2]), __uint_as_float(u[3]));
                             if (COLS) {
-                                const float4 w = *reinterpret_cast<const float4*>(cs + i * kPart + c);
+                                const float4 w = *reinterpret_cast<const float4*>(cs + g + c);
                                 lo = f2_mul(lo, f2_pack(w.x, w.y));
                                 hi = f2_mul(hi, f2_pack(w.z, w.w));
                             }
-                            f32x2* to = acc + (i * kPart + c) / 2;
+                            f32x2* to = acc + (g + c) / 2;
                             to[0] = f2_fma(lo, scale2, to[0]);
                             to[1] = f2_fma(hi, scale2, to[1]);
                         }
