@@ -1023,20 +1023,34 @@ struct Span {
     int64_t rows, bytes, stride;
 };
 
+// Rows that meet or overlap are one piece.
 Span span_of(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride, size_t size) {
+    if (rows < 1 || cols < 1) return {name, nullptr, 0, 0, 0};
     const int64_t bytes = cols * (int64_t)size, apart = stride * (int64_t)size;
-    if (rows > 1 && apart == bytes) return {name, p, 1, rows * bytes, rows * bytes};  // one piece
-    return {name, p, rows, bytes, rows > 1 ? apart : bytes};
+    if (rows == 1) return {name, p, 1, bytes, bytes};
+    if (apart > bytes) return {name, p, rows, bytes, apart};
+    const __int128 all = (__int128)(rows - 1) * apart + bytes, most = (__int128)1 << 62;
+    return {name, p, 1, (int64_t)(all < most ? all : most), (int64_t)(all < most ? all : most)};
 }
 
 constexpr int kFp8Block = 128;
+
+// A tensor's scales, by the smaller of their strides (those between them count as theirs); none that run backwards.
+Span scales_of(const char* name, const gs_fp8& t, int64_t rows, int64_t cols) {
+    const int64_t up = (rows + t.block_rows - 1) / t.block_rows, across = (cols + kFp8Block - 1) / kFp8Block;
+    if (rows < 1 || cols < 1) return {name, nullptr, 0, 0, 0};
+    const int64_t of_row = up > 1 ? t.scale_row : 0, of_block = across > 1 ? t.scale_block : 0;
+    if (of_row < 0 || of_block < 0) return {name, nullptr, 0, 0, 0};
+    const bool down = up > 1 && (across <= 1 || of_row <= of_block);  // rows' scales are the closer ones
+    return down ? span_of(name, t.scale, across, (up - 1) * of_row + 1, of_block, 4) : span_of(name, t.scale, up, (across - 1) * of_block + 1, of_row, 4);
+}
 
 // Whether rows of one meet rows of the other: exact where the strides agree (as in slices of one buffer); where they do not
 // and the ranges meet, only a common start is taken for it.
 bool meet(const Span& a, const Span& b) {
     if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-    const uintptr_t p_end = p + (a.rows - 1) * a.stride + a.bytes, q_end = q + (b.rows - 1) * b.stride + b.bytes;
+    const __int128 p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    const __int128 p_end = p + (__int128)(a.rows - 1) * a.stride + a.bytes, q_end = q + (__int128)(b.rows - 1) * b.stride + b.bytes;
     if (p_end <= q || q_end <= p) return false;
     if (a.rows == 1 || b.rows == 1) {
         const Span &one = a.rows == 1 ? a : b, &many = a.rows == 1 ? b : a;
@@ -1046,7 +1060,7 @@ bool meet(const Span& a, const Span& b) {
         return in < many.bytes || in + one.bytes > many.stride;
     }
     if (a.stride != b.stride) return a.p == b.p;
-    const int64_t in = (int64_t)(q >= p ? (q - p) % (uintptr_t)a.stride : (a.stride - (int64_t)((p - q) % (uintptr_t)a.stride)) % a.stride);
+    const int64_t in = (int64_t)(((q - p) % a.stride + a.stride) % a.stride);
     return in < a.bytes || in + b.bytes > a.stride;
 }
 
@@ -1068,14 +1082,18 @@ int check_fp8(const char* where, const char* name, const gs_fp8* t, int64_t rows
     if (rows > 1 && (t->stride < cols || t->stride > (1ll << 39) || t->stride % 16 != 0))
         return fail(GS_ERR_ARG, "%s: row stride %lld of %s: a multiple of 16 of at least %lld is needed", where, (long long)t->stride, name, (long long)cols);
     if (!t->scale || !aligned(t->scale, 4)) return fail(GS_ERR_ARG, "%s: the scales of %s are NULL or misaligned", where, name);
+    constexpr int64_t kMost = 1ll << 36;
+    if (t->scale_row > kMost || t->scale_row < -kMost || t->scale_block > kMost || t->scale_block < -kMost)
+        return fail(GS_ERR_ARG, "%s: strides %lld, %lld of the scales of %s", where, (long long)t->scale_row, (long long)t->scale_block, name);
     return GS_OK;
 }
 
 // Scales that a call writes: a place for each block.
 int check_scales(const char* where, const gs_fp8& t, int64_t rows, int64_t cols) {
     const int64_t up = (rows + t.block_rows - 1) / t.block_rows, across = (cols + kFp8Block - 1) / kFp8Block;
-    if ((up > 1 && t.scale_row == 0) || (across > 1 && t.scale_block == 0))
-        return fail(GS_ERR_ARG, "%s: scales share memory (a stride of 0)", where);
+    const int64_t r = t.scale_row, b = t.scale_block;
+    const bool fits = (up <= 1 || r > 0) && (across <= 1 || b > 0) && (up <= 1 || across <= 1 || (r < b ? (up - 1) * r < b : (across - 1) * b < r));
+    if (!fits) return fail(GS_ERR_ARG, "%s: scales share memory (strides %lld, %lld)", where, (long long)r, (long long)b);
     return GS_OK;
 }
 
@@ -1134,6 +1152,10 @@ int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64
                to_y = !q ? span_of("y", y, rows, cols, y_stride, size) : span_of("q", q->data, rows, cols, q->stride, 1),
                in[] = {span_of("x", x, rows, cols, x_stride, size), span_of("the residual", residual, rows, cols, residual_stride, size), to_h};
     if ((s = check_apart(me, to_h, in, 2, 2)) || (s = check_apart(me, to_y, in, 3, y ? 2 : 0))) return s;
+    if (q) {
+        const Span scales = scales_of("q's scale", *q, rows, cols), other[] = {in[0], in[1], to_h, to_y};
+        if ((s = check_apart(me, scales, other, 4, 0))) return s;
+    }
     if (rows == 0) return GS_OK;
     unsigned* err = error_word(&s);
     if (!err) return s;
@@ -1212,8 +1234,8 @@ int gs_quantize_fp8(const void* x, int64_t x_row_stride, int64_t x_col_stride, i
         return fail(GS_ERR_ARG, "%s: strides %lld, %lld of x: one must be 1", me, (long long)x_row_stride, (long long)x_col_stride);
     const int64_t lines = by_cols ? cols : rows, len = by_cols ? rows : cols, stride = by_cols ? x_col_stride : x_row_stride;
     if (lines > 1 && (stride < 0 || stride > (1ll << 40))) return fail(GS_ERR_ARG, "%s: stride %lld of x", me, (long long)stride);
-    const Span in = span_of("x", x, lines, len, stride < len ? len : stride, size);
-    if ((s = check_apart(me, span_of("q", q->data, rows, cols, q->stride, 1), &in, 1, 0))) return s;
+    const Span to = span_of("q", q->data, rows, cols, q->stride, 1), in[] = {span_of("x", x, lines, len, stride, size), to};
+    if ((s = check_apart(me, to, in, 1, 0)) || (s = check_apart(me, scales_of("q's scale", *q, rows, cols), in, 2, 0))) return s;
     unsigned* err = error_word(&s);
     if (!err) return s;
     cudaError_t e = launch_quantize(dtype, x, lines > 1 ? stride : 0, by_cols, rows, (int)cols, q->block_rows != 1, q->data, q->stride, q->scale,
@@ -1233,8 +1255,9 @@ int gs_matmul_fp8(const gs_fp8* a, const gs_fp8* b, int64_t m, int64_t n, int64_
     if (m == 0 || n == 0) return GS_OK;
     if ((s = check_rows(me, "out", out, out_stride, m, n, dtype))) return s;
     const Span to = span_of("out", out, m, n, out_stride, elem_bytes(dtype)),
-               in[] = {span_of("a", k ? a->data : nullptr, m, k, a->stride, 1), span_of("b", k ? b->data : nullptr, n, k, b->stride, 1)};
-    if ((s = check_apart(me, to, in, 2, 0))) return s;
+               in[] = {span_of("a", a->data, m, k, a->stride, 1), span_of("b", b->data, n, k, b->stride, 1), scales_of("a's scale", *a, m, k),
+                       scales_of("b's scale", *b, n, k)};
+    if ((s = check_apart(me, to, in, 4, 0))) return s;
     unsigned* err = error_word(&s);
     if (!err) return s;
     auto matrix = [](const gs_fp8& t) { return Fp8Matrix{t.data, t.stride, t.scale, t.scale_row, t.scale_block, t.block_rows}; };

@@ -562,7 +562,8 @@ int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs
  * float32 or float64. Row strides are in elements.                                              */
 
 /* Rows of 8-bit values, 16-byte aligned with a row stride that is a multiple of 16. The scale of row r
- * and columns 128 j .. is scale[r / block_rows * scale_row + j * scale_block] (any strides). */
+ * and columns 128 j .. is scale[r / block_rows * scale_row + j * scale_block] (any
+ * strides for scales that are read; those that are written lie apart, from one another and from the rest). */
 typedef struct gs_fp8 {
     void*   data;
     int64_t stride;

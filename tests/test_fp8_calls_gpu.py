@@ -150,3 +150,20 @@ def test_many_products_of_all_forms_at_once():
         got.append((api.gs_matmul_fp8(*args, dtype=torch.float32, stream=streams[i % 4]), want))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in got) and api.gs_device_error() == _abi.GS_OK
+
+
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_and_columns_that_repeat(dtype, block):
+    room = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    for x in (torch.randn(1, 300, device=DEV), torch.randn(70, 1, device=DEV)):
+        one = room[:x.numel() * dtype.itemsize].view(dtype).view(x.shape)
+        one.copy_(x)
+        many = one.expand(700, 300) if x.shape[0] == 1 else one.expand(70, 500)
+        out = api.gs_quantize_fp8(many.contiguous(), block)
+        # right behind the only row or column
+        at = (one.numel() * dtype.itemsize + 15) // 16 * 16
+        wide = (many.shape[1] + 15) // 16 * 16
+        q = room[at:at + many.shape[0] * wide].view(torch.float8_e4m3fn).view(-1, wide)[:, :many.shape[1]]
+        got = api.gs_quantize_fp8(many, block, out=(q, torch.empty_like(out[1])))
+        assert torch.equal(got[0].view(torch.uint8), out[0].view(torch.uint8)) and torch.equal(got[1], out[1])

@@ -117,3 +117,61 @@ def test_bindings_refuse_host_tensors():
         api.gs_grad_norm([])
     with pytest.raises(ValueError, match="float32"):
         api.gs_matmul_fp8(q, s, q, s, dtype=torch.float64)
+
+
+def _accepted(lib, status):
+    """Past the checks of the arguments (there is no device to go on with)."""
+    return status == _abi.GS_ERR_CUDA
+
+
+def test_rows_that_repeat_take_only_their_memory(lib):
+    def call(x, xr, xc, rows=1000, cols=128, q=_fp8(data=ROOM + 4096, stride=128, block=1000)):
+        return lib.gs_quantize_fp8(x, xr, xc, rows, cols, 0, _ref(q), None)
+
+    # a row, a column, windows one element apart: 512, 4,000 and 4,508 bytes
+    assert _accepted(lib, call(ROOM, 0, 1))
+    assert _accepted(lib, call(ROOM, 1, 0))
+    assert _accepted(lib, call(ROOM - 512, 1, 1))
+    for bad in ((ROOM + 4096, 0, 1), (ROOM + 3600, 0, 1), (ROOM + 100, 1, 0), (ROOM, 1, 1)):
+        assert call(*bad) == ARG and b"lies on" in lib.gs_last_error_message(), bad
+
+
+def test_scales_have_memory_of_their_own(lib):
+    def quantize(q, rows=256, cols=512):
+        return lib.gs_quantize_fp8(ROOM, 512, 1, rows, cols, 0, _ref(q), None)
+
+    def q(**kw):
+        return _fp8(**{"stride": 512, "block": 256, **kw})
+
+    assert _accepted(lib, quantize(q())) and _accepted(lib, quantize(q(row=4, block=1))) and _accepted(lib, quantize(q(row=8, block=2)))
+    for bad in (q(block=255), q(row=3, block=1), q(row=1, block=1), q(row=2, block=2), q(row=-1), q(block=-256), q(row=0), q(block=0)):
+        assert quantize(bad) == ARG and b"share memory" in lib.gs_last_error_message(), (bad.scale_row, bad.scale_block)
+    for bad in (q(scale=ROOM), q(scale=ROOM + 512 * 1024 - 4), q(scale=8 * ROOM + 512), q(scale=8 * ROOM - 4)):
+        assert quantize(bad) == ARG and b"lies on" in lib.gs_last_error_message(), bad.scale
+
+    def norm(t, y=None):
+        return lib.gs_rms_norm_fwd(ROOM, 512, 2 * ROOM, 512, 256, 512, 0, None, 0, 1e-6, 3 * ROOM, 512, y, 512, _ref(t), 4 * ROOM, None)
+
+    assert _accepted(lib, norm(q()))
+    for bad in (q(scale=ROOM), q(scale=2 * ROOM + 4), q(scale=3 * ROOM + 8), q(scale=8 * ROOM)):
+        assert norm(bad) == ARG and b"lies on" in lib.gs_last_error_message(), bad.scale
+    assert norm(q(block=255)) == ARG
+
+    def product(a, b, out=ROOM):
+        return lib.gs_matmul_fp8(_ref(a), _ref(b), 256, 256, 512, 2, out, 256, None)
+
+    b = _fp8(data=10 * ROOM, stride=512, scale=11 * ROOM, rows=128, row=4, block=1)
+    assert _accepted(lib, product(q(), b))
+    # scales that are read may repeat, or run backwards
+    for fine in (q(row=0), q(block=0), q(row=0, block=0), q(row=-1), q(block=-256), q(row=1, block=1)):
+        assert _accepted(lib, product(fine, b)), (fine.scale_row, fine.scale_block)
+    for bad in (9 * ROOM, 9 * ROOM + 4 * 1022, 11 * ROOM + 16):
+        assert product(q(), b, bad) == ARG and b"lies on" in lib.gs_last_error_message(), bad
+
+
+def test_sizes_without_an_end(lib):
+    """Rows and strides at their limits: refused or passed on, never a wrapped address."""
+    top = 1 << 40
+    assert _accepted(lib, lib.gs_quantize_fp8(ROOM, 0, 1, top, 128, 0, _ref(_fp8(data=1 << 44, scale=1 << 43, stride=128)), None))
+    assert lib.gs_quantize_fp8(ROOM, top, 1, top, 128, 0, _ref(_fp8(stride=1 << 39, block=0)), None) == ARG
+    assert lib.gs_quantize_fp8(ROOM, 1, top, top, (1 << 30) - 1, 0, _ref(_fp8(stride=1 << 39, block=top)), None) == ARG
