@@ -185,57 +185,93 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd(const RmsFwdArgs a) {
 }
 
 // Rows of more than kNormMaxCols elements: a block per row, which reads it again for y (from the L2 or the L1), or h, which
-// each thread reads as it wrote it. A warp takes 128 columns at a time, which share a scale.
-template <class T>
+// each thread reads as it wrote it.
+template <class T, int VEC, bool RES>
 __global__ void __launch_bounds__(kNormBlock) k_rms_fwd_long(const RmsFwdArgs a) {
     pdl_entry();
     __shared__ float buf[2 * kNormBlock / 32];
     int phase = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    constexpr int kLanes = kQBlock / VEC < 32 ? kQBlock / VEC : 32;  // that share a scale
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T *x = static_cast<const T*>(a.x) + row * a.x_stride, *r = a.r ? static_cast<const T*>(a.r) + row * a.r_stride : nullptr;
-        T* h = a.r ? static_cast<T*>(a.h) + row * a.h_stride : nullptr;
-        float s[1] = {0.f};
-        for (int c0 = warp * kQBlock; c0 < a.cols; c0 += kNormBlock / 32 * kQBlock)
+        const T *x = static_cast<const T*>(a.x) + row * a.x_stride, *r = static_cast<const T*>(a.r) + (RES ? row * a.r_stride : 0);
+        T* h = static_cast<T*>(a.h) + (RES ? row * a.h_stride : 0);
+        Pack<T, VEC> p[kLongLoads], add[RES ? kLongLoads : 1];
+        float s[1] = {0.f}, f[VEC];
+        for (int c0 = 0; c0 < a.cols; c0 += kLongTurn<VEC>) {
+            load_long<T, VEC>(p, x, c0, a.cols);
+            if constexpr (RES) load_long<T, VEC>(add, r, c0, a.cols);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + j * 32 + lane;
+            for (int j = 0; j < kLongLoads; ++j) {
+                const int c = long_at<VEC>(c0, j);
                 if (c >= a.cols) continue;
-                float v = to_float(x[c]);
-                if (r) {
-                    const T sum = from_float<T>(v + to_float(r[c]));
-                    h[c] = sum;
-                    v = to_float(sum);
+                unpack<T, VEC>(p[j], f);
+                if constexpr (RES) {
+                    float g[VEC];
+                    unpack<T, VEC>(add[j], g);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) f[k] += g[k];
+                    p[j] = repack<T, VEC>(f);
+                    *reinterpret_cast<Pack<T, VEC>*>(h + c) = p[j];
+                    unpack<T, VEC>(p[j], f);
                 }
-                s[0] = fmaf(v, v, s[0]);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s[0] = fmaf(f[k], f[k], s[0]);
             }
+        }
         row_sum<kNormBlock>(s, buf, phase);
         const float rstd = 1.f / sqrtf(s[0] / (float)a.cols + a.eps);
         if (threadIdx.x == 0) a.rstd[row] = rstd;
-        const T* from = r ? h : x;
-        for (int c0 = warp * kQBlock; c0 < a.cols; c0 += kNormBlock / 32 * kQBlock) {
-            float y[4];
-            unsigned top = 0;
+        for (int c0 = 0; c0 < a.cols; c0 += kLongTurn<VEC>) {
+            load_long<T, VEC>(p, RES ? h : x, c0, a.cols);
+            // the j-th y, and the largest of its magnitudes
+            auto norm = [&](int j, float (&y)[VEC]) {
+                const int c = long_at<VEC>(c0, j);
+                unsigned top = 0;
+                if (c < a.cols) {
+                    float w[VEC];
+                    load_weights<VEC>(w, a.weight, a.wdtype, c);
+                    unpack<T, VEC>(p[j], y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + j * 32 + lane;
-                y[j] = 0.f;
-                if (c >= a.cols) continue;
-                y[j] = to_float(from[c]) * (rstd * (a.weight ? load_elem(a.weight, c, a.wdtype) : 1.f));
-                top = max(top, magnitude(y[j]));
-            }
-            float scale = 1.f;
-            if (a.q) {
-                scale = block_scale(lanes_max<32>(top));
-                if (lane == 0) a.scale.at(row, c0 / kQBlock) = scale;
-            }
-            const float back = scale_back(scale);
+                    for (int k = 0; k < VEC; ++k) {
+                        y[k] *= rstd * w[k];
+                        top = max(top, magnitude(y[k]));
+                    }
+                }
+                return top;
+            };
+            if (!a.q) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + j * 32 + lane;
-                if (c >= a.cols) continue;
-                if (a.q) a.q[row * a.y_stride + c] = quantize1(y[j], back);
-                else static_cast<T*>(a.y)[row * a.y_stride + c] = from_float<T>(y[j]);
+                for (int j = 0; j < kLongLoads; ++j) {
+                    norm(j, f);
+                    if (long_at<VEC>(c0, j) < a.cols)
+                        *reinterpret_cast<Pack<T, VEC>*>(static_cast<T*>(a.y) + row * a.y_stride + long_at<VEC>(c0, j)) = repack<T, VEC>(f);
+                }
+                continue;
+            }
+            uint8_t* q = a.q + row * a.y_stride;
+            if constexpr (VEC == 1) {  // the four share a scale
+                float y[kLongLoads][1];
+                unsigned top = 0;
+#pragma unroll
+                for (int j = 0; j < kLongLoads; ++j) top = max(top, norm(j, y[j]));
+                const float scale = block_scale(lanes_max<32>(top)), back = scale_back(scale);
+                const int c = long_at<1>(c0, 0);
+                if (threadIdx.x % 32 == 0 && c < a.cols) a.scale.at(row, c / kQBlock) = scale;
+#pragma unroll
+                for (int j = 0; j < kLongLoads; ++j)
+                    if (c + 32 * j < a.cols) q[c + 32 * j] = quantize1(y[j][0], back);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kLongLoads; ++j) {  // all lanes take part in the shuffles
+                    const int c = long_at<VEC>(c0, j);
+                    const float scale = block_scale(lanes_max<kLanes>(norm(j, f))), back = scale_back(scale);
+                    if (c >= a.cols) continue;
+                    if (threadIdx.x % kLanes == 0) a.scale.at(row, c / kQBlock) = scale;
+                    Pack<uint32_t, VEC / 4> out;
+#pragma unroll
+                    for (int k = 0; k < VEC; k += 4) out.v[k / 4] = quantize4(f[k], f[k + 1], f[k + 2], f[k + 3], back);
+                    *reinterpret_cast<Pack<uint32_t, VEC / 4>*>(q + c) = out;
+                }
             }
         }
     }
@@ -267,23 +303,32 @@ cudaError_t run(const RmsFwdArgs& a, cudaStream_t st) {
     });
 }
 
+template <class T, int VEC, bool RES>
+cudaError_t run_long(const RmsFwdArgs& a, cudaStream_t st) {
+    static std::atomic<int> cache[256] = {};
+    auto* kernel = k_rms_fwd_long<T, VEC, RES>;
+    const int most = resident_blocks(kernel, kNormBlock, 0, cache);
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
+}
+
+template <class T, int VEC>
+cudaError_t run_vec(const RmsFwdArgs& a, cudaStream_t st) {
+    if (a.cols > kNormMaxCols) return a.r ? run_long<T, VEC, true>(a, st) : run_long<T, VEC, false>(a, st);
+    return a.r ? run<T, VEC, true>(a, st) : run<T, VEC, false>(a, st);
+}
+
 template <class T>
 cudaError_t run_typed(const RmsFwdArgs& a, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    if (a.cols > kNormMaxCols) {
-        static std::atomic<int> cache[256] = {};
-        const int most = resident_blocks(k_rms_fwd_long<T>, kNormBlock, 0, cache);
-        count_launches(1);
-        return launch_pdl(k_rms_fwd_long<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
-    }
     // 16-byte accesses (8-bit results: as many elements at a time) when every row starts and ends on a whole one
     auto fine = [](const void* p, long long stride, int elems, int bytes) {
         return !p || (stride % elems == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0);
     };
     const bool vec = a.cols % V == 0 && fine(a.x, a.x_stride, V, 16) && fine(a.r, a.r_stride, V, 16) &&
-                     (!a.r || fine(a.h, a.h_stride, V, 16)) && fine(a.y, a.y_stride, V, 16) && fine(a.q, a.y_stride, V, V);
-    if (a.r) return vec ? run<T, V, true>(a, st) : run<T, 1, true>(a, st);
-    return vec ? run<T, V, false>(a, st) : run<T, 1, false>(a, st);
+                     (!a.r || fine(a.h, a.h_stride, V, 16)) && fine(a.y, a.y_stride, V, 16) && fine(a.q, a.y_stride, V, V) &&
+                     (a.cols <= kNormMaxCols || fine(a.weight, 0, 1, 16));
+    return vec ? run_vec<T, V>(a, st) : run_vec<T, 1>(a, st);
 }
 
 }  // namespace

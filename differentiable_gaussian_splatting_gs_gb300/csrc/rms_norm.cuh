@@ -23,4 +23,41 @@ __device__ __forceinline__ void load_vecs(Pack<T, VEC> (&raw)[NV], const T* row,
     }
 }
 
+// Rows of more than kNormMaxCols elements belong to a block, which takes kLongTurn columns of VEC x 4 to a thread at a time and
+// has the four loads under way together. Where the j-th of them lies, from the turn's first column on: 128 consecutive elements
+// to neighbouring lanes of one warp, either way.
+constexpr int kLongLoads = 4;
+template <int VEC>
+constexpr int kLongTurn = kNormBlock * kLongLoads * VEC;
+template <int VEC>
+__device__ __forceinline__ int long_at(int c0, int j) {
+    const int t = threadIdx.x;
+    return VEC == 1 ? c0 + (t / 32) * kQBlock + j * 32 + t % 32 : c0 + (j * kNormBlock + t) * VEC;
+}
+template <class T, int VEC>
+__device__ __forceinline__ void load_long(Pack<T, VEC> (&p)[kLongLoads], const T* row, int c0, int cols) {
+#pragma unroll
+    for (int j = 0; j < kLongLoads; ++j)
+        if (long_at<VEC>(c0, j) < cols) p[j] = *reinterpret_cast<const Pack<T, VEC>*>(row + long_at<VEC>(c0, j));
+}
+// VEC weights from column c on (VEC > 1: they lie on 16 bytes), 1 without.
+template <int VEC>
+__device__ __forceinline__ void load_weights(float (&w)[VEC], const void* weight, int dtype, int c) {
+    if (!weight) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) w[k] = 1.f;
+    } else if constexpr (VEC == 1) {
+        w[0] = load_elem(weight, c, dtype);
+    } else if (dtype == GS_DTYPE_F32) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(weight) + c + k);
+            w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
+        }
+    } else if constexpr (VEC == 8) {
+        if (dtype == GS_DTYPE_F16) unpack<__half, 8>(*reinterpret_cast<const Pack<__half, 8>*>(static_cast<const __half*>(weight) + c), w);
+        else unpack<__nv_bfloat16, 8>(*reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(static_cast<const __nv_bfloat16*>(weight) + c), w);
+    }
+}
+
 }  // namespace gs

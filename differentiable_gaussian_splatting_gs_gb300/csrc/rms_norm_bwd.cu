@@ -6,6 +6,8 @@
 // Bound by memory: h, dy and dh are read once, dx is written once. As the layer norm's backward: a row's elements and the
 // thread's columns of dw stay in registers, the grid is persistent, a block leaves its sums in the workspace and a
 // second kernel adds the blocks', all in a fixed order; rows of more than a vector per thread come through the ring.
+#include <algorithm>
+
 #include "rms_norm.cuh"
 
 namespace gs {
@@ -168,40 +170,78 @@ __global__ void __launch_bounds__(kNormBlock, NV * VEC >= 12 && NV * VEC <= 16 ?
 }
 
 // Rows of more than kNormMaxCols elements: a block per row for dx, which reads the row twice.
-template <class T>
+template <class T, int VEC, bool DH>
 __global__ void __launch_bounds__(kNormBlock) k_rms_bwd_long(const RmsBwdArgs a) {
     pdl_entry();
     __shared__ float buf[2 * kNormBlock / 32];
     int phase = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *h = static_cast<const T*>(a.h) + row * a.h_stride, *dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.dh_stride : nullptr;
+        const T* dh = static_cast<const T*>(a.dh) + (DH ? row * a.dh_stride : 0);
         T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
         const float rstd = a.rstd[row];
-        float s[1] = {0.f};
-        for (int c = threadIdx.x; c < a.cols; c += kNormBlock)
-            s[0] = fmaf(to_float(dy[c]) * (a.weight ? load_elem(a.weight, c, a.wdtype) : 1.f), to_float(h[c]) * rstd, s[0]);
+        Pack<T, VEC> ph[kLongLoads], pd[kLongLoads], pe[DH ? kLongLoads : 1];
+        float s[1] = {0.f}, u[VEC], v[VEC], w[VEC];
+        for (int c0 = 0; c0 < a.cols; c0 += kLongTurn<VEC>) {
+            load_long<T, VEC>(ph, h, c0, a.cols);
+            load_long<T, VEC>(pd, dy, c0, a.cols);
+#pragma unroll
+            for (int j = 0; j < kLongLoads; ++j) {
+                if (long_at<VEC>(c0, j) >= a.cols) continue;
+                load_weights<VEC>(w, a.weight, a.wdtype, long_at<VEC>(c0, j));
+                unpack<T, VEC>(ph[j], u);
+                unpack<T, VEC>(pd[j], v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s[0] = fmaf(v[k] * w[k], u[k] * rstd, s[0]);
+            }
+        }
         row_sum<kNormBlock>(s, buf, phase);
         const float m = s[0] / (float)a.cols;
-        for (int c = threadIdx.x; c < a.cols; c += kNormBlock) {
-            const float g = to_float(dy[c]) * (a.weight ? load_elem(a.weight, c, a.wdtype) : 1.f);
-            dx[c] = from_float<T>(fmaf(rstd, g - to_float(h[c]) * rstd * m, dh ? to_float(dh[c]) : 0.f));
+        for (int c0 = 0; c0 < a.cols; c0 += kLongTurn<VEC>) {
+            load_long<T, VEC>(ph, h, c0, a.cols);
+            load_long<T, VEC>(pd, dy, c0, a.cols);
+            if constexpr (DH) load_long<T, VEC>(pe, dh, c0, a.cols);
+#pragma unroll
+            for (int j = 0; j < kLongLoads; ++j) {
+                const int c = long_at<VEC>(c0, j);
+                if (c >= a.cols) continue;
+                float e[VEC];
+                load_weights<VEC>(w, a.weight, a.wdtype, c);
+                unpack<T, VEC>(ph[j], u);
+                unpack<T, VEC>(pd[j], v);
+                if constexpr (DH) unpack<T, VEC>(pe[j], e);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = fmaf(rstd, v[k] * w[k] - u[k] * rstd * m, DH ? e[k] : 0.f);
+                *reinterpret_cast<Pack<T, VEC>*>(dx + c) = repack<T, VEC>(v);
+            }
         }
     }
 }
 
-// ... and, before it, dw of such rows: a thread per column over the block's share of the rows.
-template <class T>
+// ... and, before it, dw of such rows: VEC columns to a thread over the block's share of the rows.
+template <class T, int VEC>
 __global__ void __launch_bounds__(kNormBlock) k_rms_bwd_long_cols(const RmsBwdArgs a) {
     pdl_entry();
-    const int c = blockIdx.x * kNormBlock + threadIdx.x;
+    const int c = (blockIdx.x * kNormBlock + threadIdx.x) * VEC;
     if (c >= a.cols) return;
     const long long per = (a.rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * per;
     const long long r1 = r0 + per < a.rows ? r0 + per : a.rows;
     const T *h = static_cast<const T*>(a.h) + c, *dy = static_cast<const T*>(a.dy) + c;
-    float dw = 0.f;
-    for (long long r = r0; r < r1; ++r) dw = fmaf(to_float(dy[r * a.dy_stride]), to_float(h[r * a.h_stride]) * a.rstd[r], dw);
-    a.part[(size_t)blockIdx.y * a.cols + c] = dw;
+    float dw[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) dw[k] = 0.f;
+#pragma unroll 4
+    for (long long r = r0; r < r1; ++r) {
+        const float rstd = a.rstd[r];
+        float u[VEC], v[VEC];
+        unpack<T, VEC>(*reinterpret_cast<const Pack<T, VEC>*>(h + r * a.h_stride), u);
+        unpack<T, VEC>(*reinterpret_cast<const Pack<T, VEC>*>(dy + r * a.dy_stride), v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) dw[k] = fmaf(v[k], u[k] * rstd, dw[k]);
+    }
+    float* part = a.part + (size_t)blockIdx.y * a.cols + c;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) part[k] = dw[k];
 }
 
 // dw = the sum of the blocks' shares: 32 columns to a block, whose 32 warps take the shares in turn, in order.
@@ -255,25 +295,36 @@ cudaError_t run(const RmsBwdArgs& a, int* blocks, cudaStream_t st) {
     });
 }
 
+template <class T, int VEC, bool DH>
+cudaError_t run_long(const RmsBwdArgs& a, int* blocks, cudaStream_t st) {
+    if (a.part) {  // first: dx may overwrite dy or h
+        const int across = (int)((a.cols + (long long)kNormBlock * VEC - 1) / (kNormBlock * VEC));
+        const long long up = 8 * device_sm_count() / across;  // two thousand threads to an SM
+        *blocks = (int)std::min(shares(a.rows), up > 64 ? up : 64);
+        count_launches(1);
+        const cudaError_t e = launch_pdl(k_rms_bwd_long_cols<T, VEC>, dim3(across, *blocks), dim3(kNormBlock), 0, st, a);
+        if (e) return e;
+    }
+    static std::atomic<int> cache[256] = {};
+    auto* kernel = k_rms_bwd_long<T, VEC, DH>;
+    const int most = resident_blocks(kernel, kNormBlock, 0, cache);
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
+}
+
+template <class T, int VEC>
+cudaError_t run_vec(const RmsBwdArgs& a, int* blocks, cudaStream_t st) {
+    if (a.cols > kNormMaxCols) return a.dh ? run_long<T, VEC, true>(a, blocks, st) : run_long<T, VEC, false>(a, blocks, st);
+    return a.dh ? run<T, VEC, true>(a, blocks, st) : run<T, VEC, false>(a, blocks, st);
+}
+
 template <class T>
 cudaError_t run_typed(const RmsBwdArgs& a, int* blocks, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    if (a.cols > kNormMaxCols) {
-        if (a.part) {  // first: dx may overwrite dy or h
-            *blocks = (int)(shares(a.rows) < 64 ? shares(a.rows) : 64);
-            count_launches(1);
-            const cudaError_t e = launch_pdl(k_rms_bwd_long_cols<T>, dim3((a.cols + kNormBlock - 1) / kNormBlock, *blocks), dim3(kNormBlock), 0, st, a);
-            if (e) return e;
-        }
-        static std::atomic<int> cache[256] = {};
-        const int most = resident_blocks(k_rms_bwd_long<T>, kNormBlock, 0, cache);
-        count_launches(1);
-        return launch_pdl(k_rms_bwd_long<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kNormBlock), 0, st, a);
-    }
     auto fine = [](const void* p, long long stride) { return !p || (stride % V == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0); };
-    const bool vec = a.cols % V == 0 && fine(a.h, a.h_stride) && fine(a.dy, a.dy_stride) && fine(a.dx, a.dx_stride) && fine(a.dh, a.dh_stride);
-    if (a.dh) return vec ? run<T, V, true>(a, blocks, st) : run<T, 1, true>(a, blocks, st);
-    return vec ? run<T, V, false>(a, blocks, st) : run<T, 1, false>(a, blocks, st);
+    const bool vec = a.cols % V == 0 && fine(a.h, a.h_stride) && fine(a.dy, a.dy_stride) && fine(a.dx, a.dx_stride) && fine(a.dh, a.dh_stride) &&
+                     (a.cols <= kNormMaxCols || fine(a.weight, 0));
+    return vec ? run_vec<T, V>(a, blocks, st) : run_vec<T, 1>(a, blocks, st);
 }
 
 }  // namespace

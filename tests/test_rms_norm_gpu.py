@@ -253,3 +253,34 @@ def test_refusals():
         api.gs_rms_norm_fwd(x, None, x.clone(), out=(y := torch.empty_like(x), y, v))
     with pytest.raises(_abi.GsError, match="aligned"):
         api.gs_rms_norm_fp8(x, out=(torch.zeros(4, 48, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)[:, 8:], s, None, v))
+
+
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("cols", [8200, 9992, 16384, 16385, 24600])
+def test_rows_longer_than_a_blocks_registers(dtype, cols):
+    rows = 6
+    x, r, dy, dh = (_rand((rows, cols), dtype, cols + i, 1.5, 0.2) for i in range(4))
+    wide = _rand((cols + 8,), dtype, 9, 0.3, 1.0)
+    for w in (wide[:cols], wide[1:cols + 1], wide[:cols].float(), None):  # on 16 bytes, not, float32, none
+        _check_fwd(x, w, r)
+        _check_fp8(x, w, r)
+        _check_fp8(x, w, None)
+        _check_bwd(dy, _sum(x, r), w, dh)
+        _check_bwd(dy, x, w, None)
+    # rows apart that start on 16 bytes, or do not; results over the inputs
+    for start, apart in ((0, cols + 8 - cols % 8), (1, cols + 1)):
+        room = torch.full((3, rows * apart + 8), 7.0, device=DEV, dtype=dtype)
+        a, b, c = (room[i, start:start + rows * apart].view(rows, apart)[:, :cols] for i in range(3))
+        a.copy_(x), b.copy_(r)
+        want = api.gs_rms_norm_fwd(x, wide[:cols], r, eps=EPS)
+        y, h, _ = api.gs_rms_norm_fwd(a, wide[:cols], b, eps=EPS, out=(b, a, torch.empty(rows, device=DEV)))
+        assert torch.equal(h, want[1]) and y.data_ptr() == b.data_ptr()
+        assert ((y.double() - want[0].double()).abs() <= 2 * U[dtype] * want[0].double().abs() + 2.0 ** -18 * want[0].double().abs() + TINY[dtype] * 2).all()
+        c.copy_(dy)
+        one = api.gs_rms_norm_bwd(dy, want[1], want[2], wide[:cols], dh)
+        two = api.gs_rms_norm_bwd(c, a, want[2], wide[:cols], dh, out=(c, torch.empty_like(wide[:cols])))
+        near = one[0].double().abs() * 2 * U[dtype] + 2.0 ** -16 * (dy.double().abs() + dh.double().abs() + 1) * (1 + want[2].double().max())
+        assert ((two[0].double() - one[0].double()).abs() <= near).all()
+        for i in range(2):
+            rest = room[i, start:start + rows * apart].view(rows, apart)[:, cols:]
+            assert (rest == 7).all() and (room[i, :start] == 7).all()
