@@ -18,6 +18,15 @@
 // 512 cycles of products (750 cycles' worth), a pair's moves 64 KB.
 // Where tiles are few, a cluster of up to 8 blocks shares the inner dimension of one, joined through their shared
 // memory in a fixed order.
+//
+// Bound by the elementwise warps: a block of 256 x 256 x 128 takes its SMs 512 cycles of products and some 900 of additions (1,380
+// where scales differ by column): half of these wait for tensor memory and for one another, each packed multiply-add adds three
+// (the registers' ports; scalar ones four). 16384 x 4096 x 4096 bfloat16 takes 205 us (2.7 PFLOP/s, 70% of twice the measured bf16
+// rate), 17384 x 4096 x 1024 74 us, 4096 x 1024 x 17,384 with scales by column 98 us; few rows are bound by b's bytes and a
+// launch's latency (1 x 4096 x 1024 4.8 us, 16 x 8192 x 4096 8.3 us, 4.1 TB/s). Sixteen warps of 64 columns instead of eight of
+// 128 (234 us), the next block's values asked for before the last of this one are added (240 us), products of 128 columns with
+// four accumulators and tiles of 256 x 160 with three (298 us) were slower; so were, with scales by column, loads that give a
+// thread two columns of each eight, which read a quarter of the scales (104 to 107 us against 98).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -161,7 +170,7 @@ struct MmShape {
 
 // Scales of so many blocks of the inner dimension are copied at a time, to so many places: 8 to 12 blocks ahead of their use.
 // (Loaded into registers two blocks ahead, their latency under the tiles' traffic decided the pace of 256 x 256 tiles: 16384 x 4096
-// x 4096 bf16 took 707 us.)
+// x 4096 bf16 took 707 us where it took 220 so.)
 constexpr int kMmBatch = 4, kMmPlaces = 3;
 template <int TN, bool COLS>
 struct MmScales {
@@ -184,7 +193,7 @@ __device__ __forceinline__ void tile_store2(const CUtensorMap* map, int c0, int 
 // A warp's 32 rows of a tile, COLS columns of them in every thread's sums, the first at (q0, p0) of the result. Where its rows lie
 // on 16 bytes: by tiled copies of 128 bytes of each row, laid out (with the copies' swizzle) in BOXES times 4 KB of the warp's, which
 // the warp leaves under way. (Until they are stored the products can only go two blocks ahead. Stored by each thread from its
-// row a tile of 256 x 256 took 2.2 us, coalesced through 2 KB of shared memory 1.9 us.) Else element by element.
+// row a tile of 256 x 256 took 2.2 us, coalesced through 2 KB of shared memory 1.9 us, so 1.2.) Else element by element.
 template <int COLS, int BOXES>
 __device__ __forceinline__ void store_rows(const MmArgs& a, const f32x2 (&acc)[COLS / 2], unsigned char* stage, int p0, int q0) {
     const int lane = threadIdx.x & 31, rows = a.np - p0, left = a.nq - q0;
@@ -401,8 +410,8 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
             for (int k = k0; k < k1 && ok; k += kMmBatch) {
                 if (!(ok = warp_wait(scaled + at, at_phase, a.limit, a.err) && (!kAlone || __all_sync(0xffffffffu, mine)))) break;
-                // (unrolled, with the batch's scales of the rows in registers: 98 instead of 107 us for 4096 x 1024 x 17,384 with scales by column,
-                // whose turns wait for shared memory, but 236 instead of 223 for 16384 x 4096 x 4096 without, for want of registers)
+                // (unrolled, with the batch's scales of the rows in registers: 98 instead of 101 us for 4096 x 1024 x 17,384 with scales by column,
+                // but 307 instead of 205 for 16384 x 4096 x 4096 without, for want of registers)
                 float4 of_p = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (COLS) of_p = *reinterpret_cast<const float4*>(scales.p[at][row]);
                 const float each[kMmBatch] = {of_p.x, of_p.y, of_p.z, of_p.w};
@@ -413,8 +422,8 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                     if constexpr (COLS) scale = each[j];
                     else scale = scales.p[at][row][j] * scales.q[at][c0 / kQBlock * kMmBatch + j];
                     const f32x2 scale2 = f2_pack(scale, scale);
-                    // (kAlone: each lane waits for itself, 217 -> 205 us for 16384 x 4096 x 4096: a lane that gave up goes on with its warp to the next
-                    // batch, where all learn of it)
+                    // (kAlone: each lane waits for itself, 205 us instead of 219 for 16384 x 4096 x 4096, with 64 columns loaded at a time: a lane that gave
+                    // up goes on with its warp to the next batch, where all learn of it)
                     if constexpr (kAlone) {
                         mine &= __builtin_expect(mbar_try_wait(done + b, b_phase), 1) || mbar_wait_bounded(done + b, b_phase, a.limit, a.err);
                         __syncwarp();
