@@ -16,6 +16,7 @@ __device__ __forceinline__ int vec_at(int l, int i) {
 
 template <class T, int VEC, int NV, int LPR, int FULL>
 __device__ __forceinline__ void load_vecs(Pack<T, VEC> (&raw)[NV], const T* row, int l, int nvec, bool live) {
+    static_assert(VEC > 1 || NV % 4 != 0 || LPR <= 32 || FULL % 4 == 0, "a row's first FULL vectors are whole turns of four");
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = vec_at<VEC, NV, LPR>(l, i);
