@@ -3,7 +3,7 @@
 // Bound by memory: x is read once and a byte written for each element. Two forms, by the direction in which x is contiguous:
 // along its rows, as activations and weights are, or down its columns (the transpose of such a tensor, whose scales then
 // run along what were its rows: the operands of a weight's gradient). Both hold a block's elements in registers between the
-// maximum and the rounding. 17,384 x 4096 bfloat16 takes 45 us (4.7 TB/s, 70% of the measured copy rate), 4096 x 17,384 transposed
+// maximum and the rounding. 17,384 x 4096 bfloat16 takes 33 us (6.4 TB/s, 94% of the measured copy rate), 4096 x 17,384 transposed
 // 42 us (5.1 TB/s), 4096 x 1024 float32 by 128 x 128 3.5 us; rows that do not lie on 16 bytes 47 us (4,097 x 17,383 bfloat16,
 // transposed 61).
 #include "elem.cuh"
@@ -19,6 +19,7 @@ struct QuantArgs {
     ScaleAt scale;
     long long rows, x_stride, q_stride;  // x_stride: of rows, or of columns where these are contiguous
     int cols;
+    int beside;  // log2 of the warps of a block of threads that lie along the columns, where each has rows of its own
 };
 
 constexpr int kQuantBlock = 256;  // threads
@@ -53,23 +54,26 @@ __device__ __forceinline__ unsigned halves_top(const uint32_t (&w)[N]) {
 }
 
 // Rows, each block of 128 columns by neighbouring lanes with VEC elements in 16 bytes: a half warp (16-bit types) or a warp. A warp
-// has kRows rows, whose loads are all under way together. BLOCK: 128 rows, a block of threads', share a scale. (Elements
-// unpacked before the comparison, 8 bytes to a lane, a division for each row: 17,384 x 4096 bfloat16 75 us, so 45.)
-template <class T>
+// has kRows rows, whose kLoads loads are all under way together. BLOCK: 128 rows, a block of threads', share a scale. (17,384 x 4096
+// bfloat16: elements unpacked before the comparison, 8 bytes to a lane, a division for each row 75 us; 8 loads in 99 registers 45; 4
+// loads and 6 blocks of threads on an SM 33. With scales for 128 x 128 those registers are needed: 40, float32 58 with 8 loads and 72
+// with 4.)
+template <class T, bool BLOCK>
 struct QuantRows {
-    static constexpr int kVec = 16 / (int)sizeof(T), kLanes = kQBlock / kVec, kLoads = 8, kBeside = 32 / kLanes, kRows = kLoads * kBeside;
+    static constexpr int kVec = 16 / (int)sizeof(T), kLanes = kQBlock / kVec, kLoads = BLOCK && sizeof(T) == 4 ? 8 : 4, kBeside = 32 / kLanes, kRows = kLoads * kBeside;
 };
 template <class T, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kQBlock / QuantRows<T>::kRows * 32 : kQuantBlock) k_quantize_rows(const QuantArgs a) {
-    using R = QuantRows<T>;
+__global__ void __launch_bounds__(BLOCK ? kQBlock / QuantRows<T, BLOCK>::kRows * 32 : kQuantBlock, !BLOCK && sizeof(T) == 2 ? 6 : 0) k_quantize_rows(const QuantArgs a) {
+    using R = QuantRows<T, BLOCK>;
     constexpr int kWarps = BLOCK ? kQBlock / R::kRows : kQuantBlock / 32;
     pdl_entry();
     __shared__ unsigned tops[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l = lane % R::kLanes, beside = lane / R::kLanes;
     const int blocks = (a.cols + kQBlock - 1) / kQBlock;
-    // a block's warps take neighbouring columns of the same rows, or the rows of one block
-    const long long row0 = (BLOCK ? (long long)blockIdx.x * kQBlock + warp * R::kRows : (long long)blockIdx.x * R::kRows) + beside;
-    for (int block = BLOCK ? blockIdx.y : blockIdx.y * kWarps + warp; block < blocks; block += BLOCK ? gridDim.y : gridDim.y * kWarps) {
+    // a block's warps take neighbouring columns of the same rows (few columns: the next rows'), or the rows of one block
+    const int across = BLOCK ? 1 : 1 << a.beside, up = BLOCK ? warp : warp >> a.beside;
+    const long long row0 = (BLOCK ? (long long)blockIdx.x * kQBlock : (long long)blockIdx.x * (kWarps >> a.beside) * R::kRows) + up * R::kRows + beside;
+    for (int block = blockIdx.y * across + (BLOCK ? 0 : warp & (across - 1)); block < blocks; block += gridDim.y * across) {
         const int c = block * kQBlock + l * R::kVec;
         const bool in = c < a.cols;
         const T* x = static_cast<const T*>(a.x) + row0 * a.x_stride + c;
@@ -120,8 +124,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kQuantBlock) k_quantize_rows_odd
     __shared__ unsigned tops[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, blocks = (a.cols + kQBlock - 1) / kQBlock;
     constexpr int kWarps = kQuantBlock / 32;
-    for (int block = BLOCK ? blockIdx.y : blockIdx.y * kWarps + warp; block < blocks; block += BLOCK ? gridDim.y : gridDim.y * kWarps) {
-        const long long row0 = BLOCK ? (long long)blockIdx.x * kQBlock + warp * kQuantRows : (long long)blockIdx.x * kQuantRows;
+    const int across = BLOCK ? 1 : 1 << a.beside, up = BLOCK ? warp : warp >> a.beside;
+    const long long row0 = (BLOCK ? (long long)blockIdx.x * kQBlock : (long long)blockIdx.x * (kWarps >> a.beside) * kQuantRows) + up * kQuantRows;
+    for (int block = blockIdx.y * across + (BLOCK ? 0 : warp & (across - 1)); block < blocks; block += gridDim.y * across) {
         const int c = block * kQBlock + lane;
         const T* x = static_cast<const T*>(a.x) + row0 * a.x_stride + c;
         T v[kQuantRows][4];
@@ -269,7 +274,7 @@ cudaError_t go(void (*kernel)(const QuantArgs), long long up, long long across, 
 }
 
 template <class T>
-cudaError_t run(const QuantArgs& a, bool by_cols, bool block, cudaStream_t st) {
+cudaError_t run(QuantArgs a, bool by_cols, bool block, cudaStream_t st) {
     auto over = [](long long n, long long m) { return (n + m - 1) / m; };
     const long long across = over(a.cols, kQBlock), tiles = over(a.rows, kQBlock);
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.x);
@@ -279,13 +284,15 @@ cudaError_t run(const QuantArgs& a, bool by_cols, bool block, cudaStream_t st) {
                 return go(block ? k_quantize_cols<T, 2, true> : k_quantize_cols<T, 2, false>, tiles, across, 2 * kQBlock, a, st);
         return go(block ? k_quantize_cols<T, 1, true> : k_quantize_cols<T, 1, false>, tiles, across, 4 * kQBlock, a, st);
     }
-    using R = QuantRows<T>;
+    using R = QuantRows<T, false>;
     constexpr int kWarps = kQuantBlock / 32;
+    while (1 << a.beside < across && 1 << a.beside < kWarps) ++a.beside;
+    const long long up = kWarps >> a.beside;  // (139,072 x 100 bfloat16: 19 us with all warps along the columns)
     const bool vec = a.cols % R::kVec == 0 && a.x_stride % R::kVec == 0 && x % 16 == 0;
-    if (vec) return block ? go(k_quantize_rows<T, true>, tiles, across, kQBlock / R::kRows * 32, a, st)
-                          : go(k_quantize_rows<T, false>, over(a.rows, R::kRows), over(across, kWarps), kQuantBlock, a, st);
+    if (vec) return block ? go(k_quantize_rows<T, true>, tiles, across, kQBlock / QuantRows<T, true>::kRows * 32, a, st)
+                          : go(k_quantize_rows<T, false>, over(a.rows, up * R::kRows), over(across, 1 << a.beside), kQuantBlock, a, st);
     return block ? go(k_quantize_rows_odd<T, true>, tiles, across, 512, a, st)
-                 : go(k_quantize_rows_odd<T, false>, over(a.rows, kQuantRows), over(across, kWarps), kQuantBlock, a, st);
+                 : go(k_quantize_rows_odd<T, false>, over(a.rows, up * kQuantRows), over(across, 1 << a.beside), kQuantBlock, a, st);
 }
 
 }  // namespace

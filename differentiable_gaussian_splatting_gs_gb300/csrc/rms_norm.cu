@@ -35,8 +35,15 @@ __device__ __forceinline__ unsigned lanes_max(unsigned m) {
     }
 }
 
+// Blocks of an SM at least (0: as the registers come out), where that was faster: of rows read an element at a time the longest (8000 x
+// 8191 float16 with a residual 153 us, so 134; to 8 bits 202, 155), but for bfloat16 with a residual, which would spill (157 us, and 174
+// so); and, without a residual, those of 12 and 16 to a thread (200,000 x 333 float16 57 us, so 53; with one 107, and 127 with a fourth
+// block).
+template <class T, int VEC, int NV, bool RES>
+constexpr int kRmsBlocks = VEC > 1 ? 0 : NV > 16 ? RES && std::is_same_v<T, __nv_bfloat16> ? 0 : 2 : NV >= 12 && !RES ? 3 : 0;
+
 template <class T, int VEC, int NV, int LPR, int FULL, bool RES>
-__global__ void __launch_bounds__(kNormBlock) k_rms_fwd(const RmsFwdArgs a) {
+__global__ void __launch_bounds__(kNormBlock, kRmsBlocks<T, VEC, NV, RES>) k_rms_fwd(const RmsFwdArgs a) {
     pdl_entry();
     extern __shared__ __align__(16) float weights[];
     __shared__ float buf[2 * kNormBlock / 32];

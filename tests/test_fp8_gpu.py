@@ -60,6 +60,16 @@ def test_quantize(rows, cols, dtype, block, transposed):
     _check_quantize(x, block)
 
 
+@pytest.mark.parametrize("dtype", list(U))
+@pytest.mark.parametrize("cols", [1, 96, 100, 128, 129, 200, 256, 257, 384, 500, 512, 520, 1024, 1032])
+def test_quantize_few_columns(cols, dtype):
+    for rows in (1, 5, 31, 33, 1000):  # warps beside one another, or below
+        room = torch.full((rows + 1, (cols + 15) // 16 * 16 + 16), 0x55, dtype=torch.uint8, device=DEV)
+        scales = torch.full((rows + 2, -(-cols // 128)), 3.0, device=DEV)
+        _check_quantize(_rand((rows, cols), dtype, rows + cols), 1, out=(room[:rows, :cols].view(torch.float8_e4m3fn), scales[1:-1]))
+        assert (room[rows:] == 0x55).all() and (room[:, cols:] == 0x55).all() and (scales[0] == 3).all() and (scales[-1] == 3).all()
+
+
 @pytest.mark.parametrize("block", [1, 128])
 def test_quantize_strides_offsets_and_the_callers_tensors(block):
     base = _rand((300, 400), torch.bfloat16, 3)
