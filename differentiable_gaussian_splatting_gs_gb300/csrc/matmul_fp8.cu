@@ -44,12 +44,14 @@ constexpr int kMmSplits = 8;   // blocks of a cluster that share a tile's inner 
 
 struct MmArgs {
     CUtensorMap p, q, to;
+    const uint8_t *p_data, *q_data;
+    long long p_stride, q_stride;
     const float *p_scale, *q_scale;
     long long p_row, p_block, q_row, q_block;  // strides of the scales
     int p_shift, q_shift;                      // 2^shift rows share a scale
     void* out;
     long long out_p, out_q;  // strides of the result, one of them 1
-    int dtype, wide, boxes, np, nq, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes; boxes: columns that `to` has
+    int dtype, wide, boxes, np, nq, k, blocks, tiles_p, tiles, splits;  // wide: rows of the result lie on 16 bytes; boxes: columns that `to` has
     unsigned limit, *err;
 };
 
@@ -178,6 +180,117 @@ struct MmScales {
     float q[kMmPlaces][COLS ? kMmBatch * TN : (TN + kQBlock - 1) / kQBlock * kMmBatch];  // COLS: [batch][column], else [column / 128][batch]
 };
 
+// ---- scales at the ends of float32's range ----
+// The hot loop multiplies in float32: by the product of both scales, or (COLS) by the column's and then the row's. That holds
+// where the product is a normal number, or a value times the column's scale is (values are 0 or lie between 2^-18, the product of
+// two subnormals, and 128 x 448^2 < 2^25). The warps that copy the scales, which have the time, note the smallest and the largest;
+// a block whose scales can leave that range looks at its tiles again when they are stored, and forms the elements that have such
+// scales once more, in double precision. (The test and the other form within the hot loop took a quarter to a half of its time,
+// 16384 x 4096 x 4096 bf16 265 us instead of 210, whatever the scales.)
+struct ScaleRange {
+    unsigned least, most;  // magnitudes; the least less one, so that 0 counts as the largest; the most without infinities and NaN
+    __device__ __forceinline__ void add(float s) {
+        const unsigned m = magnitude(s);
+        least = min(least, m - 1);
+        if (m < 0x7f800000u) most = max(most, m);
+    }
+};
+constexpr float kLeastColumn = 0x1p-108f, kMostColumn = 0x1p102f;
+__device__ __forceinline__ bool leaves_range(float row, float column, bool cols) {
+    const float s = fabsf(cols ? column : row * column);
+    const bool in = cols ? s >= kLeastColumn && s <= kMostColumn : s >= 0x1p-126f && s < INFINITY;
+    return !in && row != 0.f && column != 0.f && isfinite(row) && isfinite(column);
+}
+// Whether any of the block's scales may.
+__device__ __forceinline__ bool may_leave_range(const ScaleRange& p, const ScaleRange& q, bool cols) {
+    return leaves_range(__uint_as_float(p.least + 1), __uint_as_float(q.least + 1), cols) ||
+           leaves_range(__uint_as_float(p.most), __uint_as_float(q.most), cols);
+}
+
+// Sum of the products of 16 e4m3 values.
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t u, v;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"((uint16_t)(x[i] >> 16 * h)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"((uint16_t)(y[i] >> 16 * h)));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u)), g = __half22float2(*reinterpret_cast<const __half2*>(&v));
+            s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+        }
+    return s;
+}
+// The warp's rows of a tile of `rows` x `cols` at (p0, q0) once more, where a scale leaves the range in a block of the inner dimension
+// of k0 .. k1 first (the blocks of a cluster share a tile's). A warp forms an element, 16 bytes of the inner dimension to a lane.
+__device__ __forceinline__ void form_again(const MmArgs& a, int p0, int rows, int q0, int cols, int k0, int k1, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    const bool by_col = a.q_shift == 0;
+    rows = min(rows, a.np - p0);
+    cols = min(cols, a.nq - q0);
+    for (int r = warp; r < rows; r += warps) {
+        const int p = p0 + r;
+        const float* sp = a.p_scale + (long long)(p >> a.p_shift) * a.p_row;
+        for (int c = 0, next; c < cols; c = next) {  // columns that share their scales
+            next = min(cols, (((q0 + c) >> a.q_shift) + 1 << a.q_shift) - q0);
+            const float* sq = a.q_scale + (long long)((q0 + c) >> a.q_shift) * a.q_row;
+            unsigned first = ~0u;
+            for (int k = lane; k < a.blocks && first == ~0u; k += 32)
+                if (leaves_range(sp[k * a.p_block], sq[k * a.q_block], by_col)) first = k;
+            first = __reduce_min_sync(0xffffffffu, first);
+            if (first < (unsigned)k0 || first >= (unsigned)k1) continue;
+            for (int q = q0 + c; q < q0 + next; ++q) {
+                const uint8_t *x = a.p_data + p * a.p_stride, *y = a.q_data + q * a.q_stride;
+                double sum = 0.0;
+                for (int at = lane * 16; at - lane * 16 < a.k; at += 512) {
+                    uint4 u = {}, v = {};
+                    if (at + 16 <= a.k) {
+                        u = *reinterpret_cast<const uint4*>(x + at);
+                        v = *reinterpret_cast<const uint4*>(y + at);
+                    } else {
+                        uint32_t w[8] = {};
+                        for (int i = 0; i < 16; ++i)
+                            if (at + i < a.k) {
+                                w[i / 4] |= (uint32_t)x[at + i] << 8 * (i % 4);
+                                w[4 + i / 4] |= (uint32_t)y[at + i] << 8 * (i % 4);
+                            }
+                        u = make_uint4(w[0], w[1], w[2], w[3]);
+                        v = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                    float block = dot16(u, v);  // of eight lanes
+#pragma unroll
+                    for (int o = 1; o < kMmBlock / 16; o *= 2) block += __shfl_xor_sync(0xffffffffu, block, o);
+                    const int k = at / kMmBlock;
+                    if (lane % (kMmBlock / 16) == 0 && k < a.blocks) sum = fma((double)sp[k * a.p_block] * (double)sq[k * a.q_block], (double)block, sum);
+                }
+#pragma unroll
+                for (int o = 16; o >= kMmBlock / 16; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) store_elem(a.out, p * a.out_p + q * a.out_q, a.dtype, (float)sum);
+            }
+        }
+    }
+}
+
+// ... all of the block's tiles, by `warps` of its warps, this the `warp`-th.
+__device__ __forceinline__ void form_tiles_again(const MmArgs& a, int tn, int warp, int warps) {
+    const bool pair = tn == 256;
+    const int group = pair ? 2 : a.splits, rank = blockIdx.x % group;
+    const int k0 = pair ? 0 : (int)((long long)a.blocks * rank / group), k1 = pair ? a.blocks : (int)((long long)a.blocks * (rank + 1) / group);
+    for (int t = blockIdx.x / group; t < a.tiles; t += gridDim.x / group)
+        form_again(a, t % a.tiles_p * (pair ? 2 * kMmRows : kMmRows) + (pair ? rank * kMmRows : 0), kMmRows, t / a.tiles_p * tn, tn, k0, k1, warp, warps);
+}
+// The same apart from the caller's code. (In the pair's kernel, or anywhere but at the end of its elementwise warps' part, it cost their
+// loop, which has no register left, a fifth of its time: 16384 x 4096 x 4096 bf16 247 us.)
+__device__ __noinline__ void call_form_tiles_again(const MmArgs& a, int tn, int warp, int warps) { form_tiles_again(a, tn, warp, warps); }
+
+// Barrier ID of the block, for THREADS threads: its arrivals, and those that wait for them.
+template <int ID, int THREADS>
+__device__ __forceinline__ void named_arrive() { asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory"); }
+template <int ID, int THREADS>
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory"); }
+
 // Counts an arrival of the thread once its asynchronous copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -263,6 +376,7 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
     __shared__ uint32_t tmem_at;
     __shared__ uint64_t scaled[kMmPlaces], used[kMmPlaces];
     __shared__ __align__(16) MmScales<TN, COLS> scales;
+    __shared__ ScaleRange ranges[2];  // of P's scales and of Q's
     const uint32_t tiles = (smem_u32(dynamic) + 1023) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -359,7 +473,25 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             const bool of_q = warp == S::kWarps + 3;
             constexpr int kOfQ = COLS ? (TN + 31) / 32 : 1, kMost = kOfQ > kMmRows / 32 ? kOfQ : kMmRows / 32;
             const long long next = of_q ? a.q_block : a.p_block;
-            int batch = 0;
+            int batch = 0, sizes = 0;  // sizes: of the last three batches, the last one's in the lowest four bits
+            ScaleRange range{~0u, 0u};
+            auto note = [&](int at, int n) {  // what the lane copied to a place, which has landed
+                if (of_q) {
+                    for (int j = 0; j < n; ++j)
+#pragma unroll
+                        for (int i = 0; i < kOfQ; ++i)
+                            if (COLS ? 32 * i + lane < TN : lane * kQBlock < TN) range.add(scales.q[at][COLS ? j * TN + 32 * i + lane : lane * kMmBatch + j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kMmRows / 32; ++i) {
+                        const float4 s = *reinterpret_cast<const float4*>(scales.p[at][32 * i + lane]);
+                        range.add(s.x);
+                        if (n > 1) range.add(s.y);
+                        if (n > 2) range.add(s.z);
+                        if (n > 3) range.add(s.w);
+                    }
+                }
+            };
             bool ok = true;
             for (int t = first; t < a.tiles && ok; t += step) {
                 const int p0 = t % a.tiles_p * kRows + row_of, q0 = t / a.tiles_p * TN;
@@ -372,7 +504,11 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                 }
                 for (int k = k0; k < k1; k += kMmBatch, ++batch) {
                     const int at = batch % kMmPlaces;
-                    if (batch >= kMmPlaces && !(ok = warp_wait(used + at, (batch / kMmPlaces - 1) & 1, a.limit, a.err))) break;
+                    if (batch >= kMmPlaces) {
+                        if (!(ok = warp_wait(used + at, (batch / kMmPlaces - 1) & 1, a.limit, a.err))) break;
+                        note(at, sizes >> 4 * (kMmPlaces - 1) & 15);
+                    }
+                    sizes = sizes << 4 | min(kMmBatch, k1 - k);
 #pragma unroll
                     for (int j = 0; j < kMmBatch; ++j) {
                         if (k + j >= k1) break;
@@ -391,8 +527,12 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                 }
             }
             cp_async_wait_all();
-            __syncwarp();
+            for (int i = 0; i < min(batch, kMmPlaces); ++i) note((batch - 1 - i) % kMmPlaces, sizes >> 4 * i & 15);
+            range.least = __reduce_min_sync(0xffffffffu, range.least);
+            range.most = __reduce_max_sync(0xffffffffu, range.most);
+            if (lane == 0) ranges[of_q] = range;
         }
+        if constexpr (kPair) named_arrive<1, S::kThreads>();  // the ranges are there
     } else {
         if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
         // ---- scales and sums ----
@@ -484,6 +624,10 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
         }
         if (S::template kBoxes<COLS> && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the result is written
         __syncwarp();
+        if constexpr (kPair) {
+            named_sync<1, S::kThreads>();  // all results are stored
+            if (may_leave_range(ranges[0], ranges[1], COLS)) form_tiles_again(a, TN, warp, S::kWarps);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -499,42 +643,44 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             tc_fence_after();
             tmem_free<S::kTmem>(tmem);
         }
-        if (group == 1) return;
-        // The tensor memory is free before blocks wait for one another: a block that waits for some never holds up one that
-        // waits for it.
-        cluster_sync();
-        const float* sums = reinterpret_cast<const float*>(dynamic + (tiles - smem_u32(dynamic)));
-        const int p0 = first % a.tiles_p * kMmRows, q0 = first / a.tiles_p * TN;
-        const bool by_row = a.out_q == 1;  // four elements that lie together in the result to a thread
-        const int lines = by_row ? kMmRows : TN, fours = (by_row ? TN : kMmRows) / 4, pitch = by_row ? TN + 4 : kMmRows;
-        const int l0 = lines * rank / group, l1 = lines * (rank + 1) / group;
-        for (int i = l0 * fours + threadIdx.x; i < l1 * fours; i += S::kThreads) {
-            const int line = i / fours, at = i % fours * 4;
-            const int p = p0 + (by_row ? line : at), q = q0 + (by_row ? at : line), left = by_row ? a.nq - q : a.np - p;
-            if (p >= a.np || q >= a.nq) continue;
-            float4 v[kMmSplits];
+        if (group > 1) {
+            // The tensor memory is free before blocks wait for one another: a block that waits for some never holds up one that
+            // waits for it.
+            cluster_sync();
+            const float* sums = reinterpret_cast<const float*>(dynamic + (tiles - smem_u32(dynamic)));
+            const int p0 = first % a.tiles_p * kMmRows, q0 = first / a.tiles_p * TN;
+            const bool by_row = a.out_q == 1;  // four elements that lie together in the result to a thread
+            const int lines = by_row ? kMmRows : TN, fours = (by_row ? TN : kMmRows) / 4, pitch = by_row ? TN + 4 : kMmRows;
+            const int l0 = lines * rank / group, l1 = lines * (rank + 1) / group;
+            for (int i = l0 * fours + threadIdx.x; i < l1 * fours; i += S::kThreads) {
+                const int line = i / fours, at = i % fours * 4;
+                const int p = p0 + (by_row ? line : at), q = q0 + (by_row ? at : line), left = by_row ? a.nq - q : a.np - p;
+                if (p >= a.np || q >= a.nq) continue;
+                float4 v[kMmSplits];
 #pragma unroll
-            for (int r = 0; r < kMmSplits; ++r)
-                if (r < group) v[r] = peer_floats(sums + line * pitch + at, r);
-            float4 t = v[0];
+                for (int r = 0; r < kMmSplits; ++r)
+                    if (r < group) v[r] = peer_floats(sums + line * pitch + at, r);
+                float4 t = v[0];
 #pragma unroll
-            for (int r = 1; r < kMmSplits; ++r)
-                if (r < group) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
-            const long long to = p * a.out_p + q * a.out_q;
-            if (a.wide && left >= 4) {
-                if (a.dtype == GS_DTYPE_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = t;
-                else if (a.dtype == GS_DTYPE_F16) *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) = make_uint2(pack2<__half>(t.x, t.y), pack2<__half>(t.z, t.w));
-                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) = make_uint2(pack2<__nv_bfloat16>(t.x, t.y), pack2<__nv_bfloat16>(t.z, t.w));
-            } else {
-                const float each[4] = {t.x, t.y, t.z, t.w};
+                for (int r = 1; r < kMmSplits; ++r)
+                    if (r < group) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
+                const long long to = p * a.out_p + q * a.out_q;
+                if (a.wide && left >= 4) {
+                    if (a.dtype == GS_DTYPE_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = t;
+                    else if (a.dtype == GS_DTYPE_F16) *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) = make_uint2(pack2<__half>(t.x, t.y), pack2<__half>(t.z, t.w));
+                    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) = make_uint2(pack2<__nv_bfloat16>(t.x, t.y), pack2<__nv_bfloat16>(t.z, t.w));
+                } else {
+                    const float each[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) store_elem(a.out, to + e, a.dtype, each[e]);
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) store_elem(a.out, to + e, a.dtype, each[e]);
+                }
             }
+            __syncwarp();
+            cluster_sync();  // no block's shared memory goes before the others have read it
         }
-        __syncwarp();
-        cluster_sync();  // no block's shared memory goes before the others have read it
     }
+    if (!kPair && may_leave_range(ranges[0], ranges[1], COLS)) call_form_tiles_again(a, TN, warp, S::kThreads / 32);
 }
 
 namespace {
@@ -638,6 +784,11 @@ cudaError_t launch_matmul_fp8(const MatmulFp8& x, unsigned* err, cudaStream_t st
     a.np = (int)(swap ? x.n : x.m);
     a.nq = (int)(swap ? x.m : x.n);
     a.blocks = (int)((x.k + kMmBlock - 1) / kMmBlock);
+    a.k = (int)x.k;
+    a.p_data = static_cast<const uint8_t*>(p.data);
+    a.q_data = static_cast<const uint8_t*>(q.data);
+    a.p_stride = p.stride;
+    a.q_stride = q.stride;
     a.p_scale = p.scale;
     a.q_scale = q.scale;
     a.p_row = p.scale_row;
