@@ -34,6 +34,7 @@
 #include "elem.cuh"
 #include "fp8.cuh"
 #include "gs_internal.h"
+#include "pair_ring.h"
 #include "tcgen05.cuh"
 
 namespace gs {
@@ -102,6 +103,30 @@ __device__ __forceinline__ void warp_arrive_at(uint32_t bar) {
     __syncwarp();
     if (elect_one()) asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+
+// The second block's copies are all under way: their turns to the first block's shared memory, and an arrival there.
+__device__ __forceinline__ void tell_turns(uint32_t at, uint32_t bar, int turns) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(turns) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+    unsigned ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// What end_copies does to the stages' barriers.
+struct RingEnd {
+    uint64_t* full;
+    unsigned *err, bytes;  // bytes: of one block's half
+    __device__ __forceinline__ void expect(int s) const { mbar_arrive_expect_tx(full + s, bytes); }
+    __device__ __forceinline__ void complete(int s) const {
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full + s)), "r"(bytes) : "memory");
+    }
+    __device__ __forceinline__ void drain(int s, unsigned parity) const { mbar_drain(full + s, parity, err); }
+};
 
 // A box of a matrix -> this block's shared memory, counted on `bar`: this block's, or (PAIR) one of the pair's.
 template <bool PAIR>
@@ -374,7 +399,8 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
     extern __shared__ unsigned char dynamic[];
     __shared__ uint64_t full[kStages], empty[kStages], done[kBufs], drained[kBufs], last;
     __shared__ uint32_t tmem_at;
-    __shared__ uint64_t scaled[kMmPlaces], used[kMmPlaces];
+    __shared__ uint64_t scaled[kMmPlaces], used[kMmPlaces], told;
+    __shared__ int others_turns;  // of a pair's second block, in the first
     __shared__ __align__(16) MmScales<TN, COLS> scales;
     __shared__ ScaleRange ranges[2];  // of P's scales and of Q's
     const uint32_t tiles = (smem_u32(dynamic) + 1023) & ~1023u;
@@ -393,6 +419,7 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             mbar_init(used + i, S::kWarps);
         }
         mbar_init(&last, 1);
+        if (kPair) mbar_init(&told, 1);
         fence_mbar_init();
     }
     // Tensor memory is taken once the kernel before has given up its own, and before the next one's blocks may come, which
@@ -435,9 +462,14 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
                         if (++s == kStages) s = 0, phase ^= 1;
                     }
                 }
-                // every copy has landed before the blocks end
-                if (row_of == 0)
-                    for (int i = turns > kStages ? turns - kStages : 0; i < turns; ++i) mbar_drain(full + i % kStages, (i / kStages) & 1, a.err);
+                // every copy has landed before the blocks end, in a pair those of both (which stop apart where a wait gave up)
+                if (kPair && rank == 1) {
+                    tell_turns(peer_address(&others_turns, 0), peer_address(&told, 0), turns);
+                } else {
+                    int others = turns;
+                    if (kPair && poll_drain([&] { return mbar_try_wait_cluster(&told, 0); })) others = others_turns;
+                    end_copies<kStages>(turns, others, RingEnd{full, a.err, (unsigned)S::kBytes});
+                }
             }
             __syncwarp();
         } else if (warp == S::kWarps + 1) {
