@@ -1045,23 +1045,34 @@ Span scales_of(const char* name, const gs_fp8& t, int64_t rows, int64_t cols) {
     return down ? span_of(name, t.scale, across, (up - 1) * of_row + 1, of_block, 4) : span_of(name, t.scale, up, (across - 1) * of_block + 1, of_row, 4);
 }
 
-// Whether rows of one meet rows of the other: exact where the strides agree (as in slices of one buffer); where they do not
-// and the ranges meet, only a common start is taken for it.
+// The least x >= 0 with l <= a x mod m <= r, or -1 (0 <= l <= r < m, 0 <= a < m): where no multiple of a lies in l .. r itself, the
+// least y for which one lies in m y + l .. m y + r, a question of the same kind modulo a, as in Euclid's algorithm.
+int64_t first_in(int64_t a, int64_t m, int64_t l, int64_t r) {
+    if (l == 0) return 0;
+    if (a == 0) return -1;
+    const int64_t x = (l + a - 1) / a;
+    if ((__int128)a * x <= r) return x;
+    const int64_t y = first_in(m % a, a, (a - r % a) % a, (a - l % a) % a);
+    return y < 0 ? -1 : (int64_t)(((__int128)m * y + l + a - 1) / a);
+}
+
+// Whether a byte of one lies in the other.
 bool meet(const Span& a, const Span& b) {
     if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.bytes == 0 || b.bytes == 0) return false;
-    const __int128 p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-    const __int128 p_end = p + (__int128)(a.rows - 1) * a.stride + a.bytes, q_end = q + (__int128)(b.rows - 1) * b.stride + b.bytes;
-    if (p_end <= q || q_end <= p) return false;
-    if (a.rows == 1 || b.rows == 1) {
-        const Span &one = a.rows == 1 ? a : b, &many = a.rows == 1 ? b : a;
-        const uintptr_t s = reinterpret_cast<uintptr_t>(one.p), m = reinterpret_cast<uintptr_t>(many.p);
-        if (many.rows == 1 || s <= m) return true;
-        const int64_t in = (int64_t)((s - m) % (uintptr_t)many.stride);
-        return in < many.bytes || in + one.bytes > many.stride;
-    }
-    if (a.stride != b.stride) return a.p == b.p;
-    const int64_t in = (int64_t)(((q - p) % a.stride + a.stride) % a.stride);
-    return in < a.bytes || in + b.bytes > a.stride;
+    const __int128 p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p), last = (__int128)(a.rows - 1) * a.stride;
+    if (p + last + a.bytes <= q || q + (__int128)(b.rows - 1) * b.stride + b.bytes <= p) return false;
+    // b's rows from `lo` to `hi` start where they may meet some of a's: `from` is where the first does, from a's start
+    const __int128 d = q - p, reach = d + b.bytes - 1;
+    const __int128 lo = reach >= 0 ? 0 : (-reach + b.stride - 1) / b.stride, end = last + a.bytes - 1 - d;
+    const __int128 hi = end < 0 ? -1 : std::min<__int128>(b.rows - 1, end / b.stride);
+    if (lo > hi) return false;
+    const __int128 from = d + lo * b.stride;
+    if (from < 0 || d + hi * b.stride >= last) return true;  // a's first row, or its last
+    // between these a row of b meets one of a's unless it lies in a gap: its start, with its length before it, modulo a's stride
+    const int64_t at = (int64_t)((from + b.bytes - 1) % a.stride), window = a.bytes + b.bytes - 2;
+    if (window >= a.stride - 1 || at <= window) return true;
+    const int64_t x = first_in(b.stride % a.stride, a.stride, a.stride - at, a.stride - at + window);
+    return x >= 0 && x <= hi - lo;
 }
 
 // What a call writes may lie on one of the first `same` inputs, row over row, and on nothing else.

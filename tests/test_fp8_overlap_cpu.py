@@ -1,0 +1,82 @@
+"""Overlaps of strided tensors: the calls refuse those in which a byte that is written is one that is read or written besides, and
+no others (CPU, addresses that are never read)."""
+import ctypes as C
+import random
+
+import pytest
+import torch
+
+import __graft_entry__
+from differentiable_gaussian_splatting_gs_gb300 import _abi
+
+if torch.cuda.is_available():
+    pytest.skip("made-up addresses: only where no device could follow them", allow_module_level=True)
+
+ARG = _abi.GS_ERR_ARG
+ROOM = 1 << 32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    __graft_entry__.build()
+    return _abi.load()
+
+
+def _fp8(data, stride, scale, row, block, rows=1):
+    return _abi.gs_fp8(data=data, stride=stride, scale=scale, scale_row=row, scale_block=block, block_rows=rows)
+
+
+def _lies_on(lib, status):
+    """Refused for an overlap; past the checks otherwise (there is no device to go on with)."""
+    if status == ARG:
+        assert b"lies on" in lib.gs_last_error_message(), lib.gs_last_error_message()
+        return True
+    assert status == _abi.GS_ERR_CUDA
+    return False
+
+
+def _bytes(start, rows, length, stride):
+    return {start + r * stride + i for r in range(rows) for i in range(length)}
+
+
+def test_values_and_x_of_other_strides(lib):
+    rng = random.Random(1)
+    seen = [0, 0]
+    for _ in range(4000):
+        rows, cols, wide = rng.randint(1, 9), rng.randint(1, 40), rng.choice([0, 1, 2])
+        size = 4 if wide == 0 else 2
+        xs, qs = cols + rng.randint(0, 60), (cols + 15) // 16 * 16 + 16 * rng.randint(0, 12)
+        x, q = ROOM + size * rng.randint(0, 700 // size), ROOM + 16 * rng.randint(0, 60)
+        want = bool(_bytes(x, rows, cols * size, xs * size) & _bytes(q, rows, cols, qs))
+        t = _fp8(q, qs, 2 * ROOM, 1, rows)
+        assert _lies_on(lib, lib.gs_quantize_fp8(x, xs, 1, rows, cols, wide, C.byref(t), None)) == want, (x - ROOM, xs, q - ROOM, qs, rows, cols, size)
+        seen[want] += 1
+    assert min(seen) > 500, seen
+
+
+def test_results_between_rows_of_operands(lib):
+    rng = random.Random(2)
+    seen = [0, 0]
+    for _ in range(4000):
+        m, n, k = rng.randint(1, 7), rng.randint(1, 12), rng.randint(1, 30)
+        at, os = ROOM + 16 * rng.randint(0, 20), n + rng.randint(0, 40)
+        out, a_stride = ROOM + 4 * rng.randint(0, 120), 16 * rng.randint((k + 15) // 16, 9)
+        a, b = _fp8(at, a_stride, 3 * ROOM, 1, m), _fp8(4 * ROOM, 128, 5 * ROOM, 1, n)
+        want = bool(_bytes(out, m, 4 * n, 4 * os) & _bytes(at, m, k, a_stride))
+        assert _lies_on(lib, lib.gs_matmul_fp8(C.byref(a), C.byref(b), m, n, k, 0, out, os, None)) == want, (out - ROOM, os, at - ROOM, a_stride, m, n, k)
+        seen[want] += 1
+    assert min(seen) > 500, seen
+
+
+def test_many_rows_whose_gaps_hold_the_others(lib):
+    # rows of 16 bytes 4096 apart and values of 16 bytes 8192 apart: in the gaps, or in one of a million rows
+    rows = 1 << 20
+    for start, want in ((2048, False), (4080, False), (4096 * 5, True), (8192 - 48, False), (8192 * 3 + 16, False), (8192 * 3, True)):
+        t = _fp8(ROOM + start, 8192, 4 * ROOM * 64, 1, rows)
+        assert _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, rows, 4, 0, C.byref(t), None)) == want, start
+    # strides without a common factor of the rows' length: the first that meet are far in
+    t = _fp8(ROOM + 64, 4112, 1 << 50, 1, rows)
+    assert _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, rows, 4, 0, C.byref(t), None))
+    assert not _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, 200, 4, 0, C.byref(t), None))  # row 252 is the first (64 + 252 x 16 = 4096)
+    assert _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, 260, 4, 0, C.byref(t), None))
+
