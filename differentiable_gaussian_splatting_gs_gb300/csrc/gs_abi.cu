@@ -1035,14 +1035,19 @@ Span span_of(const char* name, const void* p, int64_t rows, int64_t cols, int64_
 
 constexpr int kFp8Block = 128;
 
-// A tensor's scales, by the smaller of their strides (those between them count as theirs); none that run backwards.
+// A tensor's scales, by the smaller of their strides (those between them count as theirs).
 Span scales_of(const char* name, const gs_fp8& t, int64_t rows, int64_t cols) {
     const int64_t up = (rows + t.block_rows - 1) / t.block_rows, across = (cols + kFp8Block - 1) / kFp8Block;
     if (rows < 1 || cols < 1) return {name, nullptr, 0, 0, 0};
-    const int64_t of_row = up > 1 ? t.scale_row : 0, of_block = across > 1 ? t.scale_block : 0;
-    if (of_row < 0 || of_block < 0) return {name, nullptr, 0, 0, 0};
+    int64_t of_row = up > 1 ? t.scale_row : 0, of_block = across > 1 ? t.scale_block : 0;
+    __int128 first = reinterpret_cast<uintptr_t>(t.scale);  // of strides that run backwards the last scale
+    if (of_row < 0) first += (__int128)(up - 1) * of_row * 4, of_row = -of_row;
+    if (of_block < 0) first += (__int128)(across - 1) * of_block * 4, of_block = -of_block;
+    if (first <= 0) first = 1;
+    const void* p = reinterpret_cast<const void*>((uintptr_t)first);
     const bool down = up > 1 && (across <= 1 || of_row <= of_block);  // rows' scales are the closer ones
-    return down ? span_of(name, t.scale, across, (up - 1) * of_row + 1, of_block, 4) : span_of(name, t.scale, up, (across - 1) * of_block + 1, of_row, 4);
+    const __int128 len = (__int128)((down ? up : across) - 1) * (down ? of_row : of_block) + 1;
+    return span_of(name, p, down ? across : up, (int64_t)std::min<__int128>(len, 1ll << 59), down ? of_block : of_row, 4);
 }
 
 // The least x >= 0 with l <= a x mod m <= r, or -1 (0 <= l <= r < m, 0 <= a < m): where no multiple of a lies in l .. r itself, the
@@ -1103,7 +1108,7 @@ int check_fp8(const char* where, const char* name, const gs_fp8* t, int64_t rows
 int check_scales(const char* where, const gs_fp8& t, int64_t rows, int64_t cols) {
     const int64_t up = (rows + t.block_rows - 1) / t.block_rows, across = (cols + kFp8Block - 1) / kFp8Block;
     const int64_t r = t.scale_row, b = t.scale_block;
-    const bool fits = (up <= 1 || r > 0) && (across <= 1 || b > 0) && (up <= 1 || across <= 1 || (r < b ? (up - 1) * r < b : (across - 1) * b < r));
+    const bool fits = (up <= 1 || r > 0) && (across <= 1 || b > 0) && (up <= 1 || across <= 1 || (r < b ? (__int128)(up - 1) * r < b : (__int128)(across - 1) * b < r));
     if (!fits) return fail(GS_ERR_ARG, "%s: scales share memory (strides %lld, %lld)", where, (long long)r, (long long)b);
     return GS_OK;
 }

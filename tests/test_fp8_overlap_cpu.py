@@ -80,3 +80,20 @@ def test_many_rows_whose_gaps_hold_the_others(lib):
     assert not _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, 200, 4, 0, C.byref(t), None))  # row 252 is the first (64 + 252 x 16 = 4096)
     assert _lies_on(lib, lib.gs_quantize_fp8(ROOM, 1024, 1, 260, 4, 0, C.byref(t), None))
 
+
+def test_scales_that_run_backwards_are_where_they_are(lib):
+    def product(a, out):
+        b = _fp8(10 * ROOM, 512, 11 * ROOM, 4, 1, 128)
+        return _lies_on(lib, lib.gs_matmul_fp8(C.byref(a), C.byref(b), 256, 256, 512, 2, out, 256, None))
+
+    a = _fp8(8 * ROOM, 512, 9 * ROOM, -4, 1)
+    assert product(a, 9 * ROOM - 4096 * 2) and not product(a, 9 * ROOM + 16) and not product(a, 9 * ROOM - 4 * 4 * 255 - 131072)
+    a = _fp8(8 * ROOM, 512, 9 * ROOM, 1, -256)
+    assert product(a, 9 * ROOM - 4 * 256 * 3) and not product(a, 9 * ROOM + 4 * 256)
+
+
+def test_strides_whose_products_pass_64_bits(lib):
+    # 2^32 + 1 rows of blocks whose scales are 2^32 apart reach past the next column's, 2^36 away: 2^32 x 2^32 is not 0
+    t = _fp8(8 * ROOM, 1 << 31, 1 << 50, 1 << 32, 1 << 36, 128)
+    assert lib.gs_quantize_fp8(ROOM, 1 << 31, 1, 128 * ((1 << 32) + 1), 256, 0, C.byref(t), None) == ARG
+    assert b"share memory" in lib.gs_last_error_message()
