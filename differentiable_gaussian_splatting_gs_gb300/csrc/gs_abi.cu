@@ -1033,6 +1033,8 @@ Span span_of(const char* name, const void* p, int64_t rows, int64_t cols, int64_
     return {name, p, 1, (int64_t)(all < most ? all : most), (int64_t)(all < most ? all : most)};
 }
 
+Span vector_of(const char* name, const void* p, int64_t n, size_t size) { return span_of(name, p, 1, n, n, size); }
+
 constexpr int kFp8Block = 128;
 
 // A tensor's scales, by the smaller of their strides (those between them count as theirs).
@@ -1166,12 +1168,14 @@ int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64
     const size_t size = elem_bytes(dtype);
     const Span to_h = span_of("h", residual ? h : nullptr, rows, cols, h_stride, size),
                to_y = !q ? span_of("y", y, rows, cols, y_stride, size) : span_of("q", q->data, rows, cols, q->stride, 1),
-               in[] = {span_of("x", x, rows, cols, x_stride, size), span_of("the residual", residual, rows, cols, residual_stride, size), to_h};
-    if ((s = check_apart(me, to_h, in, 2, 2)) || (s = check_apart(me, to_y, in, 3, y ? 2 : 0))) return s;
-    if (q) {
-        const Span scales = scales_of("q's scale", *q, rows, cols), other[] = {in[0], in[1], to_h, to_y};
-        if ((s = check_apart(me, scales, other, 4, 0))) return s;
-    }
+               to_rstd = vector_of("rstd", rstd, rows, 4), scales = q ? scales_of("q's scale", *q, rows, cols) : Span{},
+               all[] = {span_of("x", x, rows, cols, x_stride, size),
+                        span_of("the residual", residual, rows, cols, residual_stride, size),
+                        vector_of("the weight", rows > 0 ? weight : nullptr, cols, elem_bytes(weight_dtype)),
+                        to_h, to_y, scales};
+    if ((s = check_apart(me, to_h, all, 3, 2)) || (s = check_apart(me, to_y, all, 4, y ? 2 : 0)) || (q && (s = check_apart(me, scales, all, 5, 0))) ||
+        (s = check_apart(me, to_rstd, all, 6, 0)))
+        return s;
     if (rows == 0) return GS_OK;
     unsigned* err = error_word(&s);
     if (!err) return s;
@@ -1218,9 +1222,12 @@ int gs_rms_norm_bwd(const void* dy, int64_t dy_stride, const void* h, int64_t h_
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
         return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
     const Span to = span_of("dx", dx, rows, cols, dx_stride, size),
-               in[] = {span_of("dy", dy, rows, cols, dy_stride, size), span_of("h", h, rows, cols, h_stride, size),
-                       span_of("dh", dh, rows, cols, dh_stride, size)};
-    if ((s = check_apart(me, to, in, 3, 3))) return s;
+               to_dw = vector_of("dweight", dweight, cols, elem_bytes(weight_dtype)), room = vector_of("the workspace", need > 0 ? workspace : nullptr, need, 1),
+               all[] = {span_of("dy", dy, rows, cols, dy_stride, size), span_of("h", h, rows, cols, h_stride, size),
+                        span_of("dh", dh, rows, cols, dh_stride, size), vector_of("rstd", rstd, rows, 4),
+                        vector_of("the weight", rows > 0 ? weight : nullptr, cols, elem_bytes(weight_dtype)), to, to_dw};
+    // (dweight is written last, when the inputs are read)
+    if ((s = check_apart(me, to, all, 5, 3)) || (s = check_apart(me, to_dw, &to, 1, 0)) || (s = check_apart(me, room, all, 7, 0))) return s;
     unsigned* err = error_word(&s);
     if (!err) return s;
     RmsTensors t{};
@@ -1300,6 +1307,14 @@ int gs_clip_grads(const gs_gradient* grads, int32_t count, int32_t clip, double 
     const size_t need = clip_workspace_bytes(grads, count);
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
         return fail(GS_ERR_ARG, "%s: workspace NULL, not 16-byte aligned or smaller than %zu bytes", me, need);
+    const Span to = vector_of("norm", norm, 1, 4), room = vector_of("the workspace", need > 0 ? workspace : nullptr, need, 1);
+    if ((s = check_apart(me, room, &to, 1, 0))) return s;
+    for (int32_t i = 0; i < count; ++i) {
+        const size_t size = elem_bytes(grads[i].dtype);
+        const Span g[] = {vector_of("a gradient", grads[i].grad, grads[i].n, size), vector_of("an output", clip ? grads[i].out : nullptr, grads[i].n, size)};
+        // (the norm alone is written when the gradients are read)
+        if ((s = check_apart(me, room, g, 2, 0)) || (clip && (s = check_apart(me, to, g, 2, 0)))) return s;
+    }
     unsigned* err = error_word(&s);
     if (!err) return s;
     cudaError_t e = launch_clip(grads, count, clip != 0, max_norm, eps, workspace, norm, as_stream(stream));

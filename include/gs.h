@@ -578,8 +578,8 @@ typedef struct gs_fp8 {
  *   weight: [cols] of weight_dtype (`dtype` or GS_DTYPE_F32) or NULL (1).
  *   Squares are float32: a row whose mean square passes its range has rstd = 0 and y = 0.
  *   y: rows of `dtype`; or NULL, and q receives y in 8 bits (block_rows 1), quantized from float32.
- * h and y may be x or the residual (with its row stride), each over its own rows; h, y and q must not
- * overlap one another or otherwise an input. rows >= 0, 1 <= cols < 2^30, eps >= 0.
+ * h and y may be x or the residual (with its row stride), each over its own rows; h, y, q, its scales and
+ * rstd must not overlap one another or otherwise an input. rows >= 0, 1 <= cols < 2^30, eps >= 0.
  * Errors: GS_ERR_ARG, GS_ERR_CUDA.                                                               */
 int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int64_t rows,
                     int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, float eps, void* h,
@@ -589,7 +589,8 @@ int gs_rms_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64
  * the gradient of x and of the residual alike, and dweight = sum over rows of dy hhat ([cols] of
  * weight_dtype, overwritten, or NULL).
  *   dh: rows, the gradient of h from its other readers, or NULL (0).
- * dx may be dy, h or dh (with its row stride). workspace: gs_rms_norm_workspace_bytes(rows, cols) bytes,
+ * dx may be dy, h or dh (with its row stride) and must not overlap otherwise an input; dweight must not
+ * overlap dx, and the workspace nothing else. workspace: gs_rms_norm_workspace_bytes(rows, cols) bytes,
  * 16-byte aligned (unused without dweight). Errors: GS_ERR_ARG, GS_ERR_CUDA.                      */
 size_t gs_rms_norm_workspace_bytes(int64_t rows, int64_t cols);
 int gs_rms_norm_bwd(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, const void* dh,
@@ -620,7 +621,8 @@ typedef struct gs_gradient {
 /* norm (one float32) = 2-norm of all elements of `count` gradients; with `clip`, each gradient times
  * min(1, max_norm / (norm + eps)) (all NaN where the norm is). Squares that float32 does not hold are
  * summed in float64. Gradients that stay as they are (the factor is 1, in place) are not written.
- * What is written must not overlap a gradient but its own, nor another `out`.
+ * What is written must not overlap a gradient but its own, nor another `out`; norm must not overlap either
+ * where they are clipped, and the workspace nothing else.
  * max_norm and eps must not be negative or NaN. workspace: gs_clip_workspace_bytes(grads, count) bytes,
  * 16-byte aligned. Errors: GS_ERR_ARG, GS_ERR_CUDA.                                              */
 size_t gs_clip_workspace_bytes(const gs_gradient* grads, int32_t count);

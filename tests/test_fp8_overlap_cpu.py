@@ -97,3 +97,43 @@ def test_strides_whose_products_pass_64_bits(lib):
     t = _fp8(8 * ROOM, 1 << 31, 1 << 50, 1 << 32, 1 << 36, 128)
     assert lib.gs_quantize_fp8(ROOM, 1 << 31, 1, 128 * ((1 << 32) + 1), 256, 0, C.byref(t), None) == ARG
     assert b"share memory" in lib.gs_last_error_message()
+
+
+@pytest.mark.parametrize("dt,size", [(0, 4), (2, 2)])
+def test_norms_outputs_on_weights_statistics_and_one_another(lib, dt, size):
+    rows, cols = 64, 512
+
+    def fwd(x=ROOM, r=2 * ROOM, w=3 * ROOM, h=4 * ROOM, y=5 * ROOM, rstd=6 * ROOM, q=None):
+        return _lies_on(lib, lib.gs_rms_norm_fwd(x, cols, r, cols, rows, cols, dt, w, 0, 1e-6, h, cols, None if q else y, cols, q and C.byref(q), rstd, None))
+
+    end = rows * cols * size
+    assert not fwd() and not fwd(q=_fp8(7 * ROOM, cols, 8 * ROOM, 1, rows)) and not fwd(w=None)
+    assert not fwd(rstd=ROOM + end) and not fwd(rstd=3 * ROOM + 4 * cols) and not fwd(h=3 * ROOM - end)
+    for bad in (dict(h=3 * ROOM), dict(y=3 * ROOM + 4 * cols - 16), dict(rstd=3 * ROOM - 4), dict(rstd=ROOM + end - 4), dict(rstd=2 * ROOM), dict(rstd=4 * ROOM + 16),
+                dict(rstd=5 * ROOM + 8)):
+        assert fwd(**bad), bad
+    t = _fp8(7 * ROOM, cols, 8 * ROOM, 1, rows)
+    for bad in (dict(rstd=7 * ROOM + 16), dict(rstd=8 * ROOM + 4), dict(w=7 * ROOM), dict(w=8 * ROOM - 4)):
+        assert fwd(q=t, **bad), bad
+    assert not fwd(q=t, rstd=8 * ROOM + 4 * rows * 4)  # behind the scales
+
+    def bwd(dy=ROOM, h=2 * ROOM, dh=3 * ROOM, rstd=4 * ROOM, w=5 * ROOM, dx=6 * ROOM, dw=7 * ROOM, ws=8 * ROOM):
+        return _lies_on(lib, lib.gs_rms_norm_bwd(dy, cols, h, cols, dh, cols, rows, cols, dt, rstd, w, 0, dx, cols, dw, ws, 1 << 20, None))
+
+    need = lib.gs_rms_norm_workspace_bytes(rows, cols)
+    assert not bwd() and not bwd(dx=ROOM) and not bwd(dx=3 * ROOM) and not bwd(ws=ROOM - need) and not bwd(w=None, dw=None, ws=ROOM)
+    assert not bwd(dw=5 * ROOM)  # written when the weights are read
+    for bad in (dict(dx=4 * ROOM), dict(dx=5 * ROOM + 16), dict(dw=6 * ROOM + 8), dict(ws=7 * ROOM), dict(ws=6 * ROOM), dict(ws=5 * ROOM), dict(ws=4 * ROOM), dict(ws=3 * ROOM),
+                dict(ws=2 * ROOM + end - 16), dict(ws=ROOM + 16 - need)):
+        assert bwd(**bad), bad
+
+
+def test_the_norm_and_the_workspace_of_clipping(lib):
+    def clip(g=ROOM, out=None, n=1000, norm=2 * ROOM, ws=3 * ROOM, clip=1):
+        t = (_abi.gs_gradient * 2)(_abi.gs_gradient(grad=4 * ROOM, out=None, n=10, dtype=2), _abi.gs_gradient(grad=g, out=out, n=n, dtype=0))
+        return _lies_on(lib, lib.gs_clip_grads(t, 2, clip, 1.0, 1e-6, norm, ws, 1 << 20, None))
+
+    assert not clip() and not clip(norm=ROOM + 4000) and not clip(out=5 * ROOM) and not clip(norm=ROOM + 16, clip=0) and not clip(norm=3 * ROOM - 4)
+    for bad in (dict(norm=ROOM + 3996), dict(norm=4 * ROOM + 16), dict(out=5 * ROOM, norm=5 * ROOM), dict(out=5 * ROOM, norm=ROOM), dict(ws=ROOM + 3984), dict(ws=2 * ROOM),
+                dict(out=5 * ROOM, ws=5 * ROOM), dict(ws=ROOM, clip=0), dict(ws=4 * ROOM)):
+        assert clip(**bad), bad
