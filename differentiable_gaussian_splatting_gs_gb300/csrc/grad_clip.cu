@@ -50,15 +50,18 @@ __device__ __forceinline__ const ClipTensor& tensor_of(const ClipTable<MOST>& a,
     return a.t[lo];
 }
 
-// f(i, v) for the chunk's elements v at i, 16 bytes at a time where the tensor allows, else one.
-template <class T, class F>
+// f(i, v) for the chunk's elements v at i: 16 bytes at a time between the first and the last whole ones, else one. WRITES: f writes
+// the same place of `out`, which may lie on 16 bytes elsewhere; then one at a time.
+template <class T, bool WRITES, class F>
 __device__ __forceinline__ void each(const ClipTensor& t, long long at, int n, F&& f) {
     constexpr int V = 16 / (int)sizeof(T);
     const T* g = static_cast<const T*>(t.g) + at;
     int done = 0;
-    if (reinterpret_cast<uintptr_t>(t.g) % 16 == 0 && reinterpret_cast<uintptr_t>(t.out) % 16 == 0) {
-        done = n / V * V;
-        int i = threadIdx.x * V;
+    if (!WRITES || (reinterpret_cast<uintptr_t>(t.g) - reinterpret_cast<uintptr_t>(t.out)) % 16 == 0) {
+        const int head = min(n, (int)(-reinterpret_cast<uintptr_t>(g) % 16 / sizeof(T)));
+        if (threadIdx.x < head) f((int)threadIdx.x, *reinterpret_cast<const Pack<T, 1>*>(g + threadIdx.x));
+        done = head + (n - head) / V * V;
+        int i = head + threadIdx.x * V;
         for (; i + 3 * kClipBlock * V < done; i += 4 * kClipBlock * V) {  // (loads would not move over f's stores by themselves)
             Pack<T, V> p[4];
 #pragma unroll
@@ -71,11 +74,11 @@ __device__ __forceinline__ void each(const ClipTensor& t, long long at, int n, F
     for (int i = done + threadIdx.x; i < n; i += kClipBlock) f(i, *reinterpret_cast<const Pack<T, 1>*>(g + i));
 }
 
-template <class F>
+template <bool WRITES, class F>
 __device__ __forceinline__ void each_of(const ClipTensor& t, long long at, int n, F&& f) {
-    if (t.dtype == GS_DTYPE_F32) each<float>(t, at, n, f);
-    else if (t.dtype == GS_DTYPE_F16) each<__half>(t, at, n, f);
-    else each<__nv_bfloat16>(t, at, n, f);
+    if (t.dtype == GS_DTYPE_F32) each<float, WRITES>(t, at, n, f);
+    else if (t.dtype == GS_DTYPE_F16) each<__half, WRITES>(t, at, n, f);
+    else each<__nv_bfloat16, WRITES>(t, at, n, f);
 }
 
 // A sum as two floats, and what did not fit them.
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kClipBlock) k_grad_squares(const __grid_consta
         const int n = (int)min((long long)a.chunk, t.n - at);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         unsigned any = 0;
-        each_of(t, at, n, [&](int, const auto& p) {
+        each_of<false>(t, at, n, [&](int, const auto& p) {
 #pragma unroll
             for (int k = 0; k < (int)(sizeof(p.v) / sizeof(p.v[0])); ++k) {
                 const float v = to_float(p.v[k]);
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kClipBlock) k_grad_squares(const __grid_consta
         if (mine > 1e-25f && mine < 1e30f) {
             add_to(sum.hi, sum.lo, mine);
         } else if (any << 1) {
-            each_of(t, at, n, [&](int, const auto& p) {
+            each_of<false>(t, at, n, [&](int, const auto& p) {
 #pragma unroll
                 for (int k = 0; k < (int)(sizeof(p.v) / sizeof(p.v[0])); ++k) {
                     const double v = to_float(p.v[k]);
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kClipBlock) k_grad_scale(const __grid_constant
         if (factor == 1.f && t.g == t.out) continue;
         const long long at = (long long)(c - t.first) * a.chunk;
         const int count = (int)min((long long)a.chunk, t.n - at);
-        each_of(t, at, count, [&](int i, const auto& p) {
+        each_of<true>(t, at, count, [&](int i, const auto& p) {
             using P = std::remove_const_t<std::remove_reference_t<decltype(p)>>;
             using T = std::remove_const_t<std::remove_reference_t<decltype(p.v[0])>>;
             P q;
