@@ -10,9 +10,9 @@
 //
 // Squares are added in float32 over one chunk and thread (up to 64 elements), from there on as pairs of float32 whose sum has
 // twice the bits. (Double precision, of which an SM does two operations a cycle, took 10 of 28 us for 14 tensors of 1.1 million
-// elements.) A thread whose sum leaves 1e-25 .. 1e30, where squares overflow or are lost below the subnormals, adds its
-// elements again in double precision, unless all are zeros (as those of hidden Gaussians are); such sums are kept apart, and all
-// others join them in the end.
+// elements.) A thread whose sum leaves 1e-25 .. 1e25, where squares are lost below the subnormals, or overflow in the sum of
+// all threads' (3e13 of them would), adds its elements again in double precision, unless all are zeros (as those of hidden
+// Gaussians are); such sums are kept apart, and all others join them in the end.
 #include <cmath>
 
 #include "elem.cuh"
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kClipBlock) k_grad_squares(const __grid_consta
             }
         });
         const float mine = (s[0] + s[1]) + (s[2] + s[3]);
-        if (mine > 1e-25f && mine < 1e30f) {
+        if (mine > 1e-25f && mine < 1e25f) {
             add_to(sum.hi, sum.lo, mine);
         } else if (any << 1) {
             each_of<false>(t, at, n, [&](int, const auto& p) {

@@ -55,3 +55,11 @@ def test_the_norm_goes_by_the_gradients_whatever_the_outputs_alignment(offset, d
             factor = torch.tensor(0.5, device=DEV) / (want + 1e-6)
             assert torch.equal(out, g if factor >= 1 else (g.float() * factor).to(dtype))
             assert (room[:to] == 7).all() and (room[to + n:] == 7).all()
+
+
+def test_more_large_gradients_than_a_float32_sum_holds():
+    # 4e10 squares of 1.1e28: every thread's 64 fit float32, their sum does not (one tensor many times: nothing is written)
+    v, n, times = 1.5 * 2.0 ** 46, 100_000_000, 400
+    g = torch.full((n,), v, device=DEV, dtype=torch.bfloat16)
+    want = (n * times) ** 0.5 * v
+    assert abs(api.gs_grad_norm([g] * times).item() / want - 1) <= 2.0 ** -23
