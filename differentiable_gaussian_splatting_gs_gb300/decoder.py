@@ -21,6 +21,14 @@ from . import api, step
 PARTS = {"mean3d": (0, 3), "log_scale": (3, 6), "quat": (6, 10), "opacity_logit": (10, 11), "sh": (11, 14)}
 
 
+def _transposed8(q, scale):
+    """8-bit values [n, k] with scales for 128 x 128 as [k, n], in rows that start on 16 bytes."""
+    n, k = q.shape
+    rows = torch.empty(k, (n + 15) // 16 * 16, dtype=torch.uint8, device=q.device)[:, :n]
+    rows.copy_(q.view(torch.uint8).t())
+    return rows.view(q.dtype), scale.t()
+
+
 class GaussianDecoder:
     """n Gaussians of SH degree 0 from tokens [1, length, token_channels].
 
@@ -90,7 +98,7 @@ class GaussianDecoder:
             self.grads[name].copy_(x.t() @ dy)
             return dy @ w[name].t()
         api.gs_matmul_fp8(*api.gs_quantize_fp8(x.t()), *api.gs_quantize_fp8(dy.t()), out=self.grads[name])
-        return api.gs_matmul_fp8(*api.gs_quantize_fp8(dy), *api.gs_quantize_fp8(self.weights[name], 128), dtype=self.dtype)
+        return api.gs_matmul_fp8(*api.gs_quantize_fp8(dy), *_transposed8(*w["8bit"][name]), dtype=self.dtype)
 
     def _scene(self, tokens):
         if tokens.dim() != 3 or tokens.shape[0] != 1 or tokens.shape[2] != self.weights["wk"].shape[0]:
