@@ -21,14 +21,6 @@ from . import api, step
 PARTS = {"mean3d": (0, 3), "log_scale": (3, 6), "quat": (6, 10), "opacity_logit": (10, 11), "sh": (11, 14)}
 
 
-def _transposed8(q, scale):
-    """8-bit values [n, k] with scales for 128 x 128 as [k, n], in rows that start on 16 bytes."""
-    n, k = q.shape
-    rows = torch.empty(k, (n + 15) // 16 * 16, dtype=torch.uint8, device=q.device)[:, :n]
-    rows.copy_(q.view(torch.uint8).t())
-    return rows.view(q.dtype), scale.t()
-
-
 class GaussianDecoder:
     """n Gaussians of SH degree 0 from tokens [1, length, token_channels].
 
@@ -83,9 +75,9 @@ class GaussianDecoder:
             return api.gs_rms_norm_fp8(x, self.weights[f"norm_{name}_weight"])[:2]
         return api.gs_quantize_fp8(self._norm(x, name)[0])
 
-    def _weights8(self) -> dict:
-        """The projections' weights in 8 bits, as the second operand of a product: [outputs, inputs]."""
-        return {name: api.gs_quantize_fp8(self.weights[name].t(), 128) for name in ("wq", "wk", "wv", "wo")}
+    def _weights8(self, backward: bool = False) -> dict:
+        """The projections' weights in 8 bits, as the second operand of a product: [outputs, inputs], backward [inputs, outputs]."""
+        return {name: api.gs_quantize_fp8(self.weights[name] if backward else self.weights[name].t(), 128) for name in ("wq", "wk", "wv", "wo")}
 
     def _project(self, x, name: str, w: dict):
         if self.fp8:
@@ -98,7 +90,7 @@ class GaussianDecoder:
             self.grads[name].copy_(x.t() @ dy)
             return dy @ w[name].t()
         api.gs_matmul_fp8(*api.gs_quantize_fp8(x.t()), *api.gs_quantize_fp8(dy.t()), out=self.grads[name])
-        return api.gs_matmul_fp8(*api.gs_quantize_fp8(dy), *_transposed8(*w["8bit"][name]), dtype=self.dtype)
+        return api.gs_matmul_fp8(*api.gs_quantize_fp8(dy), *w["8bit_bwd"][name], dtype=self.dtype)
 
     def _scene(self, tokens):
         if tokens.dim() != 3 or tokens.shape[0] != 1 or tokens.shape[2] != self.weights["wk"].shape[0]:
@@ -116,7 +108,7 @@ class GaussianDecoder:
         tokens = self._scene(tokens)
         w = {k: v.to(self.dtype) for k, v in self.weights.items()}
         if self.fp8:
-            w["8bit"] = self._weights8()
+            w["8bit"], w["8bit_bwd"] = self._weights8(), self._weights8(backward=True)  # the backward's are the forward's too
         x = w["queries"]
         h, _, stats_q = self._norm(x, "q")
         t, _, stats_t = self._norm(tokens, "t")

@@ -37,9 +37,3 @@ def test_the_backwards_8_bit_weights_are_the_forwards(norm, dtype):
     got = d.backward(grads)
     assert torch.equal(got, dtokens) and all(torch.equal(d.grads[k], want[k]) for k in want)
 
-
-@pytest.mark.parametrize("shape", [(200, 96), (128, 256), (1, 17), (300, 129)])
-def test_a_weights_blocks_transposed_are_the_transposes(shape):
-    w = torch.randn(shape, device=DEV)
-    got, want = decoder._transposed8(*api.gs_quantize_fp8(w.t(), 128)), api.gs_quantize_fp8(w, 128)
-    assert torch.equal(got[0].float(), want[0].float()) and torch.equal(got[1], want[1]) and got[0].data_ptr() % 16 == 0 and got[0].stride(0) % 16 == 0
