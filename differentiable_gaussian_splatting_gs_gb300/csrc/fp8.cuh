@@ -15,6 +15,18 @@ constexpr int kQBlock = 128;  // columns (or rows and columns) that share a scal
 
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// The largest of LANES neighbouring lanes' magnitudes.
+template <int LANES>
+__device__ __forceinline__ unsigned lanes_top(unsigned m) {
+    if constexpr (LANES == 32) {
+        return __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
+}
+
 // A product with 1/448, within an ulp of the quotient: a division for each 128 elements in every lane took a third of the
 // quantizing kernels' instructions.
 __device__ __forceinline__ float block_scale(unsigned top) {

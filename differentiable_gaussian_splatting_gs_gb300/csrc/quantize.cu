@@ -33,17 +33,6 @@ struct QuantBits<float> {
     typedef uint32_t type;
 };
 
-// The largest of LANES neighbouring lanes' magnitudes.
-template <int LANES>
-__device__ __forceinline__ unsigned lanes_top(unsigned m) {
-    if constexpr (LANES == 32) {
-        return __reduce_max_sync(0xffffffffu, m);
-    } else {
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        return m;
-    }
-}
 // Both halves of a word at once, as integers, in the order of their magnitudes.
 template <int N>
 __device__ __forceinline__ unsigned halves_top(const uint32_t (&w)[N]) {

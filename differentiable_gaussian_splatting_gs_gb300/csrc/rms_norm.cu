@@ -23,27 +23,15 @@ struct RmsFwdArgs {
     unsigned* err;
 };
 
-// The largest of a block's magnitudes: over LANES neighbouring lanes.
-template <int LANES>
-__device__ __forceinline__ unsigned lanes_max(unsigned m) {
-    if constexpr (LANES == 32) {
-        return __reduce_max_sync(0xffffffffu, m);
-    } else {
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        return m;
-    }
-}
-
 // Blocks of an SM at least (0: as the registers come out), where that was faster: of rows read an element at a time the longest (8000 x
 // 8191 float16 with a residual 153 us, so 134; to 8 bits 202, 155), but for bfloat16 with a residual, which would spill (157 us, and 174
 // so); and, without a residual, those of 12 and 16 to a thread (200,000 x 333 float16 57 us, so 53; with one 107, and 127 with a fourth
 // block).
 template <class T, int VEC, int NV, bool RES>
-constexpr int kRmsBlocks = VEC > 1 ? 0 : NV > 16 ? RES && std::is_same_v<T, __nv_bfloat16> ? 0 : 2 : NV >= 12 && !RES ? 3 : 0;
+constexpr int kRmsFwdBlocks = VEC > 1 ? 0 : NV > 16 ? RES && std::is_same_v<T, __nv_bfloat16> ? 0 : 2 : NV >= 12 && !RES ? 3 : 0;
 
 template <class T, int VEC, int NV, int LPR, int FULL, bool RES>
-__global__ void __launch_bounds__(kNormBlock, kRmsBlocks<T, VEC, NV, RES>) k_rms_fwd(const RmsFwdArgs a) {
+__global__ void __launch_bounds__(kNormBlock, kRmsFwdBlocks<T, VEC, NV, RES>) k_rms_fwd(const RmsFwdArgs a) {
     pdl_entry();
     extern __shared__ __align__(16) float weights[];
     __shared__ float buf[2 * kNormBlock / 32];
@@ -157,7 +145,7 @@ __global__ void __launch_bounds__(kNormBlock, kRmsBlocks<T, VEC, NV, RES>) k_rms
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) top = max(top, magnitude(f[k]));
                 }
-                const float scale = block_scale(lanes_max<kLanes>(top));
+                const float scale = block_scale(lanes_top<kLanes>(top));
                 if (mine) {
                     const float back = scale_back(scale);
                     Pack<uint32_t, VEC / 4> out;
@@ -182,7 +170,7 @@ __global__ void __launch_bounds__(kNormBlock, kRmsBlocks<T, VEC, NV, RES>) k_rms
                         top = max(top, magnitude(f[0]));
                     }
                 }
-                const float scale = block_scale(lanes_max<32>(top)), back = scale_back(scale);
+                const float scale = block_scale(lanes_top<32>(top)), back = scale_back(scale);
 #pragma unroll
                 for (int j = 0; j < kTurn; ++j)
                     if (live && in(i0 + j)) q[at(i0 + j)] = quantize1(y[j], back);
@@ -264,7 +252,7 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd_long(const RmsFwdArgs a)
                 unsigned top = 0;
 #pragma unroll
                 for (int j = 0; j < kLongLoads; ++j) top = max(top, norm(j, y[j]));
-                const float scale = block_scale(lanes_max<32>(top)), back = scale_back(scale);
+                const float scale = block_scale(lanes_top<32>(top)), back = scale_back(scale);
                 const int c = long_at<1>(c0, 0);
                 if (threadIdx.x % 32 == 0 && c < a.cols) a.scale.at(row, c / kQBlock) = scale;
 #pragma unroll
@@ -274,7 +262,7 @@ __global__ void __launch_bounds__(kNormBlock) k_rms_fwd_long(const RmsFwdArgs a)
 #pragma unroll
                 for (int j = 0; j < kLongLoads; ++j) {  // all lanes take part in the shuffles
                     const int c = long_at<VEC>(c0, j);
-                    const float scale = block_scale(lanes_max<kLanes>(norm(j, f))), back = scale_back(scale);
+                    const float scale = block_scale(lanes_top<kLanes>(norm(j, f))), back = scale_back(scale);
                     if (c >= a.cols) continue;
                     if (threadIdx.x % kLanes == 0) a.scale.at(row, c / kQBlock) = scale;
                     Pack<uint32_t, VEC / 4> out;

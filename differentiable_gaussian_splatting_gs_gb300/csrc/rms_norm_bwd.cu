@@ -28,10 +28,10 @@ struct RmsBwdArgs {
 // 57 us, so 50; with dh 60, and 65 so). Rows of a whole warp with dh would
 // spill, and of 8 lanes and fewer there was nothing to gain (200,000 x 64 bfloat16 15 us, and 17 so).
 template <int VEC, int NV, int LPR, bool DH>
-constexpr int kRmsBlocks = NV * VEC >= 12 && NV * VEC <= 16 ? 2 : VEC > 1 && NV == 1 && (LPR == 16 || (LPR == 32 && !DH)) ? 3 : VEC == 1 && NV <= 8 && !DH ? 0 : 1;
+constexpr int kRmsBwdBlocks = NV * VEC >= 12 && NV * VEC <= 16 ? 2 : VEC > 1 && NV == 1 && (LPR == 16 || (LPR == 32 && !DH)) ? 3 : VEC == 1 && NV <= 8 && !DH ? 0 : 1;
 
 template <class T, int VEC, int NV, int LPR, int FULL, bool DH>
-__global__ void __launch_bounds__(kNormBlock, kRmsBlocks<VEC, NV, LPR, DH>) k_rms_bwd(const RmsBwdArgs a) {
+__global__ void __launch_bounds__(kNormBlock, kRmsBwdBlocks<VEC, NV, LPR, DH>) k_rms_bwd(const RmsBwdArgs a) {
     pdl_entry();
     extern __shared__ __align__(16) float share[];  // w; at the end the block's sums
     __shared__ float buf[2 * kNormBlock / 32];

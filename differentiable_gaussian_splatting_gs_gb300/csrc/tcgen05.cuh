@@ -1,5 +1,6 @@
-// Inline PTX of the fifth-generation tensor cores (tcgen05, sm_103a) and of tiled bulk copies, as the
-// cross attention kernels use them: 16-bit operands, float32 accumulators in tensor memory, one CTA.
+// Inline PTX of the fifth-generation tensor cores (tcgen05, sm_103a) and of tiled bulk copies: tensor memory, products of 16-bit
+// operands in one CTA, as the cross attention kernels use them. What the 8-bit product has of its own (8-bit operands, pairs of
+// CTAs) is in matmul_fp8.cu.
 #pragma once
 
 #include <cuda.h>
