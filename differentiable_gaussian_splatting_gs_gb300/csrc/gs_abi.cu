@@ -1115,6 +1115,8 @@ int check_scales(const char* where, const gs_fp8& t, int64_t rows, int64_t cols)
     return GS_OK;
 }
 
+constexpr int64_t kMostGradient = 1ll << 40;  // elements
+
 int check_gradients(const char* me, const gs_gradient* g, int32_t count, bool clip) {
     if (count < 0 || (count > 0 && !g)) return fail(GS_ERR_ARG, "%s: %d gradients at %p", me, count, (const void*)g);
     struct Range {
@@ -1127,7 +1129,7 @@ int check_gradients(const char* me, const gs_gradient* g, int32_t count, bool cl
     for (int32_t i = 0; i < count; ++i) {
         const gs_gradient& t = g[i];
         if (t.dtype < GS_DTYPE_F32 || t.dtype > GS_DTYPE_BF16) return fail(GS_ERR_ARG, "%s: bad dtype %d of gradient %d", me, t.dtype, i);
-        if (t.n < 0 || t.n > (1ll << 40)) return fail(GS_ERR_ARG, "%s: gradient %d of %lld elements", me, i, (long long)t.n);
+        if (t.n < 0 || t.n > kMostGradient) return fail(GS_ERR_ARG, "%s: gradient %d of %lld elements", me, i, (long long)t.n);
         if (t.n == 0) continue;
         const size_t size = elem_bytes(t.dtype);
         if (!t.grad || !aligned(t.grad, size) || !aligned(t.out, size)) return fail(GS_ERR_ARG, "%s: gradient %d is NULL or misaligned", me, i);
@@ -1290,6 +1292,8 @@ int gs_matmul_fp8(const gs_fp8* a, const gs_fp8* b, int64_t m, int64_t n, int64_
 
 size_t gs_clip_workspace_bytes(const gs_gradient* grads, int32_t count) {
     if (count < 0 || (count > 0 && !grads)) return 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (grads[i].n < 0 || grads[i].n > kMostGradient) return 0;  // which gs_clip_grads refuses
     return clip_workspace_bytes(grads, count);
 }
 

@@ -137,3 +137,12 @@ def test_the_norm_and_the_workspace_of_clipping(lib):
     for bad in (dict(norm=ROOM + 3996), dict(norm=4 * ROOM + 16), dict(out=5 * ROOM, norm=5 * ROOM), dict(out=5 * ROOM, norm=ROOM), dict(ws=ROOM + 3984), dict(ws=2 * ROOM),
                 dict(out=5 * ROOM, ws=5 * ROOM), dict(ws=ROOM, clip=0), dict(ws=4 * ROOM)):
         assert clip(**bad), bad
+
+
+def test_the_workspace_of_gradients_that_clipping_refuses(lib):
+    def need(n):
+        t = (_abi.gs_gradient * 2)(_abi.gs_gradient(grad=ROOM, out=None, n=10, dtype=0), _abi.gs_gradient(grad=4 * ROOM, out=None, n=n, dtype=0))
+        return lib.gs_clip_workspace_bytes(t, 2)
+
+    assert need(0) > 0 and need(1 << 40) > 0
+    assert [need(n) for n in (-1, (1 << 40) + 1, (1 << 63) - 1)] == [0, 0, 0]
