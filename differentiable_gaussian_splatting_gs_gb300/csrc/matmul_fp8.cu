@@ -210,8 +210,8 @@ struct MmScales {
 // where the product is a normal number, or a value times the column's scale is (values are 0 or lie between 2^-18, the product of
 // two subnormals, and 128 x 448^2 < 2^25). The warps that copy the scales, which have the time, note the smallest and the largest;
 // a block whose scales can leave that range looks at its tiles again when they are stored, and forms the elements that have such
-// scales once more, in double precision. (The test and the other form within the hot loop took a quarter to a half of its time,
-// 16384 x 4096 x 4096 bf16 265 us instead of 210, whatever the scales.)
+// scales once more, with the scales' powers apart. (The test and another form within the hot loop took a quarter to a half of its
+// time, 16384 x 4096 x 4096 bf16 265 us instead of 210, whatever the scales.)
 struct ScaleRange {
     unsigned least, most;  // magnitudes; the least less one, so that 0 counts as the largest; the most without infinities and NaN
     __device__ __forceinline__ void add(float s) {
@@ -232,72 +232,112 @@ __device__ __forceinline__ bool may_leave_range(const ScaleRange& p, const Scale
            leaves_range(__uint_as_float(p.most), __uint_as_float(q.most), cols);
 }
 
-// Sum of the products of 16 e4m3 values.
-__device__ __forceinline__ float dot16(const uint4& a, const uint4& b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t u, v;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"((uint16_t)(x[i] >> 16 * h)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"((uint16_t)(y[i] >> 16 * h)));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u)), g = __half22float2(*reinterpret_cast<const __half2*>(&v));
-            s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
-        }
-    return s;
+// A scale as m 2^e, 1 <= |m| < 2 (zeros, infinities and NaN: e = 0), so that two of them multiply without leaving float32.
+struct SplitScale {
+    float m;
+    int e;
+    __device__ __forceinline__ explicit SplitScale(float s) : m(s), e(0) {
+        if (s == 0.f || !isfinite(s)) return;
+        if (magnitude(s) < 0x00800000u) m = s * 0x1p64f, e = -64;
+        const unsigned u = __float_as_uint(m);
+        e += (int)(u >> 23 & 255u) - 127;
+        m = __uint_as_float((u & 0x807fffffu) | 0x3f800000u);
+    }
+};
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }  // -126 <= e <= 127
+// sum + v a b: the scales' power in two parts, the one within the multiply-add a normal number, the other before it, where v 2^e a and
+// b's significands stay in range or what they give does not (|v| >= 2^-18 with 2^100 before 2^126 is an infinity, 2^27 with 2^-126 twice 0).
+__device__ __forceinline__ float add_split(float v, const SplitScale& a, const SplitScale& b, float sum) {
+    const int e = a.e + b.e, last = min(max(e, -126), 126), before = min(max(e - last, -126), 100);
+    return fmaf(v * (a.m * b.m * power_of_2(before)), power_of_2(last), sum);
 }
-// The warp's rows of a tile of `rows` x `cols` at (p0, q0) once more, where a scale leaves the range in a block of the inner dimension
-// of k0 .. k1 first (the blocks of a cluster share a tile's). A warp forms an element, 16 bytes of the inner dimension to a lane.
+
+// 16 bytes of a row from byte `at` on, zeros behind its k.
+__device__ __forceinline__ uint4 row16(const uint8_t* row, int at, int k) {
+    if (at + 16 <= k) return *reinterpret_cast<const uint4*>(row + at);
+    unsigned long long low = 0, high = 0;
+#pragma unroll 1
+    for (int i = 0; at + i < k; ++i) (i < 8 ? low : high) |= (unsigned long long)row[at + i] << 8 * (i % 8);
+    return make_uint4((uint32_t)low, (uint32_t)(low >> 32), (uint32_t)high, (uint32_t)(high >> 32));
+}
+// Two e4m3 values (of the word's lower or upper half) as float16, which holds all of them.
+__device__ __forceinline__ uint32_t halves(uint32_t w, int upper) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(w >> 16 * upper)));
+    return r;
+}
+// c [16 x 8] += a [16 x 16] b [16 x 8] of float16 in float32, by the warp.
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// The elements of a tile of `rows` x `cols` at (p0, q0) once more that have a scale which leaves the range, in a block of the inner dimension
+// of k0 .. k1 first (the blocks of a cluster share a tile's). A warp forms 16 x 16 elements where any of them does, with the warp's own
+// tensor-core products, which need neither tensor memory nor another warp: the tile's way of forming them is over. A lane has 16
+// bytes in a row of each operand's rows g and g + 8 (g = lane / 4), and the products take these in the same order in both.
 __device__ __forceinline__ void form_again(const MmArgs& a, int p0, int rows, int q0, int cols, int k0, int k1, int warp, int warps) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
     const bool by_col = a.q_shift == 0;
     rows = min(rows, a.np - p0);
     cols = min(cols, a.nq - q0);
-    for (int r = warp; r < rows; r += warps) {
-        const int p = p0 + r;
-        const float* sp = a.p_scale + (long long)(p >> a.p_shift) * a.p_row;
-        for (int c = 0, next; c < cols; c = next) {  // columns that share their scales
-            next = min(cols, (((q0 + c) >> a.q_shift) + 1 << a.q_shift) - q0);
-            const float* sq = a.q_scale + (long long)((q0 + c) >> a.q_shift) * a.q_row;
-            unsigned first = ~0u;
-            for (int k = lane; k < a.blocks && first == ~0u; k += 32)
-                if (leaves_range(sp[k * a.p_block], sq[k * a.q_block], by_col)) first = k;
-            first = __reduce_min_sync(0xffffffffu, first);
-            if (first < (unsigned)k0 || first >= (unsigned)k1) continue;
-            for (int q = q0 + c; q < q0 + next; ++q) {
-                const uint8_t *x = a.p_data + p * a.p_stride, *y = a.q_data + q * a.q_stride;
-                double sum = 0.0;
-                for (int at = lane * 16; at - lane * 16 < a.k; at += 512) {
-                    uint4 u = {}, v = {};
-                    if (at + 16 <= a.k) {
-                        u = *reinterpret_cast<const uint4*>(x + at);
-                        v = *reinterpret_cast<const uint4*>(y + at);
-                    } else {
-                        uint32_t w[8] = {};
-                        for (int i = 0; i < 16; ++i)
-                            if (at + i < a.k) {
-                                w[i / 4] |= (uint32_t)x[at + i] << 8 * (i % 4);
-                                w[4 + i / 4] |= (uint32_t)y[at + i] << 8 * (i % 4);
-                            }
-                        u = make_uint4(w[0], w[1], w[2], w[3]);
-                        v = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                    float block = dot16(u, v);  // of eight lanes
+    auto p_scale = [&](int p) { return a.p_scale + (long long)(min(p, a.np - 1) >> a.p_shift) * a.p_row; };
+    auto q_scale = [&](int q) { return a.q_scale + (long long)(min(q, a.nq - 1) >> a.q_shift) * a.q_row; };
+    for (int r0 = warp * 16; r0 < rows; r0 += warps * 16) {
+        bool any = false;
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+            if (by_col || c0 % kQBlock == 0) {  // (tiles start where their columns' common scales do, or hold no others)
+                any = false;
+                const float *sp = p_scale(p0 + r0 + lane % 16), *sq = q_scale(q0 + c0 + (by_col ? lane % 16 : 0));
+                for (int k = lane / 16; k < a.blocks; k += 2) any |= leaves_range(by_col ? 1.f : sp[k * a.p_block], sq[k * a.q_block], by_col);
+                any = __any_sync(0xffffffffu, any);
+            }
+            if (!any) continue;
+            const int p = p0 + r0 + g, q = q0 + c0 + g;
+            const uint8_t* x[2] = {a.p_data + min(p, a.np - 1) * a.p_stride, a.p_data + min(p + 8, a.np - 1) * a.p_stride};
+            const uint8_t* y[2] = {a.q_data + min(q, a.nq - 1) * a.q_stride, a.q_data + min(q + 8, a.nq - 1) * a.q_stride};
+            float sum[2][4] = {};
+            unsigned left = 0, mine = 0;  // elements that have left the range, and those that did within k0 .. k1
+            for (int k = 0; k < a.blocks; ++k) {
+                float c[2][4] = {};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int at = k * kMmBlock + 64 * h + 16 * t;
+                    const uint4 u0 = row16(x[0], at, a.k), u1 = row16(x[1], at, a.k), v0 = row16(y[0], at, a.k), v1 = row16(y[1], at, a.k);
+                    const uint32_t u[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}}, v[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
 #pragma unroll
-                    for (int o = 1; o < kMmBlock / 16; o *= 2) block += __shfl_xor_sync(0xffffffffu, block, o);
-                    const int k = at / kMmBlock;
-                    if (lane % (kMmBlock / 16) == 0 && k < a.blocks) sum = fma((double)sp[k * a.p_block] * (double)sq[k * a.q_block], (double)block, sum);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t ma[4] = {halves(u[0][i], 0), halves(u[1][i], 0), halves(u[0][i], 1), halves(u[1][i], 1)};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t mb[2] = {halves(v[j][i], 0), halves(v[j][i], 1)};
+                            warp_mma(c[j], ma, mb);
+                        }
+                    }
                 }
 #pragma unroll
-                for (int o = 16; o >= kMmBlock / 16; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) store_elem(a.out, p * a.out_p + q * a.out_q, a.dtype, (float)sum);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sp = p_scale(p + i / 2 * 8)[k * a.p_block], sq = q_scale(q0 + c0 + 8 * j + 2 * t + i % 2)[k * a.q_block];
+                        sum[j][i] = add_split(c[j][i], SplitScale(sp), SplitScale(sq), sum[j][i]);
+                        const unsigned bit = 1u << (4 * j + i);
+                        if (!(left & bit) && leaves_range(sp, sq, by_col)) {
+                            left |= bit;
+                            if (k >= k0 && k < k1) mine |= bit;
+                        }
+                    }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r0 + g + i / 2 * 8, col = c0 + 8 * j + 2 * t + i % 2;
+                    if ((mine >> (4 * j + i) & 1u) && row < rows && col < cols) store_elem(a.out, (p0 + row) * a.out_p + (q0 + col) * a.out_q, a.dtype, sum[j][i]);
+                }
         }
     }
 }
-
 // ... all of the block's tiles, by `warps` of its warps, this the `warp`-th.
 __device__ __forceinline__ void form_tiles_again(const MmArgs& a, int tn, int warp, int warps) {
     const bool pair = tn == 256;

@@ -604,8 +604,8 @@ int gs_quantize_fp8(const void* x, int64_t x_row_stride, int64_t x_col_stride, i
                     const gs_fp8* q, void* stream);
 
 /* out[m][n] (GS_DTYPE_*, row stride out_stride) = a b^T of the values that a [m][k] and b [n][k] stand
- * for; a's block_rows is 1, b's 1 or 128. Products are summed in float32, by blocks of 128 of k (in float64,
- * and slowly, where float32 does not hold the product of a block's scales, or a value times a scale). k = 0
+ * for; a's block_rows is 1, b's 1 or 128. Products are summed in float32, by blocks of 128 of k (elements for which
+ * float32 does not hold the product of a block's scales, or a value times a scale, by a slower way). k = 0
  * gives zeros. out must not overlap an input. Errors: GS_ERR_ARG, GS_ERR_CUDA; a wait that gave up is reported by gs_device_error. */
 int gs_matmul_fp8(const gs_fp8* a, const gs_fp8* b, int64_t m, int64_t n, int64_t k, int32_t dtype, void* out,
                   int64_t out_stride, void* stream);
