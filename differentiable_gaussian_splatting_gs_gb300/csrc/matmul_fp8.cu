@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(MmShape<TN>::kThreads, MmShape<TN>::kResident)
             int batch = 0, sizes = 0;  // sizes: of the last three batches, the last one's in the lowest four bits
             ScaleRange range{~0u, 0u};
             auto note = [&](int at, int n) {  // what the lane copied to a place, which has landed
-                if (of_q) {
+                if (COLS && !of_q) {  // the columns' decide
+                    range.add(1.f);
+                } else if (of_q) {
                     for (int j = 0; j < n; ++j)
 #pragma unroll
                         for (int i = 0; i < kOfQ; ++i)

@@ -109,3 +109,47 @@ def test_rows_and_columns_beside_extreme_ones_keep_their_bits(m, n, k, block):
     rows = torch.arange(m, device=DEV) % 3 != 0
     columns = (torch.arange(n, device=DEV) // block) % 2 == 0
     assert torch.equal(got[rows][:, columns], want[rows][:, columns])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("m,n,k,block", FORMS)
+def test_inside_larger_buffers_and_captured(m, n, k, block, dtype):
+    # every third row outside (by column: every second column), what lies behind the rows is NaN
+    qa, sa, qb, sb = _tensors(m, n, k, block, 6, _level(-3), _level(-1))
+    sa[::3] *= 2.0 ** -122
+    if block == 1:
+        sb[::2] *= 2.0 ** 111
+    want = api.gs_matmul_fp8(qa, sa, qb, sb, dtype=torch.float32)
+    wide = [torch.full((2 * r, (k + 15) // 16 * 16 + 32), 0x7F, dtype=torch.uint8, device=DEV) for r in (m, n)]  # NaN
+    a, b = (w[::2, 16:16 + k] for w in wide)
+    a.copy_(qa.view(torch.uint8)), b.copy_(qb.view(torch.uint8))
+    a, b = a.view(torch.float8_e4m3fn), b.view(torch.float8_e4m3fn)
+    room = torch.full((m + 2, n + 19), 5.0, device=DEV, dtype=dtype)
+    out = room[1:m + 1, 3:3 + n]
+    api.gs_matmul_fp8(a, sa.t().contiguous().t(), b, sb.t().contiguous().t(), out=out)
+    assert torch.equal(out, want.to(dtype))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        api.gs_matmul_fp8(a, sa, b, sb, out=out)
+    out.fill_(0)
+    sa.mul_(2)  # new scales of a replay
+    graph.replay()
+    torch.cuda.synchronize()
+    again = api.gs_matmul_fp8(qa, sa, qb, sb, dtype=torch.float32)
+    assert torch.equal(out, again.to(dtype))
+    out.fill_(5)
+    assert (room == 5).all() and api.gs_device_error() == _abi.GS_OK
+
+
+def test_several_at_once_with_ordinary_ones():
+    cases = []
+    for i, (m, n, k, block) in enumerate(FORMS):
+        for ea, eb in ((-70, -70), (-2, 1)):
+            t = _tensors(m, n, k, block, i, _level(ea), _level(eb if block == 128 or eb > 0 else -115))
+            cases.append((t, api.gs_matmul_fp8(*t, dtype=torch.float32)))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = [(api.gs_matmul_fp8(*t, dtype=torch.float32, stream=streams[(i + j) % 4]), want) for j in range(3) for i, (t, want) in enumerate(cases)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got) and api.gs_device_error() == _abi.GS_OK
