@@ -33,8 +33,10 @@ __device__ __forceinline__ float block_scale(unsigned top) {
     const float s = __uint_as_float(top) * (1.f / 448.f);
     return s < 1.17549435e-38f ? 1.f : s;
 }
-// The scale's reciprocal to an ulp: a quotient moves by 1.5 ulps of float32, which changes the 4-bit significand of about one
-// element in a million.
+// The scale's reciprocal to an ulp: a quotient moves by 1.5 ulps of float32. That changes one value in a million of float32 inputs.
+// Quotients of 16-bit ones often lie halfway between two 8-bit values exactly (one in 2,000 of a norm's), where either is as near:
+// there the last bits decide, in one of 10,000 otherwise than a division's. (Quotients corrected by their remainder, which round as a
+// division does: 17,384 x 4096 bfloat16 37 us instead of 33, by 128 x 128 51 instead of 40, the norm to 8 bits 3 to 7% more.)
 __device__ __forceinline__ float scale_back(float scale) { return rcp_approx(scale); }
 
 // Four values times the scale's reciprocal, the first in the lowest byte.

@@ -5,8 +5,8 @@
 // sum for each of its blocks, the second's blocks add all of these in one order (the same bits every time, no atomics) and
 // multiply. The second starts at the end of what the first read, which the L2 still holds. A tensor is cut into chunks, and a
 // block finds its chunk's tensor by bisection in a table that is part of the launch's arguments, so that no copy precedes it.
-// 94.4 million float32 in 5 tensors take 186 us (three passes at the measured copy rate: 167), the norm alone 64 (5.9 TB/s); 14
-// tensors of 1.1 million elements 9.0 us, two launches' latency and the joining of the sums.
+// Times in a graph: 94.4 million float32 in 5 tensors 187 us (three passes at the measured copy rate: 167), the norm alone 64 (5.9
+// TB/s); 14 tensors of 1.1 million elements 9.0 us, two launches' latency and the joining of the sums (called 12 to 14, the host's).
 //
 // Squares are added in float32 over one chunk and thread (up to 64 elements), from there on as pairs of float32 whose sum has
 // twice the bits. (Double precision, of which an SM does two operations a cycle, took 10 of 28 us for 14 tensors of 1.1 million

@@ -21,9 +21,9 @@
 //
 // Bound by the elementwise warps: a block of 256 x 256 x 128 takes its SMs 512 cycles of products and some 900 of additions (1,380
 // where scales differ by column): half of these wait for tensor memory and for one another, each packed multiply-add adds three
-// (the registers' ports; scalar ones four). 16384 x 4096 x 4096 bfloat16 takes 205 us (2.7 PFLOP/s, 70% of twice the measured bf16
-// rate), 17384 x 4096 x 1024 74 us, 4096 x 1024 x 17,384 with scales by column 98 us; few rows are bound by b's bytes and a
-// launch's latency (1 x 4096 x 1024 4.8 us, 16 x 8192 x 4096 8.3 us, 4.1 TB/s). Sixteen warps of 64 columns instead of eight of
+// (the registers' ports; scalar ones four). Times in a graph: 16384 x 4096 x 4096 bfloat16 209 us (2.6 PFLOP/s, 69% of twice the measured
+// bf16 rate; called back to back 236, at the power limit), 17384 x 4096 x 1024 75 us, 4096 x 1024 x 17,384 with scales by column 100 to 117 us
+// (by box); few rows are bound by b's bytes and a launch's latency (1 x 4096 x 1024 4.8 us, 16 x 8192 x 4096 8.3 us, 4.1 TB/s). Sixteen warps of 64 columns instead of eight of
 // 128 (234 us), the next block's values asked for before the last of this one are added (240 us), products of 128 columns with
 // four accumulators and tiles of 256 x 160 with three (298 us) were slower; so were, with scales by column, loads that give a
 // thread two columns of each eight, which read a quarter of the scales (104 to 107 us against 98).

@@ -4,9 +4,9 @@
 // Bound by memory: x and r are read once, h and y written once. The layout is the layer norm's (layer_norm.cuh): a row
 // stays in the registers of the threads it is laid over, the grid is persistent, weights lie in shared memory, rows of
 // more than a vector per thread come through the ring of bulk copies. A block's 128 columns belong to neighbouring lanes of
-// one warp, so that its maximum is a few shuffles. 139,072 x 1024 bfloat16 with a residual takes 165 us to 8 bits (6.1 TB/s, 89% of
-// the measured copy rate), 185 us to bfloat16; 1 x 1024 3.0 us; rows that do not lie on 16 bytes 4.3 to 5.3 TB/s in 16 bits, 6.1
-// to 6.6 in float32.
+// one warp, so that its maximum is a few shuffles. Times in a graph: 139,072 x 1024 bfloat16 with a residual 165 us to 8 bits
+// (6.1 TB/s, 89% of the measured copy rate), 185 us to bfloat16; 1 x 1024 2.9 us (a call of its own 7 to 8, the host's); rows that do
+// not lie on 16 bytes 4.3 to 5.3 TB/s in 16 bits, 6.1 to 6.6 in float32.
 #include "rms_norm.cuh"
 
 namespace gs {

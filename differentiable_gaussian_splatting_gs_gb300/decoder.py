@@ -7,9 +7,10 @@ is turned into the Gaussian's parameters by a linear head:
     h = norm(x), t = norm(tokens);  a = attention(h Wq, t Wk, t Wv);  x' = x + a Wo;  out = norm(x') Wh + bh
 
 With fp8=True the products with Wq, Wk, Wv and Wo, and those of their gradients, are 8-bit (gs_quantize_fp8, gs_matmul_fp8);
-serve() runs the forward in 8 bits with weights laid out once. The gradients of these parameters, as step.train_step leaves them
-(gs_preprocess_bwd), come back through backward(): written out by hand from the operators' own backward calls, with matrix
-products between. Weights and their gradients are float32; activations have the decoder's dtype.
+serve() runs the forward in 8 bits with weights laid out once, which is faster than bfloat16's forward (16,384 Gaussians of 4,346
+tokens, 1,024 channels: 370 us, 420); a training step is not (1,770 us, 1,615), for the quantizing. The gradients of these
+parameters, as step.train_step leaves them (gs_preprocess_bwd), come back through backward(): written out by hand from the operators'
+own backward calls, with matrix products between. Weights and their gradients are float32; activations have the decoder's dtype.
 """
 from __future__ import annotations
 
@@ -121,7 +122,8 @@ class GaussianDecoder:
         return self._gaussians(y, w["wh"])
 
     def backward(self, grads: dict):
-        """Leaves the weights' gradients in self.grads, from the parameters' (names as forward's); returns that of the tokens."""
+        """Leaves the weights' gradients in self.grads, from the parameters' (names as forward's); returns that of the tokens. Of the
+        last forward, whose weights must not have changed since (8-bit projections are kept, the others may be read again)."""
         w, x, tokens, h, stats_q, t, stats_t, q, k, v, a, lse, x2, y, stats_x, k_len, key_mask = self._saved
         g = self.grads
         dout32 = torch.cat([grads[name].reshape(self.n, -1) for name in PARTS], 1)

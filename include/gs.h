@@ -557,8 +557,9 @@ int gs_cross_attention_bwd(const gs_attention* a, const gs_heads* dout, const gs
  * 8-bit values are e4m3 (sign, 4 bits of exponent, 3 of significand, largest 448, no infinities) with
  * a float32 scale for each block of 128 columns of a row, or of 128 x 128: x = q scale with
  * scale = max |x| of the block / 448 (1 where that is below 2^-126) and q = x / scale rounded to the
- * nearest. A block with a NaN or an infinity has no finite values. Conventions as above: the calls
- * enqueue on `stream`, allocate nothing, may be captured and give the same bits every time; sums are
+ * nearest (quotients to an ulp or two of float32: one halfway between two values may go to either). A
+ * block with a NaN or an infinity has no finite values. Conventions as above: the calls enqueue
+ * on `stream`, allocate nothing, may be captured and give the same bits every time; sums are
  * float32 or float64. Row strides are in elements.                                              */
 
 /* Rows of 8-bit values, 16-byte aligned with a row stride that is a multiple of 16. The scale of row r
@@ -576,7 +577,8 @@ typedef struct gs_fp8 {
  * residual), rstd = 1 / sqrt(mean of h^2 + eps) (float32 [rows]), y = h rstd w.
  *   residual: NULL, or rows as x's; h is written only with one.
  *   weight: [cols] of weight_dtype (`dtype` or GS_DTYPE_F32) or NULL (1).
- *   Squares are float32: a row whose mean square passes its range has rstd = 0 and y = 0.
+ *   Squares are float32: a row whose sum of squares passes its range has rstd = 0 and y = 0; with eps = 0 one
+ *   whose squares lie below its normal numbers loses digits, and has rstd = inf where all of them are 0.
  *   y: rows of `dtype`; or NULL, and q receives y in 8 bits (block_rows 1), quantized from float32.
  * h and y may be x or the residual (with its row stride), each over its own rows; h, y, q, its scales and
  * rstd must not overlap one another or otherwise an input. rows >= 0, 1 <= cols < 2^30, eps >= 0.
